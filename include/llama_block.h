@@ -99,7 +99,9 @@ typedef enum llama_op {
   LLAMA_OP_GQA_ATTENTION = 2,
   LLAMA_OP_SWIGLU_FFN = 3,
   LLAMA_OP_BLOCK_FORWARD = 4,
-  LLAMA_OP_STACK_DECODE_STEP = 5
+  LLAMA_OP_STACK_DECODE_STEP = 5,
+  LLAMA_OP_GQA_ATTENTION_CHUNK_PAGED = 6,
+  LLAMA_OP_VERIFY_DRAFTS = 7
 } llama_op;
 
 /* RMSNorm over the feature axis ("Llama Architecture ...", Mathematical Foundations 1, with eps
@@ -271,6 +273,102 @@ int llama_gqa_attention_decode_paged(const llama_dims* dims, const void* q, cons
                                      const int32_t* seq_pos, int64_t max_pos, void* o, void* ws,
                                      size_t ws_bytes, void* stream);
 
+/* A serving step over the paged cache: sequences that each bring any number of new tokens (a chunk of
+ * a prompt, one token, or the last accepted token and the drafts behind it).  The new tokens are
+ * packed one sequence after the other: sequence b owns rows cu_new[b] .. cu_new[b+1]-1 of every
+ * per-token array.  In these calls' llama_dims B is the number of sequences and S the number of
+ * packed rows over all of them; rows from cu_new[B] on belong to no sequence and are left as they
+ * were, so that a captured step can run with fewer tokens than it has room for.  llama_paged_plan
+ * says where each token goes, llama_rope_append_paged puts it there, llama_gqa_attention_chunk_paged
+ * attends, llama_verify_drafts judges drafts.                                                    */
+
+/* Block tables and slot maps from the requests' lengths, on the device.
+ *   n_cached [B]     positions sequence b already holds (in its first ceil(n_cached / 128) pages)
+ *   n_new    [B]     tokens it brings (0 is allowed)
+ *   free_pages [n_free]  ids of pages no sequence holds, taken from the front in sequence order
+ *   block_table [B, max_pages]  in: the held pages; out: entries ceil(n_cached / 128) ..
+ *                    ceil((n_cached + n_new) / 128) - 1 of each row are set; no other is touched
+ *   cu_new [B + 1]   out: first packed row of each sequence, and the number of new tokens
+ *   positions, slots [n_tokens]  out: each packed row's position in its sequence and its row in the
+ *                    pool seen as [n_pages * 128] rows (128 * page + position % 128); -1 in both for
+ *                    rows from cu_new[B] on
+ *   pages_used [1]   out: pages needed from the free list
+ * All int32 device arrays, 4-byte aligned; none may overlap another.  Needs B <= 8192, n_pages <=
+ * 2^24 - 1, max_pages <= 2^17 (else LLAMA_ERR_UNSUPPORTED).  LLAMA_ERR_INVALID_ARG for negative
+ * counts, n_pages < 1, max_pages < 1 or NULL arrays.  Found on the device, and latched as
+ * LLAMA_ERR_INVALID_ARG in the device status word: a negative length or n_cached + n_new > 128 *
+ * max_pages (the sequence then brings no tokens), more new tokens than n_tokens (cu_new stops there),
+ * pages_used > n_free (block_table keeps its old entries past the free list, the tokens without a
+ * page get slot -1) and page ids outside [0, n_pages) (slot -1).                                 */
+int llama_paged_plan(const int32_t* n_cached, const int32_t* n_new, int64_t B, const int32_t* free_pages,
+                     int64_t n_free, int64_t n_pages, int32_t* block_table, int64_t max_pages,
+                     int64_t n_tokens, int32_t* cu_new, int32_t* positions, int32_t* slots,
+                     int32_t* pages_used, void* stream);
+
+/* RoPE at a position per token, and the new K and V rows written into the paged cache:
+ *   q_out[t] = R(positions[t]) q[t],  k_pool[slots[t]] = R(positions[t]) k[t],  v_pool[slots[t]] = v[t]
+ * with R as in llama_rope, for every packed row t < dims->S whose slot is not negative; other rows
+ * are skipped (nothing is written for them).
+ *   q [S, n_q, hd], k and v [S, n_kv, hd] bf16; consecutive tokens are q_stride, k_stride, v_stride
+ *   elements apart (multiples of 8, at least the row's width), so they may be views of one
+ *   projection's output; q_out [S, n_q, hd], contiguous (q itself is allowed when q_stride is
+ *   n_q * hd); k_pool, v_pool [n_pages, 128, n_kv, hd]; positions and slots [S] int32.
+ * q and q_out may both be NULL (append only), as may k, v, k_pool and v_pool (rotate only).  No two rows
+ * may name the same slot.  Positions must be in [0, 2^24) and slots below 128 * n_pages: a row that
+ * breaks this is skipped and latches LLAMA_ERR_INVALID_ARG in the device status word.  Uses S, n_q,
+ * n_kv, head_dim (a multiple of 8, at most 256) and theta_base.  bf16 only.                       */
+int llama_rope_append_paged(const llama_dims* dims, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                            const int32_t* slots, void* q_out, void* k_pool, void* v_pool, int64_t n_pages,
+                            void* stream);
+
+/* Causal GQA attention of the packed new tokens over a paged cache that already holds their K and V:
+ * the i-th new token of sequence b is at position n_cached[b] + i and attends to positions
+ * 0 .. n_cached[b] + i of its sequence.
+ *   q, o [S, n_q, hd] bf16, packed rows; k_pool, v_pool [n_pages, 128, n_kv, hd] bf16
+ *   block_table [B, max_pages], cu_new [B + 1] (non-decreasing from 0, at most S), n_cached [B]: int32
+ *   max_pos: an upper bound of every new token's position (host value; sizes the work split and the
+ *   workspace, llama_workspace_bytes(LLAMA_OP_GQA_ATTENTION_CHUNK_PAGED, dims, ..., kv_capacity =
+ *   max_pos + 1))
+ * Sequences may bring any number of tokens, none included; pages may be shared between sequences.
+ * Pool rows past a sequence's last position are never used, whatever they hold, and a key or value a
+ * query does not see never reaches it, infinite or NaN values included.  bf16, head_dim 64 or 128,
+ * n_q / n_kv <= 128, n_pages < 2^24 (else LLAMA_ERR_UNSUPPORTED).  Found on the device and latched as
+ * LLAMA_ERR_INVALID_ARG in the device status word: a page id outside [0, n_pages) among the entries a
+ * sequence uses, or a position above max_pos (the outputs of that sequence are then undefined; no
+ * other memory is touched).                                                                       */
+int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const void* k_pool,
+                                    const void* v_pool, int64_t n_pages, const int32_t* block_table,
+                                    int64_t max_pages, const int32_t* cu_new, const int32_t* n_cached,
+                                    int64_t max_pos, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* Verification of drafted tokens (rejection sampling, so that what is kept is distributed as draws
+ * from the target).  Row j of a sequence holds the logits after its j-th new token: it judges token
+ * j + 1, and the last row, which judges none, gives the token after the drafts.  With p = softmax(z / T)
+ * and q = softmax(y / T), z and y rows of logits and draft_logits:
+ *   a draft d = tokens[t + 1] is accepted while u[t] * q(d) < p(d);
+ *   at the first rejection the sequence's new token is argmax_i max(p_i - q_i, 0) / noise[b, i] (over p_i
+ *   / noise[b, i] if no p_i exceeds q_i);
+ *   with every draft accepted it is argmax_i p_i / noise[b, i] of the last row.
+ * noise holds independent draws of the exponential distribution with mean 1 (then the argmax is a draw
+ * in proportion to the weights), u uniform draws in [0, 1).  draft_logits NULL: drafts without a
+ * distribution, q = 1 at the draft and 0 elsewhere.  temperature <= 0: a draft is accepted when it is
+ * the argmax of z and the new token is the argmax (draft_logits, u and noise are not read).
+ *   logits [n_tokens, ld], draft_logits [n_tokens, draft_ld] fp32, first `vocab` entries used: finite
+ *   values or -inf, at least one finite per row; the last row of a sequence in draft_logits is not read
+ *   cu_new [B + 1] int32; tokens [n_tokens] int32, the packed new tokens; u [n_tokens], noise [B, noise_ld] fp32
+ *   n_accepted [B] int32: accepted drafts; 0 for a sequence without rows
+ *   out_tokens [n_tokens] int32: the accepted drafts from the sequence's first row on, then the new
+ *   token, then -1; rows from cu_new[B] on are left as they were
+ *   ws: llama_workspace_bytes(LLAMA_OP_VERIFY_DRAFTS, dims with S = n_tokens, ..., vocab) bytes
+ * Equal scores go to the lower id.  Probabilities are formed in fp32.  A draft outside [0, vocab) is
+ * rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.                           */
+int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, int64_t ld,
+                        const float* draft_logits, int64_t draft_ld, float temperature,
+                        const int32_t* cu_new, int64_t B, const int32_t* tokens, const float* u,
+                        const float* noise, int64_t noise_ld, int32_t* n_accepted, int32_t* out_tokens,
+                        void* ws, size_t ws_bytes, void* stream);
+
 /* Next-token choice from the LM head's logits ("LLaMA-3 8B 现代 LLM 架构、计算规模与能耗", section 十:
  * softmax over the vocabulary, then argmax, or a draw shaped by temperature, top-k and top-p).
  *   logits  [B, ld] fp32 (device), row b's first `vocab` entries used; finite values or -inf,
@@ -304,8 +402,9 @@ int llama_embed(int dtype, const void* table, int64_t vocab, int64_t d_model, co
 /* Synchronises `stream`, then reads and clears the device status word of the current device.
  * *out receives LLAMA_OK, LLAMA_ERR_TIMEOUT (a kernel's bounded wait ran out and it exited),
  * LLAMA_ERR_BOUNDS (bounds-checking builds: a kernel met an index outside its tensor) or
- * LLAMA_ERR_INVALID_ARG (llama_embed met a token id outside the table), in that order of
- * precedence when several were latched.
+ * LLAMA_ERR_INVALID_ARG (llama_embed or llama_verify_drafts met a token id outside the vocabulary, or
+ * a paged call lengths, pages or slots outside their range), in that order of precedence when several
+ * were latched.
  * Returns LLAMA_OK, or LLAMA_ERR_CUDA if the synchronisation or the copy failed.             */
 int llama_get_device_status(int* out, void* stream);
 

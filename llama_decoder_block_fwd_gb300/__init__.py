@@ -18,16 +18,17 @@ __all__ = [
     "llama_block_forward", "llama_stack_decode_step", "llama_workspace_bytes",
     "llama_sample", "llama_embed", "llama_kv_quantize", "llama_gqa_attention_decode_kv8",
     "llama_stack_decode_step_kv8", "llama_stack_decode_step_paged", "llama_gqa_attention_decode_paged",
+    "llama_paged_plan", "llama_rope_append_paged", "llama_gqa_attention_chunk_paged", "llama_verify_drafts",
     "llama_get_device_status", "llama_status_string", "llama_profile_enable", "llama_profile_read",
     "llama_selftest_bounded_wait", "llama_selftest_bounds", "llama_build_info", "BUILD_BOUNDS_CHECKS", "DEBUG_BUILD",
     "OP_RMSNORM", "OP_ROPE", "OP_GQA_ATTENTION", "OP_SWIGLU_FFN", "OP_BLOCK_FORWARD",
-    "OP_STACK_DECODE_STEP",
+    "OP_STACK_DECODE_STEP", "OP_GQA_ATTENTION_CHUNK_PAGED", "OP_VERIFY_DRAFTS",
 ]
 
 F32, BF16 = 0, 1
 X_F32, Y_F32 = 0x100, 0x200   # residual-stream flags for llama_block_forward's dtype (x fp32, y fp32)
 (OP_RMSNORM, OP_ROPE, OP_GQA_ATTENTION, OP_SWIGLU_FFN, OP_BLOCK_FORWARD,
- OP_STACK_DECODE_STEP) = range(6)
+ OP_STACK_DECODE_STEP, OP_GQA_ATTENTION_CHUNK_PAGED, OP_VERIFY_DRAFTS) = range(8)
 STATUS_NAMES = {0: "LLAMA_OK", 1: "LLAMA_ERR_INVALID_ARG", 2: "LLAMA_ERR_UNSUPPORTED",
                 3: "LLAMA_ERR_ALIGNMENT", 4: "LLAMA_ERR_WORKSPACE", 5: "LLAMA_ERR_CUDA",
                 6: "LLAMA_ERR_TIMEOUT", 7: "LLAMA_ERR_BOUNDS"}
@@ -93,6 +94,11 @@ def lib() -> ctypes.CDLL:
                 "llama_stack_decode_step_paged": [pd, i32, ctypes.POINTER(BlockWeights), vp, vp, i64, vp, vp, vp,
                                                   i64, vp, i64, vp, i64, vp, vp, sz, vp],
                 "llama_gqa_attention_decode_paged": [pd, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp],
+                "llama_paged_plan": [vp, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp],
+                "llama_rope_append_paged": [pd, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp],
+                "llama_gqa_attention_chunk_paged": [pd, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp],
+                "llama_verify_drafts": [vp, i64, i64, i64, vp, i64, ctypes.c_float, vp, i64, vp, vp, vp, i64, vp, vp,
+                                        vp, sz, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -266,6 +272,146 @@ def llama_gqa_attention_decode_paged(dims, q, k_pool, v_pool, block_table, seq_p
                                                   int(k_pool.shape[0]), _p(block_table), int(block_table.shape[1]),
                                                   _p(seq_pos), int(max_pos), _p(o), _p(ws), _nbytes(ws), _s(stream)),
            "llama_gqa_attention_decode_paged")
+
+
+def _check_tensors(where, dtype, **tensors):
+    """Refuse tensors whose element type or layout the call would misread: the library sees addresses
+    only.  Every tensor given must be contiguous, of torch's `dtype` and on the current device."""
+    import torch
+    dt, dev = getattr(torch, dtype), torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype is not dt:
+            raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        _on_device(where, name, t, dev)
+
+
+def _on_device(where, name, t, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{where}: expected a CUDA tensor, got {name} on {t.device}")
+    if t.device.index != dev:
+        raise ValueError(f"{where}: {name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _shape(where, name, t, shape):
+    """`shape` entries of None match any size."""
+    got = tuple(t.shape)
+    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        want = tuple("?" if w is None else w for w in shape)
+        raise ValueError(f"{where}: {name} must have shape {want}, got {got}")
+
+
+def _token_stride(where, name, t, heads, hd, rows, dev):
+    """The token stride of a [rows, heads, hd] bf16 view whose heads are contiguous."""
+    import torch
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{where}: {name} must be bfloat16, got {t.dtype}")
+    _on_device(where, name, t, dev)
+    _shape(where, name, t, (rows, heads, hd))
+    st = t.stride()
+    if rows and (st[2] != 1 or (heads > 1 and st[1] != hd)):
+        raise ValueError(f"{where}: the heads of {name} must be contiguous, got strides {st}")
+    return st[0] if rows > 1 else max(st[0], heads * hd)
+
+
+def llama_paged_plan(n_cached, n_new, free_pages, n_pages, block_table, cu_new, positions, slots, pages_used,
+                     stream=None):
+    """Extend block_table [B, max_pages] by the pages the new tokens need (from free_pages, in order) and
+    fill cu_new [B+1], positions [n_tokens], slots [n_tokens] and pages_used [1]; all int32."""
+    w = "llama_paged_plan"
+    _check_tensors(w, "int32", n_cached=n_cached, n_new=n_new, free_pages=free_pages, block_table=block_table,
+                   cu_new=cu_new, positions=positions, slots=slots, pages_used=pages_used)
+    B, T = int(n_cached.numel()), int(positions.numel())
+    _shape(w, "n_new", n_new, (B,))
+    _shape(w, "block_table", block_table, (B, None))
+    _shape(w, "cu_new", cu_new, (B + 1,))
+    _shape(w, "slots", slots, (T,))
+    if pages_used.numel() < 1:
+        raise ValueError(f"{w}: pages_used must hold one element")
+    _check(lib().llama_paged_plan(_p(n_cached), _p(n_new), B, _p(free_pages), int(free_pages.numel()), int(n_pages),
+                                  _p(block_table), int(block_table.shape[1]), T, _p(cu_new), _p(positions), _p(slots),
+                                  _p(pages_used), _s(stream)), w)
+
+
+def llama_rope_append_paged(dims, q, k, v, positions, slots, q_out, k_pool, v_pool, stream=None):
+    """q_out[t] = R(positions[t]) q[t]; k_pool / v_pool (as [n_pages * 128] rows) at slots[t] <- R k[t], v[t].
+    q [S, n_q, hd], k / v [S, n_kv, hd] may be views with a token stride; None, None for q, q_out (append
+    only) or for k, v, k_pool, v_pool (rotate only)."""
+    w = "llama_rope_append_paged"
+    import torch
+    d, dev = _d(dims), torch.cuda.current_device()
+    S, hd = d.S, d.head_dim
+    _check_tensors(w, "int32", positions=positions, slots=slots)
+    _check_tensors(w, "bfloat16", q_out=q_out, k_pool=k_pool, v_pool=v_pool)
+    _shape(w, "positions", positions, (S,))
+    _shape(w, "slots", slots, (S,))
+    qs = ks = vs = n_pages = 0
+    if q is not None and q_out is not None:
+        qs = _token_stride(w, "q", q, d.n_q, hd, S, dev)
+        _shape(w, "q_out", q_out, (S, d.n_q, hd))
+    if k is not None and v is not None and k_pool is not None and v_pool is not None:
+        ks = _token_stride(w, "k", k, d.n_kv, hd, S, dev)
+        vs = _token_stride(w, "v", v, d.n_kv, hd, S, dev)
+        _shape(w, "k_pool", k_pool, (None, 128, d.n_kv, hd))
+        _shape(w, "v_pool", v_pool, tuple(k_pool.shape))
+        n_pages = int(k_pool.shape[0])
+    _check(lib().llama_rope_append_paged(ctypes.byref(d), _p(q), qs, _p(k), ks, _p(v), vs, _p(positions), _p(slots),
+                                         _p(q_out), _p(k_pool), _p(v_pool), n_pages, _s(stream)), w)
+
+
+def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new, n_cached, max_pos, o, ws,
+                                    stream=None):
+    """Packed new tokens q [S, n_q, hd] over k_pool / v_pool [n_pages, 128, n_kv, hd] (one layer): sequence b
+    owns rows cu_new[b] .. cu_new[b+1]-1, at positions n_cached[b] onward; o [S, n_q, hd]."""
+    w = "llama_gqa_attention_chunk_paged"
+    d = _d(dims)
+    _check_tensors(w, "bfloat16", q=q, k_pool=k_pool, v_pool=v_pool, o=o)
+    _check_tensors(w, "int32", block_table=block_table, cu_new=cu_new, n_cached=n_cached)
+    _shape(w, "q", q, (d.S, d.n_q, d.head_dim))
+    _shape(w, "o", o, (d.S, d.n_q, d.head_dim))
+    _shape(w, "k_pool", k_pool, (None, 128, d.n_kv, d.head_dim))
+    _shape(w, "v_pool", v_pool, tuple(k_pool.shape))
+    _shape(w, "block_table", block_table, (d.B, None))
+    _shape(w, "cu_new", cu_new, (d.B + 1,))
+    _shape(w, "n_cached", n_cached, (d.B,))
+    _check(lib().llama_gqa_attention_chunk_paged(ctypes.byref(d), _p(q), _p(k_pool), _p(v_pool), int(k_pool.shape[0]),
+                                                 _p(block_table), int(block_table.shape[1]), _p(cu_new), _p(n_cached),
+                                                 int(max_pos), _p(o), _p(ws), _nbytes(ws), _s(stream)), w)
+
+
+def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, noise, n_accepted, out_tokens, ws,
+                        vocab=None, stream=None):
+    """Accept drafts by rejection sampling: logits / draft_logits fp32 [n_tokens, ld] (draft_logits may be
+    None), tokens int32 [n_tokens], u fp32 [n_tokens], noise fp32 [B, ld] exponential draws; fills
+    n_accepted int32 [B] and out_tokens int32 [n_tokens]."""
+    w = "llama_verify_drafts"
+    import torch
+    dev = torch.cuda.current_device()
+    T, B = int(tokens.numel()), int(n_accepted.numel())
+    V = int(logits.shape[1]) if vocab is None else int(vocab)
+    _check_tensors(w, "int32", cu_new=cu_new, tokens=tokens, n_accepted=n_accepted, out_tokens=out_tokens)
+    _check_tensors(w, "float32", u=u)
+    _shape(w, "cu_new", cu_new, (B + 1,))
+    _shape(w, "out_tokens", out_tokens, (T,))
+    if u is not None:
+        _shape(w, "u", u, (T,))
+    ld = [0, 0, 0]
+    for i, (name, t, rows) in enumerate((("logits", logits, T), ("draft_logits", draft_logits, T), ("noise", noise, B))):
+        if t is None:
+            continue
+        if t.dtype is not torch.float32:
+            raise ValueError(f"{w}: {name} must be float32, got {t.dtype}")
+        _on_device(w, name, t, dev)
+        _shape(w, name, t, (rows, None))
+        if t.shape[1] < V or (V > 1 and t.stride(1) != 1):
+            raise ValueError(f"{w}: the rows of {name} must hold {V} contiguous entries")
+        ld[i] = max(int(t.stride(0)), V) if rows <= 1 else int(t.stride(0))
+    _check(lib().llama_verify_drafts(_p(logits), T, V, ld[0], _p(draft_logits), ld[1], float(temperature), _p(cu_new), B,
+                                     _p(tokens), _p(u), _p(noise), ld[2], _p(n_accepted), _p(out_tokens), _p(ws),
+                                     _nbytes(ws), _s(stream)), w)
 
 
 def llama_workspace_bytes(op, dims, dtype, n_layers=0, vocab=0, kv_capacity=0) -> int:

@@ -728,6 +728,13 @@ int decode_stack_tc(const llama_dims* d, int n_layers, const llama_block_weights
   return run_gemm(g, "gemm_lm_head", st);
 }
 
+// The shapes the paged chunk attention handles: the bf16 pools' head widths, and the query heads of one
+// KV group within one 128-row tile.
+bool chunk_dims_ok(const llama_dims* d, int dtype) {
+  return dtype == LLAMA_BF16 && d->B > 0 && d->S > 0 && d->n_q > 0 && d->n_kv > 0 && d->n_q % d->n_kv == 0 &&
+         (d->head_dim == 64 || d->head_dim == 128) && d->n_q / d->n_kv <= 128;
+}
+
 }  // namespace
 LLAMA_DEFINE_BOUNDS_READER(api)
 
@@ -799,11 +806,12 @@ int llama_get_device_status(int* out, void* stream) {
     bounds = bounds_read_clear_api() | bounds_read_clear_kernels_simt() | bounds_read_clear_gemm_tc() |
              bounds_read_clear_gemm_tc2() | bounds_read_clear_gemm_skinny() | bounds_read_clear_attn_tc() |
              bounds_read_clear_decode_attn() | bounds_read_clear_decode_attn8() | bounds_read_clear_decode_fin() |
-             bounds_read_clear_sample() | bounds_read_clear_selftest();
+             bounds_read_clear_sample() | bounds_read_clear_selftest() | bounds_read_clear_paged() |
+             bounds_read_clear_chunk_attn() | bounds_read_clear_verify();
   *out = (v & STATUS_TIMEOUT) ? LLAMA_ERR_TIMEOUT
          : bounds             ? LLAMA_ERR_BOUNDS
-         : (v & STATUS_BAD_TOKEN) ? LLAMA_ERR_INVALID_ARG
-                                  : LLAMA_OK;
+         : (v & (STATUS_BAD_TOKEN | STATUS_BAD_PLAN)) ? LLAMA_ERR_INVALID_ARG
+                                                      : LLAMA_OK;
   return LLAMA_OK;
 }
 
@@ -839,7 +847,7 @@ int llama_embed(int dtype, const void* table, int64_t vocab, int64_t d_model, co
 
 size_t llama_workspace_bytes(int op, const llama_dims* d, int dtype, int n_layers, int64_t vocab,
                              int64_t kv_capacity) {
-  (void)n_layers; (void)vocab;
+  (void)n_layers;
   if (!d || check_dtype(dtype) != LLAMA_OK) return 0;
   const size_t es = esize(dtype);
   switch (op) {
@@ -849,6 +857,10 @@ size_t llama_workspace_bytes(int op, const llama_dims* d, int dtype, int n_layer
     case LLAMA_OP_STACK_DECODE_STEP:
       return decode_tc_path(d, dtype) ? plan_decode_tc(d, nullptr, kv_capacity).bytes
                                       : plan_decode(d, dtype, nullptr, kv_capacity).bytes;
+    case LLAMA_OP_GQA_ATTENTION_CHUNK_PAGED:
+      return chunk_dims_ok(d, dtype) ? chunk_attn_ws_bytes(d->B, d->S, d->n_q, d->n_kv, d->head_dim, kv_capacity - 1) : 0;
+    case LLAMA_OP_VERIFY_DRAFTS:
+      return d->S > 0 && vocab > 0 && verify_supported(d->S, vocab) ? verify_ws_bytes(d->S, vocab) : 0;
     default: return 0;
   }
 }
@@ -1143,6 +1155,128 @@ int llama_kv_quantize(const void* x, int64_t n_tokens, int64_t n_kv, int64_t hea
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof::begin("kv_quantize", st);
   const int rc = launch_kv_quantize(x, scale, codes, n_tokens * n_kv * head_dim, (int)n_kv, (int)head_dim, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_paged_plan(const int32_t* n_cached, const int32_t* n_new, int64_t B, const int32_t* free_pages,
+                     int64_t n_free, int64_t n_pages, int32_t* block_table, int64_t max_pages, int64_t n_tokens,
+                     int32_t* cu_new, int32_t* positions, int32_t* slots, int32_t* pages_used, void* stream) {
+  if (B < 0 || n_free < 0 || n_pages < 1 || max_pages < 1 || n_tokens < 0) return LLAMA_ERR_INVALID_ARG;
+  if (B > kPlanMaxSeqs || n_pages > INT32_MAX / 128 || max_pages > kMaxPos / 128 || n_free > INT32_MAX ||
+      n_tokens > INT32_MAX - 1)
+    return LLAMA_ERR_UNSUPPORTED;
+  if (!cu_new || !pages_used || (n_tokens > 0 && (!positions || !slots)) || (n_free > 0 && !free_pages) ||
+      (B > 0 && (!n_cached || !n_new || !block_table)))
+    return LLAMA_ERR_INVALID_ARG;
+  const void* ps[8] = {n_cached, n_new, free_pages, block_table, cu_new, positions, slots, pages_used};
+  for (const void* p : ps)
+    if ((uintptr_t)p & 3) return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("paged_plan", st);
+  const int rc = launch_paged_plan(n_cached, n_new, free_pages, B, n_free, n_pages, max_pages, block_table, n_tokens,
+                                   cu_new, positions, slots, pages_used, num_sms(), status, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_rope_append_paged(const llama_dims* d, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const int32_t* positions, const int32_t* slots,
+                            void* q_out, void* k_pool, void* v_pool, int64_t n_pages, void* stream) {
+  int rc;
+  if ((rc = check_dims(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if (d->head_dim % 8 != 0 || d->S > INT32_MAX - 8 || d->n_q > 4096 || d->n_kv > 4096) return LLAMA_ERR_UNSUPPORTED;
+  if (!k != !v || !k != !k_pool || !k != !v_pool || !q != !q_out) return LLAMA_ERR_INVALID_ARG;
+  if ((q && q_stride < d->n_q * d->head_dim) || (k && (k_stride < d->n_kv * d->head_dim || v_stride < d->n_kv * d->head_dim)))
+    return LLAMA_ERR_INVALID_ARG;
+  if (q && q_out == q && q_stride != d->n_q * d->head_dim) return LLAMA_ERR_INVALID_ARG;
+  if (k && (n_pages < 1 || n_pages > INT32_MAX / 128)) return n_pages < 1 ? LLAMA_ERR_INVALID_ARG : LLAMA_ERR_UNSUPPORTED;
+  if (d->S == 0 || (!q && !k)) return LLAMA_OK;
+  if (!positions || !slots) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[6] = {q, k, v, q_out, k_pool, v_pool};
+  for (const void* p : ps)
+    if (!aligned16(p)) return LLAMA_ERR_ALIGNMENT;
+  if ((q && q_stride % 8) || (k && (k_stride % 8 || v_stride % 8)) || ((uintptr_t)positions & 3) || ((uintptr_t)slots & 3))
+    return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  RopeFreq f[kMaxRopePairs];
+  rope_freqs(d, f);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("rope_append_paged", st);
+  // without a pool a row is live when its slot is not negative, whatever its value
+  rc = launch_rope_append(q, q_stride, k, k_stride, v, v_stride, positions, slots, q_out, k_pool, v_pool, d->S, d->n_q,
+                          d->n_kv, (int)d->head_dim, k ? n_pages : INT32_MAX / 128, f, num_sms(), status, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_gqa_attention_chunk_paged(const llama_dims* d, const void* q, const void* k_pool, const void* v_pool,
+                                    int64_t n_pages, const int32_t* block_table, int64_t max_pages,
+                                    const int32_t* cu_new, const int32_t* n_cached, int64_t max_pos, void* o, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if (n_pages < 1 || max_pages < 1 || max_pos < 0 || max_pos + 1 > max_pages * 128 || max_pos + 1 > kMaxPos)
+    return LLAMA_ERR_INVALID_ARG;
+  if (n_pages > INT32_MAX / 128 || max_pages > INT32_MAX) return LLAMA_ERR_UNSUPPORTED;
+  if (d->B == 0 || d->S == 0) return LLAMA_OK;
+  if (!chunk_dims_ok(d, LLAMA_BF16)) return LLAMA_ERR_UNSUPPORTED;
+  if (!q || !k_pool || !v_pool || !block_table || !cu_new || !n_cached || !o) return LLAMA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(o) || ((uintptr_t)block_table & 3) ||
+      ((uintptr_t)cu_new & 3) || ((uintptr_t)n_cached & 3))
+    return LLAMA_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < chunk_attn_ws_bytes(d->B, d->S, d->n_q, d->n_kv, d->head_dim, max_pos)) return LLAMA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  ChunkAttnDesc a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.k_pool = k_pool; a.v_pool = v_pool; a.o = o;
+  a.B = d->B; a.T = d->S; a.n_q = d->n_q; a.n_kv = d->n_kv; a.hd = d->head_dim;
+  a.n_pages = n_pages; a.max_pages = max_pages; a.max_pos = max_pos;
+  a.block_table = block_table; a.cu_new = cu_new; a.n_cached = n_cached;
+  a.scale = (float)(1.0 / std::sqrt((double)d->head_dim));
+  a.ws = ws;
+  a.status = status_ptr();
+  if (!a.status) return LLAMA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("attn_chunk_paged", st);
+  rc = launch_chunk_attn(a, num_sms(), st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, int64_t ld, const float* draft_logits,
+                        int64_t draft_ld, float temperature, const int32_t* cu_new, int64_t B, const int32_t* tokens,
+                        const float* u, const float* noise, int64_t noise_ld, int32_t* n_accepted, int32_t* out_tokens,
+                        void* ws, size_t ws_bytes, void* stream) {
+  if (B < 0 || n_tokens < 0 || vocab < 1 || vocab > (int64_t(1) << 30) || ld < vocab || std::isnan(temperature))
+    return LLAMA_ERR_INVALID_ARG;
+  const bool draw = temperature > 0.f;
+  if ((draw && noise_ld < vocab) || (draw && draft_logits && draft_ld < vocab)) return LLAMA_ERR_INVALID_ARG;
+  if (B > INT32_MAX / 16 || n_tokens > INT32_MAX || !verify_supported(n_tokens, vocab)) return LLAMA_ERR_UNSUPPORTED;
+  if (B == 0) return LLAMA_OK;
+  if (!cu_new || !n_accepted) return LLAMA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!logits || !tokens || !out_tokens || (draw && (!u || !noise)))) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[8] = {logits, draft_logits, cu_new, tokens, u, noise, n_accepted, out_tokens};
+  for (const void* p : ps)
+    if ((uintptr_t)p & 3) return LLAMA_ERR_ALIGNMENT;
+  if (n_tokens > 0 && (!ws || ws_bytes < verify_ws_bytes(n_tokens, vocab))) return LLAMA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  VerifyDesc v;
+  memset(&v, 0, sizeof(v));
+  v.logits = logits; v.draft_logits = draft_logits;
+  v.T = n_tokens; v.V = vocab; v.B = B; v.ld = ld; v.draft_ld = draft_ld; v.noise_ld = noise_ld;
+  v.temperature = temperature;
+  v.cu_new = cu_new; v.tokens = tokens; v.u = u; v.noise = noise;
+  v.n_accepted = n_accepted; v.out_tokens = out_tokens;
+  v.ws = ws;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("verify_drafts", st);
+  const int rc = launch_verify(v, num_sms(), status, st);
   prof::end(st);
   return rc ? LLAMA_ERR_CUDA : launch_status();
 }

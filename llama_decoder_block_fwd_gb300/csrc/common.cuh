@@ -14,7 +14,7 @@ namespace llama {
 
 // ---------------------------------------------------------------- status word
 // Bit flags latched by kernels; read and cleared by llama_get_device_status().
-enum : unsigned { STATUS_TIMEOUT = 1u, STATUS_BAD_TOKEN = 2u };
+enum : unsigned { STATUS_TIMEOUT = 1u, STATUS_BAD_TOKEN = 2u, STATUS_BAD_PLAN = 4u };
 
 // ---------------------------------------------------------------- bounds checks (-DLLAMA_DEBUG)
 // Built with -DLLAMA_DEBUG, the kernels check every global store's index range and every TMA box

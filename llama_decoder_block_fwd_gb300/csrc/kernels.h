@@ -25,6 +25,9 @@ unsigned bounds_read_clear_decode_attn8();
 unsigned bounds_read_clear_decode_fin();
 unsigned bounds_read_clear_sample();
 unsigned bounds_read_clear_selftest();
+unsigned bounds_read_clear_paged();
+unsigned bounds_read_clear_chunk_attn();
+unsigned bounds_read_clear_verify();
 
 // What a GEMM does with its fp32 result D[r, c] (r < M, c < N).
 enum EpiKind : int {
@@ -202,6 +205,47 @@ int launch_sample(const float* logits, int64_t B, int64_t V, int64_t ld, float t
                   float top_p, const float* u, int* tokens, cudaStream_t st);
 int launch_embed(int dtype, const void* table, int64_t V, int64_t d, const int* tokens, int64_t n, void* x,
                  unsigned* status, cudaStream_t st);
+
+// paged.cu: where new tokens go in a paged cache, and writing them there
+constexpr int64_t kPlanMaxSeqs = 8192;   // the plan keeps two integers per sequence in shared memory
+int launch_paged_plan(const int* n_cached, const int* n_new, const int* free_pages, int64_t B, int64_t n_free,
+                      int64_t n_pages, int64_t max_pages, int* block_table, int64_t n_tokens, int* cu_new,
+                      int* positions, int* slots, int* pages_used, int num_sms, unsigned* status, cudaStream_t st);
+int launch_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, const int* positions, const int* slots, void* q_out, void* k_pool,
+                       void* v_pool, int64_t T, int64_t n_q, int64_t n_kv, int hd, int64_t n_pages,
+                       const RopeFreq* freq, int num_sms, unsigned* status, cudaStream_t st);
+
+// chunk_attn.cu: attention of packed new tokens over a paged cache (bf16, hd 64 or 128)
+struct ChunkAttnDesc {
+  const void* q;          // [T, n_q, hd]
+  const void* k_pool;     // [n_pages, 128, n_kv, hd]
+  const void* v_pool;
+  void* o;                // [T, n_q, hd]
+  int64_t B, T, n_q, n_kv, hd, n_pages, max_pages, max_pos;
+  const int* block_table; // [B, max_pages]
+  const int* cu_new;      // [B + 1]
+  const int* n_cached;    // [B]
+  float scale;
+  void* ws;
+  unsigned* status;
+};
+size_t chunk_attn_ws_bytes(int64_t B, int64_t T, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_pos);
+int launch_chunk_attn(const ChunkAttnDesc& a, int num_sms, cudaStream_t st);
+
+// verify.cu: drafted tokens against the target's probabilities
+struct VerifyDesc {
+  const float *logits, *draft_logits;   // [T, ld], [T, draft_ld] (may be null)
+  int64_t T, V, B, ld, draft_ld, noise_ld;
+  float temperature;
+  const int *cu_new, *tokens;           // [B + 1], [T]
+  const float *u, *noise;               // [T], [B, noise_ld]
+  int *n_accepted, *out_tokens;         // [B], [T]
+  void* ws;
+};
+bool verify_supported(int64_t T, int64_t V);
+size_t verify_ws_bytes(int64_t T, int64_t V);
+int launch_verify(const VerifyDesc& d, int num_sms, unsigned* status, cudaStream_t st);
 
 // The current device's status word (device address) and SM count.
 unsigned* status_ptr();
