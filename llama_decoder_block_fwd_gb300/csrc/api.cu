@@ -732,7 +732,8 @@ int decode_stack_tc(const llama_dims* d, int n_layers, const llama_block_weights
 // KV group within one 128-row tile.
 bool chunk_dims_ok(const llama_dims* d, int dtype) {
   return dtype == LLAMA_BF16 && d->B > 0 && d->S > 0 && d->n_q > 0 && d->n_kv > 0 && d->n_q % d->n_kv == 0 &&
-         (d->head_dim == 64 || d->head_dim == 128) && d->n_q / d->n_kv <= 128;
+         (d->head_dim == 64 || d->head_dim == 128) && d->n_q / d->n_kv <= 128 &&
+         chunk_attn_supported(d->B, d->S, d->n_q, d->n_kv);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "attn_common.cuh"
 #include "kernels.h"
 
 namespace llama {
@@ -32,7 +33,6 @@ namespace {
 
 constexpr int AT_THREADS = 320;
 constexpr uint32_t TMEM_COLS_ATTN = 512;
-constexpr float kRescaleLog2 = 8.0f;
 
 struct AttnParams {   // 128-byte aligned by its tensor maps
   CUtensorMap tmQ;   // [B*S, n_q, hd], box (64, r, 128/r)
@@ -55,77 +55,6 @@ struct Smem {
   static constexpr uint32_t OFF_BAR = OFF_V + 2 * KV;
   static constexpr uint32_t TOTAL = OFF_BAR + 256 + 1024;
 };
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z,
-                                            int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// 2^x with one MUFU instruction (PTX ex2.approx.ftz: relative error about 2^-22, subnormal
-// results flushed to zero -- exact enough for P, which is rounded to bf16).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-}
-
-// Packed pairs of fp32 (sm_100 and later): (d0, d1) = (a0 b0 + c0, a1 b1 + c1) in one instruction,
-// and (s0, s1) += (a0, a1).
-__device__ __forceinline__ void fma_f32x2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0,
-                                          float c1) {
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-__device__ __forceinline__ void add_f32x2(float& s0, float& s1, float a0, float a1) {
-  asm("{\n\t.reg .b64 ra, rs;\n\t"
-      "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%0, %1};\n\t"
-      "add.rn.f32x2 rs, rs, ra;\n\tmov.b64 {%0, %1}, rs;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(a0), "f"(a1));
-}
-
-// 32 scores of a row -> 16 bf16 pairs of P = 2^(s * scale - m) stored at TMEM column `col`; the
-// fp32 values are added to the row sums.  The scaling and the sums run on packed pairs.
-__device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t col, float scale, float m, float& ls0,
-                                          float& ls1) {
-  uint32_t w[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    float a0, a1;
-    fma_f32x2(a0, a1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), scale, scale, -m, -m);
-    const float p0 = ex2(a0);
-    const float p1 = ex2(a1);
-    add_f32x2(ls0, ls1, p0, p1);
-    w[e] = pack_bf16x2(p0, p1);
-  }
-  tmem_st16(col, w);
-}
 
 template <int HD>
 __global__ void __launch_bounds__(AT_THREADS, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {

@@ -1,60 +1,854 @@
 // Causal GQA attention of ragged chunks of new tokens over a paged KV cache ("Llama Architecture
 // ...", Mathematical Foundations 4; "LLaMA-3 8B ...", section 四.4): token i of sequence b sits at
-// position c_b + i and attends to positions 0 .. c_b + i of its sequence.
+// position c_b + i and attends to positions 0 .. c_b + i of its sequence,
+//     o = sum_j softmax_j(q . k_j / sqrt(hd)) v_j,
+// taken over 128-key tiles (one page each) with a running maximum and sum.
+//
+// One form for every mix of lengths, from one token against a long cache (bound by reading K and V
+// once) to long prompts (bound by the tensor cores):
+//   * A Q tile is 128 rows: (128 / r) consecutive tokens x the r query heads of one KV group.  An item is
+//     a pair of adjacent Q tiles of one (sequence, KV group), which share every K/V tile staged; a
+//     sequence's only or odd last Q tile is an item by itself.  Its key tiles then alternate between
+//     the two softmax groups (even tiles, odd tiles), each with its own O, merged at the end, so that
+//     the two groups still take turns with the tensor core.
+//   * chunk_plan_kernel cuts the items' key ranges into units: a sequence's tiles into n_chunk equal
+//     parts of at least one tile, as many as make the units come out even over the SMs (see there).
+//   * chunk_attn_kernel: one CTA per SM takes units from a counter.  Warp 0 fetches units and runs TMA
+//     (Q tiles through two slots, K and V tiles through one ring of slots, across unit borders), warp 1
+//     issues the MMAs, warps 2-5 / 6-9 are the softmax groups, one thread per row (TMEM lane).  A unit
+//     that holds all of its item's keys stores o; otherwise it leaves (m, l, O) in the workspace.
+//   * chunk_combine_kernel merges the parts of the rows that were cut.
+// TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
+#include "attn_common.cuh"
 #include "kernels.h"
 
 namespace llama {
 namespace {
 
-// One warp per (token, query head), lanes over the head dimension, running maximum and sum.
-__global__ void chunk_attn_simt_kernel(const __grid_constant__ ChunkAttnDesc a) {
+constexpr int CA_THREADS = 320;
+constexpr uint32_t CA_TMEM_COLS = 512;
+constexpr int CP_THREADS = 1024;
+
+// Per sequence, written by the plan.
+struct ChunkSeq {
+  int unit0;          // first unit
+  int lo, n, c;       // first packed row, new tokens, cached positions
+  int np;             // items per KV group: pairs of Q tiles
+  int nc, ct;         // key chunks and tiles per chunk
+  int part0;          // first partial row (nc > 1): partial row of token i in chunk k is part0 + k * n + i
+  int split0;         // rows of cut sequences before this one (cut: nc > 1)
+};
+struct ChunkHead {
+  int n_units, counter, n_split, pad;
+};
+
+struct ChunkParams {   // 128-byte aligned by its tensor maps
+  CUtensorMap tmQ;     // [T, n_q, hd], box (64, r, tpt)
+  CUtensorMap tmK;     // [n_pages, 128, n_kv, hd], box (64, 1, 128, 1)
+  CUtensorMap tmV;
+  uint16_t* o;         // [T, n_q, hd]
+  const uint16_t* v_pool;
+  const int *block_table, *cu_new, *n_cached;
+  int B, T, n_q, n_kv, r, tpt, n_pages, max_pages, max_pos;
+  float scale_log2;    // log2(e) / sqrt(hd)
+  ChunkHead* head;
+  ChunkSeq* seq;
+  float* part_o;       // [part_rows, n_q, hd]
+  float2* part_ml;     // [part_rows, n_q]  (m in log2 units, l)
+  int part_rows, grid;
+  unsigned* status;
+};
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// The last b of B (a power-of-32 search by one warp) with key(b) <= x; key is non-decreasing, key(0) <= x.
+template <typename F>
+__device__ __forceinline__ int warp_search(int B, int x, F&& key) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int t = (int)(w / a.n_q), h = (int)(w % a.n_q), g = h / (int)(a.n_q / a.n_kv);
-  if (t >= a.T || t >= a.cu_new[a.B]) return;
-  int b = 0;
-  while (b + 1 < a.B && a.cu_new[b + 1] <= t) ++b;
-  const int pos = a.n_cached[b] + t - a.cu_new[b];
-  if (pos < 0 || pos > a.max_pos) {
-    if (lane == 0) atomicOr(a.status, STATUS_BAD_PLAN);
-    return;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = cdiv(n, 32), at = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < n && key(lo + at) <= x);
+    const int k = 31 - __clz(le);     // lane 0 always holds
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  const int hd = (int)a.hd, per = hd / 32;
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((int64_t)t * a.n_q + h) * hd;
-  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int e = 0; e < per; ++e) qv[e] = bf2f(q[lane + 32 * e]) * a.scale;
-  for (int j = 0; j <= pos; ++j) {
-    const int page = a.block_table[(int64_t)b * a.max_pages + j / 128];
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) atomicOr(a.status, STATUS_BAD_PLAN);
-      return;
-    }
-    const int64_t row = (((int64_t)page * 128 + j % 128) * a.n_kv + g) * hd;
-    float s = 0.f;
-    for (int e = 0; e < per; ++e) s += qv[e] * bf2f(static_cast<const uint16_t*>(a.k_pool)[row + lane + 32 * e]);
+  return lo;
+}
+
+// ------------------------------------------------------------------------------------------ plan
+// A sequence of n new tokens after c cached has np = ceil(n / (2 tpt)) items per KV group of nt =
+// ceil((c + n) / 128) key tiles or less.  With at most C tiles per unit its ranges are cut into nc =
+// ceil(nt / C).  C is the candidate of least estimated time, in units of one tile's time:
+//   units in rounds of one per CTA x (mean unit + kUnitCost), at least the longest unit, + the
+//   merge if anything is cut,
+// where a unit costs kUnitCost more than its tiles (its pipeline fills and drains) and kCutCost more
+// when it leaves partials.  The candidates run from 1 tile to all in steps of sqrt(2), one per warp;
+// those whose partials do not fit the workspace are out, the last (nothing cut) always fits.
+constexpr float kUnitCost = 1.5f, kCutCost = 1.5f, kMergeCost = 3.0f;
+
+struct SeqShape { int lo, n, c, np, nt; bool bad; };
+__device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b) {
+  SeqShape s;
+  s.lo = __ldg(p.cu_new + b);
+  const int hi = __ldg(p.cu_new + b + 1);
+  s.c = __ldg(p.n_cached + b);
+  s.n = hi - s.lo;
+  s.bad = s.lo < 0 || s.n < 0 || hi > p.T || (s.n > 0 && (s.c < 0 || (int64_t)s.c + s.n - 1 > p.max_pos));
+  if (s.bad || s.n == 0) { s.n = 0; s.np = 0; s.nt = 0; s.c = 0; return s; }
+  s.np = cdiv(s.n, 2 * p.tpt);
+  s.nt = cdiv(s.c + s.n, 128);
+  return s;
+}
+
+__device__ __forceinline__ void cut(int nt, int C, int& nc, int& ct) {
+  nc = max(1, cdiv(nt, C));
+  ct = max(1, cdiv(nt, nc));
+  nc = max(1, cdiv(nt, ct));
+}
+
+__global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ float est[32];
+  __shared__ int warp_sum[3][32];
+  __shared__ int chosen;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  // candidate of warp w: about 2^(w / 2) tiles, the last one unbounded
+  const int C = warp == 31 ? INT_MAX / 2 : (warp & 1) ? (3 << (warp >> 1)) >> 1 : 1 << (warp >> 1);
+  float units = 0.f, cost = 0.f, longest = 0.f;
+  int64_t rows = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const SeqShape s = seq_shape(p, b);
+    if (s.n == 0) continue;
+    int nc, ct;
+    cut(s.nt, C, nc, ct);
+    const float mean = fminf((float)s.nt, ((float)s.c + 0.5f * (float)(s.n + min(s.n, 2 * p.tpt))) * (1.f / 128.f) + 0.5f);
+    const float k = fmaxf(1.f, mean / (float)ct);             // units per item
+    const float items = (float)s.np * (float)p.n_kv;
+    const float over = kUnitCost + (nc > 1 ? kCutCost : 0.f);
+    units += items * k;
+    cost += items * (mean + k * over);
+    longest = fmaxf(longest, (float)min(ct, s.nt) + over);
+    if (nc > 1) rows += (int64_t)nc * s.n;
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s), c = expf(m - mn), pv = expf(s - mn);
-    m = mn;
-    l = l * c + pv;
-    for (int e = 0; e < per; ++e)
-      acc[e] = acc[e] * c + pv * bf2f(static_cast<const uint16_t*>(a.v_pool)[row + lane + 32 * e]);
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    cost += __shfl_xor_sync(0xffffffffu, cost, o);
+    longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    rows += __shfl_xor_sync(0xffffffffu, rows, o);
   }
-  uint16_t* o = static_cast<uint16_t*>(a.o) + ((int64_t)t * a.n_q + h) * hd;
-  for (int e = 0; e < per; ++e) o[lane + 32 * e] = f2bf(acc[e] / l);
+  if (lane == 0) {
+    float e = units > 0.f ? fmaxf(longest, ceilf(units / (float)p.grid) * cost / units) : 0.f;
+    if (rows > 0) e += kMergeCost;
+    est[warp] = rows <= p.part_rows ? e : INFINITY;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int best = 31;
+    for (int w = 30; w >= 0; --w)
+      if (est[w] < est[best]) best = w;
+    chosen = best;
+  }
+  __syncthreads();
+  const int pick = chosen;
+  const int Cp = pick == 31 ? INT_MAX / 2 : (pick & 1) ? (3 << (pick >> 1)) >> 1 : 1 << (pick >> 1);
+  // ---- exclusive prefix sums of (units, partial rows, cut rows) over contiguous runs of sequences
+  const int per = cdiv(p.B, CP_THREADS);
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int v[3] = {0, 0, 0};
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const SeqShape s = seq_shape(p, b);
+    bad = bad || s.bad;
+    int nc, ct;
+    cut(s.nt, Cp, nc, ct);
+    v[0] += s.n ? nc * s.np * p.n_kv : 0;
+    v[1] += nc > 1 ? nc * s.n : 0;
+    v[2] += nc > 1 ? s.n : 0;
+  }
+  if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
+  int incl[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    incl[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += y;
+    }
+    if (lane == 31) warp_sum[i][warp] = incl[i];
+  }
+  __syncthreads();
+  int at[3], total[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int before = 0, all = 0;
+    for (int w = 0; w < CP_THREADS / 32; ++w) {
+      if (w < warp) before += warp_sum[i][w];
+      all += warp_sum[i][w];
+    }
+    at[i] = before + incl[i] - v[i];
+    total[i] = all;
+  }
+  for (int b = b0; b < b1; ++b) {
+    const SeqShape s = seq_shape(p, b);
+    ChunkSeq r;
+    cut(s.nt, Cp, r.nc, r.ct);
+    r.unit0 = at[0];
+    r.lo = s.lo; r.n = s.n; r.c = s.c; r.np = s.np;
+    r.part0 = at[1];
+    r.split0 = at[2];
+    if (in_extent(b, 1, p.B)) p.seq[b] = r;
+    at[0] += s.n ? r.nc * s.np * p.n_kv : 0;
+    at[1] += r.nc > 1 ? r.nc * s.n : 0;
+    at[2] += r.nc > 1 ? s.n : 0;
+  }
+  if (tid == 0) {
+    ChunkHead h;
+    h.n_units = total[0];
+    h.counter = p.grid;      // unit i < grid is CTA i's first
+    h.n_split = total[2];
+    h.pad = 0;
+    *p.head = h;
+  }
+}
+
+// ------------------------------------------------------------------------------------- attention
+template <int HD>
+struct CaSmem {
+  static constexpr uint32_t TILE = 128 * HD * 2;             // one Q, K or V tile
+  static constexpr int SLOTS = HD == 128 ? 5 : 10;           // K/V ring: 160 KB
+  static constexpr uint32_t OFF_Q = 0;                       // 2 Q tiles
+  static constexpr uint32_t OFF_KV = 2 * TILE;
+  static constexpr uint32_t OFF_ML = OFF_KV + SLOTS * TILE;  // group 1's (m, l) of a lone Q tile
+  static constexpr uint32_t OFF_UNIT = OFF_ML + 128 * 8;     // 2 unit records
+  static constexpr uint32_t OFF_BAR = OFF_UNIT + 2 * 64;
+  static constexpr uint32_t TOTAL = OFF_BAR + 384 + 1024;
+};
+
+// One unit, as the roles of a CTA see it.
+struct __align__(16) ChunkUnit {
+  int live;            // 0: no more units
+  int t0;              // first key tile
+  int n0, n1;          // rounds of groups 0 and 1
+  int lone;            // 1: one Q tile, key tiles alternate between the groups
+  int row0, row1;      // first packed row of each group's Q tile
+  int end;             // the sequence's end row
+  int pos_off;         // position = packed row + pos_off
+  int g;               // KV group
+  int kv_len;          // keys of the sequence
+  int clean;           // tiles from here on hold keys that some row of the unit does not see
+  int part;            // partial row = packed row + part; INT_MIN: store o
+  int b;
+  int pad0, pad1;
+};
+static_assert(sizeof(ChunkUnit) == 64, "unit record");
+
+// Element-wise: non-finite bf16 values of a 16-byte piece replaced by 0; returns whether there were any.
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
+  const uint32_t f = nonfinite_bits(w);
+  if (f & 0x8000u) w &= 0xFFFF0000u;
+  if (f & 0x80000000u) w &= 0x0000FFFFu;
+  return w;
+}
+
+// The non-finite values among keys j0..j1 of sequence b, added to the row stored at `at` (which was summed
+// without them).  Called for tiles at a sequence's end only, and only when one was met.
+template <int HD>
+__device__ __noinline__ void add_nonfinite(const ChunkParams& p, int b, int g, int j0, int j1, int64_t at, bool part) {
+  for (int j = j0; j <= j1; ++j) {
+    const int page = p.block_table[(int64_t)b * p.max_pages + j / 128];
+    if (page < 0 || page >= p.n_pages) continue;
+    const uint16_t* vr = p.v_pool + (((int64_t)page * 128 + j % 128) * p.n_kv + g) * HD;
+    for (int k = 0; k < HD; ++k) {
+      const float a = bf2f(vr[k]);
+      if (fabsf(a) < INFINITY) continue;
+      if (part) p.part_o[at * HD + k] += a;
+      else p.o[at * HD + k] = f2bf(bf2f(p.o[at * HD + k]) + a);
+    }
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_constant__ ChunkParams p) {
+  using L = CaSmem<HD>;
+  constexpr int HALVES = HD / 64;
+  constexpr int NS = L::SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* q_full = bars + 0;       // [2] per Q slot
+  uint64_t* q_empty = bars + 2;      // [2]
+  uint64_t* u_full = bars + 4;       // [2] per unit record
+  uint64_t* u_empty = bars + 6;      // [2] (MMA thread + 8 softmax warps)
+  uint64_t* s_full = bars + 8;       // [2] per group
+  uint64_t* p_full = bars + 10;      // [2] (128 arrivals)
+  uint64_t* o_done = bars + 12;      // [2]
+  uint64_t* o_free = bars + 14;      // [2] (128 arrivals)
+  uint64_t* ml_full = bars + 16;     //     (128 arrivals)
+  uint64_t* drain = bars + 17;
+  uint64_t* kv_full = bars + 18;     // [NS]
+  uint64_t* kv_empty = kv_full + NS; // [NS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + NS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* dirty = reinterpret_cast<volatile int*>(tmem_slot + 2);   // serial of the last unit with non-finite V
+  volatile ChunkUnit* units = reinterpret_cast<volatile ChunkUnit*>(smem + L::OFF_UNIT);
+  float2* ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 18 + 2 * NS; ++i)
+      mbar_init(&bars[i], (i == 6 || i == 7) ? 9 : (i == 10 || i == 11 || (i >= 14 && i <= 16)) ? 128 : 1);
+    *abort_flag = 0;
+    *dirty = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmQ);
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
+  }
+  if (warp == 1) { tmem_alloc(tmem_slot, CA_TMEM_COLS); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  pdl_wait();   // the plan
+
+  if (warp == 0) {  // ---------------------------------------------------- units and TMA (whole warp)
+    const int n_units = p.head->n_units;
+    int u = blockIdx.x, hint = 0, serial = 0, qi = 0, e = 0;
+    bool ok = true;
+    const uint32_t q_bytes = (uint32_t)(HALVES * p.r * p.tpt * 128);
+    while (ok) {
+      ChunkUnit d;
+      d.live = 0;
+      while (u < n_units) {       // the next unit that has keys
+        hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
+        const ChunkSeq s = p.seq[hint];
+        const int x = u - s.unit0;
+        const int g = x % p.n_kv, y = x / p.n_kv;
+        const int chunk = y / s.np, pair = s.np - 1 - y % s.np;      // the longest items of a chunk first
+        const int first = pair * 2 * p.tpt;                           // token of the earlier Q tile
+        const int tail = s.n - first;                                 // tokens from there on
+        const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
+        const int t0 = chunk * s.ct, t1 = min(t0 + s.ct, nt0);
+        d.lone = tail <= p.tpt;
+        if (t0 < t1) {
+          d.live = 1;
+          d.t0 = t0;
+          d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
+          d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
+          d.row1 = s.lo + first;
+          d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
+          d.end = s.lo + s.n;
+          d.pos_off = s.c - s.lo;
+          d.g = g;
+          d.kv_len = s.c + s.n;
+          d.clean = (s.c + first + 1) / 128;
+          d.part = s.nc > 1 ? s.part0 + chunk * s.n - s.lo : INT_MIN;
+          d.b = hint;
+        }
+        if (lane == 0) u = atomicAdd(&p.head->counter, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (d.live) break;
+      }
+      // ---- hand the unit over
+      const int us = serial & 1;
+      if (lane == 0) {
+        ok = mbar_wait(&u_empty[us], ((serial >> 1) & 1) ^ 1, abort_flag, p.status);
+        if (ok) {
+          volatile int* dst = reinterpret_cast<volatile int*>(units + us);
+          const int* src = reinterpret_cast<const int*>(&d);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i] = src[i];
+          mbar_arrive(&u_full[us]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok || !d.live) break;
+      ++serial;
+      // ---- Q tiles
+      for (int x = 0; ok && x < (d.lone ? 1 : 2); ++x) {
+        if (!d.lone && x == 1 && d.n1 == 0) break;
+        if (lane == 0) {
+          const int qs = qi & 1, row = x == 0 ? d.row0 : d.row1;
+          ok = mbar_wait(&q_empty[qs], ((qi >> 1) & 1) ^ 1, abort_flag, p.status);
+          if (ok && !box_in(0, HD, (int64_t)d.g * p.r, p.n_q, row, p.T)) { *abort_flag = 1; ok = false; }
+          if (ok) {
+            mbar_arrive_expect_tx(&q_full[qs], q_bytes);
+            for (int hh = 0; hh < HALVES; ++hh)
+              tma_load_3d(sbase + L::OFF_Q + qs * L::TILE + hh * 16384, &p.tmQ, &q_full[qs], hh * 64, d.g * p.r, row);
+          }
+        }
+        if (ok) ++qi;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      // ---- K and V tiles; the page ids come 32 at a time
+      const int nt = d.lone ? d.n0 + d.n1 : d.n0;
+      const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
+      int page_reg = 0;
+      for (int t = 0; ok && t < nt; ++t) {
+        if ((t & 31) == 0) {
+          page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
+          if (page_reg < 0 || page_reg >= p.n_pages) {
+            atomicOr(p.status, STATUS_BAD_PLAN);
+            page_reg = p.n_pages;            // outside the tensor: the copy fills the tile with zeros
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, page_reg, t & 31);
+        if (lane == 0) {
+          for (int kv = 0; ok && kv < 2; ++kv, ++e) {
+            const int slot = e % NS;
+            ok = mbar_wait(&kv_empty[slot], ((e / NS) & 1) ^ 1, abort_flag, p.status);
+            if (ok && !box_in(0, HD, d.g, p.n_kv, 0, 128, page, (int64_t)p.n_pages + 1)) { *abort_flag = 1; ok = false; }
+            if (!ok) break;
+            mbar_arrive_expect_tx(&kv_full[slot], L::TILE);
+            for (int hh = 0; hh < HALVES; ++hh)
+              tma_load_4d(sbase + L::OFF_KV + slot * L::TILE + hh * 16384, kv ? &p.tmV : &p.tmK, &kv_full[slot], hh * 64,
+                          d.g, 0, page);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+    }
+    // every copy issued has landed before the CTA leaves (at once, unless a wait ran out)
+    if (lane == 0) {
+      int no_abort = 0;
+      for (int k = max(0, e - NS); k < e; ++k) mbar_wait(&kv_full[k % NS], (k / NS) & 1, &no_abort, p.status);
+      for (int k = max(0, qi - 2); k < qi; ++k) mbar_wait(&q_full[k & 1], (k >> 1) & 1, &no_abort, p.status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {  // ------------------------------------------------ MMA issuer
+      const uint32_t idesc_s = idesc_bf16(128, 128);
+      const uint32_t idesc_o = idesc_bf16(128, HD, /*b_mn_major=*/true);
+      int qi = 0, e = 0;                            // Q tiles and ring entries so far
+      int pc[2] = {0, 0}, oc[2] = {0, 0};           // per group: rounds, and units with any
+      bool ok = true;
+      for (int serial = 0; ok; ++serial) {
+        const int us = serial & 1;
+        if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
+        volatile const ChunkUnit* d = units + us;
+        const int live = d->live, lone = d->lone, n0 = d->n0, n1 = d->n1;
+        if (!live) break;
+        mbar_arrive(&u_empty[us]);   // its fields are in registers
+        const int n[2] = {n0, n1};
+        const int nq = lone || n1 == 0 ? 1 : 2;
+        for (int x = 0; ok && x < nq; ++x) ok = mbar_wait(&q_full[(qi + x) & 1], ((qi + x) >> 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        auto tile_of = [&](int x, int i) { return lone ? 2 * i + x : i; };
+        // whether group x is the last to use the tile of its round i
+        auto last_user = [&](int x, int i) { return lone || x == 1 || i >= n1; };
+        auto issue_s = [&](int x, int i) -> bool {
+          const int en = e + 2 * tile_of(x, i), slot = en % NS;
+          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint32_t qa = sbase + L::OFF_Q + ((qi + (lone ? 0 : x)) & 1) * L::TILE;
+          const uint64_t ad0 = sdesc_sw128(qa, 16, 1024);
+          const uint64_t bd0 = sdesc_sw128(sbase + L::OFF_KV + slot * L::TILE, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+            tc_mma(tmem + x * 128, ad0 + off, bd0 + off, idesc_s, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[x]);
+          if (last_user(x, i)) tc_commit(&kv_empty[slot]);
+          // the last scores of a Q tile release its slot
+          if (lone ? 2 * i + x == n0 + n1 - 1 : i == n[x] - 1) tc_commit(&q_empty[(qi + (lone ? 0 : x)) & 1]);
+          return true;
+        };
+        auto issue_pv = [&](int x, int i) -> bool {
+          const int en = e + 2 * tile_of(x, i) + 1, slot = en % NS;
+          if (!mbar_wait(&p_full[x], pc[x] & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint64_t bd0 = sdesc_sw128(sbase + L::OFF_KV + slot * L::TILE, 16384, 1024);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd0 + (uint64_t)(k * 2048 >> 4), idesc_o,
+                      (i > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&o_done[x]);
+          if (last_user(x, i)) tc_commit(&kv_empty[slot]);
+          ++pc[x];
+          return true;
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && n[x] > 0) ok = issue_s(x, 0);
+        // the first P V of a unit overwrites O_x: what the last unit that used it left must have been
+        // read (o_free counts those units only: a phase is never completed before it is waited for)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && n[x] > 0) ok = mbar_wait(&o_free[x], (oc[x]++ & 1) ^ 1, abort_flag, p.status);
+        for (int i = 0; ok && i < n0; ++i) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || i >= n[x]) continue;
+            ok = issue_pv(x, i);
+            if (ok && i + 1 < n[x]) ok = issue_s(x, i + 1);
+          }
+        }
+        if (!ok) break;
+        qi += nq;
+        e += 2 * (lone ? n0 + n1 : n0);
+      }
+      int no_abort = 0;
+      tc_commit(drain);
+      mbar_wait(drain, 0, &no_abort, p.status);
+    }
+  } else {  // ------------------------------------------------------------ softmax groups
+    const int x = (warp - 2) >> 2;
+    const int qw = warp & 3;
+    const int row = qw * 32 + lane;                     // TMEM lane = Q tile row
+    const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
+    const uint32_t tS = tmem + x * 128 + lane_off;
+    const uint32_t tO = tmem + 256 + x * 128 + lane_off;
+    const int tok_in = row / p.r, head_in = row - tok_in * p.r;
+    const bool row_used = row < p.r * p.tpt;
+    int rc = 0, e = 0, lone_count = 0;                  // rounds of this group, ring entries, lone units with n1 > 0
+    bool ok = true;
+    for (int serial = 0; ok; ++serial) {
+      const int us = serial & 1;
+      if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
+      // read from shared memory where it is used, and released at the unit's end: registers are short
+      const volatile ChunkUnit& d = units[us];
+      if (!d.live) break;
+      const int n = x ? d.n1 : d.n0, lone = d.lone;
+      const int tok = (x ? d.row1 : d.row0) + tok_in;   // packed row of the token
+      const int qpos = tok + d.pos_off;
+      const int full = (qpos - tok_in + 1) / 128;       // tiles every row of the Q tile sees
+      float m_ref = -INFINITY, l = 0.f;
+      for (int i = 0; i < n; ++i, ++rc) {
+        const int jt = lone ? 2 * i + x : i, j = d.t0 + jt;
+        if (!mbar_wait(&s_full[x], rc & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const int kbase = j * 128;
+        uint32_t v0[32], v1[32], v2[32], v3[32];
+        tmem_ld32(tS + 0, v0);
+        tmem_ld32(tS + 32, v1);
+        tmem_ld32(tS + 64, v2);
+        tmem_ld32(tS + 96, v3);
+        tc_wait_ld();
+        if (j >= full) {   // keys past the query's position
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (kbase + k > qpos) v0[k] = __float_as_uint(-INFINITY);
+            if (kbase + 32 + k > qpos) v1[k] = __float_as_uint(-INFINITY);
+            if (kbase + 64 + k > qpos) v2[k] = __float_as_uint(-INFINITY);
+            if (kbase + 96 + k > qpos) v3[k] = __float_as_uint(-INFINITY);
+          }
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          m0 = max3(m0, __uint_as_float(v0[k]), __uint_as_float(v0[k + 1]));
+          m1 = max3(m1, __uint_as_float(v1[k]), __uint_as_float(v1[k + 1]));
+          m2 = max3(m2, __uint_as_float(v2[k]), __uint_as_float(v2[k + 1]));
+          m3 = max3(m3, __uint_as_float(v3[k]), __uint_as_float(v3[k + 1]));
+        }
+        const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
+        float alpha = 1.f;
+        bool resc = false;
+        if (i == 0) {
+          m_ref = mt;
+        } else if (mt > m_ref + kRescaleLog2) {
+          alpha = ex2(m_ref - mt);
+          m_ref = mt;
+          resc = true;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, resc)) {
+          if (!mbar_wait(&o_done[x], (rc - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16_at(tO + c * 16, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+            tmem_st16(tO + c * 16, ov);
+          }
+          tc_wait_st();
+        }
+        // a row that has seen no key yet keeps m = -inf; its P is 0
+        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+        float ls0 = 0.f, ls1 = 0.f;
+        exp_chunk(v0, tS + 0, p.scale_log2, mb, ls0, ls1);
+        exp_chunk(v1, tS + 16, p.scale_log2, mb, ls0, ls1);
+        exp_chunk(v2, tS + 32, p.scale_log2, mb, ls0, ls1);
+        exp_chunk(v3, tS + 48, p.scale_log2, mb, ls0, ls1);
+        tc_wait_st();
+        l += ls0 + ls1;
+        // Tiles with keys that some row does not see: P is 0 there, and 0 x V must stay 0.  Rows past
+        // the sequence's end are zeroed; non-finite elements of the others too, and what they add to
+        // the rows that do see them is added at the end (below).  Thread `row` takes key `row`.
+        if (j >= d.clean) {
+          const int en = e + 2 * jt + 1, slot = en % NS;
+          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) { ok = false; break; }
+          uint8_t* vrow = smem + L::OFF_KV + slot * L::TILE + row * 128;
+          const bool past = kbase + row >= d.kv_len;
+#pragma unroll
+          for (int c = 0; c < HD / 8; ++c) {   // pieces in an order that spreads the banks
+            uint4* at = reinterpret_cast<uint4*>(vrow + (c >> 3) * 16384 + ((c ^ row) & 7) * 16);
+            if (past) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              const uint4 w = *at;
+              const uint32_t f = nonfinite_bits(w.x) | nonfinite_bits(w.y) | nonfinite_bits(w.z) | nonfinite_bits(w.w);
+              if (f) {   // the mark first: who finds the values gone finds the mark
+                *dirty = serial;
+                __threadfence_block();
+                *at = make_uint4(drop_nonfinite(w.x), drop_nonfinite(w.y), drop_nonfinite(w.z), drop_nonfinite(w.w));
+              }
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+      }
+      const int n_tiles = lone ? d.n0 + d.n1 : d.n0;
+      e += 2 * n_tiles;
+      if (!ok) break;
+      // ---- the unit's result
+      if (n > 0 && !mbar_wait(&o_done[x], (rc - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+      tc_fence_after();
+      if (lone && x == 1) {                         // hand (m, l, O_1) to group 0
+        if (n > 0) {
+          ml[row] = make_float2(m_ref, l);
+          tc_fence_before();
+          mbar_arrive(ml_full);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[us]);
+        continue;
+      }
+      float w0 = 1.f, w1 = 0.f;
+      const bool merge = lone && d.n1 > 0;
+      if (merge) {
+        if (!mbar_wait(ml_full, lone_count & 1, abort_flag, p.status)) { ok = false; break; }
+        ++lone_count;
+        tc_fence_after();
+        const float2 o = ml[row];
+        const float m = fmaxf(m_ref, o.x);
+        const float mu = m == -INFINITY ? 0.f : m;
+        w0 = ex2(m_ref - mu);
+        w1 = ex2(o.x - mu);
+        l = l * w0 + o.y * w1;
+        m_ref = m;
+      }
+      const bool store_part = d.part != INT_MIN;
+      const bool live = row_used && tok < d.end && n > 0;
+      const int h = d.g * p.r + head_in;
+      if (!store_part) {
+        const float inv = 1.f / l;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      const int64_t at = store_part ? (int64_t)(tok + d.part) * p.n_q + h : (int64_t)tok * p.n_q + h;
+      const int64_t extent = store_part ? (int64_t)p.part_rows * p.n_q : (int64_t)p.T * p.n_q;
+      const bool inside = !live || in_extent(at, 1, extent);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tO + c * 32, v);
+        if (merge) {
+          uint32_t v1[32];
+          tmem_ld32(tO + 128 + c * 32, v1);
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            v[k] = __float_as_uint(fmaf(__uint_as_float(v1[k]), w1, __uint_as_float(v[k]) * w0));
+        } else {
+          tc_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * w0);
+        }
+        if (live && inside && store_part) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
+                                 __uint_as_float(v[4 * k + 3]));
+        } else if (live && inside) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + at * HD + c * 32);
+#pragma unroll
+          for (int k = 0; k < 16; k += 4)
+            dst[k / 4] = make_uint4(pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])),
+                                    pack_bf16x2(__uint_as_float(v[2 * k + 2]), __uint_as_float(v[2 * k + 3])),
+                                    pack_bf16x2(__uint_as_float(v[2 * k + 4]), __uint_as_float(v[2 * k + 5])),
+                                    pack_bf16x2(__uint_as_float(v[2 * k + 6]), __uint_as_float(v[2 * k + 7])));
+        }
+      }
+      tc_fence_before();
+      if (n > 0) mbar_arrive(&o_free[x]);
+      if (merge) mbar_arrive(&o_free[1]);
+      if (live && inside) {
+        if (store_part) p.part_ml[at] = make_float2(m_ref, l);
+        if (*dirty == serial)
+          add_nonfinite<HD>(p, d.b, d.g, max(d.clean, d.t0) * 128, min(qpos, (d.t0 + (lone ? n_tiles : n)) * 128 - 1), at,
+                            store_part);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[us]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, CA_TMEM_COLS);
+  }
+}
+
+// ----------------------------------------------------------------------------------------- merge
+// o = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the chunks k that hold keys the token sees;
+// one warp per (token, head) of the cut sequences.
+template <int HD>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int PER = HD / 32;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const int64_t total = (int64_t)p.head->n_split * p.n_q;
+  const int64_t step = (int64_t)gridDim.x * 8;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += step) {
+    const int x = (int)(w / p.n_q), h = (int)(w - (int64_t)x * p.n_q);
+    // sequences that were not cut hold no split rows, so the last one starting at or before x is it
+    const int b = warp_search(p.B, x, [&](int i) { return p.seq[i].split0; });
+    const ChunkSeq s = p.seq[b];
+    const int i = x - s.split0;
+    const int nk = min(s.nc, cdiv((s.c + i) / 128 + 1, s.ct));
+    const int64_t row = (int64_t)(s.part0 + i) * p.n_q + h, stride = (int64_t)s.n * p.n_q;
+    float M = -INFINITY;
+    for (int k = lane; k < nk; k += 32) M = fmaxf(M, p.part_ml[row + k * stride].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float l = 0.f, acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < nk; k0 += 32) {
+      float2 a = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < nk) a = p.part_ml[row + (k0 + lane) * stride];
+      const float wl = ex2(a.x - mu);
+      l += wl * a.y;
+      const int kn = min(32, nk - k0);
+#pragma unroll 4
+      for (int k = 0; k < kn; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, wl, k);
+        const float* src = p.part_o + (row + (k0 + k) * stride) * HD + lane * PER;
+        if (PER == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
+          acc[PER - 2] = fmaf(wk, v.z, acc[PER - 2]);
+          acc[PER - 1] = fmaf(wk, v.w, acc[PER - 1]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = 1.f / l;
+    const int64_t at = ((int64_t)(s.lo + i) * p.n_q + h) * HD + lane * PER;
+    if (!in_extent(at, PER, (int64_t)p.T * p.n_q * HD)) continue;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at);
+    dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (PER == 4) dst[1] = pack_bf16x2(acc[PER - 2] * inv, acc[PER - 1] * inv);
+  }
+}
+
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// Partial rows the workspace holds: no more than every token in chunks of one tile, and no more than
+// about 8 x 152 units of two full Q tiles (162 MB at hd 128), past which cutting pays no more.
+int64_t part_rows_of(int64_t T, int64_t n_q, int64_t max_pos) {
+  const int64_t tiles = max_pos / 128 + 1;
+  if (tiles < 2) return 0;
+  return std::min(T * tiles, std::max<int64_t>(1, 8 * 152 * 256 / n_q));
+}
+
+template <int HD>
+int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
+  ChunkParams p;
+  memset(&p, 0, sizeof(p));
+  const int r = (int)(a.n_q / a.n_kv), tpt = 128 / r;
+  if (!encode_tmap_3d_bf16(&p.tmQ, a.q, HD, (uint64_t)a.n_q, (uint64_t)a.T, HD * 2, (uint64_t)a.n_q * HD * 2, 64,
+                           (uint32_t)r, (uint32_t)tpt))
+    return -1;
+  const uint64_t dims[4] = {HD, (uint64_t)a.n_kv, 128, (uint64_t)a.n_pages};
+  const uint64_t strides[3] = {HD * 2, (uint64_t)a.n_kv * HD * 2, (uint64_t)128 * a.n_kv * HD * 2};
+  const uint32_t box[4] = {64, 1, 128, 1};
+  if (!encode_tmap_4d_bf16(&p.tmK, a.k_pool, dims, strides, box) || !encode_tmap_4d_bf16(&p.tmV, a.v_pool, dims, strides, box))
+    return -1;
+  p.o = static_cast<uint16_t*>(a.o);
+  p.v_pool = static_cast<const uint16_t*>(a.v_pool);
+  p.block_table = a.block_table; p.cu_new = a.cu_new; p.n_cached = a.n_cached;
+  p.B = (int)a.B; p.T = (int)a.T; p.n_q = (int)a.n_q; p.n_kv = (int)a.n_kv; p.r = r; p.tpt = tpt;
+  p.n_pages = (int)a.n_pages; p.max_pages = (int)a.max_pages; p.max_pos = (int)a.max_pos;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.part_rows = (int)part_rows_of(a.T, a.n_q, a.max_pos);
+  char* ws = static_cast<char*>(a.ws);
+  p.head = reinterpret_cast<ChunkHead*>(ws);
+  ws += 256;
+  p.seq = reinterpret_cast<ChunkSeq*>(ws);
+  ws += round256((size_t)a.B * sizeof(ChunkSeq));
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += round256((size_t)p.part_rows * a.n_q * HD * 4);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  p.grid = num_sms;
+  p.status = a.status;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool attr_set[64] = {};
+  if (dev < 0 || dev >= 64) return -1;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(chunk_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, CaSmem<HD>::TOTAL) !=
+        cudaSuccess)
+      return -1;
+    attr_set[dev] = true;
+  }
+  chunk_plan_kernel<<<1, CP_THREADS, 0, st>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  // the attention's set-up overlaps the plan, and the merge's launch the attention
+  const bool pdl = pdl_enabled();
+  set_pdl(true);
+  cudaError_t e = launch_k(chunk_attn_kernel<HD>, dim3(num_sms), dim3(CA_THREADS), CaSmem<HD>::TOTAL, st, p);
+  if (e == cudaSuccess && p.part_rows > 0) {
+    const int64_t warps = (a.T * a.n_q + 7) / 8;
+    e = launch_k(chunk_combine_kernel<HD>, dim3((unsigned)std::min<int64_t>(warps, 8 * num_sms)), dim3(256), 0, st, p);
+  }
+  set_pdl(pdl);
+  return e == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
 
-size_t chunk_attn_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 256; }
+// Units are counted in 32 bits.
+bool chunk_attn_supported(int64_t B, int64_t T, int64_t n_q, int64_t n_kv) {
+  const int64_t tpt = 128 / (n_q / n_kv);
+  return T <= INT32_MAX / 2 && B <= INT32_MAX / 256 && (T / (2 * tpt) + B) * n_kv <= (int64_t)1 << 28 && n_q <= 65536;
+}
 
-int launch_chunk_attn(const ChunkAttnDesc& a, int, cudaStream_t st) {
-  const int64_t warps = a.T * a.n_q;
-  chunk_attn_simt_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(a);
-  return 0;
+size_t chunk_attn_ws_bytes(int64_t B, int64_t T, int64_t n_q, int64_t, int64_t hd, int64_t max_pos) {
+  const size_t rows = (size_t)part_rows_of(T, n_q, max_pos) * n_q;
+  return 256 + round256((size_t)B * sizeof(ChunkSeq)) + round256(rows * hd * 4) + round256(rows * 8);
+}
+
+int launch_chunk_attn(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
+  return a.hd == 128 ? launch_hd<128>(a, num_sms, st) : launch_hd<64>(a, num_sms, st);
 }
 
 LLAMA_DEFINE_BOUNDS_READER(chunk_attn)

@@ -230,6 +230,7 @@ struct ChunkAttnDesc {
   void* ws;
   unsigned* status;
 };
+bool chunk_attn_supported(int64_t B, int64_t T, int64_t n_q, int64_t n_kv);
 size_t chunk_attn_ws_bytes(int64_t B, int64_t T, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_pos);
 int launch_chunk_attn(const ChunkAttnDesc& a, int num_sms, cudaStream_t st);
 
