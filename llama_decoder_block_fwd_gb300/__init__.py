@@ -146,9 +146,9 @@ def _p(t) -> int | None:
 
 
 def _s(stream) -> int | None:
-    if stream is None:
+    if stream is None:   # the address alone: a Stream object costs several times as much
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -274,47 +274,47 @@ def llama_gqa_attention_decode_paged(dims, q, k_pool, v_pool, block_table, seq_p
            "llama_gqa_attention_decode_paged")
 
 
-def _check_tensors(where, dtype, **tensors):
-    """Refuse tensors whose element type or layout the call would misread: the library sees addresses
-    only.  Every tensor given must be contiguous, of torch's `dtype` and on the current device."""
-    import torch
-    dt, dev = getattr(torch, dtype), torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is None or isinstance(t, int):
-            continue
-        if t.dtype is not dt:
-            raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
-        _on_device(where, name, t, dev)
+def _arg(where, name, t, dtype, dev, shape=None):
+    """The address of a contiguous tensor of `dtype` (and, when given, `shape`) on device `dev`.  The library
+    sees addresses only, so what it would misread is refused here."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(where, name, t, dtype, dev, shape)
+    return t.data_ptr()
 
 
-def _on_device(where, name, t, dev):
+def _refuse(where, name, t, dtype, dev, shape):
     if not t.is_cuda:
         raise ValueError(f"{where}: expected a CUDA tensor, got {name} on {t.device}")
-    if t.device.index != dev:
+    if t.get_device() != dev:
         raise ValueError(f"{where}: {name} is on {t.device}, the current device is cuda:{dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{where}: {name} must be contiguous, got strides {t.stride()}")
 
 
-def _shape(where, name, t, shape):
-    """`shape` entries of None match any size."""
-    got = tuple(t.shape)
-    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-        want = tuple("?" if w is None else w for w in shape)
-        raise ValueError(f"{where}: {name} must have shape {want}, got {got}")
-
-
-def _token_stride(where, name, t, heads, hd, rows, dev):
-    """The token stride of a [rows, heads, hd] bf16 view whose heads are contiguous."""
-    import torch
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{where}: {name} must be bfloat16, got {t.dtype}")
-    _on_device(where, name, t, dev)
-    _shape(where, name, t, (rows, heads, hd))
+def _rows(where, name, t, dtype, dev, shape, inner):
+    """(address, row stride in elements) of a view whose rows are contiguous; `inner` are the strides a
+    row of more than one element has behind its first dimension."""
+    if t is None or t.__class__ is int:
+        raise ValueError(f"{where}: {name} must be a tensor")
     st = t.stride()
-    if rows and (st[2] != 1 or (heads > 1 and st[1] != hd)):
-        raise ValueError(f"{where}: the heads of {name} must be contiguous, got strides {st}")
-    return st[0] if rows > 1 else max(st[0], heads * hd)
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(where, name, t, dtype, dev, shape)
+    width = 1
+    for n, want, got in zip(reversed(shape[1:]), reversed(inner), reversed(st[1:])):
+        if n > 1 and want != got:
+            raise ValueError(f"{where}: the rows of {name} must be contiguous, got strides {st}")
+        width *= n
+    return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], width)
+
+
+def _torch_dev():
+    import torch
+    return torch, torch.cuda.current_device()
 
 
 def llama_paged_plan(n_cached, n_new, free_pages, n_pages, block_table, cu_new, positions, slots, pages_used,
@@ -322,18 +322,14 @@ def llama_paged_plan(n_cached, n_new, free_pages, n_pages, block_table, cu_new, 
     """Extend block_table [B, max_pages] by the pages the new tokens need (from free_pages, in order) and
     fill cu_new [B+1], positions [n_tokens], slots [n_tokens] and pages_used [1]; all int32."""
     w = "llama_paged_plan"
-    _check_tensors(w, "int32", n_cached=n_cached, n_new=n_new, free_pages=free_pages, block_table=block_table,
-                   cu_new=cu_new, positions=positions, slots=slots, pages_used=pages_used)
-    B, T = int(n_cached.numel()), int(positions.numel())
-    _shape(w, "n_new", n_new, (B,))
-    _shape(w, "block_table", block_table, (B, None))
-    _shape(w, "cu_new", cu_new, (B + 1,))
-    _shape(w, "slots", slots, (T,))
-    if pages_used.numel() < 1:
-        raise ValueError(f"{w}: pages_used must hold one element")
-    _check(lib().llama_paged_plan(_p(n_cached), _p(n_new), B, _p(free_pages), int(free_pages.numel()), int(n_pages),
-                                  _p(block_table), int(block_table.shape[1]), T, _p(cu_new), _p(positions), _p(slots),
-                                  _p(pages_used), _s(stream)), w)
+    torch, dev = _torch_dev()
+    i32, B, T, P = torch.int32, n_cached.numel(), positions.numel(), block_table.shape[-1]
+    _check(lib().llama_paged_plan(
+        _arg(w, "n_cached", n_cached, i32, dev), _arg(w, "n_new", n_new, i32, dev, (B,)), B,
+        _arg(w, "free_pages", free_pages, i32, dev), free_pages.numel(), int(n_pages),
+        _arg(w, "block_table", block_table, i32, dev, (B, P)), P, T, _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)),
+        _arg(w, "positions", positions, i32, dev), _arg(w, "slots", slots, i32, dev, (T,)),
+        _arg(w, "pages_used", pages_used, i32, dev, (1,)), _s(stream)), w)
 
 
 def llama_rope_append_paged(dims, q, k, v, positions, slots, q_out, k_pool, v_pool, stream=None):
@@ -341,25 +337,25 @@ def llama_rope_append_paged(dims, q, k, v, positions, slots, q_out, k_pool, v_po
     q [S, n_q, hd], k / v [S, n_kv, hd] may be views with a token stride; None, None for q, q_out (append
     only) or for k, v, k_pool, v_pool (rotate only)."""
     w = "llama_rope_append_paged"
-    import torch
-    d, dev = _d(dims), torch.cuda.current_device()
-    S, hd = d.S, d.head_dim
-    _check_tensors(w, "int32", positions=positions, slots=slots)
-    _check_tensors(w, "bfloat16", q_out=q_out, k_pool=k_pool, v_pool=v_pool)
-    _shape(w, "positions", positions, (S,))
-    _shape(w, "slots", slots, (S,))
+    torch, dev = _torch_dev()
+    d, i32, bf16 = _d(dims), torch.int32, torch.bfloat16
+    S, hd, n_q, n_kv = d.S, d.head_dim, d.n_q, d.n_kv
+    qa = ka = va = None
     qs = ks = vs = n_pages = 0
-    if q is not None and q_out is not None:
-        qs = _token_stride(w, "q", q, d.n_q, hd, S, dev)
-        _shape(w, "q_out", q_out, (S, d.n_q, hd))
-    if k is not None and v is not None and k_pool is not None and v_pool is not None:
-        ks = _token_stride(w, "k", k, d.n_kv, hd, S, dev)
-        vs = _token_stride(w, "v", v, d.n_kv, hd, S, dev)
-        _shape(w, "k_pool", k_pool, (None, 128, d.n_kv, hd))
-        _shape(w, "v_pool", v_pool, tuple(k_pool.shape))
-        n_pages = int(k_pool.shape[0])
-    _check(lib().llama_rope_append_paged(ctypes.byref(d), _p(q), qs, _p(k), ks, _p(v), vs, _p(positions), _p(slots),
-                                         _p(q_out), _p(k_pool), _p(v_pool), n_pages, _s(stream)), w)
+    if q is not None:
+        qa, qs = _rows(w, "q", q, bf16, dev, (S, n_q, hd), (hd, 1))
+    if k is not None:
+        ka, ks = _rows(w, "k", k, bf16, dev, (S, n_kv, hd), (hd, 1))
+    if v is not None:
+        va, vs = _rows(w, "v", v, bf16, dev, (S, n_kv, hd), (hd, 1))
+    pool = None
+    if k_pool is not None:
+        n_pages = k_pool.shape[0]
+        pool = (n_pages, 128, n_kv, hd)
+    _check(lib().llama_rope_append_paged(
+        ctypes.byref(d), qa, qs, ka, ks, va, vs, _arg(w, "positions", positions, i32, dev, (S,)),
+        _arg(w, "slots", slots, i32, dev, (S,)), _arg(w, "q_out", q_out, bf16, dev, (S, n_q, hd)),
+        _arg(w, "k_pool", k_pool, bf16, dev, pool), _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, _s(stream)), w)
 
 
 def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new, n_cached, max_pos, o, ws,
@@ -367,19 +363,16 @@ def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new
     """Packed new tokens q [S, n_q, hd] over k_pool / v_pool [n_pages, 128, n_kv, hd] (one layer): sequence b
     owns rows cu_new[b] .. cu_new[b+1]-1, at positions n_cached[b] onward; o [S, n_q, hd]."""
     w = "llama_gqa_attention_chunk_paged"
-    d = _d(dims)
-    _check_tensors(w, "bfloat16", q=q, k_pool=k_pool, v_pool=v_pool, o=o)
-    _check_tensors(w, "int32", block_table=block_table, cu_new=cu_new, n_cached=n_cached)
-    _shape(w, "q", q, (d.S, d.n_q, d.head_dim))
-    _shape(w, "o", o, (d.S, d.n_q, d.head_dim))
-    _shape(w, "k_pool", k_pool, (None, 128, d.n_kv, d.head_dim))
-    _shape(w, "v_pool", v_pool, tuple(k_pool.shape))
-    _shape(w, "block_table", block_table, (d.B, None))
-    _shape(w, "cu_new", cu_new, (d.B + 1,))
-    _shape(w, "n_cached", n_cached, (d.B,))
-    _check(lib().llama_gqa_attention_chunk_paged(ctypes.byref(d), _p(q), _p(k_pool), _p(v_pool), int(k_pool.shape[0]),
-                                                 _p(block_table), int(block_table.shape[1]), _p(cu_new), _p(n_cached),
-                                                 int(max_pos), _p(o), _p(ws), _nbytes(ws), _s(stream)), w)
+    torch, dev = _torch_dev()
+    d, i32, bf16 = _d(dims), torch.int32, torch.bfloat16
+    B, hd = d.B, d.head_dim
+    rows, n_pages, P = (d.S, d.n_q, hd), k_pool.shape[0], block_table.shape[-1]
+    pool = (n_pages, 128, d.n_kv, hd)
+    _check(lib().llama_gqa_attention_chunk_paged(
+        ctypes.byref(d), _arg(w, "q", q, bf16, dev, rows), _arg(w, "k_pool", k_pool, bf16, dev, pool),
+        _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, _arg(w, "block_table", block_table, i32, dev, (B, P)), P,
+        _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), _arg(w, "n_cached", n_cached, i32, dev, (B,)), int(max_pos),
+        _arg(w, "o", o, bf16, dev, rows), _p(ws), _nbytes(ws), _s(stream)), w)
 
 
 def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, noise, n_accepted, out_tokens, ws,
@@ -388,30 +381,24 @@ def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, no
     None), tokens int32 [n_tokens], u fp32 [n_tokens], noise fp32 [B, ld] exponential draws; fills
     n_accepted int32 [B] and out_tokens int32 [n_tokens]."""
     w = "llama_verify_drafts"
-    import torch
-    dev = torch.cuda.current_device()
-    T, B = int(tokens.numel()), int(n_accepted.numel())
-    V = int(logits.shape[1]) if vocab is None else int(vocab)
-    _check_tensors(w, "int32", cu_new=cu_new, tokens=tokens, n_accepted=n_accepted, out_tokens=out_tokens)
-    _check_tensors(w, "float32", u=u)
-    _shape(w, "cu_new", cu_new, (B + 1,))
-    _shape(w, "out_tokens", out_tokens, (T,))
-    if u is not None:
-        _shape(w, "u", u, (T,))
-    ld = [0, 0, 0]
-    for i, (name, t, rows) in enumerate((("logits", logits, T), ("draft_logits", draft_logits, T), ("noise", noise, B))):
+    torch, dev = _torch_dev()
+    i32, f32 = torch.int32, torch.float32
+    T, B = tokens.numel(), n_accepted.numel()
+    V = logits.shape[1] if vocab is None else int(vocab)
+
+    def rows(name, t, n):
         if t is None:
-            continue
-        if t.dtype is not torch.float32:
-            raise ValueError(f"{w}: {name} must be float32, got {t.dtype}")
-        _on_device(w, name, t, dev)
-        _shape(w, name, t, (rows, None))
-        if t.shape[1] < V or (V > 1 and t.stride(1) != 1):
-            raise ValueError(f"{w}: the rows of {name} must hold {V} contiguous entries")
-        ld[i] = max(int(t.stride(0)), V) if rows <= 1 else int(t.stride(0))
-    _check(lib().llama_verify_drafts(_p(logits), T, V, ld[0], _p(draft_logits), ld[1], float(temperature), _p(cu_new), B,
-                                     _p(tokens), _p(u), _p(noise), ld[2], _p(n_accepted), _p(out_tokens), _p(ws),
-                                     _nbytes(ws), _s(stream)), w)
+            return None, 0
+        if t.shape[-1] < V:
+            raise ValueError(f"{w}: the rows of {name} must hold {V} entries, got {tuple(t.shape)}")
+        return _rows(w, name, t, f32, dev, (n, t.shape[-1]), (1,))
+
+    (z, ldz), (y, ldy), (e, lde) = rows("logits", logits, T), rows("draft_logits", draft_logits, T), rows("noise", noise, B)
+    _check(lib().llama_verify_drafts(
+        z, T, V, ldz, y, ldy, float(temperature), _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), B,
+        _arg(w, "tokens", tokens, i32, dev), _arg(w, "u", u, f32, dev, (T,)), e, lde,
+        _arg(w, "n_accepted", n_accepted, i32, dev), _arg(w, "out_tokens", out_tokens, i32, dev, (T,)), _p(ws), _nbytes(ws),
+        _s(stream)), w)
 
 
 def llama_workspace_bytes(op, dims, dtype, n_layers=0, vocab=0, kv_capacity=0) -> int:

@@ -424,85 +424,98 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
       for (int k = max(0, e - NS); k < e; ++k) mbar_wait(&kv_full[k % NS], (k / NS) & 1, &no_abort, p.status);
       for (int k = max(0, qi - 2); k < qi; ++k) mbar_wait(&q_full[k & 1], (k >> 1) & 1, &no_abort, p.status);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {  // ------------------------------------------------ MMA issuer
-      const uint32_t idesc_s = idesc_bf16(128, 128);
-      const uint32_t idesc_o = idesc_bf16(128, HD, /*b_mn_major=*/true);
-      int qi = 0, e = 0;                            // Q tiles and ring entries so far
-      int pc[2] = {0, 0}, oc[2] = {0, 0};           // per group: rounds, and units with any
-      bool ok = true;
-      for (int serial = 0; ok; ++serial) {
-        const int us = serial & 1;
-        if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
-        volatile const ChunkUnit* d = units + us;
-        const int live = d->live, lone = d->lone, n0 = d->n0, n1 = d->n1;
-        if (!live) break;
-        mbar_arrive(&u_empty[us]);   // its fields are in registers
-        const int n[2] = {n0, n1};
-        const int nq = lone || n1 == 0 ? 1 : 2;
-        for (int x = 0; ok && x < nq; ++x) ok = mbar_wait(&q_full[(qi + x) & 1], ((qi + x) >> 1) & 1, abort_flag, p.status);
-        if (!ok) break;
+  } else if (warp == 1) {  // -------------------------------------------- MMA issuer (whole warp)
+    // Every lane runs the loop and one elected lane's instructions take effect: the control flow stays
+    // uniform, so descriptors live in uniform registers.  Issued from a one-lane branch, each MMA's
+    // operands were moved there one by one: 600-900 cycles per 8 MMAs against the 512 they execute in
+    // (clock stamps at hd 128), and the tensor cores waited for their issuer half of the time.
+    const uint32_t one = elect_one();
+    const uint32_t idesc_s = idesc_bf16(128, 128);
+    const uint32_t idesc_o = idesc_bf16(128, HD, /*b_mn_major=*/true);
+    const uint64_t kdesc = sdesc_sw128(sbase + L::OFF_KV, 16, 1024);
+    const uint64_t vdesc = sdesc_sw128(sbase + L::OFF_KV, 16384, 1024);
+    const uint64_t qdesc = sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
+    int qi = 0;                                   // Q tiles so far
+    int ks = 0, kph = 0, vs = 1, vph = 0;         // ring slot and phase of the next K and V tile
+    int pc[2] = {0, 0}, oc[2] = {0, 0};           // per group: rounds, and units with any
+    bool ok = true;
+    for (int serial = 0; ok; ++serial) {
+      const int us = serial & 1;
+      if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
+      volatile const ChunkUnit* d = units + us;
+      const int live = __shfl_sync(0xffffffffu, d->live, 0), lone = __shfl_sync(0xffffffffu, d->lone, 0);
+      const int n0 = __shfl_sync(0xffffffffu, d->n0, 0), n1 = __shfl_sync(0xffffffffu, d->n1, 0);
+      if (!live) break;
+      if (one) mbar_arrive(&u_empty[us]);   // its fields are in registers
+      const int n[2] = {n0, n1};
+      const int nq = lone || n1 == 0 ? 1 : 2;
+      for (int x = 0; ok && x < nq; ++x) ok = mbar_wait(&q_full[(qi + x) & 1], ((qi + x) >> 1) & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const int s_last = lone ? n0 + n1 : 0;       // lone: the S after which the Q tile is free
+      int s_count = 0;
+      // S_x = Q_x K^T of the next K tile; `last`: no other group uses the tile
+      auto issue_s = [&](int x, int i, bool last) -> bool {
+        if ((x == 0 || lone) && !mbar_wait(&kv_full[ks], kph, abort_flag, p.status)) return false;
         tc_fence_after();
-        auto tile_of = [&](int x, int i) { return lone ? 2 * i + x : i; };
-        // whether group x is the last to use the tile of its round i
-        auto last_user = [&](int x, int i) { return lone || x == 1 || i >= n1; };
-        auto issue_s = [&](int x, int i) -> bool {
-          const int en = e + 2 * tile_of(x, i), slot = en % NS;
-          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint32_t qa = sbase + L::OFF_Q + ((qi + (lone ? 0 : x)) & 1) * L::TILE;
-          const uint64_t ad0 = sdesc_sw128(qa, 16, 1024);
-          const uint64_t bd0 = sdesc_sw128(sbase + L::OFF_KV + slot * L::TILE, 16, 1024);
+        const int qs = (qi + (lone ? 0 : x)) & 1;
+        const uint64_t ad0 = qdesc + (uint64_t)(qs * (int)(L::TILE >> 4));
+        const uint64_t bd0 = kdesc + (uint64_t)(ks * (int)(L::TILE >> 4));
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
-            tc_mma(tmem + x * 128, ad0 + off, bd0 + off, idesc_s, k > 0 ? 1u : 0u);
-          }
-          tc_commit(&s_full[x]);
-          if (last_user(x, i)) tc_commit(&kv_empty[slot]);
-          // the last scores of a Q tile release its slot
-          if (lone ? 2 * i + x == n0 + n1 - 1 : i == n[x] - 1) tc_commit(&q_empty[(qi + (lone ? 0 : x)) & 1]);
-          return true;
-        };
-        auto issue_pv = [&](int x, int i) -> bool {
-          const int en = e + 2 * tile_of(x, i) + 1, slot = en % NS;
-          if (!mbar_wait(&p_full[x], pc[x] & 1, abort_flag, p.status)) return false;
-          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint64_t bd0 = sdesc_sw128(sbase + L::OFF_KV + slot * L::TILE, 16384, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_ts(tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd0 + (uint64_t)(k * 2048 >> 4), idesc_o,
-                      (i > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&o_done[x]);
-          if (last_user(x, i)) tc_commit(&kv_empty[slot]);
-          ++pc[x];
-          return true;
-        };
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ok && n[x] > 0) ok = issue_s(x, 0);
-        // the first P V of a unit overwrites O_x: what the last unit that used it left must have been
-        // read (o_free counts those units only: a phase is never completed before it is waited for)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ok && n[x] > 0) ok = mbar_wait(&o_free[x], (oc[x]++ & 1) ^ 1, abort_flag, p.status);
-        for (int i = 0; ok && i < n0; ++i) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || i >= n[x]) continue;
-            ok = issue_pv(x, i);
-            if (ok && i + 1 < n[x]) ok = issue_s(x, i + 1);
-          }
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+          tc_mma_if(one, tmem + x * 128, ad0 + off, bd0 + off, idesc_s, k > 0 ? 1u : 0u);
         }
-        if (!ok) break;
-        qi += nq;
-        e += 2 * (lone ? n0 + n1 : n0);
+        tc_commit_if(one, &s_full[x]);
+        ++s_count;
+        if (lone ? s_count == s_last : i == n[x] - 1) tc_commit_if(one, &q_empty[qs]);
+        if (last) {
+          tc_commit_if(one, &kv_empty[ks]);
+          ks += 2;
+          if (ks >= NS) { ks -= NS; kph ^= 1; }
+        }
+        return true;
+      };
+      // O_x += P_x V of the next V tile
+      auto issue_pv = [&](int x, int i, bool last) -> bool {
+        if ((x == 0 || lone) && !mbar_wait(&kv_full[vs], vph, abort_flag, p.status)) return false;
+        if (!mbar_wait(&p_full[x], pc[x] & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        const uint64_t bd0 = vdesc + (uint64_t)(vs * (int)(L::TILE >> 4));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)   // 16 keys per step; P_x k-step k is TMEM columns 8k..8k+7
+          tc_mma_ts_if(one, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd0 + (uint64_t)(k * 2048 >> 4), idesc_o,
+                       k > 0 ? 1u : (i > 0 ? 1u : 0u));
+        tc_commit_if(one, &o_done[x]);
+        ++pc[x];
+        if (last) {
+          tc_commit_if(one, &kv_empty[vs]);
+          vs += 2;
+          if (vs >= NS) { vs -= NS; vph ^= 1; }
+        }
+        return true;
+      };
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (ok && n[x] > 0) ok = issue_s(x, 0, lone || x == 1 || n1 == 0);
+      // the first P V of a unit overwrites O_x: what the last unit that used it left must have been
+      // read (o_free counts those units only: a phase is never completed before it is waited for)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (ok && n[x] > 0) ok = mbar_wait(&o_free[x], (oc[x]++ & 1) ^ 1, abort_flag, p.status);
+      for (int i = 0; ok && i < n0; ++i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || i >= n[x]) continue;
+          ok = issue_pv(x, i, lone || x == 1 || i >= n1);
+          if (ok && i + 1 < n[x]) ok = issue_s(x, i + 1, lone || x == 1 || i + 1 >= n1);
+        }
       }
-      int no_abort = 0;
-      tc_commit(drain);
-      mbar_wait(drain, 0, &no_abort, p.status);
+      qi += nq;
     }
+    int no_abort = 0;
+    tc_commit_if(one, drain);
+    mbar_wait(drain, 0, &no_abort, p.status);
   } else {  // ------------------------------------------------------------ softmax groups
     const int x = (warp - 2) >> 2;
     const int qw = warp & 3;

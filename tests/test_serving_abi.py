@@ -111,27 +111,40 @@ def test_binding_refuses_what_the_library_would_misread():
     torch = pytest.importorskip("torch")
 
     class Fake:                       # what the checks look at, without device memory
-        is_cuda = True
+        def __init__(self, shape, dtype, strides, device=0):
+            self.shape, self.dtype, self._st, self._dev = torch.Size(shape), dtype, strides, device
+            self.is_cuda, self.device = device >= 0, f"cuda:{device}" if device >= 0 else "cpu"
 
-        def __init__(self, shape, dtype, strides=None, device=0):
-            self.shape, self.dtype, self._st = shape, dtype, strides
-            self.device = type("D", (), {"index": device, "__str__": lambda s: f"cuda:{device}"})()
+        def stride(self):
+            return self._st
 
-        def stride(self, i=None):
-            return self._st if i is None else self._st[i]
+        def get_device(self):
+            return self._dev
 
-    from llama_decoder_block_fwd_gb300 import _on_device, _shape, _token_stride
-    bf = torch.bfloat16
-    assert _token_stride("f", "q", Fake((4, 2, 64), bf, (512, 64, 1)), 2, 64, 4, 0) == 512
-    assert _token_stride("f", "q", Fake((1, 2, 64), bf, (0, 64, 1)), 2, 64, 1, 0) == 128
-    for bad in (Fake((4, 2, 64), torch.float16, (512, 64, 1)), Fake((4, 2, 64), bf, (512, 32, 1)),
-                Fake((4, 2, 64), bf, (512, 64, 2)), Fake((4, 3, 64), bf, (512, 64, 1)),
-                Fake((4, 2, 64), bf, (512, 64, 1), device=1)):
+        def is_contiguous(self):
+            return self._st == tuple(torch.empty(self.shape, device="meta").stride())
+
+        def data_ptr(self):
+            return 0x1000
+
+    from llama_decoder_block_fwd_gb300 import _arg, _rows
+    bf, f32 = torch.bfloat16, torch.float32
+    assert _arg("f", "x", Fake((4, 3), f32, (3, 1)), f32, 0, (4, 3)) == 0x1000
+    assert _arg("f", "x", None, f32, 0) is None and _arg("f", "x", 0x20, f32, 0) == 0x20
+    for bad, what in ((Fake((4, 3), bf, (3, 1)), "float32"), (Fake((4, 3), f32, (6, 1)), "contiguous"),
+                      (Fake((4, 2), f32, (2, 1)), "shape"), (Fake((4, 3), f32, (3, 1), 1), "current device"),
+                      (Fake((4, 3), f32, (3, 1), -1), "CUDA tensor")):
+        with pytest.raises(ValueError, match=what):
+            _arg("f", "x", bad, f32, 0, (4, 3))
+    view = lambda *a, **k: _rows("f", "q", Fake(*a, **k), bf, 0, (4, 2, 64), (64, 1))
+    assert view((4, 2, 64), bf, (512, 64, 1)) == (0x1000, 512)
+    assert _rows("f", "q", Fake((1, 2, 64), bf, (0, 64, 1)), bf, 0, (1, 2, 64), (64, 1)) == (0x1000, 128)
+    assert _rows("f", "q", Fake((4, 1, 64), bf, (80, 5, 1)), bf, 0, (4, 1, 64), (64, 1)) == (0x1000, 80)
+    for bad in (((4, 2, 64), torch.float16, (512, 64, 1)), ((4, 2, 64), bf, (512, 32, 1)), ((4, 2, 64), bf, (512, 64, 2)),
+                ((4, 3, 64), bf, (512, 64, 1))):
         with pytest.raises(ValueError):
-            _token_stride("f", "q", bad, 2, 64, 4, 0)
-    with pytest.raises(ValueError, match="current device"):
-        _on_device("f", "q", Fake((1,), bf, device=1), 0)
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        _on_device("f", "q", torch.zeros(1), 0)
-    with pytest.raises(ValueError, match="shape"):
-        _shape("f", "q", torch.zeros(2, 3), (2, 4))
+            view(*bad)
+    with pytest.raises(ValueError):
+        view((4, 2, 64), bf, (512, 64, 1), device=1)
+    with pytest.raises(ValueError, match="tensor"):
+        _rows("f", "q", 0x1000, bf, 0, (4, 2, 64), (64, 1))
