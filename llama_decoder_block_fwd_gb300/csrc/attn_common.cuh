@@ -80,6 +80,46 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&v)[32], uint32_t col,
   tmem_st16(col, w);
 }
 
+// mbar_wait in few instructions (what a warp executes between two waits has to come from the
+// instruction cache): only every 64th failed try leaves the loop, to look at the abort flag and the
+// clock.  Returns false when the wait was given up, as mbar_wait does.
+static __device__ __noinline__ unsigned long long wait_check(unsigned long long t0, volatile int* abort, unsigned* status) {
+  if (*abort) return 0;
+  const unsigned long long t = globaltimer_ns();
+  if (t0 == 0) return t;
+  if (t - t0 <= kWaitLimitNs) return t0;
+  atomicOr(status, STATUS_TIMEOUT);
+  *abort = 1;
+  return 0;
+}
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  unsigned long long t0 = 0;
+  uint32_t tries = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++tries & 63u) == 0 && !(t0 = wait_check(t0, abort, status))) return false;
+  }
+  return true;
+}
+
+// The same for a whole warp whose control flow is to stay uniform: the loop's exit is a vote.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  uint32_t tries = 0;
+  unsigned long long t0 = 0;
+  while (__ballot_sync(0xffffffffu, mbar_try_wait(bar, parity)) != 0xffffffffu) {
+    if ((++tries & 63u) == 0) {
+      if (__ballot_sync(0xffffffffu, *abort != 0) != 0u) return false;
+      const unsigned long long t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (__ballot_sync(0xffffffffu, t - t0 > kWaitLimitNs) != 0u) {
+        atomicOr(status, STATUS_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 // ---- tcgen05 issued from a whole warp: every lane runs the instruction stream, the lane with `one` != 0
 //      issues.  The flow stays uniform, so operands stay in uniform registers.
 __device__ __forceinline__ uint32_t elect_one() {
@@ -105,12 +145,16 @@ __device__ __forceinline__ void tc_mma_ts_if(uint32_t one, uint32_t d_tmem, uint
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void tc_commit_if(uint32_t one, uint64_t* bar) {
+__device__ __forceinline__ void tc_commit_if(uint32_t one, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
       "r"(one)
       : "memory");
 }
+
+// Registers per thread of a warpgroup, moved between warpgroups of a running block.
+template <int N> __device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 }  // namespace llama

@@ -15,7 +15,7 @@
 //     parts of at least one tile, as many as make the units come out even over the SMs (see there).
 //   * chunk_attn_kernel: one CTA per SM takes units from a counter.  Warp 0 fetches units and runs TMA
 //     (Q tiles through two slots, K and V tiles through one ring of slots, across unit borders), warp 1
-//     issues the MMAs, warps 2-5 / 6-9 are the softmax groups, one thread per row (TMEM lane).  A unit
+//     issues the MMAs, warps 4-7 / 8-11 are the softmax groups, one thread per row (TMEM lane).  A unit
 //     that holds all of its item's keys stores o; otherwise it leaves (m, l, O) in the workspace.
 //   * chunk_combine_kernel merges the parts of the rows that were cut.
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
@@ -29,7 +29,11 @@
 namespace llama {
 namespace {
 
-constexpr int CA_THREADS = 320;
+// Three warpgroups: warp 0 TMA, warp 1 MMA (2 and 3 leave), then the two softmax groups.  Launched with 168
+// registers a thread (384 x 168 = 64512), of which the first warpgroup gives up what the others take.
+constexpr int CA_THREADS = 384;
+constexpr int CA_REGS_ISSUE = 88, CA_REGS_SOFTMAX = 208;
+static_assert(CA_REGS_ISSUE + 2 * CA_REGS_SOFTMAX <= 3 * 168, "register split");
 constexpr uint32_t CA_TMEM_COLS = 512;
 constexpr int CP_THREADS = 1024;
 
@@ -231,6 +235,21 @@ struct CaSmem {
   static constexpr uint32_t TOTAL = OFF_BAR + 384 + 1024;
 };
 
+// Barriers, one arrival each unless noted.
+enum : int {
+  BAR_Q_FULL = 0,    // [2] per Q slot
+  BAR_Q_EMPTY = 2,   // [2]
+  BAR_U_FULL = 4,    // [2] per unit record
+  BAR_U_EMPTY = 6,   // [2] MMA warp and 8 softmax warps
+  BAR_S_FULL = 8,    // [2] per group
+  BAR_O_DONE = 10,   // [2]
+  BAR_P_FULL = 12,   // [2][2] per group and half of P; 128 threads
+  BAR_O_FREE = 16,   // [2] 128 threads
+  BAR_ML_FULL = 18,  // 128 threads
+  BAR_DRAIN = 19,
+  BAR_KV_FULL = 20,  // [NS], then [NS] empty ones
+};
+
 // One unit, as the roles of a CTA see it.
 struct __align__(16) ChunkUnit {
   int live;            // 0: no more units
@@ -258,6 +277,35 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t w) {
   return w;
 }
 
+// Keys past the last visible one of a row's 32 scores.
+__device__ __forceinline__ void mask_keys(uint32_t (&v)[32], int seen) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k > seen) v[k] = __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ float row_max(const uint32_t (&v)[32]) {
+  float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
+#pragma unroll
+  for (int k = 2; k < 30; k += 4) {
+    m0 = max3(m0, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+    m1 = max3(m1, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+  }
+  return fmaxf(max3(m0, __uint_as_float(v[30]), __uint_as_float(v[31])), m1);
+}
+// 32 scores of a row -> 16 bf16 pairs of P = 2^(s * scale - m); the fp32 values are added to the row sums.
+__device__ __forceinline__ void exp_pack(const uint32_t (&v)[32], uint32_t* w, float scale, float m, float& ls0,
+                                         float& ls1) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float a0, a1;
+    fma_f32x2(a0, a1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), scale, scale, -m, -m);
+    const float p0 = ex2(a0);
+    const float p1 = ex2(a1);
+    add_f32x2(ls0, ls1, p0, p1);
+    w[e] = pack_bf16x2(p0, p1);
+  }
+}
+
 // The non-finite values among keys j0..j1 of sequence b, added to the row stored at `at` (which was summed
 // without them).  Called for tiles at a sequence's end only, and only when one was met.
 template <int HD>
@@ -283,18 +331,17 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* q_full = bars + 0;       // [2] per Q slot
-  uint64_t* q_empty = bars + 2;      // [2]
-  uint64_t* u_full = bars + 4;       // [2] per unit record
-  uint64_t* u_empty = bars + 6;      // [2] (MMA thread + 8 softmax warps)
-  uint64_t* s_full = bars + 8;       // [2] per group
-  uint64_t* p_full = bars + 10;      // [2] (128 arrivals)
-  uint64_t* o_done = bars + 12;      // [2]
-  uint64_t* o_free = bars + 14;      // [2] (128 arrivals)
-  uint64_t* ml_full = bars + 16;     //     (128 arrivals)
-  uint64_t* drain = bars + 17;
-  uint64_t* kv_full = bars + 18;     // [NS]
-  uint64_t* kv_empty = kv_full + NS; // [NS]
+  uint64_t* q_full = bars + BAR_Q_FULL;
+  uint64_t* q_empty = bars + BAR_Q_EMPTY;
+  uint64_t* u_full = bars + BAR_U_FULL;
+  uint64_t* u_empty = bars + BAR_U_EMPTY;
+  uint64_t* s_full = bars + BAR_S_FULL;
+  uint64_t* o_done = bars + BAR_O_DONE;
+  uint64_t* p_full = bars + BAR_P_FULL;
+  uint64_t* o_free = bars + BAR_O_FREE;
+  uint64_t* ml_full = bars + BAR_ML_FULL;
+  uint64_t* kv_full = bars + BAR_KV_FULL;
+  uint64_t* kv_empty = kv_full + NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + NS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* dirty = reinterpret_cast<volatile int*>(tmem_slot + 2);   // serial of the last unit with non-finite V
@@ -304,8 +351,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 18 + 2 * NS; ++i)
-      mbar_init(&bars[i], (i == 6 || i == 7) ? 9 : (i == 10 || i == 11 || (i >= 14 && i <= 16)) ? 128 : 1);
+    for (int i = 0; i < BAR_KV_FULL + 2 * NS; ++i)
+      mbar_init(&bars[i], i >= BAR_U_EMPTY && i < BAR_U_EMPTY + 2 ? 9
+                          : i >= BAR_P_FULL && i <= BAR_ML_FULL   ? 128
+                                                                  : 1);
     *abort_flag = 0;
     *dirty = -1;
     fence_mbar_init();
@@ -321,203 +370,207 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
   const uint32_t sbase = smem_u32(smem);
   pdl_wait();   // the plan
 
-  if (warp == 0) {  // ---------------------------------------------------- units and TMA (whole warp)
-    const int n_units = p.head->n_units;
-    int u = blockIdx.x, hint = 0, serial = 0, qi = 0, e = 0;
-    bool ok = true;
-    const uint32_t q_bytes = (uint32_t)(HALVES * p.r * p.tpt * 128);
-    while (ok) {
-      ChunkUnit d;
-      d.live = 0;
-      while (u < n_units) {       // the next unit that has keys
-        hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
-        const ChunkSeq s = p.seq[hint];
-        const int x = u - s.unit0;
-        const int g = x % p.n_kv, y = x / p.n_kv;
-        const int chunk = y / s.np, pair = s.np - 1 - y % s.np;      // the longest items of a chunk first
-        const int first = pair * 2 * p.tpt;                           // token of the earlier Q tile
-        const int tail = s.n - first;                                 // tokens from there on
-        const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
-        const int t0 = chunk * s.ct, t1 = min(t0 + s.ct, nt0);
-        d.lone = tail <= p.tpt;
-        if (t0 < t1) {
-          d.live = 1;
-          d.t0 = t0;
-          d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
-          d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
-          d.row1 = s.lo + first;
-          d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
-          d.end = s.lo + s.n;
-          d.pos_off = s.c - s.lo;
-          d.g = g;
-          d.kv_len = s.c + s.n;
-          d.clean = (s.c + first + 1) / 128;
-          d.part = s.nc > 1 ? s.part0 + chunk * s.n - s.lo : INT_MIN;
-          d.b = hint;
+  if (warp < 4) {
+    regs_give<CA_REGS_ISSUE>();
+    if (warp == 0) {  // ---------------------------------------------------- units and TMA (whole warp)
+      const int n_units = p.head->n_units;
+      int u = blockIdx.x, hint = 0, serial = 0, qi = 0, e = 0;
+      bool ok = true;
+      const uint32_t q_bytes = (uint32_t)(HALVES * p.r * p.tpt * 128);
+      while (ok) {
+        ChunkUnit d;
+        d.live = 0;
+        while (u < n_units) {       // the next unit that has keys
+          hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
+          const ChunkSeq s = p.seq[hint];
+          const int x = u - s.unit0;
+          const int g = x % p.n_kv, y = x / p.n_kv;
+          const int chunk = y / s.np, pair = s.np - 1 - y % s.np;      // the longest items of a chunk first
+          const int first = pair * 2 * p.tpt;                           // token of the earlier Q tile
+          const int tail = s.n - first;                                 // tokens from there on
+          const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
+          const int t0 = chunk * s.ct, t1 = min(t0 + s.ct, nt0);
+          d.lone = tail <= p.tpt;
+          if (t0 < t1) {
+            d.live = 1;
+            d.t0 = t0;
+            d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
+            d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
+            d.row1 = s.lo + first;
+            d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
+            d.end = s.lo + s.n;
+            d.pos_off = s.c - s.lo;
+            d.g = g;
+            d.kv_len = s.c + s.n;
+            d.clean = (s.c + first + 1) / 128;
+            d.part = s.nc > 1 ? s.part0 + chunk * s.n - s.lo : INT_MIN;
+            d.b = hint;
+          }
+          if (lane == 0) u = atomicAdd(&p.head->counter, 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+          if (d.live) break;
         }
-        if (lane == 0) u = atomicAdd(&p.head->counter, 1);
-        u = __shfl_sync(0xffffffffu, u, 0);
-        if (d.live) break;
-      }
-      // ---- hand the unit over
-      const int us = serial & 1;
-      if (lane == 0) {
-        ok = mbar_wait(&u_empty[us], ((serial >> 1) & 1) ^ 1, abort_flag, p.status);
-        if (ok) {
-          volatile int* dst = reinterpret_cast<volatile int*>(units + us);
-          const int* src = reinterpret_cast<const int*>(&d);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) dst[i] = src[i];
-          mbar_arrive(&u_full[us]);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok || !d.live) break;
-      ++serial;
-      // ---- Q tiles
-      for (int x = 0; ok && x < (d.lone ? 1 : 2); ++x) {
-        if (!d.lone && x == 1 && d.n1 == 0) break;
+        // ---- hand the unit over
+        const int us = serial & 1;
         if (lane == 0) {
-          const int qs = qi & 1, row = x == 0 ? d.row0 : d.row1;
-          ok = mbar_wait(&q_empty[qs], ((qi >> 1) & 1) ^ 1, abort_flag, p.status);
-          if (ok && !box_in(0, HD, (int64_t)d.g * p.r, p.n_q, row, p.T)) { *abort_flag = 1; ok = false; }
+          ok = mbar_wait(&u_empty[us], ((serial >> 1) & 1) ^ 1, abort_flag, p.status);
           if (ok) {
-            mbar_arrive_expect_tx(&q_full[qs], q_bytes);
-            for (int hh = 0; hh < HALVES; ++hh)
-              tma_load_3d(sbase + L::OFF_Q + qs * L::TILE + hh * 16384, &p.tmQ, &q_full[qs], hh * 64, d.g * p.r, row);
-          }
-        }
-        if (ok) ++qi;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      }
-      // ---- K and V tiles; the page ids come 32 at a time
-      const int nt = d.lone ? d.n0 + d.n1 : d.n0;
-      const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
-      int page_reg = 0;
-      for (int t = 0; ok && t < nt; ++t) {
-        if ((t & 31) == 0) {
-          page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
-          if (page_reg < 0 || page_reg >= p.n_pages) {
-            atomicOr(p.status, STATUS_BAD_PLAN);
-            page_reg = p.n_pages;            // outside the tensor: the copy fills the tile with zeros
-          }
-        }
-        const int page = __shfl_sync(0xffffffffu, page_reg, t & 31);
-        if (lane == 0) {
-          for (int kv = 0; ok && kv < 2; ++kv, ++e) {
-            const int slot = e % NS;
-            ok = mbar_wait(&kv_empty[slot], ((e / NS) & 1) ^ 1, abort_flag, p.status);
-            if (ok && !box_in(0, HD, d.g, p.n_kv, 0, 128, page, (int64_t)p.n_pages + 1)) { *abort_flag = 1; ok = false; }
-            if (!ok) break;
-            mbar_arrive_expect_tx(&kv_full[slot], L::TILE);
-            for (int hh = 0; hh < HALVES; ++hh)
-              tma_load_4d(sbase + L::OFF_KV + slot * L::TILE + hh * 16384, kv ? &p.tmV : &p.tmK, &kv_full[slot], hh * 64,
-                          d.g, 0, page);
+            volatile int* dst = reinterpret_cast<volatile int*>(units + us);
+            const int* src = reinterpret_cast<const int*>(&d);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dst[i] = src[i];
+            mbar_arrive(&u_full[us]);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok || !d.live) break;
+        ++serial;
+        // ---- Q tiles
+        for (int x = 0; ok && x < (d.lone ? 1 : 2); ++x) {
+          if (!d.lone && x == 1 && d.n1 == 0) break;
+          if (lane == 0) {
+            const int qs = qi & 1, row = x == 0 ? d.row0 : d.row1;
+            ok = mbar_wait(&q_empty[qs], ((qi >> 1) & 1) ^ 1, abort_flag, p.status);
+            if (ok && !box_in(0, HD, (int64_t)d.g * p.r, p.n_q, row, p.T)) { *abort_flag = 1; ok = false; }
+            if (ok) {
+              mbar_arrive_expect_tx(&q_full[qs], q_bytes);
+              for (int hh = 0; hh < HALVES; ++hh)
+                tma_load_3d(sbase + L::OFF_Q + qs * L::TILE + hh * 16384, &p.tmQ, &q_full[qs], hh * 64, d.g * p.r, row);
+            }
+          }
+          if (ok) ++qi;
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        // ---- K and V tiles; the page ids come 32 at a time
+        const int nt = d.lone ? d.n0 + d.n1 : d.n0;
+        const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
+        int page_reg = 0;
+        for (int t = 0; ok && t < nt; ++t) {
+          if ((t & 31) == 0) {
+            page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
+            if (page_reg < 0 || page_reg >= p.n_pages) {
+              atomicOr(p.status, STATUS_BAD_PLAN);
+              page_reg = p.n_pages;            // outside the tensor: the copy fills the tile with zeros
+            }
+          }
+          const int page = __shfl_sync(0xffffffffu, page_reg, t & 31);
+          if (lane == 0) {
+            for (int kv = 0; ok && kv < 2; ++kv, ++e) {
+              const int slot = e % NS;
+              ok = mbar_wait(&kv_empty[slot], ((e / NS) & 1) ^ 1, abort_flag, p.status);
+              if (ok && !box_in(0, HD, d.g, p.n_kv, 0, 128, page, (int64_t)p.n_pages + 1)) { *abort_flag = 1; ok = false; }
+              if (!ok) break;
+              mbar_arrive_expect_tx(&kv_full[slot], L::TILE);
+              for (int hh = 0; hh < HALVES; ++hh)
+                tma_load_4d(sbase + L::OFF_KV + slot * L::TILE + hh * 16384, kv ? &p.tmV : &p.tmK, &kv_full[slot], hh * 64,
+                            d.g, 0, page);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
       }
-    }
-    // every copy issued has landed before the CTA leaves (at once, unless a wait ran out)
-    if (lane == 0) {
+      // every copy issued has landed before the CTA leaves (at once, unless a wait ran out)
+      if (lane == 0) {
+        int no_abort = 0;
+        for (int k = max(0, e - NS); k < e; ++k) mbar_wait(&kv_full[k % NS], (k / NS) & 1, &no_abort, p.status);
+        for (int k = max(0, qi - 2); k < qi; ++k) mbar_wait(&q_full[k & 1], (k >> 1) & 1, &no_abort, p.status);
+      }
+    } else if (warp == 1) {  // ------------------------------------------ MMA issuer (whole warp)
+      // Every lane runs the loop and one elected lane's instructions take effect, and every wait ends by a
+      // vote: the control flow stays uniform, so descriptors live in uniform registers.  Issued from a
+      // one-lane branch, 8 MMAs took 600-900 cycles against the 512 they execute in (clock stamps, hd 128):
+      // 2048 tokens after 30720 took 1014 us, 807 from the whole warp, 756 with P in halves and votes.
+      const uint32_t one = elect_one();
+      const uint32_t idesc_s = idesc_bf16(128, 128);
+      const uint32_t idesc_o = idesc_bf16(128, HD, /*b_mn_major=*/true);
+      const uint64_t kdesc = sdesc_sw128(sbase + L::OFF_KV, 16, 1024);
+      const uint64_t vdesc = sdesc_sw128(sbase + L::OFF_KV, 16384, 1024);
+      const uint64_t qdesc = sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
+      constexpr int TILE16 = (int)(L::TILE >> 4);
+      constexpr int BAR_KV_EMPTY = BAR_KV_FULL + NS;
+      const uint32_t bar = smem_u32(bars);
+      auto B = [&](int i) { return bar + 8u * (uint32_t)i; };
+      auto wait = [&](int i, int parity) { return mbar_wait_warp(B(i), (uint32_t)parity, abort_flag, p.status); };
+      int qi = 0;                            // Q tiles so far
+      int ks = 0, kph = 0, vs = 1, vph = 0;  // ring slot and phase of the next K and V tile
+      int rounds[2] = {0, 0}, used[2] = {0, 0};   // per group: rounds, and units with any
+      bool ok = true;
+      for (int serial = 0; ok; ++serial) {
+        const int us = serial & 1;
+        if (!wait(BAR_U_FULL + us, (serial >> 1) & 1)) break;
+        volatile const ChunkUnit* d = units + us;
+        const int live = __shfl_sync(0xffffffffu, d->live, 0), lone = __shfl_sync(0xffffffffu, d->lone, 0);
+        const int n0 = __shfl_sync(0xffffffffu, d->n0, 0), n1 = __shfl_sync(0xffffffffu, d->n1, 0);
+        if (!live) break;
+        if (one) mbar_arrive(bars + BAR_U_EMPTY + us);   // its fields are in registers
+        const int nq = lone || n1 == 0 ? 1 : 2;
+        // S_x = Q_x K^T of the next K tile; `last`: no other group reads the tile
+        auto issue_s = [&](int x, int i, bool last) -> bool {
+          if ((x == 0 || lone) && !wait(BAR_KV_FULL + ks, kph)) return false;
+          tc_fence_after();
+          const int qs = (qi + (lone ? 0 : x)) & 1;
+          const uint64_t ad0 = qdesc + (uint64_t)(qs * TILE16);
+          const uint64_t bd0 = kdesc + (uint64_t)(ks * TILE16);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
+            tc_mma_if(one, tmem + x * 128, ad0 + off, bd0 + off, idesc_s, k > 0 ? 1u : 0u);
+          }
+          tc_commit_if(one, B(BAR_S_FULL + x));
+          if (last) {
+            tc_commit_if(one, B(BAR_KV_EMPTY + ks));
+            ks += 2;
+            if (ks >= NS) { ks -= NS; kph ^= 1; }
+          }
+          if (lone ? 2 * i + x == n0 + n1 - 1 : i == (x ? n1 : n0) - 1) tc_commit_if(one, B(BAR_Q_EMPTY + qs));
+          return true;
+        };
+        // O_x += P_x V of the next V tile
+        auto issue_pv = [&](int x, int i, bool last) -> bool {
+          if ((x == 0 || lone) && !wait(BAR_KV_FULL + vs, vph)) return false;
+          const uint64_t bd0 = vdesc + (uint64_t)(vs * TILE16);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {   // P comes in two halves of 64 keys
+            if (!wait(BAR_P_FULL + 2 * x + half, rounds[x] & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)   // 16 keys per step: TMEM columns 8k..8k+7 of P_x
+              tc_mma_ts_if(one, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd0 + (uint64_t)(k * 2048 >> 4), idesc_o,
+                           k > 0 ? 1u : (i > 0 ? 1u : 0u));
+          }
+          if (i == (x ? n1 : n0) - 1) tc_commit_if(one, B(BAR_O_DONE + x));
+          ++rounds[x];
+          if (last) {
+            tc_commit_if(one, B(BAR_KV_EMPTY + vs));
+            vs += 2;
+            if (vs >= NS) { vs -= NS; vph ^= 1; }
+          }
+          return true;
+        };
+        ok = wait(BAR_Q_FULL + (qi & 1), (qi >> 1) & 1) &&
+             (nq == 1 || wait(BAR_Q_FULL + ((qi + 1) & 1), ((qi + 1) >> 1) & 1));
+        if (ok) ok = issue_s(0, 0, lone || n1 == 0);
+        if (ok && n1 > 0) ok = issue_s(1, 0, true);
+        // the first P V of a unit overwrites O_x: what the last unit that used it left must have been
+        // read (o_free counts those units only: a phase is never completed before it is waited for)
+        if (ok) ok = wait(BAR_O_FREE, (used[0]++ & 1) ^ 1);
+        if (ok && n1 > 0) ok = wait(BAR_O_FREE + 1, (used[1]++ & 1) ^ 1);
+        for (int i = 0; ok && i < n0; ++i) {
+          ok = issue_pv(0, i, lone || i >= n1);
+          if (ok && i + 1 < n0) ok = issue_s(0, i + 1, lone || i + 1 >= n1);
+          if (!ok || i >= n1) continue;
+          ok = issue_pv(1, i, true);
+          if (ok && i + 1 < n1) ok = issue_s(1, i + 1, true);
+        }
+        qi += nq;
+      }
       int no_abort = 0;
-      for (int k = max(0, e - NS); k < e; ++k) mbar_wait(&kv_full[k % NS], (k / NS) & 1, &no_abort, p.status);
-      for (int k = max(0, qi - 2); k < qi; ++k) mbar_wait(&q_full[k & 1], (k >> 1) & 1, &no_abort, p.status);
+      tc_commit_if(one, B(BAR_DRAIN));
+      mbar_wait(bars + BAR_DRAIN, 0, &no_abort, p.status);
     }
-  } else if (warp == 1) {  // -------------------------------------------- MMA issuer (whole warp)
-    // Every lane runs the loop and one elected lane's instructions take effect: the control flow stays
-    // uniform, so descriptors live in uniform registers.  Issued from a one-lane branch, each MMA's
-    // operands were moved there one by one: 600-900 cycles per 8 MMAs against the 512 they execute in
-    // (clock stamps at hd 128), and the tensor cores waited for their issuer half of the time.
-    const uint32_t one = elect_one();
-    const uint32_t idesc_s = idesc_bf16(128, 128);
-    const uint32_t idesc_o = idesc_bf16(128, HD, /*b_mn_major=*/true);
-    const uint64_t kdesc = sdesc_sw128(sbase + L::OFF_KV, 16, 1024);
-    const uint64_t vdesc = sdesc_sw128(sbase + L::OFF_KV, 16384, 1024);
-    const uint64_t qdesc = sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
-    int qi = 0;                                   // Q tiles so far
-    int ks = 0, kph = 0, vs = 1, vph = 0;         // ring slot and phase of the next K and V tile
-    int pc[2] = {0, 0}, oc[2] = {0, 0};           // per group: rounds, and units with any
-    bool ok = true;
-    for (int serial = 0; ok; ++serial) {
-      const int us = serial & 1;
-      if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
-      volatile const ChunkUnit* d = units + us;
-      const int live = __shfl_sync(0xffffffffu, d->live, 0), lone = __shfl_sync(0xffffffffu, d->lone, 0);
-      const int n0 = __shfl_sync(0xffffffffu, d->n0, 0), n1 = __shfl_sync(0xffffffffu, d->n1, 0);
-      if (!live) break;
-      if (one) mbar_arrive(&u_empty[us]);   // its fields are in registers
-      const int n[2] = {n0, n1};
-      const int nq = lone || n1 == 0 ? 1 : 2;
-      for (int x = 0; ok && x < nq; ++x) ok = mbar_wait(&q_full[(qi + x) & 1], ((qi + x) >> 1) & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      const int s_last = lone ? n0 + n1 : 0;       // lone: the S after which the Q tile is free
-      int s_count = 0;
-      // S_x = Q_x K^T of the next K tile; `last`: no other group uses the tile
-      auto issue_s = [&](int x, int i, bool last) -> bool {
-        if ((x == 0 || lone) && !mbar_wait(&kv_full[ks], kph, abort_flag, p.status)) return false;
-        tc_fence_after();
-        const int qs = (qi + (lone ? 0 : x)) & 1;
-        const uint64_t ad0 = qdesc + (uint64_t)(qs * (int)(L::TILE >> 4));
-        const uint64_t bd0 = kdesc + (uint64_t)(ks * (int)(L::TILE >> 4));
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint64_t off = (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4);
-          tc_mma_if(one, tmem + x * 128, ad0 + off, bd0 + off, idesc_s, k > 0 ? 1u : 0u);
-        }
-        tc_commit_if(one, &s_full[x]);
-        ++s_count;
-        if (lone ? s_count == s_last : i == n[x] - 1) tc_commit_if(one, &q_empty[qs]);
-        if (last) {
-          tc_commit_if(one, &kv_empty[ks]);
-          ks += 2;
-          if (ks >= NS) { ks -= NS; kph ^= 1; }
-        }
-        return true;
-      };
-      // O_x += P_x V of the next V tile
-      auto issue_pv = [&](int x, int i, bool last) -> bool {
-        if ((x == 0 || lone) && !mbar_wait(&kv_full[vs], vph, abort_flag, p.status)) return false;
-        if (!mbar_wait(&p_full[x], pc[x] & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        const uint64_t bd0 = vdesc + (uint64_t)(vs * (int)(L::TILE >> 4));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)   // 16 keys per step; P_x k-step k is TMEM columns 8k..8k+7
-          tc_mma_ts_if(one, tmem + 256 + x * 128, tmem + x * 128 + k * 8, bd0 + (uint64_t)(k * 2048 >> 4), idesc_o,
-                       k > 0 ? 1u : (i > 0 ? 1u : 0u));
-        tc_commit_if(one, &o_done[x]);
-        ++pc[x];
-        if (last) {
-          tc_commit_if(one, &kv_empty[vs]);
-          vs += 2;
-          if (vs >= NS) { vs -= NS; vph ^= 1; }
-        }
-        return true;
-      };
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (ok && n[x] > 0) ok = issue_s(x, 0, lone || x == 1 || n1 == 0);
-      // the first P V of a unit overwrites O_x: what the last unit that used it left must have been
-      // read (o_free counts those units only: a phase is never completed before it is waited for)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (ok && n[x] > 0) ok = mbar_wait(&o_free[x], (oc[x]++ & 1) ^ 1, abort_flag, p.status);
-      for (int i = 0; ok && i < n0; ++i) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || i >= n[x]) continue;
-          ok = issue_pv(x, i, lone || x == 1 || i >= n1);
-          if (ok && i + 1 < n[x]) ok = issue_s(x, i + 1, lone || x == 1 || i + 1 >= n1);
-        }
-      }
-      qi += nq;
-    }
-    int no_abort = 0;
-    tc_commit_if(one, drain);
-    mbar_wait(drain, 0, &no_abort, p.status);
   } else {  // ------------------------------------------------------------ softmax groups
-    const int x = (warp - 2) >> 2;
+    regs_take<CA_REGS_SOFTMAX>();
+    const int x = (warp - 4) >> 2;
     const int qw = warp & 3;
     const int row = qw * 32 + lane;                     // TMEM lane = Q tile row
     const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
@@ -525,87 +578,32 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
     const uint32_t tO = tmem + 256 + x * 128 + lane_off;
     const int tok_in = row / p.r, head_in = row - tok_in * p.r;
     const bool row_used = row < p.r * p.tpt;
-    int rc = 0, e = 0, lone_count = 0;                  // rounds of this group, ring entries, lone units with n1 > 0
+    int rc = 0, unit_count = 0, lone_count = 0;         // rounds of this group, units with any, lone units with n1 > 0
+    int e = 0;                                          // ring entries of the units before
     bool ok = true;
     for (int serial = 0; ok; ++serial) {
       const int us = serial & 1;
-      if (!mbar_wait(&u_full[us], (serial >> 1) & 1, abort_flag, p.status)) break;
+      if (!mbar_wait_short(smem_u32(&u_full[us]), (serial >> 1) & 1, abort_flag, p.status)) break;
       // read from shared memory where it is used, and released at the unit's end: registers are short
       const volatile ChunkUnit& d = units[us];
       if (!d.live) break;
-      const int n = x ? d.n1 : d.n0, lone = d.lone;
+      const int n1 = d.n1, n = x ? n1 : d.n0, lone = d.lone;
       const int tok = (x ? d.row1 : d.row0) + tok_in;   // packed row of the token
       const int qpos = tok + d.pos_off;
       const int full = (qpos - tok_in + 1) / 128;       // tiles every row of the Q tile sees
       float m_ref = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i, ++rc) {
         const int jt = lone ? 2 * i + x : i, j = d.t0 + jt;
-        if (!mbar_wait(&s_full[x], rc & 1, abort_flag, p.status)) { ok = false; break; }
+        if (!mbar_wait_short(smem_u32(&s_full[x]), rc & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
         const int kbase = j * 128;
-        uint32_t v0[32], v1[32], v2[32], v3[32];
-        tmem_ld32(tS + 0, v0);
-        tmem_ld32(tS + 32, v1);
-        tmem_ld32(tS + 64, v2);
-        tmem_ld32(tS + 96, v3);
-        tc_wait_ld();
-        if (j >= full) {   // keys past the query's position
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (kbase + k > qpos) v0[k] = __float_as_uint(-INFINITY);
-            if (kbase + 32 + k > qpos) v1[k] = __float_as_uint(-INFINITY);
-            if (kbase + 64 + k > qpos) v2[k] = __float_as_uint(-INFINITY);
-            if (kbase + 96 + k > qpos) v3[k] = __float_as_uint(-INFINITY);
-          }
-        }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          m0 = max3(m0, __uint_as_float(v0[k]), __uint_as_float(v0[k + 1]));
-          m1 = max3(m1, __uint_as_float(v1[k]), __uint_as_float(v1[k + 1]));
-          m2 = max3(m2, __uint_as_float(v2[k]), __uint_as_float(v2[k + 1]));
-          m3 = max3(m3, __uint_as_float(v3[k]), __uint_as_float(v3[k + 1]));
-        }
-        const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
-        float alpha = 1.f;
-        bool resc = false;
-        if (i == 0) {
-          m_ref = mt;
-        } else if (mt > m_ref + kRescaleLog2) {
-          alpha = ex2(m_ref - mt);
-          m_ref = mt;
-          resc = true;
-        }
-        if (i > 0 && __any_sync(0xffffffffu, resc)) {
-          if (!mbar_wait(&o_done[x], (rc - 1) & 1, abort_flag, p.status)) { ok = false; break; }
-          tc_fence_after();
-          l *= alpha;
-#pragma unroll 1
-          for (int c = 0; c < HD / 16; ++c) {
-            uint32_t ov[16];
-            tmem_ld16_at(tO + c * 16, ov);
-            tc_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-            tmem_st16(tO + c * 16, ov);
-          }
-          tc_wait_st();
-        }
-        // a row that has seen no key yet keeps m = -inf; its P is 0
-        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
-        float ls0 = 0.f, ls1 = 0.f;
-        exp_chunk(v0, tS + 0, p.scale_log2, mb, ls0, ls1);
-        exp_chunk(v1, tS + 16, p.scale_log2, mb, ls0, ls1);
-        exp_chunk(v2, tS + 32, p.scale_log2, mb, ls0, ls1);
-        exp_chunk(v3, tS + 48, p.scale_log2, mb, ls0, ls1);
-        tc_wait_st();
-        l += ls0 + ls1;
+        const int seen = j >= full ? qpos - kbase : 127;   // keys 0..seen of the tile are visible
         // Tiles with keys that some row does not see: P is 0 there, and 0 x V must stay 0.  Rows past
         // the sequence's end are zeroed; non-finite elements of the others too, and what they add to
         // the rows that do see them is added at the end (below).  Thread `row` takes key `row`.
         if (j >= d.clean) {
           const int en = e + 2 * jt + 1, slot = en % NS;
-          if (!mbar_wait(&kv_full[slot], (en / NS) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!mbar_wait_short(smem_u32(&kv_full[slot]), (en / NS) & 1, abort_flag, p.status)) { ok = false; break; }
           uint8_t* vrow = smem + L::OFF_KV + slot * L::TILE + row * 128;
           const bool past = kbase + row >= d.kv_len;
 #pragma unroll
@@ -625,14 +623,82 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           }
           fence_proxy_async_smem();
         }
+        // A unit's first tile finds its maximum before anything else, a tile with unseen keys has them
+        // masked in place: one rolled pass over the scores in TMEM, off the common path.
+        if (i == 0 || j >= full) {
+          float m = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t t[32];
+            tmem_ld32(tS + c, t);
+            tc_wait_ld();
+            if (j >= full) {
+              mask_keys(t, seen - c);
+              tmem_st32(tS + c, t);
+            }
+            m = fmaxf(m, row_max(t));
+          }
+          tc_wait_st();
+          if (i == 0) m_ref = m * p.scale_log2;
+        }
+        // P in two halves, each handed over as soon as it is stored: the first half's P V runs while the
+        // second half is formed.  The first half is formed against the reference maximum so far while
+        // the tile's maximum is found (exp2 and max run in different pipes); the rare tile that grows
+        // it by more than 2^8 forms it again.
+        uint32_t va[32], vb[32], vc[32], vd[32], w[32];
+        float l0, l1, l2, l3;
+        for (;;) {
+          // a row that has seen no key yet keeps m = -inf; its P is 0
+          const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+          tmem_ld32(tS, va);
+          tmem_ld32(tS + 32, vb);
+          tmem_ld32(tS + 64, vc);
+          tmem_ld32(tS + 96, vd);
+          tc_wait_ld();
+          l0 = l1 = l2 = l3 = 0.f;
+          float m = row_max(va);
+          exp_pack(va, w, p.scale_log2, mb, l0, l1);
+          m = fmaxf(m, fmaxf(row_max(vb), row_max(vc)));
+          exp_pack(vb, w + 16, p.scale_log2, mb, l2, l3);
+          const float mt = fmaxf(m, row_max(vd)) * p.scale_log2;
+          const bool grow = mt > m_ref + kRescaleLog2;
+          if (!__any_sync(0xffffffffu, grow)) break;
+          // (i > 0: the first tile's reference is its maximum)  S of this round having arrived, O holds
+          // the P V of all the tiles before it
+          const float alpha = grow ? ex2(m_ref - mt) : 1.f;
+          if (grow) m_ref = mt;
+          l *= alpha;
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16_at(tO + c * 16, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+            tmem_st16(tO + c * 16, ov);
+          }
+          tc_wait_st();
+        }
+        if (!ok) break;
+        tmem_st32(tS, w);
+        tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[2 * x]);
+        const float mb = m_ref == -INFINITY ? 0.f : m_ref;
+        float l4 = 0.f, l5 = 0.f, l6 = 0.f, l7 = 0.f;
+        exp_pack(vc, w, p.scale_log2, mb, l4, l5);
+        exp_pack(vd, w + 16, p.scale_log2, mb, l6, l7);
+        tmem_st32(tS + 32, w);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[2 * x + 1]);
+        l += ((l0 + l1) + (l2 + l3)) + ((l4 + l5) + (l6 + l7));
       }
-      const int n_tiles = lone ? d.n0 + d.n1 : d.n0;
-      e += 2 * n_tiles;
+      const int n_tiles = lone ? d.n0 + n1 : d.n0;
       if (!ok) break;
       // ---- the unit's result
-      if (n > 0 && !mbar_wait(&o_done[x], (rc - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+      if (n > 0 && !mbar_wait_short(smem_u32(&o_done[x]), unit_count++ & 1, abort_flag, p.status)) { ok = false; break; }
+      e += 2 * n_tiles;
       tc_fence_after();
       if (lone && x == 1) {                         // hand (m, l, O_1) to group 0
         if (n > 0) {
@@ -645,9 +711,9 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
         continue;
       }
       float w0 = 1.f, w1 = 0.f;
-      const bool merge = lone && d.n1 > 0;
+      const bool merge = lone && n1 > 0;
       if (merge) {
-        if (!mbar_wait(ml_full, lone_count & 1, abort_flag, p.status)) { ok = false; break; }
+        if (!mbar_wait_short(smem_u32(ml_full), lone_count & 1, abort_flag, p.status)) { ok = false; break; }
         ++lone_count;
         tc_fence_after();
         const float2 o = ml[row];

@@ -268,6 +268,24 @@ def test_chunk_attention(case):
     b.check(o, every=1 if b.T * (max(cached) + 300) * n_q < 1e6 else 37)
 
 
+@pytest.mark.parametrize("n_q,n_kv,hd", [(32, 8, 128), (8, 8, 64)])
+@pytest.mark.parametrize("kind", ["lone", "pairs", "both"])
+def test_chunk_attention_many_units_per_sm(kind, n_q, n_kv, hd):
+    """More work units than SMs, of many key tiles each: every CTA walks from unit to unit, between
+    lone Q tiles and pairs."""
+    rng = np.random.default_rng(len(kind))
+    B = 40
+    cached = [int(c) for c in rng.integers(0, 4000, B)]
+    tile = 128 // (n_q // n_kv)
+    few = [int(n) for n in rng.integers(1, min(tile, 6) + 1, B)]
+    many = [int(n) for n in rng.integers(tile + 1, 3 * tile, B)]
+    new = {"lone": few, "pairs": many, "both": [few[b] if b % 2 else many[b] for b in range(B)]}[kind]
+    b = Batch(cached, new, n_q, n_kv, hd, seed=B)
+    o = b.run()
+    assert _status() == 0
+    b.check(o, every=97)
+
+
 def test_chunk_attention_long_and_mixed():
     """One long prompt chunk among short decodes, and sharp rows (scores of +-100)."""
     b = Batch([3000, 20, 7000, 1], [1, 1500, 4, 1], 32, 8, 128, seed=5, q_std=8.0)
