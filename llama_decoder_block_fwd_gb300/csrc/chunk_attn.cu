@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "kernels.h"
@@ -36,19 +37,39 @@ constexpr int CA_REGS_ISSUE = 88, CA_REGS_SOFTMAX = 208;
 static_assert(CA_REGS_ISSUE + 2 * CA_REGS_SOFTMAX <= 3 * 168, "register split");
 constexpr uint32_t CA_TMEM_COLS = 512;
 constexpr int CP_THREADS = 1024;
+constexpr int kMaxGrid = 256;            // attention CTAs at most (one per SM; sizes the workspace)
 
 // Per sequence, written by the plan.
 struct ChunkSeq {
   int unit0;          // first unit
   int lo, n, c;       // first packed row, new tokens, cached positions
-  int np;             // items per KV group: pairs of Q tiles
-  int nc, ct;         // key chunks and tiles per chunk
-  int part0;          // first partial row (nc > 1): partial row of token i in chunk k is part0 + k * n + i
-  int split0;         // rows of cut sequences before this one (cut: nc > 1)
+  int np, wp;         // items per KV group (pairs of Q tiles); the last wp of them are not cut
+  int nc, ct;         // key chunks of the others and tiles per chunk
+  int cut_n;          // tokens with partial rows (0 if nc = 1): those of the items that are cut
+  int part0;          // first partial row: token i's in chunk k is part0 + k * cut_n + i
+  int split0;         // cut_n of the sequences before this one
 };
 struct ChunkHead {
   int n_units, counter, n_split, pad;
 };
+
+// One unit, as the roles of a CTA see it.
+struct __align__(16) ChunkUnit {
+  int live;            // 0: no more units
+  int t0;              // first key tile
+  int n0, n1;          // rounds of groups 0 and 1
+  int lone;            // 1: one Q tile, key tiles alternate between the groups
+  int row0, row1;      // first packed row of each group's Q tile
+  int end;             // the sequence's end row
+  int pos_off;         // position = packed row + pos_off
+  int g;               // KV group
+  int kv_len;          // keys of the sequence
+  int clean;           // tiles from here on hold keys that some row of the unit does not see
+  int part;            // partial row = packed row + part; INT_MIN: store o
+  int b;
+  int pad0, pad1;
+};
+static_assert(sizeof(ChunkUnit) == 64, "unit record");
 
 struct ChunkParams {   // 128-byte aligned by its tensor maps
   CUtensorMap tmQ;     // [T, n_q, hd], box (64, r, tpt)
@@ -60,7 +81,8 @@ struct ChunkParams {   // 128-byte aligned by its tensor maps
   int B, T, n_q, n_kv, r, tpt, n_pages, max_pages, max_pos;
   float scale_log2;    // log2(e) / sqrt(hd)
   ChunkHead* head;
-  ChunkSeq* seq;
+  ChunkUnit* first;    // [grid]
+  ChunkSeq* seq;       // [B]
   float* part_o;       // [part_rows, n_q, hd]
   float2* part_ml;     // [part_rows, n_q]  (m in log2 units, l)
   int part_rows, grid;
@@ -86,131 +108,244 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 
 // ------------------------------------------------------------------------------------------ plan
 // A sequence of n new tokens after c cached has np = ceil(n / (2 tpt)) items per KV group of nt =
-// ceil((c + n) / 128) key tiles or less.  With at most C tiles per unit its ranges are cut into nc =
-// ceil(nt / C).  C is the candidate of least estimated time, in units of one tile's time:
-//   units in rounds of one per CTA x (mean unit + kUnitCost), at least the longest unit, + the
-//   merge if anything is cut,
-// where a unit costs kUnitCost more than its tiles (its pipeline fills and drains) and kCutCost more
-// when it leaves partials.  The candidates run from 1 tile to all in steps of sqrt(2), one per warp;
-// those whose partials do not fit the workspace are out, the last (nothing cut) always fits.
-constexpr float kUnitCost = 1.5f, kCutCost = 1.5f, kMergeCost = 3.0f;
+// ceil((c + n) / 128) key tiles or less.  With at most C tiles per unit a range is cut into nc =
+// ceil(nt / C).  Of the items that share their K and V with others of their sequence the first `whole`
+// (whole rounds of one per CTA, or none) are not cut, only what is left over after them; K and V that one
+// item reads alone are read once however it is cut.  (C, whole) is the candidate of least estimated time,
+// in units of one tile's time (1.4 us for a pair at hd 128).  A unit costs kUnitCost more than its tiles
+// (its pipeline fills and drains); one that leaves partials kCutCost, and kRowCost for 256 rows of them,
+// written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
+// others fill up to half of the longest one.  Replayed on a list scheduler over 70 mixes of lengths this
+// is within 1% of the best candidate on average.  C runs from 1 tile to all in steps of sqrt(2), one per
+// warp; candidates whose partials do not fit the workspace are out, the last C (nothing cut) always fits.
+//
+// One CTA does this while all the others wait, so it is written for few instructions: 32 warps on one SM
+// are bound by its issue slots (integer division alone cost 3 us of 9.5 at 64 sequences).
+constexpr float kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost = 2.0f, kMergeCost = 2.0f;
+constexpr int CP_SEQS = 1024;      // sequences whose shapes are kept in shared memory (one per thread)
 
-struct SeqShape { int lo, n, c, np, nt; bool bad; };
-__device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b) {
+// floor(a / b) for 0 <= a < 2^22, 0 < b, inv within a few ulp of 1 / b
+__device__ __forceinline__ int div_by(int a, int b, float inv) {
+  int q = (int)((float)a * inv);
+  if (q * b > a) --q;
+  if ((q + 1) * b <= a) ++q;
+  return q;
+}
+__device__ __forceinline__ int cdiv_by(int a, int b, float inv) { return div_by(a + b - 1, b, inv); }
+
+struct SeqShape { int lo, n, c, np, nt; };
+// cu, n_cached -> the sequence's shape; lengths that cannot be right bring nothing and set bad
+__device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b, bool& bad) {
   SeqShape s;
   s.lo = __ldg(p.cu_new + b);
   const int hi = __ldg(p.cu_new + b + 1);
   s.c = __ldg(p.n_cached + b);
   s.n = hi - s.lo;
-  s.bad = s.lo < 0 || s.n < 0 || hi > p.T || (s.n > 0 && (s.c < 0 || (int64_t)s.c + s.n - 1 > p.max_pos));
-  if (s.bad || s.n == 0) { s.n = 0; s.np = 0; s.nt = 0; s.c = 0; return s; }
+  const bool wrong = s.lo < 0 || s.n < 0 || hi > p.T || (s.n > 0 && (s.c < 0 || (int64_t)s.c + s.n - 1 > p.max_pos));
+  bad = bad || wrong;
+  if (wrong || s.n == 0) { s.n = 0; s.c = 0; }
   s.np = cdiv(s.n, 2 * p.tpt);
-  s.nt = cdiv(s.c + s.n, 128);
+  s.nt = (s.c + s.n + 127) >> 7;
   return s;
 }
 
-__device__ __forceinline__ void cut(int nt, int C, int& nc, int& ct) {
-  nc = max(1, cdiv(nt, C));
-  ct = max(1, cdiv(nt, nc));
-  nc = max(1, cdiv(nt, ct));
+// nt tiles in chunks of at most C (inv = 1 / C): their number and their tiles
+__device__ __forceinline__ void cut(int nt, int C, float inv, int& nc, int& ct) {
+  nc = nt <= C ? 1 : cdiv_by(nt, C, inv);
+  const float inv_nc = __frcp_rn((float)nc);
+  ct = max(1, cdiv_by(nt, nc, inv_nc));
+  nc = max(1, cdiv_by(nt, ct, __frcp_rn((float)ct)));
+}
+// candidate w of 32: about 2^(w / 2) tiles, the last one unbounded
+__device__ __forceinline__ int candidate(int w) {
+  return w == 31 ? 1 << 20 : (w & 1) ? (3 << (w >> 1)) >> 1 : 1 << (w >> 1);
 }
 
-__global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ float est[32];
-  __shared__ int warp_sum[3][32];
-  __shared__ int chosen;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  // candidate of warp w: about 2^(w / 2) tiles, the last one unbounded
-  const int C = warp == 31 ? INT_MAX / 2 : (warp & 1) ? (3 << (warp >> 1)) >> 1 : 1 << (warp >> 1);
-  float units = 0.f, cost = 0.f, longest = 0.f;
-  int64_t rows = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const SeqShape s = seq_shape(p, b);
-    if (s.n == 0) continue;
-    int nc, ct;
-    cut(s.nt, C, nc, ct);
-    const float mean = fminf((float)s.nt, ((float)s.c + 0.5f * (float)(s.n + min(s.n, 2 * p.tpt))) * (1.f / 128.f) + 0.5f);
-    const float k = fmaxf(1.f, mean / (float)ct);             // units per item
-    const float items = (float)s.np * (float)p.n_kv;
-    const float over = kUnitCost + (nc > 1 ? kCutCost : 0.f);
-    units += items * k;
-    cost += items * (mean + k * over);
-    longest = fmaxf(longest, (float)min(ct, s.nt) + over);
-    if (nc > 1) rows += (int64_t)nc * s.n;
-  }
+// Unit u of sequence b (seq[b].unit0 <= u); false if no row of it sees its keys.
+__device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& s, int b, int u, ChunkUnit& d) {
+  // first the uncut items, the longest first, then the others chunk by chunk
+  const int x = u - s.unit0, whole = s.wp * p.n_kv, nq = s.np - s.wp;
+  const int y = (x < whole ? x : x - whole) / p.n_kv;
+  const int chunk = x < whole ? 0 : y / nq, pair = x < whole ? s.np - 1 - y : nq - 1 - y % nq;
+  const int first = pair * 2 * p.tpt;                                       // token of the earlier Q tile
+  const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
+  const int t0 = chunk * s.ct, t1 = x < whole ? nt0 : min(t0 + s.ct, nt0);
+  d.live = t0 < t1;
+  d.t0 = t0;
+  d.lone = s.n - first <= p.tpt;
+  d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
+  d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
+  d.row1 = s.lo + first;
+  d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
+  d.end = s.lo + s.n;
+  d.pos_off = s.c - s.lo;
+  d.g = x % p.n_kv;
+  d.kv_len = s.c + s.n;
+  d.clean = (s.c + first + 1) / 128;
+  d.part = x >= whole && s.cut_n > 0 ? s.part0 + chunk * s.cut_n - s.lo : INT_MIN;
+  d.b = b;
+  d.pad0 = d.pad1 = 0;
+  return d.live;
+}
+
+// Exclusive prefix sums over the block of N integers per thread; total gets the block's sums.  buf: [N][32].
+template <int N>
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*buf)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl[N];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    units += __shfl_xor_sync(0xffffffffu, units, o);
-    cost += __shfl_xor_sync(0xffffffffu, cost, o);
-    longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-    rows += __shfl_xor_sync(0xffffffffu, rows, o);
-  }
-  if (lane == 0) {
-    float e = units > 0.f ? fmaxf(longest, ceilf(units / (float)p.grid) * cost / units) : 0.f;
-    if (rows > 0) e += kMergeCost;
-    est[warp] = rows <= p.part_rows ? e : INFINITY;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int best = 31;
-    for (int w = 30; w >= 0; --w)
-      if (est[w] < est[best]) best = w;
-    chosen = best;
-  }
-  __syncthreads();
-  const int pick = chosen;
-  const int Cp = pick == 31 ? INT_MAX / 2 : (pick & 1) ? (3 << (pick >> 1)) >> 1 : 1 << (pick >> 1);
-  // ---- exclusive prefix sums of (units, partial rows, cut rows) over contiguous runs of sequences
-  const int per = cdiv(p.B, CP_THREADS);
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int v[3] = {0, 0, 0};
-  bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    const SeqShape s = seq_shape(p, b);
-    bad = bad || s.bad;
-    int nc, ct;
-    cut(s.nt, Cp, nc, ct);
-    v[0] += s.n ? nc * s.np * p.n_kv : 0;
-    v[1] += nc > 1 ? nc * s.n : 0;
-    v[2] += nc > 1 ? s.n : 0;
-  }
-  if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
-  int incl[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < N; ++i) {
     incl[i] = v[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl[i], o);
       if (lane >= o) incl[i] += y;
     }
-    if (lane == 31) warp_sum[i][warp] = incl[i];
+    if (lane == 31) buf[i][warp] = incl[i];
   }
   __syncthreads();
-  int at[3], total[3];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    int before = 0, all = 0;
-    for (int w = 0; w < CP_THREADS / 32; ++w) {
-      if (w < warp) before += warp_sum[i][w];
-      all += warp_sum[i][w];
+  for (int i = 0; i < N; ++i) {
+    const int w = buf[i][lane];
+    int y = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
     }
-    at[i] = before + incl[i] - v[i];
-    total[i] = all;
+    total[i] = __shfl_sync(0xffffffffu, y, 31);
+    v[i] = __shfl_sync(0xffffffffu, y - w, warp) + incl[i] - v[i];
   }
-  for (int b = b0; b < b1; ++b) {
-    const SeqShape s = seq_shape(p, b);
+}
+
+__global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ int4 shapes[CP_SEQS];  // (n, np, nt, tiles of the shortest item)
+  __shared__ int before[CP_SEQS];   // items per KV group that may be left whole, in the sequences before
+  __shared__ int unit0[CP_SEQS];
+  __shared__ float est[64];
+  __shared__ int sums[4][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  bool bad = false;
+  const int per = cdiv(p.B, CP_THREADS);                              // contiguous runs of sequences
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  const int tpt2 = 2 * p.tpt;
+  SeqShape mine = {0, 0, 0, 0, 0};                                    // the first of this thread's
+  if (b0 < b1) mine = seq_shape(p, b0, bad);
+  auto shape = [&](int b) { return b == b0 ? mine : seq_shape(p, b, bad); };
+  auto shape4 = [&](const SeqShape& s) { return make_int4(s.n, s.np, s.nt, (s.c + min(s.n, tpt2) + 127) >> 7); };
+  const bool table = p.B <= CP_SEQS;
+  if (table && b0 < b1) shapes[b0] = shape4(mine);
+  __syncthreads();
+  const int C_est = candidate(warp);
+  const float inv_C = __frcp_rn((float)C_est), n_kv = (float)p.n_kv, row_cost = kRowCost / 256.f * (float)p.r;
+  int rounds_whole = 0;
+  for (int f = 0; f < 2; ++f) {
+    float nw = 0.f, cw = 0.f, lw = 0.f, nu = 0.f, cu = 0.f, lu = 0.f;   // units, their time, the longest
+    float rows = 0.f;                                                    // exact below 2^24, beyond it too many
+    int share = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const int4 v = table ? shapes[b] : shape4(seq_shape(p, b, bad));
+      if (v.x == 0) continue;
+      // an item that shares its K and V with others of its sequence may be left whole
+      const int sharing = v.y > 1 ? v.y : 0, wp = f ? min(max(rounds_whole - before[b], 0), sharing) : 0;
+      share += sharing;
+      int nc, ct;
+      cut(v.z, C_est, inv_C, nc, ct);
+      const float nt = (float)v.z, lo = (float)v.w, step = __fdividef(nt - lo, (float)max(v.y - 1, 1));
+      if (wp > 0) {
+        const float items = (float)wp * n_kv;
+        nw += items;
+        cw += items * (nt - 0.5f * step * (float)(wp - 1) + kUnitCost);
+        lw = fmaxf(lw, nt + kUnitCost);
+      }
+      if (v.y > wp) {
+        const float mean = 0.5f * (nt - step * (float)wp + lo);
+        const float k = nc > 1 ? fmaxf(1.f, ceilf(__fdividef(mean, (float)ct) - 0.25f)) : 1.f;
+        const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, tpt2) : 0.f);
+        const float items = (float)(v.y - wp) * n_kv;
+        nu += items * k;
+        cu += items * (mean + k * over);
+        lu = fmaxf(lu, (float)min(ct, v.z) + over);
+        if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * tpt2);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (f) {
+        nw += __shfl_xor_sync(0xffffffffu, nw, o);
+        cw += __shfl_xor_sync(0xffffffffu, cw, o);
+        lw = fmaxf(lw, __shfl_xor_sync(0xffffffffu, lw, o));
+      }
+      nu += __shfl_xor_sync(0xffffffffu, nu, o);
+      cu += __shfl_xor_sync(0xffffffffu, cu, o);
+      lu = fmaxf(lu, __shfl_xor_sync(0xffffffffu, lu, o));
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    }
+    if (lane == 0) {
+      const float g = (float)p.grid, mw = nw > 0.f ? cw / nw : 0.f, mu = nu > 0.f ? cu / nu : 0.f;
+      const float e = lw <= 1.2f * mw && lu <= 1.2f * mu ? ceilf(nw / g) * mw + ceilf(nu / g) * mu
+                                                         : (cw + cu) / g + 0.5f * (nu > 0.f ? lu : lw);
+      est[32 * f + warp] =
+          rows <= (float)p.part_rows ? fmaxf(e, fmaxf(lw, lu)) + (rows > 0.f ? kMergeCost : 0.f) : INFINITY;
+    }
+    if (f) break;
+    // whole rounds of such items, one per CTA (larger batches than the table: none)
+    share = __reduce_add_sync(0xffffffffu, share);
+    rounds_whole = table ? (int)((int64_t)share * p.n_kv / p.grid * p.grid / p.n_kv) : 0;
+    if (rounds_whole == 0) {
+      if (lane == 0) est[32 + warp] = INFINITY;
+      break;
+    }
+    int at[1] = {b0 < b1 && mine.np > 1 ? mine.np : 0}, all[1];
+    block_scan<1>(at, all, sums);
+    if (b0 < b1) before[b0] = at[0];
+    __syncthreads();
+  }
+  __syncthreads();
+  // the least estimate, the larger C of equals (every warp finds it for itself)
+  float e = est[lane];
+  int pick = lane;
+  if (est[32 + lane] < e) { e = est[32 + lane]; pick = 32 + lane; }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float oe = __shfl_xor_sync(0xffffffffu, e, o);
+    const int op = __shfl_xor_sync(0xffffffffu, pick, o);
+    if (oe < e || (oe == e && op > pick)) { e = oe; pick = op; }
+  }
+  const int C = candidate(pick & 31), whole = pick >= 32 ? rounds_whole : 0;
+  const float inv = __frcp_rn((float)C);
+  // ---- the sequences' records; prefix sums of (units, partial rows, cut tokens)
+  auto record = [&](int b) {
+    const SeqShape s = shape(b);
     ChunkSeq r;
-    cut(s.nt, Cp, r.nc, r.ct);
-    r.unit0 = at[0];
+    cut(s.nt, C, inv, r.nc, r.ct);
     r.lo = s.lo; r.n = s.n; r.c = s.c; r.np = s.np;
-    r.part0 = at[1];
-    r.split0 = at[2];
+    r.wp = whole && s.np > 1 ? min(max(whole - before[b], 0), s.np) : 0;
+    r.cut_n = r.nc > 1 ? min(s.n, (s.np - r.wp) * tpt2) : 0;
+    return r;
+  };
+  int v[3] = {0, 0, 0}, total[3];
+  ChunkSeq mine_r;
+  for (int b = b0; b < b1; ++b) {
+    const ChunkSeq r = record(b);
+    if (b == b0) mine_r = r;
+    v[0] += (r.wp + r.nc * (r.np - r.wp)) * p.n_kv;
+    v[1] += r.nc * r.cut_n;
+    v[2] += r.cut_n;
+  }
+  if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
+  block_scan<3>(v, total, sums + 1);
+  for (int b = b0; b < b1; ++b) {
+    ChunkSeq r = b == b0 ? mine_r : record(b);
+    r.unit0 = v[0];
+    r.part0 = v[1];
+    r.split0 = v[2];
     if (in_extent(b, 1, p.B)) p.seq[b] = r;
-    at[0] += s.n ? r.nc * s.np * p.n_kv : 0;
-    at[1] += r.nc > 1 ? r.nc * s.n : 0;
-    at[2] += r.nc > 1 ? s.n : 0;
+    if (table) unit0[b] = v[0];
+    v[0] += (r.wp + r.nc * (r.np - r.wp)) * p.n_kv;
+    v[1] += r.nc * r.cut_n;
+    v[2] += r.cut_n;
   }
   if (tid == 0) {
     ChunkHead h;
@@ -219,6 +354,21 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
     h.n_split = total[2];
     h.pad = 0;
     *p.head = h;
+  }
+  // ---- the CTAs' first units, ready to use: found here in parallel, not each by its own CTA's chain of loads
+  __syncthreads();
+  for (int u = tid; u < p.grid; u += CP_THREADS) {
+    ChunkUnit d;
+    d.live = 0;
+    if (u < total[0]) {
+      int lo = 0, hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((table ? unit0[mid] : p.seq[mid].unit0) <= u) lo = mid; else hi = mid;
+      }
+      make_unit(p, p.seq[lo], lo, u, d);
+    }
+    if (in_extent(u, 1, p.grid)) p.first[u] = d;
   }
 }
 
@@ -249,24 +399,6 @@ enum : int {
   BAR_DRAIN = 19,
   BAR_KV_FULL = 20,  // [NS], then [NS] empty ones
 };
-
-// One unit, as the roles of a CTA see it.
-struct __align__(16) ChunkUnit {
-  int live;            // 0: no more units
-  int t0;              // first key tile
-  int n0, n1;          // rounds of groups 0 and 1
-  int lone;            // 1: one Q tile, key tiles alternate between the groups
-  int row0, row1;      // first packed row of each group's Q tile
-  int end;             // the sequence's end row
-  int pos_off;         // position = packed row + pos_off
-  int g;               // KV group
-  int kv_len;          // keys of the sequence
-  int clean;           // tiles from here on hold keys that some row of the unit does not see
-  int part;            // partial row = packed row + part; INT_MIN: store o
-  int b;
-  int pad0, pad1;
-};
-static_assert(sizeof(ChunkUnit) == 64, "unit record");
 
 // Element-wise: non-finite bf16 values of a 16-byte piece replaced by 0; returns whether there were any.
 __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
@@ -349,7 +481,6 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
   float2* ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < BAR_KV_FULL + 2 * NS; ++i)
       mbar_init(&bars[i], i >= BAR_U_EMPTY && i < BAR_U_EMPTY + 2 ? 9
@@ -368,47 +499,30 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(smem);
-  pdl_wait();   // the plan
+  pdl_wait();      // the plan
+  pdl_trigger();   // the merge may start: what it reads before its own wait is the plan's
 
   if (warp < 4) {
     regs_give<CA_REGS_ISSUE>();
     if (warp == 0) {  // ---------------------------------------------------- units and TMA (whole warp)
+      ChunkUnit d = p.first[blockIdx.x];
       const int n_units = p.head->n_units;
-      int u = blockIdx.x, hint = 0, serial = 0, qi = 0, e = 0;
-      bool ok = true;
+      const bool more = n_units > p.grid;   // units besides every CTA's first
+      int next = 0, hint = 0, serial = 0, qi = 0, e = 0;
+      bool ok = true, asked = false;
       const uint32_t q_bytes = (uint32_t)(HALVES * p.r * p.tpt * 128);
       while (ok) {
-        ChunkUnit d;
-        d.live = 0;
-        while (u < n_units) {       // the next unit that has keys
+        while (!d.live && more) {   // the next unit that has keys
+          if (!asked && lane == 0) next = atomicAdd(&p.head->counter, 1);
+          asked = false;
+          const int u = __shfl_sync(0xffffffffu, next, 0);
+          if (u >= n_units) break;
           hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
-          const ChunkSeq s = p.seq[hint];
-          const int x = u - s.unit0;
-          const int g = x % p.n_kv, y = x / p.n_kv;
-          const int chunk = y / s.np, pair = s.np - 1 - y % s.np;      // the longest items of a chunk first
-          const int first = pair * 2 * p.tpt;                           // token of the earlier Q tile
-          const int tail = s.n - first;                                 // tokens from there on
-          const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
-          const int t0 = chunk * s.ct, t1 = min(t0 + s.ct, nt0);
-          d.lone = tail <= p.tpt;
-          if (t0 < t1) {
-            d.live = 1;
-            d.t0 = t0;
-            d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
-            d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
-            d.row1 = s.lo + first;
-            d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
-            d.end = s.lo + s.n;
-            d.pos_off = s.c - s.lo;
-            d.g = g;
-            d.kv_len = s.c + s.n;
-            d.clean = (s.c + first + 1) / 128;
-            d.part = s.nc > 1 ? s.part0 + chunk * s.n - s.lo : INT_MIN;
-            d.b = hint;
-          }
-          if (lane == 0) u = atomicAdd(&p.head->counter, 1);
-          u = __shfl_sync(0xffffffffu, u, 0);
-          if (d.live) break;
+          make_unit(p, p.seq[hint], hint, u, d);
+        }
+        if (d.live && more) {       // the one after it is asked for now and looked at later
+          if (lane == 0) next = atomicAdd(&p.head->counter, 1);
+          asked = true;
         }
         // ---- hand the unit over
         const int us = serial & 1;
@@ -468,6 +582,7 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
+        d.live = 0;
       }
       // every copy issued has landed before the CTA leaves (at once, unless a wait ran out)
       if (lane == 0) {
@@ -790,63 +905,100 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
 }
 
 // ----------------------------------------------------------------------------------------- merge
-// o = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the chunks k that hold keys the token sees;
-// one warp per (token, head) of the cut sequences.
-template <int HD>
-__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+// o = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the chunks k that hold keys the token sees.
+// A warp takes a token of the cut sequences and HB of its heads at a time, KB chunks of each: their loads
+// are all in flight together (one head at a time, each waiting for its own, took 45 us for the 136 MB
+// of parts of 2048 tokens x 32 heads).
+template <int HD, int HB, int KB>
+__device__ __forceinline__ void combine_rows(const ChunkParams& p, int n_split, bool& waited) {
   constexpr int PER = HD / 32;
+  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
   const int lane = threadIdx.x & 31;
-  pdl_wait();
-  const int64_t total = (int64_t)p.head->n_split * p.n_q;
-  const int64_t step = (int64_t)gridDim.x * 8;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += step) {
-    const int x = (int)(w / p.n_q), h = (int)(w - (int64_t)x * p.n_q);
+  const int warps = gridDim.x * 8, groups = cdiv(p.n_q, HB);
+  const int64_t total = (int64_t)n_split * groups;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += warps) {
+    const int x = (int)(w / groups), h0 = (int)(w - (int64_t)x * groups) * HB;
+    const int hn = min(HB, p.n_q - h0);
     // sequences that were not cut hold no split rows, so the last one starting at or before x is it
     const int b = warp_search(p.B, x, [&](int i) { return p.seq[i].split0; });
     const ChunkSeq s = p.seq[b];
     const int i = x - s.split0;
     const int nk = min(s.nc, cdiv((s.c + i) / 128 + 1, s.ct));
-    const int64_t row = (int64_t)(s.part0 + i) * p.n_q + h, stride = (int64_t)s.n * p.n_q;
-    float M = -INFINITY;
-    for (int k = lane; k < nk; k += 32) M = fmaxf(M, p.part_ml[row + k * stride].x);
+    const int64_t stride = (int64_t)s.cut_n * p.n_q, row0 = (int64_t)(s.part0 + i) * p.n_q + h0;
+    if (!waited) pdl_wait();   // the parts
+    waited = true;
+    float M[HB], l[HB], acc[HB][PER];
+    float2 a[HB];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f, acc[PER];
+    for (int h = 0; h < HB; ++h)
+      a[h] = h < hn && lane < nk ? p.part_ml[row0 + h + lane * stride] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int h = 0; h < HB; ++h) M[h] = a[h].x;
+    for (int k = lane + 32; k < nk; k += 32)
+#pragma unroll
+      for (int h = 0; h < HB; ++h)
+        if (h < hn) M[h] = fmaxf(M[h], p.part_ml[row0 + h + k * stride].x);
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
+      if (M[h] == -INFINITY) M[h] = 0.f;
+      l[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[h][e] = 0.f;
+    }
     for (int k0 = 0; k0 < nk; k0 += 32) {
-      float2 a = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < nk) a = p.part_ml[row + (k0 + lane) * stride];
-      const float wl = ex2(a.x - mu);
-      l += wl * a.y;
+      float wl[HB];
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        if (k0 > 0) a[h] = h < hn && k0 + lane < nk ? p.part_ml[row0 + h + (k0 + lane) * stride] : make_float2(-INFINITY, 0.f);
+        wl[h] = ex2(a[h].x - M[h]);   // 0 past the last chunk
+        l[h] += wl[h] * a[h].y;
+      }
       const int kn = min(32, nk - k0);
-#pragma unroll 4
-      for (int k = 0; k < kn; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, wl, k);
-        const float* src = p.part_o + (row + (k0 + k) * stride) * HD + lane * PER;
-        if (PER == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] = fmaf(wk, v.x, acc[0]);
-          acc[1] = fmaf(wk, v.y, acc[1]);
-          acc[PER - 2] = fmaf(wk, v.z, acc[PER - 2]);
-          acc[PER - 1] = fmaf(wk, v.w, acc[PER - 1]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(wk, v.x, acc[0]);
-          acc[1] = fmaf(wk, v.y, acc[1]);
-        }
+      for (int k = 0; k < kn; k += KB) {
+        const float* src = p.part_o + (row0 + (k0 + k) * stride) * HD + lane * PER;
+        Vec v[KB][HB];
+#pragma unroll
+        for (int q = 0; q < KB; ++q)
+#pragma unroll
+          for (int h = 0; h < HB; ++h)
+            if (h < hn && k + q < kn) v[q][h] = *reinterpret_cast<const Vec*>(src + q * stride * HD + h * HD);
+#pragma unroll
+        for (int q = 0; q < KB; ++q)
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            const float wk = __shfl_sync(0xffffffffu, wl[h], (k + q) & 31);
+            if (h < hn && k + q < kn) {
+              const float* f = reinterpret_cast<const float*>(&v[q][h]);
+#pragma unroll
+              for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(wk, f[e], acc[h][e]);
+            }
+          }
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = 1.f / l;
-    const int64_t at = ((int64_t)(s.lo + i) * p.n_q + h) * HD + lane * PER;
-    if (!in_extent(at, PER, (int64_t)p.T * p.n_q * HD)) continue;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at);
-    dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (PER == 4) dst[1] = pack_bf16x2(acc[PER - 2] * inv, acc[PER - 1] * inv);
+    for (int h = 0; h < HB; ++h) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+      const float inv = 1.f / l[h];
+      const int64_t at = ((int64_t)(s.lo + i) * p.n_q + h0 + h) * HD + lane * PER;
+      if (h >= hn || !in_extent(at, PER, (int64_t)p.T * p.n_q * HD)) continue;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[h][2 * e] * inv, acc[h][2 * e + 1] * inv);
+    }
   }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(256, 4) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+  const int n_split = p.head->n_split;
+  bool waited = false;
+  // four heads per warp when that leaves every warp some, else one head and more of its chunks at a time
+  if ((int64_t)n_split * p.n_q >= (int64_t)4 * 8 * gridDim.x) combine_rows<HD, 4, 1>(p, n_split, waited);
+  else combine_rows<HD, 1, 4>(p, n_split, waited);
+  if (!waited) pdl_wait();   // every CTA of the merge outlives the attention: the next call may reuse the workspace
 }
 
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -881,13 +1033,14 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   p.part_rows = (int)part_rows_of(a.T, a.n_q, a.max_pos);
   char* ws = static_cast<char*>(a.ws);
   p.head = reinterpret_cast<ChunkHead*>(ws);
-  ws += 256;
+  p.first = reinterpret_cast<ChunkUnit*>(ws + 256);
+  ws += 256 + kMaxGrid * sizeof(ChunkUnit);
   p.seq = reinterpret_cast<ChunkSeq*>(ws);
   ws += round256((size_t)a.B * sizeof(ChunkSeq));
   p.part_o = reinterpret_cast<float*>(ws);
   ws += round256((size_t)p.part_rows * a.n_q * HD * 4);
   p.part_ml = reinterpret_cast<float2*>(ws);
-  p.grid = num_sms;
+  p.grid = std::min(num_sms, kMaxGrid);
   p.status = a.status;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -904,7 +1057,7 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   // the attention's set-up overlaps the plan, and the merge's launch the attention
   const bool pdl = pdl_enabled();
   set_pdl(true);
-  cudaError_t e = launch_k(chunk_attn_kernel<HD>, dim3(num_sms), dim3(CA_THREADS), CaSmem<HD>::TOTAL, st, p);
+  cudaError_t e = launch_k(chunk_attn_kernel<HD>, dim3(p.grid), dim3(CA_THREADS), CaSmem<HD>::TOTAL, st, p);
   if (e == cudaSuccess && p.part_rows > 0) {
     const int64_t warps = (a.T * a.n_q + 7) / 8;
     e = launch_k(chunk_combine_kernel<HD>, dim3((unsigned)std::min<int64_t>(warps, 8 * num_sms)), dim3(256), 0, st, p);
@@ -923,7 +1076,7 @@ bool chunk_attn_supported(int64_t B, int64_t T, int64_t n_q, int64_t n_kv) {
 
 size_t chunk_attn_ws_bytes(int64_t B, int64_t T, int64_t n_q, int64_t, int64_t hd, int64_t max_pos) {
   const size_t rows = (size_t)part_rows_of(T, n_q, max_pos) * n_q;
-  return 256 + round256((size_t)B * sizeof(ChunkSeq)) + round256(rows * hd * 4) + round256(rows * 8);
+  return 256 + kMaxGrid * sizeof(ChunkUnit) + round256((size_t)B * sizeof(ChunkSeq)) + round256(rows * hd * 4) + round256(rows * 8);
 }
 
 int launch_chunk_attn(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
