@@ -9,11 +9,12 @@
 //   argmax_i p_i / e_i of the last row.  Drafts without a distribution have q = 1 at d: accept while
 //   u < p(d), remainder p without d.  T <= 0: accept while d is the argmax, new token the argmax.
 //
-// HBM bound: phase 1 reads every judged row of z and y once and leaves (max, sum of exponentials)
-// of each 8192-logit part; phase 2 (a cluster of CTAs per sequence) merges the parts, finds the
-// first rejection and reads one row of z, y and e again for the race.  A part's sums are formed in a
-// fixed order and merged in a fixed order, and the race keeps (score, lowest id), so the result does
-// not depend on timing.
+// HBM bound.  Phase 1 (verify_stats_kernel) reads every judged row of z and y once: warps take the
+// 1024-logit parts of all rows in turn, a part's loads in flight together, and leave its (max, sum of
+// exponentials).  Phase 2 (verify_pick_kernel, a cluster of up to 8 CTAs per
+// sequence) merges the parts, finds the first rejection and reads that row of z, y and e for the race.
+// A part's sums are formed and merged in a fixed order, and the race keeps the largest score and of equals
+// the lowest id, so the result does not depend on timing.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -28,17 +29,19 @@ namespace llama {
 namespace {
 
 constexpr int VF_THREADS = 256;
-constexpr int VF_UNITS = 8;                               // float4 units per thread in a part
-constexpr int VF_PART = VF_THREADS * VF_UNITS * 4;        // logits per part
+constexpr int VF_WARPS = VF_THREADS / 32;
+constexpr int VF_UNITS = 8;                               // float4 units per lane in a part
+constexpr int VF_PART = 32 * VF_UNITS * 4;                // logits per part, one warp's
+constexpr int VF_RACE = 2;                                // float4 units of each row in flight per thread
+constexpr int VF_STATS_CTAS = 5, VF_PICK_CTAS = 4;        // per SM (registers)
+constexpr int VF_ROWS = 32;                               // rows whose merged statistics are kept
 constexpr int VF_CLUSTER = 8;
-using u64 = unsigned long long;
 
 struct VerifyParams {
   const float *z, *y;              // [T, ld], [T, ld_y]; y may be null
   int64_t ld, ld_y, ld_e;
   int T, V, B, parts, greedy;
-  float c_hi, c_lo;                // log2(e) / T as an unevaluated sum of two floats
-  float d_min;                     // (z - m) below this has no weight
+  float c;                         // log2(e) / T
   const int *cu, *tokens;
   const float *u, *e;              // [T], [B, ld_e]
   int *n_acc, *out;                // [B], [T]
@@ -52,13 +55,9 @@ __device__ __forceinline__ float vf_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// exp((z - m) / T) for z <= m; the exponent is formed to about 2^-24 relative before ex2 (2^-22).  A
-// masked logit (-inf) has weight 0; differences are cut off where the weight is below 2^-1000, so
-// that masks of the type's lowest value stay finite on the way.
-__device__ __forceinline__ float vf_exp(const VerifyParams& p, float z, float m) {
-  const float d = fmaxf(z - m, p.d_min);
-  return z == -INFINITY ? 0.f : vf_ex2(fmaf(d, p.c_hi, d * p.c_lo));
-}
+// exp((z - m) / T) for z <= m, m finite: two roundings in the exponent and ex2 (2^-22 relative).  A
+// masked logit (-inf) has weight 0, and no finite z or T gives a NaN on the way (c > 0).
+__device__ __forceinline__ float vf_exp(const VerifyParams& p, float z, float m) { return vf_ex2((z - m) * p.c); }
 
 __device__ __forceinline__ float4 vf_load4(const float* row, int i, int V, bool vec) {
   if (vec && i + 4 <= V) return __ldg(reinterpret_cast<const float4*>(row + i));
@@ -72,81 +71,109 @@ __device__ __forceinline__ float4 vf_load4(const float* row, int i, int V, bool 
 
 __device__ __forceinline__ bool vf_aligned(const float* row) { return (reinterpret_cast<uintptr_t>(row) & 15) == 0; }
 
-// one CTA per (row, part) of z (blockIdx.y = 0) and of y (blockIdx.y = 1)
-__global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ float red_m[VF_THREADS / 32], red_s[VF_THREADS / 32];
-  __shared__ int red_i[VF_THREADS / 32];
-  const int row = blockIdx.x / p.parts, part = blockIdx.x - row * p.parts;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool draft = blockIdx.y == 1;
-  const float* src = draft ? p.y + (int64_t)row * p.ld_y : p.z + (int64_t)row * p.ld;
-  const bool vec = vf_aligned(src);
-  const int i0 = part * VF_PART;
-  pdl_trigger();
-  // rows behind the last sequence hold nothing, and the last row of a sequence judges no draft
-  bool skip = row >= __ldg(p.cu + p.B);
-  if (draft)
-    for (int b = tid; b < p.B; b += VF_THREADS) skip = skip || __ldg(p.cu + b + 1) - 1 == row;
-  if (__syncthreads_or(skip)) return;
-  float4 w[VF_UNITS];
-#pragma unroll
-  for (int j = 0; j < VF_UNITS; ++j) w[j] = vf_load4(src, i0 + (j * VF_THREADS + tid) * 4, p.V, vec);
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < VF_UNITS; ++j) m = fmaxf(m, fmaxf(fmaxf(w[j].x, w[j].y), fmaxf(w[j].z, w[j].w)));
-  float mw = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
-  if (lane == 0) red_m[warp] = mw;
-  __syncthreads();
-  float mb = red_m[0];
-#pragma unroll
-  for (int k = 1; k < VF_THREADS / 32; ++k) mb = fmaxf(mb, red_m[k]);
-  float2* stat = (draft ? p.stat_y : p.stat_z) + (int64_t)row * p.parts + part;
-  if (p.greedy) {   // the lowest id that holds the maximum
-    int id = INT_MAX;
-#pragma unroll
-    for (int j = VF_UNITS - 1; j >= 0; --j) {
-      const int i = i0 + (j * VF_THREADS + tid) * 4;
-      if (w[j].w == mb && i + 3 < p.V) id = i + 3;
-      if (w[j].z == mb && i + 2 < p.V) id = i + 2;
-      if (w[j].y == mb && i + 1 < p.V) id = i + 1;
-      if (w[j].x == mb && i < p.V) id = i;
-    }
-    id = __reduce_min_sync(0xffffffffu, id);
-    if (lane == 0) red_i[warp] = id;
-    __syncthreads();
-    if (tid == 0) {
-      for (int k = 1; k < VF_THREADS / 32; ++k) id = min(id, red_i[k]);
-      *stat = make_float2(mb, __int_as_float(id));
-    }
-    return;
+// The last sequence b whose rows start at or before `row` (cu[0] = 0 <= row), by a whole warp.
+__device__ __forceinline__ int sequence_of(const VerifyParams& p, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < n && __ldg(p.cu + lo + at) <= row);
+    const int k = le ? 31 - __clz(le) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  const float mu = mb == -INFINITY ? 0.f : mb;
-  float s = 0.f;
+  return lo;
+}
+
+// Part u of the rows of z, then of y: the address of its row, null where there is nothing to do (rows
+// behind the last sequence; in y the last row of a sequence, which judges no draft).
+__device__ __forceinline__ const float* part_row(const VerifyParams& p, int u, int total, int rows_used, int& row,
+                                                 int& part) {
+  row = 0;
+  part = 0;
+  if (u >= total) return nullptr;
+  const int r = u / p.parts;
+  part = u - r * p.parts;
+  const bool draft = r >= p.T;
+  row = draft ? r - p.T : r;
+  if (row >= rows_used) return nullptr;
+  if (!draft) return p.z + (int64_t)row * p.ld;
+  return __ldg(p.cu + sequence_of(p, row) + 1) - 1 == row ? nullptr : p.y + (int64_t)row * p.ld_y;
+}
+
+__device__ __forceinline__ void load_part(const VerifyParams& p, const float* src, int part, float4 (&w)[VF_UNITS]) {
+  if (!src) return;
+  const bool vec = vf_aligned(src);
+  const int i0 = part * VF_PART + (threadIdx.x & 31) * 4;
 #pragma unroll
-  for (int j = 0; j < VF_UNITS; ++j)
-    s += (vf_exp(p, w[j].x, mu) + vf_exp(p, w[j].y, mu)) + (vf_exp(p, w[j].z, mu) + vf_exp(p, w[j].w, mu));
+  for (int j = 0; j < VF_UNITS; ++j) w[j] = vf_load4(src, i0 + j * 128, p.V, vec);
+}
+
+template <bool GREEDY>
+__global__ void __launch_bounds__(VF_THREADS, VF_STATS_CTAS) verify_stats_kernel(const __grid_constant__ VerifyParams p) {
+  const int lane = threadIdx.x & 31, nw = gridDim.x * VF_WARPS;
+  const int total = p.T * p.parts * (p.y ? 2 : 1);
+  pdl_trigger();
+  const int rows_used = min(p.T, __ldg(p.cu + p.B));
+  for (int u = blockIdx.x * VF_WARPS + (threadIdx.x >> 5); u < total; u += nw) {
+    int row, part;
+    const float* src = part_row(p, u, total, rows_used, row, part);
+    float4 w[VF_UNITS];
+    load_part(p, src, part, w);
+    if (src) {
+      float m = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) red_s[warp] = s;
-  __syncthreads();
-  if (tid == 0) {
-    for (int k = 1; k < VF_THREADS / 32; ++k) s += red_s[k];
-    *stat = make_float2(mb, s);
+      for (int j = 0; j < VF_UNITS; ++j) m = fmaxf(m, fmaxf(fmaxf(w[j].x, w[j].y), fmaxf(w[j].z, w[j].w)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float second;
+      if (GREEDY) {   // the lowest id that holds the maximum
+        int id = INT_MAX;
+#pragma unroll
+        for (int j = VF_UNITS - 1; j >= 0; --j) {
+          const int i = part * VF_PART + j * 128 + lane * 4;
+          if (w[j].w == m && i + 3 < p.V) id = i + 3;
+          if (w[j].z == m && i + 2 < p.V) id = i + 2;
+          if (w[j].y == m && i + 1 < p.V) id = i + 1;
+          if (w[j].x == m && i < p.V) id = i;
+        }
+        second = __int_as_float((int)__reduce_min_sync(0xffffffffu, id));
+      } else {
+        const float mu = m == -INFINITY ? 0.f : m;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < VF_UNITS; ++j)
+          s += (vf_exp(p, w[j].x, mu) + vf_exp(p, w[j].y, mu)) + (vf_exp(p, w[j].z, mu) + vf_exp(p, w[j].w, mu));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        second = s;
+      }
+      const int64_t at = (int64_t)row * p.parts + part;
+      if (lane == 0 && in_extent(at, 1, (int64_t)p.T * p.parts)) {
+        float2* stat = u / p.parts >= p.T ? p.stat_y : p.stat_z;
+        stat[at] = make_float2(m, second);
+      }
+    }
   }
 }
 
 // A row's (max, 1 / sum) from its parts, by one warp.
 __device__ __forceinline__ float2 merge_parts(const VerifyParams& p, const float2* stat) {
   const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-  for (int i = lane; i < p.parts; i += 32) m = fmaxf(m, stat[i].x);
+  float2 a[4];                     // the first 128 parts (131072 logits) in flight together
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[j] = lane + 32 * j < p.parts ? __ldcg(stat + lane + 32 * j) : make_float2(-INFINITY, 0.f);
+  float m = fmaxf(fmaxf(a[0].x, a[1].x), fmaxf(a[2].x, a[3].x));
+  for (int i = lane + 128; i < p.parts; i += 32) m = fmaxf(m, __ldcg(stat + i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float s = 0.f;
-  for (int i = lane; i < p.parts; i += 32)
-    if (stat[i].y > 0.f) s += stat[i].y * vf_exp(p, stat[i].x, m);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s += a[j].y * vf_exp(p, a[j].x, m);   // a masked part has sum 0
+  for (int i = lane + 128; i < p.parts; i += 32) {
+    const float2 b = __ldcg(stat + i);
+    s += b.y * vf_exp(p, b.x, m);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return make_float2(m, 1.f / s);
@@ -156,8 +183,10 @@ __device__ __forceinline__ int merge_argmax(const VerifyParams& p, const float2*
   const int lane = threadIdx.x & 31;
   float m = -INFINITY;
   int id = INT_MAX;
-  for (int i = lane; i < p.parts; i += 32)
-    if (stat[i].x > m) { m = stat[i].x; id = __float_as_int(stat[i].y); }
+  for (int i = lane; i < p.parts; i += 32) {
+    const float2 a = __ldcg(stat + i);
+    if (a.x > m) { m = a.x; id = __float_as_int(a.y); }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float om = __shfl_xor_sync(0xffffffffu, m, o);
@@ -167,31 +196,87 @@ __device__ __forceinline__ int merge_argmax(const VerifyParams& p, const float2*
   return id == INT_MAX ? 0 : id;
 }
 
-// (score, id) as one word: larger score first, then the lower id.  Scores are >= 0; NaN loses.
-__device__ __forceinline__ u64 race_key(float s, int i) {
-  return s >= 0.f ? ((u64)(__float_as_uint(s) + 1u) << 32) | (0xFFFFFFFFu - (uint32_t)i) : 0ull;
+// The better of two (score, id): the larger score, of equals the lower id.
+__device__ __forceinline__ void race_max(float& s, int& id, float os, int oid) {
+  if (os > s || (os == s && oid < id)) { s = os; id = oid; }
 }
 
-__global__ void __launch_bounds__(VF_THREADS) verify_pick_kernel(const __grid_constant__ VerifyParams p) {
+// What the race runs over: REST max(p - q, 0); NO_DRAFT p without the draft; ALL p.
+enum RaceKind : int { REST, NO_DRAFT, ALL };
+
+// This CTA's share of the vocabulary: (best score, its lowest id); scores of 0 do not count.
+template <int KIND>
+__device__ __forceinline__ void race(const VerifyParams& p, const float* z, const float* y, const float* e, int d,
+                                     float2 sz, float2 sy, int cr, int P, float& best, int& id) {
+  const bool vz = vf_aligned(z), vy = KIND == REST && vf_aligned(y), ve = vf_aligned(e);
+  const int units = (p.V + 3) >> 2, step = P * VF_THREADS;
+  best = 0.f;
+  id = INT_MAX;
+  for (int q0 = cr * VF_THREADS + (int)threadIdx.x; q0 < units; q0 += VF_RACE * step) {
+    float4 a[VF_RACE], c[VF_RACE], n[VF_RACE];
+#pragma unroll
+    for (int j = 0; j < VF_RACE; ++j) {   // past the end: -inf, which has no weight
+      const int i = (q0 + j * step) * 4;
+      a[j] = vf_load4(z, i, p.V, vz);
+      if (KIND == REST) c[j] = vf_load4(y, i, p.V, vy);
+      n[j] = vf_load4(e, i, p.V, ve);
+    }
+#pragma unroll
+    for (int j = 0; j < VF_RACE; ++j) {
+      const int i = (q0 + j * step) * 4;
+      const float za[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, ea[4] = {n[j].x, n[j].y, n[j].z, n[j].w};
+      float ya[4] = {0.f, 0.f, 0.f, 0.f};
+      if (KIND == REST) { ya[0] = c[j].x; ya[1] = c[j].y; ya[2] = c[j].z; ya[3] = c[j].w; }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float w = vf_exp(p, za[t], sz.x) * sz.y;
+        if (KIND == REST) w -= vf_exp(p, ya[t], sy.x) * sy.y;
+        if (KIND == NO_DRAFT && i + t == d) w = 0.f;
+        const float s = __fdividef(w, ea[t]);
+        if (w > 0.f && s > best) { best = s; id = i + t; }   // ids grow: an equal later one does not count
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(const __grid_constant__ VerifyParams p) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cl = cg::this_cluster();
   const int P = (int)cl.num_blocks(), cr = (int)cl.block_rank(), b = blockIdx.x / P;
-  __shared__ int stop_sh;
-  __shared__ float2 sz_sh, sy_sh;
-  __shared__ int top_sh;
-  __shared__ u64 best[2], wbest[2][VF_THREADS / 32];
+  __shared__ int stop_sh, top_sh, wid[VF_WARPS], cid;
+  __shared__ float2 sz_sh[VF_ROWS], sy_sh[VF_ROWS];
+  __shared__ float wbest[VF_WARPS], cbest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
+  // the caller's inputs may be read before the statistics are there
   const int lo = max(0, __ldg(p.cu + b)), hi = min(p.T, __ldg(p.cu + b + 1));
+  if (tid == 0) stop_sh = hi - 1;
+  __syncthreads();
+  int row = lo + warp, d = -1;
+  float zd = 0.f, yd = 0.f, u = 0.f;
+  auto inputs = [&]() {   // what row `row` judges its draft by
+    if (row >= hi - 1) return;   // the last row judges none
+    d = __ldg(p.tokens + row + 1);
+    if (p.greedy) return;
+    u = __ldg(p.u + row);
+    if (d < 0 || d >= p.V) return;
+    zd = __ldg(p.z + (int64_t)row * p.ld + d);
+    if (p.y) yd = __ldg(p.y + (int64_t)row * p.ld_y + d);
+  };
+  inputs();
+  pdl_wait();
   if (hi <= lo) {           // a sequence without rows (the whole cluster leaves)
     if (cr == 0 && tid == 0 && in_extent(b, 1, p.B)) p.n_acc[b] = 0;
     return;
   }
-  if (tid == 0) stop_sh = hi - 1;
-  __syncthreads();
   // ---- the first row whose draft is turned down (the last row if none is)
-  for (int row = lo + warp; row < hi - 1; row += VF_THREADS / 32) {
-    const int d = __ldg(p.tokens + row + 1);
+  for (; row < hi; row += VF_WARPS, inputs()) {
+    if (row == hi - 1) {   // its statistics, should it be the one
+      if (!p.greedy && row - lo < VF_ROWS) {
+        const float2 sz = merge_parts(p, p.stat_z + (int64_t)row * p.parts);
+        if (lane == 0) sz_sh[row - lo] = sz;
+      }
+      break;
+    }
     const bool real = d >= 0 && d < p.V;
     bool ok;
     if (p.greedy) {
@@ -201,10 +286,11 @@ __global__ void __launch_bounds__(VF_THREADS) verify_pick_kernel(const __grid_co
       float qd = 1.f, pd = 0.f;
       if (p.y) {
         const float2 sy = merge_parts(p, p.stat_y + (int64_t)row * p.parts);
-        if (real) qd = vf_exp(p, __ldg(p.y + (int64_t)row * p.ld_y + d), sy.x) * sy.y;
+        if (real) qd = vf_exp(p, yd, sy.x) * sy.y;
+        if (lane == 0 && row - lo < VF_ROWS) sy_sh[row - lo] = sy;
       }
-      if (real) pd = vf_exp(p, __ldg(p.z + (int64_t)row * p.ld + d), sz.x) * sz.y;
-      float u = __ldg(p.u + row);
+      if (lane == 0 && row - lo < VF_ROWS) sz_sh[row - lo] = sz;
+      if (real) pd = vf_exp(p, zd, sz.x) * sz.y;
       u = (u >= 0.f) ? fminf(u, 0.99999994f) : 0.f;
       ok = (double)u * (double)qd < (double)pd;   // the product is exact
     }
@@ -225,72 +311,54 @@ __global__ void __launch_bounds__(VF_THREADS) verify_pick_kernel(const __grid_co
     __syncthreads();
     token = top_sh;
   } else {
-    if (warp == 0) {
-      const float2 s = merge_parts(p, p.stat_z + (int64_t)stop * p.parts);
-      if (lane == 0) sz_sh = s;
+    const int kept = min(stop - lo, VF_ROWS - 1);
+    if (stop - lo >= VF_ROWS) {   // a long sequence: merged again, in the last place
+      __syncthreads();
+      if (warp == 0) {
+        const float2 s = merge_parts(p, p.stat_z + (int64_t)stop * p.parts);
+        if (lane == 0) sz_sh[kept] = s;
+      }
+      if (warp == 1 && p.y && rejected) {
+        const float2 s = merge_parts(p, p.stat_y + (int64_t)stop * p.parts);
+        if (lane == 0) sy_sh[kept] = s;
+      }
+      __syncthreads();
     }
-    if (warp == 1 && p.y && rejected) {
-      const float2 s = merge_parts(p, p.stat_y + (int64_t)stop * p.parts);
-      if (lane == 0) sy_sh = s;
-    }
-    __syncthreads();
-    // ---- the race over this CTA's share of the vocabulary: key[0] over the remainder
-    //      max(p - q, 0), key[1] over p (taken when nothing was rejected or nothing remains)
     const float* z = p.z + (int64_t)stop * p.ld;
-    const float* y = p.y && rejected ? p.y + (int64_t)stop * p.ld_y : nullptr;
     const float* e = p.e + (int64_t)b * p.ld_e;
-    const bool vz = vf_aligned(z), vy = y && vf_aligned(y), ve = vf_aligned(e);
-    const int d = rejected ? __ldg(p.tokens + stop + 1) : -1;
-    const float2 sz = sz_sh, sy = y ? sy_sh : make_float2(0.f, 0.f);
-    u64 k0 = 0ull, k1 = 0ull;
-    const int units = (p.V + 3) >> 2;
-    for (int q0 = cr * VF_THREADS + tid; q0 < units; q0 += P * VF_THREADS) {
-      const int i = q0 * 4;
-      const float4 a = vf_load4(z, i, p.V, vz), n = vf_load4(e, i, p.V, ve);
-      const float4 c = y ? vf_load4(y, i, p.V, vy) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float za[4] = {a.x, a.y, a.z, a.w}, ya[4] = {c.x, c.y, c.z, c.w}, ea[4] = {n.x, n.y, n.z, n.w};
+    const float2 sz = sz_sh[kept], sy = p.y && rejected ? sy_sh[kept] : sz;
+    const int judged = rejected ? __ldg(p.tokens + stop + 1) : -1;
+    // The race over the remainder; over p when nothing was rejected, or (the second turn) when no p
+    // exceeds its q.  Every CTA of the cluster sees the same result.
+    for (int turn = 0; turn < 2; ++turn) {
+      float best;
+      int id;
+      if (!rejected || turn) race<ALL>(p, z, nullptr, e, -1, sz, sz, cr, P, best, id);
+      else if (p.y) race<REST>(p, z, p.y + (int64_t)stop * p.ld_y, e, -1, sz, sy, cr, P, best, id);
+      else race<NO_DRAFT>(p, z, nullptr, e, judged, sz, sz, cr, P, best, id);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (i + t >= p.V) break;
-        const float pi = vf_exp(p, za[t], sz.x) * sz.y;
-        float w = pi;
-        if (y) w = fmaxf(pi - vf_exp(p, ya[t], sy.x) * sy.y, 0.f);
-        else if (i + t == d) w = 0.f;
-        const u64 a0 = race_key(__fdividef(w, ea[t]), i + t), a1 = race_key(__fdividef(pi, ea[t]), i + t);
-        if (a0 > k0 && w > 0.f) k0 = a0;
-        if (a1 > k1) k1 = a1;
+      for (int o = 16; o > 0; o >>= 1)
+        race_max(best, id, __shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, id, o));
+      if (lane == 0) { wbest[warp] = best; wid[warp] = id; }
+      __syncthreads();
+      if (tid == 0) {
+        for (int k = 1; k < VF_WARPS; ++k) race_max(best, id, wbest[k], wid[k]);
+        cbest = best;
+        cid = id;
       }
+      cl.sync();
+      best = 0.f;
+      id = INT_MAX;
+      for (int r = 0; r < P; ++r) race_max(best, id, *cl.map_shared_rank(&cbest, r), *cl.map_shared_rank(&cid, r));
+      cl.sync();   // no CTA leaves, or writes its result again, while another still reads it
+      token = id == INT_MAX ? 0 : id;
+      if (!rejected || id != INT_MAX) break;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const u64 o0 = __shfl_xor_sync(0xffffffffu, k0, o), o1 = __shfl_xor_sync(0xffffffffu, k1, o);
-      k0 = o0 > k0 ? o0 : k0;
-      k1 = o1 > k1 ? o1 : k1;
-    }
-    if (lane == 0) { wbest[0][warp] = k0; wbest[1][warp] = k1; }
-    __syncthreads();
-    if (tid < 2) {
-      u64 k = wbest[tid][0];
-      for (int i = 1; i < VF_THREADS / 32; ++i) k = wbest[tid][i] > k ? wbest[tid][i] : k;
-      best[tid] = k;
-    }
-    cl.sync();
-    if (cr == 0) {
-      k0 = k1 = 0ull;
-      for (int r = 0; r < P; ++r) {
-        const u64* o = cl.map_shared_rank(best, r);
-        k0 = o[0] > k0 ? o[0] : k0;
-        k1 = o[1] > k1 ? o[1] : k1;
-      }
-    }
-    cl.sync();   // the others' shared memory stays until the leader has read it
-    const u64 k = k0 ? k0 : k1;
-    token = k ? (int)(0xFFFFFFFFu - (uint32_t)k) : 0;
   }
   if (cr != 0) return;
   if (tid == 0 && in_extent(b, 1, p.B)) p.n_acc[b] = stop - lo;
-  for (int row = lo + tid; row < hi; row += VF_THREADS)
-    if (in_extent(row, 1, p.T)) p.out[row] = row < stop ? __ldg(p.tokens + row + 1) : row == stop ? token : -1;
+  for (int r = lo + tid; r < hi; r += VF_THREADS)
+    if (in_extent(r, 1, p.T)) p.out[r] = r < stop ? __ldg(p.tokens + r + 1) : r == stop ? token : -1;
 }
 
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -298,31 +366,38 @@ int64_t parts_of(int64_t V) { return (V + VF_PART - 1) / VF_PART; }
 
 }  // namespace
 
-bool verify_supported(int64_t T, int64_t V) { return T * parts_of(V) <= INT32_MAX; }   // one CTA per part
+// Parts are counted in 32 bits.
+bool verify_supported(int64_t T, int64_t V) { return 2 * T * parts_of(V) <= INT32_MAX / 2; }
 
 size_t verify_ws_bytes(int64_t T, int64_t V) { return 2 * round256((size_t)T * parts_of(V) * sizeof(float2)); }
 
-int launch_verify(const VerifyDesc& d, int, unsigned* status, cudaStream_t st) {
+int launch_verify(const VerifyDesc& d, int num_sms, unsigned* status, cudaStream_t st) {
   VerifyParams p;
   p.z = d.logits; p.y = d.temperature > 0.f ? d.draft_logits : nullptr;
   p.ld = d.ld; p.ld_y = d.draft_ld; p.ld_e = d.noise_ld;
   p.T = (int)d.T; p.V = (int)d.V; p.B = (int)d.B;
   p.parts = (int)parts_of(d.V);
   p.greedy = !(d.temperature > 0.f);
-  const double c = p.greedy ? 0.0 : 1.4426950408889634074 / (double)d.temperature;
-  p.c_hi = (float)c;
-  p.c_lo = (float)(c - (double)p.c_hi);
-  p.d_min = (float)std::max(-1000.0 / c, -(double)FLT_MAX);   // T = inf: c = 0, no cut
+  // kept a positive finite number for every T > 0, infinity included
+  p.c = p.greedy ? 1.f : (float)std::min(std::max(1.4426950408889634074 / (double)d.temperature, (double)FLT_MIN),
+                                         (double)FLT_MAX);
   p.cu = d.cu_new; p.tokens = d.tokens; p.u = d.u; p.e = d.noise;
   p.n_acc = d.n_accepted; p.out = d.out_tokens;
   p.stat_z = static_cast<float2*>(d.ws);
   p.stat_y = reinterpret_cast<float2*>(static_cast<char*>(d.ws) + round256((size_t)d.T * p.parts * sizeof(float2)));
   p.status = status;
-  if (d.T > 0) verify_stats_kernel<<<dim3((unsigned)(p.parts * d.T), p.y ? 2 : 1), VF_THREADS, 0, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (d.T > 0) {
+    const int64_t total = d.T * p.parts * (p.y ? 2 : 1);
+    const unsigned grid = (unsigned)std::min<int64_t>((total + VF_WARPS - 1) / VF_WARPS, VF_STATS_CTAS * num_sms);
+    if (p.greedy) verify_stats_kernel<true><<<grid, VF_THREADS, 0, st>>>(p);
+    else verify_stats_kernel<false><<<grid, VF_THREADS, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return -1;
+  }
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  const int P = p.greedy ? 1 : VF_CLUSTER;
+  // as many CTAs per sequence as are resident together, up to a cluster
+  int P = 1;
+  while (!p.greedy && P < VF_CLUSTER && 2 * P * d.B <= VF_PICK_CTAS * num_sms) P *= 2;
   cfg.gridDim = dim3((unsigned)(d.B * P));
   cfg.blockDim = dim3(VF_THREADS);
   cfg.stream = st;
