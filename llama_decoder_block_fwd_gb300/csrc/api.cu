@@ -183,15 +183,23 @@ int check_dims(const llama_dims* d, unsigned need) {
   return LLAMA_OK;
 }
 
-// theta_k = theta_base^(-2k/head_dim), split into two floats (hi = fl(theta_k)).
+// theta_k = theta_base^(-2k/head_dim), split into two floats (hi = fl(theta_k)).  64 calls of pow cost
+// the host about 3 us, so a thread keeps the table of the last (theta_base, head_dim).
 void rope_freqs(const llama_dims* d, RopeFreq* out) {
+  static thread_local RopeFreq table[kMaxRopePairs];
+  static thread_local double base = 0.0;
+  static thread_local int64_t hd = 0;
   const int half = (int)(d->head_dim / 2);
-  for (int k = 0; k < half; ++k) {
-    const double th = std::pow(d->theta_base, -2.0 * (double)k / (double)d->head_dim);
-    const float hi = (float)th;
-    out[k].hi = hi;
-    out[k].lo = (float)(th - (double)hi);
+  if (base != d->theta_base || hd != d->head_dim) {
+    for (int k = 0; k < half; ++k) {
+      const double th = std::pow(d->theta_base, -2.0 * (double)k / (double)d->head_dim);
+      table[k].hi = (float)th;
+      table[k].lo = (float)(th - (double)table[k].hi);
+    }
+    base = d->theta_base;
+    hd = d->head_dim;
   }
+  memcpy(out, table, sizeof(RopeFreq) * half);
 }
 
 int launch_status() {

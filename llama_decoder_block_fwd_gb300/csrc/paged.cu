@@ -166,10 +166,25 @@ __device__ __forceinline__ uint32_t rotate_pair(uint32_t w, float2 cs) {
 
 template <int TOK>
 __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ float2 cs[TOK][kMaxRopePairs];
+  __shared__ __align__(16) float2 cs[TOK][kMaxRopePairs];
   __shared__ int slot_sh[TOK];
-  const int half = p.hd / 2;
-  const int t0 = blockIdx.x * TOK;
+  const int half = p.hd / 2, vph = p.hd / 8;                 // vectors per head
+  const int total = p.q_vec + 2 * p.kv_vec;
+  const int t0 = blockIdx.x * TOK, n = min(TOK, p.T - t0);
+  // vector i of the tokens: which part of the row it belongs to, and where it comes from
+  auto load = [&](int i, uint4 (&w)[TOK]) {
+    if (i >= total) return;
+    const bool is_q = i < p.q_vec, is_v = i >= p.q_vec + p.kv_vec;
+    const int o = is_q ? i : i - p.q_vec - (is_v ? p.kv_vec : 0);
+    const uint16_t* src = is_q ? p.q : is_v ? p.v : p.k;
+    const int64_t stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+#pragma unroll
+    for (int tk = 0; tk < TOK; ++tk)
+      if (tk < n) w[tk] = *reinterpret_cast<const uint4*>(src + (t0 + tk) * stride + o * 8);
+  };
+  // the first vectors are on their way while the angles are formed
+  uint4 w[TOK];
+  load(threadIdx.x, w);
   if (threadIdx.x < TOK) {
     const int t = t0 + threadIdx.x;
     int slot = -1;
@@ -183,38 +198,37 @@ __global__ void __launch_bounds__(RA_THREADS) rope_append_kernel(const __grid_co
     }
     slot_sh[threadIdx.x] = slot;
   }
+  // neighbouring threads take the tokens of one pair: a warp then reads few different frequencies,
+  // which come from the kernel's parameters one address at a time
   for (int i = threadIdx.x; i < TOK * half; i += RA_THREADS) {
-    const int tk = i / half, j = i - tk * half;
-    if (t0 + tk < p.T) rope_sincos((float)__ldg(p.positions + t0 + tk), p.freq[j], cs[tk][j].y, cs[tk][j].x);
+    const int tk = i % TOK, j = i / TOK;
+    if (tk < n) rope_sincos((float)__ldg(p.positions + t0 + tk), p.freq[j], cs[tk][j].y, cs[tk][j].x);
   }
   __syncthreads();
-  const int vph = p.hd / 8;                                  // vectors per head
-  const int total = p.q_vec + 2 * p.kv_vec;
   for (int i = threadIdx.x; i < total; i += RA_THREADS) {
+    uint4 next[TOK];
+    load(i + RA_THREADS, next);
     const bool is_q = i < p.q_vec, is_v = i >= p.q_vec + p.kv_vec;
     const int o = is_q ? i : i - p.q_vec - (is_v ? p.kv_vec : 0);   // vector within its part
-    const uint16_t* src = is_q ? p.q : is_v ? p.v : p.k;
-    const int64_t stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
-    const int j = (o % vph) * 4;                             // first pair
-    uint4 w[TOK];
-#pragma unroll
-    for (int tk = 0; tk < TOK; ++tk)
-      if (slot_sh[tk] >= 0) w[tk] = *reinterpret_cast<const uint4*>(src + (t0 + tk) * stride + o * 8);
+    const int j = (o % vph) * 4;                                    // first pair
+    uint16_t* dst = is_q ? p.q_out : is_v ? p.v_pool : p.k_pool;
 #pragma unroll
     for (int tk = 0; tk < TOK; ++tk) {
       const int slot = slot_sh[tk];
       if (slot < 0) continue;
       if (!is_v) {
-        w[tk].x = rotate_pair(w[tk].x, cs[tk][j]);
-        w[tk].y = rotate_pair(w[tk].y, cs[tk][j + 1]);
-        w[tk].z = rotate_pair(w[tk].z, cs[tk][j + 2]);
-        w[tk].w = rotate_pair(w[tk].w, cs[tk][j + 3]);
+        const float4 c0 = *reinterpret_cast<const float4*>(&cs[tk][j]), c1 = *reinterpret_cast<const float4*>(&cs[tk][j + 2]);
+        w[tk].x = rotate_pair(w[tk].x, make_float2(c0.x, c0.y));
+        w[tk].y = rotate_pair(w[tk].y, make_float2(c0.z, c0.w));
+        w[tk].z = rotate_pair(w[tk].z, make_float2(c1.x, c1.y));
+        w[tk].w = rotate_pair(w[tk].w, make_float2(c1.z, c1.w));
       }
-      uint16_t* dst = is_q ? p.q_out : is_v ? p.v_pool : p.k_pool;
       const int64_t at = is_q ? (int64_t)(t0 + tk) * p.q_vec + o : (int64_t)slot * p.kv_vec + o;
       if (in_extent(at, 1, is_q ? (int64_t)p.T * p.q_vec : p.n_slots * p.kv_vec))
         *reinterpret_cast<uint4*>(dst + at * 8) = w[tk];
     }
+#pragma unroll
+    for (int tk = 0; tk < TOK; ++tk) w[tk] = next[tk];
   }
 }
 
