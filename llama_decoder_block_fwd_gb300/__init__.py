@@ -296,25 +296,37 @@ def _refuse(where, name, t, dtype, dev, shape):
     raise ValueError(f"{where}: {name} must be contiguous, got strides {t.stride()}")
 
 
-def _rows(where, name, t, dtype, dev, shape, inner):
-    """(address, row stride in elements) of a view whose rows are contiguous; `inner` are the strides a
-    row of more than one element has behind its first dimension."""
-    if t is None or t.__class__ is int:
-        raise ValueError(f"{where}: {name} must be a tensor")
-    st = t.stride()
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(where, name, t, dtype, dev, shape)
-    width = 1
-    for n, want, got in zip(reversed(shape[1:]), reversed(inner), reversed(st[1:])):
-        if n > 1 and want != got:
-            raise ValueError(f"{where}: the rows of {name} must be contiguous, got strides {st}")
-        width *= n
-    return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], width)
+def _heads(where, name, t, dtype, dev, rows, heads, hd):
+    """(address, row stride) of a [rows, heads, hd] view whose rows are contiguous; None, 0 for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, heads, hd):
+        _refuse(where, name, t, dtype, dev, (rows, heads, hd))
+    s0, s1, s2 = t.stride()
+    if (hd > 1 and s2 != 1) or (heads > 1 and s1 != hd):
+        raise ValueError(f"{where}: the rows of {name} must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), s0 if rows > 1 else heads * hd
 
 
-def _torch_dev():
+def _matrix(where, name, t, dtype, dev, rows, width):
+    """(address, row stride) of a [rows, >= width] view whose rows are contiguous; None, 0 for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != rows:
+        _refuse(where, name, t, dtype, dev, (rows, max(width, t.shape[-1])))
+    s0, s1 = t.stride()
+    if t.shape[1] < width or (width > 1 and s1 != 1):
+        raise ValueError(f"{where}: the rows of {name} must hold {width} contiguous entries, got shape {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return t.data_ptr(), s0 if rows > 1 else width
+
+
+def _here(stream):
+    """(library, torch, current device, stream address) for one call."""
     import torch
-    return torch, torch.cuda.current_device()
+    dev = torch.cuda.current_device()
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream)
+    return (_lib if _lib is not None else lib()), torch, dev, st
 
 
 def llama_paged_plan(n_cached, n_new, free_pages, n_pages, block_table, cu_new, positions, slots, pages_used,
@@ -322,14 +334,14 @@ def llama_paged_plan(n_cached, n_new, free_pages, n_pages, block_table, cu_new, 
     """Extend block_table [B, max_pages] by the pages the new tokens need (from free_pages, in order) and
     fill cu_new [B+1], positions [n_tokens], slots [n_tokens] and pages_used [1]; all int32."""
     w = "llama_paged_plan"
-    torch, dev = _torch_dev()
+    L, torch, dev, st = _here(stream)
     i32, B, T, P = torch.int32, n_cached.numel(), positions.numel(), block_table.shape[-1]
-    _check(lib().llama_paged_plan(
+    _check(L.llama_paged_plan(
         _arg(w, "n_cached", n_cached, i32, dev), _arg(w, "n_new", n_new, i32, dev, (B,)), B,
-        _arg(w, "free_pages", free_pages, i32, dev), free_pages.numel(), int(n_pages),
+        _arg(w, "free_pages", free_pages, i32, dev), free_pages.numel(), n_pages,
         _arg(w, "block_table", block_table, i32, dev, (B, P)), P, T, _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)),
         _arg(w, "positions", positions, i32, dev), _arg(w, "slots", slots, i32, dev, (T,)),
-        _arg(w, "pages_used", pages_used, i32, dev, (1,)), _s(stream)), w)
+        _arg(w, "pages_used", pages_used, i32, dev, (1,)), st), w)
 
 
 def llama_rope_append_paged(dims, q, k, v, positions, slots, q_out, k_pool, v_pool, stream=None):
@@ -337,25 +349,18 @@ def llama_rope_append_paged(dims, q, k, v, positions, slots, q_out, k_pool, v_po
     q [S, n_q, hd], k / v [S, n_kv, hd] may be views with a token stride; None, None for q, q_out (append
     only) or for k, v, k_pool, v_pool (rotate only)."""
     w = "llama_rope_append_paged"
-    torch, dev = _torch_dev()
+    L, torch, dev, st = _here(stream)
     d, i32, bf16 = _d(dims), torch.int32, torch.bfloat16
     S, hd, n_q, n_kv = d.S, d.head_dim, d.n_q, d.n_kv
-    qa = ka = va = None
-    qs = ks = vs = n_pages = 0
-    if q is not None:
-        qa, qs = _rows(w, "q", q, bf16, dev, (S, n_q, hd), (hd, 1))
-    if k is not None:
-        ka, ks = _rows(w, "k", k, bf16, dev, (S, n_kv, hd), (hd, 1))
-    if v is not None:
-        va, vs = _rows(w, "v", v, bf16, dev, (S, n_kv, hd), (hd, 1))
-    pool = None
-    if k_pool is not None:
-        n_pages = k_pool.shape[0]
-        pool = (n_pages, 128, n_kv, hd)
-    _check(lib().llama_rope_append_paged(
+    qa, qs = _heads(w, "q", q, bf16, dev, S, n_q, hd)
+    ka, ks = _heads(w, "k", k, bf16, dev, S, n_kv, hd)
+    va, vs = _heads(w, "v", v, bf16, dev, S, n_kv, hd)
+    n_pages = 0 if k_pool is None else k_pool.shape[0]
+    pool = (n_pages, 128, n_kv, hd)
+    _check(L.llama_rope_append_paged(
         ctypes.byref(d), qa, qs, ka, ks, va, vs, _arg(w, "positions", positions, i32, dev, (S,)),
         _arg(w, "slots", slots, i32, dev, (S,)), _arg(w, "q_out", q_out, bf16, dev, (S, n_q, hd)),
-        _arg(w, "k_pool", k_pool, bf16, dev, pool), _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, _s(stream)), w)
+        _arg(w, "k_pool", k_pool, bf16, dev, pool), _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, st), w)
 
 
 def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new, n_cached, max_pos, o, ws,
@@ -363,16 +368,16 @@ def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new
     """Packed new tokens q [S, n_q, hd] over k_pool / v_pool [n_pages, 128, n_kv, hd] (one layer): sequence b
     owns rows cu_new[b] .. cu_new[b+1]-1, at positions n_cached[b] onward; o [S, n_q, hd]."""
     w = "llama_gqa_attention_chunk_paged"
-    torch, dev = _torch_dev()
+    L, torch, dev, st = _here(stream)
     d, i32, bf16 = _d(dims), torch.int32, torch.bfloat16
     B, hd = d.B, d.head_dim
     rows, n_pages, P = (d.S, d.n_q, hd), k_pool.shape[0], block_table.shape[-1]
     pool = (n_pages, 128, d.n_kv, hd)
-    _check(lib().llama_gqa_attention_chunk_paged(
+    _check(L.llama_gqa_attention_chunk_paged(
         ctypes.byref(d), _arg(w, "q", q, bf16, dev, rows), _arg(w, "k_pool", k_pool, bf16, dev, pool),
         _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, _arg(w, "block_table", block_table, i32, dev, (B, P)), P,
-        _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), _arg(w, "n_cached", n_cached, i32, dev, (B,)), int(max_pos),
-        _arg(w, "o", o, bf16, dev, rows), _p(ws), _nbytes(ws), _s(stream)), w)
+        _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), _arg(w, "n_cached", n_cached, i32, dev, (B,)), max_pos,
+        _arg(w, "o", o, bf16, dev, rows), _p(ws), _nbytes(ws), st), w)
 
 
 def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, noise, n_accepted, out_tokens, ws,
@@ -381,24 +386,18 @@ def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, no
     None), tokens int32 [n_tokens], u fp32 [n_tokens], noise fp32 [B, ld] exponential draws; fills
     n_accepted int32 [B] and out_tokens int32 [n_tokens]."""
     w = "llama_verify_drafts"
-    torch, dev = _torch_dev()
+    L, torch, dev, st = _here(stream)
     i32, f32 = torch.int32, torch.float32
     T, B = tokens.numel(), n_accepted.numel()
     V = logits.shape[1] if vocab is None else int(vocab)
-
-    def rows(name, t, n):
-        if t is None:
-            return None, 0
-        if t.shape[-1] < V:
-            raise ValueError(f"{w}: the rows of {name} must hold {V} entries, got {tuple(t.shape)}")
-        return _rows(w, name, t, f32, dev, (n, t.shape[-1]), (1,))
-
-    (z, ldz), (y, ldy), (e, lde) = rows("logits", logits, T), rows("draft_logits", draft_logits, T), rows("noise", noise, B)
-    _check(lib().llama_verify_drafts(
-        z, T, V, ldz, y, ldy, float(temperature), _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), B,
+    z, ldz = _matrix(w, "logits", logits, f32, dev, T, V)
+    y, ldy = _matrix(w, "draft_logits", draft_logits, f32, dev, T, V)
+    e, lde = _matrix(w, "noise", noise, f32, dev, B, V)
+    _check(L.llama_verify_drafts(
+        z, T, V, ldz, y, ldy, temperature, _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), B,
         _arg(w, "tokens", tokens, i32, dev), _arg(w, "u", u, f32, dev, (T,)), e, lde,
         _arg(w, "n_accepted", n_accepted, i32, dev), _arg(w, "out_tokens", out_tokens, i32, dev, (T,)), _p(ws), _nbytes(ws),
-        _s(stream)), w)
+        st), w)
 
 
 def llama_workspace_bytes(op, dims, dtype, n_layers=0, vocab=0, kv_capacity=0) -> int:

@@ -124,10 +124,13 @@ def test_binding_refuses_what_the_library_would_misread():
         def is_contiguous(self):
             return self._st == tuple(torch.empty(self.shape, device="meta").stride())
 
+        def dim(self):
+            return len(self.shape)
+
         def data_ptr(self):
             return 0x1000
 
-    from llama_decoder_block_fwd_gb300 import _arg, _rows
+    from llama_decoder_block_fwd_gb300 import _arg, _heads, _matrix
     bf, f32 = torch.bfloat16, torch.float32
     assert _arg("f", "x", Fake((4, 3), f32, (3, 1)), f32, 0, (4, 3)) == 0x1000
     assert _arg("f", "x", None, f32, 0) is None and _arg("f", "x", 0x20, f32, 0) == 0x20
@@ -136,15 +139,21 @@ def test_binding_refuses_what_the_library_would_misread():
                       (Fake((4, 3), f32, (3, 1), -1), "CUDA tensor")):
         with pytest.raises(ValueError, match=what):
             _arg("f", "x", bad, f32, 0, (4, 3))
-    view = lambda *a, **k: _rows("f", "q", Fake(*a, **k), bf, 0, (4, 2, 64), (64, 1))
+    view = lambda *a, **k: _heads("f", "q", Fake(*a, **k), bf, 0, 4, 2, 64)
+    assert _heads("f", "q", None, bf, 0, 4, 2, 64) == (None, 0)
     assert view((4, 2, 64), bf, (512, 64, 1)) == (0x1000, 512)
-    assert _rows("f", "q", Fake((1, 2, 64), bf, (0, 64, 1)), bf, 0, (1, 2, 64), (64, 1)) == (0x1000, 128)
-    assert _rows("f", "q", Fake((4, 1, 64), bf, (80, 5, 1)), bf, 0, (4, 1, 64), (64, 1)) == (0x1000, 80)
+    assert _heads("f", "q", Fake((1, 2, 64), bf, (0, 64, 1)), bf, 0, 1, 2, 64) == (0x1000, 128)
+    assert _heads("f", "q", Fake((4, 1, 64), bf, (80, 5, 1)), bf, 0, 4, 1, 64) == (0x1000, 80)
     for bad in (((4, 2, 64), torch.float16, (512, 64, 1)), ((4, 2, 64), bf, (512, 32, 1)), ((4, 2, 64), bf, (512, 64, 2)),
                 ((4, 3, 64), bf, (512, 64, 1))):
         with pytest.raises(ValueError):
             view(*bad)
     with pytest.raises(ValueError):
         view((4, 2, 64), bf, (512, 64, 1), device=1)
-    with pytest.raises(ValueError, match="tensor"):
-        _rows("f", "q", 0x1000, bf, 0, (4, 2, 64), (64, 1))
+    mat = lambda *a, **k: _matrix("f", "z", Fake(*a, **k), f32, 0, 4, 10)
+    assert mat((4, 12), f32, (16, 1)) == (0x1000, 16)
+    assert _matrix("f", "z", Fake((1, 12), f32, (0, 1)), f32, 0, 1, 10) == (0x1000, 10)
+    for bad in (((4, 9), f32, (9, 1)), ((4, 12), f32, (16, 2)), ((3, 12), f32, (12, 1)), ((4, 12), bf, (12, 1)),
+                ((48,), f32, (1,))):
+        with pytest.raises(ValueError):
+            mat(*bad)
