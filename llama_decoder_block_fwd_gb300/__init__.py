@@ -303,7 +303,7 @@ def _heads(where, name, t, dtype, dev, rows, heads, hd):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, heads, hd):
         _refuse(where, name, t, dtype, dev, (rows, heads, hd))
     s0, s1, s2 = t.stride()
-    if (hd > 1 and s2 != 1) or (heads > 1 and s1 != hd):
+    if rows and ((hd > 1 and s2 != 1) or (heads > 1 and s1 != hd)):
         raise ValueError(f"{where}: the rows of {name} must be contiguous, got strides {t.stride()}")
     return t.data_ptr(), s0 if rows > 1 else heads * hd
 
@@ -315,7 +315,7 @@ def _matrix(where, name, t, dtype, dev, rows, width):
     if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2 or t.shape[0] != rows:
         _refuse(where, name, t, dtype, dev, (rows, max(width, t.shape[-1])))
     s0, s1 = t.stride()
-    if t.shape[1] < width or (width > 1 and s1 != 1):
+    if t.shape[1] < width or (rows and width > 1 and s1 != 1):
         raise ValueError(f"{where}: the rows of {name} must hold {width} contiguous entries, got shape {tuple(t.shape)} "
                          f"with strides {t.stride()}")
     return t.data_ptr(), s0 if rows > 1 else width

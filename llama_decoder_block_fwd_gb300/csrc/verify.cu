@@ -229,8 +229,9 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
       if (KIND == REST) { ya[0] = c[j].x; ya[1] = c[j].y; ya[2] = c[j].z; ya[3] = c[j].w; }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        float w = vf_exp(p, za[t], sz.x) * sz.y;
-        if (KIND == REST) w -= vf_exp(p, ya[t], sy.x) * sy.y;
+        // both products rounded: fused into the difference, one of them would leave its rounding where p = q
+        float w = __fmul_rn(vf_exp(p, za[t], sz.x), sz.y);
+        if (KIND == REST) w = __fsub_rn(w, __fmul_rn(vf_exp(p, ya[t], sy.x), sy.y));
         if (KIND == NO_DRAFT && i + t == d) w = 0.f;
         const float s = __fdividef(w, ea[t]);
         if (w > 0.f && s > best) { best = s; id = i + t; }   // ids grow: an equal later one does not count

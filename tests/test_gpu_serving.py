@@ -450,6 +450,57 @@ def test_verify_masked_logits_and_equal_models():
     assert (n_acc == 2).all() and (out.reshape(-1, 3)[:, 2] == 0).all()
 
 
+def test_verify_long_sequences_and_many():
+    """More rows than the statistics that are kept on the chip, and more sequences than CTAs per cluster."""
+    for new, V in (([70, 1, 33, 34, 40], 3000), ([2] * 700, 60)):
+        z, y, tokens, u, noise = _verify_inputs(new, V, seed=8, off=0.02)
+        for d in (y, None):
+            got = _verify(z, d, 1.0, new, tokens, u, noise)
+            assert _status() == 0
+            _check_verify(got, z, d, 1.0, new, tokens, u, noise)
+    new, tokens = [70, 1, 33, 34, 40], np.full(178, 7, np.int32)
+    z, y, _, u, noise = _verify_inputs(new, 3000, seed=8)
+    z[:, 7], y[:, 7] = 60.0, 60.0                           # no doubt: every draft stands, however many
+    n_acc, out = _verify(z, y, 1.0, new, tokens, u, noise)
+    assert n_acc.tolist() == [n - 1 for n in new] and (out == 7).all()
+    z[50, 9], y[50, 9] = 200.0, 0.0                         # the 51st row wants another token
+    n_acc, out = _verify(z, y, 1.0, new, tokens, u, noise)
+    assert n_acc.tolist() == [50, 0, 32, 33, 39] and out[50] == 9 and (out[51:70] == -1).all() and (out[70:] == 7).all()
+
+
+def test_verify_extreme_temperatures():
+    V, new = 500, [3] * 12
+    z, y, tokens, u, noise = _verify_inputs(new, V, seed=12)
+    z[:, ::3] = -np.inf
+    flat = lambda a: np.where(np.isfinite(a), 0.0, -np.inf).astype(np.float32)
+    for d in (y, None):
+        got = _verify(z, d, float("inf"), new, tokens, u, noise)          # every token that is left alike
+        assert _status() == 0
+        _check_verify(got, flat(z), None if d is None else flat(d), 1.0, new, tokens, u, noise)
+        for T in (1e-30, 1e-38, 1e-42):                                   # the argmax
+            got = _verify(z, d, T, new, tokens, u, noise)
+            assert _status() == 0
+            _check_verify(got, z, d, T, new, tokens, u, noise)
+
+
+def test_verify_draft_that_neither_model_allows():
+    """Equal models, a draft of weight 0 in both: turned down with nothing in the remainder, so the new token is
+    drawn from p."""
+    V, new = 900, [2, 3]
+    z, y, tokens, u, noise = _verify_inputs(new, V, seed=13, off=0.0)
+    tokens[1] = tokens[3] = 40
+    z[:, 40] = y[:, 40] = -np.inf
+    got = _verify(z, y, 1.0, new, tokens, u, noise)
+    assert _status() == 0 and got[0].tolist() == [0, 0] and 0 <= got[1][0] < V and got[1][0] != 40
+    _check_verify(got, z, y, 1.0, new, tokens, u, noise)
+
+
+def test_verify_without_rows():
+    n_acc, out = _verify(np.zeros((0, 5), np.float32), None, 1.0, [0, 0, 0], np.zeros(0, np.int32), np.zeros(0, np.float32),
+                         np.ones((3, 5), np.float32))
+    assert _status() == 0 and n_acc.tolist() == [0, 0, 0]
+
+
 def test_verify_rejects_drafts_outside_the_vocabulary():
     V, new = 300, [3, 3]
     z, y, tokens, u, noise = _verify_inputs(new, V, seed=9)
