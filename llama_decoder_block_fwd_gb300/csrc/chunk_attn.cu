@@ -887,7 +887,8 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
       if (merge) mbar_arrive(&o_free[1]);
       if (live && inside) {
         if (store_part) p.part_ml[at] = make_float2(m_ref, l);
-        if (*dirty == serial)
+        // (a later serial: group 1 met such values in its next unit already; then this looks without need)
+        if (*dirty >= serial)
           add_nonfinite<HD>(p, d.b, d.g, max(d.clean, d.t0) * 128, min(qpos, (d.t0 + (lone ? n_tiles : n)) * 128 - 1), at,
                             store_part);
       }

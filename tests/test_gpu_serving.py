@@ -322,6 +322,48 @@ def test_chunk_attention_unseen_values_do_not_reach_a_query(cached, new, bad, hd
     b.kp = kp
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_chunk_attention_unseen_values_in_every_unit(hd):
+    """Units follow each other on an SM, each with a value that is not finite in its last tiles."""
+    import torch
+    rng = np.random.default_rng(hd)
+    new = [int(n) for n in rng.integers(129, 256, 250)]
+    b = Batch([0] * len(new), new, 8, 8, hd, seed=4)
+    clean = b.run()
+    bad = torch.zeros(b.q.shape, dtype=torch.bool)
+    for i, n in enumerate(new):
+        at = int(rng.integers(0, n))
+        b.vp[int(b.table[i, at // 128]), at % 128, :, i % hd] = float("inf")
+        bad[b.cu[i] + at:b.cu[i + 1], :, i % hd] = True
+    got = b.run()
+    assert _status() == 0
+    bad = bad.cuda()
+    assert torch.equal(got[~bad], clean[~bad]) and bool((got[bad] == float("inf")).all())
+
+
+@pytest.mark.parametrize("B,seed", [(1500, 0), (2600, 1)])
+def test_chunk_attention_many_sequences(B, seed):
+    """More sequences than the shapes that are kept on the chip, most of them without new tokens or short."""
+    rng = np.random.default_rng(seed)
+    cached = [int(c) for c in rng.integers(0, 200, B)]
+    new = [int(n) for n in rng.integers(0, 4, B)]
+    cached[B // 2], new[B // 2], new[-1] = 3000, 90, 5
+    b = Batch(cached, new, 4, 2, 64, seed=seed)
+    o = b.run()
+    assert _status() == 0
+    b.check(o, every=7)
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd", [(100, 1, 64), (128, 1, 128), (42, 2, 128), (5, 5, 64)])
+def test_chunk_attention_head_layouts_over_many_units(n_q, n_kv, hd):
+    rng = np.random.default_rng(n_q)
+    cached, new = [int(c) for c in rng.integers(0, 1500, 24)], [int(n) for n in rng.integers(0, 60, 24)]
+    b = Batch(cached, new, n_q, n_kv, hd, seed=n_q)
+    o = b.run()
+    assert _status() == 0
+    b.check(o, every=19)
+
+
 def test_chunk_attention_shares_pages_between_sequences():
     """Two sequences over one prefix: the first pages of both are the same pages."""
     b = Batch([384, 384], [5, 70], 8, 2, 128, seed=11)
