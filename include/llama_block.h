@@ -294,7 +294,7 @@ int llama_gqa_attention_decode_paged(const llama_dims* dims, const void* q, cons
  *                    rows from cu_new[B] on
  *   pages_used [1]   out: pages needed from the free list
  * All int32 device arrays, 4-byte aligned; none may overlap another.  Needs B <= 8192, n_pages <=
- * 2^24 - 1, max_pages <= 2^17 (else LLAMA_ERR_UNSUPPORTED).  LLAMA_ERR_INVALID_ARG for negative
+ * 2^24 - 1, max_pages <= 2^17, n_tokens < 2^30 (else LLAMA_ERR_UNSUPPORTED).  LLAMA_ERR_INVALID_ARG for negative
  * counts, n_pages < 1, max_pages < 1 or NULL arrays.  Found on the device, and latched as
  * LLAMA_ERR_INVALID_ARG in the device status word: a negative length or n_cached + n_new > 128 *
  * max_pages (the sequence then brings no tokens), more new tokens than n_tokens (cu_new stops there),
@@ -361,7 +361,7 @@ int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const
  *   out_tokens [n_tokens] int32: the accepted drafts from the sequence's first row on, then the new
  *   token, then -1; rows from cu_new[B] on are left as they were
  *   ws: llama_workspace_bytes(LLAMA_OP_VERIFY_DRAFTS, dims with S = n_tokens, ..., vocab) bytes
- * Equal scores go to the lower id.  Probabilities are formed in fp32.  A draft outside [0, vocab) is
+ * The outputs may not overlap the inputs.  Equal scores go to the lower id.  Probabilities are formed in fp32.  A draft outside [0, vocab) is
  * rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.                           */
 int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, int64_t ld,
                         const float* draft_logits, int64_t draft_ld, float temperature,

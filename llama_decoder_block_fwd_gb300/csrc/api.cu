@@ -183,6 +183,14 @@ int check_dims(const llama_dims* d, unsigned need) {
   return LLAMA_OK;
 }
 
+// The same for packed rows: B counts sequences and S the rows of all of them, so their product bounds nothing.
+int check_packed(const llama_dims* d, unsigned need) {
+  if (!d || d->B < 0) return LLAMA_ERR_INVALID_ARG;
+  llama_dims one = *d;
+  one.B = 1;
+  return check_dims(&one, need);
+}
+
 // theta_k = theta_base^(-2k/head_dim), split into two floats (hi = fl(theta_k)).  64 calls of pow cost
 // the host about 3 us, so a thread keeps the table of the last (theta_base, head_dim).
 void rope_freqs(const llama_dims* d, RopeFreq* out) {
@@ -1173,7 +1181,7 @@ int llama_paged_plan(const int32_t* n_cached, const int32_t* n_new, int64_t B, c
                      int32_t* cu_new, int32_t* positions, int32_t* slots, int32_t* pages_used, void* stream) {
   if (B < 0 || n_free < 0 || n_pages < 1 || max_pages < 1 || n_tokens < 0) return LLAMA_ERR_INVALID_ARG;
   if (B > kPlanMaxSeqs || n_pages > INT32_MAX / 128 || max_pages > kMaxPos / 128 || n_free > INT32_MAX ||
-      n_tokens > INT32_MAX - 1)
+      n_tokens > INT32_MAX / 2)
     return LLAMA_ERR_UNSUPPORTED;
   if (!cu_new || !pages_used || (n_tokens > 0 && (!positions || !slots)) || (n_free > 0 && !free_pages) ||
       (B > 0 && (!n_cached || !n_new || !block_table)))
@@ -1195,7 +1203,7 @@ int llama_rope_append_paged(const llama_dims* d, const void* q, int64_t q_stride
                             const void* v, int64_t v_stride, const int32_t* positions, const int32_t* slots,
                             void* q_out, void* k_pool, void* v_pool, int64_t n_pages, void* stream) {
   int rc;
-  if ((rc = check_dims(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if ((rc = check_packed(d, NEED_HEADS)) != LLAMA_OK) return rc;
   if (d->head_dim % 8 != 0 || d->S > INT32_MAX - 8 || d->n_q > 4096 || d->n_kv > 4096) return LLAMA_ERR_UNSUPPORTED;
   if (!k != !v || !k != !k_pool || !k != !v_pool || !q != !q_out) return LLAMA_ERR_INVALID_ARG;
   if ((q && q_stride < d->n_q * d->head_dim) || (k && (k_stride < d->n_kv * d->head_dim || v_stride < d->n_kv * d->head_dim)))
@@ -1227,7 +1235,7 @@ int llama_gqa_attention_chunk_paged(const llama_dims* d, const void* q, const vo
                                     const int32_t* cu_new, const int32_t* n_cached, int64_t max_pos, void* o, void* ws,
                                     size_t ws_bytes, void* stream) {
   int rc;
-  if ((rc = check_dims(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if ((rc = check_packed(d, NEED_HEADS)) != LLAMA_OK) return rc;
   if (n_pages < 1 || max_pages < 1 || max_pos < 0 || max_pos + 1 > max_pages * 128 || max_pos + 1 > kMaxPos)
     return LLAMA_ERR_INVALID_ARG;
   if (n_pages > INT32_MAX / 128 || max_pages > INT32_MAX) return LLAMA_ERR_UNSUPPORTED;

@@ -91,6 +91,15 @@ def test_verify_refuses(kw, want):
     assert _verify(**kw) == want
 
 
+def test_rows_times_sequences_are_no_limit():
+    """B counts sequences and S packed rows: a large batch of many rows is refused for nothing but its arguments."""
+    big = _dims(B=8192, S=1 << 20)
+    assert _chunk(dims=big, ws=None) == WORKSPACE and _append(dims=big, slots=None) == INVALID
+    assert L.llama_workspace_bytes(L.OP_GQA_ATTENTION_CHUNK_PAGED, big, L.BF16, kv_capacity=500) > 0
+    assert _chunk(dims=_dims(B=-1)) == INVALID and _append(dims=_dims(B=-1)) == INVALID
+    assert _plan(n_tokens=1 << 30) == UNSUPPORTED
+
+
 def test_workspace_sizes():
     d = _dims()
     small = L.llama_workspace_bytes(L.OP_GQA_ATTENTION_CHUNK_PAGED, d, L.BF16, kv_capacity=500)
@@ -153,6 +162,8 @@ def test_binding_refuses_what_the_library_would_misread():
     mat = lambda *a, **k: _matrix("f", "z", Fake(*a, **k), f32, 0, 4, 10)
     assert mat((4, 12), f32, (16, 1)) == (0x1000, 16)
     assert _matrix("f", "z", Fake((1, 12), f32, (0, 1)), f32, 0, 1, 10) == (0x1000, 10)
+    assert _matrix("f", "z", Fake((0, 12), f32, (0, 0)), f32, 0, 0, 10) == (0x1000, 10)    # no rows, no strides
+    assert _heads("f", "q", Fake((0, 2, 64), bf, (0, 0, 0)), bf, 0, 0, 2, 64) == (0x1000, 128)
     for bad in (((4, 9), f32, (9, 1)), ((4, 12), f32, (16, 2)), ((3, 12), f32, (12, 1)), ((4, 12), bf, (12, 1)),
                 ((48,), f32, (1,))):
         with pytest.raises(ValueError):
