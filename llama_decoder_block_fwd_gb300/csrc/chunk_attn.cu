@@ -36,7 +36,7 @@ constexpr int CA_THREADS = 384;
 constexpr int CA_REGS_ISSUE = 88, CA_REGS_SOFTMAX = 208;
 static_assert(CA_REGS_ISSUE + 2 * CA_REGS_SOFTMAX <= 3 * 168, "register split");
 constexpr uint32_t CA_TMEM_COLS = 512;
-constexpr int CP_THREADS = 1024;
+constexpr int CP_THREADS = 1024, CP_WARPS = CP_THREADS / 32;
 constexpr int kMaxGrid = 256;            // attention CTAs at most (one per SM; sizes the workspace)
 
 // Per sequence, written by the plan.
@@ -86,6 +86,7 @@ struct ChunkParams {   // 128-byte aligned by its tensor maps
   float* part_o;       // [part_rows, n_q, hd]
   float2* part_ml;     // [part_rows, n_q]  (m in log2 units, l)
   int part_rows, grid;
+  unsigned inv_kv, inv_grid, inv_pair;   // floor(2^32 / x) of n_kv, grid and 2 tpt
   unsigned* status;
 };
 
@@ -117,19 +118,30 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
 // others fill up to half of the longest one.  Replayed on a list scheduler over 70 mixes of lengths this
 // is within 1% of the best candidate on average.  C runs from 1 tile to all in steps of sqrt(2), one per
-// warp; candidates whose partials do not fit the workspace are out, the last C (nothing cut) always fits.
+// warp (those past the longest range cut nothing, like the last, and are skipped); candidates whose partials do not fit the workspace are out, the last C (nothing cut) always fits.
 //
-// One CTA does this while all the others wait, so it is written for few instructions: 32 warps on one SM
-// are bound by its issue slots (integer division alone cost 3 us of 9.5 at 64 sequences).
+// One CTA does this while all the others wait: a chain of dependent steps (loads, scans, estimate, scans,
+// records) of about 8000 cycles, whose length is what counts: divisions go through reciprocals (integer and
+// IEEE divisions cost 1.6 us of it), and 512 threads or a warm instruction cache change nothing.
 constexpr float kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost = 2.0f, kMergeCost = 2.0f;
-constexpr int CP_SEQS = 1024;      // sequences whose shapes are kept in shared memory (one per thread)
+constexpr int CP_SEQS = CP_THREADS;      // sequences whose shapes are kept in shared memory (one per thread)
 
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // floor(a / b) for 0 <= a < 2^22, 0 < b, inv within a few ulp of 1 / b
 __device__ __forceinline__ int div_by(int a, int b, float inv) {
   int q = (int)((float)a * inv);
   if (q * b > a) --q;
   if ((q + 1) * b <= a) ++q;
   return q;
+}
+// floor(a / b), a >= 0, inv = floor(2^32 / b): a * inv / 2^32 is less than 1 + a / 2^32 below a / b
+__device__ __forceinline__ int div_inv(int a, int b, unsigned inv) {
+  const int q = (int)__umulhi((unsigned)a, inv);
+  return b == 1 ? a : q + ((q + 1) * b <= a);
 }
 __device__ __forceinline__ int cdiv_by(int a, int b, float inv) { return div_by(a + b - 1, b, inv); }
 
@@ -144,7 +156,7 @@ __device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b, bool&
   const bool wrong = s.lo < 0 || s.n < 0 || hi > p.T || (s.n > 0 && (s.c < 0 || (int64_t)s.c + s.n - 1 > p.max_pos));
   bad = bad || wrong;
   if (wrong || s.n == 0) { s.n = 0; s.c = 0; }
-  s.np = cdiv(s.n, 2 * p.tpt);
+  s.np = div_inv(s.n + 2 * p.tpt - 1, 2 * p.tpt, p.inv_pair);
   s.nt = (s.c + s.n + 127) >> 7;
   return s;
 }
@@ -152,9 +164,9 @@ __device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b, bool&
 // nt tiles in chunks of at most C (inv = 1 / C): their number and their tiles
 __device__ __forceinline__ void cut(int nt, int C, float inv, int& nc, int& ct) {
   nc = nt <= C ? 1 : cdiv_by(nt, C, inv);
-  const float inv_nc = __frcp_rn((float)nc);
+  const float inv_nc = rcp((float)nc);
   ct = max(1, cdiv_by(nt, nc, inv_nc));
-  nc = max(1, cdiv_by(nt, ct, __frcp_rn((float)ct)));
+  nc = max(1, cdiv_by(nt, ct, rcp((float)ct)));
 }
 // candidate w of 32: about 2^(w / 2) tiles, the last one unbounded
 __device__ __forceinline__ int candidate(int w) {
@@ -164,12 +176,13 @@ __device__ __forceinline__ int candidate(int w) {
 // Unit u of sequence b (seq[b].unit0 <= u); false if no row of it sees its keys.
 __device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& s, int b, int u, ChunkUnit& d) {
   // first the uncut items, the longest first, then the others chunk by chunk
-  const int x = u - s.unit0, whole = s.wp * p.n_kv, nq = s.np - s.wp;
-  const int y = (x < whole ? x : x - whole) / p.n_kv;
-  const int chunk = x < whole ? 0 : y / nq, pair = x < whole ? s.np - 1 - y : nq - 1 - y % nq;
+  const int x = u - s.unit0, item = div_inv(x, p.n_kv, p.inv_kv), y = item < s.wp ? item : item - s.wp, nq = s.np - s.wp;
+  const bool uncut = item < s.wp;
+  const int chunk = uncut || s.nc == 1 ? 0 : div_by(y, nq, rcp((float)nq));   // parts are bounded, so y is
+  const int pair = uncut ? s.np - 1 - y : nq - 1 - (y - chunk * nq);
   const int first = pair * 2 * p.tpt;                                       // token of the earlier Q tile
   const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
-  const int t0 = chunk * s.ct, t1 = x < whole ? nt0 : min(t0 + s.ct, nt0);
+  const int t0 = chunk * s.ct, t1 = uncut ? nt0 : min(t0 + s.ct, nt0);
   d.live = t0 < t1;
   d.t0 = t0;
   d.lone = s.n - first <= p.tpt;
@@ -179,194 +192,228 @@ __device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& 
   d.row0 = d.lone ? d.row1 : d.row1 + p.tpt;
   d.end = s.lo + s.n;
   d.pos_off = s.c - s.lo;
-  d.g = x % p.n_kv;
+  d.g = x - item * p.n_kv;
   d.kv_len = s.c + s.n;
   d.clean = (s.c + first + 1) / 128;
-  d.part = x >= whole && s.cut_n > 0 ? s.part0 + chunk * s.cut_n - s.lo : INT_MIN;
+  d.part = !uncut && s.cut_n > 0 ? s.part0 + chunk * s.cut_n - s.lo : INT_MIN;
   d.b = b;
   d.pad0 = d.pad1 = 0;
   return d.live;
 }
 
-// Exclusive prefix sums over the block of N integers per thread; total gets the block's sums.  buf: [N][32].
-template <int N>
-__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*buf)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl[N];
+// Inclusive prefix sum over a warp.
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    incl[i] = v[i];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl[i], o);
-      if (lane >= o) incl[i] += y;
-    }
-    if (lane == 31) buf[i][warp] = incl[i];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int w = buf[i][lane];
-    int y = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    total[i] = __shfl_sync(0xffffffffu, y, 31);
-    v[i] = __shfl_sync(0xffffffffu, y - w, warp) + incl[i] - v[i];
-  }
+  return v;
 }
+
+// What a lane, then a warp, adds up for one candidate: items left whole and pieces of the others, their
+// time, the longest, partial rows.
+struct Estimate {
+  float nw = 0.f, cw = 0.f, lw = 0.f, nu = 0.f, cu = 0.f, lu = 0.f;
+  float rows = 0.f;   // exact below 2^24, beyond it too many
+  // v: (n, np, nt, tiles of the shortest item), cut in nc chunks of ct tiles but for wp items left whole
+  __device__ __forceinline__ void add(const ChunkParams& p, const int4& v, int nc, int ct, int wp) {
+    const float n_kv = (float)p.n_kv, nt = (float)v.z, lo = (float)v.w;
+    const float step = __fdividef(nt - lo, (float)max(v.y - 1, 1));
+    if (wp > 0) {
+      const float items = (float)wp * n_kv;
+      nw += items;
+      cw += items * (nt - 0.5f * step * (float)(wp - 1) + kUnitCost);
+      lw = fmaxf(lw, nt + kUnitCost);
+    }
+    if (v.y > wp) {
+      const float mean = 0.5f * (nt - step * (float)wp + lo);
+      const float k = nc > 1 ? fmaxf(1.f, ceilf(__fdividef(mean, (float)ct) - 0.25f)) : 1.f;
+      const float row_cost = kRowCost / 256.f * (float)p.r;
+      const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, 2 * p.tpt) : 0.f);
+      const float items = (float)(v.y - wp) * n_kv;
+      nu += items * k;
+      cu += items * (mean + k * over);
+      lu = fmaxf(lu, (float)min(ct, v.z) + over);
+      if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * 2 * p.tpt);
+    }
+  }
+  __device__ __forceinline__ float time(const ChunkParams& p, bool some_whole) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      if (some_whole) {
+        nw += __shfl_xor_sync(0xffffffffu, nw, o);
+        cw += __shfl_xor_sync(0xffffffffu, cw, o);
+      }
+      nu += __shfl_xor_sync(0xffffffffu, nu, o);
+      cu += __shfl_xor_sync(0xffffffffu, cu, o);
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    }
+    // (not negative, so ordered as their bits)
+    if (some_whole) lw = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lw)));
+    lu = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lu)));
+    const float g = rcp((float)p.grid), mw = nw > 0.f ? __fdividef(cw, nw) : 0.f, mu = nu > 0.f ? __fdividef(cu, nu) : 0.f;
+    const float e = lw <= 1.2f * mw && lu <= 1.2f * mu ? ceilf(nw * g - 0.01f) * mw + ceilf(nu * g - 0.01f) * mu
+                                                       : (cw + cu) * g + 0.5f * (nu > 0.f ? lu : lw);
+    return rows <= (float)p.part_rows ? fmaxf(e, fmaxf(lw, lu)) + (rows > 0.f ? kMergeCost : 0.f) : INFINITY;
+  }
+};
 
 __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ int4 shapes[CP_SEQS];  // (n, np, nt, tiles of the shortest item)
-  __shared__ int before[CP_SEQS];   // items per KV group that may be left whole, in the sequences before
+  __shared__ int4 places[CP_SEQS];  // (first packed row, cached positions, first partial row, items left whole)
+  __shared__ int before[CP_SEQS];   // items per KV group that may be left whole, in the sequences before of the same 32
   __shared__ int unit0[CP_SEQS];
   __shared__ float est[64];
-  __shared__ int sums[4][32];
+  __shared__ int most[CP_WARPS], shares[CP_WARPS], sums[3][CP_WARPS];   // per warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   bool bad = false;
   const int per = cdiv(p.B, CP_THREADS);                              // contiguous runs of sequences
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  const bool active = warp * 32 * per < p.B;                          // this warp has sequences
+  const bool table = p.B <= CP_SEQS;
   const int tpt2 = 2 * p.tpt;
   SeqShape mine = {0, 0, 0, 0, 0};                                    // the first of this thread's
   if (b0 < b1) mine = seq_shape(p, b0, bad);
   auto shape = [&](int b) { return b == b0 ? mine : seq_shape(p, b, bad); };
   auto shape4 = [&](const SeqShape& s) { return make_int4(s.n, s.np, s.nt, (s.c + min(s.n, tpt2) + 127) >> 7); };
-  const bool table = p.B <= CP_SEQS;
-  if (table && b0 < b1) shapes[b0] = shape4(mine);
+  int nt_max = 0, share = 0;
+  if (active) {
+    for (int b = b0; b < b1; ++b) nt_max = max(nt_max, shape(b).nt);
+    nt_max = __reduce_max_sync(0xffffffffu, nt_max);
+    if (table) {   // one sequence per thread
+      const int own = mine.np > 1 ? mine.np : 0;
+      share = warp_scan(own);
+      if (b0 < b1) {
+        shapes[b0] = shape4(mine);
+        before[b0] = share - own;
+      }
+    }
+  }
+  if (lane == 31) {
+    most[warp] = nt_max;
+    shares[warp] = share;
+  }
+  if (tid < 64) est[tid] = INFINITY;
   __syncthreads();
-  const int C_est = candidate(warp);
-  const float inv_C = __frcp_rn((float)C_est), n_kv = (float)p.n_kv, row_cost = kRowCost / 256.f * (float)p.r;
-  int rounds_whole = 0;
-  for (int f = 0; f < 2; ++f) {
-    float nw = 0.f, cw = 0.f, lw = 0.f, nu = 0.f, cu = 0.f, lu = 0.f;   // units, their time, the longest
-    float rows = 0.f;                                                    // exact below 2^24, beyond it too many
-    int share = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      const int4 v = table ? shapes[b] : shape4(seq_shape(p, b, bad));
-      if (v.x == 0) continue;
-      // an item that shares its K and V with others of its sequence may be left whole
-      const int sharing = v.y > 1 ? v.y : 0, wp = f ? min(max(rounds_whole - before[b], 0), sharing) : 0;
-      share += sharing;
-      int nc, ct;
-      cut(v.z, C_est, inv_C, nc, ct);
-      const float nt = (float)v.z, lo = (float)v.w, step = __fdividef(nt - lo, (float)max(v.y - 1, 1));
-      if (wp > 0) {
-        const float items = (float)wp * n_kv;
-        nw += items;
-        cw += items * (nt - 0.5f * step * (float)(wp - 1) + kUnitCost);
-        lw = fmaxf(lw, nt + kUnitCost);
+  nt_max = __reduce_max_sync(0xffffffffu, lane < CP_WARPS ? most[lane] : 0);
+  // whole rounds of items that share their K and V with others, one per CTA (batches beyond the table: none)
+  const int all = __reduce_add_sync(0xffffffffu, lane < CP_WARPS ? shares[lane] : 0) * p.n_kv;
+  const int rounds_whole = div_inv(div_inv(all, p.grid, p.inv_grid) * p.grid, p.n_kv, p.inv_kv);
+  for (int w = warp; w < 32; w += CP_WARPS) {
+    const int C_est = candidate(w);
+    if (C_est >= nt_max && w != 31) continue;   // from the longest range on they all cut nothing
+    const float inv_C = rcp((float)C_est);
+    Estimate e0, e1;
+    for (int k = 0, base = 0; 32 * k < p.B; ++k) {
+      const int b = 32 * k + lane;
+      if (b < p.B) {
+        const int4 v = table ? shapes[b] : shape4(seq_shape(p, b, bad));
+        if (v.x > 0) {
+          int nc, ct;
+          cut(v.z, C_est, inv_C, nc, ct);
+          e0.add(p, v, nc, ct, 0);
+          if (rounds_whole > 0) e1.add(p, v, nc, ct, v.y > 1 ? min(max(rounds_whole - base - before[b], 0), v.y) : 0);
+        }
       }
-      if (v.y > wp) {
-        const float mean = 0.5f * (nt - step * (float)wp + lo);
-        const float k = nc > 1 ? fmaxf(1.f, ceilf(__fdividef(mean, (float)ct) - 0.25f)) : 1.f;
-        const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, tpt2) : 0.f);
-        const float items = (float)(v.y - wp) * n_kv;
-        nu += items * k;
-        cu += items * (mean + k * over);
-        lu = fmaxf(lu, (float)min(ct, v.z) + over);
-        if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * tpt2);
-      }
+      if (rounds_whole > 0) base += shares[k];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (f) {
-        nw += __shfl_xor_sync(0xffffffffu, nw, o);
-        cw += __shfl_xor_sync(0xffffffffu, cw, o);
-        lw = fmaxf(lw, __shfl_xor_sync(0xffffffffu, lw, o));
-      }
-      nu += __shfl_xor_sync(0xffffffffu, nu, o);
-      cu += __shfl_xor_sync(0xffffffffu, cu, o);
-      lu = fmaxf(lu, __shfl_xor_sync(0xffffffffu, lu, o));
-      rows += __shfl_xor_sync(0xffffffffu, rows, o);
-    }
+    const float t0 = e0.time(p, false), t1 = rounds_whole > 0 ? e1.time(p, true) : INFINITY;
     if (lane == 0) {
-      const float g = (float)p.grid, mw = nw > 0.f ? cw / nw : 0.f, mu = nu > 0.f ? cu / nu : 0.f;
-      const float e = lw <= 1.2f * mw && lu <= 1.2f * mu ? ceilf(nw / g) * mw + ceilf(nu / g) * mu
-                                                         : (cw + cu) / g + 0.5f * (nu > 0.f ? lu : lw);
-      est[32 * f + warp] =
-          rows <= (float)p.part_rows ? fmaxf(e, fmaxf(lw, lu)) + (rows > 0.f ? kMergeCost : 0.f) : INFINITY;
+      est[w] = t0;
+      est[32 + w] = t1;
     }
-    if (f) break;
-    // whole rounds of such items, one per CTA (larger batches than the table: none)
-    share = __reduce_add_sync(0xffffffffu, share);
-    rounds_whole = table ? (int)((int64_t)share * p.n_kv / p.grid * p.grid / p.n_kv) : 0;
-    if (rounds_whole == 0) {
-      if (lane == 0) est[32 + warp] = INFINITY;
-      break;
-    }
-    int at[1] = {b0 < b1 && mine.np > 1 ? mine.np : 0}, all[1];
-    block_scan<1>(at, all, sums);
-    if (b0 < b1) before[b0] = at[0];
-    __syncthreads();
   }
   __syncthreads();
   // the least estimate, the larger C of equals (every warp finds it for itself)
-  float e = est[lane];
-  int pick = lane;
-  if (est[32 + lane] < e) { e = est[32 + lane]; pick = 32 + lane; }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float oe = __shfl_xor_sync(0xffffffffu, e, o);
-    const int op = __shfl_xor_sync(0xffffffffu, pick, o);
-    if (oe < e || (oe == e && op > pick)) { e = oe; pick = op; }
-  }
+  const bool second = est[32 + lane] < est[lane];
+  const unsigned bits = __float_as_uint(second ? est[32 + lane] : est[lane]);
+  const unsigned least = __reduce_min_sync(0xffffffffu, bits);
+  const int pick = __reduce_max_sync(0xffffffffu, bits == least ? lane + (second ? 32 : 0) : 0);
   const int C = candidate(pick & 31), whole = pick >= 32 ? rounds_whole : 0;
-  const float inv = __frcp_rn((float)C);
+  const float inv = rcp((float)C);
   // ---- the sequences' records; prefix sums of (units, partial rows, cut tokens)
+  const int share0 = __reduce_add_sync(0xffffffffu, lane < warp ? shares[lane] : 0);
   auto record = [&](int b) {
     const SeqShape s = shape(b);
     ChunkSeq r;
     cut(s.nt, C, inv, r.nc, r.ct);
     r.lo = s.lo; r.n = s.n; r.c = s.c; r.np = s.np;
-    r.wp = whole && s.np > 1 ? min(max(whole - before[b], 0), s.np) : 0;
+    r.wp = whole && s.np > 1 ? min(max(whole - share0 - before[b], 0), s.np) : 0;
     r.cut_n = r.nc > 1 ? min(s.n, (s.np - r.wp) * tpt2) : 0;
     return r;
   };
-  int v[3] = {0, 0, 0}, total[3];
+  int v[3] = {0, 0, 0};
   ChunkSeq mine_r;
+  auto count = [&](const ChunkSeq& r) {
+    v[0] += (r.wp + r.nc * (r.np - r.wp)) * p.n_kv;
+    v[1] += r.nc * r.cut_n;
+    v[2] += r.cut_n;
+  };
   for (int b = b0; b < b1; ++b) {
     const ChunkSeq r = record(b);
     if (b == b0) mine_r = r;
-    v[0] += (r.wp + r.nc * (r.np - r.wp)) * p.n_kv;
-    v[1] += r.nc * r.cut_n;
-    v[2] += r.cut_n;
+    count(r);
   }
   if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
-  block_scan<3>(v, total, sums + 1);
-  for (int b = b0; b < b1; ++b) {
-    ChunkSeq r = b == b0 ? mine_r : record(b);
-    r.unit0 = v[0];
-    r.part0 = v[1];
-    r.split0 = v[2];
-    if (in_extent(b, 1, p.B)) p.seq[b] = r;
-    if (table) unit0[b] = v[0];
-    v[0] += (r.wp + r.nc * (r.np - r.wp)) * p.n_kv;
-    v[1] += r.nc * r.cut_n;
-    v[2] += r.cut_n;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int own = v[i], incl = active ? warp_scan(own) : 0;
+    if (lane == 31) sums[i][warp] = incl;
+    v[i] = incl - own;
   }
-  if (tid == 0) {
-    ChunkHead h;
-    h.n_units = total[0];
-    h.counter = p.grid;      // unit i < grid is CTA i's first
-    h.n_split = total[2];
-    h.pad = 0;
-    *p.head = h;
+  __syncthreads();
+  const int n_units = __reduce_add_sync(0xffffffffu, lane < CP_WARPS ? sums[0][lane] : 0);
+  if (active) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] += __reduce_add_sync(0xffffffffu, lane < warp ? sums[i][lane] : 0);
+    for (int b = b0; b < b1; ++b) {
+      ChunkSeq r = b == b0 ? mine_r : record(b);
+      r.unit0 = v[0];
+      r.part0 = v[1];
+      r.split0 = v[2];
+      if (in_extent(b, 1, p.B)) p.seq[b] = r;
+      if (table) {
+        unit0[b] = v[0];
+        places[b] = make_int4(r.lo, r.c, r.part0, r.wp);
+      }
+      count(r);
+    }
+  }
+  if (warp == CP_WARPS - 1) {
+    const int n_split = __reduce_add_sync(0xffffffffu, lane < CP_WARPS ? sums[2][lane] : 0);
+    if (lane == 0) {
+      ChunkHead h;
+      h.n_units = n_units;
+      h.counter = p.grid;      // unit i < grid is CTA i's first
+      h.n_split = n_split;
+      h.pad = 0;
+      *p.head = h;
+    }
   }
   // ---- the CTAs' first units, ready to use: found here in parallel, not each by its own CTA's chain of loads
   __syncthreads();
   for (int u = tid; u < p.grid; u += CP_THREADS) {
     ChunkUnit d;
     d.live = 0;
-    if (u < total[0]) {
+    if (u < n_units) {
       int lo = 0, hi = p.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if ((table ? unit0[mid] : p.seq[mid].unit0) <= u) lo = mid; else hi = mid;
       }
-      make_unit(p, p.seq[lo], lo, u, d);
+      ChunkSeq r;
+      if (table) {
+        const int4 a = shapes[lo], q = places[lo];
+        cut(a.z, C, inv, r.nc, r.ct);
+        r.unit0 = unit0[lo]; r.lo = q.x; r.n = a.x; r.c = q.y; r.np = a.y; r.wp = q.w; r.part0 = q.z;
+        r.cut_n = r.nc > 1 ? min(a.x, (a.y - q.w) * tpt2) : 0;
+      } else {
+        r = p.seq[lo];
+      }
+      make_unit(p, r, lo, u, d);
     }
     if (in_extent(u, 1, p.grid)) p.first[u] = d;
   }
@@ -1042,6 +1089,10 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   ws += round256((size_t)p.part_rows * a.n_q * HD * 4);
   p.part_ml = reinterpret_cast<float2*>(ws);
   p.grid = std::min(num_sms, kMaxGrid);
+  auto inverse = [](int64_t x) { return (unsigned)std::min<uint64_t>((1ull << 32) / (uint64_t)x, UINT32_MAX); };
+  p.inv_kv = inverse(a.n_kv);
+  p.inv_grid = inverse(p.grid);
+  p.inv_pair = inverse(2 * tpt);
   p.status = a.status;
   int dev = 0;
   cudaGetDevice(&dev);
