@@ -510,6 +510,64 @@ def test_verify_long_sequences_and_many():
     assert n_acc.tolist() == [50, 0, 32, 33, 39] and out[50] == 9 and (out[51:70] == -1).all() and (out[70:] == 7).all()
 
 
+@pytest.mark.parametrize("V,new", [(128256, [5, 0, 3, 1, 4] * 7), (32003, [4, 1, 2, 0, 0, 9, 40, 3] * 4), (1000, [3] * 2500),
+                                   (5000, [0] * 300 + [70, 1] * 30 + [0] * 5), (151936, [66])])
+@pytest.mark.parametrize("T", [0.0, 0.8])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_verify_large_batches(V, new, T, drafts):
+    """Rows by the hundred, empty sequences in a row, vocabularies that end inside a part."""
+    z, y, tokens, u, noise = _verify_inputs(new, V, seed=len(new), off=0.2, pad=1)
+    y = y if drafts else None
+    for strided in (0, 1):
+        got = _verify(z, y, T, new, tokens, u, noise, strided)
+        assert _status() == 0
+        _check_verify(got, z, y, T, new, tokens, u, noise)
+
+
+def test_verify_large_batch_with_nothing_remaining():
+    """Equal models, a draft of weight 0 in both, in every sequence of a large batch."""
+    V, new = 20000, [3] * 120
+    z, y, tokens, u, noise = _verify_inputs(new, V, seed=15, off=0.0)
+    tokens[1::3] = 40
+    z[:, 40] = y[:, 40] = -np.inf
+    got = _verify(z, y, 1.0, new, tokens, u, noise)
+    assert _status() == 0 and (got[0] == 0).all()
+    _check_verify(got, z, y, 1.0, new, tokens, u, noise)
+
+
+def test_verify_large_batches_captured_and_on_two_streams():
+    """Two calls in flight at once, each captured and replayed with other inputs."""
+    import torch
+    V, runs = 30011, []
+    for seed, new in enumerate(([4] * 70, [2, 9, 0, 1] * 30)):
+        z, y, tokens, u, noise = _verify_inputs(new, V, seed=20 + seed)
+        t = [_dev(z), _dev(y), _i32(np.concatenate([[0], np.cumsum(new)])), _i32(tokens), _dev(u), _dev(noise)]
+        n_acc, out = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (len(new), sum(new)))
+        dims = L.dims_of(len(new), sum(new), 128, 1, 1, 128, 128, THETA, 1e-5)
+        ws = torch.full((L.llama_workspace_bytes(L.OP_VERIFY_DRAFTS, dims, L.F32, vocab=V),), 0xFF, dtype=torch.uint8,
+                        device="cuda")
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            L.llama_verify_drafts(t[0], t[1], 0.9, t[2], t[3], t[4], t[5], n_acc, out, ws)
+        runs.append((new, t, n_acc, out, st, g, ws))
+    for turn in range(3):
+        inputs = []
+        for seed, (new, t, _, _, _, _, _) in enumerate(runs):
+            z, y, tokens, u, noise = _verify_inputs(new, V, seed=30 + 10 * turn + seed)
+            for dst, a in zip((t[0], t[1], t[3], t[4], t[5]), (z, y, tokens, u, noise)):
+                dst.copy_(torch.from_numpy(a))
+            inputs.append((z, y, tokens, u, noise))
+        torch.cuda.synchronize()
+        for _, _, _, _, st, g, _ in runs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        assert _status() == 0
+        for (new, _, n_acc, out, _, _, _), (z, y, tokens, u, noise) in zip(runs, inputs):
+            _check_verify((n_acc.cpu().numpy(), out.cpu().numpy()), z, y, 0.9, new, tokens, u, noise)
+
+
 def test_verify_extreme_temperatures():
     V, new = 500, [3] * 12
     z, y, tokens, u, noise = _verify_inputs(new, V, seed=12)
