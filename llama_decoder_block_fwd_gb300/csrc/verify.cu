@@ -11,8 +11,13 @@
 //
 // HBM bound.  Phase 1 (verify_stats_kernel) reads every judged row of z and y once: warps take the
 // 1024-logit parts of all rows in turn, a part's loads in flight together, and leave its (max, sum of
-// exponentials).  Phase 2 (verify_pick_kernel, a cluster of up to 8 CTAs per
-// sequence) merges the parts, finds the first rejection and reads that row of z, y and e for the race.
+// exponentials).  Phase 2 (verify_pick_kernel, a cluster of up to 8 CTAs per sequence) merges the parts,
+// finds the first rejection and reads that row of z, y and e for the race.
+// 64 sequences x 2-5 rows x 128256 logits with a draft distribution: 55.3 us, of which phase 1 27 us (200 MB,
+// the slowest SM 27 us, the median warp 24), merging and judging 2, the race 12 (99 MB from L2 and HBM, in
+// eight dependent turns), cluster exchange and result 4, launches the rest; the bytes alone would take 34.
+// One kernel over both phases (items from a counter, races behind the statistics) took 111 us: each item
+// paid two barriers, a fence and three dependent atomics with too few loads in flight.
 // A part's sums are formed and merged in a fixed order, and the race keeps the largest score and of equals
 // the lowest id, so the result does not depend on timing.
 #include <cooperative_groups.h>
@@ -244,9 +249,9 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
   namespace cg = cooperative_groups;
   const cg::cluster_group cl = cg::this_cluster();
   const int P = (int)cl.num_blocks(), cr = (int)cl.block_rank(), b = blockIdx.x / P;
-  __shared__ int stop_sh, top_sh, wid[VF_WARPS], cid;
+  __shared__ int stop_sh, top_sh, wid[VF_WARPS], cid[2][VF_CLUSTER];
   __shared__ float2 sz_sh[VF_ROWS], sy_sh[VF_ROWS];
-  __shared__ float wbest[VF_WARPS], cbest;
+  __shared__ float wbest[VF_WARPS], cbest[2][VF_CLUSTER];   // per turn, every CTA's best
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the caller's inputs may be read before the statistics are there
   const int lo = max(0, __ldg(p.cu + b)), hi = min(p.T, __ldg(p.cu + b + 1));
@@ -342,16 +347,17 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
         race_max(best, id, __shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, id, o));
       if (lane == 0) { wbest[warp] = best; wid[warp] = id; }
       __syncthreads();
-      if (tid == 0) {
+      if (tid < P) {   // to every CTA of the cluster, which after the barrier reads only its own memory
+        best = wbest[0];
+        id = wid[0];
         for (int k = 1; k < VF_WARPS; ++k) race_max(best, id, wbest[k], wid[k]);
-        cbest = best;
-        cid = id;
+        *cl.map_shared_rank(&cbest[turn][cr], tid) = best;
+        *cl.map_shared_rank(&cid[turn][cr], tid) = id;
       }
       cl.sync();
       best = 0.f;
       id = INT_MAX;
-      for (int r = 0; r < P; ++r) race_max(best, id, *cl.map_shared_rank(&cbest, r), *cl.map_shared_rank(&cid, r));
-      cl.sync();   // no CTA leaves, or writes its result again, while another still reads it
+      for (int r = 0; r < P; ++r) race_max(best, id, cbest[turn][r], cid[turn][r]);
       token = id == INT_MAX ? 0 : id;
       if (!rejected || id != INT_MAX) break;
     }
@@ -396,9 +402,11 @@ int launch_verify(const VerifyDesc& d, int num_sms, unsigned* status, cudaStream
   }
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  // as many CTAs per sequence as are resident together, up to a cluster
+  // as many CTAs per sequence as are resident together, up to a cluster; an eighth of the room is left to
+  // how clusters fall on the GPCs (64 x 128256, three CTAs per SM: clusters of 7 in all the room took a
+  // second wave, 70 us; clusters of 6, 57.6 us; of 8 at four per SM, 55.3 us)
   int P = 1;
-  while (!p.greedy && P < VF_CLUSTER && 2 * P * d.B <= VF_PICK_CTAS * num_sms) P *= 2;
+  if (!p.greedy) P = (int)std::min<int64_t>(VF_CLUSTER, std::max<int64_t>(1, VF_PICK_CTAS * num_sms * 7 / 8 / d.B));
   cfg.gridDim = dim3((unsigned)(d.B * P));
   cfg.blockDim = dim3(VF_THREADS);
   cfg.stream = st;
