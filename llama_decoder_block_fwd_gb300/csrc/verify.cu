@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
   __shared__ float2 sz_sh[VF_ROWS], sy_sh[VF_ROWS];
   __shared__ float wbest[VF_WARPS], cbest[2][VF_CLUSTER];   // per turn, every CTA's best
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cl.barrier_arrive();      // waited for before another CTA's memory is written: that CTA has started then
   // the caller's inputs may be read before the statistics are there
   const int lo = max(0, __ldg(p.cu + b)), hi = min(p.T, __ldg(p.cu + b + 1));
   if (tid == 0) stop_sh = hi - 1;
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
   inputs();
   pdl_wait();
   if (hi <= lo) {           // a sequence without rows (the whole cluster leaves)
+    cl.barrier_wait();
     if (cr == 0 && tid == 0 && in_extent(b, 1, p.B)) p.n_acc[b] = 0;
     return;
   }
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
   const int stop = stop_sh;
   const bool rejected = stop < hi - 1;
   int token;
+  cl.barrier_wait();
   if (p.greedy) {
     if (warp == 0) {
       const int id = merge_argmax(p, p.stat_z + (int64_t)stop * p.parts);
