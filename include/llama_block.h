@@ -330,7 +330,8 @@ int llama_rope_append_paged(const llama_dims* dims, const void* q, int64_t q_str
  *   max_pos: an upper bound of every new token's position (host value; sizes the work split and the
  *   workspace, llama_workspace_bytes(LLAMA_OP_GQA_ATTENTION_CHUNK_PAGED, dims, ..., kv_capacity =
  *   max_pos + 1))
- * Sequences may bring any number of tokens, none included; pages may be shared between sequences.
+ * Sequences may bring any number of tokens, none included; pages may be shared between sequences.  o may
+ * not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
  * Pool rows past a sequence's last position are never used, whatever they hold, and a key or value a
  * query does not see never reaches it, infinite or NaN values included.  bf16, head_dim 64 or 128,
  * n_q / n_kv <= 128, n_pages < 2^24 (else LLAMA_ERR_UNSUPPORTED).  Found on the device and latched as

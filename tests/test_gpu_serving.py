@@ -393,6 +393,66 @@ def test_chunk_attention_reports_pages_outside_the_pool():
     b.check(b.run())
 
 
+def test_pools_past_2_to_the_31_elements():
+    """The last pages of pools of 2.4e9 elements: append writes them and attention reads them."""
+    import torch
+    n_pages, n_q, n_kv, hd, c, n = 18400, 32, 8, 128, 130, 5
+    rng = np.random.default_rng(3)
+    kp, vp = (torch.empty((n_pages, 128, n_kv, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = np.array([[n_pages - 1, n_pages - 3]], np.int32)
+    x = _dev(rng.normal(size=(c + n, n_q + 2 * n_kv, hd)), torch.bfloat16)
+    pos = np.arange(c + n)
+    slots = table[0, pos // 128].astype(np.int64) * 128 + pos % 128
+    dims = L.dims_of(1, c + n, 128, n_q, n_kv, hd, 128, THETA, 1e-5)
+    q = torch.empty((c + n, n_q, hd), dtype=torch.bfloat16, device="cuda")
+    L.llama_rope_append_paged(dims, x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], _i32(pos), _i32(slots), q, kp, vp)
+    dims = L.dims_of(1, n, 128, n_q, n_kv, hd, 128, THETA, 1e-5)
+    o, q = torch.empty((n, n_q, hd), dtype=torch.bfloat16, device="cuda"), q[c:].contiguous()
+    ws = torch.empty(L.llama_workspace_bytes(L.OP_GQA_ATTENTION_CHUNK_PAGED, dims, L.BF16, kv_capacity=c + n),
+                     dtype=torch.uint8, device="cuda")
+    L.llama_gqa_attention_chunk_paged(dims, q, kp, vp, _dev(table), _i32([0, n]), _i32([c]), c + n - 1, o, ws)
+    assert _status() == 0
+    at = torch.from_numpy(slots).cuda()
+    k, v = to_f64(kp.view(-1, n_kv, hd)[at]), to_f64(vp.view(-1, n_kv, hd)[at])
+    _assert_rotated(k, to_f64(x)[:, n_q:n_q + n_kv], pos, "k")
+    assert np.array_equal(v, to_f64(x)[:, n_q + n_kv:])
+    assert_parity(to_f64(o), R.attention(to_f64(q), k, v, c), BF16, "far pages")
+
+
+def test_packed_rows_past_2_to_the_31_elements():
+    """q and o of 2.2e9 elements: 540 sequences of 1000 tokens, 32 heads over one KV head."""
+    import torch
+    B, n, n_q, n_kv, hd = 540, 1000, 32, 1, 128
+    gen = torch.Generator("cuda").manual_seed(1)
+    kp, vp = (torch.randn((8 * B, 128, n_kv, hd), generator=gen, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.empty((B * n, n_q, hd), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    o = torch.full_like(q, 7.0)
+    table = torch.arange(8 * B, dtype=torch.int32, device="cuda").view(B, 8)
+    dims = L.dims_of(B, B * n, 128, n_q, n_kv, hd, 128, THETA, 1e-5)
+    ws = torch.empty(L.llama_workspace_bytes(L.OP_GQA_ATTENTION_CHUNK_PAGED, dims, L.BF16, kv_capacity=n),
+                     dtype=torch.uint8, device="cuda")
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    L.llama_gqa_attention_chunk_paged(dims, q, kp, vp, table, cu, torch.zeros(B, dtype=torch.int32, device="cuda"), n - 1, o, ws)
+    assert _status() == 0
+    for b in (0, 270, B - 1):
+        k, v = (to_f64(t[8 * b:8 * b + 8]).reshape(-1, n_kv, hd) for t in (kp, vp))
+        for i in (0, 500, n - 1):
+            ref = R.attention(to_f64(q[b * n + i:b * n + i + 1]), k[:i + 1], v[:i + 1], i)
+            assert_parity(to_f64(o[b * n + i:b * n + i + 1]), ref, BF16, f"seq {b}, token {i}")
+
+
+def test_calls_on_a_given_stream():
+    """The stream argument, from outside any stream context."""
+    import torch
+    b = Batch([300, 7], [20, 3], 8, 2, 64, seed=31)
+    want = b.run()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = b.run(stream=st)
+    torch.cuda.synchronize()
+    assert _status() == 0 and torch.equal(got, want)
+
+
 def test_chunk_attention_agrees_with_the_decode_call():
     import torch
     b = Batch([900, 17, 2048], [1, 1, 1], 32, 8, 128, seed=21)
@@ -593,6 +653,21 @@ def test_verify_draft_that_neither_model_allows():
     got = _verify(z, y, 1.0, new, tokens, u, noise)
     assert _status() == 0 and got[0].tolist() == [0, 0] and 0 <= got[1][0] < V and got[1][0] != 40
     _check_verify(got, z, y, 1.0, new, tokens, u, noise)
+
+
+def test_verify_uses_the_first_vocab_columns():
+    import torch
+    V, new = 700, [3, 1, 4]
+    z, y, tokens, u, noise = _verify_inputs(new, V + 9, seed=17)
+    tokens = np.minimum(tokens, V - 1)
+    z[:, V:], noise[:, V:] = 50.0, 1e-9                      # what stands behind them would win
+    n_acc, out = (torch.full((k,), -9, dtype=torch.int32, device="cuda") for k in (3, 8))
+    dims = L.dims_of(3, 8, 128, 1, 1, 128, 128, THETA, 1e-5)
+    ws = torch.empty(L.llama_workspace_bytes(L.OP_VERIFY_DRAFTS, dims, L.F32, vocab=V), dtype=torch.uint8, device="cuda")
+    L.llama_verify_drafts(_dev(z), _dev(y), 1.0, _i32([0, 3, 4, 8]), _i32(tokens), _dev(u), _dev(noise), n_acc, out, ws,
+                          vocab=V)
+    assert _status() == 0
+    _check_verify((n_acc.cpu().numpy(), out.cpu().numpy()), z[:, :V], y[:, :V], 1.0, new, tokens, u, noise[:, :V])
 
 
 def test_verify_without_rows():
