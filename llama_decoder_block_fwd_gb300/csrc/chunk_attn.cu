@@ -18,6 +18,10 @@
 //     issues the MMAs, warps 4-7 / 8-11 are the softmax groups, one thread per row (TMEM lane).  A unit
 //     that holds all of its item's keys stores o; otherwise it leaves (m, l, O) in the workspace.
 //   * chunk_combine_kernel merges the parts of the rows that were cut.
+// Measured (one call, plan and merge included): 2048 tokens after 30720, 32/8 heads x 128, 650-665 us = 1640
+// TFLOP/s (the attention kernel alone 1700, tensor pipe 72% active, its softmax warps' instructions in
+// the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 215 us, the attention
+// kernel 200 = 6.4 TB/s; three single tokens 14.3 us (plan 5, attention 6, merge 2.5).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
 #include <algorithm>
 #include <cmath>
@@ -86,7 +90,7 @@ struct ChunkParams {   // 128-byte aligned by its tensor maps
   float* part_o;       // [part_rows, n_q, hd]
   float2* part_ml;     // [part_rows, n_q]  (m in log2 units, l)
   int part_rows, grid;
-  unsigned inv_kv, inv_grid, inv_pair;   // floor(2^32 / x) of n_kv, grid and 2 tpt
+  unsigned inv_q, inv_kv, inv_grid, inv_pair;   // floor(2^32 / x) of n_q, n_kv, grid and 2 tpt
   unsigned* status;
 };
 
@@ -118,7 +122,8 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
 // others fill up to half of the longest one.  Replayed on a list scheduler over 70 mixes of lengths this
 // is within 1% of the best candidate on average.  C runs from 1 tile to all in steps of sqrt(2), one per
-// warp (those past the longest range cut nothing, like the last, and are skipped); candidates whose partials do not fit the workspace are out, the last C (nothing cut) always fits.
+// warp (those past the longest range cut nothing, like the last, and are skipped); candidates whose partials
+// do not fit the workspace are out, the last C (nothing cut) always fits.
 //
 // One CTA does this while all the others wait: a chain of dependent steps (loads, scans, estimate, scans,
 // records) of about 8000 cycles, whose length is what counts: divisions go through reciprocals (integer and
@@ -954,98 +959,69 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
 
 // ----------------------------------------------------------------------------------------- merge
 // o = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k over the chunks k that hold keys the token sees.
-// A warp takes a token of the cut sequences and HB of its heads at a time, KB chunks of each: their loads
-// are all in flight together (one head at a time, each waiting for its own, took 45 us for the 136 MB
-// of parts of 2048 tokens x 32 heads).
-template <int HD, int HB, int KB>
-__device__ __forceinline__ void combine_rows(const ChunkParams& p, int n_split, bool& waited) {
+// A warp takes one head of a token of the cut sequences, the loads of CC_CHUNKS of its parts in flight
+// together (each waiting for its own, 45 us for the 136 MB of parts of 2048 tokens x 32 heads; now 17).  Four
+// heads a warp, to have as many loads in flight from few chunks, cost registers and lost everywhere: 64
+// sequences of 3-5 tokens 224 us for the whole call against 217, three single tokens 19.5 against 14.6.
+constexpr int CC_CHUNKS = 4;
+
+template <int HD>
+__global__ void __launch_bounds__(256, 4) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int PER = HD / 32;
   using Vec = typename std::conditional<PER == 4, float4, float2>::type;
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8, groups = cdiv(p.n_q, HB);
-  const int64_t total = (int64_t)n_split * groups;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += warps) {
-    const int x = (int)(w / groups), h0 = (int)(w - (int64_t)x * groups) * HB;
-    const int hn = min(HB, p.n_q - h0);
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+  const int total = p.head->n_split * p.n_q;   // no more than the parts
+  bool waited = false;
+  for (int w = blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += warps) {
+    const int x = div_inv(w, p.n_q, p.inv_q), h = w - x * p.n_q;
     // sequences that were not cut hold no split rows, so the last one starting at or before x is it
     const int b = warp_search(p.B, x, [&](int i) { return p.seq[i].split0; });
     const ChunkSeq s = p.seq[b];
     const int i = x - s.split0;
     const int nk = min(s.nc, cdiv((s.c + i) / 128 + 1, s.ct));
-    const int64_t stride = (int64_t)s.cut_n * p.n_q, row0 = (int64_t)(s.part0 + i) * p.n_q + h0;
+    const int64_t stride = (int64_t)s.cut_n * p.n_q, row0 = (int64_t)(s.part0 + i) * p.n_q + h;
     if (!waited) pdl_wait();   // the parts
     waited = true;
-    float M[HB], l[HB], acc[HB][PER];
-    float2 a[HB];
+    float2 a = lane < nk ? p.part_ml[row0 + lane * stride] : make_float2(-INFINITY, 0.f);
+    float M = a.x;
+    for (int k = lane + 32; k < nk; k += 32) M = fmaxf(M, p.part_ml[row0 + k * stride].x);
 #pragma unroll
-    for (int h = 0; h < HB; ++h)
-      a[h] = h < hn && lane < nk ? p.part_ml[row0 + h + lane * stride] : make_float2(-INFINITY, 0.f);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    float l = 0.f, acc[PER];
 #pragma unroll
-    for (int h = 0; h < HB; ++h) M[h] = a[h].x;
-    for (int k = lane + 32; k < nk; k += 32)
-#pragma unroll
-      for (int h = 0; h < HB; ++h)
-        if (h < hn) M[h] = fmaxf(M[h], p.part_ml[row0 + h + k * stride].x);
-#pragma unroll
-    for (int h = 0; h < HB; ++h) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
-      if (M[h] == -INFINITY) M[h] = 0.f;
-      l[h] = 0.f;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[h][e] = 0.f;
-    }
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
     for (int k0 = 0; k0 < nk; k0 += 32) {
-      float wl[HB];
-#pragma unroll
-      for (int h = 0; h < HB; ++h) {
-        if (k0 > 0) a[h] = h < hn && k0 + lane < nk ? p.part_ml[row0 + h + (k0 + lane) * stride] : make_float2(-INFINITY, 0.f);
-        wl[h] = ex2(a[h].x - M[h]);   // 0 past the last chunk
-        l[h] += wl[h] * a[h].y;
-      }
+      if (k0 > 0) a = k0 + lane < nk ? p.part_ml[row0 + (k0 + lane) * stride] : make_float2(-INFINITY, 0.f);
+      const float wl = ex2(a.x - M);   // 0 past the last chunk
+      l += wl * a.y;
       const int kn = min(32, nk - k0);
-      for (int k = 0; k < kn; k += KB) {
+      for (int k = 0; k < kn; k += CC_CHUNKS) {
         const float* src = p.part_o + (row0 + (k0 + k) * stride) * HD + lane * PER;
-        Vec v[KB][HB];
+        Vec v[CC_CHUNKS];
 #pragma unroll
-        for (int q = 0; q < KB; ++q)
+        for (int q = 0; q < CC_CHUNKS; ++q)
+          if (k + q < kn) v[q] = *reinterpret_cast<const Vec*>(src + q * stride * HD);
 #pragma unroll
-          for (int h = 0; h < HB; ++h)
-            if (h < hn && k + q < kn) v[q][h] = *reinterpret_cast<const Vec*>(src + q * stride * HD + h * HD);
+        for (int q = 0; q < CC_CHUNKS; ++q) {
+          const float wk = __shfl_sync(0xffffffffu, wl, (k + q) & 31);
+          if (k + q < kn) {
+            const float* f = reinterpret_cast<const float*>(&v[q]);
 #pragma unroll
-        for (int q = 0; q < KB; ++q)
-#pragma unroll
-          for (int h = 0; h < HB; ++h) {
-            const float wk = __shfl_sync(0xffffffffu, wl[h], (k + q) & 31);
-            if (h < hn && k + q < kn) {
-              const float* f = reinterpret_cast<const float*>(&v[q][h]);
-#pragma unroll
-              for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(wk, f[e], acc[h][e]);
-            }
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(wk, f[e], acc[e]);
           }
+        }
       }
     }
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = 1.f / l;
+    const int64_t at = ((int64_t)(s.lo + i) * p.n_q + h) * HD + lane * PER;
+    if (!in_extent(at, PER, (int64_t)p.T * p.n_q * HD)) continue;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-      const float inv = 1.f / l[h];
-      const int64_t at = ((int64_t)(s.lo + i) * p.n_q + h0 + h) * HD + lane * PER;
-      if (h >= hn || !in_extent(at, PER, (int64_t)p.T * p.n_q * HD)) continue;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + at);
-#pragma unroll
-      for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[h][2 * e] * inv, acc[h][2 * e + 1] * inv);
-    }
+    for (int e = 0; e < PER / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   }
-}
-
-template <int HD>
-__global__ void __launch_bounds__(256, 4) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
-  const int n_split = p.head->n_split;
-  bool waited = false;
-  // four heads per warp when that leaves every warp some, else one head and more of its chunks at a time
-  if ((int64_t)n_split * p.n_q >= (int64_t)4 * 8 * gridDim.x) combine_rows<HD, 4, 1>(p, n_split, waited);
-  else combine_rows<HD, 1, 4>(p, n_split, waited);
   if (!waited) pdl_wait();   // every CTA of the merge outlives the attention: the next call may reuse the workspace
 }
 
@@ -1090,6 +1066,7 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   p.part_ml = reinterpret_cast<float2*>(ws);
   p.grid = std::min(num_sms, kMaxGrid);
   auto inverse = [](int64_t x) { return (unsigned)std::min<uint64_t>((1ull << 32) / (uint64_t)x, UINT32_MAX); };
+  p.inv_q = inverse(a.n_q);
   p.inv_kv = inverse(a.n_kv);
   p.inv_grid = inverse(p.grid);
   p.inv_pair = inverse(2 * tpt);
