@@ -206,15 +206,19 @@ __device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& 
   return d.live;
 }
 
-// Inclusive prefix sum over a warp.
-__device__ __forceinline__ int warp_scan(int v) {
+// Inclusive prefix sums over a warp of N integers per lane, their chains side by side.
+template <int N>
+__device__ __forceinline__ void warp_scan(int (&v)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+    int y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = __shfl_up_sync(0xffffffffu, v[i], o);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane >= o) v[i] += y[i];
   }
-  return v;
 }
 
 // What a lane, then a warp, adds up for one candidate: items left whole and pieces of the others, their
@@ -244,16 +248,19 @@ struct Estimate {
       if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * 2 * p.tpt);
     }
   }
-  __device__ __forceinline__ float time(const ChunkParams& p, bool some_whole) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+  // summed over the lanes, of which the first `lanes` hold something
+  __device__ __forceinline__ float time(const ChunkParams& p, bool some_whole, int lanes) {
+    for (int o = lanes > 16 ? 16 : lanes > 4 ? 8 : 2; o > 0; o >>= 1) {
+      const float y0 = __shfl_xor_sync(0xffffffffu, nu, o), y1 = __shfl_xor_sync(0xffffffffu, cu, o);
+      const float y2 = __shfl_xor_sync(0xffffffffu, rows, o);
       if (some_whole) {
-        nw += __shfl_xor_sync(0xffffffffu, nw, o);
-        cw += __shfl_xor_sync(0xffffffffu, cw, o);
+        const float y3 = __shfl_xor_sync(0xffffffffu, nw, o), y4 = __shfl_xor_sync(0xffffffffu, cw, o);
+        nw += y3;
+        cw += y4;
       }
-      nu += __shfl_xor_sync(0xffffffffu, nu, o);
-      cu += __shfl_xor_sync(0xffffffffu, cu, o);
-      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      nu += y0;
+      cu += y1;
+      rows += y2;
     }
     // (not negative, so ordered as their bits)
     if (some_whole) lw = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lw)));
@@ -290,7 +297,9 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
     nt_max = __reduce_max_sync(0xffffffffu, nt_max);
     if (table) {   // one sequence per thread
       const int own = mine.np > 1 ? mine.np : 0;
-      share = warp_scan(own);
+      int incl[1] = {own};
+      warp_scan(incl);
+      share = incl[0];
       if (b0 < b1) {
         shapes[b0] = shape4(mine);
         before[b0] = share - own;
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
       }
       if (rounds_whole > 0) base += shares[k];
     }
-    const float t0 = e0.time(p, false), t1 = rounds_whole > 0 ? e1.time(p, true) : INFINITY;
+    const float t0 = e0.time(p, false, p.B), t1 = rounds_whole > 0 ? e1.time(p, true, p.B) : INFINITY;
     if (lane == 0) {
       est[w] = t0;
       est[32 + w] = t1;
@@ -363,11 +372,12 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
     count(r);
   }
   if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
+  int incl[3] = {v[0], v[1], v[2]};
+  if (active) warp_scan(incl);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const int own = v[i], incl = active ? warp_scan(own) : 0;
-    if (lane == 31) sums[i][warp] = incl;
-    v[i] = incl - own;
+    if (lane == 31) sums[i][warp] = incl[i];
+    v[i] = incl[i] - v[i];
   }
   __syncthreads();
   const int n_units = __reduce_add_sync(0xffffffffu, lane < CP_WARPS ? sums[0][lane] : 0);
