@@ -7,10 +7,10 @@
 // One form for every mix of lengths, from one token against a long cache (bound by reading K and V
 // once) to long prompts (bound by the tensor cores):
 //   * A Q tile is 128 rows: (128 / r) consecutive tokens x the r query heads of one KV group.  An item is
-//     a pair of adjacent Q tiles of one (sequence, KV group), which share every K/V tile staged; a
-//     sequence's only or odd last Q tile is an item by itself.  Its key tiles then alternate between
-//     the two softmax groups (even tiles, odd tiles), each with its own O, merged at the end, so that
-//     the two groups still take turns with the tensor core.
+//     a pair of adjacent Q tiles of one (sequence, KV group), which share every K/V tile staged, or one Q
+//     tile: a sequence's only or odd last one, and every one of a batch too small to fill the SMs with pairs.
+//     A single tile's key tiles alternate between the two softmax groups (even tiles, odd tiles), each with
+//     its own O, merged at the end, so that the two groups still take turns with the tensor core.
 //   * chunk_plan_kernel cuts the items' key ranges into units: a sequence's tiles into n_chunk equal
 //     parts of at least one tile, as many as make the units come out even over the SMs (see there).
 //   * chunk_attn_kernel: one CTA per SM takes units from a counter.  Warp 0 fetches units and runs TMA
@@ -47,7 +47,8 @@ constexpr int kMaxGrid = 256;            // attention CTAs at most (one per SM; 
 struct ChunkSeq {
   int unit0;          // first unit
   int lo, n, c;       // first packed row, new tokens, cached positions
-  int np, wp;         // items per KV group (pairs of Q tiles); the last wp of them are not cut
+  int np, wp;         // items per KV group; the last wp of them are not cut
+  int span;           // tokens per item: two Q tiles' or one's
   int nc, ct;         // key chunks of the others and tiles per chunk
   int cut_n;          // tokens with partial rows (0 if nc = 1): those of the items that are cut
   int part0;          // first partial row: token i's in chunk k is part0 + k * cut_n + i
@@ -90,7 +91,7 @@ struct ChunkParams {   // 128-byte aligned by its tensor maps
   float* part_o;       // [part_rows, n_q, hd]
   float2* part_ml;     // [part_rows, n_q]  (m in log2 units, l)
   int part_rows, grid;
-  unsigned inv_q, inv_kv, inv_grid, inv_pair;   // floor(2^32 / x) of n_q, n_kv, grid and 2 tpt
+  unsigned inv_q, inv_kv, inv_grid, inv_pair, inv_tile;   // floor(2^32 / x) of n_q, n_kv, grid, 2 tpt and tpt
   unsigned* status;
 };
 
@@ -116,7 +117,11 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // ceil((c + n) / 128) key tiles or less.  With at most C tiles per unit a range is cut into nc =
 // ceil(nt / C).  Of the items that share their K and V with others of their sequence the first `whole`
 // (whole rounds of one per CTA, or none) are not cut, only what is left over after them; K and V that one
-// item reads alone are read once however it is cut.  (C, whole) is the candidate of least estimated time,
+// item reads alone are read once however it is cut.  With less than a round of items, items of one Q tile
+// are the other choice: twice the items, each tile of them kSingleTile of a pair's, its key tiles taken by
+// both groups in turn (32/8 heads x 128: 200 tokens 16.7 -> 14.6 us, 2 x 100 after 1000 25.8 -> 21.1, 4 x 64
+// after 500 22.6 -> 18.2; forced on 1500 tokens among 40 decodes, 107 against 99.6).  (C, whole or single) is
+// the candidate of least estimated time,
 // in units of one tile's time (1.4 us for a pair at hd 128).  A unit costs kUnitCost more than its tiles
 // (its pipeline fills and drains); one that leaves partials kCutCost, and kRowCost for 256 rows of them,
 // written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
@@ -128,7 +133,7 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // One CTA does this while all the others wait: a chain of dependent steps (loads, scans, estimate, scans,
 // records) of about 8000 cycles, whose length is what counts: divisions go through reciprocals (integer and
 // IEEE divisions cost 1.6 us of it), and 512 threads or a warm instruction cache change nothing.
-constexpr float kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost = 2.0f, kMergeCost = 2.0f;
+constexpr float kSingleTile = 0.62f, kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost = 2.0f, kMergeCost = 2.0f;
 constexpr int CP_SEQS = CP_THREADS;      // sequences whose shapes are kept in shared memory (one per thread)
 
 __device__ __forceinline__ float rcp(float x) {
@@ -185,12 +190,12 @@ __device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& 
   const bool uncut = item < s.wp;
   const int chunk = uncut || s.nc == 1 ? 0 : div_by(y, nq, rcp((float)nq));   // parts are bounded, so y is
   const int pair = uncut ? s.np - 1 - y : nq - 1 - (y - chunk * nq);
-  const int first = pair * 2 * p.tpt;                                       // token of the earlier Q tile
-  const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + 2 * p.tpt), 128);
+  const int first = pair * s.span;                                          // token of the earlier Q tile
+  const int nt1 = cdiv(s.c + min(s.n, first + p.tpt), 128), nt0 = cdiv(s.c + min(s.n, first + s.span), 128);
   const int t0 = chunk * s.ct, t1 = uncut ? nt0 : min(t0 + s.ct, nt0);
   d.live = t0 < t1;
   d.t0 = t0;
-  d.lone = s.n - first <= p.tpt;
+  d.lone = min(s.n - first, s.span) <= p.tpt;
   d.n0 = d.lone ? (t1 - t0 + 1) / 2 : t1 - t0;
   d.n1 = d.lone ? (t1 - t0) / 2 : max(0, min(t1, nt1) - t0);
   d.row1 = s.lo + first;
@@ -226,8 +231,9 @@ __device__ __forceinline__ void warp_scan(int (&v)[N]) {
 struct Estimate {
   float nw = 0.f, cw = 0.f, lw = 0.f, nu = 0.f, cu = 0.f, lu = 0.f;
   float rows = 0.f;   // exact below 2^24, beyond it too many
-  // v: (n, np, nt, tiles of the shortest item), cut in nc chunks of ct tiles but for wp items left whole
-  __device__ __forceinline__ void add(const ChunkParams& p, const int4& v, int nc, int ct, int wp) {
+  // v: (n, items, nt, tiles of the shortest item), cut in nc chunks of ct tiles but for wp items left whole;
+  // an item has `span` tokens, and a tile of it takes `tile`
+  __device__ __forceinline__ void add(const ChunkParams& p, const int4& v, int nc, int ct, int wp, int span, float tile) {
     const float n_kv = (float)p.n_kv, nt = (float)v.z, lo = (float)v.w;
     const float step = __fdividef(nt - lo, (float)max(v.y - 1, 1));
     if (wp > 0) {
@@ -240,12 +246,12 @@ struct Estimate {
       const float mean = 0.5f * (nt - step * (float)wp + lo);
       const float k = nc > 1 ? fmaxf(1.f, ceilf(__fdividef(mean, (float)ct) - 0.25f)) : 1.f;
       const float row_cost = kRowCost / 256.f * (float)p.r;
-      const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, 2 * p.tpt) : 0.f);
+      const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, span) : 0.f);
       const float items = (float)(v.y - wp) * n_kv;
       nu += items * k;
-      cu += items * (mean + k * over);
-      lu = fmaxf(lu, (float)min(ct, v.z) + over);
-      if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * 2 * p.tpt);
+      cu += items * (mean * tile + k * over);
+      lu = fmaxf(lu, (float)min(ct, v.z) * tile + over);
+      if (nc > 1) rows += (float)nc * (float)min(v.x, (v.y - wp) * span);
     }
   }
   // summed over the lanes, of which the first `lanes` hold something
@@ -292,8 +298,13 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
   auto shape = [&](int b) { return b == b0 ? mine : seq_shape(p, b, bad); };
   auto shape4 = [&](const SeqShape& s) { return make_int4(s.n, s.np, s.nt, (s.c + min(s.n, tpt2) + 127) >> 7); };
   int nt_max = 0, share = 0;
+  bool several_tiles = false;
   if (active) {
-    for (int b = b0; b < b1; ++b) nt_max = max(nt_max, shape(b).nt);
+    for (int b = b0; b < b1; ++b) {
+      const SeqShape s = shape(b);
+      nt_max = max(nt_max, s.nt);
+      several_tiles = several_tiles || s.n > p.tpt;
+    }
     nt_max = __reduce_max_sync(0xffffffffu, nt_max);
     if (table) {   // one sequence per thread
       const int own = mine.np > 1 ? mine.np : 0;
@@ -311,11 +322,14 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
     shares[warp] = share;
   }
   if (tid < 64) est[tid] = INFINITY;
-  __syncthreads();
+  const bool several = __syncthreads_or(several_tiles);   // a sequence of more than one Q tile
   nt_max = __reduce_max_sync(0xffffffffu, lane < CP_WARPS ? most[lane] : 0);
   // whole rounds of items that share their K and V with others, one per CTA (batches beyond the table: none)
   const int all = __reduce_add_sync(0xffffffffu, lane < CP_WARPS ? shares[lane] : 0) * p.n_kv;
   const int rounds_whole = div_inv(div_inv(all, p.grid, p.inv_grid) * p.grid, p.n_kv, p.inv_kv);
+  // with less than a round of them, items of one Q tile are looked at instead
+  const bool singles = rounds_whole == 0 && several;
+  auto tiles_of = [&](int n) { return div_inv(n + p.tpt - 1, p.tpt, p.inv_tile); };
   for (int w = warp; w < 32; w += CP_WARPS) {
     const int C_est = candidate(w);
     if (C_est >= nt_max && w != 31) continue;   // from the longest range on they all cut nothing
@@ -328,13 +342,16 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
         if (v.x > 0) {
           int nc, ct;
           cut(v.z, C_est, inv_C, nc, ct);
-          e0.add(p, v, nc, ct, 0);
-          if (rounds_whole > 0) e1.add(p, v, nc, ct, v.y > 1 ? min(max(rounds_whole - base - before[b], 0), v.y) : 0);
+          e0.add(p, v, nc, ct, 0, tpt2, 1.f);
+          if (rounds_whole > 0)
+            e1.add(p, v, nc, ct, v.y > 1 ? min(max(rounds_whole - base - before[b], 0), v.y) : 0, tpt2, 1.f);
+          else if (singles)
+            e1.add(p, make_int4(v.x, tiles_of(v.x), v.z, v.w), nc, ct, 0, p.tpt, v.x > p.tpt ? kSingleTile : 1.f);
         }
       }
       if (rounds_whole > 0) base += shares[k];
     }
-    const float t0 = e0.time(p, false, p.B), t1 = rounds_whole > 0 ? e1.time(p, true, p.B) : INFINITY;
+    const float t0 = e0.time(p, false, p.B), t1 = rounds_whole > 0 || singles ? e1.time(p, !singles, p.B) : INFINITY;
     if (lane == 0) {
       est[w] = t0;
       est[32 + w] = t1;
@@ -347,6 +364,7 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
   const unsigned least = __reduce_min_sync(0xffffffffu, bits);
   const int pick = __reduce_max_sync(0xffffffffu, bits == least ? lane + (second ? 32 : 0) : 0);
   const int C = candidate(pick & 31), whole = pick >= 32 ? rounds_whole : 0;
+  const int span = pick >= 32 && singles ? p.tpt : tpt2;
   const float inv = rcp((float)C);
   // ---- the sequences' records; prefix sums of (units, partial rows, cut tokens)
   const int share0 = __reduce_add_sync(0xffffffffu, lane < warp ? shares[lane] : 0);
@@ -354,9 +372,10 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
     const SeqShape s = shape(b);
     ChunkSeq r;
     cut(s.nt, C, inv, r.nc, r.ct);
-    r.lo = s.lo; r.n = s.n; r.c = s.c; r.np = s.np;
+    r.lo = s.lo; r.n = s.n; r.c = s.c; r.span = span;
+    r.np = span == tpt2 ? s.np : tiles_of(s.n);
     r.wp = whole && s.np > 1 ? min(max(whole - share0 - before[b], 0), s.np) : 0;
-    r.cut_n = r.nc > 1 ? min(s.n, (s.np - r.wp) * tpt2) : 0;
+    r.cut_n = r.nc > 1 ? min(s.n, (r.np - r.wp) * span) : 0;
     return r;
   };
   int v[3] = {0, 0, 0};
@@ -423,8 +442,9 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
       if (table) {
         const int4 a = shapes[lo], q = places[lo];
         cut(a.z, C, inv, r.nc, r.ct);
-        r.unit0 = unit0[lo]; r.lo = q.x; r.n = a.x; r.c = q.y; r.np = a.y; r.wp = q.w; r.part0 = q.z;
-        r.cut_n = r.nc > 1 ? min(a.x, (a.y - q.w) * tpt2) : 0;
+        r.unit0 = unit0[lo]; r.lo = q.x; r.n = a.x; r.c = q.y; r.wp = q.w; r.part0 = q.z; r.span = span;
+        r.np = span == tpt2 ? a.y : tiles_of(a.x);
+        r.cut_n = r.nc > 1 ? min(a.x, (r.np - q.w) * span) : 0;
       } else {
         r = p.seq[lo];
       }
@@ -1080,6 +1100,7 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   p.inv_kv = inverse(a.n_kv);
   p.inv_grid = inverse(p.grid);
   p.inv_pair = inverse(2 * tpt);
+  p.inv_tile = inverse(tpt);
   p.status = a.status;
   int dev = 0;
   cudaGetDevice(&dev);

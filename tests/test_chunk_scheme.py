@@ -27,21 +27,22 @@ def cut(nt, C):
     return max(1, cdiv(nt, ct)), ct
 
 
-def plan(cached, new, r, n_kv, C, rounds_whole):
+def plan(cached, new, r, n_kv, C, rounds_whole, tiles):
     """The sequences' records as the plan kernel leaves them."""
     tpt, out = 128 // r, []
     unit0 = part0 = split0 = before = lo = 0
     for c, n in zip(cached, new):
         if n == 0:
             c = 0
-        np_, nt = cdiv(n, 2 * tpt), cdiv(c + n, 128)
+        np_, nt = cdiv(n, tiles * tpt), cdiv(c + n, 128)
         nc, ct = cut(nt, C)
         wp = 0
         if np_ > 1:
             wp = min(max(rounds_whole - before, 0), np_)
             before += np_
-        cut_n = min(n, (np_ - wp) * 2 * tpt) if nc > 1 else 0
-        out.append(dict(unit0=unit0, lo=lo, n=n, c=c, np=np_, wp=wp, nc=nc, ct=ct, cut_n=cut_n, part0=part0, split0=split0))
+        cut_n = min(n, (np_ - wp) * tiles * tpt) if nc > 1 else 0
+        out.append(dict(unit0=unit0, lo=lo, n=n, c=c, np=np_, wp=wp, nc=nc, ct=ct, cut_n=cut_n, part0=part0, split0=split0,
+                        span=tiles * tpt))
         unit0 += (wp + nc * (np_ - wp)) * n_kv
         part0 += nc * cut_n
         split0 += cut_n
@@ -58,14 +59,14 @@ def make_unit(s, u, r, n_kv):
     y, nq = (item if uncut else item - s["wp"]), s["np"] - s["wp"]
     chunk = 0 if uncut or s["nc"] == 1 else y // nq
     pair = s["np"] - 1 - y if uncut else nq - 1 - (y - chunk * nq)
-    first = pair * 2 * tpt
+    first = pair * s["span"]
     nt1 = cdiv(s["c"] + min(s["n"], first + tpt), 128)
-    nt0 = cdiv(s["c"] + min(s["n"], first + 2 * tpt), 128)
+    nt0 = cdiv(s["c"] + min(s["n"], first + s["span"]), 128)
     t0 = chunk * s["ct"]
     t1 = nt0 if uncut else min(t0 + s["ct"], nt0)
     if t0 >= t1:
         return None
-    lone = s["n"] - first <= tpt
+    lone = min(s["n"] - first, s["span"]) <= tpt
     n0 = (t1 - t0 + 1) // 2 if lone else t1 - t0
     n1 = (t1 - t0) // 2 if lone else max(0, min(t1, nt1) - t0)
     row1 = s["lo"] + first
@@ -73,9 +74,9 @@ def make_unit(s, u, r, n_kv):
     return x - item * n_kv, t0, n0, n1, lone, (row1 if lone else row1 + tpt, row1), part
 
 
-def check_split(cached, new, r, n_kv, C, rounds_whole):
+def check_split(cached, new, r, n_kv, C, rounds_whole, tiles):
     tpt = 128 // r
-    seqs, n_units, n_parts, n_split = plan(cached, new, r, n_kv, C, rounds_whole)
+    seqs, n_units, n_parts, n_split = plan(cached, new, r, n_kv, C, rounds_whole, tiles)
     seen, parts = {}, {}
     for b, s in enumerate(seqs):
         end = seqs[b + 1]["unit0"] if b + 1 < len(seqs) else n_units
@@ -119,7 +120,8 @@ def test_every_tile_in_one_unit(seed):
     cached = [r.choice([0, r.randrange(0, 300), r.randrange(0, 3000)]) for _ in range(B)]
     items = sum(cdiv(n, 2 * (128 // ratio)) for n in new)
     for C in (1, 2, 3, 6, 11, 1 << 20):
-        check_split(cached, new, ratio, n_kv, C, r.choice([0, r.randrange(0, items + 2)]))
+        check_split(cached, new, ratio, n_kv, C, r.choice([0, r.randrange(0, items + 2)]), 2)
+        check_split(cached, new, ratio, n_kv, C, 0, 1)
 
 
 # ---------------------------------------------------------------------------------------- barriers
