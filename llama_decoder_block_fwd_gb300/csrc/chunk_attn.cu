@@ -20,7 +20,7 @@
 //   * chunk_combine_kernel merges the parts of the rows that were cut.
 // Measured (one call, plan and merge included): 2048 tokens after 30720, 32/8 heads x 128, 650-665 us = 1640
 // TFLOP/s (the attention kernel alone 1700, tensor pipe 72% active, its softmax warps' instructions in
-// the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 215 us, the attention
+// the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 211 us, the attention
 // kernel 200 = 6.4 TB/s; three single tokens 14.3 us (plan 5, attention 6, merge 2.5).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
 #include <algorithm>
@@ -125,10 +125,11 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // in units of one tile's time (1.4 us for a pair at hd 128).  A unit costs kUnitCost more than its tiles
 // (its pipeline fills and drains); one that leaves partials kCutCost, and kRowCost for 256 rows of them,
 // written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
-// others fill up to half of the longest one.  Replayed on a list scheduler over 70 mixes of lengths this
-// is within 1% of the best candidate on average.  C runs from 1 tile to all in steps of sqrt(2), one per
-// warp (those past the longest range cut nothing, like the last, and are skipped); candidates whose partials
-// do not fit the workspace are out, the last C (nothing cut) always fits.
+// others fill up to half of the longest one, and no round takes more than its longest.  Against the best of
+// all candidates, forced one by one on 39 mixes of lengths and heads, the choice is 2% slower on average
+// and 10% at most.  C runs from 1 tile to all in steps of sqrt(2), one per warp (those past the longest range
+// cut nothing, like the last, and are skipped); candidates whose partials do not fit the workspace are out,
+// the last C (nothing cut) always fits.
 //
 // One CTA does this while all the others wait: a chain of dependent steps (loads, scans, estimate, scans,
 // records) of about 8000 cycles, whose length is what counts: divisions go through reciprocals (integer and
@@ -244,7 +245,9 @@ struct Estimate {
     }
     if (v.y > wp) {
       const float mean = 0.5f * (nt - step * (float)wp + lo);
-      const float k = nc > 1 ? fmaxf(1.f, ceilf(__fdividef(mean, (float)ct) - 0.25f)) : 1.f;
+      // chunks that hold keys, on average over the items: their tiles are spread over lo .. nt
+      const float part = __fdividef(mean, (float)ct), spread = nt - step * (float)wp - lo;
+      const float k = nc > 1 ? fminf((float)nc, spread < (float)ct ? ceilf(part) : part + 0.5f) : 1.f;
       const float row_cost = kRowCost / 256.f * (float)p.r;
       const float over = kUnitCost + (nc > 1 ? kCutCost + row_cost * (float)min(v.x, span) : 0.f);
       const float items = (float)(v.y - wp) * n_kv;
@@ -273,7 +276,8 @@ struct Estimate {
     lu = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lu)));
     const float g = rcp((float)p.grid), mw = nw > 0.f ? __fdividef(cw, nw) : 0.f, mu = nu > 0.f ? __fdividef(cu, nu) : 0.f;
     const float e = lw <= 1.2f * mw && lu <= 1.2f * mu ? ceilf(nw * g - 0.01f) * mw + ceilf(nu * g - 0.01f) * mu
-                                                       : (cw + cu) * g + 0.5f * (nu > 0.f ? lu : lw);
+                                                       : fminf((cw + cu) * g + 0.5f * (nu > 0.f ? lu : lw),
+                                                               ceilf((nw + nu) * g - 0.01f) * fmaxf(lw, lu));
     return rows <= (float)p.part_rows ? fmaxf(e, fmaxf(lw, lu)) + (rows > 0.f ? kMergeCost : 0.f) : INFINITY;
   }
 };
@@ -455,6 +459,10 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------------------------- attention
+// Tiles before a unit's last copies at which its CTA takes the next one: late, so that what is left goes to
+// those who are done (taken at the unit's start: 1248 tokens of 32/4 heads 35 us against 29, 64 sequences of
+// 3-5 tokens 216 against 211, nine ragged prompts 19.5 against 17), but early enough to hide the look-up.
+constexpr int kAskTiles = 2;
 template <int HD>
 struct CaSmem {
   static constexpr uint32_t TILE = 128 * HD * 2;             // one Q, K or V tile
@@ -602,10 +610,6 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
           make_unit(p, p.seq[hint], hint, u, d);
         }
-        if (d.live && more) {       // the one after it is asked for now and looked at later
-          if (lane == 0) next = atomicAdd(&p.head->counter, 1);
-          asked = true;
-        }
         // ---- hand the unit over
         const int us = serial & 1;
         if (lane == 0) {
@@ -642,6 +646,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
         const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
         int page_reg = 0;
         for (int t = 0; ok && t < nt; ++t) {
+          if (more && t == max(0, nt - kAskTiles)) {   // the next unit is asked for now and looked at later
+            if (lane == 0) next = atomicAdd(&p.head->counter, 1);
+            asked = true;
+          }
           if ((t & 31) == 0) {
             page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
             if (page_reg < 0 || page_reg >= p.n_pages) {
@@ -949,11 +957,12 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * w0);
         }
         if (live && inside && store_part) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + c * 32);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.part_o + at * HD + c * 32);   // whole sectors: 32 bytes each
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]), __uint_as_float(v[4 * k + 2]),
-                                 __uint_as_float(v[4 * k + 3]));
+          for (int k = 0; k < 32; k += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + k), "r"(v[k]), "r"(v[k + 1]),
+                         "r"(v[k + 2]), "r"(v[k + 3]), "r"(v[k + 4]), "r"(v[k + 5]), "r"(v[k + 6]), "r"(v[k + 7])
+                         : "memory");
         } else if (live && inside) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + at * HD + c * 32);
 #pragma unroll
@@ -1091,6 +1100,7 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   ws += 256 + kMaxGrid * sizeof(ChunkUnit);
   p.seq = reinterpret_cast<ChunkSeq*>(ws);
   ws += round256((size_t)a.B * sizeof(ChunkSeq));
+  ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));   // 32-byte stores
   p.part_o = reinterpret_cast<float*>(ws);
   ws += round256((size_t)p.part_rows * a.n_q * HD * 4);
   p.part_ml = reinterpret_cast<float2*>(ws);
@@ -1136,7 +1146,8 @@ bool chunk_attn_supported(int64_t B, int64_t T, int64_t n_q, int64_t n_kv) {
 
 size_t chunk_attn_ws_bytes(int64_t B, int64_t T, int64_t n_q, int64_t, int64_t hd, int64_t max_pos) {
   const size_t rows = (size_t)part_rows_of(T, n_q, max_pos) * n_q;
-  return 256 + kMaxGrid * sizeof(ChunkUnit) + round256((size_t)B * sizeof(ChunkSeq)) + round256(rows * hd * 4) + round256(rows * 8);
+  return 256 + kMaxGrid * sizeof(ChunkUnit) + round256((size_t)B * sizeof(ChunkSeq)) + round256(rows * hd * 4) + 32 +
+         round256(rows * 8);
 }
 
 int launch_chunk_attn(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
