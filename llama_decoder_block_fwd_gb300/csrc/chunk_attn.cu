@@ -610,6 +610,10 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           hint += warp_search(p.B - hint, u, [&](int b) { return p.seq[hint + b].unit0; });
           make_unit(p, p.seq[hint], hint, u, d);
         }
+        // the page ids come 32 at a time, the first on their way while the unit is handed over
+        const int nt = d.lone ? d.n0 + d.n1 : d.n0;
+        const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
+        int page_reg = d.live && lane < nt ? __ldg(pages + lane) : 0;
         // ---- hand the unit over
         const int us = serial & 1;
         if (lane == 0) {
@@ -641,17 +645,14 @@ __global__ void __launch_bounds__(CA_THREADS, 1) chunk_attn_kernel(const __grid_
           if (ok) ++qi;
           ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        // ---- K and V tiles; the page ids come 32 at a time
-        const int nt = d.lone ? d.n0 + d.n1 : d.n0;
-        const int* pages = p.block_table + (int64_t)d.b * p.max_pages + d.t0;
-        int page_reg = 0;
+        // ---- K and V tiles
         for (int t = 0; ok && t < nt; ++t) {
           if (more && t == max(0, nt - kAskTiles)) {   // the next unit is asked for now and looked at later
             if (lane == 0) next = atomicAdd(&p.head->counter, 1);
             asked = true;
           }
           if ((t & 31) == 0) {
-            page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
+            if (t > 0) page_reg = t + lane < nt ? __ldg(pages + t + lane) : 0;
             if (page_reg < 0 || page_reg >= p.n_pages) {
               atomicOr(p.status, STATUS_BAD_PLAN);
               page_reg = p.n_pages;            // outside the tensor: the copy fills the tile with zeros
