@@ -19,7 +19,7 @@
 //     that holds all of its item's keys stores o; otherwise it leaves (m, l, O) in the workspace.
 //   * chunk_combine_kernel merges the parts of the rows that were cut.
 // Measured (one call, plan and merge included): 2048 tokens after 30720, 32/8 heads x 128, 650-665 us = 1640
-// TFLOP/s (the attention kernel alone 1700, tensor pipe 72% active, its softmax warps' instructions in
+// TFLOP/s (the attention kernel alone 1710, tensor pipe 73% active, its softmax warps' instructions in
 // the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 211 us, the attention
 // kernel 200 = 6.4 TB/s; three single tokens 14.3 us (plan 5, attention 6, merge 2.5).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
