@@ -362,8 +362,10 @@ int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const
  *   out_tokens [n_tokens] int32: the accepted drafts from the sequence's first row on, then the new
  *   token, then -1; rows from cu_new[B] on are left as they were
  *   ws: llama_workspace_bytes(LLAMA_OP_VERIFY_DRAFTS, dims with S = n_tokens, ..., vocab) bytes
- * The outputs may not overlap the inputs.  Equal scores go to the lower id.  Probabilities are formed in fp32.  A draft outside [0, vocab) is
- * rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.                           */
+ * The outputs may not overlap the inputs.  Equal scores go to the lower id.  Probabilities are formed in fp32 (good
+ * to a few 2^-20 of themselves), p_i - q_i as their difference or, where the new token's would be less than p_i / 64,
+ * from the logits' differences, so that it keeps its digits when the draft is close to the target.  A draft outside
+ * [0, vocab) is rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.             */
 int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, int64_t ld,
                         const float* draft_logits, int64_t draft_ld, float temperature,
                         const int32_t* cu_new, int64_t B, const int32_t* tokens, const float* u,

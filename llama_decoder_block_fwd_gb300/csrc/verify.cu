@@ -202,15 +202,39 @@ __device__ __forceinline__ int merge_argmax(const VerifyParams& p, const float2*
   return id == INT_MAX ? 0 : id;
 }
 
-// The better of two (score, id): the larger score, of equals the lower id.
-__device__ __forceinline__ void race_max(float& s, int& id, float os, int oid) {
-  if (os > s || (os == s && oid < id)) { s = os; id = oid; }
+// ---- the remainder p - q = p (1 - q / p)
+// Where the models are close, the difference of two fp32 probabilities is mostly their rounding.  So it is taken
+// from the logits there: log2(q / p) = c ((y - z) - (my - mz)) - log2(Sy / Sz), my, mz the rows' maxima and Sy,
+// Sz their sums, in which y - z and my - mz of close models are exact.
+constexpr float VF_CLOSE = 0x1p-6f;     // 1 - q / p of a winner below which the models are close
+constexpr float VF_SERIES = 0.25f;      // |log2(q / p)| below which 1 - q / p comes from a series
+
+__device__ __forceinline__ float log2_ratio(const VerifyParams& p, float z, float y, float shift) {
+  return __fmul_rn(__fsub_rn(__fsub_rn(y, z), shift), p.c);
+}
+// 2^t - 1 for |t| < VF_SERIES: the exponential series up to x^6 / 720 leaves 0.18^6 / 5040 = 7e-9 of it
+__device__ __forceinline__ float exp2_less_1(float t) {
+  const float x = t * 0.693147180559945f;
+  float s = fmaf(x, 1.f / 720.f, 1.f / 120.f);
+  s = fmaf(x, s, 1.f / 24.f);
+  s = fmaf(x, s, 1.f / 6.f);
+  s = fmaf(x, s, 0.5f);
+  s = fmaf(x, s, 1.f);
+  return x * s;
 }
 
-// What the race runs over: REST max(p - q, 0); NO_DRAFT p without the draft; ALL p.
-enum RaceKind : int { REST, NO_DRAFT, ALL };
+// The better of two (score, key), key = 2 id + mark: the larger score, of equals the lower id.
+constexpr unsigned kNone = UINT_MAX;
+__device__ __forceinline__ void race_max(float& s, unsigned& key, float os, unsigned okey) {
+  if (os > s || (os == s && okey < key)) { s = os; key = okey; }
+}
 
-// This CTA's share of the vocabulary: a thread's (best score, its lowest id); scores of 0 do not count.
+// What the race runs over: REST max(p - q, 0); CLOSE the same for models that are close; NO_DRAFT p without the
+// draft; ALL p.
+enum RaceKind : int { REST, CLOSE, NO_DRAFT, ALL };
+
+// This CTA's share of the vocabulary: a thread's (best score, its lowest id); scores of 0 do not count.  `lr` is
+// log2(Sy / Sz) (CLOSE); in REST the winner's key is marked where its p and q are close.
 // p_i / e_i bounds a score from above, so a token whose p_i is below top * e_i, top the CTA's best score so far
 // (less 2^-20, more than the quotients' errors), is out of the race: it needs one exponential and no
 // division in place of two and one (48 lookups of 128256 logits: 35.7 -> 33.1 us; with a draft distribution
@@ -219,26 +243,37 @@ enum RaceKind : int { REST, NO_DRAFT, ALL };
 // judged, give the CTA a score to start from.
 template <int KIND>
 __device__ __forceinline__ void race(const VerifyParams& p, const float* z, const float* y, const float* e, int d,
-                                     float2 sz, float2 sy, int cr, int P, unsigned* top, float& best, int& id) {
-  const bool vz = vf_aligned(z), vy = KIND == REST && vf_aligned(y), ve = vf_aligned(e);
+                                     float2 sz, float2 sy, float lr, int cr, int P, unsigned* top, float& best,
+                                     unsigned& key) {
+  constexpr bool DRAFT = KIND == REST || KIND == CLOSE;
+  const bool vz = vf_aligned(z), vy = DRAFT && vf_aligned(y), ve = vf_aligned(e);
   const int units = (p.V + 3) >> 2, step = P * VF_THREADS, first = cr * VF_THREADS + (int)threadIdx.x;
   best = 0.f;
-  id = INT_MAX;
+  key = kNone;
   auto weight = [&](float zi, int i) {
     const float w = __fmul_rn(vf_exp(p, zi, sz.x), sz.y);
     return KIND == NO_DRAFT && i == d ? 0.f : w;
   };
-  // both products rounded: fused into the difference, one of them would leave its rounding where p = q
-  auto rest = [&](float w, float yi) { return __fsub_rn(w, __fmul_rn(vf_exp(p, yi, sy.x), sy.y)); };
-  auto score = [&](float w, float ei, int i) {
-    const float s = __fdividef(w, ei);
-    if (w > 0.f && s > best) { best = s; id = i; }   // ids grow: an equal later one does not count
+  auto score = [&](float w, float zi, float yi, float ei, int i) {
+    float r = w;
+    if (KIND == CLOSE) {
+      const float t = log2_ratio(p, zi, yi, sy.x - sz.x) - lr;
+      if (fabsf(t) < VF_SERIES) r = -w * exp2_less_1(t);
+      else r = w - vf_exp(p, yi, sy.x) * sy.y;
+    } else if (KIND == REST) {   // both products rounded: fused, one of them would leave its rounding where p = q
+      r = __fsub_rn(w, __fmul_rn(vf_exp(p, yi, sy.x), sy.y));
+    }
+    const float s = __fdividef(r, ei);
+    if (r > 0.f && s > best) {   // ids grow: an equal later one does not count
+      best = s;
+      key = 2u * (unsigned)i + (KIND == REST && r < w * VF_CLOSE);
+    }
   };
   auto publish = [&]() {
     const unsigned m = __reduce_max_sync(0xffffffffu, __float_as_uint(best));
     if ((threadIdx.x & 31) == 0 && m > *(volatile unsigned*)top) atomicMax(top, m);
   };
-  constexpr int DEPTH = KIND == REST ? VF_RACE_REST : VF_RACE;
+  constexpr int DEPTH = DRAFT ? VF_RACE_REST : VF_RACE;
   float4 a[DEPTH], n[DEPTH], c[DEPTH];
   auto load = [&](int q0) {
 #pragma unroll
@@ -246,19 +281,19 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
       const int i = (q0 + j * step) * 4;
       a[j] = vf_load4(z, i, p.V, vz);
       n[j] = vf_load4(e, i, p.V, ve);
-      if (KIND == REST) c[j] = vf_load4(y, i, p.V, vy);
+      if (DRAFT) c[j] = vf_load4(y, i, p.V, vy);
     }
   };
   {
     const float4 z0 = vf_load4(z, first * 4, p.V, vz), e0 = vf_load4(e, first * 4, p.V, ve);
     float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (KIND == REST) y0 = vf_load4(y, first * 4, p.V, vy);
+    if (DRAFT) y0 = vf_load4(y, first * 4, p.V, vy);
     load(first + step);
     const float za[4] = {z0.x, z0.y, z0.z, z0.w}, ea[4] = {e0.x, e0.y, e0.z, e0.w}, ya[4] = {y0.x, y0.y, y0.z, y0.w};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const float w = weight(za[t], first * 4 + t);
-      score(KIND == REST ? rest(w, ya[t]) : w, ea[t], first * 4 + t);
+      score(w, za[t], ya[t], ea[t], first * 4 + t);
     }
     publish();
   }
@@ -271,12 +306,12 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
       const int i = (q0 + j * step) * 4;
       const float za[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, ea[4] = {n[j].x, n[j].y, n[j].z, n[j].w};
       float ya[4] = {0.f, 0.f, 0.f, 0.f};
-      if (KIND == REST) { ya[0] = c[j].x; ya[1] = c[j].y; ya[2] = c[j].z; ya[3] = c[j].w; }
+      if (DRAFT) { ya[0] = c[j].x; ya[1] = c[j].y; ya[2] = c[j].z; ya[3] = c[j].w; }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float w = weight(za[t], i + t);
         if (w > 0.f && !(w < low * ea[t])) {   // (a draw of 0 against an infinite score: NaN, and in)
-          score(KIND == REST ? rest(w, ya[t]) : w, ea[t], i + t);
+          score(w, za[t], ya[t], ea[t], i + t);
           low = fmaxf(low, best * (1.f - 0x1p-20f));
         }
       }
@@ -285,21 +320,109 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
   }
 }
 
+// What the CTAs of a cluster tell each other, per turn of the race.
+struct PickShared {
+  float wbest[VF_WARPS];
+  unsigned wkey[VF_WARPS];
+  float best[3][VF_CLUSTER];      // every CTA's best, written by that CTA
+  unsigned key[3][VF_CLUSTER];
+  float sum[VF_CLUSTER];
+  unsigned top[3];                // the best score so far
+};
+
+// The threads' best candidates -> the cluster's; the same for every CTA.
+__device__ __forceinline__ unsigned race_end(PickShared& sh, int turn, int cr, int P, float best, unsigned key) {
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    race_max(best, key, __shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, key, o));
+  if ((tid & 31) == 0) { sh.wbest[tid >> 5] = best; sh.wkey[tid >> 5] = key; }
+  __syncthreads();
+  if (tid < P) {   // to every CTA of the cluster, which after the barrier reads only its own memory
+    best = sh.wbest[0];
+    key = sh.wkey[0];
+    for (int k = 1; k < VF_WARPS; ++k) race_max(best, key, sh.wbest[k], sh.wkey[k]);
+    *cl.map_shared_rank(&sh.best[turn][cr], tid) = best;
+    *cl.map_shared_rank(&sh.key[turn][cr], tid) = key;
+  }
+  cl.sync();
+  best = 0.f;
+  key = kNone;
+  for (int r = 0; r < P; ++r) race_max(best, key, sh.best[turn][r], sh.key[turn][r]);
+  return key;
+}
+
+// log2(Sy / Sz) again, for models that are close: Sy / Sz 2^(c (my - mz)) - 1 = sum_i p_i (2^t_i - 1), t_i the
+// log2 ratio without the sums.  The terms are as small as the models' differences, and so is what they are off
+// by, where the sums as they stand are off by about 2^-23 of 1.  One more pass over the two rows, and a race after
+// it, which only a rejection between close models asks for.
+__device__ __forceinline__ float row_ratio(const VerifyParams& p, const float* z, const float* y, float2 sz, float2 sy,
+                                           int cr, int P, PickShared& sh) {
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cl = cg::this_cluster();
+  const bool vz = vf_aligned(z), vy = vf_aligned(y);
+  const float shift = sy.x - sz.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t i = 4 * (cr * VF_THREADS + (int)threadIdx.x); i < p.V; i += 4 * P * VF_THREADS) {
+    const float4 z4 = vf_load4(z, (int)i, p.V, vz), y4 = vf_load4(y, (int)i, p.V, vy);
+    const float za[4] = {z4.x, z4.y, z4.z, z4.w}, ya[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = vf_exp(p, za[k], sz.x) * sz.y, t = log2_ratio(p, za[k], ya[k], shift);
+      acc[k] += fabsf(t) < VF_SERIES ? w * exp2_less_1(t) : vf_exp(p, ya[k], sy.x) * sz.y - w;
+    }
+  }
+  float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) sh.wbest[warp] = s;
+  __syncthreads();
+  if (threadIdx.x < P) {
+    s = 0.f;
+    for (int k = 0; k < VF_WARPS; ++k) s += sh.wbest[k];
+    *cl.map_shared_rank(&sh.sum[cr], threadIdx.x) = s;
+  }
+  cl.sync();
+  s = 0.f;
+  for (int r = 0; r < P; ++r) s += sh.sum[r];
+  return log1pf(s) * 1.44269504088896f;
+}
+
+// What rarely follows the race of a rejected draft (kept out of the way of its registers): the remainder of close
+// models with their ratio found again (turn 1), then, where no p exceeds its q, p (turn 2).
+__device__ __noinline__ unsigned race_again(const VerifyParams& p, const float* z, const float* y, const float* e,
+                                            float2 sz, float2 sy, int cr, int P, PickShared& sh) {
+  float best;
+  unsigned key = kNone;
+  if (y) {
+    const float lr = row_ratio(p, z, y, sz, sy, cr, P, sh);
+    race<CLOSE>(p, z, y, e, -1, sz, sy, lr, cr, P, sh.top + 1, best, key);
+    key = race_end(sh, 1, cr, P, best, key);
+  }
+  if (key == kNone) {
+    race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top + 2, best, key);
+    key = race_end(sh, 2, cr, P, best, key);
+  }
+  return key;
+}
+
 __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(const __grid_constant__ VerifyParams p) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cl = cg::this_cluster();
   const int P = (int)cl.num_blocks(), cr = (int)cl.block_rank(), b = blockIdx.x / P;
-  __shared__ int stop_sh, top_sh, wid[VF_WARPS], cid[2][VF_CLUSTER];
+  __shared__ int stop_sh, top_sh;
+  __shared__ PickShared sh;
   __shared__ float2 sz_sh[VF_ROWS], sy_sh[VF_ROWS];
-  __shared__ float wbest[VF_WARPS], cbest[2][VF_CLUSTER];   // per turn, every CTA's best
-  __shared__ unsigned top[2];   // per turn, the best score so far
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cl.barrier_arrive();      // waited for before another CTA's memory is written: that CTA has started then
   // the caller's inputs may be read before the statistics are there
   const int lo = max(0, __ldg(p.cu + b)), hi = min(p.T, __ldg(p.cu + b + 1));
   if (tid == 0) {
     stop_sh = hi - 1;
-    top[0] = top[1] = 0;
+    sh.top[0] = sh.top[1] = sh.top[2] = 0;
   }
   __syncthreads();
   int row = lo + warp, d = -1;
@@ -381,33 +504,15 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
     const float* e = p.e + (int64_t)b * p.ld_e;
     const float2 sz = sz_sh[kept], sy = p.y && rejected ? sy_sh[kept] : sz;
     const int judged = rejected ? __ldg(p.tokens + stop + 1) : -1;
-    // The race over the remainder; over p when nothing was rejected, or (the second turn) when no p
-    // exceeds its q.  Every CTA of the cluster sees the same result.
-    for (int turn = 0; turn < 2; ++turn) {
-      float best;
-      int id;
-      if (!rejected || turn) race<ALL>(p, z, nullptr, e, -1, sz, sz, cr, P, top + turn, best, id);
-      else if (p.y) race<REST>(p, z, p.y + (int64_t)stop * p.ld_y, e, -1, sz, sy, cr, P, top + turn, best, id);
-      else race<NO_DRAFT>(p, z, nullptr, e, judged, sz, sz, cr, P, top + turn, best, id);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        race_max(best, id, __shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, id, o));
-      if (lane == 0) { wbest[warp] = best; wid[warp] = id; }
-      __syncthreads();
-      if (tid < P) {   // to every CTA of the cluster, which after the barrier reads only its own memory
-        best = wbest[0];
-        id = wid[0];
-        for (int k = 1; k < VF_WARPS; ++k) race_max(best, id, wbest[k], wid[k]);
-        *cl.map_shared_rank(&cbest[turn][cr], tid) = best;
-        *cl.map_shared_rank(&cid[turn][cr], tid) = id;
-      }
-      cl.sync();
-      best = 0.f;
-      id = INT_MAX;
-      for (int r = 0; r < P; ++r) race_max(best, id, cbest[turn][r], cid[turn][r]);
-      token = id == INT_MAX ? 0 : id;
-      if (!rejected || id != INT_MAX) break;
-    }
+    const float* y = p.y && rejected ? p.y + (int64_t)stop * p.ld_y : nullptr;
+    float best;
+    unsigned key;
+    if (!rejected) race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top, best, key);
+    else if (y) race<REST>(p, z, y, e, -1, sz, sy, 0.f, cr, P, sh.top, best, key);
+    else race<NO_DRAFT>(p, z, nullptr, e, judged, sz, sz, 0.f, cr, P, sh.top, best, key);
+    key = race_end(sh, 0, cr, P, best, key);
+    if (rejected && (key == kNone || (key & 1))) key = race_again(p, z, y, e, sz, sy, cr, P, sh);
+    token = key == kNone ? 0 : (int)(key >> 1);
   }
   if (cr != 0) return;
   if (tid == 0 && in_extent(b, 1, p.B)) p.n_acc[b] = stop - lo;

@@ -1,0 +1,90 @@
+"""Draft verification where the draft's distribution is close to the target's: the remainder p - q is then a
+small difference of nearly equal numbers, and its race is decided by digits that p and q alone do not hold."""
+import numpy as np
+import pytest
+
+import llama_decoder_block_fwd_gb300 as L
+from tests import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+# Relative error of a probability: an exponent of at most 40 formed to 2^-24, ex2 2^-22, a sum in a tree of
+# depth under 40, the quotient 2^-22.
+PROB = 40 * 2.0 ** -24 + 2.0 ** -22 + 40 * 2.0 ** -24 + 2.0 ** -22
+
+
+def _call(z, y, T, new, tokens, u, noise):
+    import torch
+    B, N, V = len(new), z.shape[0], z.shape[1]
+    d = lambda a, t: torch.from_numpy(np.ascontiguousarray(a.astype(t))).cuda()
+    n_acc, out = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (B, N))
+    dims = L.dims_of(B, N, 128, 1, 1, 128, 128, 1e4, 1e-5)
+    ws = torch.full((L.llama_workspace_bytes(L.OP_VERIFY_DRAFTS, dims, L.F32, vocab=V),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    L.llama_verify_drafts(d(z, np.float32), d(y, np.float32), T, d(np.concatenate([[0], np.cumsum(new)]), np.int32),
+                          d(tokens, np.int32), d(u, np.float32), d(noise, np.float32), n_acc, out, ws)
+    assert L.llama_get_device_status() == 0
+    return n_acc.cpu().numpy(), out.cpu().numpy()
+
+
+def _refused(B, V, off, seed):
+    """B sequences of one draft each, which the target does not allow at all: it is turned down whatever its
+    (small) weight in the draft model."""
+    rng = np.random.default_rng(seed)
+    z = (2.5 * rng.normal(size=(2 * B, V))).astype(np.float32)
+    y = (z + off * rng.normal(size=z.shape)).astype(np.float32)
+    tokens = rng.integers(0, V, 2 * B)
+    z[np.arange(0, 2 * B, 2), tokens[1::2]] = -np.inf
+    y[np.arange(0, 2 * B, 2), tokens[1::2]] = -12.0
+    return z, y, tokens, np.full(2 * B, 0.5), rng.exponential(size=(B, V)).astype(np.float32)
+
+
+def _winner(z, y, T, noise):
+    """The remainder's winner in 64 bits and whether the stated error leaves no other: the weight p (1 - q / p)
+    has p's relative error, and 1 - q / p = -expm1(x0 - log R), x0 = (y - z - (max y - max z)) / T, is off by a
+    share PROB of what x0 and R are made of (R - 1 = sum p expm1(x0)) where models are close, by 2 PROB else."""
+    z, y = z.astype(np.float64) / T, y.astype(np.float64) / T
+    p, q = R.softmax(z, 1.0), R.softmax(y, 1.0)
+    with np.errstate(invalid="ignore"):
+        x0 = np.where(p > 0, y - z - (y.max() - z.max()), 0.0)
+    rest = np.maximum(p - q, 0.0)
+    score = rest / noise
+    top = int(np.argmax(score))
+    if rest[top] < p[top] / 128:
+        off = 2 * PROB * (np.abs(x0) + np.sum(p * np.abs(np.expm1(np.minimum(x0, 1.0)))) + np.sum(q[p == 0]))
+    else:
+        off = 2 * PROB
+    err = 2 * PROB * score + np.minimum(off, 1.0) * p / noise
+    others = np.delete(score + err, top)
+    return top, score[top] - err[top] > others.max()
+
+
+@pytest.mark.parametrize("off", [1e-6, 1e-5, 1e-4, 1e-3, 0.02, 0.3])
+@pytest.mark.parametrize("V,T,B", [(4000, 1.0, 150), (4001, 0.7, 40), (32000, 1.0, 60), (1000, 3.0, 700)])
+def test_remainder_of_close_models(V, T, B, off):
+    z, y, tokens, u, noise = _refused(B, V, off, seed=int(V + 1e6 * off))
+    n_acc, out = _call(z, y, T, [2] * B, tokens, u, noise)
+    assert (n_acc == 0).all()
+    want = [_winner(z[2 * b], y[2 * b], T, noise[b].astype(np.float64)) for b in range(B)]
+    clear = [b for b in range(B) if want[b][1]]
+    assert len(clear) >= 0.9 * B
+    wrong = [(b, want[b][0], int(out[2 * b])) for b in clear if out[2 * b] != want[b][0]]
+    assert not wrong, f"{len(wrong)} of {len(clear)}: {wrong[:4]}"
+
+
+@pytest.mark.parametrize("shift", [0.0, 1.0, -64.0])
+def test_models_that_differ_by_a_constant(shift):
+    """Logits that differ by a constant are one distribution: nothing remains, and the token is drawn from p."""
+    B, V = 30, 3000
+    rng = np.random.default_rng(3)
+    z = (np.round(rng.normal(size=(2 * B, V)) * 2.5 * 1024) / 1024).astype(np.float32)
+    tokens = rng.integers(0, V, 2 * B)
+    z[np.arange(0, 2 * B, 2), tokens[1::2]] = -np.inf
+    y, u, noise = z + np.float32(shift), np.full(2 * B, 0.5), rng.exponential(size=(B, V)).astype(np.float32)
+    n_acc, out = _call(z, y, 1.0, [2] * B, tokens, u, noise)
+    assert (n_acc == 0).all()
+    for b in range(B):
+        score = R.softmax(z[2 * b], 1.0) / noise[b].astype(np.float64)
+        best = np.sort(score)[-2:]
+        if best[1] > best[0] * (1 + 4 * PROB):
+            assert out[2 * b] == int(np.argmax(score))
