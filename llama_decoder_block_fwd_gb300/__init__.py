@@ -321,6 +321,13 @@ def _matrix(where, name, t, dtype, dev, rows, width):
     return t.data_ptr(), s0 if rows > 1 else width
 
 
+def _scratch(where, ws, dev):
+    """(address, bytes) of a workspace: a contiguous tensor of any type on device `dev`; None, 0 for None."""
+    if ws is None:
+        return None, 0
+    return _arg(where, "ws", ws, ws.dtype, dev), ws.numel() * ws.element_size()
+
+
 def _here(stream):
     """(library, torch, current device, stream address) for one call."""
     import torch
@@ -377,7 +384,7 @@ def llama_gqa_attention_chunk_paged(dims, q, k_pool, v_pool, block_table, cu_new
         ctypes.byref(d), _arg(w, "q", q, bf16, dev, rows), _arg(w, "k_pool", k_pool, bf16, dev, pool),
         _arg(w, "v_pool", v_pool, bf16, dev, pool), n_pages, _arg(w, "block_table", block_table, i32, dev, (B, P)), P,
         _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), _arg(w, "n_cached", n_cached, i32, dev, (B,)), max_pos,
-        _arg(w, "o", o, bf16, dev, rows), _p(ws), _nbytes(ws), st), w)
+        _arg(w, "o", o, bf16, dev, rows), *_scratch(w, ws, dev), st), w)
 
 
 def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, noise, n_accepted, out_tokens, ws,
@@ -396,8 +403,8 @@ def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, no
     _check(L.llama_verify_drafts(
         z, T, V, ldz, y, ldy, temperature, _arg(w, "cu_new", cu_new, i32, dev, (B + 1,)), B,
         _arg(w, "tokens", tokens, i32, dev), _arg(w, "u", u, f32, dev, (T,)), e, lde,
-        _arg(w, "n_accepted", n_accepted, i32, dev), _arg(w, "out_tokens", out_tokens, i32, dev, (T,)), _p(ws), _nbytes(ws),
-        st), w)
+        _arg(w, "n_accepted", n_accepted, i32, dev), _arg(w, "out_tokens", out_tokens, i32, dev, (T,)),
+        *_scratch(w, ws, dev), st), w)
 
 
 def llama_workspace_bytes(op, dims, dtype, n_layers=0, vocab=0, kv_capacity=0) -> int:
