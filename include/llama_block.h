@@ -314,9 +314,9 @@ int llama_paged_plan(const int32_t* n_cached, const int32_t* n_new, int64_t B, c
  *   projection's output; q_out [S, n_q, hd], contiguous (q itself is allowed when q_stride is
  *   n_q * hd); k_pool, v_pool [n_pages, 128, n_kv, hd]; positions and slots [S] int32.
  * q and q_out may both be NULL (append only), as may k, v, k_pool and v_pool (rotate only).  No two rows
- * may name the same slot.  Positions must be in [0, 2^24) and slots below 128 * n_pages: a row that
- * breaks this is skipped and latches LLAMA_ERR_INVALID_ARG in the device status word.  Uses S, n_q,
- * n_kv, head_dim (a multiple of 8, at most 256) and theta_base.  bf16 only.                       */
+ * may name the same slot.  Positions must be in [0, 2^24) and, where there are pools, slots below
+ * 128 * n_pages: a row that breaks this is skipped and latches LLAMA_ERR_INVALID_ARG in the device status
+ * word.  Uses S, n_q, n_kv, head_dim (a multiple of 8, at most 256) and theta_base.  bf16 only.    */
 int llama_rope_append_paged(const llama_dims* dims, const void* q, int64_t q_stride, const void* k,
                             int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
                             const int32_t* slots, void* q_out, void* k_pool, void* v_pool, int64_t n_pages,

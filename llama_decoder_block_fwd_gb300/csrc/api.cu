@@ -1225,7 +1225,7 @@ int llama_rope_append_paged(const llama_dims* d, const void* q, int64_t q_stride
   prof::begin("rope_append_paged", st);
   // without a pool a row is live when its slot is not negative, whatever its value
   rc = launch_rope_append(q, q_stride, k, k_stride, v, v_stride, positions, slots, q_out, k_pool, v_pool, d->S, d->n_q,
-                          d->n_kv, (int)d->head_dim, k ? n_pages : INT32_MAX / 128, f, num_sms(), status, st);
+                          d->n_kv, (int)d->head_dim, k ? n_pages : (int64_t)1 << 24, f, num_sms(), status, st);
   prof::end(st);
   return rc ? LLAMA_ERR_CUDA : launch_status();
 }
