@@ -277,10 +277,10 @@ int llama_gqa_attention_decode_paged(const llama_dims* dims, const void* q, cons
  * a prompt, one token, or the last accepted token and the drafts behind it).  The new tokens are
  * packed one sequence after the other: sequence b owns rows cu_new[b] .. cu_new[b+1]-1 of every
  * per-token array.  In these calls' llama_dims B is the number of sequences and S the number of
- * packed rows over all of them; rows from cu_new[B] on belong to no sequence and are left as they
- * were, so that a captured step can run with fewer tokens than it has room for.  llama_paged_plan
- * says where each token goes, llama_rope_append_paged puts it there, llama_gqa_attention_chunk_paged
- * attends, llama_verify_drafts judges drafts.                                                    */
+ * packed rows over all of them; rows from cu_new[B] on belong to no sequence and their outputs are left
+ * as they were (but for the plan's positions and slots, which say so), so that a captured step can run with
+ * fewer tokens than it has room for.  llama_paged_plan says where each token goes, llama_rope_append_paged
+ * puts it there, llama_gqa_attention_chunk_paged attends, llama_verify_drafts judges drafts.     */
 
 /* Block tables and slot maps from the requests' lengths, on the device.
  *   n_cached [B]     positions sequence b already holds (in its first ceil(n_cached / 128) pages)
@@ -293,9 +293,9 @@ int llama_gqa_attention_decode_paged(const llama_dims* dims, const void* q, cons
  *                    pool seen as [n_pages * 128] rows (128 * page + position % 128); -1 in both for
  *                    rows from cu_new[B] on
  *   pages_used [1]   out: pages needed from the free list
- * All int32 device arrays, 4-byte aligned; none may overlap another.  Needs B <= 8192, n_pages <=
- * 2^24 - 1, max_pages <= 2^17, n_tokens < 2^30 (else LLAMA_ERR_UNSUPPORTED).  LLAMA_ERR_INVALID_ARG for negative
- * counts, n_pages < 1, max_pages < 1 or NULL arrays.  Found on the device, and latched as
+ * All int32 device arrays, 4-byte aligned (else LLAMA_ERR_ALIGNMENT); none may overlap another.  Needs B <=
+ * 8192, n_pages < 2^24, max_pages <= 2^17, n_tokens < 2^30, n_free < 2^31 (else LLAMA_ERR_UNSUPPORTED).
+ * LLAMA_ERR_INVALID_ARG for negative counts, n_pages < 1, max_pages < 1 or NULL arrays.  Found on the device, and latched as
  * LLAMA_ERR_INVALID_ARG in the device status word: a negative length or n_cached + n_new > 128 *
  * max_pages (the sequence then brings no tokens), more new tokens than n_tokens (cu_new stops there),
  * pages_used > n_free (block_table keeps its old entries past the free list, the tokens without a
@@ -316,7 +316,11 @@ int llama_paged_plan(const int32_t* n_cached, const int32_t* n_new, int64_t B, c
  * q and q_out may both be NULL (append only), as may k, v, k_pool and v_pool (rotate only).  No two rows
  * may name the same slot.  Positions must be in [0, 2^24) and, where there are pools, slots below
  * 128 * n_pages: a row that breaks this is skipped and latches LLAMA_ERR_INVALID_ARG in the device status
- * word.  Uses S, n_q, n_kv, head_dim (a multiple of 8, at most 256) and theta_base.  bf16 only.    */
+ * word.  Uses S, n_q, n_kv, head_dim and theta_base.  bf16 only.
+ * LLAMA_ERR_UNSUPPORTED for head_dim above 256 or no multiple of 8, n_q or n_kv above 4096, S >= 2^31 - 8, n_pages
+ * >= 2^24; LLAMA_ERR_INVALID_ARG for other bad dims, strides below the row's width, n_pages < 1 with pools, one of
+ * a group of pointers NULL; LLAMA_ERR_ALIGNMENT for strides that are no multiples of 8, bf16 arrays not 16-byte
+ * or integer arrays not 4-byte aligned.                                                          */
 int llama_rope_append_paged(const llama_dims* dims, const void* q, int64_t q_stride, const void* k,
                             int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
                             const int32_t* slots, void* q_out, void* k_pool, void* v_pool, int64_t n_pages,
@@ -333,8 +337,12 @@ int llama_rope_append_paged(const llama_dims* dims, const void* q, int64_t q_str
  * Sequences may bring any number of tokens, none included; pages may be shared between sequences.  o may
  * not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
  * Pool rows past a sequence's last position are never used, whatever they hold, and a key or value a
- * query does not see never reaches it, infinite or NaN values included.  bf16, head_dim 64 or 128,
- * n_q / n_kv <= 128, n_pages < 2^24 (else LLAMA_ERR_UNSUPPORTED).  Found on the device and latched as
+ * query does not see never reaches it, infinite or NaN values included.
+ * LLAMA_ERR_UNSUPPORTED unless head_dim is 64 or 128, n_q / n_kv <= 128, n_q <= 65536, n_pages < 2^24, max_pages <
+ * 2^31, S < 2^30, B < 2^23 and (S / (2 floor(128 n_kv / n_q)) + B) n_kv <= 2^28 (whole quotients);
+ * LLAMA_ERR_INVALID_ARG for other bad dims, n_pages < 1, max_pages < 1, max_pos < 0, max_pos >= 128 * max_pages or
+ * 2^24, NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte or others not 16-byte aligned;
+ * LLAMA_ERR_WORKSPACE for a workspace that is too small.  Found on the device and latched as
  * LLAMA_ERR_INVALID_ARG in the device status word: a page id outside [0, n_pages) among the entries a
  * sequence uses, or a position above max_pos (the outputs of that sequence are then undefined; no
  * other memory is touched).                                                                       */
@@ -357,7 +365,8 @@ int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const
  * the argmax of z and the new token is the argmax (draft_logits, u and noise are not read).
  *   logits [n_tokens, ld], draft_logits [n_tokens, draft_ld] fp32, first `vocab` entries used: finite
  *   values or -inf, at least one finite per row; the last row of a sequence in draft_logits is not read
- *   cu_new [B + 1] int32; tokens [n_tokens] int32, the packed new tokens; u [n_tokens], noise [B, noise_ld] fp32
+ *   cu_new [B + 1] int32 (non-decreasing from 0, at most n_tokens); tokens [n_tokens] int32, the packed new tokens;
+ *   u [n_tokens], noise [B, noise_ld] fp32
  *   n_accepted [B] int32: accepted drafts; 0 for a sequence without rows
  *   out_tokens [n_tokens] int32: the accepted drafts from the sequence's first row on, then the new
  *   token, then -1; rows from cu_new[B] on are left as they were
@@ -365,7 +374,11 @@ int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const
  * The outputs may not overlap the inputs.  Equal scores go to the lower id.  Probabilities are formed in fp32 (good
  * to a few 2^-20 of themselves), p_i - q_i as their difference or, where the new token's would be less than p_i / 64,
  * from the logits' differences, so that it keeps its digits when the draft is close to the target.  A draft outside
- * [0, vocab) is rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.             */
+ * [0, vocab) is rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.
+ * LLAMA_ERR_UNSUPPORTED for n_tokens * ceil(vocab / 1024) >= 2^29, n_tokens >= 2^31 or B >= 2^27;
+ * LLAMA_ERR_INVALID_ARG for negative counts, vocab < 1 or > 2^30 (as llama_sample), a row stride below vocab, a NaN
+ * temperature or NULL arrays; LLAMA_ERR_ALIGNMENT for arrays not 4-byte aligned or ws not 16-byte aligned;
+ * LLAMA_ERR_WORKSPACE for a workspace that is too small.                                         */
 int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, int64_t ld,
                         const float* draft_logits, int64_t draft_ld, float temperature,
                         const int32_t* cu_new, int64_t B, const int32_t* tokens, const float* u,
