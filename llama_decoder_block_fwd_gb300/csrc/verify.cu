@@ -458,16 +458,21 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
       ok = merge_argmax(p, p.stat_z + (int64_t)row * p.parts) == d;
     } else {
       const float2 sz = merge_parts(p, p.stat_z + (int64_t)row * p.parts);
-      float qd = 1.f, pd = 0.f;
+      // u q < p with both sides scaled by the larger exponent, so that it does not depend on how small both are
+      // (a p below 2^-1074 is 0, as in 64 bits: a logit masked with the type's lowest value)
+      const float xz = (zd - sz.x) * p.c;
+      float qd = 1.f, scale = 0.f;
       if (p.y) {
         const float2 sy = merge_parts(p, p.stat_y + (int64_t)row * p.parts);
-        if (real) qd = vf_exp(p, yd, sy.x) * sy.y;
+        const float xy = (yd - sy.x) * p.c;
+        scale = fmaxf(xz, xy);
+        qd = vf_ex2(xy - scale) * sy.y;
         if (lane == 0 && row - lo < VF_ROWS) sy_sh[row - lo] = sy;
       }
       if (lane == 0 && row - lo < VF_ROWS) sz_sh[row - lo] = sz;
-      if (real) pd = vf_exp(p, zd, sz.x) * sz.y;
       u = (u >= 0.f) ? fminf(u, 0.99999994f) : 0.f;
-      ok = (double)u * (double)qd < (double)pd;   // the product is exact
+      ok = xz > -1074.f &&
+           (u == 0.f || (double)u * (double)qd < (double)(vf_ex2(xz - scale) * sz.y));   // the left product is exact
     }
     if (lane == 0) {
       if (!real && cr == 0) atomicOr(p.status, STATUS_BAD_TOKEN);

@@ -88,3 +88,32 @@ def test_models_that_differ_by_a_constant(shift):
         best = np.sort(score)[-2:]
         if best[1] > best[0] * (1 + 4 * PROB):
             assert out[2 * b] == int(np.argmax(score))
+
+
+@pytest.mark.parametrize("T", [1.0, 0.3, 2.5])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_drafts_of_weights_below_the_least_normal_number(T, drafts):
+    """Whether u q < p does not depend on how small both are, nor u = 0 on how small p is."""
+    B, V = 400, 50
+    rng = np.random.default_rng(5)
+    z = rng.normal(size=(2 * B, V)).astype(np.float32)
+    y = rng.normal(size=(2 * B, V)).astype(np.float32)
+    tokens, u = rng.integers(0, V, 2 * B), rng.random(2 * B).astype(np.float32)
+    low = rng.uniform(60, 300, B).astype(np.float32) * np.float32(T)
+    row, d = np.arange(0, 2 * B, 2), tokens[1::2]
+    z[row, d], y[row, d] = -low, -low + T * rng.normal(size=B).astype(np.float32)
+    u[row[::5]] = 0.0
+    off = np.arange(0, B, 9)                                 # not allowed by the target, nor (some) by the draft
+    z[row[off], d[off]] = rng.choice([-np.inf, np.finfo(np.float32).min], off.size)
+    y[row[off[::2]], d[off[::2]]] = np.finfo(np.float32).min
+    noise = rng.exponential(size=(B, V)).astype(np.float32)
+    n_acc, _ = _call(z, y if drafts else None, T, [2] * B, tokens, u, noise)
+    compared = 0
+    for b in range(B):
+        r = 2 * b
+        want, _, margin = R.verify(z[r:r + 2], y[r:r + 2] if drafts else None, T, tokens[r:r + 2], u[r:r + 2], noise[b])
+        # exponents of up to 440 (300 / ln 2) formed to 2^-24 on both sides, besides the rest
+        if u[r] == 0 or margin > 2 * (440 * 2.0 ** -24 + PROB):
+            compared += 1
+            assert n_acc[b] == want, (b, float(low[b]), float(u[r]))
+    assert compared > 0.95 * B
