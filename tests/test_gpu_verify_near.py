@@ -16,7 +16,7 @@ PROB = 40 * 2.0 ** -24 + 2.0 ** -22 + 40 * 2.0 ** -24 + 2.0 ** -22
 def _call(z, y, T, new, tokens, u, noise):
     import torch
     B, N, V = len(new), z.shape[0], z.shape[1]
-    d = lambda a, t: torch.from_numpy(np.ascontiguousarray(a.astype(t))).cuda()
+    d = lambda a, t: None if a is None else torch.from_numpy(np.ascontiguousarray(a.astype(t))).cuda()
     n_acc, out = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (B, N))
     dims = L.dims_of(B, N, 128, 1, 1, 128, 128, 1e4, 1e-5)
     ws = torch.full((L.llama_workspace_bytes(L.OP_VERIFY_DRAFTS, dims, L.F32, vocab=V),), 0xFF, dtype=torch.uint8,
