@@ -207,6 +207,8 @@ __device__ __forceinline__ int merge_argmax(const VerifyParams& p, const float2*
 // from the logits there: log2(q / p) = c ((y - z) - (my - mz)) - log2(Sy / Sz), my, mz the rows' maxima and Sy,
 // Sz their sums, in which y - z and my - mz of close models are exact.
 constexpr float VF_CLOSE = 0x1p-6f;     // 1 - q / p of a winner below which the models are close
+constexpr float VF_PEAK = 0x1p-13f;     // and so they are where its score is less than this of the largest p / e: what
+                                        // that token's p - q is off by could be as large
 constexpr float VF_SERIES = 0.25f;      // |log2(q / p)| below which 1 - q / p comes from a series
 
 __device__ __forceinline__ float log2_ratio(const VerifyParams& p, float z, float y, float shift) {
@@ -234,7 +236,8 @@ __device__ __forceinline__ void race_max(float& s, unsigned& key, float os, unsi
 enum RaceKind : int { REST, CLOSE, NO_DRAFT, ALL };
 
 // This CTA's share of the vocabulary: a thread's (best score, its lowest id); scores of 0 do not count.  `lr` is
-// log2(Sy / Sz) (CLOSE); in REST the winner's key is marked where its p and q are close.
+// log2(Sy / Sz) (CLOSE); in REST the winner's key is marked where its p and q are close, and `peak` is the largest
+// p / e of the tokens that are judged (all those above the best score).
 // p_i / e_i bounds a score from above, so a token whose p_i is below top * e_i, top the CTA's best score so far
 // (less 2^-20, more than the quotients' errors), is out of the race: it needs one exponential and no
 // division in place of two and one (48 lookups of 128256 logits: 35.7 -> 33.1 us; with a draft distribution
@@ -244,11 +247,11 @@ enum RaceKind : int { REST, CLOSE, NO_DRAFT, ALL };
 template <int KIND>
 __device__ __forceinline__ void race(const VerifyParams& p, const float* z, const float* y, const float* e, int d,
                                      float2 sz, float2 sy, float lr, int cr, int P, unsigned* top, float& best,
-                                     unsigned& key) {
+                                     unsigned& key, float& peak) {
   constexpr bool DRAFT = KIND == REST || KIND == CLOSE;
   const bool vz = vf_aligned(z), vy = DRAFT && vf_aligned(y), ve = vf_aligned(e);
   const int units = (p.V + 3) >> 2, step = P * VF_THREADS, first = cr * VF_THREADS + (int)threadIdx.x;
-  best = 0.f;
+  best = peak = 0.f;
   key = kNone;
   auto weight = [&](float zi, int i) {
     const float w = __fmul_rn(vf_exp(p, zi, sz.x), sz.y);
@@ -263,6 +266,7 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
     } else if (KIND == REST) {   // both products rounded: fused, one of them would leave its rounding where p = q
       r = __fsub_rn(w, __fmul_rn(vf_exp(p, yi, sy.x), sy.y));
     }
+    if (KIND == REST) peak = fmaxf(peak, __fdividef(w, ei));   // (0 / 0 is left out)
     const float s = __fdividef(r, ei);
     if (r > 0.f && s > best) {   // ids grow: an equal later one does not count
       best = s;
@@ -324,21 +328,28 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
 struct PickShared {
   float wbest[VF_WARPS];
   unsigned wkey[VF_WARPS];
+  float wpeak[VF_WARPS];
   float best[3][VF_CLUSTER];      // every CTA's best, written by that CTA
   unsigned key[3][VF_CLUSTER];
-  float sum[VF_CLUSTER];
+  float sum[VF_CLUSTER], peak[VF_CLUSTER];
   unsigned top[3];                // the best score so far
 };
 
-// The threads' best candidates -> the cluster's; the same for every CTA.
-__device__ __forceinline__ unsigned race_end(PickShared& sh, int turn, int cr, int P, float best, unsigned key) {
+// The threads' best candidates -> the cluster's; the same for every CTA.  With PEAK the largest `peak` too.
+template <bool PEAK>
+__device__ __forceinline__ unsigned race_end(PickShared& sh, int turn, int cr, int P, float& best, unsigned key, float& peak) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     race_max(best, key, __shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, key, o));
-  if ((tid & 31) == 0) { sh.wbest[tid >> 5] = best; sh.wkey[tid >> 5] = key; }
+  if (PEAK) peak = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(peak)));
+  if ((tid & 31) == 0) {
+    sh.wbest[tid >> 5] = best;
+    sh.wkey[tid >> 5] = key;
+    if (PEAK) sh.wpeak[tid >> 5] = peak;
+  }
   __syncthreads();
   if (tid < P) {   // to every CTA of the cluster, which after the barrier reads only its own memory
     best = sh.wbest[0];
@@ -346,11 +357,18 @@ __device__ __forceinline__ unsigned race_end(PickShared& sh, int turn, int cr, i
     for (int k = 1; k < VF_WARPS; ++k) race_max(best, key, sh.wbest[k], sh.wkey[k]);
     *cl.map_shared_rank(&sh.best[turn][cr], tid) = best;
     *cl.map_shared_rank(&sh.key[turn][cr], tid) = key;
+    if (PEAK) {
+      for (int k = 0; k < VF_WARPS; ++k) peak = fmaxf(peak, sh.wpeak[k]);
+      *cl.map_shared_rank(&sh.peak[cr], tid) = peak;
+    }
   }
   cl.sync();
   best = 0.f;
   key = kNone;
-  for (int r = 0; r < P; ++r) race_max(best, key, sh.best[turn][r], sh.key[turn][r]);
+  for (int r = 0; r < P; ++r) {
+    race_max(best, key, sh.best[turn][r], sh.key[turn][r]);
+    if (PEAK) peak = fmaxf(peak, sh.peak[r]);
+  }
   return key;
 }
 
@@ -395,16 +413,16 @@ __device__ __forceinline__ float row_ratio(const VerifyParams& p, const float* z
 // models with their ratio found again (turn 1), then, where no p exceeds its q, p (turn 2).
 __device__ __noinline__ unsigned race_again(const VerifyParams& p, const float* z, const float* y, const float* e,
                                             float2 sz, float2 sy, int cr, int P, PickShared& sh) {
-  float best;
+  float best, peak;
   unsigned key = kNone;
   if (y) {
     const float lr = row_ratio(p, z, y, sz, sy, cr, P, sh);
-    race<CLOSE>(p, z, y, e, -1, sz, sy, lr, cr, P, sh.top + 1, best, key);
-    key = race_end(sh, 1, cr, P, best, key);
+    race<CLOSE>(p, z, y, e, -1, sz, sy, lr, cr, P, sh.top + 1, best, key, peak);
+    key = race_end<false>(sh, 1, cr, P, best, key, peak);
   }
   if (key == kNone) {
-    race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top + 2, best, key);
-    key = race_end(sh, 2, cr, P, best, key);
+    race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top + 2, best, key, peak);
+    key = race_end<false>(sh, 2, cr, P, best, key, peak);
   }
   return key;
 }
@@ -510,13 +528,13 @@ __global__ void __launch_bounds__(VF_THREADS, VF_PICK_CTAS) verify_pick_kernel(c
     const float2 sz = sz_sh[kept], sy = p.y && rejected ? sy_sh[kept] : sz;
     const int judged = rejected ? __ldg(p.tokens + stop + 1) : -1;
     const float* y = p.y && rejected ? p.y + (int64_t)stop * p.ld_y : nullptr;
-    float best;
+    float best, peak;
     unsigned key;
-    if (!rejected) race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top, best, key);
-    else if (y) race<REST>(p, z, y, e, -1, sz, sy, 0.f, cr, P, sh.top, best, key);
-    else race<NO_DRAFT>(p, z, nullptr, e, judged, sz, sz, 0.f, cr, P, sh.top, best, key);
-    key = race_end(sh, 0, cr, P, best, key);
-    if (rejected && (key == kNone || (key & 1))) key = race_again(p, z, y, e, sz, sy, cr, P, sh);
+    if (!rejected) race<ALL>(p, z, nullptr, e, -1, sz, sz, 0.f, cr, P, sh.top, best, key, peak);
+    else if (y) race<REST>(p, z, y, e, -1, sz, sy, 0.f, cr, P, sh.top, best, key, peak);
+    else race<NO_DRAFT>(p, z, nullptr, e, judged, sz, sz, 0.f, cr, P, sh.top, best, key, peak);
+    key = race_end<true>(sh, 0, cr, P, best, key, peak);
+    if (rejected && (key == kNone || (key & 1) || best < peak * VF_PEAK)) key = race_again(p, z, y, e, sz, sy, cr, P, sh);
     token = key == kNone ? 0 : (int)(key >> 1);
   }
   if (cr != 0) return;

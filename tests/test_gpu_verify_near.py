@@ -40,18 +40,23 @@ def _refused(B, V, off, seed):
 
 
 def _winner(z, y, T, noise):
-    """The remainder's winner in 64 bits and whether the stated error leaves no other: the weight p (1 - q / p)
-    has p's relative error, and 1 - q / p = -expm1(x0 - log R), x0 = (y - z - (max y - max z)) / T, is off by a
-    share PROB of what x0 and R are made of (R - 1 = sum p expm1(x0)) where models are close, by 2 PROB else."""
-    z, y = z.astype(np.float64) / T, y.astype(np.float64) / T
-    p, q = R.softmax(z, 1.0), R.softmax(y, 1.0)
+    """The remainder's winner in 64 bits and whether the stated error leaves no other.  The weight is p (1 - q / p),
+    1 - q / p = -expm1(x0 - log R), x0 = (y - z - (max y - max z)) / T, R - 1 = sum p expm1(x0): as p - q, 64 bits
+    would leave 2^-53 of p, which of a p near 1 is more than the others' whole remainders.  The weight has p's
+    relative error, and x0 - log R is off by a share PROB of what x0 and R are made of where the remainder is
+    small beside p, at the winner or at the token of the largest p / noise, by 2 PROB else."""
+    z, y = z.astype(np.float64), y.astype(np.float64)
+    p = R.softmax(z, T)
     with np.errstate(invalid="ignore"):
-        x0 = np.where(p > 0, y - z - (y.max() - z.max()), 0.0)
-    rest = np.maximum(p - q, 0.0)
+        x0 = np.where(p > 0, (y - z - (y.max() - z.max())) / T, 0.0)
+    extra = np.exp((y[p == 0] - y.max()) / T).sum() / np.exp((z - z.max()) / T).sum()
+    terms = p * np.expm1(x0)
+    x = x0 - np.log1p(terms.sum() + extra)
+    rest = np.maximum(-p * np.expm1(x), 0.0)
     score = rest / noise
     top = int(np.argmax(score))
-    if rest[top] < p[top] / 128:
-        off = 2 * PROB * (np.abs(x0) + np.sum(p * np.abs(np.expm1(np.minimum(x0, 1.0)))) + np.sum(q[p == 0]))
+    if rest[top] < p[top] / 128 or score[top] < (p / noise).max() / 2 ** 14:
+        off = 2 * PROB * (np.abs(x0) + np.abs(terms).sum() + extra)
     else:
         off = 2 * PROB
     err = 2 * PROB * score + np.minimum(off, 1.0) * p / noise
@@ -117,3 +122,25 @@ def test_drafts_of_weights_below_the_least_normal_number(T, drafts):
             compared += 1
             assert n_acc[b] == want, (b, float(low[b]), float(u[r]))
     assert compared > 0.95 * B
+
+
+@pytest.mark.parametrize("gap", [8.0, 14.0, 18.0, 30.0])
+@pytest.mark.parametrize("off", [1e-3, 0.3])
+def test_remainder_beside_a_token_of_almost_all_weight(gap, off):
+    """p and q of one token near 1: the rounding of its p - q is larger than the other tokens' p - q, so that
+    their race alone would not tell whether the remainder is theirs or its."""
+    B, V = 300, 60
+    z, y, tokens, u, noise = _refused(B, V, off, seed=int(gap))
+    peak = np.random.default_rng(1).integers(0, V, 2 * B)
+    peak[tokens[1::2].repeat(2) == peak] += 1
+    peak %= V
+    r = np.arange(2 * B)
+    z[r, peak] = y[r, peak] = gap + 6.0
+    y[np.arange(0, 2 * B, 2), tokens[1::2]] = np.where(np.arange(B) % 2, -12.0, 2.0)   # the draft's share of q
+    n_acc, out = _call(z, y, 1.0, [2] * B, tokens, u, noise)
+    assert (n_acc == 0).all()
+    want = [_winner(z[2 * b], y[2 * b], 1.0, noise[b].astype(np.float64)) for b in range(B)]
+    clear = [b for b in range(B) if want[b][1]]
+    assert len(clear) >= 0.5 * B
+    wrong = [(b, want[b][0], int(out[2 * b])) for b in clear if out[2 * b] != want[b][0]]
+    assert not wrong, f"{len(wrong)} of {len(clear)}: {wrong[:4]}"
