@@ -372,8 +372,9 @@ int llama_gqa_attention_chunk_paged(const llama_dims* dims, const void* q, const
  *   token, then -1; rows from cu_new[B] on are left as they were
  *   ws: llama_workspace_bytes(LLAMA_OP_VERIFY_DRAFTS, dims with S = n_tokens, ..., vocab) bytes
  * The outputs may not overlap the inputs.  Equal scores go to the lower id.  Probabilities are formed in fp32 (good
- * to a few 2^-20 of themselves), p_i - q_i as their difference or, where the new token's would be less than p_i / 64,
- * from the logits' differences, so that it keeps its digits when the draft is close to the target.  A draft outside
+ * to a few 2^-20 of themselves; below 2^-126 they have no part in the draw), p_i - q_i as their difference or, where
+ * that is less than p_i / 64 at the new token or small beside the rounding of a much larger p, from the logits'
+ * differences, so that it keeps its digits when the draft is close to the target.  A draft outside
  * [0, vocab) is rejected and latches LLAMA_ERR_INVALID_ARG in the device status word.
  * LLAMA_ERR_UNSUPPORTED for n_tokens * ceil(vocab / 1024) >= 2^29, n_tokens >= 2^31 or B >= 2^27;
  * LLAMA_ERR_INVALID_ARG for negative counts, vocab < 1 or > 2^30 (as llama_sample), a row stride below vocab, a NaN

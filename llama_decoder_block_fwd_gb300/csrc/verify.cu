@@ -205,14 +205,22 @@ __device__ __forceinline__ int merge_argmax(const VerifyParams& p, const float2*
 // ---- the remainder p - q = p (1 - q / p)
 // Where the models are close, the difference of two fp32 probabilities is mostly their rounding.  So it is taken
 // from the logits there: log2(q / p) = c ((y - z) - (my - mz)) - log2(Sy / Sz), my, mz the rows' maxima and Sy,
-// Sz their sums, in which y - z and my - mz of close models are exact.
+// Sz their sums; y - z and my - mz are taken with what their rounding leaves (the models' logits may be a constant
+// apart), which makes the difference of the two exact for close models.
 constexpr float VF_CLOSE = 0x1p-6f;     // 1 - q / p of a winner below which the models are close
 constexpr float VF_PEAK = 0x1p-13f;     // and so they are where its score is less than this of the largest p / e: what
                                         // that token's p - q is off by could be as large
 constexpr float VF_SERIES = 0.25f;      // |log2(q / p)| below which 1 - q / p comes from a series
 
-__device__ __forceinline__ float log2_ratio(const VerifyParams& p, float z, float y, float shift) {
-  return __fmul_rn(__fsub_rn(__fsub_rn(y, z), shift), p.c);
+// a - b and what its rounding left out (Knuth's two-sum); NaN in the latter where the difference is not finite
+__device__ __forceinline__ float2 two_diff(float a, float b) {
+  const float d = __fsub_rn(a, b), v = __fsub_rn(d, a);
+  return make_float2(d, __fsub_rn(__fsub_rn(a, __fsub_rn(d, v)), __fadd_rn(b, v)));
+}
+// c ((y - z) - (my - mz)), shift = two_diff(my, mz)
+__device__ __forceinline__ float log2_ratio(const VerifyParams& p, float z, float y, float2 shift) {
+  const float2 d = two_diff(y, z);
+  return __fmul_rn(__fadd_rn(__fsub_rn(d.x, shift.x), __fsub_rn(d.y, shift.y)), p.c);
 }
 // 2^t - 1 for |t| < VF_SERIES: the exponential series up to x^6 / 720 leaves 0.18^6 / 5040 = 7e-9 of it
 __device__ __forceinline__ float exp2_less_1(float t) {
@@ -260,7 +268,7 @@ __device__ __forceinline__ void race(const VerifyParams& p, const float* z, cons
   auto score = [&](float w, float zi, float yi, float ei, int i) {
     float r = w;
     if (KIND == CLOSE) {
-      const float t = log2_ratio(p, zi, yi, sy.x - sz.x) - lr;
+      const float t = log2_ratio(p, zi, yi, two_diff(sy.x, sz.x)) - lr;
       if (fabsf(t) < VF_SERIES) r = -w * exp2_less_1(t);
       else r = w - vf_exp(p, yi, sy.x) * sy.y;
     } else if (KIND == REST) {   // both products rounded: fused, one of them would leave its rounding where p = q
@@ -381,7 +389,7 @@ __device__ __forceinline__ float row_ratio(const VerifyParams& p, const float* z
   namespace cg = cooperative_groups;
   const cg::cluster_group cl = cg::this_cluster();
   const bool vz = vf_aligned(z), vy = vf_aligned(y);
-  const float shift = sy.x - sz.x;
+  const float2 shift = two_diff(sy.x, sz.x);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t i = 4 * (cr * VF_THREADS + (int)threadIdx.x); i < p.V; i += 4 * P * VF_THREADS) {

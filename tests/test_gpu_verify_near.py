@@ -67,7 +67,17 @@ def _winner(z, y, T, noise):
 @pytest.mark.parametrize("off", [1e-6, 1e-5, 1e-4, 1e-3, 0.02, 0.3])
 @pytest.mark.parametrize("V,T,B", [(4000, 1.0, 150), (4001, 0.7, 40), (32000, 1.0, 60), (1000, 3.0, 700)])
 def test_remainder_of_close_models(V, T, B, off):
-    z, y, tokens, u, noise = _refused(B, V, off, seed=int(V + 1e6 * off))
+    _check_remainders(*_refused(B, V, off, seed=int(V + 1e6 * off)), T)
+
+
+@pytest.mark.parametrize("shift", [3.0, 0.7, -40.0])
+def test_remainder_of_close_models_a_constant_apart(shift):
+    z, y, tokens, u, noise = _refused(200, 3000, 0.0, seed=2)
+    _check_remainders(z, y + np.float32(shift), tokens, u, noise, 1.0)         # the sums' rounding is all that differs
+
+
+def _check_remainders(z, y, tokens, u, noise, T):
+    B = len(noise)
     n_acc, out = _call(z, y, T, [2] * B, tokens, u, noise)
     assert (n_acc == 0).all()
     want = [_winner(z[2 * b], y[2 * b], T, noise[b].astype(np.float64)) for b in range(B)]
