@@ -18,10 +18,11 @@
 //     issues the MMAs, warps 4-7 / 8-11 are the softmax groups, one thread per row (TMEM lane).  A unit
 //     that holds all of its item's keys stores o; otherwise it leaves (m, l, O) in the workspace.
 //   * chunk_combine_kernel merges the parts of the rows that were cut.
-// Measured (one call, plan and merge included): 2048 tokens after 30720, 32/8 heads x 128, 650-665 us = 1640
-// TFLOP/s (the attention kernel alone 1710, tensor pipe 73% active, its softmax warps' instructions in
-// the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 211 us, the attention
-// kernel 200 = 6.4 TB/s; three single tokens 14.3 us (plan 5, attention 6, merge 2.5).
+// Measured (one call, plan and merge included, back to back for over a second): 2048 tokens after 30720, 32/8
+// heads x 128, 687-700 us = 1520-1550 TFLOP/s at the 1.76-1.85 GHz that the power cap leaves (a few calls after
+// a pause 643-653 us, the attention kernel alone 620 at 1.89 GHz, tensor pipe 73% active, its softmax warps'
+// instructions in the way of the rest); 64 sequences of 3-5 tokens after 2-8 K, 1.28 GB of K and V, 208 us, the
+// attention kernel 197-200 = 6.4 TB/s; three single tokens 14.0 us (plan 5, attention 6, merge 2.5).
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
 #include <algorithm>
 #include <cmath>
@@ -125,17 +126,20 @@ __device__ __forceinline__ int warp_search(int B, int x, F&& key) {
 // in units of one tile's time (1.4 us for a pair at hd 128).  A unit costs kUnitCost more than its tiles
 // (its pipeline fills and drains); one that leaves partials kCutCost, and kRowCost for 256 rows of them,
 // written and read again; the merge kMergeCost.  Units of about one size go in rounds of one per CTA;
-// others fill up to half of the longest one, and no round takes more than its longest.  Against the best of
-// all candidates, forced one by one on 39 mixes of lengths and heads, the choice is 2% slower on average
-// and 10% at most.  C runs from 1 tile to all in steps of sqrt(2), one per warp (those past the longest range
-// cut nothing, like the last, and are skipped); candidates whose partials do not fit the workspace are out,
-// the last C (nothing cut) always fits.
+// others fill up to half of the longest one, and no round takes more than its longest.  C takes 32 values, one
+// per warp: 1, 1, 2, 3, 4, 6, 8, 12, .. 32768 tiles and all (1 stands twice: 2^(w/2) rounded down; those past the
+// longest range cut nothing, like the last, and are skipped); candidates whose partials do not fit the
+// workspace are out, the last C (nothing cut) always fits.
 //
 // One CTA does this while all the others wait: a chain of dependent steps (loads, scans, estimate, scans,
 // records) of about 8000 cycles, whose length is what counts: divisions go through reciprocals (integer and
 // IEEE divisions cost 1.6 us of it), and 512 threads or a warm instruction cache change nothing.
 constexpr float kSingleTile = 0.62f, kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost = 2.0f, kMergeCost = 2.0f;
-constexpr int CP_SEQS = CP_THREADS;      // sequences whose shapes are kept in shared memory (one per thread)
+// Sequences whose shapes are kept in shared memory (one per thread).  Beyond them every estimate reads the lengths
+// from memory, a warp's 32 sequences after another, and nothing is left whole: the plan takes 23 us for 1024
+// single tokens, 27 for 1025 and 217 for 8192 (of calls of 269, 274 and 2117 us), 35 against 30 with a prompt of
+// 2000 tokens among them (312 against 308 us).
+constexpr int CP_SEQS = CP_THREADS;
 
 __device__ __forceinline__ float rcp(float x) {
   float r;
@@ -179,7 +183,7 @@ __device__ __forceinline__ void cut(int nt, int C, float inv, int& nc, int& ct) 
   ct = max(1, cdiv_by(nt, nc, inv_nc));
   nc = max(1, cdiv_by(nt, ct, rcp((float)ct)));
 }
-// candidate w of 32: about 2^(w / 2) tiles, the last one unbounded
+// candidate w of 32: 2^(w / 2) tiles, 1.5 x 2^((w - 1) / 2) for odd w (rounded down), the last one unbounded
 __device__ __forceinline__ int candidate(int w) {
   return w == 31 ? 1 << 20 : (w & 1) ? (3 << (w >> 1)) >> 1 : 1 << (w >> 1);
 }
@@ -460,8 +464,9 @@ __global__ void __launch_bounds__(CP_THREADS) chunk_plan_kernel(const __grid_con
 
 // ------------------------------------------------------------------------------------- attention
 // Tiles before a unit's last copies at which its CTA takes the next one: late, so that what is left goes to
-// those who are done (taken at the unit's start: 1248 tokens of 32/4 heads 35 us against 29, 64 sequences of
-// 3-5 tokens 216 against 211, nine ragged prompts 19.5 against 17), but early enough to hide the look-up.
+// those who are done (taken at the unit's start: 1248 tokens of 32/4 heads x 128 from an empty cache 33.2 us
+// against 29.3, 1216 28.6 both, 64 sequences of 3-5 tokens 213 against 208, nine ragged prompts 18.2 against
+// 16.9), but early enough to hide the look-up.
 constexpr int kAskTiles = 2;
 template <int HD>
 struct CaSmem {
@@ -514,7 +519,8 @@ __device__ __forceinline__ float row_max(const uint32_t (&v)[32]) {
   }
   return fmaxf(max3(m0, __uint_as_float(v[30]), __uint_as_float(v[31])), m1);
 }
-// 32 scores of a row -> 16 bf16 pairs of P = 2^(s * scale - m); the fp32 values are added to the row sums.
+// 32 scores of a row -> 16 bf16 pairs of P = 2^(s * scale - m); the fp32 values are added to the row sums.  P is
+// rounded (2^-9 of each weight) because the tensor core takes both operands of the second product in V's type.
 __device__ __forceinline__ void exp_pack(const uint32_t (&v)[32], uint32_t* w, float scale, float m, float& ls0,
                                          float& ls1) {
 #pragma unroll
@@ -1123,6 +1129,8 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
       return -1;
     attr_set[dev] = true;
   }
+  // launched plainly: the merge reads the plan's records before its own dependency wait, and they are complete
+  // when the attention triggers it, because the attention has waited for the plan and the plan for all before
   chunk_plan_kernel<<<1, CP_THREADS, 0, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   // the attention's set-up overlaps the plan, and the merge's launch the attention

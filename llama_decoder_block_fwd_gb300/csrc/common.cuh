@@ -300,7 +300,9 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 
 // Programmatic dependent launch: let the next kernel of the stream begin launching, and wait until
 // every earlier kernel has completed and its writes are visible (no-ops without the launch
-// attribute).  A kernel reads nothing an earlier kernel wrote, and writes nothing, before pdl_wait.
+// attribute).  A kernel reads nothing an earlier kernel wrote, and writes nothing, before pdl_wait; but
+// what was complete before its predecessor began (launched plainly, or past its own pdl_wait when it triggered)
+// may be read (the draft verification's inputs, the chunk attention's plan in its merge).
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

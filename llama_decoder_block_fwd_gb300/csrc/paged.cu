@@ -18,8 +18,8 @@ namespace {
 // A few hundred bytes to a megabyte move, so the launch and the latency of dependent loads are
 // what it costs.  Every CTA scans the whole batch's lengths into its own shared memory (two loads
 // per sequence and a block scan, cheaper than a second launch), then finds the owner of each token
-// row and of each new page by bisection there.  64 sequences with drafts 3.3 us, 1024 sequences of which one
-// brings 8192 tokens 4.3 us (a launch alone takes about 2).
+// row and of each new page by bisection there.  64 sequences with drafts 3.2 us, 1024 sequences of which one
+// brings 8192 tokens 4.1 us (a launch alone takes about 2).
 constexpr int PL_THREADS = 512;
 
 struct PlanParams {
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(PL_THREADS) paged_plan_kernel(const __grid_con
 // HBM bound: every row is read once and written once, in 16-byte pieces.  A CTA takes TOK tokens,
 // forms each token's hd/2 cosines and sines once in shared memory (all heads share them), then
 // walks the tokens' q, k and v vectors, the next ones on their way.  8192 tokens of 32/8 heads x 128, 201 MB:
-// 34.6 us = 5.8 TB/s (a persistent grid, other token counts and 3 to 6 CTAs per SM: 34.6 to 37.7); 300 tokens
-// 3.4 us.  RA_TOK tokens share a pass over the row where every SM gets them, else one: 1216 tokens 6.7
-// against 7.5 us, 8192 34.3 against 37.2, but 300 tokens 5.1 against 4.2 (608: equal).
+// 33.4 us = 6.0 TB/s (a persistent grid, other token counts and 3 to 6 CTAs per SM: no faster, up to 9% slower);
+// 300 tokens 3.2 us.  RA_TOK tokens share a pass over the row where every SM gets them, else one.  RA_TOK
+// against one, back to back: 300 tokens 4.0 / 3.2 us, 608 4.1 / 4.0, 1216 5.3 / 6.2, 8192 33.3 / 36.2.
 constexpr int RA_THREADS = 256;
 constexpr int RA_TOK = 4;
 

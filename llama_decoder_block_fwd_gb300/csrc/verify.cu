@@ -12,10 +12,13 @@
 // HBM bound.  Phase 1 (verify_stats_kernel) reads every judged row of z and y once: warps take the
 // 1024-logit parts of all rows in turn, a part's loads in flight together, and leave its (max, sum of
 // exponentials).  Phase 2 (verify_pick_kernel, a cluster of up to 8 CTAs per sequence) merges the parts,
-// finds the first rejection and reads that row of z, y and e for the race.
-// 64 sequences x 2-5 rows x 128256 logits with a draft distribution: 54.1 us, of which phase 1 27 us (200 MB,
+// finds the first rejection and reads that row of z, y and e for the race.  Where the remainder is a small
+// difference of large p and q the race is run again over 1 - q / p from the logits' differences.
+// 64 sequences x 2-5 rows x 128256 logits with a draft distribution: 49.3 us, of which phase 1 27 us (200 MB,
 // the slowest SM 27 us, the median warp 24), merging and judging 2, the race 10 (99 MB from L2 and HBM, in
-// six dependent turns), cluster exchange and result 4, launches the rest; the bytes alone would take 34.
+// six dependent turns), cluster exchange and result 4, launches the rest; the bytes alone would take 34.  With
+// rows of 128257 logits, three of four of which are not 16-byte aligned and are read a logit at a time, 57.3.
+// 48 sequences without a draft distribution 32.4 (36.6); T <= 0 23.5.
 // One kernel over both phases (items from a counter, races behind the statistics) took 111 us: each item
 // paid two barriers, a fence and three dependent atomics with too few loads in flight.
 // A part's sums are formed and merged in a fixed order, and the race keeps the largest score and of equals
@@ -383,7 +386,8 @@ __device__ __forceinline__ unsigned race_end(PickShared& sh, int turn, int cr, i
 // log2(Sy / Sz) again, for models that are close: Sy / Sz 2^(c (my - mz)) - 1 = sum_i p_i (2^t_i - 1), t_i the
 // log2 ratio without the sums.  The terms are as small as the models' differences, and so is what they are off
 // by, where the sums as they stand are off by about 2^-23 of 1.  One more pass over the two rows, and a race after
-// it, which only a rejection between close models asks for.
+// it, which only a rejection between close models asks for (64 sequences x 128256, every one of them: 95 us
+// against 48).
 __device__ __forceinline__ float row_ratio(const VerifyParams& p, const float* z, const float* y, float2 sz, float2 sy,
                                            int cr, int P, PickShared& sh) {
   namespace cg = cooperative_groups;
@@ -577,6 +581,8 @@ int launch_verify(const VerifyDesc& d, int num_sms, unsigned* status, cudaStream
   p.stat_y = reinterpret_cast<float2*>(static_cast<char*>(d.ws) + round256((size_t)d.T * p.parts * sizeof(float2)));
   p.status = status;
   if (d.T > 0) {
+    // Launched plainly, and that has to stay: the pick kernel reads the caller's inputs before its dependency wait,
+    // and they are complete only because this launch has waited for all that came before it.
     const int64_t total = d.T * p.parts * (p.y ? 2 : 1);
     const unsigned grid = (unsigned)std::min<int64_t>((total + VF_WARPS - 1) / VF_WARPS, VF_STATS_CTAS * num_sms);
     if (p.greedy) verify_stats_kernel<true><<<grid, VF_THREADS, 0, st>>>(p);
