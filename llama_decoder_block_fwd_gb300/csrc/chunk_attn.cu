@@ -96,7 +96,9 @@ struct ChunkParams {   // 128-byte aligned by its tensor maps
   unsigned* status;
 };
 
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+// The arithmetic of the work split runs on the host too, where its tests call it.
+#define LLAMA_BOTH __host__ __device__ __forceinline__
+LLAMA_BOTH int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // The last b of B (a power-of-32 search by one warp) with key(b) <= x; key is non-decreasing, key(0) <= x.
 template <typename F>
@@ -141,24 +143,38 @@ constexpr float kSingleTile = 0.62f, kUnitCost = 1.5f, kCutCost = 1.0f, kRowCost
 // 2000 tokens among them (312 against 308 us).
 constexpr int CP_SEQS = CP_THREADS;
 
-__device__ __forceinline__ float rcp(float x) {
+#ifndef LLAMA_HOST_RCP
+#define LLAMA_HOST_RCP(x) (1.f / (x))
+#endif
+LLAMA_BOTH float rcp(float x) {
+#ifdef __CUDA_ARCH__
   float r;
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+#else
+  return LLAMA_HOST_RCP(x);
+#endif
+}
+LLAMA_BOTH unsigned mul_high(unsigned a, unsigned b) {
+#ifdef __CUDA_ARCH__
+  return __umulhi(a, b);
+#else
+  return (unsigned)(((uint64_t)a * b) >> 32);
+#endif
 }
 // floor(a / b) for 0 <= a < 2^22, 0 < b, inv within a few ulp of 1 / b
-__device__ __forceinline__ int div_by(int a, int b, float inv) {
+LLAMA_BOTH int div_by(int a, int b, float inv) {
   int q = (int)((float)a * inv);
   if (q * b > a) --q;
   if ((q + 1) * b <= a) ++q;
   return q;
 }
 // floor(a / b), a >= 0, inv = floor(2^32 / b): a * inv / 2^32 is less than 1 + a / 2^32 below a / b
-__device__ __forceinline__ int div_inv(int a, int b, unsigned inv) {
-  const int q = (int)__umulhi((unsigned)a, inv);
+LLAMA_BOTH int div_inv(int a, int b, unsigned inv) {
+  const int q = (int)mul_high((unsigned)a, inv);
   return b == 1 ? a : q + ((q + 1) * b <= a);
 }
-__device__ __forceinline__ int cdiv_by(int a, int b, float inv) { return div_by(a + b - 1, b, inv); }
+LLAMA_BOTH int cdiv_by(int a, int b, float inv) { return div_by(a + b - 1, b, inv); }
 
 struct SeqShape { int lo, n, c, np, nt; };
 // cu, n_cached -> the sequence's shape; lengths that cannot be right bring nothing and set bad
@@ -176,20 +192,23 @@ __device__ __forceinline__ SeqShape seq_shape(const ChunkParams& p, int b, bool&
   return s;
 }
 
+// floor(2^32 / x), for div_inv
+unsigned inverse(int64_t x) { return (unsigned)std::min<uint64_t>((1ull << 32) / (uint64_t)x, UINT32_MAX); }
+
 // nt tiles in chunks of at most C (inv = 1 / C): their number and their tiles
-__device__ __forceinline__ void cut(int nt, int C, float inv, int& nc, int& ct) {
+LLAMA_BOTH void cut(int nt, int C, float inv, int& nc, int& ct) {
   nc = nt <= C ? 1 : cdiv_by(nt, C, inv);
   const float inv_nc = rcp((float)nc);
   ct = max(1, cdiv_by(nt, nc, inv_nc));
   nc = max(1, cdiv_by(nt, ct, rcp((float)ct)));
 }
 // candidate w of 32: 2^(w / 2) tiles, 1.5 x 2^((w - 1) / 2) for odd w (rounded down), the last one unbounded
-__device__ __forceinline__ int candidate(int w) {
+LLAMA_BOTH int candidate(int w) {
   return w == 31 ? 1 << 20 : (w & 1) ? (3 << (w >> 1)) >> 1 : 1 << (w >> 1);
 }
 
 // Unit u of sequence b (seq[b].unit0 <= u); false if no row of it sees its keys.
-__device__ __forceinline__ bool make_unit(const ChunkParams& p, const ChunkSeq& s, int b, int u, ChunkUnit& d) {
+LLAMA_BOTH bool make_unit(const ChunkParams& p, const ChunkSeq& s, int b, int u, ChunkUnit& d) {
   // first the uncut items, the longest first, then the others chunk by chunk
   const int x = u - s.unit0, item = div_inv(x, p.n_kv, p.inv_kv), y = item < s.wp ? item : item - s.wp, nq = s.np - s.wp;
   const bool uncut = item < s.wp;
@@ -1112,7 +1131,6 @@ int launch_hd(const ChunkAttnDesc& a, int num_sms, cudaStream_t st) {
   ws += round256((size_t)p.part_rows * a.n_q * HD * 4);
   p.part_ml = reinterpret_cast<float2*>(ws);
   p.grid = std::min(num_sms, kMaxGrid);
-  auto inverse = [](int64_t x) { return (unsigned)std::min<uint64_t>((1ull << 32) / (uint64_t)x, UINT32_MAX); };
   p.inv_q = inverse(a.n_q);
   p.inv_kv = inverse(a.n_kv);
   p.inv_grid = inverse(p.grid);
