@@ -154,3 +154,71 @@ def test_remainder_beside_a_token_of_almost_all_weight(gap, off):
     assert len(clear) >= 0.5 * B
     wrong = [(b, want[b][0], int(out[2 * b])) for b in clear if out[2 * b] != want[b][0]]
     assert not wrong, f"{len(wrong)} of {len(clear)}: {wrong[:4]}"
+
+
+def test_close_models_late_in_a_long_sequence():
+    """The refused row lies behind the rows whose merged statistics are kept."""
+    V, n, B = 2000, 70, 12
+    rng = np.random.default_rng(9)
+    z = (2.5 * rng.normal(size=(B * n, V))).astype(np.float32)
+    y = (z + 1e-5 * rng.normal(size=z.shape)).astype(np.float32)
+    tokens, u = rng.integers(0, V, B * n), np.full(B * n, 0.5)
+    stop = rng.integers(30, n - 1, B)
+    for b in range(B):
+        row = b * n + stop[b]
+        z[row, tokens[row + 1]], y[row, tokens[row + 1]] = -np.inf, -12.0
+    noise = rng.exponential(size=(B, V)).astype(np.float32)
+    n_acc, out = _call(z, y, 1.0, [n] * B, tokens, u, noise)
+    assert n_acc.tolist() == stop.tolist()
+    want = [_winner(z[b * n + stop[b]], y[b * n + stop[b]], 1.0, noise[b].astype(np.float64)) for b in range(B)]
+    assert sum(w[1] for w in want) >= B - 1
+    assert all(out[b * n + stop[b]] == w[0] for b, w in enumerate(want) if w[1])
+
+
+def test_close_and_other_models_in_one_captured_call():
+    """One graph, replayed with models that are close in some sequences and not in others, and with none of either;
+    two such graphs in flight at once.  Replays of the same inputs agree."""
+    import torch
+    B, V = 90, 3000
+    far, near = _refused(B, V, 0.5, seed=1), _refused(B, V, 1e-5, seed=2)
+    dims = L.dims_of(B, 2 * B, 128, 1, 1, 128, 128, 1e4, 1e-5)
+    cu = torch.arange(0, 2 * B + 1, 2, dtype=torch.int32, device="cuda")
+    runs = []
+    for _ in range(2):
+        z, y = (torch.empty((2 * B, V), device="cuda") for _ in range(2))
+        tokens, u = torch.empty(2 * B, dtype=torch.int32, device="cuda"), torch.full((2 * B,), 0.5, device="cuda")
+        noise = torch.ones((B, V), device="cuda")
+        z.normal_(), y.copy_(z), tokens.fill_(1)
+        n_acc, out = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (B, 2 * B))
+        ws = torch.empty(L.llama_workspace_bytes(L.OP_VERIFY_DRAFTS, dims, L.F32, vocab=V), dtype=torch.uint8, device="cuda")
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            L.llama_verify_drafts(z, y, 1.0, cu, tokens, u, noise, n_acc, out, ws)
+        runs.append((z, y, tokens, noise, n_acc, out, st, g, ws))
+    for turn in range(3):
+        mixes = []
+        for k, (z, y, tokens, noise, *_) in enumerate(runs):
+            pick = np.arange(B) % 3 == turn if k == 0 else np.full(B, turn == 1)
+            rows = pick.repeat(2)[:, None]
+            mix = [np.where(r, a, b) for r, a, b in ((rows, near[0], far[0]), (rows, near[1], far[1]),
+                                                     (rows[:, 0], near[2], far[2]), (pick[:, None], near[4], far[4]))]
+            for dst, a in zip((z, y, tokens, noise), mix):
+                dst.copy_(torch.from_numpy(np.ascontiguousarray(a)))
+            mixes.append(mix)
+        results = []
+        for _ in range(3):
+            torch.cuda.synchronize()
+            for run in runs:
+                with torch.cuda.stream(run[6]):
+                    run[7].replay()
+            torch.cuda.synchronize()
+            results.append([(run[4].clone(), run[5].clone()) for run in runs])
+        assert L.llama_get_device_status() == 0
+        assert all(torch.equal(a, b) for again in results[1:] for x, w in zip(results[0], again) for a, b in zip(x, w))
+        for (z, y, _, noise), (n_acc, out) in zip(mixes, results[0]):
+            assert (n_acc == 0).all()
+            out = out.cpu().numpy()
+            for b in range(B):
+                top, clear = _winner(z[2 * b], y[2 * b], 1.0, noise[b].astype(np.float64))
+                assert not clear or out[2 * b] == top
