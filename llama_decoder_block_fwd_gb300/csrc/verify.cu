@@ -248,7 +248,8 @@ enum RaceKind : int { REST, CLOSE, NO_DRAFT, ALL };
 
 // This CTA's share of the vocabulary: a thread's (best score, its lowest id); scores of 0 do not count.  `lr` is
 // log2(Sy / Sz) (CLOSE); in REST the winner's key is marked where its p and q are close, and `peak` is the largest
-// p / e of the tokens that are judged (all those above the best score).
+// p / e of the tokens that are judged: all those above the best score, and whatever others, which being below it
+// do not count where peak is compared with it.
 // p_i / e_i bounds a score from above, so a token whose p_i is below top * e_i, top the CTA's best score so far
 // (less 2^-20, more than the quotients' errors), is out of the race: it needs one exponential and no
 // division in place of two and one (48 lookups of 128256 logits: 35.7 -> 33.1 us; with a draft distribution
