@@ -101,7 +101,10 @@ typedef enum llama_op {
   LLAMA_OP_BLOCK_FORWARD = 4,
   LLAMA_OP_STACK_DECODE_STEP = 5,
   LLAMA_OP_GQA_ATTENTION_CHUNK_PAGED = 6,
-  LLAMA_OP_VERIFY_DRAFTS = 7
+  LLAMA_OP_VERIFY_DRAFTS = 7,
+  LLAMA_OP_GQA_ATTENTION_DECODE_PAGED_KV8 = 8,
+  LLAMA_OP_BEAM_SELECT = 9,
+  LLAMA_OP_BEAM_REORDER_PAGED = 10
 } llama_op;
 
 /* RMSNorm over the feature axis ("Llama Architecture ...", Mathematical Foundations 1, with eps
@@ -386,6 +389,129 @@ int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, in
                         const float* noise, int64_t noise_ld, int32_t* n_accepted, int32_t* out_tokens,
                         void* ws, size_t ws_bytes, void* stream);
 
+/* 8-bit paged cache: pages as above, K and V as E4M3 codes with one fp32 scale per position and KV head, set
+ * when the row is written (llama_kv_quantize's scales are fixed per head beforehand).  One layer's cache:
+ *   k_codes, v_codes [n_pages, 128, n_kv, head_dim], one byte per element
+ *   k_scale, v_scale [n_pages, n_kv, 128] fp32: value = code * scale; a head's 128 scales of a page are
+ *                    contiguous.  Scales are positive and lie in 2^-100 .. 2^100.
+ * block tables, slots and positions are those of the bf16 paged calls, llama_paged_plan among them.    */
+
+/* llama_rope_append_paged into an 8-bit cache:
+ *   q_out[t] = R(positions[t]) q[t];  the rows R(positions[t]) k[t] and v[t] go to slots[t] as codes, with the scale
+ *   2^e, e the smallest integer in -100 .. 100 with u <= 448 * 2^e; u is the largest |v_i| of the head's row for V,
+ *   and for K the largest |a| + |b| over its rotated pairs (a, b), which no rotation exceeds (so a key's scale does
+ *   not depend on its position).  code = E4M3(x * 2^-e), rounded once from the fp32 rotation, ties to even,
+ *   saturating at +-448 (an infinite x at the scale 2^100); a NaN stays NaN, and it, or a pair that holds one,
+ *   has no part in u.
+ * Other arguments, skipped rows, latched errors and refusals as llama_rope_append_paged; q and q_out may both
+ * be NULL (append only).  k, v and the four pool arrays may not (LLAMA_ERR_INVALID_ARG; to rotate alone, that
+ * call serves).  LLAMA_ERR_ALIGNMENT also for codes or scales not 16-byte aligned.                      */
+int llama_rope_append_paged_kv8(const llama_dims* dims, const void* q, int64_t q_stride, const void* k,
+                                int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                                const int32_t* slots, void* q_out, void* k_codes, float* k_scale, void* v_codes,
+                                float* v_scale, int64_t n_pages, void* stream);
+
+/* An 8-bit cache read back to bf16 pages, for the calls that read those (llama_gqa_attention_chunk_paged takes k_pool
+ * and v_pool with the same block table): rows 0 .. n_pos[b]-1 of every sequence's pages,
+ *   k_pool[page, row] = bf16(k_codes[page, row] * k_scale[page, :, row]), and the same for V
+ * (exact for the scales that llama_rope_append_paged_kv8 writes, where bf16 has the value).  k_pool and v_pool
+ * [n_pages, 128, n_kv, head_dim] bf16: one layer's worth serves every layer in turn.  Rows that no sequence holds
+ * are left as they were; pages may be shared between sequences.  Uses B, n_kv and head_dim.
+ *   n_pos [B] int32: positions to read back, 0 .. 128 * max_pages
+ * LLAMA_ERR_UNSUPPORTED for head_dim above 256 or no multiple of 8, n_kv > 4096, B > 65535, n_pages >= 2^24,
+ * max_pages >= 2^31; LLAMA_ERR_INVALID_ARG for other bad dims, n_pages < 1, max_pages < 1, NULL arrays;
+ * LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte or others not 16-byte aligned.  Latched as
+ * LLAMA_ERR_INVALID_ARG in the device status word: n_pos outside its range (the sequence is skipped) and page ids
+ * outside [0, n_pages) (the page is).                                                             */
+int llama_kv_dequantize_paged(const llama_dims* dims, const void* k_codes, const float* k_scale, const void* v_codes,
+                              const float* v_scale, int64_t n_pages, const int32_t* block_table, int64_t max_pages,
+                              const int32_t* n_pos, void* k_pool, void* v_pool, void* stream);
+
+/* One-token attention over an 8-bit paged cache: sequence b's query attends to the cached values (code * scale)
+ * at positions 0 .. seq_pos[b] (its own among them, already written); seq_pos[b] = -1: nothing to attend to, a
+ * row of zeros.
+ *   q, o bf16 [B, n_q, head_dim], S = 1; codes, scales, block_table [B, max_pages] as above
+ *   max_pos: an upper bound of seq_pos (host value; sizes the work split and the workspace,
+ *   llama_workspace_bytes(LLAMA_OP_GQA_ATTENTION_DECODE_PAGED_KV8, dims, ..., kv_capacity = max_pos + 1))
+ * head_dim 64 or 128, any n_q / n_kv.  Pages may be shared; rows past a sequence's position are never used, whatever
+ * they hold.  o may not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
+ * Numerics: scores, softmax statistics and sums in fp32; q and the products of softmax weight and V scale enter
+ * the 8-bit tensor-core products as two E4M3 values each (8 significant bits, the second 2^-5 finer than the
+ * format's own range), relative to the largest of their row.
+ * LLAMA_ERR_UNSUPPORTED for another head_dim, n_q > 65536, B > 65535, B n_kv >= 2^24, n_pages >= 2^24, max_pages >= 2^31;
+ * LLAMA_ERR_INVALID_ARG for S != 1, other bad dims, n_pages < 1, max_pages < 1, max_pos < 0, max_pos >= 128 * max_pages
+ * or 2^24, NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte or others not 16-byte aligned;
+ * LLAMA_ERR_WORKSPACE for a workspace that is too small.  Latched as LLAMA_ERR_INVALID_ARG in the device status
+ * word: a position below -1 or above max_pos (the sequence's rows are then zeros) or a page id outside [0, n_pages)
+ * among the entries a sequence uses (its rows are then undefined; no other memory is touched).           */
+int llama_gqa_attention_decode_paged_kv8(const llama_dims* dims, const void* q, const void* k_codes,
+                                         const float* k_scale, const void* v_codes, const float* v_scale,
+                                         int64_t n_pages, const int32_t* block_table, int64_t max_pages,
+                                         const int32_t* seq_pos, int64_t max_pos, void* o, void* ws, size_t ws_bytes,
+                                         void* stream);
+
+/* Beam search over the paged cache: B requests of W beams each, beam w of request b being sequence b * W + w of
+ * every per-sequence array (llama_paged_plan's and the attention's included).  llama_beam_select picks the beams
+ * of the next step, llama_beam_reorder_paged makes the cache follow them.                            */
+
+/* The n_out best continuations of each request.  Beam w and token i score
+ *   scores[b, w] + z_i - log(sum_j exp(z_j)),   z = logits[b * W + w]
+ * and the best over all beams and tokens are kept, larger first, equal scores by the lower beam, then the lower
+ * token.
+ *   logits [B * W, ld] fp32, first `vocab` entries used: finite values or -inf (no candidate)
+ *   scores [B, W] fp32: finite values or -inf (a beam without candidates)
+ *   finished [B, W] int32, may be NULL: a beam marked by a value other than 0 has one candidate, pad_token with
+ *                the beam's score unchanged (its logits are not read)
+ *   parents, tokens [B, n_out] int32: beam (0 .. W-1) and token of each; out_scores [B, n_out] fp32.  Where there are
+ *                fewer candidates: -1, -1 and -inf
+ *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_SELECT, dims with B and S = W, ..., vocab) bytes, for any n_out
+ * The outputs may not overlap the inputs.  Sums of exponentials in fp32, logarithm and scores in fp64 (out_scores
+ * rounds once): candidates of one beam are ranked by their logits, those of different beams by scores good to
+ * about 2^-22; equal rows with equal scores give equal scores.
+ * LLAMA_ERR_UNSUPPORTED for W > 32, n_out > 64 or B * W >= 2^22; LLAMA_ERR_INVALID_ARG for B < 0, W < 1, n_out < 1,
+ * vocab < 1 or > 2^30, ld < vocab, pad_token outside [0, vocab) with finished given, NULL arrays; LLAMA_ERR_ALIGNMENT for arrays
+ * not 4-byte aligned or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE for a workspace that is too small.    */
+int llama_beam_select(const float* logits, int64_t B, int64_t W, int64_t vocab, int64_t ld, const float* scores,
+                      const int32_t* finished, int32_t pad_token, int64_t n_out, int32_t* parents, int32_t* tokens,
+                      float* out_scores, void* ws, size_t ws_bytes, void* stream);
+
+/* One array of a paged cache, seen as [n_layers, n_pages, parts, 128, row_bytes]: K or V rows have parts = 1 and
+ * row_bytes = n_kv * head_dim * element size, scales [n_layers, n_pages, n_kv, 128] parts = n_kv and row_bytes = 4. */
+typedef struct llama_page_pool {
+  void* base;          /* 16-byte aligned */
+  int64_t n_layers, parts, row_bytes;
+} llama_page_pool;
+
+/* The cache follows the chosen beams: new beam w of request b continues old beam p = parents[b, w].
+ *   n_cached_out[b, w] = n_cached[b, p], and the entries 0 .. ceil(n_cached / 128) - 1 of its row of block_table_out are
+ *   p's, but for an open page (the last one, where n_cached is no multiple of 128): the beams will write to it, so the first of
+ *   the new beams (by w) whose last page it is keeps it, and each other one gets a page of its own with the open page's
+ *   n_cached % 128 rows copied into it, in every pool and layer.
+ *   A page that old beams held and no kept beam holds is dead.  The copies of a request, by w, go into its dead pages, by
+ *   column and then beam, and into free_pages, in request order from the front, where those do not suffice.
+ *   freed_pages: the dead pages left over, by request, column and beam; counts[0] = pages taken from free_pages,
+ *   counts[1] = dead pages left over.
+ * parents[b, w] = -1: the new beam is empty (n_cached_out 0; its row is left as it was).  Entries behind a row's pages are left
+ * as they were.  block_table_out may be block_table and n_cached_out n_cached (in place); otherwise none overlap.
+ *   parents [B, W], n_cached and n_cached_out [B * W], block_table and block_table_out [B * W, max_pages], free_pages [n_free],
+ *   freed_pages [freed_room], counts [2]: int32 device arrays
+ *   pools: HOST array of n_pools records (base: device memory), read before the call returns
+ *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_REORDER_PAGED, dims with B and S = W, ..., kv_capacity = 128 * max_pages)
+ * A page may stand in several rows of a request, in the same column; other requests may share pages that some kept beam of
+ * each holds (a common prompt).  No pool row is written but the copied rows.
+ * LLAMA_ERR_UNSUPPORTED for W > 32, B > 8192, n_pages >= 2^24, max_pages > 2^17, n_free or freed_room >= 2^31, n_pools > 8,
+ * parts * row_bytes > 2^24, n_layers > 65536, 2^44 bytes and more of one page over all layers; LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's
+ * n_layers, parts or row_bytes < 1, row_bytes no multiple of 4), NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte,
+ * pools or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE.  Latched as LLAMA_ERR_INVALID_ARG in the device status
+ * word: a parent outside [-1, W) (taken as -1), n_cached outside [0, 128 * max_pages] (taken as 0), page ids outside
+ * [0, n_pages) among the held ones (never freed; not copied: the entry is -1), more copies than pages (their entries are -1;
+ * counts[0] says what was needed) and more dead pages than freed_room (the rest is not listed; counts[1] counts them). */
+int llama_beam_reorder_paged(const int32_t* parents, int64_t B, int64_t W, const int32_t* n_cached,
+                             int32_t* n_cached_out, const int32_t* block_table, int32_t* block_table_out,
+                             int64_t max_pages, const int32_t* free_pages, int64_t n_free, int64_t n_pages,
+                             const llama_page_pool* pools, int n_pools, int32_t* freed_pages, int64_t freed_room,
+                             int32_t* counts, void* ws, size_t ws_bytes, void* stream);
+
 /* Next-token choice from the LM head's logits ("LLaMA-3 8B 现代 LLM 架构、计算规模与能耗", section 十:
  * softmax over the vocabulary, then argmax, or a draw shaped by temperature, top-k and top-p).
  *   logits  [B, ld] fp32 (device), row b's first `vocab` entries used; finite values or -inf,
@@ -420,7 +546,7 @@ int llama_embed(int dtype, const void* table, int64_t vocab, int64_t d_model, co
  * *out receives LLAMA_OK, LLAMA_ERR_TIMEOUT (a kernel's bounded wait ran out and it exited),
  * LLAMA_ERR_BOUNDS (bounds-checking builds: a kernel met an index outside its tensor) or
  * LLAMA_ERR_INVALID_ARG (llama_embed or llama_verify_drafts met a token id outside the vocabulary, or
- * a paged call lengths, pages or slots outside their range), in that order of precedence when several
+ * a paged call lengths, pages, slots or parents outside their range), in that order of precedence when several
  * were latched.
  * Returns LLAMA_OK, or LLAMA_ERR_CUDA if the synchronisation or the copy failed.             */
 int llama_get_device_status(int* out, void* stream);

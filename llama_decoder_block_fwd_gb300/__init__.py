@@ -19,16 +19,20 @@ __all__ = [
     "llama_sample", "llama_embed", "llama_kv_quantize", "llama_gqa_attention_decode_kv8",
     "llama_stack_decode_step_kv8", "llama_stack_decode_step_paged", "llama_gqa_attention_decode_paged",
     "llama_paged_plan", "llama_rope_append_paged", "llama_gqa_attention_chunk_paged", "llama_verify_drafts",
+    "llama_rope_append_paged_kv8", "llama_kv_dequantize_paged", "llama_gqa_attention_decode_paged_kv8",
+    "llama_beam_select", "llama_beam_reorder_paged", "PagePool",
     "llama_get_device_status", "llama_status_string", "llama_profile_enable", "llama_profile_read",
     "llama_selftest_bounded_wait", "llama_selftest_bounds", "llama_build_info", "BUILD_BOUNDS_CHECKS", "DEBUG_BUILD",
     "OP_RMSNORM", "OP_ROPE", "OP_GQA_ATTENTION", "OP_SWIGLU_FFN", "OP_BLOCK_FORWARD",
     "OP_STACK_DECODE_STEP", "OP_GQA_ATTENTION_CHUNK_PAGED", "OP_VERIFY_DRAFTS",
+    "OP_GQA_ATTENTION_DECODE_PAGED_KV8", "OP_BEAM_SELECT", "OP_BEAM_REORDER_PAGED",
 ]
 
 F32, BF16 = 0, 1
 X_F32, Y_F32 = 0x100, 0x200   # residual-stream flags for llama_block_forward's dtype (x fp32, y fp32)
 (OP_RMSNORM, OP_ROPE, OP_GQA_ATTENTION, OP_SWIGLU_FFN, OP_BLOCK_FORWARD,
- OP_STACK_DECODE_STEP, OP_GQA_ATTENTION_CHUNK_PAGED, OP_VERIFY_DRAFTS) = range(8)
+ OP_STACK_DECODE_STEP, OP_GQA_ATTENTION_CHUNK_PAGED, OP_VERIFY_DRAFTS, OP_GQA_ATTENTION_DECODE_PAGED_KV8,
+ OP_BEAM_SELECT, OP_BEAM_REORDER_PAGED) = range(11)
 STATUS_NAMES = {0: "LLAMA_OK", 1: "LLAMA_ERR_INVALID_ARG", 2: "LLAMA_ERR_UNSUPPORTED",
                 3: "LLAMA_ERR_ALIGNMENT", 4: "LLAMA_ERR_WORKSPACE", 5: "LLAMA_ERR_CUDA",
                 6: "LLAMA_ERR_TIMEOUT", 7: "LLAMA_ERR_BOUNDS"}
@@ -50,6 +54,11 @@ _WEIGHT_FIELDS = ["attn_norm_g", "wq", "wk", "wv", "wo", "ffn_norm_g", "w_gate",
 
 class BlockWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _WEIGHT_FIELDS]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("n_layers", ctypes.c_int64), ("parts", ctypes.c_int64),
+                ("row_bytes", ctypes.c_int64)]
 
 
 class LlamaError(RuntimeError):
@@ -99,6 +108,12 @@ def lib() -> ctypes.CDLL:
                 "llama_gqa_attention_chunk_paged": [pd, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, sz, vp],
                 "llama_verify_drafts": [vp, i64, i64, i64, vp, i64, ctypes.c_float, vp, i64, vp, vp, vp, i64, vp, vp,
                                         vp, sz, vp],
+                "llama_rope_append_paged_kv8": [pd, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp],
+                "llama_kv_dequantize_paged": [pd, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp],
+                "llama_gqa_attention_decode_paged_kv8": [pd, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp],
+                "llama_beam_select": [vp, i64, i64, i64, i64, vp, vp, i32, i64, vp, vp, vp, vp, sz, vp],
+                "llama_beam_reorder_paged": [vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, ctypes.POINTER(PagePool), i32,
+                                             vp, i64, vp, vp, sz, vp],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -405,6 +420,126 @@ def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, no
         _arg(w, "tokens", tokens, i32, dev), _arg(w, "u", u, f32, dev, (T,)), e, lde,
         _arg(w, "n_accepted", n_accepted, i32, dev), _arg(w, "out_tokens", out_tokens, i32, dev, (T,)),
         *_scratch(w, ws, dev), st), w)
+
+
+def _codes(where, name, t, dev, shape):
+    """The address of a contiguous tensor of E4M3 codes: uint8, or torch's float8_e4m3fn."""
+    import torch
+    dtype = torch.float8_e4m3fn if getattr(t, "dtype", None) is torch.float8_e4m3fn else torch.uint8
+    return _arg(where, name, t, dtype, dev, shape)
+
+
+def llama_rope_append_paged_kv8(dims, q, k, v, positions, slots, q_out, k_codes, k_scale, v_codes, v_scale, stream=None):
+    """llama_rope_append_paged into an 8-bit cache: codes [n_pages, 128, n_kv, hd] (uint8 or float8_e4m3fn) and
+    scales fp32 [n_pages, n_kv, 128].  None, None for q, q_out: append only."""
+    w = "llama_rope_append_paged_kv8"
+    L, torch, dev, st = _here(stream)
+    d, i32, bf16, f32 = _d(dims), torch.int32, torch.bfloat16, torch.float32
+    S, hd, n_q, n_kv = d.S, d.head_dim, d.n_q, d.n_kv
+    qa, qs = _heads(w, "q", q, bf16, dev, S, n_q, hd)
+    ka, ks = _heads(w, "k", k, bf16, dev, S, n_kv, hd)
+    va, vs = _heads(w, "v", v, bf16, dev, S, n_kv, hd)
+    n_pages = k_codes.shape[0]
+    pool, rows = (n_pages, 128, n_kv, hd), (n_pages, n_kv, 128)
+    _check(L.llama_rope_append_paged_kv8(
+        ctypes.byref(d), qa, qs, ka, ks, va, vs, _arg(w, "positions", positions, i32, dev, (S,)),
+        _arg(w, "slots", slots, i32, dev, (S,)), _arg(w, "q_out", q_out, bf16, dev, (S, n_q, hd)),
+        _codes(w, "k_codes", k_codes, dev, pool), _arg(w, "k_scale", k_scale, f32, dev, rows),
+        _codes(w, "v_codes", v_codes, dev, pool), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages, st), w)
+
+
+def llama_kv_dequantize_paged(k_codes, k_scale, v_codes, v_scale, block_table, n_pos, k_pool, v_pool, stream=None):
+    """Rows 0 .. n_pos[b]-1 of every sequence's pages from codes and scales to bf16 pools [n_pages, 128, n_kv, hd]."""
+    w = "llama_kv_dequantize_paged"
+    L, torch, dev, st = _here(stream)
+    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
+    n_pages, _, n_kv, hd = k_pool.shape
+    B, P, rows, codes = n_pos.numel(), block_table.shape[-1], (n_pages, n_kv, 128), (n_pages, 128, n_kv, hd)
+    d = Dims(B, 0, 0, 0, n_kv, hd, 0, 1.0, 0.0)
+    _check(L.llama_kv_dequantize_paged(
+        ctypes.byref(d), _codes(w, "k_codes", k_codes, dev, codes), _arg(w, "k_scale", k_scale, f32, dev, rows),
+        _codes(w, "v_codes", v_codes, dev, codes), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages,
+        _arg(w, "block_table", block_table, i32, dev, (B, P)), P, _arg(w, "n_pos", n_pos, i32, dev),
+        _arg(w, "k_pool", k_pool, bf16, dev, codes), _arg(w, "v_pool", v_pool, bf16, dev, codes), st), w)
+
+
+def llama_gqa_attention_decode_paged_kv8(dims, q, k_codes, k_scale, v_codes, v_scale, block_table, seq_pos, max_pos, o,
+                                         ws, stream=None):
+    """One new token per sequence, q [B, n_q, hd], over an 8-bit cache: codes [n_pages, 128, n_kv, hd], scales
+    fp32 [n_pages, n_kv, 128]; positions 0 .. seq_pos[b] (-1: none) of sequence b."""
+    w = "llama_gqa_attention_decode_paged_kv8"
+    L, torch, dev, st = _here(stream)
+    d, i32, bf16, f32 = _d(dims), torch.int32, torch.bfloat16, torch.float32
+    B, hd, n_kv = d.B, d.head_dim, d.n_kv
+    n_pages, P = k_codes.shape[0], block_table.shape[-1]
+    pool, rows, heads = (n_pages, 128, n_kv, hd), (n_pages, n_kv, 128), (B, d.n_q, hd)
+    _check(L.llama_gqa_attention_decode_paged_kv8(
+        ctypes.byref(d), _arg(w, "q", q, bf16, dev, heads), _codes(w, "k_codes", k_codes, dev, pool),
+        _arg(w, "k_scale", k_scale, f32, dev, rows), _codes(w, "v_codes", v_codes, dev, pool),
+        _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages, _arg(w, "block_table", block_table, i32, dev, (B, P)), P,
+        _arg(w, "seq_pos", seq_pos, i32, dev, (B,)), max_pos, _arg(w, "o", o, bf16, dev, heads), *_scratch(w, ws, dev),
+        st), w)
+
+
+def llama_beam_select(logits, scores, finished, pad_token, parents, tokens, out_scores, ws, vocab=None, stream=None):
+    """parents, tokens int32 and out_scores fp32 [B, n_out] <- the best continuations of B requests of W beams:
+    logits fp32 [B * W, ld], scores fp32 [B, W], finished int32 [B, W] or None."""
+    w = "llama_beam_select"
+    L, torch, dev, st = _here(stream)
+    i32, f32 = torch.int32, torch.float32
+    (B, W), kept = scores.shape, parents.shape
+    V = logits.shape[1] if vocab is None else int(vocab)
+    z, ld = _matrix(w, "logits", logits, f32, dev, B * W, V)
+    _check(L.llama_beam_select(
+        z, B, W, V, ld, _arg(w, "scores", scores, f32, dev, (B, W)), _arg(w, "finished", finished, i32, dev, (B, W)),
+        pad_token, kept[-1], _arg(w, "parents", parents, i32, dev, (B, kept[-1])), _arg(w, "tokens", tokens, i32, dev, kept),
+        _arg(w, "out_scores", out_scores, f32, dev, kept), *_scratch(w, ws, dev), st), w)
+
+
+def _pools(where, name, pools, dev, n_pages, scales):
+    """PagePool records of [n_layers, n_pages, 128, ...] tensors, or of scales [n_layers, n_pages, parts, 128]; the
+    layers' axis may be missing."""
+    out = []
+    for i, t in enumerate(pools):
+        _arg(where, f"{name}[{i}]", t, t.dtype, dev)
+        s = tuple(t.shape)
+        layers = len(s) > (3 if scales else 4)
+        lead, rest = (s[0], s[1:]) if layers else (1, s)
+        if scales:
+            ok = len(rest) == 3 and rest[0] == n_pages and rest[2] == 128
+            parts, row = (rest[1], t.element_size()) if ok else (0, 0)
+        else:
+            ok = len(rest) >= 2 and rest[0] == n_pages and rest[1] == 128
+            parts, row = 1, 0
+            if ok:
+                row = t.element_size()
+                for x in rest[2:]:
+                    row *= x
+        if not ok:
+            raise ValueError(f"{where}: {name}[{i}] must be [n_layers, {n_pages}, " +
+                             (f"parts, 128], got {s}" if scales else f"128, ...], got {s}"))
+        out.append(PagePool(t.data_ptr(), lead, parts, row))
+    return out
+
+
+def llama_beam_reorder_paged(parents, n_cached, n_cached_out, block_table, block_table_out, free_pages, n_pages, kv_pools,
+                             scale_pools, freed_pages, counts, ws, stream=None):
+    """The paged cache follows parents int32 [B, W]: n_cached [B * W] and block_table [B * W, max_pages] to their _out
+    tensors (which may be the same), open pages copied in every pool.  kv_pools: tensors [n_layers, n_pages, 128, n_kv, hd]
+    (or without the first axis); scale_pools: [n_layers, n_pages, n_kv, 128], or ()."""
+    w = "llama_beam_reorder_paged"
+    L, torch, dev, st = _here(stream)
+    i32 = torch.int32
+    B, W = parents.shape
+    P = block_table.shape[-1]
+    records = _pools(w, "kv_pools", kv_pools, dev, n_pages, False) + _pools(w, "scale_pools", scale_pools, dev, n_pages, True)
+    arr = (PagePool * max(1, len(records)))(*records)
+    _check(L.llama_beam_reorder_paged(
+        _arg(w, "parents", parents, i32, dev), B, W, _arg(w, "n_cached", n_cached, i32, dev, (B * W,)),
+        _arg(w, "n_cached_out", n_cached_out, i32, dev, (B * W,)), _arg(w, "block_table", block_table, i32, dev, (B * W, P)),
+        _arg(w, "block_table_out", block_table_out, i32, dev, (B * W, P)), P, _arg(w, "free_pages", free_pages, i32, dev),
+        free_pages.numel(), n_pages, arr, len(records), _arg(w, "freed_pages", freed_pages, i32, dev), freed_pages.numel(),
+        _arg(w, "counts", counts, i32, dev, (2,)), *_scratch(w, ws, dev), st), w)
 
 
 def llama_workspace_bytes(op, dims, dtype, n_layers=0, vocab=0, kv_capacity=0) -> int:

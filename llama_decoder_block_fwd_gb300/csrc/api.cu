@@ -824,7 +824,8 @@ int llama_get_device_status(int* out, void* stream) {
              bounds_read_clear_gemm_tc2() | bounds_read_clear_gemm_skinny() | bounds_read_clear_attn_tc() |
              bounds_read_clear_decode_attn() | bounds_read_clear_decode_attn8() | bounds_read_clear_decode_fin() |
              bounds_read_clear_sample() | bounds_read_clear_selftest() | bounds_read_clear_paged() |
-             bounds_read_clear_chunk_attn() | bounds_read_clear_verify();
+             bounds_read_clear_chunk_attn() | bounds_read_clear_verify() | bounds_read_clear_paged8() |
+             bounds_read_clear_decode_attn8p() | bounds_read_clear_beam();
   *out = (v & STATUS_TIMEOUT) ? LLAMA_ERR_TIMEOUT
          : bounds             ? LLAMA_ERR_BOUNDS
          : (v & (STATUS_BAD_TOKEN | STATUS_BAD_PLAN)) ? LLAMA_ERR_INVALID_ARG
@@ -878,6 +879,19 @@ size_t llama_workspace_bytes(int op, const llama_dims* d, int dtype, int n_layer
       return chunk_dims_ok(d, dtype) ? chunk_attn_ws_bytes(d->B, d->S, d->n_q, d->n_kv, d->head_dim, kv_capacity - 1) : 0;
     case LLAMA_OP_VERIFY_DRAFTS:
       return d->S > 0 && vocab > 0 && verify_supported(d->S, vocab) ? verify_ws_bytes(d->S, vocab) : 0;
+    case LLAMA_OP_GQA_ATTENTION_DECODE_PAGED_KV8:
+      return dtype == LLAMA_BF16 && check_dims(d, NEED_HEADS) == LLAMA_OK && d->B > 0 && kv_capacity > 0 && kv_capacity <= kMaxPos &&
+                     decode_attn8p_supported(d->B, d->n_q, d->n_kv, d->head_dim)
+                 ? decode_attn8p_ws_bytes(d->B, d->n_q, d->n_kv, d->head_dim, kv_capacity - 1)
+                 : 0;
+    case LLAMA_OP_BEAM_SELECT:
+      return d->B > 0 && d->S > 0 && vocab > 0 && vocab <= (int64_t(1) << 30) && beam_select_supported(d->B, d->S)
+                 ? beam_select_ws_bytes(d->B, d->S, vocab)
+                 : 0;
+    case LLAMA_OP_BEAM_REORDER_PAGED:
+      return d->B > 0 && d->S > 0 && d->B <= kPlanMaxSeqs && d->S <= kBeamMaxW && kv_capacity > 0 && kv_capacity <= kMaxPos
+                 ? beam_reorder_ws_bytes(d->B, d->S, (kv_capacity + 127) / 128)
+                 : 0;
     default: return 0;
   }
 }
@@ -1294,6 +1308,169 @@ int llama_verify_drafts(const float* logits, int64_t n_tokens, int64_t vocab, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof::begin("verify_drafts", st);
   const int rc = launch_verify(v, num_sms(), status, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_rope_append_paged_kv8(const llama_dims* d, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, const int32_t* positions, const int32_t* slots,
+                                void* q_out, void* k_codes, float* k_scale, void* v_codes, float* v_scale,
+                                int64_t n_pages, void* stream) {
+  int rc;
+  if ((rc = check_packed(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if (d->head_dim % 8 != 0 || d->S > INT32_MAX - 8 || d->n_q > 4096 || d->n_kv > 4096) return LLAMA_ERR_UNSUPPORTED;
+  if (!q != !q_out || n_pages < 1) return LLAMA_ERR_INVALID_ARG;
+  if ((q && q_stride < d->n_q * d->head_dim) || k_stride < d->n_kv * d->head_dim || v_stride < d->n_kv * d->head_dim)
+    return LLAMA_ERR_INVALID_ARG;
+  if (q && q_out == q && q_stride != d->n_q * d->head_dim) return LLAMA_ERR_INVALID_ARG;
+  if (n_pages > INT32_MAX / 128) return LLAMA_ERR_UNSUPPORTED;
+  if (d->S == 0) return LLAMA_OK;
+  if (!k || !v || !k_codes || !k_scale || !v_codes || !v_scale || !positions || !slots) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[8] = {q, k, v, q_out, k_codes, k_scale, v_codes, v_scale};
+  for (const void* p : ps)
+    if (!aligned16(p)) return LLAMA_ERR_ALIGNMENT;
+  if ((q && q_stride % 8) || k_stride % 8 || v_stride % 8 || ((uintptr_t)positions & 3) || ((uintptr_t)slots & 3))
+    return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  RopeFreq f[kMaxRopePairs];
+  rope_freqs(d, f);
+  Append8Desc a;
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.positions = positions; a.slots = slots;
+  a.q_out = q_out; a.k_codes = k_codes; a.v_codes = v_codes; a.k_scale = k_scale; a.v_scale = v_scale;
+  a.T = d->S; a.n_q = d->n_q; a.n_kv = d->n_kv; a.hd = d->head_dim; a.n_pages = n_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("rope_append_paged_kv8", st);
+  rc = launch_rope_append8(a, f, num_sms(), status, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_kv_dequantize_paged(const llama_dims* d, const void* k_codes, const float* k_scale, const void* v_codes,
+                              const float* v_scale, int64_t n_pages, const int32_t* block_table, int64_t max_pages,
+                              const int32_t* n_pos, void* k_pool, void* v_pool, void* stream) {
+  if (!d || d->B < 0 || d->n_kv <= 0 || d->head_dim <= 0 || n_pages < 1 || max_pages < 1) return LLAMA_ERR_INVALID_ARG;
+  if (d->head_dim % 8 != 0 || d->head_dim > 2 * kMaxRopePairs || d->n_kv > 4096 || d->B > 65535 || n_pages > INT32_MAX / 128 ||
+      max_pages > INT32_MAX)
+    return LLAMA_ERR_UNSUPPORTED;
+  if (d->B == 0) return LLAMA_OK;
+  if (!k_codes || !k_scale || !v_codes || !v_scale || !block_table || !n_pos || !k_pool || !v_pool) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[6] = {k_codes, k_scale, v_codes, v_scale, k_pool, v_pool};
+  for (const void* p : ps)
+    if (!aligned16(p)) return LLAMA_ERR_ALIGNMENT;
+  if (((uintptr_t)block_table & 3) || ((uintptr_t)n_pos & 3)) return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  Dequant8Desc a;
+  a.k_codes = k_codes; a.v_codes = v_codes; a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.n_pos = n_pos;
+  a.k_pool = k_pool; a.v_pool = v_pool;
+  a.B = d->B; a.n_kv = d->n_kv; a.hd = d->head_dim; a.n_pages = n_pages; a.max_pages = max_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("kv_dequantize_paged", st);
+  const int rc = launch_kv_dequant_paged(a, num_sms(), status, st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_gqa_attention_decode_paged_kv8(const llama_dims* d, const void* q, const void* k_codes, const float* k_scale,
+                                         const void* v_codes, const float* v_scale, int64_t n_pages,
+                                         const int32_t* block_table, int64_t max_pages, const int32_t* seq_pos,
+                                         int64_t max_pos, void* o, void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(d, NEED_HEADS)) != LLAMA_OK) return rc;
+  if (d->S != 1 || n_pages < 1 || max_pages < 1 || max_pos < 0 || max_pos / 128 >= max_pages || max_pos + 1 > kMaxPos)
+    return LLAMA_ERR_INVALID_ARG;
+  if (n_pages > INT32_MAX / 128 || max_pages > INT32_MAX) return LLAMA_ERR_UNSUPPORTED;
+  if (d->B == 0) return LLAMA_OK;
+  if (!decode_attn8p_supported(d->B, d->n_q, d->n_kv, d->head_dim)) return LLAMA_ERR_UNSUPPORTED;
+  if (!q || !k_codes || !k_scale || !v_codes || !v_scale || !block_table || !seq_pos || !o) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[6] = {q, k_codes, k_scale, v_codes, v_scale, o};
+  for (const void* p : ps)
+    if (!aligned16(p)) return LLAMA_ERR_ALIGNMENT;
+  if (((uintptr_t)block_table & 3) || ((uintptr_t)seq_pos & 3)) return LLAMA_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < decode_attn8p_ws_bytes(d->B, d->n_q, d->n_kv, d->head_dim, max_pos)) return LLAMA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  DecodeAttn8pDesc a;
+  a.q = q; a.k_codes = k_codes; a.v_codes = v_codes; a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.seq_pos = seq_pos; a.o = o;
+  a.B = d->B; a.n_q = d->n_q; a.n_kv = d->n_kv; a.hd = d->head_dim;
+  a.n_pages = n_pages; a.max_pages = max_pages; a.max_pos = max_pos;
+  a.scale = (float)(1.0 / std::sqrt((double)d->head_dim));
+  a.ws = ws;
+  a.status = status_ptr();
+  if (!a.status) return LLAMA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("attn_decode_paged_kv8", st);
+  rc = launch_decode_attn8p(a, num_sms(), st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_beam_select(const float* logits, int64_t B, int64_t W, int64_t vocab, int64_t ld, const float* scores,
+                      const int32_t* finished, int32_t pad_token, int64_t n_out, int32_t* parents, int32_t* tokens,
+                      float* out_scores, void* ws, size_t ws_bytes, void* stream) {
+  if (B < 0 || W < 1 || n_out < 1 || vocab < 1 || vocab > (int64_t(1) << 30) || ld < vocab) return LLAMA_ERR_INVALID_ARG;
+  if (finished && (pad_token < 0 || pad_token >= vocab)) return LLAMA_ERR_INVALID_ARG;
+  if (n_out > kBeamMaxOut || !beam_select_supported(B, W)) return LLAMA_ERR_UNSUPPORTED;
+  if (B == 0) return LLAMA_OK;
+  if (!logits || !scores || !parents || !tokens || !out_scores) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[6] = {logits, scores, finished, parents, tokens, out_scores};
+  for (const void* p : ps)
+    if ((uintptr_t)p & 3) return LLAMA_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < beam_select_ws_bytes(B, W, vocab)) return LLAMA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  BeamSelectDesc a;
+  a.logits = logits; a.B = B; a.W = W; a.V = vocab; a.ld = ld; a.n_out = n_out;
+  a.scores = scores; a.finished = finished; a.pad_token = pad_token;
+  a.parents = parents; a.tokens = tokens; a.out_scores = out_scores;
+  a.ws = ws;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("beam_select", st);
+  const int rc = launch_beam_select(a, num_sms(), st);
+  prof::end(st);
+  return rc ? LLAMA_ERR_CUDA : launch_status();
+}
+
+int llama_beam_reorder_paged(const int32_t* parents, int64_t B, int64_t W, const int32_t* n_cached, int32_t* n_cached_out,
+                             const int32_t* block_table, int32_t* block_table_out, int64_t max_pages,
+                             const int32_t* free_pages, int64_t n_free, int64_t n_pages, const llama_page_pool* pools,
+                             int n_pools, int32_t* freed_pages, int64_t freed_room, int32_t* counts, void* ws,
+                             size_t ws_bytes, void* stream) {
+  if (B < 0 || W < 1 || max_pages < 1 || n_free < 0 || n_pages < 1 || n_pools < 0 || freed_room < 0) return LLAMA_ERR_INVALID_ARG;
+  if (W > kBeamMaxW || B > kPlanMaxSeqs || n_pages > INT32_MAX / 128 || max_pages > kMaxPos / 128 || n_free > INT32_MAX ||
+      freed_room > INT32_MAX || n_pools > kBeamMaxPools)
+    return LLAMA_ERR_UNSUPPORTED;
+  if (n_pools > 0 && !pools) return LLAMA_ERR_INVALID_ARG;
+  for (int k = 0; k < n_pools; ++k) {
+    const llama_page_pool& q = pools[k];
+    if (q.n_layers < 1 || q.parts < 1 || q.row_bytes < 1 || q.row_bytes % 4) return LLAMA_ERR_INVALID_ARG;
+    constexpr int64_t most = 1 << 24;
+    if (q.n_layers > 65536 || q.parts > most || q.row_bytes > most || q.parts * q.row_bytes > most) return LLAMA_ERR_UNSUPPORTED;
+    if (!q.base) return LLAMA_ERR_INVALID_ARG;
+    if (!aligned16(q.base)) return LLAMA_ERR_ALIGNMENT;
+  }
+  if (beam_copy_units(pools, n_pools) > (int64_t(1) << 30)) return LLAMA_ERR_UNSUPPORTED;
+  if (!counts || (n_free > 0 && !free_pages) || (freed_room > 0 && !freed_pages)) return LLAMA_ERR_INVALID_ARG;
+  if (B > 0 && (!parents || !n_cached || !n_cached_out || !block_table || !block_table_out)) return LLAMA_ERR_INVALID_ARG;
+  const void* ps[8] = {parents, n_cached, n_cached_out, block_table, block_table_out, free_pages, freed_pages, counts};
+  for (const void* p : ps)
+    if ((uintptr_t)p & 3) return LLAMA_ERR_ALIGNMENT;
+  if (B > 0 && (!ws || ws_bytes < beam_reorder_ws_bytes(B, W, max_pages))) return LLAMA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
+  BeamReorderDesc a;
+  a.parents = parents; a.n_cached = n_cached; a.table = block_table; a.free_pages = free_pages;
+  a.n_cached_out = n_cached_out; a.table_out = block_table_out; a.freed = freed_pages; a.counts = counts;
+  a.B = B; a.W = W; a.max_pages = max_pages; a.n_free = n_free; a.n_pages = n_pages; a.freed_room = freed_room;
+  a.pools = pools; a.n_pools = n_pools;
+  a.ws = ws;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof::begin("beam_reorder_paged", st);
+  const int rc = launch_beam_reorder(a, num_sms(), status, st);
   prof::end(st);
   return rc ? LLAMA_ERR_CUDA : launch_status();
 }

@@ -20,8 +20,7 @@
 #include <cmath>
 #include <cstring>
 
-#include <cuda_fp16.h>
-
+#include "e4m3.cuh"
 #include "kernels.h"
 
 namespace llama {
@@ -115,18 +114,6 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// Two floats to two E4M3 codes (round to nearest even, saturating): a in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
-  return c;
-}
-// Two E4M3 codes (low byte first) back to floats.
-__device__ __forceinline__ float2 e4m3x2_to_f2(uint32_t c) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(c));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 // x = hi + lo in E4M3 (both codes of each pair in one byte, a first): returns hi codes, sets lo codes.
 __device__ __forceinline__ uint32_t split_e4m3x2(float a, float b, uint32_t& lo) {
   const uint32_t hi = e4m3x2(a, b);

@@ -28,6 +28,9 @@ unsigned bounds_read_clear_selftest();
 unsigned bounds_read_clear_paged();
 unsigned bounds_read_clear_chunk_attn();
 unsigned bounds_read_clear_verify();
+unsigned bounds_read_clear_paged8();
+unsigned bounds_read_clear_decode_attn8p();
+unsigned bounds_read_clear_beam();
 
 // What a GEMM does with its fp32 result D[r, c] (r < M, c < N).
 enum EpiKind : int {
@@ -247,6 +250,69 @@ struct VerifyDesc {
 bool verify_supported(int64_t T, int64_t V);
 size_t verify_ws_bytes(int64_t T, int64_t V);
 int launch_verify(const VerifyDesc& d, int num_sms, unsigned* status, cudaStream_t st);
+
+// paged8.cu: an 8-bit paged cache written (RoPE, a scale per position and KV head) and read back to bf16 pages
+struct Append8Desc {
+  const void *q, *k, *v;                 // q may be null with q_out
+  int64_t q_stride, k_stride, v_stride;
+  const int *positions, *slots;
+  void *q_out, *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  int64_t T, n_q, n_kv, hd, n_pages;
+};
+int launch_rope_append8(const Append8Desc& d, const RopeFreq* freq, int num_sms, unsigned* status, cudaStream_t st);
+struct Dequant8Desc {
+  const void *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int *block_table, *n_pos;        // [B, max_pages], [B]
+  void *k_pool, *v_pool;
+  int64_t B, n_kv, hd, n_pages, max_pages;
+};
+int launch_kv_dequant_paged(const Dequant8Desc& d, int num_sms, unsigned* status, cudaStream_t st);
+
+// decode_attn8p.cu: one-token attention over an 8-bit paged cache with a scale per position and KV head
+struct DecodeAttn8pDesc {
+  const void* q;                         // [B, n_q, hd]
+  const void *k_codes, *v_codes;         // [n_pages, 128, n_kv, hd]
+  const float *k_scale, *v_scale;        // [n_pages, n_kv, 128]
+  const int *block_table, *seq_pos;      // [B, max_pages], [B]
+  void* o;
+  int64_t B, n_q, n_kv, hd, n_pages, max_pages, max_pos;
+  float scale;
+  void* ws;
+  unsigned* status;
+};
+bool decode_attn8p_supported(int64_t B, int64_t n_q, int64_t n_kv, int64_t hd);
+size_t decode_attn8p_ws_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_pos);
+int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st);
+
+// beam.cu: the next beams, and the paged cache made to follow them
+constexpr int64_t kBeamMaxOut = 64, kBeamMaxW = 32;
+struct BeamSelectDesc {
+  const float* logits;                   // [B W, ld]
+  int64_t B, W, V, ld, n_out;
+  const float* scores;                   // [B, W]
+  const int* finished;                   // [B, W] or null
+  int pad_token;
+  int *parents, *tokens;                 // [B, n_out]
+  float* out_scores;
+  void* ws;
+};
+bool beam_select_supported(int64_t B, int64_t W);
+size_t beam_select_ws_bytes(int64_t B, int64_t W, int64_t V);
+int launch_beam_select(const BeamSelectDesc& d, int num_sms, cudaStream_t st);
+constexpr int kBeamMaxPools = 8;
+struct BeamReorderDesc {
+  const int *parents, *n_cached, *table, *free_pages;
+  int *n_cached_out, *table_out, *freed, *counts;
+  int64_t B, W, max_pages, n_free, n_pages, freed_room;
+  const llama_page_pool* pools;
+  int n_pools;
+  void* ws;
+};
+int64_t beam_copy_units(const llama_page_pool* pools, int n_pools);   // of one page's copy, over pools and layers
+size_t beam_reorder_ws_bytes(int64_t B, int64_t W, int64_t max_pages);
+int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status, cudaStream_t st);
 
 // The current device's status word (device address) and SM count.
 unsigned* status_ptr();
