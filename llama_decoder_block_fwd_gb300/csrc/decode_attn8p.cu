@@ -1,8 +1,28 @@
-// One-token GQA attention over an 8-bit paged cache with a scale per position and KV head.
+// One-token GQA attention over an 8-bit paged cache with a scale per position and KV head ("LLaMA-3 8B ...", section 九:
+// a decode step reads every cached key and value once; 8-bit rows halve that).
 //
 //   o_h = sum_j exp(s_hj) vs_j c_j / sum_j exp(s_hj),   s_hj = ks_j (q_h . kc_j) / sqrt(hd)
 //
 // kc_j, c_j the E4M3 codes of key and value j of the query head's KV head, ks_j, vs_j their scales.
+//
+// What bounds it: the codes and scales are read once, 2 (hd + 4) bytes per position and KV head, at a few operations
+// per byte, so HBM does, where there are enough tiles, and the latency of one tile's chain where there are few.
+//
+// Tiles.  A tile is one page (128 positions) by 128 bytes of a row: one KV head of 128, or two of 64 side by side, which
+//   one product serves (each head's query rows hold zeros in the other's bytes).  tcgen05 kind::f8f6f4 reads the codes as
+//   TMA lands them: S^T = K Q^T (M = 128 keys) and O^T += V^T P^T (M = 128 bytes of the row, V as the MN-major operand).
+//   One thread per key does the softmax of its tile; the scales come with the tile by bulk copies, a head's 128
+//   scales of a page being contiguous.
+// Operands.  The other side is E4M3 too, so q and P enter as x = hi + 2^-5 lo, hi = e4m3(x), lo = e4m3(32 (x - hi)): 8
+//   significant bits, and 2^-5 below the format's smallest step for what is small beside its row's largest (the
+//   tail beside one heavy key).  The lo rows ride in the padding of the operand's N = 16 (32 for 16 rows).
+// Scales.  A key's scale multiplies its row of S^T.  A value's scale cannot leave the sum over keys, so P holds
+//   w_j = exp(s_j) vs_j, as 2^(s_j + log2 vs_j - m) with m the running maximum of that exponent: the largest
+//   product, not the largest weight, has the format's full precision.  The sum of weights is that of w_j / vs_j in fp32.
+// Split.  The pages of all sequences, one after the other, are cut into equal ranges; range i of head group g is CTA
+//   i * groups + g, so the CTAs that run side by side read all heads of the same pages (a page's rows are contiguous
+//   over heads).  A sequence inside one range is finished there; of one that a cut goes through, each range leaves a part
+//   (m, l, O) in the workspace, at most two parts a range, and a second kernel joins them.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -13,81 +33,640 @@
 namespace llama {
 namespace {
 
-struct DecodeAttn8pParams {
+constexpr int DP_THREADS = 224;   // warp 0 TMA, 1 MMA, 2-5 softmax, 6 q -> E4M3 hi / lo
+// two CTAs per SM (2 x 108.8 KB of shared memory), so that one's hand-offs overlap the other's
+constexpr int DP_KSTAGES = 3;
+constexpr int DP_VSTAGES = 2;
+constexpr int DP_SSTAGES = 4;     // scales
+constexpr int DP_CTAS_PER_SM = 2;
+constexpr uint32_t DP_TMEM_COLS = 128;   // S^T 2 x NP (cols 0..63), O^T NP (cols 64..)
+// O and l keep their reference until a tile's maximum exceeds it by 2 (log2), so w <= 4 before the 2^6 below
+// and w * 2^6 <= 256 stays under E4M3's 448 (the factor cancels in O / l); 32 (x - hi) <= 256 there too.
+constexpr float kDpRescaleLog2 = 2.0f;
+constexpr float kDpPScaleLog2 = 6.0f;
+constexpr float kDpLo = 32.0f;
+
+struct SplitInfo { int b, last; };   // the sequence whose first part is this range's tail (-1: none), the range of its last part
+
+struct DecodeAttn8pParams {   // 128-byte aligned by its tensor maps
+  CUtensorMap tmK;   // codes as [n_pages * 128, n_kv * hd] bytes, box (128, 128), 128-byte swizzle
+  CUtensorMap tmV;
   const uint16_t* q;
-  const uint8_t *k_codes, *v_codes;
   const float *k_scale, *v_scale;
   const int *block_table, *seq_pos;
   uint16_t* o;
-  int B, n_q, n_kv, n_pages;
+  float* part_o;       // [2 n_ranges, groups, R, 128]
+  float2* part_ml;     // [2 n_ranges, groups, R]  (m in log2 units, l)
+  SplitInfo* split;    // [n_ranges]
+  int B, n_q, n_kv, r, hd, n_pages, max_pos;
+  int n_ranges, groups, subs;   // group = (packed KV heads, block of their query heads)
   int64_t max_pages;
-  int max_pos;
   float scale_log2;
   unsigned* status;
 };
 
-// One CTA per (sequence, query head); thread t scores key t of each page and keeps output element t.
-template <int HD>
-__global__ void __launch_bounds__(128) decode_attn8p_kernel(const __grid_constant__ DecodeAttn8pParams p) {
-  __shared__ float q[HD], w[128], red[4];
-  const int b = blockIdx.y, h = blockIdx.x, g = h / (p.n_q / p.n_kv), t = threadIdx.x;
-  int pos = __ldg(p.seq_pos + b);
-  if (pos < -1 || pos > p.max_pos) {
-    if (t == 0) atomicOr(p.status, STATUS_BAD_PLAN);
-    pos = -1;
-  }
-  if (t < HD) q[t] = bf2f(p.q[((int64_t)b * p.n_q + h) * HD + t]) * p.scale_log2;
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j = 0; j * 128 <= pos; ++j) {
-    const int page = __ldg(p.block_table + (int64_t)b * p.max_pages + j);
-    if (page < 0 || page >= p.n_pages) {
-      if (t == 0) atomicOr(p.status, STATUS_BAD_PLAN);
-      continue;
+struct DpSmem {
+  static constexpr uint32_t F8 = 128 * 128;     // one code tile
+  static constexpr uint32_t OPB = 32 * 128;     // q or P operand: up to 32 rows of 128 codes
+  static constexpr uint32_t SC = 4 * 512;       // scales of a tile: K of two heads, V of two heads
+  static constexpr uint32_t OFF_K8 = 0;
+  static constexpr uint32_t OFF_V8 = OFF_K8 + DP_KSTAGES * F8;
+  static constexpr uint32_t OFF_Q = OFF_V8 + DP_VSTAGES * F8;  // 2 buffers
+  static constexpr uint32_t OFF_P = OFF_Q + 2 * OPB;           // 2 buffers
+  static constexpr uint32_t OFF_SC = OFF_P + 2 * OPB;
+  static constexpr uint32_t OFF_RED = OFF_SC + DP_SSTAGES * SC;  // [3][4][16] floats
+  static constexpr uint32_t OFF_QS = OFF_RED + 3 * 4 * 16 * 4;   // inverse q scales [2][16]
+  static constexpr uint32_t OFF_BAR = OFF_QS + 2 * 16 * 4;
+  static constexpr uint32_t TOTAL = OFF_BAR + 512 + 1024;
+};
+static_assert(DP_CTAS_PER_SM * (DpSmem::TOTAL + 1024) <= 233472, "two CTAs per SM");
+
+enum : int {   // barrier slots
+  P_KF = 0, P_VF = 3, P_KE = 5, P_VE = 8, P_QR = 10, P_QE = 12, P_SF = 14, P_SFREE = 16, P_PF = 18, P_OD = 20, P_OFREE = 22,
+  P_DRAIN = 23, P_QC = 24, P_SCF = 26, P_SCE = 30, P_COUNT = 34
+};
+
+__device__ __forceinline__ void tmem_ld16_dp(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void softmax_sync_dp() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ float warp_max_dp(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format 0) and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn_major = false) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// x = hi + lo / 32 in E4M3 (a first): returns hi codes, sets lo codes.
+__device__ __forceinline__ uint32_t split_fine(float a, float b, uint32_t& lo) {
+  const uint32_t hi = e4m3x2(a, b);
+  const float2 h = e4m3x2_to_f2(hi);
+  lo = e4m3x2((a - h.x) * kDpLo, (b - h.y) * kDpLo);
+  return hi;
+}
+// Byte offset of (row n, byte c) in a K-major operand of 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128_at(int n, int c) {
+  return (uint32_t)(n * 128 + ((((c >> 4) ^ (n & 7))) << 4) + (c & 15));
+}
+
+// ---- the work split
+__device__ __forceinline__ int good_pos(int pos, int max_pos) { return pos < -1 || pos > max_pos ? -1 : pos; }
+__device__ __forceinline__ int tiles_at(const DecodeAttn8pParams& p, int b) {
+  return (good_pos(__ldg(p.seq_pos + b), p.max_pos) + 128) / 128;
+}
+__device__ __forceinline__ int64_t range_first(int64_t T, int n, int i) { return (int64_t)i * T / n; }
+// The range that holds tile x.
+__device__ __forceinline__ int range_with(int64_t T, int n, int64_t x) {
+  int i = (int)min((int64_t)n - 1, x * n / T);
+  while (i + 1 < n && range_first(T, n, i + 1) <= x) ++i;
+  while (i > 0 && range_first(T, n, i) > x) --i;
+  return i;
+}
+
+// The pieces of a CTA's range: tiles [t0, t1) of sequence b, n_keys positions in all.
+struct Pieces { int b, t; int64_t left; int next_pos; };
+__device__ __forceinline__ bool next_piece(const DecodeAttn8pParams& p, Pieces& s, int& b, int& t0, int& t1, int& nt, int& n_keys) {
+  if (s.left <= 0) return false;
+  int pos = good_pos(s.next_pos, p.max_pos);
+  while (pos < 0 && s.b + 1 < p.B) pos = good_pos(__ldg(p.seq_pos + ++s.b), p.max_pos);   // empty sequences have no tiles
+  if (pos < 0) return false;
+  b = s.b;
+  t0 = s.t;
+  nt = (pos + 128) / 128;
+  t1 = (int)min((int64_t)nt, t0 + s.left);
+  n_keys = pos + 1;
+  s.left -= t1 - t0;
+  s.t = 0;
+  if (s.left > 0 && s.b + 1 < p.B) s.next_pos = __ldg(p.seq_pos + ++s.b);   // on its way while this piece runs
+  return true;
+}
+
+// R query rows per CTA: R / PACK query heads of each of its PACK KV heads.
+template <int R, int PACK>
+__global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kernel(const __grid_constant__ DecodeAttn8pParams p) {
+  using L = DpSmem;
+  constexpr int HD = 128 / PACK, RH = R / PACK;
+  constexpr int NP = R <= 8 ? 16 : 32;   // operand rows: hi 0..R-1, lo R..2R-1, zero padding
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + P_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* start = reinterpret_cast<int*>(tmem_slot + 2);                  // first sequence and tile of the range
+  int64_t* wsum = reinterpret_cast<int64_t*>(bars + P_COUNT + 2);      // [7]
+  float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
+  float* qinv = reinterpret_cast<float*>(smem + L::OFF_QS);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int range = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
+  const int g0 = group / p.subs * PACK, sub = group % p.subs;          // first KV head, block of query heads
+  // query head of row h, -1 for a padding row
+  auto head_of = [&](int h) {
+    const int g = g0 + h / RH, i = sub * RH + h % RH;
+    return g < p.n_kv && i < p.r ? g * p.r + i : -1;
+  };
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < P_COUNT; ++i) {
+      int cnt = 1;
+      if (i == P_QR || i == P_QR + 1) cnt = 32;
+      if (i == P_SFREE || i == P_SFREE + 1 || i == P_PF || i == P_PF + 1 || i == P_OFREE || i == P_QC || i == P_QC + 1 ||
+          (i >= P_SCE && i < P_SCE + DP_SSTAGES))
+        cnt = 128;
+      mbar_init(&bars[i], cnt);
     }
-    const int n = min(128, pos + 1 - j * 128);
-    const int64_t row0 = (int64_t)page * 128, s0 = ((int64_t)page * p.n_kv + g) * 128;
-    float s = -INFINITY;
-    if (t < n) {
-      const uint4* kc = reinterpret_cast<const uint4*>(p.k_codes + ((row0 + t) * p.n_kv + g) * HD);
-      float d = 0.f;
-      for (int i = 0; i < HD / 16; ++i) {
-        const uint4 c = kc[i];
-        const uint32_t e[4] = {c.x, c.y, c.z, c.w};
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
+  }
+  // the padding rows and, of packed heads, the other head's bytes stay zero in the q and P operands
+  for (int i = threadIdx.x; i < (int)(4 * L::OPB) / 16; i += DP_THREADS)
+    reinterpret_cast<uint4*>(smem + L::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  if (warp == 1) { tmem_alloc(tmem_slot, DP_TMEM_COLS); tmem_relinquish(); }
+
+  // tiles of all sequences: thread i adds up the contiguous sequences [i * per, (i + 1) * per)
+  const int per = (p.B + DP_THREADS - 1) / DP_THREADS;
+  const int s0 = min(p.B, (int)threadIdx.x * per), s1 = min(p.B, s0 + per);
+  int64_t mine = 0;
+  for (int b = s0; b < s1; ++b) {
+    const int pos = __ldg(p.seq_pos + b);
+    const int nt = (good_pos(pos, p.max_pos) + 128) / 128;
+    mine += nt;
+    if (blockIdx.x == 0 && pos != good_pos(pos, p.max_pos)) atomicOr(p.status, STATUS_BAD_PLAN);
+    if (nt == 0 && b % p.n_ranges == range) {   // nothing to attend to: this group's rows are zeros
+      for (int h = 0; h < R; ++h) {
+        const int64_t at = ((int64_t)b * p.n_q + head_of(h)) * HD;
+        if (head_of(h) >= 0 && in_extent(at, HD, (int64_t)p.B * p.n_q * HD))
+          for (int i = 0; i < HD / 8; ++i) reinterpret_cast<uint4*>(p.o + at)[i] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  int64_t upto = mine;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = e4m3x2_to_f2(e[k] & 0xFFFFu), hi = e4m3x2_to_f2(e[k] >> 16);
-          d += q[i * 16 + k * 4] * lo.x + q[i * 16 + k * 4 + 1] * lo.y + q[i * 16 + k * 4 + 2] * hi.x + q[i * 16 + k * 4 + 3] * hi.y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) wsum[warp] = upto;
+  __syncthreads();
+  int64_t T = 0, first = upto - mine;
+  for (int w = 0; w < DP_THREADS / 32; ++w) {
+    if (w < warp) first += wsum[w];
+    T += wsum[w];
+  }
+  // no more ranges than tiles, so that each of them has some and leaves its parts; CTAs past them have nothing to do
+  const int n_ranges = (int)min((int64_t)p.n_ranges, T);
+  const int64_t x0 = range < n_ranges ? range_first(T, n_ranges, range) : 0;
+  const int64_t x1 = range < n_ranges ? range_first(T, n_ranges, range + 1) : 0;
+  if (x0 < x1) {
+    if (first <= x0 && x0 < first + mine) {
+      int64_t off = first;
+      int b = s0, nt = tiles_at(p, b);
+      while (off + nt <= x0) { off += nt; nt = tiles_at(p, ++b); }
+      start[0] = b;
+      start[1] = (int)(x0 - off);
+    }
+    if (group == 0 && first <= x1 - 1 && x1 - 1 < first + mine) {
+      int64_t off = first;
+      int b = s0, nt = tiles_at(p, b);
+      while (off + nt <= x1 - 1) { off += nt; nt = tiles_at(p, ++b); }
+      SplitInfo s{-1, 0};
+      if (off >= x0 && off + nt > x1) { s.b = b; s.last = range_with(T, n_ranges, off + nt - 1); }
+      if (in_extent(range, 1, p.n_ranges)) p.split[range] = s;
+    }
+  } else if (group == 0 && threadIdx.x == 0 && in_extent(range, 1, p.n_ranges)) {
+    p.split[range] = SplitInfo{-1, 0};
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem;          // S^T buffers: columns 0..NP-1 and NP..2NP-1
+  const uint32_t tO = tmem + 64;     // O^T: columns 64..64+NP-1
+  const uint32_t sbase = smem_u32(smem);
+  Pieces it0;
+  it0.left = x1 - x0;
+  it0.b = x0 < x1 ? start[0] : 0;
+  it0.t = x0 < x1 ? start[1] : 0;
+  it0.next_pos = x0 < x1 ? __ldg(p.seq_pos + it0.b) : -1;
+  int b, t0, t1, nt, n_keys;
+
+  if (warp == 0) {  // -------------------------------------------------------- TMA producer
+    // V(j) is requested one tile after K(j): P V needs it only after S^T and the softmax of its tile
+    const int n_sc = min(PACK, p.n_kv - g0);        // heads whose scales there are
+    int tile = 0, v_page = 0;
+    bool ok = true;
+    auto issue_v = [&](int gt) -> bool {
+      const int vs = gt % DP_VSTAGES;
+      if (!mbar_wait(&bars[P_VE + vs], ((gt / DP_VSTAGES) & 1) ^ 1, abort_flag, p.status)) return false;
+      if (!box_in(g0 * HD, p.n_kv * HD, (int64_t)v_page * 128, (int64_t)p.n_pages * 128)) { *abort_flag = 1; return false; }
+      mbar_arrive_expect_tx(&bars[P_VF + vs], L::F8);
+      tma_load_2d(sbase + L::OFF_V8 + vs * L::F8, &p.tmV, &bars[P_VF + vs], g0 * HD, v_page * 128);
+      return true;
+    };
+    Pieces s = it0;
+    while (ok && next_piece(p, s, b, t0, t1, nt, n_keys)) {
+      const int* row = p.block_table + (int64_t)b * p.max_pages;
+      int ids = 0;
+      for (int t = t0; t < t1; ++t, ++tile) {
+        if (((t - t0) & 31) == 0) {                 // the pages of the next 32 tiles, one per lane
+          ids = t + lane < t1 ? __ldg(row + t + lane) : 0;
+          if (ids < 0 || ids >= p.n_pages) { atomicOr(p.status, STATUS_BAD_PLAN); ids = 0; }
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, (t - t0) & 31);
+        if (lane == 0) {
+          const int ks = tile % DP_KSTAGES, sc = tile % DP_SSTAGES;
+          ok = mbar_wait(&bars[P_KE + ks], ((tile / DP_KSTAGES) & 1) ^ 1, abort_flag, p.status) &&
+               mbar_wait(&bars[P_SCE + sc], ((tile / DP_SSTAGES) & 1) ^ 1, abort_flag, p.status);
+          if (ok && !box_in(g0 * HD, p.n_kv * HD, (int64_t)page * 128, (int64_t)p.n_pages * 128)) { *abort_flag = 1; ok = false; }
+          if (ok) {
+            mbar_arrive_expect_tx(&bars[P_KF + ks], L::F8);
+            tma_load_2d(sbase + L::OFF_K8 + ks * L::F8, &p.tmK, &bars[P_KF + ks], g0 * HD, page * 128);
+            const uint32_t bytes = n_sc * 512, dst = sbase + L::OFF_SC + sc * L::SC;
+            const int64_t at = ((int64_t)page * p.n_kv + g0) * 128;
+            mbar_arrive_expect_tx(&bars[P_SCF + sc], 2 * bytes);
+            bulk_load(dst, p.k_scale + at, bytes, &bars[P_SCF + sc]);
+            bulk_load(dst + 1024, p.v_scale + at, bytes, &bars[P_SCF + sc]);
+            if (tile > 0) ok = issue_v(tile - 1);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        if (!ok) break;
+        v_page = page;
+      }
+    }
+    if (ok && tile > 0 && lane == 0) issue_v(tile - 1);
+  } else if (warp == 1) {
+    if (lane == 0) {  // ---------------------------------------------------- MMA issuer
+      const uint32_t idesc_s = idesc_f8(128, NP);
+      const uint32_t idesc_o = idesc_f8(128, NP, /*a_mn_major=*/true);
+      int tile = 0, it = 0;
+      bool ok = true;
+      Pieces s = it0;
+      for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
+        const int qb = it & 1;
+        if (!mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint64_t qd0 = sdesc_sw128(sbase + L::OFF_Q + qb * L::OPB, 16, 1024);
+        const int n = t1 - t0;
+        auto issue_s = [&](int j) -> bool {
+          const int gt = tile + j;
+          const int st = gt % DP_KSTAGES, sb = gt & 1;
+          if (!mbar_wait(&bars[P_KF + st], (gt / DP_KSTAGES) & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&bars[P_SFREE + sb], ((gt >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint64_t kd0 = sdesc_sw128(sbase + L::OFF_K8 + st * L::F8, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)   // 32 bytes of the row per step
+            tc_mma_e4m3(tS + sb * NP, kd0 + (uint64_t)(2 * k), qd0 + (uint64_t)(2 * k), idesc_s, k > 0 ? 1u : 0u);
+          tc_commit(&bars[P_SF + sb]);
+          tc_commit(&bars[P_KE + st]);
+          return true;
+        };
+        auto issue_pv = [&](int j) -> bool {
+          const int gt = tile + j;
+          const int st = gt % DP_VSTAGES, pb = gt & 1;
+          if (!mbar_wait(&bars[P_PF + pb], (gt >> 1) & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&bars[P_VF + st], (gt / DP_VSTAGES) & 1, abort_flag, p.status)) return false;
+          if (j == 0 && !mbar_wait(&bars[P_OFREE], (it & 1) ^ 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          // V^T: M = bytes of the row (MN-major), 8-key groups 1024 bytes apart
+          const uint64_t vd0 = sdesc_sw128(sbase + L::OFF_V8 + st * L::F8, 16384, 1024);
+          const uint64_t pd0 = sdesc_sw128(sbase + L::OFF_P + pb * L::OPB, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)   // 32 keys per step
+            tc_mma_e4m3(tO, vd0 + (uint64_t)(k * 4096 >> 4), pd0 + (uint64_t)(2 * k), idesc_o, (j > 0 || k > 0) ? 1u : 0u);
+          tc_commit(&bars[P_OD + pb]);
+          tc_commit(&bars[P_VE + st]);
+          return true;
+        };
+        for (int j = 0; j < n; ++j) {
+          if (!issue_s(j)) { ok = false; break; }
+          if (j > 0 && !issue_pv(j - 1)) { ok = false; break; }
+        }
+        if (!ok) break;
+        tc_commit(&bars[P_QE + qb]);
+        if (!issue_pv(n - 1)) break;
+        tile += n;
+      }
+      int no_abort = 0;
+      tc_commit(&bars[P_DRAIN]);
+      mbar_wait(&bars[P_DRAIN], 0, &no_abort, p.status);
+    }
+  } else if (warp == 6) {  // ------------------------------------------- q -> E4M3 hi / lo operand
+    constexpr int VH = HD / 8;                  // 8-element chunks of a row
+    constexpr int NCH = R * VH;
+    constexpr int PER = (NCH + 31) / 32;
+    int it = 0;
+    Pieces s = it0;
+    for (; next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
+      const int qb = it & 1;
+      uint4 w[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int c = lane + 32 * j, head = c < NCH ? head_of(c / VH) : -1;
+        w[j] = head >= 0 ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.n_q + head) * HD + c % VH * 8)
+                         : make_uint4(0, 0, 0, 0);
+      }
+      // the buffer is free once the MMAs of piece it - 2 have read it and the softmax warps its scales
+      if (!mbar_wait(&bars[P_QE + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+      if (!mbar_wait(&bars[P_QC + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) break;
+      uint8_t* qop = smem + L::OFF_Q + qb * L::OPB;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int c = lane + 32 * j, h = c / VH;
+        const uint32_t e[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int o = VH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // a power of two per row: amax * qs in [128, 256)
+        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+        const int up = min(max(7 - ex, -126), 126);
+        const float qs = exp2_int(up);
+        if (c < NCH) {
+          const int d = c % VH * 8 + h / RH * HD;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            hi[k] = split_fine(__uint_as_float(e[k] << 16) * qs, __uint_as_float(e[k] & 0xFFFF0000u) * qs, lo[k]);
+          *reinterpret_cast<uint2*>(qop + sw128_at(h, d)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(qop + sw128_at(R + h, d)) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          if (c % VH == 0) qinv[qb * 16 + h] = exp2_int(-up);
         }
       }
-      s = d * p.k_scale[s0 + t];
+      fence_proxy_async_smem();
+      __syncwarp();
+      mbar_arrive(&bars[P_QR + qb]);
     }
-    float mx = s;
+  } else {  // ------------------------------------------------------------ softmax warps 2..5
+    const int qw = warp & 3;   // a warp reaches TMEM lanes 32 * (warp % 4) ..
+    const int t = qw * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
+    int tile = 0, it = 0;
+    bool ok = true;
+    Pieces s = it0;
+    for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
+      const int qb = it & 1;
+      if (!mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
+      float sc[R], m_ref[R], lsum[R];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((t & 31) == 0) red[t >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float alpha = exp2f(m - mx);
-    m = mx;
-    const float e = t < n ? exp2f(s - m) : 0.f;
-    l = l * alpha + e;
-    w[t] = t < n ? e * p.v_scale[s0 + t] : 0.f;
-    __syncthreads();
-    acc *= alpha;
-    if (t < HD) {
-      const uint8_t* vc = p.v_codes + (row0 * p.n_kv + g) * HD + t;
-      for (int i = 0; i < n; ++i) acc += w[i] * e4m3x2_to_f2(vc[(int64_t)i * p.n_kv * HD]).x;
+      for (int h = 0; h < R; ++h) {
+        sc[h] = p.scale_log2 * qinv[qb * 16 + h];
+        m_ref[h] = -INFINITY;
+        lsum[h] = 0.f;
+      }
+      mbar_arrive(&bars[P_QC + qb]);
+      for (int tt = t0; tt < t1; ++tt, ++tile) {
+        const int sb = tile & 1, ss = tile % DP_SSTAGES;
+        const bool valid = tt * 128 + t < n_keys;
+        if (!mbar_wait(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+        float ks[PACK], lvs[PACK], ivs[PACK];
+        {
+          const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC);
+#pragma unroll
+          for (int k = 0; k < PACK; ++k) {
+            ks[k] = scales[k * 128 + t];
+            const float v = fmaxf(scales[256 + k * 128 + t], 7.88860905e-31f);   // 2^-100: a zero scale has a logarithm too
+            lvs[k] = __log2f(v);
+            ivs[k] = valid ? 1.f / v : 0.f;
+          }
+        }
+        mbar_arrive(&bars[P_SCE + ss]);
+        if (!mbar_wait(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sv[NP];
+#pragma unroll
+        for (int c = 0; c < NP / 16; ++c) tmem_ld16_dp(tS + sb * NP + c * 16 + lane_off, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
+        tc_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&bars[P_SFREE + sb]);
+        float e[R];   // log2 of weight * value scale
+#pragma unroll
+        for (int h = 0; h < R; ++h)
+          e[h] = valid ? fmaf(fmaf(__uint_as_float(sv[R + h]), 1.f / kDpLo, __uint_as_float(sv[h])), sc[h] * ks[h / RH], lvs[h / RH])
+                       : -INFINITY;
+        float* rbuf = red + (tile & 1) * 64;
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          const float v = warp_max_dp(e[h]);
+          if (lane == h) rbuf[qw * 16 + h] = v;
+        }
+        softmax_sync_dp();
+        float alpha[R];
+        bool resc = false;
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          const float tm = fmaxf(fmaxf(rbuf[h], rbuf[16 + h]), fmaxf(rbuf[32 + h], rbuf[48 + h]));
+          alpha[h] = 1.f;
+          if (m_ref[h] == -INFINITY) {
+            m_ref[h] = tm;
+          } else if (tm > m_ref[h] + kDpRescaleLog2) {
+            alpha[h] = exp2f(m_ref[h] - tm);
+            m_ref[h] = tm;
+            resc = true;
+          }
+        }
+        const int pb = tile & 1;
+        if (tile >= 2) {
+          if (!mbar_wait(&bars[P_OD + pb], ((tile - 2) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        }
+        if (resc) {   // the same in all 128 threads, which saw the same maxima
+          if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < NP / 16; ++c) {
+            uint32_t ov[16];
+            tmem_ld16_dp(tO + c * 16 + lane_off, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int col = c * 16 + k;
+              if (col < 2 * R) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha[col % R]);
+            }
+            tmem_st16(tO + c * 16 + lane_off, ov);
+          }
+          tc_wait_st();
+#pragma unroll
+          for (int h = 0; h < R; ++h) lsum[h] *= alpha[h];
+        }
+        // P^T rows: h (hi) and R + h (lo), this thread's key in byte t of each row
+        uint8_t* pbase = smem + L::OFF_P + pb * L::OPB;
+#pragma unroll
+        for (int h = 0; h < R; ++h) {
+          const float w = exp2f(e[h] - (m_ref[h] - kDpPScaleLog2));
+          uint32_t lo;
+          const uint32_t hi = split_fine(w, 0.f, lo);
+          lsum[h] = fmaf(w, ivs[h / RH], lsum[h]);
+          pbase[sw128_at(h, t)] = (uint8_t)(hi & 0xFFu);
+          pbase[sw128_at(R + h, t)] = (uint8_t)(lo & 0xFFu);
+        }
+        if ((tt + 1) * 128 > n_keys) {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
+          const int vs = tile % DP_VSTAGES;
+          if (!mbar_wait(&bars[P_VF + vs], (tile / DP_VSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!valid) {
+            uint4* vrow = reinterpret_cast<uint4*>(smem + L::OFF_V8 + vs * L::F8 + t * 128);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars[P_PF + pb]);
+      }
+      if (!ok) break;
+      if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t ov[NP];
+#pragma unroll
+      for (int c = 0; c < NP / 16; ++c) tmem_ld16_dp(tO + c * 16 + lane_off, *reinterpret_cast<uint32_t(*)[16]>(ov + 16 * c));
+      tc_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&bars[P_OFREE]);
+      float* lbuf = red + 128;
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        float v = lsum[h];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == h) lbuf[qw * 16 + h] = v;
+      }
+      softmax_sync_dp();
+      const bool whole = t0 == 0 && t1 == nt;
+      const int64_t part = ((int64_t)(2 * range + (t0 == 0 ? 1 : 0)) * p.groups + group) * R;
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float l = (lbuf[h] + lbuf[16 + h]) + (lbuf[32 + h] + lbuf[48 + h]);
+        const float ot = fmaf(__uint_as_float(ov[R + h]), 1.f / kDpLo, __uint_as_float(ov[h]));
+        const bool own = h / RH == t / HD;      // lane t holds byte t of the row: another head's, for half the rows
+        if (whole) {
+          const int head = head_of(h);
+          const int64_t at = ((int64_t)b * p.n_q + head) * HD + t % HD;
+          if (own && head >= 0 && in_extent(at, 1, (int64_t)p.B * p.n_q * HD)) p.o[at] = f2bf(ot / l);
+        } else if (in_extent(part + h, 1, (int64_t)2 * p.n_ranges * p.groups * R)) {
+          if (own) p.part_o[(part + h) * HD + t % HD] = ot;
+          if (t == 0) p.part_ml[part + h] = make_float2(m_ref[h], l);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, DP_TMEM_COLS);
+  }
+}
+
+// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (range, group,
+// row): the sequence whose first part is the range's tail; thread d its output element d.
+__global__ void __launch_bounds__(128) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
+  __shared__ float wgt[128];
+  __shared__ float red[8];
+  pdl_wait();
+  const int range = blockIdx.x, group = blockIdx.y, h = blockIdx.z, d = threadIdx.x, lane = d & 31, warp = d >> 5;
+  const SplitInfo s = p.split[range];
+  const int RH = R / pack, g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
+  if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges || g >= p.n_kv || i >= p.r) return;
+  const int n = s.last - range + 1;      // parts: the tail of `range`, then the first of each range up to `last`
+  auto slot = [&](int k) { return ((int64_t)(k == 0 ? 2 * range + 1 : 2 * (range + k)) * p.groups + group) * R + h; };
+  float m = -INFINITY;
+  for (int k = d; k < n; k += 128) m = fmaxf(m, p.part_ml[slot(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float l = 0.f, acc = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 128) {
+    const int k = k0 + d;
+    float w = 0.f;
+    if (k < n) {
+      const float2 ml = p.part_ml[slot(k)];
+      w = exp2f(ml.x - m);
+      l += w * ml.y;
     }
     __syncthreads();
+    wgt[d] = w;
+    __syncthreads();
+    if (d < p.hd) {
+#pragma unroll 8
+      for (int j = 0; j < min(128, n - k0); ++j) acc = fmaf(wgt[j], p.part_o[slot(k0 + j) * p.hd + d], acc);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if ((t & 31) == 0) red[t >> 5] = l;
+  if (lane == 0) red[4 + warp] = l;
   __syncthreads();
-  l = red[0] + red[1] + red[2] + red[3];
-  const int64_t at = ((int64_t)b * p.n_q + h) * HD + t;
-  if (t < HD && in_extent(at, 1, (int64_t)p.B * p.n_q * HD)) p.o[at] = f2bf(pos >= 0 ? acc / l : 0.f);
+  l = (red[4] + red[5]) + (red[6] + red[7]);
+  const int64_t at = ((int64_t)s.b * p.n_q + (int64_t)g * p.r + i) * p.hd + d;
+  if (d < p.hd && in_extent(at, 1, (int64_t)p.B * p.n_q * p.hd)) p.o[at] = f2bf(acc / l);
+}
+
+// Query rows of a CTA, head groups and, at most, ranges.
+struct Shape { int R, pack, subs, groups; };
+Shape shape_of(int64_t n_q, int64_t n_kv, int64_t hd) {
+  Shape s;
+  s.pack = hd == 64 ? 2 : 1;
+  const int64_t r = n_q / n_kv, most = 16 / s.pack;
+  int64_t rh = 1;
+  while (rh < most && rh < r) rh *= 2;
+  s.R = (int)rh * s.pack;
+  s.subs = (int)((r + rh - 1) / rh);
+  s.groups = (int)((n_kv + s.pack - 1) / s.pack) * s.subs;
+  return s;
+}
+int ranges_of(const Shape& s, int64_t B, int64_t max_pos, int sms) {
+  const int64_t tiles = B * ((max_pos + 128) / 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(DP_CTAS_PER_SM * sms / s.groups, tiles));
+}
+constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+struct Parts { size_t ml, split, total; };
+Parts parts_of(const Shape& s, int ranges, int64_t hd) {
+  const size_t rows = (size_t)2 * ranges * s.groups * s.R;
+  Parts a;
+  a.ml = round256(rows * hd * sizeof(float));
+  a.split = a.ml + round256(rows * sizeof(float2));
+  a.total = a.split + round256((size_t)ranges * sizeof(SplitInfo));
+  return a;
+}
+constexpr int kMaxSms = 256;   // sizes the workspace, so that it does not depend on the device
+
+template <int R, int PACK>
+int launch_attn(const DecodeAttn8pParams& p, int dev, cudaStream_t st) {
+  static bool attr_set[64] = {};
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(decode_attn8p_kernel<R, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, DpSmem::TOTAL) != cudaSuccess)
+      return -1;
+    attr_set[dev] = true;
+  }
+  // launched plainly: everything before it in the stream is complete
+  decode_attn8p_kernel<R, PACK><<<(unsigned)(p.n_ranges * p.groups), DP_THREADS, DpSmem::TOTAL, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
@@ -97,27 +676,66 @@ bool decode_attn8p_supported(int64_t B, int64_t n_q, int64_t n_kv, int64_t hd) {
 }
 
 size_t decode_attn8p_ws_bytes(int64_t B, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_pos) {
-  (void)B; (void)n_q; (void)n_kv; (void)hd; (void)max_pos;
-  return 256;
+  const Shape s = shape_of(n_q, n_kv, hd);
+  return parts_of(s, ranges_of(s, B, max_pos, kMaxSms), hd).total;
 }
 
 int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st) {
-  (void)num_sms;
   DecodeAttn8pParams p;
+  memset(&p, 0, sizeof(p));
+  const Shape s = shape_of(d.n_q, d.n_kv, d.hd);
+  const int ranges = ranges_of(s, d.B, d.max_pos, std::min(num_sms, kMaxSms));
+  const Parts parts = parts_of(s, ranges, d.hd);
+  const uint64_t inner = (uint64_t)(d.n_kv * d.hd), rows = (uint64_t)d.n_pages * 128;
+  if (!encode_tmap_2d_u8(&p.tmK, d.k_codes, inner, rows, inner, 128, 128)) return -1;
+  if (!encode_tmap_2d_u8(&p.tmV, d.v_codes, inner, rows, inner, 128, 128)) return -1;
   p.q = static_cast<const uint16_t*>(d.q);
-  p.k_codes = static_cast<const uint8_t*>(d.k_codes); p.v_codes = static_cast<const uint8_t*>(d.v_codes);
   p.k_scale = d.k_scale; p.v_scale = d.v_scale;
   p.block_table = d.block_table; p.seq_pos = d.seq_pos;
   p.o = static_cast<uint16_t*>(d.o);
-  p.B = (int)d.B; p.n_q = (int)d.n_q; p.n_kv = (int)d.n_kv; p.n_pages = (int)d.n_pages;
-  p.max_pages = d.max_pages;
+  char* ws = static_cast<char*>(d.ws);
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + parts.ml);
+  p.split = reinterpret_cast<SplitInfo*>(ws + parts.split);
+  p.B = (int)d.B; p.n_q = (int)d.n_q; p.n_kv = (int)d.n_kv; p.r = (int)(d.n_q / d.n_kv); p.hd = (int)d.hd;
+  p.n_pages = (int)d.n_pages;
   p.max_pos = (int)d.max_pos;
+  p.n_ranges = ranges; p.groups = s.groups; p.subs = s.subs;
+  p.max_pages = d.max_pages;
   p.scale_log2 = d.scale * 1.4426950408889634f;
   p.status = d.status;
-  const dim3 grid((unsigned)d.n_q, (unsigned)d.B);
-  if (d.hd == 128) decode_attn8p_kernel<128><<<grid, 128, 0, st>>>(p);
-  else decode_attn8p_kernel<64><<<grid, 128, 0, st>>>(p);
-  return 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return -1;
+  int rc = -1;
+  if (s.pack == 1) {
+    switch (s.R) {
+      case 1: rc = launch_attn<1, 1>(p, dev, st); break;
+      case 2: rc = launch_attn<2, 1>(p, dev, st); break;
+      case 4: rc = launch_attn<4, 1>(p, dev, st); break;
+      case 8: rc = launch_attn<8, 1>(p, dev, st); break;
+      case 16: rc = launch_attn<16, 1>(p, dev, st); break;
+    }
+  } else {
+    switch (s.R) {
+      case 2: rc = launch_attn<2, 2>(p, dev, st); break;
+      case 4: rc = launch_attn<4, 2>(p, dev, st); break;
+      case 8: rc = launch_attn<8, 2>(p, dev, st); break;
+      case 16: rc = launch_attn<16, 2>(p, dev, st); break;
+    }
+  }
+  if (rc != 0 || ranges == 1) return rc;   // one range cuts nothing
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join8p_kernel, p, s.R, s.pack) == cudaSuccess ? 0 : -1;
 }
 
 LLAMA_DEFINE_BOUNDS_READER(decode_attn8p)
