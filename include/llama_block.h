@@ -501,7 +501,7 @@ typedef struct llama_page_pool {
  * A page may stand in several rows of a request, in the same column; other requests may share pages that some kept beam of
  * each holds (a common prompt).  No pool row is written but the copied rows.
  * LLAMA_ERR_UNSUPPORTED for W > 32, B > 8192, n_pages >= 2^24, max_pages > 2^17, n_free or freed_room >= 2^31, n_pools > 8,
- * parts * row_bytes > 2^24, n_layers > 65536, 2^44 bytes and more of one page over all layers; LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's
+ * parts * row_bytes > 2^24, n_layers * parts * row_bytes > 2^27 (16 GB of one page over all layers of a pool); LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's
  * n_layers, parts or row_bytes < 1, row_bytes no multiple of 4), NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte,
  * pools or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE.  Latched as LLAMA_ERR_INVALID_ARG in the device status
  * word: a parent outside [-1, W) (taken as -1), n_cached outside [0, 128 * max_pages] (taken as 0), page ids outside

@@ -1461,11 +1461,11 @@ int llama_beam_reorder_paged(const int32_t* parents, int64_t B, int64_t W, const
     const llama_page_pool& q = pools[k];
     if (q.n_layers < 1 || q.parts < 1 || q.row_bytes < 1 || q.row_bytes % 4) return LLAMA_ERR_INVALID_ARG;
     constexpr int64_t most = 1 << 24;
-    if (q.n_layers > 65536 || q.parts > most || q.row_bytes > most || q.parts * q.row_bytes > most) return LLAMA_ERR_UNSUPPORTED;
+    if (q.parts > most || q.row_bytes > most || q.parts * q.row_bytes > most || q.n_layers > most || q.n_layers * q.parts * q.row_bytes > most * 8)
+      return LLAMA_ERR_UNSUPPORTED;
     if (!q.base) return LLAMA_ERR_INVALID_ARG;
     if (!aligned16(q.base)) return LLAMA_ERR_ALIGNMENT;
   }
-  if (beam_copy_units(pools, n_pools) > (int64_t(1) << 30)) return LLAMA_ERR_UNSUPPORTED;
   if (!counts || (n_free > 0 && !free_pages) || (freed_room > 0 && !freed_pages)) return LLAMA_ERR_INVALID_ARG;
   if (B > 0 && (!parents || !n_cached || !n_cached_out || !block_table || !block_table_out)) return LLAMA_ERR_INVALID_ARG;
   const void* ps[8] = {parents, n_cached, n_cached_out, block_table, block_table_out, free_pages, freed_pages, counts};

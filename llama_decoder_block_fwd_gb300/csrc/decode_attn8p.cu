@@ -725,17 +725,8 @@ int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st
     }
   }
   if (rc != 0 || ranges == 1) return rc;   // one range cuts nothing
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join8p_kernel, p, s.R, s.pack) == cudaSuccess ? 0 : -1;
+  return launch_after(decode_join8p_kernel, dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R), dim3(128), 0, st, p,
+                      s.R, s.pack) == cudaSuccess ? 0 : -1;
 }
 
 LLAMA_DEFINE_BOUNDS_READER(decode_attn8p)

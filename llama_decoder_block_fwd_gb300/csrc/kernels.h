@@ -203,6 +203,24 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// A kernel that may begin while its predecessor in the stream drains, whatever pdl_enabled() says: for the second kernel of a
+// call, which waits in pdl_wait.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // sample.cu: next-token choice (one CTA per row) and the embedding lookup
 int launch_sample(const float* logits, int64_t B, int64_t V, int64_t ld, float temperature, int64_t top_k,
                   float top_p, const float* u, int* tokens, cudaStream_t st);
@@ -310,7 +328,6 @@ struct BeamReorderDesc {
   int n_pools;
   void* ws;
 };
-int64_t beam_copy_units(const llama_page_pool* pools, int n_pools);   // of one page's copy, over pools and layers
 size_t beam_reorder_ws_bytes(int64_t B, int64_t W, int64_t max_pages);
 int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status, cudaStream_t st);
 

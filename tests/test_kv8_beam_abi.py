@@ -125,9 +125,9 @@ def reorder(pools=((FAKE, 2, 1, 1024), (FAKE, 2, 8, 4)), **kw):
     (dict(pools=[(None, 1, 1, 16)]), INVALID), (dict(pools=[(FAKE + 8, 1, 1, 16)]), ALIGNMENT), (dict(pools=[(FAKE, 0, 1, 16)]), INVALID),
     (dict(pools=[(FAKE, 1, 0, 16)]), INVALID), (dict(pools=[(FAKE, 1, 1, 0)]), INVALID), (dict(pools=[(FAKE, 1, 1, 6)]), INVALID),
     (dict(pools=[(FAKE, 1, 1, 2 ** 24)], ws=None), WORKSPACE), (dict(pools=[(FAKE, 1, 2, 2 ** 24)]), UNSUPPORTED),
-    (dict(pools=[(FAKE, 1, 2 ** 40, 2 ** 40)]), UNSUPPORTED), (dict(pools=[(FAKE, 65536, 1, 16)], ws=None), WORKSPACE),
-    (dict(pools=[(FAKE, 65537, 1, 16)]), UNSUPPORTED), (dict(pools=[(FAKE, 8192, 1, 2 ** 24)], ws=None), WORKSPACE),
-    (dict(pools=[(FAKE, 8193, 1, 2 ** 24)]), UNSUPPORTED)])
+    (dict(pools=[(FAKE, 1, 2 ** 40, 2 ** 40)]), UNSUPPORTED), (dict(pools=[(FAKE, 2 ** 23, 1, 16)], ws=None), WORKSPACE),
+    (dict(pools=[(FAKE, 2 ** 24 + 1, 1, 4)]), UNSUPPORTED), (dict(pools=[(FAKE, 8, 2, 2 ** 23)], ws=None), WORKSPACE),
+    (dict(pools=[(FAKE, 9, 2, 2 ** 23)]), UNSUPPORTED)])
 def test_reorder_refuses(kw, want):
     assert reorder(**kw) == want
 
