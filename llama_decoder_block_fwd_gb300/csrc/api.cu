@@ -1435,6 +1435,8 @@ int llama_beam_select(const float* logits, int64_t B, int64_t W, int64_t vocab, 
     if ((uintptr_t)p & 3) return LLAMA_ERR_ALIGNMENT;
   if (!ws || ws_bytes < beam_select_ws_bytes(B, W, vocab)) return LLAMA_ERR_WORKSPACE;
   if (!aligned16(ws)) return LLAMA_ERR_ALIGNMENT;
+  unsigned* status = status_ptr();
+  if (!status) return LLAMA_ERR_CUDA;
   BeamSelectDesc a;
   a.logits = logits; a.B = B; a.W = W; a.V = vocab; a.ld = ld; a.n_out = n_out;
   a.scores = scores; a.finished = finished; a.pad_token = pad_token;
@@ -1442,7 +1444,7 @@ int llama_beam_select(const float* logits, int64_t B, int64_t W, int64_t vocab, 
   a.ws = ws;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof::begin("beam_select", st);
-  const int rc = launch_beam_select(a, num_sms(), st);
+  const int rc = launch_beam_select(a, num_sms(), status, st);
   prof::end(st);
   return rc ? LLAMA_ERR_CUDA : launch_status();
 }

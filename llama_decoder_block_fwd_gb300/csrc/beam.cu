@@ -18,32 +18,41 @@ namespace {
 constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
 // ---------------------------------------------------------------------------------------- select
-// HBM bound for many rows, latency for few.  A CTA reads one part of a row once, a batch of BS_BATCH logits in registers at
-// a time, the next on its way.  Each thread keeps a running maximum and sum of exponentials; what beats the part's
-// n_out-th best so far goes to a list in shared memory, which is cut back to the n_out best when it has grown.  All rows
-// of a call are cut and summed alike, so equal rows give equal sums.  The second kernel joins a request's parts.
+// HBM bound for many rows, latency for few.  The rows' batches of BS_BATCH logits, one row after the other, are cut into
+// equal ranges, one per CTA (rows that need not be read left out).  A producer warp streams a range's batches into a ring in
+// shared memory (bulk copies), 256 threads take them.  Each warp sums the exponentials of its 512 logits of a batch from
+// their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
+// n_out-th best of a row's piece so far goes to a list in shared memory, which is cut back to the n_out best when it has
+// grown.  The second kernel joins a request's lists and sums.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
 constexpr int BS_PER = 16;                              // logits of a thread in a batch
 constexpr int BS_BATCH = BS_THREADS * BS_PER;
+constexpr int BS_STAGES = 3;
 constexpr int BS_MAX_K = (int)kBeamMaxOut;
-constexpr int BS_KEPT = 2 * BS_MAX_K + 64;              // entries that the list may have between batches
-constexpr int BS_LIST = BS_KEPT + 2 * BS_MAX_K * BS_PER;
-constexpr int BS_CTAS_PER_SM = 4;
-constexpr int BS_MAX_PARTS = 32;
+constexpr int BS_SLACK = 16;                            // entries beyond n_out that the list may keep
+constexpr int BS_CTAS_PER_SM = 3;
+constexpr int BS_MAX_PIECES = 32;                       // of a row, on average: what the join has to look through
+constexpr int BS_SCAN = 1 << 14;                        // rows up to which every CTA counts those that have to be read
+__host__ __device__ constexpr int bs_list(int K) { return K + BS_SLACK + 2 * K * BS_PER; }
+__host__ __device__ constexpr int bs_smem(int K, bool vec) { return (vec ? BS_STAGES * BS_BATCH * 4 : 0) + 2 * bs_list(K) * 8; }
+
+struct RowPieces { int slot, n; };   // a row's lists are slot, slot + 1, ..
 
 struct SelectParams {
   const float* z;
   int64_t ld;
-  int B, W, V, K;
-  int parts, part_len;
+  int B, W, V, K, nb;     // nb: batches of a row
   const float* scores;
   const int* finished;
   int pad;
   int *parents, *tokens;
   float* out;
-  uint64_t* keys;   // [B W, parts, K] the best tokens of a part, best first (0: none)
-  float2* stat;     // [B W, parts] maximum and sum of exp(z - maximum)
+  uint64_t* keys;      // [B W + CTAs, K] the best tokens of a piece, best first (0: none)
+  RowPieces* pieces;   // [B W]
+  float2* stat;        // [B W, nb, warps] maximum and sum of exp(z - maximum)
+  int64_t n_lists;
+  unsigned* status;
 };
 
 // Logits as integers that order as they do, the lower token above at equal ones: larger is better, 0 is no candidate.
@@ -58,254 +67,540 @@ __device__ __forceinline__ float key_logit(uint64_t k) {
 }
 __device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// exp(x - m) with the difference formed first, so that large logits keep their digits.
+__device__ __forceinline__ float exp_from(float x, float m) { return exp2_fast((x - m) * 1.4426950408889634f); }
 __device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2) {
   const float mx = fmaxf(m, m2);
-  if (mx > -INFINITY) s = s * __expf(m - mx) + s2 * __expf(m2 - mx);
+  if (mx > -INFINITY) s = s * exp_from(m, mx) + s2 * exp_from(m2, mx);
   m = mx;
 }
-
-// VEC: rows start on 16 bytes, a thread's logits come four at a time.
-template <bool VEC>
-__global__ void __launch_bounds__(BS_THREADS, BS_CTAS_PER_SM) beam_part_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ uint64_t list[2][BS_LIST];
-  __shared__ int n_sh, more_sh;
-  __shared__ float red[2][BS_WARPS];
-  const int row = blockIdx.x / p.parts, part = blockIdx.x % p.parts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  if ((p.finished && __ldg(p.finished + row)) || !(__ldg(p.scores + row) > -INFINITY)) return;   // nothing to read
-  const float* z = p.z + (int64_t)row * p.ld;
-  const int e0 = part * p.part_len, e1 = min(p.V, e0 + p.part_len), K = p.K;
-  // element k of this thread in the batch that starts at e
-  auto place = [&](int e, int k) { return VEC ? e + (k / 4) * BS_THREADS * 4 + tid * 4 + k % 4 : e + k * BS_THREADS + tid; };
-  auto load = [&](int e, float (&x)[BS_PER]) {
-#pragma unroll
-    for (int k = 0; k < BS_PER; k += VEC ? 4 : 1) {
-      const int i = place(e, k);
-      if (VEC && i + 3 < e1) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(z + i));
-        x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
-      } else {
-#pragma unroll
-        for (int c = 0; c < (VEC ? 4 : 1); ++c) x[k + c] = i + c < e1 ? __ldcs(z + i + c) : -INFINITY;
-      }
-    }
-  };
-  if (tid == 0) { n_sh = 0; more_sh = 0; }
-  float m = -INFINITY, s = 0.f;
-  uint64_t floor = 0;        // the part's K-th best so far: what does not beat it is no candidate
-  int cur = 0, n = 0;        // the list in use and its length
-  float x[BS_PER], next[BS_PER];
-  load(e0, x);
-  __syncthreads();
-  for (int e = e0; e < e1; e += BS_BATCH) {
-    if (e + BS_BATCH < e1) load(e + BS_BATCH, next);
-    float top = x[0];
-#pragma unroll
-    for (int k = 1; k < BS_PER; ++k) top = fmaxf(top, x[k]);
-    if (top > -INFINITY) {
-      if (top > m) {
-        s *= __expf(m - top);
-        m = top;
-      }
-      float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < BS_PER; ++k) a[k % 4] += __expf(x[k] - m);
-      s += (a[0] + a[1]) + (a[2] + a[3]);
-    }
-    // a later logit equal to the floor's has the higher token, so only larger ones count
-    const float bar = floor ? key_logit(floor) : -INFINITY;
-    if (__syncthreads_or(top > bar)) {
-      int mine = 0;
-      uint64_t best = 0;
-#pragma unroll
-      for (int k = 0; k < BS_PER; ++k) mine += x[k] > bar;
-      if (mine) {
-        atomicAdd(&more_sh, mine);
-#pragma unroll
-        for (int k = 0; k < BS_PER; ++k)
-          if (x[k] > bar) {
-            const uint64_t key = cand_key(x[k], place(e, k));
-            best = key > best ? key : best;
-          }
-      }
-      __syncthreads();
-      uint64_t least = 1;
-      if (more_sh > BS_KEPT - K) {
-        // Too many: a bar that K to 2 K threads' best logits reach, by bisection on the keys.  At least K logits
-        // reach it, and at most BS_PER of each of those threads.
-        uint64_t hi = ~0ull;
-        if (__syncthreads_count(best >= least) >= 2 * K)
-          while (hi - least > 1) {
-            const uint64_t mid = least + (hi - least) / 2;
-            const int c = __syncthreads_count(best >= mid);
-            if (c >= K) {
-              least = mid;
-              if (c <= 2 * K) break;
-            } else {
-              hi = mid;
-            }
-          }
-      }
-      if (best >= least && mine) {
-#pragma unroll
-        for (int k = 0; k < BS_PER; ++k)
-          if (x[k] > bar) {
-            const uint64_t key = cand_key(x[k], place(e, k));
-            if (key >= least) {
-              const int at = atomicAdd(&n_sh, 1);
-              if (at < BS_LIST) list[cur][at] = key;    // (there is room, see above)
-            }
-          }
-      }
-      __syncthreads();
-      n = min(n_sh, BS_LIST);
-      if (n > K + 64 || (n > K && !floor)) {            // back to the K best, in order
-        for (int i = tid; i < n; i += BS_THREADS) {
-          const uint64_t key = list[cur][i];
-          int rank = 0;
-          for (int j = 0; j < n; ++j) rank += list[cur][j] > key;
-          if (rank < K) list[cur ^ 1][rank] = key;
-        }
-        __syncthreads();
-        cur ^= 1;
-        n = K;
-        floor = list[cur][K - 1];
-      }
-      if (tid == 0) { n_sh = n; more_sh = 0; }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < BS_PER; ++k) x[k] = next[k];
-  }
-  // the part's list in order, and its maximum and sum
-  const int64_t at = (int64_t)row * p.parts + part;
-  const bool in = in_extent(at, 1, (int64_t)p.B * p.W * p.parts);
-  for (int i = tid; i < n; i += BS_THREADS) {
-    const uint64_t key = list[cur][i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += list[cur][j] > key;
-    if (rank < K && in) p.keys[at * K + rank] = key;
-  }
-  for (int i = n + tid; i < K; i += BS_THREADS)
-    if (in) p.keys[at * K + i] = 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join_sums(m, s, m2, s2);
-  }
-  if (lane == 0) { red[0][warp] = m; red[1][warp] = s; }
-  __syncthreads();
-  if (tid == 0 && in) {
-    for (int w = 1; w < BS_WARPS; ++w) join_sums(m, s, red[0][w], red[1][w]);
-    p.stat[at] = make_float2(m, s);
+// Two at a time (one instruction each).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%1, %2};\n\tmov.b64 v, {%3, %4};\n\tadd.rn.f32x2 %0, u, v;\n\t}" : "=l"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%1, %2};\n\tmov.b64 v, {%3, %4};\n\tmul.rn.f32x2 %0, u, v;\n\t}" : "=l"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 exp_from2(float a, float b, float m) {
+  const float2 t = mul2(add2(make_float2(a, b), make_float2(-m, -m)), make_float2(1.4426950408889634f, 1.4426950408889634f));
+  return make_float2(exp2_fast(t.x), exp2_fast(t.y));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The n-th largest of a warp's values (equal ones counted each; -inf counts).
+__device__ __forceinline__ float warp_nth(float v, int n) {
+  const int lane = threadIdx.x & 31;
+  float t = v;
+  for (int i = 1;; ++i) {
+    float mx;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(t));
+    if (i == n) return mx;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, t == mx)) - 1) t = -INFINITY;
   }
 }
 
-// Joins the parts of a request's rows: each part's list is in order, so a candidate below the n_out-th best of the lists'
-// heads is none of the n_out best; the others are ranked against each other.
+// The 256 threads that take the logits.
+__device__ __forceinline__ void takers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ int takers_count(bool v) {
+  int n;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.popc.u32 %0, 1, 256, p;\n\t}" : "=r"(n) : "r"((int)v) : "memory");
+  return n;
+}
+
+__device__ __forceinline__ bool row_live(const SelectParams& p, int row) {
+  return !(p.finished && __ldg(p.finished + row)) && __ldg(p.scores + row) > -INFINITY;
+}
+// The pieces of a CTA's range: batches [b0, b1) of a row, the row's place among those that are read.
+struct RowWalk { int row, b; int64_t place, left; };
+__device__ __forceinline__ bool next_row_piece(const SelectParams& p, RowWalk& s, bool all, int& row, int& b0, int& b1, int64_t& place) {
+  if (s.left <= 0) return false;
+  if (!all)
+    while (!row_live(p, s.row)) {
+      if (++s.row >= p.B * p.W) return false;
+    }
+  row = s.row++;
+  place = s.place++;
+  b0 = s.b;
+  b1 = (int)min((int64_t)p.nb, b0 + s.left);
+  s.left -= b1 - b0;
+  s.b = 0;
+  return true;
+}
+
+// VEC: rows start on 16 bytes and come by bulk copies; else each thread loads its own.
+template <bool VEC>
+__global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) uint8_t bs_smem_raw[];
+  float* ring = reinterpret_cast<float*>(bs_smem_raw);
+  const int K = p.K, room = bs_list(K);
+  uint64_t* list = reinterpret_cast<uint64_t*>(bs_smem_raw + (VEC ? BS_STAGES * BS_BATCH * 4 : 0));
+  uint64_t* other = list + room;
+  __shared__ uint64_t full[BS_STAGES], pushed[BS_STAGES];   // a batch has landed; every warp has read it and pushed its candidates
+  __shared__ int n_sh, cnt[BS_STAGES], wsum[BS_WARPS + 1], start;
+  __shared__ volatile int abort_sh;
+  __shared__ float red[BS_WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = p.B * p.W;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < BS_STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&pushed[i], BS_WARPS);
+      cnt[i] = 0;
+    }
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  // the range: of the rows that have to be read, or, of very many, of all (and the others are passed over)
+  const bool all = rows > BS_SCAN;
+  const int per = all ? 0 : (rows + BS_THREADS + 31) / (BS_THREADS + 32), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += row_live(p, r);
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) wsum[warp] = upto;
+  __syncthreads();
+  int live = 0, first = upto - mine;
+  for (int w = 0; w <= BS_WARPS; ++w) {
+    if (w < warp) first += wsum[w];
+    live += wsum[w];
+  }
+  if (all) live = rows;
+  const int64_t T = (int64_t)live * p.nb;
+  // no more ranges than batches, so that each of them has some
+  const int ranges = (int)min((int64_t)gridDim.x, T);
+  if ((int)blockIdx.x >= ranges) return;
+  const int64_t x0 = (int64_t)blockIdx.x * T / ranges, x1 = (int64_t)(blockIdx.x + 1) * T / ranges;
+  const int place0 = (int)(x0 / p.nb);
+  if (!all && first <= place0 && place0 < first + mine) {
+    int r = r0, k = first;
+    for (;; ++r)
+      if (row_live(p, r) && k++ == place0) break;
+    start = r;
+  }
+  __syncthreads();
+  RowWalk walk{all ? place0 : start, (int)(x0 % p.nb), place0, x1 - x0};
+  int row, b0, b1;
+  int64_t place;
+  if (warp == BS_WARPS) {   // ------------------------------------------------ producer
+    if (VEC && lane == 0) {
+      int j = 0;
+      while (next_row_piece(p, walk, all, row, b0, b1, place)) {
+        if (all && !row_live(p, row)) continue;
+        const float* z = p.z + (int64_t)row * p.ld;
+        for (int b = b0; b < b1; ++b, ++j) {
+          const int st = j % BS_STAGES, e = b * BS_BATCH;
+          if (j >= BS_STAGES && !mbar_wait(&pushed[st], (j / BS_STAGES - 1) & 1, &abort_sh, p.status)) return;
+          const uint32_t bytes = (min(e + BS_BATCH, p.V) - e) / 4 * 16;   // whole vectors; up to three logits behind them are read directly
+          mbar_arrive_expect_tx(&full[st], bytes);
+          if (bytes)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(ring + st * BS_BATCH)), "l"(reinterpret_cast<uint64_t>(z + e)), "r"(bytes), "r"(smem_u32(&full[st]))
+                         : "memory");
+        }
+      }
+    }
+    return;
+  }
+  int j = 0;   // batches of this CTA so far
+  while (next_row_piece(p, walk, all, row, b0, b1, place)) {
+    if (all && !row_live(p, row)) continue;
+    const float* z = p.z + (int64_t)row * p.ld;
+    // token k of this thread in batch b
+    auto token = [&](int b, int k) { return b * BS_BATCH + (VEC ? (k / 4) * BS_THREADS * 4 + tid * 4 + k % 4 : k * BS_THREADS + tid); };
+    auto load = [&](int b, float (&x)[BS_PER]) {   // from global memory
+#pragma unroll
+      for (int k = 0; k < BS_PER; ++k) x[k] = token(b, k) < p.V ? __ldg(z + token(b, k)) : -INFINITY;
+    };
+    uint64_t floor = 0;        // the piece's K-th best so far: what does not beat it is no candidate
+    float bar = -INFINITY;     // its logit; a later equal one has the higher token, so only larger ones count
+    int n = 0;                 // length of the list
+    float x[BS_PER], four[BS_PER / 4];   // a batch's logits, the largest of each four
+    // batch b, the CTA's j-th: its logits into x, its sums to memory; *top gets this thread's largest
+    auto take = [&](int b, float* top) -> bool {
+      const int st = j % BS_STAGES;
+      if (!VEC) {
+        load(b, x);
+      } else {
+        if (!mbar_wait(&full[st], (j / BS_STAGES) & 1, &abort_sh, p.status)) return false;
+        const float4* v = reinterpret_cast<const float4*>(ring + st * BS_BATCH) + tid;
+#pragma unroll
+        for (int k = 0; k < BS_PER; k += 4) {
+          const float4 w = v[k / 4 * BS_THREADS];
+          x[k] = w.x; x[k + 1] = w.y; x[k + 2] = w.z; x[k + 3] = w.w;
+        }
+        if ((b + 1) * BS_BATCH > p.V) {   // the last one: nothing behind the row's end, and the logits behind the last whole vector
+#pragma unroll
+          for (int k = 0; k < BS_PER; ++k) {
+            const int i = token(b, k);
+            if (i >= p.V) x[k] = -INFINITY;
+            else if (i >= (p.V & ~3)) x[k] = __ldg(z + i);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < BS_PER; k += 4) four[k / 4] = fmaxf(max3(x[k], x[k + 1], x[k + 2]), x[k + 3]);
+      float t = four[0];
+#pragma unroll
+      for (int k = 1; k < BS_PER / 4; ++k) t = fmaxf(t, four[k]);
+      *top = t;
+      float m;
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(t));
+      float sum = 0.f;
+      if (m > -INFINITY) {
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int k = 0; k < BS_PER; k += 2) acc[k / 2 % 2] = add2(acc[k / 2 % 2], exp_from2(x[k], x[k + 1], m));
+        sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      }
+      const int64_t at = ((int64_t)row * p.nb + b) * BS_WARPS + warp;
+      if (lane == 0 && in_extent(at, 1, (int64_t)rows * p.nb * BS_WARPS)) p.stat[at] = make_float2(m, sum);
+      return true;
+    };
+    // back to the K best, in order
+    auto cut = [&]() {
+      if (n > K + BS_SLACK || (n > K && !floor)) {
+        for (int i = tid; i < n; i += BS_THREADS) {
+          const uint64_t key = list[i];
+          int rank = 0;
+          for (int c = 0; c < n; ++c) rank += list[c] > key;
+          if (rank < K) other[rank] = key;
+        }
+        takers_sync();
+        uint64_t* t = list;
+        list = other;
+        other = t;
+        n = K;
+        floor = list[K - 1];
+        bar = key_logit(floor);
+      }
+    };
+    // No room for what is above the bar in the batch y (one warp's logits, equal ones, rising rows): a higher bar that the
+    // bests of K to 2 K threads reach, by bisection on the keys, which differ.  At least K logits reach it, and at most
+    // BS_PER of each of those threads.
+    auto squeeze = [&](int b, const float (&y)[BS_PER]) {
+      uint64_t best = 0, lo = 1, hi = ~0ull;
+#pragma unroll
+      for (int k = 0; k < BS_PER; ++k) {
+        const uint64_t key = y[k] > bar ? cand_key(y[k], token(b, k)) : 0;
+        best = key > best ? key : best;
+      }
+      if (takers_count(best >= lo) >= 2 * K)
+        while (hi - lo > 1) {
+          const uint64_t mid = lo + (hi - lo) / 2;
+          const int c = takers_count(best >= mid);
+          if (c >= K) {
+            lo = mid;
+            if (c <= 2 * K) break;
+          } else {
+            hi = mid;
+          }
+        }
+      if (tid == 0) n_sh = n;
+      takers_sync();
+      if (best >= lo) {
+#pragma unroll
+        for (int k = 0; k < BS_PER; ++k) {
+          const uint64_t key = y[k] > bar ? cand_key(y[k], token(b, k)) : 0;
+          if (key >= lo) {
+            const int at = atomicAdd(&n_sh, 1);
+            if (at < room) list[at] = key;
+          }
+        }
+      }
+      takers_sync();
+      n = min(n_sh, room);
+    };
+    auto push = [&](int b, auto counts) {   // what counts(logit) says
+      int* counter = &cnt[j % BS_STAGES];
+#pragma unroll
+      for (int g = 0; g < BS_PER / 4; ++g)
+        if (counts(four[g])) {
+#pragma unroll
+          for (int k = 4 * g; k < 4 * g + 4; ++k)
+            if (counts(x[k])) {
+              const int at = n + atomicAdd(counter, 1);
+              if (at < room) list[at] = cand_key(x[k], token(b, k));
+            }
+        }
+    };
+    {  // the first batch: in each warp the bests of at least ceil(K / 8) threads reach its own n-th, so at least K logits
+       // reach the least of these
+      float top;
+      if (!take(b0, &top)) return;
+      const float w = warp_nth(top, (K + BS_WARPS - 1) / BS_WARPS);
+      if (lane == 0) red[warp] = w;
+      takers_sync();
+      if (tid == 0) cnt[(j + BS_STAGES - 1) % BS_STAGES] = 0;
+      float least = red[0];
+#pragma unroll
+      for (int i = 1; i < BS_WARPS; ++i) least = fminf(least, red[i]);
+      if (top >= least) push(b0, [&](float v) { return v >= least && v > -INFINITY; });
+      takers_sync();
+      if (lane == 0) mbar_arrive(&pushed[j % BS_STAGES]);
+      const int c = cnt[j % BS_STAGES];
+      if (c > room) squeeze(b0, x);
+      else n = c;
+      cut();
+      ++j;
+    }
+    // The others push what beats the bar and go on; the list is looked at when the next batch has been summed up, so that the
+    // warps need not wait for one another.  The CTA's batch i counts in cnt[i % BS_STAGES].
+    auto settle = [&](int i, int b) -> bool {
+      if (!mbar_wait(&pushed[i % BS_STAGES], (i / BS_STAGES) & 1, &abort_sh, p.status)) return false;
+      const int c = cnt[i % BS_STAGES];
+      if (tid == 0) cnt[(i + BS_STAGES - 1) % BS_STAGES] = 0;      // batch i - 1's, which everyone has read
+      if (n + c > room) {
+        float y[BS_PER];
+        load(b, y);
+        squeeze(b, y);
+      } else {
+        n += c;
+      }
+      cut();
+      return true;
+    };
+    for (int b = b0 + 1; b < b1; ++b, ++j) {
+      float top;
+      if (!take(b, &top)) return;
+      if (b > b0 + 1 && !settle(j - 1, b - 1)) return;
+      if (top > bar) push(b, [&](float v) { return v > bar; });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pushed[j % BS_STAGES]);
+    }
+    if (b1 > b0 + 1 && !settle(j - 1, b1 - 1)) return;
+    // the piece's list in order
+    const int64_t slot = place + blockIdx.x;
+    const bool in = in_extent(slot, 1, p.n_lists);
+    for (int i = tid; i < n; i += BS_THREADS) {
+      const uint64_t key = list[i];
+      int rank = 0;
+      for (int c = 0; c < n; ++c) rank += list[c] > key;
+      if (rank < K && in) p.keys[slot * K + rank] = key;
+    }
+    for (int i = n + tid; i < K; i += BS_THREADS)
+      if (in) p.keys[slot * K + i] = 0;
+    if (b0 == 0 && tid == 0) {   // the row's first piece says how many there are
+      const int64_t last = place * p.nb + p.nb - 1;
+      int c = (int)min((int64_t)ranges - 1, last * ranges / T);
+      while (c + 1 < ranges && (int64_t)(c + 1) * T / ranges <= last) ++c;
+      while (c > 0 && (int64_t)c * T / ranges > last) --c;
+      if (in_extent(row, 1, rows)) p.pieces[row] = RowPieces{(int)slot, c - (int)blockIdx.x + 1};
+    }
+  }
+}
+
+// Joins a request's rows: each piece's list is in order, so a candidate below the n_out-th best of the lists' heads is none
+// of the n_out best; the others are ranked against each other.
 constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: n_out lists (or fewer lists than n_out) of n_out
-constexpr int BM_SMEM = BM_MOST * (int)(sizeof(double) + sizeof(int));
+constexpr int BM_SMEM = BM_MOST * (int)(sizeof(int64_t) + sizeof(int));
+
+// Doubles as integers that order as they do.
+__device__ __forceinline__ int64_t ordered(double s) {
+  const int64_t v = __double_as_longlong(s + 0.0);
+  return v < 0 ? v ^ 0x7FFFFFFFFFFFFFFFll : v;
+}
+__device__ __forceinline__ double from_ordered(int64_t v) { return __longlong_as_double(v < 0 ? v ^ 0x7FFFFFFFFFFFFFFFll : v); }
+constexpr int64_t BM_NONE = INT64_MIN;
+
+// log s to 2^-25 for s >= 1, where a double logarithm would cost a few microseconds of this card's 64-bit units: the exponent
+// times log 2, and the fp32 logarithm of what lies in [0.75, 1.5).
+__device__ __forceinline__ double log_sum(float s) {
+  int e = (int)(__float_as_uint(s) >> 23) - 127;
+  float f = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);
+  if (f >= 1.5f) { f *= 0.5f; ++e; }
+  return (double)e * 0.6931471805599453094 + (double)logf(f);
+}
 
 __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ double score[];                      // [BM_MOST], then their places
+  extern __shared__ int64_t score[];                     // [BM_MOST], then their places
   int* place = reinterpret_cast<int*>(score + BM_MOST);
-  __shared__ double lsum[kBeamMaxW], bar_sh;   // log of a row's sum of exp(z - its maximum)
+  __shared__ double lsum[kBeamMaxW];                     // log of a row's sum of exp(z - its maximum)
+  __shared__ int64_t bar_sh;
   __shared__ float base_sh[kBeamMaxW], top[kBeamMaxW];
-  __shared__ int kind[kBeamMaxW], n_sh, bar_at;
-  const int b = blockIdx.x, tid = threadIdx.x, K = p.K, lists = p.W * p.parts;
+  __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh, bar_at;   // first: list of each row, of the request's
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, K = p.K;
   pdl_wait();
   // kind: 0 no candidates, 1 logits, 2 finished
-  for (int w = tid; w < p.W; w += BS_THREADS) {
-    const int row = b * p.W + w;
-    const float base = p.scores[row];
-    const bool done = p.finished && p.finished[row];
-    int kd = base > -INFINITY ? (done ? 2 : 1) : 0;
-    float m = -INFINITY;
-    if (kd == 1) {
-      for (int q = 0; q < p.parts; ++q) m = fmaxf(m, p.stat[(int64_t)row * p.parts + q].x);
-      double s = 0.0;
-      for (int q = 0; q < p.parts; ++q) {
-        const float2 st = p.stat[(int64_t)row * p.parts + q];
-        if (st.x > -INFINITY) s += (double)(st.y * expf(st.x - m));
-      }
-      if (m > -INFINITY) lsum[w] = log(s);
-      else kd = 0;
+  if (tid < 32) {
+    int n = 0;
+    if (lane < p.W) {
+      const int row = b * p.W + lane;
+      const float base = p.scores[row];
+      const bool done = p.finished && p.finished[row];
+      const RowPieces r = p.pieces[row];                 // (set for kind 1 alone)
+      kind[lane] = !(base > -INFINITY) ? 0 : done ? 2 : 1;
+      base_sh[lane] = base;
+      n = kind[lane] == 1 ? r.n : kind[lane] == 2;
+      slot0[lane] = r.slot;
     }
-    top[w] = m;
-    base_sh[w] = base;
-    kind[w] = kd;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    first[lane + 1] = x;
+    if (lane == 0) { first[0] = 0; n_sh = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
   }
-  if (tid == 0) { n_sh = 0; bar_sh = -INFINITY; bar_at = INT_MAX; }
   __syncthreads();
-  // candidate c: entry c % K of list c / K; its score, -inf for none
-  auto value = [&](int c) -> double {
-    const int l = c / K, w = l / p.parts;
-    if (kind[w] == 0) return -INFINITY;
-    if (kind[w] == 2) return c == w * p.parts * K ? (double)base_sh[w] : -INFINITY;
-    const uint64_t key = p.keys[((int64_t)b * lists + l) * K + c % K];
-    return key ? (double)base_sh[w] + (((double)key_logit(key) - (double)top[w]) - lsum[w]) : -INFINITY;
+  const int lists = first[p.W];
+  auto row_of = [&](int c) {   // the row of candidate c, entry c % K of list c / K
+    const int l = c / K;
+    int lo = 0, hi = p.W;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= l) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  auto key_of = [&](int c, int w) -> uint64_t {
+    return kind[w] == 1 ? p.keys[(int64_t)(slot0[w] + c / K - first[w]) * K + c % K] : c % K == 0 ? 1 : 0;
+  };
+  // the first candidates are on their way while the sums are joined
+  constexpr int AHEAD = 4;
+  uint64_t key[AHEAD];
+  int kw[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int c = tid + i * BS_THREADS;
+    key[i] = 0;
+    kw[i] = 0;
+    if (c < lists * K) { kw[i] = row_of(c); key[i] = key_of(c, kw[i]); }
+  }
+  for (int w = tid >> 5; w < p.W; w += BS_WARPS) {   // a warp per row
+    if (kind[w] != 1) continue;
+    const float2* st = p.stat + (int64_t)(b * p.W + w) * p.nb * BS_WARPS;
+    const int n = p.nb * BS_WARPS;
+    float m = -INFINITY, s = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32 * 8) {   // 8 loads of a lane at a time
+      float2 v[8];
+      float top8 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * 32 + lane;
+        v[k] = i < n ? st[i] : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top8 = fmaxf(top8, v[k].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top8 = fmaxf(top8, __shfl_xor_sync(0xffffffffu, top8, o));
+      if (top8 == -INFINITY) continue;
+      float s8 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s8 += v[k].y * exp_from(v[k].x, top8);
+      join_sums(m, s, top8, s8);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      lsum[w] = s > 0.f ? log_sum(s) : 0.0;   // (a row of -inf has no keys)
+      top[w] = m;
+    }
+  }
+  __syncthreads();
+  // a candidate's score
+  auto value = [&](int w, uint64_t key) -> int64_t {
+    if (!key) return BM_NONE;
+    const double s = kind[w] == 2 ? (double)base_sh[w] : (double)base_sh[w] + (((double)key_logit(key) - (double)top[w]) - lsum[w]);
+    return s > -INFINITY ? ordered(s) : BM_NONE;
   };
   // equal scores: the lower beam; within a beam the logits decide, whatever the score's size leaves of them
-  auto key_of = [&](int c) { return kind[c / K / p.parts] == 1 ? p.keys[((int64_t)b * lists + c / K) * K + c % K] : 0ull; };
-  auto beats = [&](double s, int c, double s2, int c2) {
-    if (s != s2) return s > s2;
-    const int w = c / K / p.parts, w2 = c2 / K / p.parts;
-    if (w != w2) return w < w2;
-    return c != c2 && key_of(c) > key_of(c2);
+  auto before = [&](int c, int c2) {
+    const int w = row_of(c), w2 = row_of(c2);
+    return w != w2 ? w < w2 : c != c2 && key_of(c, w) > key_of(c2, w2);
   };
+  // how many of score[0 .. n-1], whose candidates at() names, come before one of score s at c (itself among them)
+  auto rank_of = [&](int64_t s, int c, int n, auto at) {
+    int rank = 0, same = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const int64_t o = score[j];
+      rank += o > s;
+      same += o == s;
+    }
+    if (same > 1)
+      for (int j = 0; j < n; ++j)
+        if (score[j] == s) rank += before(at(j), c);
+    return rank;
+  };
+  int64_t sc[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) sc[i] = value(kw[i], key[i]);
   if (lists >= K) {   // the K-th best head
-    for (int l = tid; l < lists; l += BS_THREADS) score[l] = value(l * K);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int c = tid + i * BS_THREADS;
+      if (c < lists * K && c % K == 0) score[c / K] = sc[i];
+    }
+    for (int l = tid; l < lists; l += BS_THREADS)
+      if (l * K >= AHEAD * BS_THREADS) score[l] = value(row_of(l * K), key_of(l * K, row_of(l * K)));
     __syncthreads();
     for (int l = tid; l < lists; l += BS_THREADS) {
-      const double s = score[l];
-      if (s == -INFINITY) continue;
-      int rank = 0;
-      for (int j = 0; j < lists; ++j) rank += beats(score[j], j * K, s, l * K);
+      const int64_t s = score[l];
+      if (s == BM_NONE) continue;
+      const int rank = rank_of(s, l * K, lists, [&](int j) { return j * K; });
       if (rank == K - 1) { bar_sh = s; bar_at = l * K; }
     }
     __syncthreads();
   }
-  const double bar = bar_sh;
+  const int64_t bar = bar_sh;
   const int at_bar = bar_at;
-  for (int c = tid; c < lists * K; c += BS_THREADS) {
-    const double s = value(c);
-    if (s > -INFINITY && (at_bar == INT_MAX || c == at_bar || !beats(bar, at_bar, s, c))) {
+  auto keep = [&](int c, int64_t s) {
+    if (s != BM_NONE && (s > bar || at_bar == INT_MAX || (s == bar && !before(at_bar, c)))) {
       const int i = atomicAdd(&n_sh, 1);
       if (i < BM_MOST) { score[i] = s; place[i] = c; }
     }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) keep(tid + i * BS_THREADS, sc[i]);
+  for (int c = tid + AHEAD * BS_THREADS; c < lists * K; c += BS_THREADS) {
+    const int w = row_of(c);
+    keep(c, value(w, key_of(c, w)));
   }
   __syncthreads();
   const int n = min(n_sh, BM_MOST);
   const int64_t out = (int64_t)b * K;
   const bool in = in_extent(out, K, (int64_t)p.B * K);
   for (int i = tid; i < n; i += BS_THREADS) {
-    const double s = score[i];
-    const int c = place[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += beats(score[j], place[j], s, c);
+    const int64_t s = score[i];
+    const int c = place[i], w = row_of(c);
+    const uint64_t key = key_of(c, w);
+    const int rank = rank_of(s, c, n, [&](int j) { return place[j]; });
     if (rank < K && in) {
-      const int w = c / K / p.parts;
       p.parents[out + rank] = w;
-      p.tokens[out + rank] = kind[w] == 2 ? p.pad : key_token(key_of(c));
-      p.out[out + rank] = (float)s;
+      p.tokens[out + rank] = kind[w] == 2 ? p.pad : key_token(key);
+      p.out[out + rank] = (float)from_ordered(s);
     }
   }
   for (int i = n + tid; i < K; i += BS_THREADS)
     if (in) { p.parents[out + i] = -1; p.tokens[out + i] = -1; p.out[out + i] = -INFINITY; }
 }
 
-// Parts of a row: the count at which the last wave of CTAs is fullest, parts of a batch at least, the fewest at equal waste.
-int select_parts(int64_t rows, int64_t V, int sms) {
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(BS_MAX_PARTS, (V + BS_BATCH - 1) / BS_BATCH));
-  const int64_t room = (int64_t)BS_CTAS_PER_SM * sms;
-  int best = 1;
-  double least = 1e300;
-  for (int64_t n = 1; n <= most; ++n) {
-    // waves of parts, each with what a part costs before and after its share of the row (about a batch)
-    const double cost = (double)((rows * n + room - 1) / room) * ((double)V / n + BS_BATCH);
-    if (cost < least) { least = cost; best = (int)n; }
-  }
-  return best;
+// CTAs of the first kernel, at most
+int64_t select_grid(int64_t rows, int64_t nb, int64_t ctas) {
+  return std::max<int64_t>(1, std::min({ctas, rows * nb, rows * (int64_t)BS_MAX_PIECES}));
 }
 
 // --------------------------------------------------------------------------------------- reorder
@@ -340,39 +635,41 @@ struct ReorderParams {
 // 16-byte vectors of `rows` rows of a page in one run of a pool, and in all of it.
 __device__ __forceinline__ int run_vecs(const BeamPool& q, int rows) { return (rows * q.row_bytes + 15) / 16; }
 
-// One request per CTA: its new table rows, the copies its new beams need, and its dead pages in order.
-__global__ void __launch_bounds__(BR_THREADS) beam_plan_kernel(const __grid_constant__ ReorderParams p) {
-  __shared__ int n[BR_MAX_W], par[BR_MAX_W], tile[BR_MAX_W][BR_THREADS], wsum[BR_THREADS / 32];
-  __shared__ unsigned kept_sh;
-  __shared__ int most_sh, n_copy_sh;
+// One request per CTA: its new table rows, the copies its new beams need, and its dead pages in order.  A thread takes one
+// entry of the table, (column, beam) in that order; the latency of three dependent loads is what it costs.
+__global__ void __launch_bounds__(BR_THREADS) beam_plan_kernel(const __grid_constant__ ReorderParams p, int beams_pow2) {
+  __shared__ int n[BR_MAX_W], par[BR_MAX_W], tile[BR_THREADS], wsum[BR_THREADS / 32];
+  __shared__ int n_copy_sh;
   __shared__ int64_t vecs_sh;
-  const int b = blockIdx.x, W = p.W, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.x, W = p.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t P = p.max_pages;
   pdl_trigger();
   const int* old = p.table + (int64_t)b * W * P;
   int* out = p.table_out + (int64_t)b * W * P;
   bool bad = false;
-  if (warp == 0) {
+  if (tid < BR_MAX_W) {
     int c = 0, q = -1;
-    if (lane < W) {
-      c = p.n_cached[b * W + lane];
-      q = p.parents[b * W + lane];
+    if (tid < W) {
+      c = p.n_cached[b * W + tid];
+      q = p.parents[b * W + tid];
       if (c < 0 || c > P * 128) { bad = true; c = 0; }
       if (q < -1 || q >= W) { bad = true; q = -1; }
     }
-    n[lane] = c;
-    par[lane] = q;
-    __syncwarp();
-    int most = c, mine = q >= 0 ? n[q] : 0;   // positions of the new beam
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    unsigned kept = 0;
-    for (int w = 0; w < W; ++w)
-      if (par[w] >= 0) kept |= 1u << par[w];
+    n[tid] = c;
+    par[tid] = q;
+  }
+  __syncthreads();
+  unsigned kept = 0;
+  int most = 0;
+  for (int w = 0; w < W; ++w) {
+    if (par[w] >= 0) kept |= 1u << par[w];
+    most = max(most, (n[w] + 127) / 128);
+  }
+  if (warp == 0) {
     // open pages that an earlier new beam already ends in
-    int page = -2 - lane;
+    const int q = par[lane], mine = q >= 0 ? n[q] : 0;   // positions of the new beam
     const bool open = mine % 128 != 0;
-    if (open) page = old[(int64_t)q * P + mine / 128];
+    int page = open ? old[(int64_t)q * P + mine / 128] : 0;
     bool copy = false;
     for (int w = 0; w < W; ++w) {
       const int other = __shfl_sync(0xffffffffu, page, w);
@@ -383,66 +680,48 @@ __global__ void __launch_bounds__(BR_THREADS) beam_plan_kernel(const __grid_cons
     const unsigned copies = __ballot_sync(0xffffffffu, copy);
     int64_t vecs = 0;
     if (copy) {
-      BeamCopy c2;
-      c2.src = page;
-      c2.rows = mine % 128;
-      c2.beam = lane;
-      c2.column = mine / 128;
-      for (int k = 0; k < p.n_pools; ++k) vecs += (int64_t)p.pool[k].runs * run_vecs(p.pool[k], c2.rows);
-      if (in_extent((int64_t)b * W + __popc(copies & ((1u << lane) - 1)), 1, (int64_t)p.B * W))
-        p.copies[(int64_t)b * W + __popc(copies & ((1u << lane) - 1))] = c2;
+      BeamCopy c;
+      c.src = page;
+      c.rows = mine % 128;
+      c.beam = lane;
+      c.column = mine / 128;
+      for (int k = 0; k < p.n_pools; ++k) vecs += (int64_t)p.pool[k].runs * run_vecs(p.pool[k], c.rows);
+      const int64_t at = (int64_t)b * W + __popc(copies & ((1u << lane) - 1));
+      if (in_extent(at, 1, (int64_t)p.B * W)) p.copies[at] = c;
     }
     if (lane < W && in_extent(b * W + lane, 1, (int64_t)p.B * W)) p.n_cached_out[b * W + lane] = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) vecs += __shfl_xor_sync(0xffffffffu, vecs, o);
-    if (lane == 0) { kept_sh = kept; most_sh = (most + 127) / 128; n_copy_sh = __popc(copies); vecs_sh = vecs; }
+    if (lane == 0) { n_copy_sh = __popc(copies); vecs_sh = vecs; }
+  }
+  const int w = tid % beams_pow2, cols = BR_THREADS / beams_pow2, col0 = tid - w;   // entries of this column: tile[col0 ..]
+  int n_dead = 0;
+  for (int j0 = 0; j0 < most; j0 += cols) {
+    const int j = j0 + tid / beams_pow2;
+    const bool held = w < W && j * 128 < n[w];
+    const int page = held ? old[w * P + j] : -1;
+    tile[tid] = page;
+    __syncthreads();       // (behind it the column may be overwritten: the new rows may be written in place)
+    bool dead = held;
+    if (held && (page < 0 || page >= p.n_pages)) { bad = true; dead = false; }
+    if (dead && ((kept >> w) & 1)) dead = false;
+    for (int v = 0; dead && v < W; ++v)   // held by a beam that is kept, or listed for a lower one
+      if (v != w && tile[col0 + v] == page && (v < w || ((kept >> v) & 1))) dead = false;
+    if (w < W && par[w] >= 0 && j * 128 < n[par[w]] && in_extent((int64_t)(b * W + w) * P + j, 1, (int64_t)p.B * W * P))
+      out[w * P + j] = tile[col0 + par[w]];
+    const unsigned mask = __ballot_sync(0xffffffffu, dead);
+    if (lane == 0) wsum[warp] = __popc(mask);
+    __syncthreads();
+    int at = n_dead + __popc(mask & ((1u << lane) - 1));
+    for (int v = 0; v < BR_THREADS / 32; ++v) {
+      if (v < warp) at += wsum[v];
+      n_dead += wsum[v];
+    }
+    if (dead && in_extent((int64_t)b * W * P + at, 1, (int64_t)p.B * W * P)) p.dead[(int64_t)b * W * P + at] = page;
+    __syncthreads();
   }
   __syncthreads();
-  const unsigned kept = kept_sh;
-  int n_dead = 0;
-  for (int j0 = 0; j0 < most_sh; j0 += BR_THREADS) {
-    const int j = j0 + threadIdx.x;
-    unsigned dead = 0;
-    if (j < most_sh) {
-      for (int w = 0; w < W; ++w) tile[w][threadIdx.x] = j * 128 < n[w] ? old[w * P + j] : -1;
-      for (int w = 0; w < W; ++w) {
-        if (j * 128 >= n[w]) continue;
-        const int page = tile[w][threadIdx.x];
-        if (page < 0 || page >= p.n_pages) { bad = true; continue; }
-        bool gone = !((kept >> w) & 1);
-        for (int v = 0; gone && v < W; ++v)
-          if (v != w && tile[v][threadIdx.x] == page && (v < w || ((kept >> v) & 1))) gone = false;
-        if (gone) dead |= 1u << w;
-      }
-      for (int w = 0; w < W; ++w)
-        if (par[w] >= 0 && j * 128 < n[par[w]] && in_extent((int64_t)(b * W + w) * P + j, 1, (int64_t)p.B * W * P))
-          out[w * P + j] = tile[par[w]][threadIdx.x];
-    }
-    // dead pages in the order of columns, then beams
-    const int c = __popc(dead);
-    int x = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int before = n_dead, all = 0;
-    for (int w = 0; w < BR_THREADS / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
-    }
-    int at = before + x - c;
-    for (int w = 0; w < W; ++w)
-      if ((dead >> w) & 1) {
-        const int64_t i = (int64_t)b * W * P + at++;
-        if (in_extent(i, 1, (int64_t)p.B * W * P)) p.dead[i] = tile[w][threadIdx.x];
-      }
-    n_dead += all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0 && in_extent(b, 1, p.B)) p.found[b] = BeamFound{n_copy_sh, n_dead, vecs_sh};
+  if (tid == 0 && in_extent(b, 1, p.B)) p.found[b] = BeamFound{n_copy_sh, n_dead, vecs_sh};
   if (bad) atomicOr(p.status, STATUS_BAD_PLAN);
 }
 
@@ -452,6 +731,13 @@ __device__ __forceinline__ int copy_target(const ReorderParams& p, int b, int i,
   if (i < n_dead) dst = p.dead[(int64_t)b * p.W * p.max_pages + i];
   else if (first_taken + i - n_dead < p.n_free) dst = p.free_pages[first_taken + i - n_dead];
   return src >= 0 && dst >= 0 && dst < p.n_pages ? dst : -1;
+}
+
+// The 16 bytes at `at` of a run of `bytes`, w where they are whole, else word by word.
+__device__ __forceinline__ void store_vec(const char* src, char* to, int at, int bytes, const uint4& w) {
+  if (at + 16 <= bytes) *reinterpret_cast<uint4*>(to + at) = w;
+  else
+    for (; at < bytes; at += 4) *reinterpret_cast<uint32_t*>(to + at) = *reinterpret_cast<const uint32_t*>(src + at);
 }
 
 // Bound by HBM for many copies, by the latency of a few dependent loads for few.  Every CTA sums up the requests' pages
@@ -548,26 +834,33 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
       const int v_from = (int)(x - first), v_to = (int)min(total, x1 - first);
       const char* src = q.base + (int64_t)c.src * q.page_bytes;
       char* to = q.base + (int64_t)dst * q.page_bytes;
-      for (int v = v_from + tid; dst >= 0 && v < v_to; v += BR_THREADS * BR_DEEP) {
-        uint4 w[BR_DEEP];
-        int64_t o[BR_DEEP];
-        int left[BR_DEEP];
+      if (dst < 0) {
+      } else if (nv >= BR_THREADS) {   // long runs, one after the other
+        int run = v_from / nv, r0 = v_from - run * nv, layer = run / q.parts, part = run - layer * q.parts;
+        for (int v = v_from; v < v_to;) {
+          const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
+          const int r1 = min(nv, r0 + v_to - v);
+          for (int r = r0 + tid; r < r1; r += BR_THREADS * BR_DEEP) {
+            uint4 w[BR_DEEP];
 #pragma unroll
-        for (int j = 0; j < BR_DEEP; ++j) {
-          const int vj = v + j * BR_THREADS;
-          left[j] = 0;
-          if (vj < v_to) {
-            const int run = vj / nv, r = vj - run * nv, layer = run / q.parts, part = run - layer * q.parts;
-            o[j] = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes + (int64_t)r * 16;
-            left[j] = bytes - r * 16;
-            if (left[j] >= 16) w[j] = *reinterpret_cast<const uint4*>(src + o[j]);
+            for (int j = 0; j < BR_DEEP; ++j)
+              if (r + j * BR_THREADS < r1 && (r + j * BR_THREADS) * 16 + 16 <= bytes)
+                w[j] = *reinterpret_cast<const uint4*>(src + o + (int64_t)(r + j * BR_THREADS) * 16);
+#pragma unroll
+            for (int j = 0; j < BR_DEEP; ++j)
+              if (r + j * BR_THREADS < r1) store_vec(src + o, to + o, (r + j * BR_THREADS) * 16, bytes, w[j]);
           }
+          v += r1 - r0;
+          r0 = 0;
+          if (++part == q.parts) { part = 0; ++layer; }
         }
-#pragma unroll
-        for (int j = 0; j < BR_DEEP; ++j) {
-          if (left[j] >= 16) *reinterpret_cast<uint4*>(to + o[j]) = w[j];
-          else
-            for (int y = 0; y < left[j]; y += 4) *reinterpret_cast<uint32_t*>(to + o[j] + y) = *reinterpret_cast<const uint32_t*>(src + o[j] + y);
+      } else {
+        for (int v = v_from + tid; v < v_to; v += BR_THREADS) {
+          const int run = v / nv, layer = run / q.parts, part = run - layer * q.parts, r = (v - run * nv) * 16;
+          const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (r + 16 <= bytes) w = *reinterpret_cast<const uint4*>(src + o + r);
+          store_vec(src + o, to + o, r, bytes, w);
         }
       }
       x = first + v_to;
@@ -581,35 +874,47 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
 
 bool beam_select_supported(int64_t B, int64_t W) { return W <= kBeamMaxW && B < ((int64_t)1 << 22) && B * W < ((int64_t)1 << 22); }
 constexpr int kMaxSms = 256;   // sizes the workspace, so that it does not depend on the device
-size_t beam_select_ws_bytes(int64_t B, int64_t W, int64_t V) {
-  // as many parts as any device may take
-  const size_t lists = (size_t)(B * W) * std::max<int64_t>(1, std::min<int64_t>(BS_MAX_PARTS, (V + BS_BATCH - 1) / BS_BATCH));
-  return round256(lists * kBeamMaxOut * sizeof(uint64_t)) + round256(lists * sizeof(float2));
+struct SelectWs { size_t pieces, stat, total; int64_t lists; };
+SelectWs select_ws(int64_t rows, int64_t V) {
+  const int64_t nb = (V + BS_BATCH - 1) / BS_BATCH;
+  SelectWs w;
+  w.lists = rows + select_grid(rows, nb, BS_CTAS_PER_SM * kMaxSms);
+  w.pieces = round256((size_t)w.lists * BS_MAX_K * sizeof(uint64_t));
+  w.stat = w.pieces + round256((size_t)rows * sizeof(RowPieces));
+  w.total = w.stat + round256((size_t)rows * nb * BS_WARPS * sizeof(float2));
+  return w;
 }
+size_t beam_select_ws_bytes(int64_t B, int64_t W, int64_t V) { return select_ws(B * W, V).total; }
 
-int launch_beam_select(const BeamSelectDesc& d, int num_sms, cudaStream_t st) {
+int launch_beam_select(const BeamSelectDesc& d, int num_sms, unsigned* status, cudaStream_t st) {
   SelectParams p;
+  const SelectWs ws = select_ws(d.B * d.W, d.V);
   p.z = d.logits; p.ld = d.ld;
   p.B = (int)d.B; p.W = (int)d.W; p.V = (int)d.V; p.K = (int)d.n_out;
-  p.parts = select_parts(d.B * d.W, d.V, num_sms);
-  p.part_len = (int)(((d.V + p.parts - 1) / p.parts + 3) & ~(int64_t)3);
+  p.nb = (int)((d.V + BS_BATCH - 1) / BS_BATCH);
   p.scores = d.scores; p.finished = d.finished; p.pad = d.pad_token;
   p.parents = d.parents; p.tokens = d.tokens; p.out = d.out_scores;
   p.keys = static_cast<uint64_t*>(d.ws);
-  const size_t lists = (size_t)(d.B * d.W) * p.parts;
-  p.stat = reinterpret_cast<float2*>(static_cast<char*>(d.ws) + round256(lists * p.K * sizeof(uint64_t)));
+  p.pieces = reinterpret_cast<RowPieces*>(static_cast<char*>(d.ws) + ws.pieces);
+  p.stat = reinterpret_cast<float2*>(static_cast<char*>(d.ws) + ws.stat);
+  p.n_lists = ws.lists;
+  p.status = status;
+  const bool vec = ((reinterpret_cast<uintptr_t>(d.logits) | (uintptr_t)(d.ld * 4)) & 15) == 0;
+  const int smem = bs_smem(p.K, vec);
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return -1;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BM_SMEM) != cudaSuccess) return -1;
+    if (cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BM_SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(beam_part_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bs_smem(BS_MAX_K, true)) != cudaSuccess ||
+        cudaFuncSetAttribute(beam_part_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bs_smem(BS_MAX_K, false)) != cudaSuccess)
+      return -1;
     attr_set[dev] = true;
   }
-  const unsigned grid = (unsigned)(d.B * d.W * p.parts);
-  const bool vec = ((reinterpret_cast<uintptr_t>(d.logits) | (uintptr_t)(d.ld * 4)) & 15) == 0;
-  if (vec) beam_part_kernel<true><<<grid, BS_THREADS, 0, st>>>(p);
-  else beam_part_kernel<false><<<grid, BS_THREADS, 0, st>>>(p);
+  const unsigned grid = (unsigned)select_grid(d.B * d.W, p.nb, BS_CTAS_PER_SM * std::min(num_sms, kMaxSms));
+  if (vec) beam_part_kernel<true><<<grid, BS_THREADS + 32, smem, st>>>(p);
+  else beam_part_kernel<false><<<grid, BS_THREADS + 32, smem, st>>>(p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   return launch_after(beam_merge_kernel, dim3((unsigned)d.B), dim3(BS_THREADS), BM_SMEM, st, p) == cudaSuccess ? 0 : -1;
 }
@@ -657,7 +962,9 @@ int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status,
     attr_set[dev] = true;
   }
   if (d.B > 0) {
-    beam_plan_kernel<<<(unsigned)d.B, BR_THREADS, 0, st>>>(p);
+    int pow2 = 1;
+    while (pow2 < d.W) pow2 *= 2;
+    beam_plan_kernel<<<(unsigned)d.B, BR_THREADS, 0, st>>>(p, pow2);
     if (cudaGetLastError() != cudaSuccess) return -1;
   }
   // CTAs for a few thousand vectors each, were every beam but one of each request to copy a whole page

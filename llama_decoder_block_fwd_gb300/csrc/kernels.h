@@ -318,7 +318,7 @@ struct BeamSelectDesc {
 };
 bool beam_select_supported(int64_t B, int64_t W);
 size_t beam_select_ws_bytes(int64_t B, int64_t W, int64_t V);
-int launch_beam_select(const BeamSelectDesc& d, int num_sms, cudaStream_t st);
+int launch_beam_select(const BeamSelectDesc& d, int num_sms, unsigned* status, cudaStream_t st);
 constexpr int kBeamMaxPools = 8;
 struct BeamReorderDesc {
   const int *parents, *n_cached, *table, *free_pages;
