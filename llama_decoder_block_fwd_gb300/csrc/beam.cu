@@ -607,7 +607,7 @@ int64_t select_grid(int64_t rows, int64_t nb, int64_t ctas) {
 constexpr int BR_THREADS = 256;
 constexpr int BR_MAX_W = (int)kBeamMaxW;
 constexpr int BR_MAX_POOLS = kBeamMaxPools;
-constexpr int BR_CTAS_PER_SM = 4;
+constexpr int BR_CTAS_PER_SM = 3;
 constexpr int BR_DEEP = 4;           // loads of a thread in flight
 
 struct BeamPool {
@@ -797,23 +797,9 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
     }
   }
   __syncthreads();
-  // entries of the copies, and the dead pages left over
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const BeamFound v = p.found[b];
-    if (tid < v.copies) {
-      const BeamCopy c = p.copies[(int64_t)b * p.W + tid];
-      const int dst = copy_target(p, b, tid, v.dead, t0[b], c.src);
-      if (c.src >= 0 && dst < 0) atomicOr(p.status, STATUS_BAD_PLAN);
-      const int64_t e = ((int64_t)b * p.W + c.beam) * p.max_pages + c.column;
-      if (in_extent(e, 1, (int64_t)p.B * p.W * p.max_pages)) p.table_out[e] = dst;
-    }
-    for (int i = tid; i < v.dead - v.copies; i += BR_THREADS)
-      if ((int64_t)f0[b] + i < p.freed_room) p.freed[f0[b] + i] = p.dead[(int64_t)b * p.W * p.max_pages + v.copies + i];
-  }
   // this CTA's range of vectors
   int64_t x = (int64_t)blockIdx.x * all[0] / gridDim.x;
   const int64_t x1 = (int64_t)(blockIdx.x + 1) * all[0] / gridDim.x;
-  if (x >= x1) return;
   int lo = 0, hi = p.B;
   while (hi - lo > 1) {   // the last request whose first vector is not behind x
     const int mid = (lo + hi) >> 1;
@@ -867,6 +853,19 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
       first += total;
     }
     ++i;
+  }
+  // entries of the copies, and the dead pages left over
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const BeamFound v = p.found[b];
+    if (tid < v.copies) {
+      const BeamCopy c = p.copies[(int64_t)b * p.W + tid];
+      const int dst = copy_target(p, b, tid, v.dead, t0[b], c.src);
+      if (c.src >= 0 && dst < 0) atomicOr(p.status, STATUS_BAD_PLAN);
+      const int64_t e = ((int64_t)b * p.W + c.beam) * p.max_pages + c.column;
+      if (in_extent(e, 1, (int64_t)p.B * p.W * p.max_pages)) p.table_out[e] = dst;
+    }
+    for (int i = tid; i < v.dead - v.copies; i += BR_THREADS)
+      if ((int64_t)f0[b] + i < p.freed_room) p.freed[f0[b] + i] = p.dead[(int64_t)b * p.W * p.max_pages + v.copies + i];
   }
 }
 
