@@ -185,6 +185,9 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
     return g < p.n_kv && i < p.r ? g * p.r + i : -1;
   };
   pdl_trigger();
+  const int per = (p.B + DP_THREADS - 1) / DP_THREADS;
+  const int s0 = min(p.B, (int)threadIdx.x * per), s1 = min(p.B, s0 + per);
+  const int pos0 = s0 < s1 ? __ldg(p.seq_pos + s0) : -1;   // on its way while the CTA is set up
   if (threadIdx.x == 0) {
     for (int i = 0; i < P_COUNT; ++i) {
       int cnt = 1;
@@ -206,11 +209,9 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
   if (warp == 1) { tmem_alloc(tmem_slot, DP_TMEM_COLS); tmem_relinquish(); }
 
   // tiles of all sequences: thread i adds up the contiguous sequences [i * per, (i + 1) * per)
-  const int per = (p.B + DP_THREADS - 1) / DP_THREADS;
-  const int s0 = min(p.B, (int)threadIdx.x * per), s1 = min(p.B, s0 + per);
   int64_t mine = 0;
   for (int b = s0; b < s1; ++b) {
-    const int pos = __ldg(p.seq_pos + b);
+    const int pos = b == s0 ? pos0 : __ldg(p.seq_pos + b);
     const int nt = (good_pos(pos, p.max_pos) + 128) / 128;
     mine += nt;
     if (blockIdx.x == 0 && pos != good_pos(pos, p.max_pos)) atomicOr(p.status, STATUS_BAD_PLAN);
@@ -583,48 +584,60 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
 }
 
 // Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (range, group,
-// row): the sequence whose first part is the range's tail; thread d its output element d.
-__global__ void __launch_bounds__(128) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
-  __shared__ float wgt[128];
-  __shared__ float red[8];
-  pdl_wait();
-  const int range = blockIdx.x, group = blockIdx.y, h = blockIdx.z, d = threadIdx.x, lane = d & 31, warp = d >> 5;
-  const SplitInfo s = p.split[range];
+// row): the sequence whose first part is the range's tail.  The latency of its dependent loads is what it costs, so every warp
+// forms all weights, one part per lane, and takes every fourth part's row, four elements per lane, all loads in flight.
+constexpr int DJ_WARPS = 4;
+__global__ void __launch_bounds__(32 * DJ_WARPS) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
+  __shared__ float4 sum[DJ_WARPS][32];
+  const int range = blockIdx.x, group = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int RH = R / pack, g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
+  pdl_wait();
+  const SplitInfo s = p.split[range];
   if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges || g >= p.n_kv || i >= p.r) return;
   const int n = s.last - range + 1;      // parts: the tail of `range`, then the first of each range up to `last`
   auto slot = [&](int k) { return ((int64_t)(k == 0 ? 2 * range + 1 : 2 * (range + k)) * p.groups + group) * R + h; };
   float m = -INFINITY;
-  for (int k = d; k < n; k += 128) m = fmaxf(m, p.part_ml[slot(k)].x);
+  for (int k = lane; k < n; k += 32) m = fmaxf(m, p.part_ml[slot(k)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float l = 0.f, acc = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 128) {
-    const int k = k0 + d;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool in = lane * 4 < p.hd;
+  for (int k0 = 0; k0 < n; k0 += 32) {
     float w = 0.f;
-    if (k < n) {
-      const float2 ml = p.part_ml[slot(k)];
+    if (k0 + lane < n) {
+      const float2 ml = p.part_ml[slot(k0 + lane)];
       w = exp2f(ml.x - m);
       l += w * ml.y;
     }
-    __syncthreads();
-    wgt[d] = w;
-    __syncthreads();
-    if (d < p.hd) {
-#pragma unroll 8
-      for (int j = 0; j < min(128, n - k0); ++j) acc = fmaf(wgt[j], p.part_o[slot(k0 + j) * p.hd + d], acc);
+    float4 v[32 / DJ_WARPS];
+#pragma unroll
+    for (int j = 0; j < 32 / DJ_WARPS; ++j) {
+      const int k = k0 + j * DJ_WARPS + warp;
+      v[j] = in && k < n ? reinterpret_cast<const float4*>(p.part_o + slot(k) * p.hd)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int j = 0; j < 32 / DJ_WARPS; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j * DJ_WARPS + warp);
+      acc.x = fmaf(wj, v[j].x, acc.x);
+      acc.y = fmaf(wj, v[j].y, acc.y);
+      acc.z = fmaf(wj, v[j].z, acc.z);
+      acc.w = fmaf(wj, v[j].w, acc.w);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[4 + warp] = l;
+  sum[warp][lane] = acc;
   __syncthreads();
-  l = (red[4] + red[5]) + (red[6] + red[7]);
-  const int64_t at = ((int64_t)s.b * p.n_q + (int64_t)g * p.r + i) * p.hd + d;
-  if (d < p.hd && in_extent(at, 1, (int64_t)p.B * p.n_q * p.hd)) p.o[at] = f2bf(acc / l);
+  const int64_t at = ((int64_t)s.b * p.n_q + (int64_t)g * p.r + i) * p.hd + lane * 4;
+  if (warp == 0 && in && in_extent(at, 4, (int64_t)p.B * p.n_q * p.hd)) {
+#pragma unroll
+    for (int w = 1; w < DJ_WARPS; ++w) {
+      const float4 v = sum[w][lane];
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l, acc.y / l), pack_bf2(acc.z / l, acc.w / l));
+  }
 }
 
 // Query rows of a CTA, head groups and, at most, ranges.
@@ -725,7 +738,7 @@ int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st
     }
   }
   if (rc != 0 || ranges == 1) return rc;   // one range cuts nothing
-  return launch_after(decode_join8p_kernel, dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R), dim3(128), 0, st, p,
+  return launch_after(decode_join8p_kernel, dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R), dim3(32 * DJ_WARPS), 0, st, p,
                       s.R, s.pack) == cudaSuccess ? 0 : -1;
 }
 
