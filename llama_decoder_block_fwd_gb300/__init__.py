@@ -422,11 +422,10 @@ def llama_verify_drafts(logits, draft_logits, temperature, cu_new, tokens, u, no
         *_scratch(w, ws, dev), st), w)
 
 
-def _codes(where, name, t, dev, shape):
+def _codes(where, name, t, torch, dev, shape):
     """The address of a contiguous tensor of E4M3 codes: uint8, or torch's float8_e4m3fn."""
-    import torch
-    dtype = torch.float8_e4m3fn if getattr(t, "dtype", None) is torch.float8_e4m3fn else torch.uint8
-    return _arg(where, name, t, dtype, dev, shape)
+    f8 = torch.float8_e4m3fn
+    return _arg(where, name, t, f8 if getattr(t, "dtype", None) is f8 else torch.uint8, dev, shape)
 
 
 def llama_rope_append_paged_kv8(dims, q, k, v, positions, slots, q_out, k_codes, k_scale, v_codes, v_scale, stream=None):
@@ -444,8 +443,8 @@ def llama_rope_append_paged_kv8(dims, q, k, v, positions, slots, q_out, k_codes,
     _check(L.llama_rope_append_paged_kv8(
         ctypes.byref(d), qa, qs, ka, ks, va, vs, _arg(w, "positions", positions, i32, dev, (S,)),
         _arg(w, "slots", slots, i32, dev, (S,)), _arg(w, "q_out", q_out, bf16, dev, (S, n_q, hd)),
-        _codes(w, "k_codes", k_codes, dev, pool), _arg(w, "k_scale", k_scale, f32, dev, rows),
-        _codes(w, "v_codes", v_codes, dev, pool), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages, st), w)
+        _codes(w, "k_codes", k_codes, torch, dev, pool), _arg(w, "k_scale", k_scale, f32, dev, rows),
+        _codes(w, "v_codes", v_codes, torch, dev, pool), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages, st), w)
 
 
 def llama_kv_dequantize_paged(k_codes, k_scale, v_codes, v_scale, block_table, n_pos, k_pool, v_pool, stream=None):
@@ -457,8 +456,8 @@ def llama_kv_dequantize_paged(k_codes, k_scale, v_codes, v_scale, block_table, n
     B, P, rows, codes = n_pos.numel(), block_table.shape[-1], (n_pages, n_kv, 128), (n_pages, 128, n_kv, hd)
     d = Dims(B, 0, 0, 0, n_kv, hd, 0, 1.0, 0.0)
     _check(L.llama_kv_dequantize_paged(
-        ctypes.byref(d), _codes(w, "k_codes", k_codes, dev, codes), _arg(w, "k_scale", k_scale, f32, dev, rows),
-        _codes(w, "v_codes", v_codes, dev, codes), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages,
+        ctypes.byref(d), _codes(w, "k_codes", k_codes, torch, dev, codes), _arg(w, "k_scale", k_scale, f32, dev, rows),
+        _codes(w, "v_codes", v_codes, torch, dev, codes), _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages,
         _arg(w, "block_table", block_table, i32, dev, (B, P)), P, _arg(w, "n_pos", n_pos, i32, dev),
         _arg(w, "k_pool", k_pool, bf16, dev, codes), _arg(w, "v_pool", v_pool, bf16, dev, codes), st), w)
 
@@ -474,8 +473,8 @@ def llama_gqa_attention_decode_paged_kv8(dims, q, k_codes, k_scale, v_codes, v_s
     n_pages, P = k_codes.shape[0], block_table.shape[-1]
     pool, rows, heads = (n_pages, 128, n_kv, hd), (n_pages, n_kv, 128), (B, d.n_q, hd)
     _check(L.llama_gqa_attention_decode_paged_kv8(
-        ctypes.byref(d), _arg(w, "q", q, bf16, dev, heads), _codes(w, "k_codes", k_codes, dev, pool),
-        _arg(w, "k_scale", k_scale, f32, dev, rows), _codes(w, "v_codes", v_codes, dev, pool),
+        ctypes.byref(d), _arg(w, "q", q, bf16, dev, heads), _codes(w, "k_codes", k_codes, torch, dev, pool),
+        _arg(w, "k_scale", k_scale, f32, dev, rows), _codes(w, "v_codes", v_codes, torch, dev, pool),
         _arg(w, "v_scale", v_scale, f32, dev, rows), n_pages, _arg(w, "block_table", block_table, i32, dev, (B, P)), P,
         _arg(w, "seq_pos", seq_pos, i32, dev, (B,)), max_pos, _arg(w, "o", o, bf16, dev, heads), *_scratch(w, ws, dev),
         st), w)
@@ -500,25 +499,16 @@ def _pools(where, name, pools, dev, n_pages, scales):
     """PagePool records of [n_layers, n_pages, 128, ...] tensors, or of scales [n_layers, n_pages, parts, 128]; the
     layers' axis may be missing."""
     out = []
-    for i, t in enumerate(pools):
-        _arg(where, f"{name}[{i}]", t, t.dtype, dev)
-        s = tuple(t.shape)
-        layers = len(s) > (3 if scales else 4)
-        lead, rest = (s[0], s[1:]) if layers else (1, s)
-        if scales:
-            ok = len(rest) == 3 and rest[0] == n_pages and rest[2] == 128
-            parts, row = (rest[1], t.element_size()) if ok else (0, 0)
+    for t in pools:
+        at, s, size = _arg(where, name, t, t.dtype, dev), t.shape, t.element_size()
+        k = len(s) - (3 if scales else 4)                # axes before the pages' own
+        if scales and 0 <= k <= 1 and s[k] == n_pages and s[-1] == 128:
+            out.append(PagePool(at, s[0] if k else 1, s[-2], size))
+        elif not scales and 0 <= k <= 1 and s[k] == n_pages and s[k + 1] == 128:
+            out.append(PagePool(at, s[0] if k else 1, 1, s[-2] * s[-1] * size))
         else:
-            ok = len(rest) >= 2 and rest[0] == n_pages and rest[1] == 128
-            parts, row = 1, 0
-            if ok:
-                row = t.element_size()
-                for x in rest[2:]:
-                    row *= x
-        if not ok:
-            raise ValueError(f"{where}: {name}[{i}] must be [n_layers, {n_pages}, " +
-                             (f"parts, 128], got {s}" if scales else f"128, ...], got {s}"))
-        out.append(PagePool(t.data_ptr(), lead, parts, row))
+            raise ValueError(f"{where}: {name} must be [n_layers, {n_pages}, " +
+                             (f"parts, 128], got {tuple(s)}" if scales else f"128, heads, width], got {tuple(s)}"))
     return out
 
 

@@ -156,7 +156,6 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
   __shared__ volatile int abort_sh;
   __shared__ float red[BS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = p.B * p.W;
-  pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < BS_STAGES; ++i) {
       mbar_init(&full[i], 1);
@@ -166,6 +165,8 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     abort_sh = 0;
     fence_mbar_init();
   }
+  pdl_wait();
+  pdl_trigger();
   // the range: of the rows that have to be read, or, of very many, of all (and the others are passed over)
   const bool all = rows > BS_SCAN;
   const int per = all ? 0 : (rows + BS_THREADS + 31) / (BS_THREADS + 32), r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
@@ -442,6 +443,7 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
   __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh, bar_at;   // first: list of each row, of the request's
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, K = p.K;
   pdl_wait();
+  pdl_trigger();
   // kind: 0 no candidates, 1 logits, 2 finished
   if (tid < 32) {
     int n = 0;
@@ -643,6 +645,7 @@ __global__ void __launch_bounds__(BR_THREADS) beam_plan_kernel(const __grid_cons
   __shared__ int64_t vecs_sh;
   const int b = blockIdx.x, W = p.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t P = p.max_pages;
+  pdl_wait();
   pdl_trigger();
   const int* old = p.table + (int64_t)b * W * P;
   int* out = p.table_out + (int64_t)b * W * P;
@@ -912,9 +915,10 @@ int launch_beam_select(const BeamSelectDesc& d, int num_sms, unsigned* status, c
     attr_set[dev] = true;
   }
   const unsigned grid = (unsigned)select_grid(d.B * d.W, p.nb, BS_CTAS_PER_SM * std::min(num_sms, kMaxSms));
-  if (vec) beam_part_kernel<true><<<grid, BS_THREADS + 32, smem, st>>>(p);
-  else beam_part_kernel<false><<<grid, BS_THREADS + 32, smem, st>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  const dim3 threads(BS_THREADS + 32);
+  if ((vec ? launch_after(beam_part_kernel<true>, dim3(grid), threads, smem, st, p)
+           : launch_after(beam_part_kernel<false>, dim3(grid), threads, smem, st, p)) != cudaSuccess)
+    return -1;
   return launch_after(beam_merge_kernel, dim3((unsigned)d.B), dim3(BS_THREADS), BM_SMEM, st, p) == cudaSuccess ? 0 : -1;
 }
 
@@ -963,8 +967,7 @@ int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status,
   if (d.B > 0) {
     int pow2 = 1;
     while (pow2 < d.W) pow2 *= 2;
-    beam_plan_kernel<<<(unsigned)d.B, BR_THREADS, 0, st>>>(p, pow2);
-    if (cudaGetLastError() != cudaSuccess) return -1;
+    if (launch_after(beam_plan_kernel, dim3((unsigned)d.B), dim3(BR_THREADS), 0, st, p, pow2) != cudaSuccess) return -1;
   }
   // CTAs for a few thousand vectors each, were every beam but one of each request to copy a whole page
   const int64_t work = std::max<int64_t>(d.B, (d.B * (d.W - 1) * vecs + 4 * BR_THREADS * BR_DEEP - 1) / (4 * BR_THREADS * BR_DEEP));

@@ -184,10 +184,6 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
     const int g = g0 + h / RH, i = sub * RH + h % RH;
     return g < p.n_kv && i < p.r ? g * p.r + i : -1;
   };
-  pdl_trigger();
-  const int per = (p.B + DP_THREADS - 1) / DP_THREADS;
-  const int s0 = min(p.B, (int)threadIdx.x * per), s1 = min(p.B, s0 + per);
-  const int pos0 = s0 < s1 ? __ldg(p.seq_pos + s0) : -1;   // on its way while the CTA is set up
   if (threadIdx.x == 0) {
     for (int i = 0; i < P_COUNT; ++i) {
       int cnt = 1;
@@ -208,10 +204,14 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
   fence_proxy_async_smem();
   if (warp == 1) { tmem_alloc(tmem_slot, DP_TMEM_COLS); tmem_relinquish(); }
 
+  pdl_wait();   // nothing of the caller's is read or written before
+  pdl_trigger();
   // tiles of all sequences: thread i adds up the contiguous sequences [i * per, (i + 1) * per)
+  const int per = (p.B + DP_THREADS - 1) / DP_THREADS;
+  const int s0 = min(p.B, (int)threadIdx.x * per), s1 = min(p.B, s0 + per);
   int64_t mine = 0;
   for (int b = s0; b < s1; ++b) {
-    const int pos = b == s0 ? pos0 : __ldg(p.seq_pos + b);
+    const int pos = __ldg(p.seq_pos + b);
     const int nt = (good_pos(pos, p.max_pos) + 128) / 128;
     mine += nt;
     if (blockIdx.x == 0 && pos != good_pos(pos, p.max_pos)) atomicOr(p.status, STATUS_BAD_PLAN);
@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(32 * DJ_WARPS) decode_join8p_kernel(const __gr
   const int range = blockIdx.x, group = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int RH = R / pack, g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
   pdl_wait();
+  pdl_trigger();
   const SplitInfo s = p.split[range];
   if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges || g >= p.n_kv || i >= p.r) return;
   const int n = s.last - range + 1;      // parts: the tail of `range`, then the first of each range up to `last`
@@ -677,9 +678,10 @@ int launch_attn(const DecodeAttn8pParams& p, int dev, cudaStream_t st) {
       return -1;
     attr_set[dev] = true;
   }
-  // launched plainly: everything before it in the stream is complete
-  decode_attn8p_kernel<R, PACK><<<(unsigned)(p.n_ranges * p.groups), DP_THREADS, DpSmem::TOTAL, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_after(decode_attn8p_kernel<R, PACK>, dim3((unsigned)(p.n_ranges * p.groups)), dim3(DP_THREADS), DpSmem::TOTAL, st, p) ==
+                 cudaSuccess
+             ? 0
+             : -1;
 }
 
 }  // namespace

@@ -203,8 +203,9 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// A kernel that may begin while its predecessor in the stream drains, whatever pdl_enabled() says: for the second kernel of a
-// call, which waits in pdl_wait.
+// A kernel that may begin while its predecessor in the stream drains, whatever pdl_enabled() says: it waits in pdl_wait before it
+// touches memory, and triggers, if at all, behind that wait.  A kernel that writes to a cache does not trigger: others read
+// cached rows before they wait (see pdl_wait).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg;
