@@ -417,7 +417,7 @@ int llama_rope_append_paged_kv8(const llama_dims* dims, const void* q, int64_t q
  * (exact for the scales that llama_rope_append_paged_kv8 writes, where bf16 has the value).  k_pool and v_pool
  * [n_pages, 128, n_kv, head_dim] bf16: one layer's worth serves every layer in turn.  Rows that no sequence holds
  * are left as they were; pages may be shared between sequences.  Uses B, n_kv and head_dim.
- *   n_pos [B] int32: positions to read back, 0 .. 128 * max_pages
+ *   n_pos [B] int32: positions to read back, 0 .. 128 * max_pages, at most 2^24
  * LLAMA_ERR_UNSUPPORTED for head_dim above 256 or no multiple of 8, n_kv > 4096, B > 65535, n_pages >= 2^24,
  * max_pages >= 2^31; LLAMA_ERR_INVALID_ARG for other bad dims, n_pages < 1, max_pages < 1, NULL arrays;
  * LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte or others not 16-byte aligned.  Latched as

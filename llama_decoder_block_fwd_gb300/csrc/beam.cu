@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
         for (int b = b0; b < b1; ++b, ++j) {
           const int st = j % BS_STAGES, e = b * BS_BATCH;
           if (j >= BS_STAGES && !mbar_wait(&pushed[st], (j / BS_STAGES - 1) & 1, &abort_sh, p.status)) return;
+          if (!in_extent((int64_t)row * p.ld + e, min(BS_BATCH, p.V - e), (int64_t)(rows - 1) * p.ld + p.V)) { abort_sh = 1; return; }
           const uint32_t bytes = (min(e + BS_BATCH, p.V) - e) / 4 * 16;   // whole vectors; up to three logits behind them are read directly
           mbar_arrive_expect_tx(&full[st], bytes);
           if (bytes)
@@ -823,7 +824,10 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
       const int v_from = (int)(x - first), v_to = (int)min(total, x1 - first);
       const char* src = q.base + (int64_t)c.src * q.page_bytes;
       char* to = q.base + (int64_t)dst * q.page_bytes;
-      if (dst < 0) {
+      // (a layer holds both pages whole; the last row that is written lies in the last run)
+      const bool in = in_extent((int64_t)max(dst, 0) * q.page_bytes, q.page_bytes, q.layer_bytes) &&
+                      in_extent((int64_t)(q.parts - 1) * 128 * q.row_bytes, bytes, q.page_bytes);
+      if (dst < 0 || !in) {
       } else if (nv >= BR_THREADS) {   // long runs, one after the other
         int run = v_from / nv, r0 = v_from - run * nv, layer = run / q.parts, part = run - layer * q.parts;
         for (int v = v_from; v < v_to;) {
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
       if (in_extent(e, 1, (int64_t)p.B * p.W * p.max_pages)) p.table_out[e] = dst;
     }
     for (int i = tid; i < v.dead - v.copies; i += BR_THREADS)
-      if ((int64_t)f0[b] + i < p.freed_room) p.freed[f0[b] + i] = p.dead[(int64_t)b * p.W * p.max_pages + v.copies + i];
+      if ((int64_t)f0[b] + i < p.freed_room && in_extent(f0[b], 1, p.freed_room)) p.freed[f0[b] + i] = p.dead[(int64_t)b * p.W * p.max_pages + v.copies + i];
   }
 }
 

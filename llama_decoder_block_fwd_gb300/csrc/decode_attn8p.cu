@@ -300,7 +300,11 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
           const int ks = tile % DP_KSTAGES, sc = tile % DP_SSTAGES;
           ok = mbar_wait(&bars[P_KE + ks], ((tile / DP_KSTAGES) & 1) ^ 1, abort_flag, p.status) &&
                mbar_wait(&bars[P_SCE + sc], ((tile / DP_SSTAGES) & 1) ^ 1, abort_flag, p.status);
-          if (ok && !box_in(g0 * HD, p.n_kv * HD, (int64_t)page * 128, (int64_t)p.n_pages * 128)) { *abort_flag = 1; ok = false; }
+          if (ok && !(box_in(g0 * HD, p.n_kv * HD, (int64_t)page * 128, (int64_t)p.n_pages * 128) &&
+                      in_extent(((int64_t)page * p.n_kv + g0) * 128, n_sc * 128, (int64_t)p.n_pages * p.n_kv * 128))) {
+            *abort_flag = 1;
+            ok = false;
+          }
           if (ok) {
             mbar_arrive_expect_tx(&bars[P_KF + ks], L::F8);
             tma_load_2d(sbase + L::OFF_K8 + ks * L::F8, &p.tmK, &bars[P_KF + ks], g0 * HD, page * 128);
@@ -661,7 +665,7 @@ int ranges_of(const Shape& s, int64_t B, int64_t max_pos, int sms) {
 constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 struct Parts { size_t ml, split, total; };
 Parts parts_of(const Shape& s, int ranges, int64_t hd) {
-  const size_t rows = (size_t)2 * ranges * s.groups * s.R;
+  const size_t rows = ranges > 1 ? (size_t)2 * ranges * s.groups * s.R : 0;   // one range cuts nothing
   Parts a;
   a.ml = round256(rows * hd * sizeof(float));
   a.split = a.ml + round256(rows * sizeof(float2));

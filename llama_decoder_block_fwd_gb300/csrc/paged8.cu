@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(DQ_THREADS, DQ_CTAS_PER_SM) dequant8_kernel(co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto pages_of = [&](int b, bool tell) {
     const int n = __ldg(p.n_pos + b);
-    const bool bad = n < 0 || n > p.max_pages * 128;
+    const bool bad = n < 0 || n > p.max_pages * 128 || n > (1 << 24);
     if (bad && tell) atomicOr(p.status, STATUS_BAD_PLAN);
     return bad ? 0 : (n + 127) / 128;
   };

@@ -144,6 +144,33 @@ def test_select_of_sharp_and_far_logits():
     _check_select(z, scores, None, 0, K, got)
 
 
+def test_select_of_very_many_rows():
+    """More rows than every CTA looks through for the ones to read: none left out, finished and empty ones passed over."""
+    rng = np.random.default_rng(9)
+    B, W, V, K = 900, 20, 37, 5
+    z = rng.normal(size=(B, W, V)) * 2
+    scores = -10 * rng.random((B, W))
+    scores[rng.random((B, W)) < 0.2] = -np.inf
+    finished = (rng.random((B, W)) < 0.2).astype(np.int32)
+    scores[3], finished[4], finished[5] = -np.inf, 1, 0
+    got = _select(z, scores, finished, 2, K)
+    some = list(range(0, B, 29)) + [3, 4, 5, B - 1]
+    _check_select(z[some], scores[some], finished[some], 2, K, tuple(g[some] for g in got))
+
+
+def test_select_gives_the_same_bits_again_and_for_equal_rows():
+    rng = np.random.default_rng(11)
+    row = rng.normal(size=128256) * 2.5
+    z = np.broadcast_to(row, (3, 7, 128256))
+    scores = np.full((3, 7), -4.0)
+    a, b = _select(z, scores, None, 0, 9), _select(z, scores, None, 0, 9, ld=128260)
+    for x, y in zip(a, b):
+        np.testing.assert_array_equal(x, y)
+    # equal beams: each token from every beam in turn
+    np.testing.assert_array_equal(a[0][0], [0, 1, 2, 3, 4, 5, 6, 0, 1])
+    assert len(set(a[2][0][:7].tolist())) == 1 and len(set(a[1][0][:7].tolist())) == 1
+
+
 def test_select_captured_and_on_two_streams():
     import torch
     B, W, V, K = 2, 4, 32000, 8

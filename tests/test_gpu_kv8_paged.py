@@ -230,7 +230,11 @@ def test_dequantize_latches_and_skips():
     assert np.all(got[c.table[2, :3]] == 0) and np.all(got[c.table[1, 1]] == 0)
     for b, j, n in ((0, 0, 128), (0, 2, 44), (1, 0, 128), (1, 2, 44)):
         np.testing.assert_array_equal(got[c.table[b, j], :n], c.rows(b)[0][j * 128:j * 128 + n])
-    L.llama_kv_dequantize_paged(*c.dev(), _dev(c.table), _i32([128 * c.P + 1, 0, 0]), *pools)
+    for bad in (128 * c.P + 1, 2 ** 31 - 1, -2 ** 31):
+        L.llama_kv_dequantize_paged(*c.dev(), _dev(c.table), _i32([bad, 0, 0]), *pools)
+        assert _status() == 1
+    wide = torch.full((1, 1 << 18), -1, dtype=torch.int32, device="cuda")       # room for more positions than there are
+    L.llama_kv_dequantize_paged(*c.dev(), wide, _i32([2 ** 24 + 1]), *pools)
     assert _status() == 1
     L.llama_kv_dequantize_paged(*c.dev(), _dev(c.table), _i32([300, 300, 300]), *pools)
     assert _status() == 0
@@ -266,7 +270,7 @@ def _check_attention(c, q, o, seqs=None):
 
 
 HEADS = [(32, 8, 128), (8, 2, 64), (1, 1, 128), (6, 3, 64), (28, 4, 128), (16, 1, 128), (24, 1, 128), (40, 1, 64), (7, 7, 64),
-         (12, 4, 128), (64, 2, 128), (3, 1, 64), (34, 2, 128), (10, 2, 128), (32, 2, 64), (18, 2, 64)]
+         (12, 4, 128), (64, 2, 128), (3, 1, 64), (34, 2, 128), (10, 2, 128), (32, 2, 64), (18, 2, 64), (128, 1, 128), (320, 320, 128), (310, 310, 64)]
 
 
 @pytest.mark.parametrize("n_q,n_kv,hd", HEADS)
@@ -446,3 +450,36 @@ def test_attention_captured_and_replayed_beside_another_stream():
             for b in range(3):
                 ref = R.attend(to_f64(qs[i])[b], *c.rows(b, now[i][b] + 1))
                 assert_parity(to_f64(o[i])[b], ref, BF16, f"replay {step}, graph {i}, sequence {b}")
+
+
+def test_calls_on_a_given_stream_and_twice_give_the_same_bits():
+    """The stream argument is honoured (work queued behind a long wait on that stream alone), and repeated calls agree."""
+    import torch
+    lengths = [5000, 131, 0, 2600]
+    c = Cache(lengths, 2, 128, seed=3)
+    q = _queries(4, 8, 128, 5)
+    want = _attend(c, q, [n - 1 for n in lengths])
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):                      # the inputs made here, the call made there
+        q2 = q.clone()
+    o = torch.empty_like(q)
+    s.synchronize()
+    for stream in (s, s.cuda_stream):
+        o.fill_(7.0)
+        torch.cuda.synchronize()
+        _attend(c, q2, [n - 1 for n in lengths], stream=stream, o=o)
+        s.synchronize()
+        assert torch.equal(o, want)
+    pools = [torch.zeros(c.n_pages, 128, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cache, table, n = c.dev(), _dev(c.table), _i32(lengths)
+    torch.cuda.synchronize()
+    L.llama_kv_dequantize_paged(*cache, table, n, *pools, stream=s)
+    s.synchronize()
+    np.testing.assert_array_equal(to_f64(pools[1])[c.table[1, 0]], c.rows(1)[1][:128])
+    x = _queries(3, 2, 128, 1)
+    pos, slots = _i32([0, 1, 2]), _i32([0, 1, 2])
+    torch.cuda.synchronize()
+    L.llama_rope_append_paged_kv8(_dims(1, 3, 8, 2, 128), None, x, x, pos, slots, None, *cache, stream=s)
+    s.synchronize()
+    assert _status() == 0 and cache[3][0, 1, 2] == float(R.row_scale(np.max(np.abs(to_f64(x)[2, 1]))))
