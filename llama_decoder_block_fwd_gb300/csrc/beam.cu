@@ -26,7 +26,7 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // grown.  The second kernel joins a request's lists and sums.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
-constexpr int BS_PER = 16;                              // logits of a thread in a batch
+constexpr int BS_PER = 20;                              // logits of a thread in a batch
 constexpr int BS_BATCH = BS_THREADS * BS_PER;
 constexpr int BS_STAGES = 3;
 constexpr int BS_MAX_K = (int)kBeamMaxOut;
@@ -298,14 +298,17 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
         bar = key_logit(floor);
       }
     };
-    // No room for what is above the bar in the batch y (one warp's logits, equal ones, rising rows): a higher bar that the
+    // A logit of batch b again, for the few that are looked at twice.
+    auto again = [&](int b, int k) { return token(b, k) < p.V ? __ldg(z + token(b, k)) : -INFINITY; };
+    // No room for what is above the bar in batch b (one warp's logits, equal ones, rising rows): a higher bar that the
     // bests of K to 2 K threads reach, by bisection on the keys, which differ.  At least K logits reach it, and at most
     // BS_PER of each of those threads.
-    auto squeeze = [&](int b, const float (&y)[BS_PER]) {
+    auto squeeze = [&](int b) {
       uint64_t best = 0, lo = 1, hi = ~0ull;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < BS_PER; ++k) {
-        const uint64_t key = y[k] > bar ? cand_key(y[k], token(b, k)) : 0;
+        const float v = again(b, k);
+        const uint64_t key = v > bar ? cand_key(v, token(b, k)) : 0;
         best = key > best ? key : best;
       }
       if (takers_count(best >= lo) >= 2 * K)
@@ -321,31 +324,41 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
         }
       if (tid == 0) n_sh = n;
       takers_sync();
-      if (best >= lo) {
-#pragma unroll
+      if (best >= lo)
+#pragma unroll 1
         for (int k = 0; k < BS_PER; ++k) {
-          const uint64_t key = y[k] > bar ? cand_key(y[k], token(b, k)) : 0;
+          const float v = again(b, k);
+          const uint64_t key = v > bar ? cand_key(v, token(b, k)) : 0;
           if (key >= lo) {
             const int at = atomicAdd(&n_sh, 1);
             if (at < room) list[at] = key;
           }
         }
-      }
       takers_sync();
       n = min(n_sh, room);
     };
-    auto push = [&](int b, auto counts) {   // what counts(logit) says
+    // What counts(logit) says of batch b, the CTA's j-th, to the list: the fours that have some are looked at again where
+    // they lie (a loop, since a kernel this short pays for the code that it runs through once).
+    auto push = [&](int b, auto counts) {
       int* counter = &cnt[j % BS_STAGES];
+      unsigned fours = 0;
 #pragma unroll
-      for (int g = 0; g < BS_PER / 4; ++g)
-        if (counts(four[g])) {
+      for (int g = 0; g < BS_PER / 4; ++g) fours |= counts(four[g]) ? 1u << g : 0u;
+      const bool whole = VEC && (b + 1) * BS_BATCH <= p.V;
+#pragma unroll 1
+      for (; fours; fours &= fours - 1) {
+        const int k = 4 * (__ffs(fours) - 1);
+        float4 v;
+        if (whole) v = reinterpret_cast<const float4*>(ring + j % BS_STAGES * BS_BATCH)[k / 4 * BS_THREADS + tid];
+        else v = make_float4(again(b, k), again(b, k + 1), again(b, k + 2), again(b, k + 3));
+        const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 4 * g; k < 4 * g + 4; ++k)
-            if (counts(x[k])) {
-              const int at = n + atomicAdd(counter, 1);
-              if (at < room) list[at] = cand_key(x[k], token(b, k));
-            }
-        }
+        for (int c = 0; c < 4; ++c)
+          if (counts(w[c])) {
+            const int at = n + atomicAdd(counter, 1);
+            if (at < room) list[at] = cand_key(w[c], token(b, k + c));
+          }
+      }
     };
     {  // the first batch: in each warp the bests of at least ceil(K / 8) threads reach its own n-th, so at least K logits
        // reach the least of these
@@ -362,7 +375,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       takers_sync();
       if (lane == 0) mbar_arrive(&pushed[j % BS_STAGES]);
       const int c = cnt[j % BS_STAGES];
-      if (c > room) squeeze(b0, x);
+      if (c > room) squeeze(b0);
       else n = c;
       cut();
       ++j;
@@ -373,13 +386,8 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       if (!mbar_wait(&pushed[i % BS_STAGES], (i / BS_STAGES) & 1, &abort_sh, p.status)) return false;
       const int c = cnt[i % BS_STAGES];
       if (tid == 0) cnt[(i + BS_STAGES - 1) % BS_STAGES] = 0;      // batch i - 1's, which everyone has read
-      if (n + c > room) {
-        float y[BS_PER];
-        load(b, y);
-        squeeze(b, y);
-      } else {
-        n += c;
-      }
+      if (n + c > room) squeeze(b);
+      else n += c;
       cut();
       return true;
     };
@@ -415,8 +423,10 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
 
 // Joins a request's rows: each piece's list is in order, so a candidate below the n_out-th best of the lists' heads is none
 // of the n_out best; the others are ranked against each other.
-constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: n_out lists (or fewer lists than n_out) of n_out
-constexpr int BM_SMEM = BM_MOST * (int)(sizeof(int64_t) + sizeof(int));
+constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: the bar leaves n_out of n_out lists, or of fewer all
+constexpr int BM_LISTS = (int)kBeamMaxW + BS_CTAS_PER_SM * 256;   // of a request, at most (256: kMaxSms)
+constexpr int BM_LEAD = 64;
+constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS;
 
 // Doubles as integers that order as they do.
 __device__ __forceinline__ int64_t ordered(double s) {
@@ -436,12 +446,14 @@ __device__ __forceinline__ double log_sum(float s) {
 }
 
 __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ int64_t score[];                     // [BM_MOST], then their places
-  int* place = reinterpret_cast<int*>(score + BM_MOST);
-  __shared__ double lsum[kBeamMaxW];                     // log of a row's sum of exp(z - its maximum)
+  extern __shared__ int64_t score[];                     // [BM_MOST], then their keys and places, then each list's row
+  uint64_t* key_sh = reinterpret_cast<uint64_t*>(score + BM_MOST);
+  int* place = reinterpret_cast<int*>(key_sh + BM_MOST);
+  uint8_t* row_of = reinterpret_cast<uint8_t*>(place + BM_MOST);
+  // a row's candidates score (logit - top) + offset, offset its beam's score less the log of its sum of exp(z - top)
+  __shared__ double offset[kBeamMaxW], top[kBeamMaxW];
   __shared__ int64_t bar_sh;
-  __shared__ float base_sh[kBeamMaxW], top[kBeamMaxW];
-  __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh, bar_at;   // first: list of each row, of the request's
+  __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh[2], bar_at;   // first: list of each row, of the request's
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, K = p.K;
   pdl_wait();
   pdl_trigger();
@@ -454,7 +466,8 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
       const bool done = p.finished && p.finished[row];
       const RowPieces r = p.pieces[row];                 // (set for kind 1 alone)
       kind[lane] = !(base > -INFINITY) ? 0 : done ? 2 : 1;
-      base_sh[lane] = base;
+      offset[lane] = base;
+      top[lane] = 0.0;
       n = kind[lane] == 1 ? r.n : kind[lane] == 2;
       slot0[lane] = r.slot;
     }
@@ -465,137 +478,99 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
       if (lane >= o) x += y;
     }
     first[lane + 1] = x;
-    if (lane == 0) { first[0] = 0; n_sh = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
+    if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
   }
   __syncthreads();
   const int lists = first[p.W];
-  auto row_of = [&](int c) {   // the row of candidate c, entry c % K of list c / K
-    const int l = c / K;
-    int lo = 0, hi = p.W;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= l) lo = mid; else hi = mid;
-    }
-    return lo;
+  for (int w = 0; w < p.W; ++w)
+    for (int l = first[w] + tid; l < first[w + 1]; l += BS_THREADS) row_of[l] = (uint8_t)w;
+  auto key_of = [&](int l, int k, int w) -> uint64_t {   // entry k of list l, of row w
+    return kind[w] == 1 ? p.keys[(int64_t)(slot0[w] + l - first[w]) * K + k] : k == 0 ? cand_key(0.f, p.pad) : 0;
   };
-  auto key_of = [&](int c, int w) -> uint64_t {
-    return kind[w] == 1 ? p.keys[(int64_t)(slot0[w] + c / K - first[w]) * K + c % K] : c % K == 0 ? 1 : 0;
-  };
-  // the first candidates are on their way while the sums are joined
-  constexpr int AHEAD = 4;
-  uint64_t key[AHEAD];
-  int kw[AHEAD];
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    const int c = tid + i * BS_THREADS;
-    key[i] = 0;
-    kw[i] = 0;
-    if (c < lists * K) { kw[i] = row_of(c); key[i] = key_of(c, kw[i]); }
-  }
   for (int w = tid >> 5; w < p.W; w += BS_WARPS) {   // a warp per row
     if (kind[w] != 1) continue;
     const float2* st = p.stat + (int64_t)(b * p.W + w) * p.nb * BS_WARPS;
     const int n = p.nb * BS_WARPS;
     float m = -INFINITY, s = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32 * 8) {   // 8 loads of a lane at a time
-      float2 v[8];
-      float top8 = -INFINITY;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32 * 4) {   // 4 loads of a lane at a time
+      float2 v[4];
+      float top4 = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         const int i = i0 + k * 32 + lane;
         v[k] = i < n ? st[i] : make_float2(-INFINITY, 0.f);
+        top4 = fmaxf(top4, v[k].x);
       }
+      float mx;
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(top4));
+      if (mx == -INFINITY) continue;
+      float s4 = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top8 = fmaxf(top8, v[k].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top8 = fmaxf(top8, __shfl_xor_sync(0xffffffffu, top8, o));
-      if (top8 == -INFINITY) continue;
-      float s8 = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s8 += v[k].y * exp_from(v[k].x, top8);
-      join_sums(m, s, top8, s8);
+      for (int k = 0; k < 4; ++k) s4 += v[k].y * exp_from(v[k].x, mx);
+      join_sums(m, s, mx, s4);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      lsum[w] = s > 0.f ? log_sum(s) : 0.0;   // (a row of -inf has no keys)
+    if (lane == 0 && s > 0.f) {   // (a row of -inf has no keys)
+      offset[w] -= log_sum(s);
       top[w] = m;
     }
   }
   __syncthreads();
-  // a candidate's score
-  auto value = [&](int w, uint64_t key) -> int64_t {
-    if (!key) return BM_NONE;
-    const double s = kind[w] == 2 ? (double)base_sh[w] : (double)base_sh[w] + (((double)key_logit(key) - (double)top[w]) - lsum[w]);
-    return s > -INFINITY ? ordered(s) : BM_NONE;
-  };
-  // equal scores: the lower beam; within a beam the logits decide, whatever the score's size leaves of them
-  auto before = [&](int c, int c2) {
-    const int w = row_of(c), w2 = row_of(c2);
-    return w != w2 ? w < w2 : c != c2 && key_of(c, w) > key_of(c2, w2);
-  };
-  // how many of score[0 .. n-1], whose candidates at() names, come before one of score s at c (itself among them)
-  auto rank_of = [&](int64_t s, int c, int n, auto at) {
-    int rank = 0, same = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const int64_t o = score[j];
-      rank += o > s;
-      same += o == s;
-    }
-    if (same > 1)
-      for (int j = 0; j < n; ++j)
-        if (score[j] == s) rank += before(at(j), c);
-    return rank;
-  };
-  int64_t sc[AHEAD];
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) sc[i] = value(kw[i], key[i]);
-  if (lists >= K) {   // the K-th best head
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int c = tid + i * BS_THREADS;
-      if (c < lists * K && c % K == 0) score[c / K] = sc[i];
-    }
-    for (int l = tid; l < lists; l += BS_THREADS)
-      if (l * K >= AHEAD * BS_THREADS) score[l] = value(row_of(l * K), key_of(l * K, row_of(l * K)));
-    __syncthreads();
-    for (int l = tid; l < lists; l += BS_THREADS) {
-      const int64_t s = score[l];
-      if (s == BM_NONE) continue;
-      const int rank = rank_of(s, l * K, lists, [&](int j) { return j * K; });
-      if (rank == K - 1) { bar_sh = s; bar_at = l * K; }
-    }
-    __syncthreads();
-  }
-  const int64_t bar = bar_sh;
-  const int at_bar = bar_at;
-  auto keep = [&](int c, int64_t s) {
-    if (s != BM_NONE && (s > bar || at_bar == INT_MAX || (s == bar && !before(at_bar, c)))) {
-      const int i = atomicAdd(&n_sh, 1);
-      if (i < BM_MOST) { score[i] = s; place[i] = c; }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) keep(tid + i * BS_THREADS, sc[i]);
-  for (int c = tid + AHEAD * BS_THREADS; c < lists * K; c += BS_THREADS) {
-    const int w = row_of(c);
-    keep(c, value(w, key_of(c, w)));
-  }
-  __syncthreads();
-  const int n = min(n_sh, BM_MOST);
+  // First the lists' leading entries, n_out or some BM_LEAD in all: their n_out-th best is a bar.  Then what reaches it, of all
+  // entries.  (One loop for both: a kernel this short pays for the code that it runs through once.)
+  const int lead = lists ? min(K, max((K + lists - 1) / lists, BM_LEAD / lists)) : 0;   // of each list
   const int64_t out = (int64_t)b * K;
   const bool in = in_extent(out, K, (int64_t)p.B * K);
-  for (int i = tid; i < n; i += BS_THREADS) {
-    const int64_t s = score[i];
-    const int c = place[i], w = row_of(c);
-    const uint64_t key = key_of(c, w);
-    const int rank = rank_of(s, c, n, [&](int j) { return place[j]; });
-    if (rank < K && in) {
-      p.parents[out + rank] = w;
-      p.tokens[out + rank] = kind[w] == 2 ? p.pad : key_token(key);
-      p.out[out + rank] = (float)from_ordered(s);
+  int n = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    const int64_t bar = bar_sh;
+    const int at_bar = bar_at, of_each = pass ? K : lead;
+    const uint64_t bar_key = at_bar == INT_MAX ? 0 : key_sh[at_bar];
+    const int bar_row = at_bar == INT_MAX ? 0 : place[at_bar];
+    __syncthreads();   // (the bar is read before the lists are written again)
+#pragma unroll 1
+    for (int i = tid; i < lists * of_each; i += BS_THREADS) {
+      const int l = i / of_each, w = row_of[l];
+      const uint64_t key = key_of(l, i - l * of_each, w);
+      if (!key) continue;
+      const double s = ((double)key_logit(key) - top[w]) + offset[w];
+      if (!(s > -INFINITY)) continue;
+      const int64_t o = ordered(s);
+      // equal scores: the lower beam; within a beam the logits decide, whatever the score's size leaves of them
+      if (o > bar || at_bar == INT_MAX || (o == bar && (w < bar_row || (w == bar_row && key >= bar_key)))) {
+        const int at = atomicAdd(&n_sh[pass], 1);
+        if (at < BM_MOST) { score[at] = o; key_sh[at] = key; place[at] = w; }
+      }
     }
+    __syncthreads();
+    n = min(n_sh[pass], BM_MOST);
+#pragma unroll 1
+    for (int i = tid; i < n; i += BS_THREADS) {
+      const int64_t s = score[i];
+      const uint64_t key = key_sh[i];
+      const int w = place[i];
+      int rank = 0, same = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const int64_t o = score[j];
+        rank += o > s;
+        same += o == s;
+      }
+      if (same > 1)
+        for (int j = 0; j < n; ++j)
+          if (score[j] == s) rank += place[j] < w || (place[j] == w && key_sh[j] > key);
+      if (pass == 0) {
+        if (rank == K - 1) { bar_sh = s; bar_at = i; }
+      } else if (rank < K && in) {
+        p.parents[out + rank] = w;
+        p.tokens[out + rank] = key_token(key);
+        p.out[out + rank] = (float)from_ordered(s);
+      }
+    }
+    __syncthreads();
   }
   for (int i = n + tid; i < K; i += BS_THREADS)
     if (in) { p.parents[out + i] = -1; p.tokens[out + i] = -1; p.out[out + i] = -INFINITY; }
@@ -880,6 +855,7 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
 
 bool beam_select_supported(int64_t B, int64_t W) { return W <= kBeamMaxW && B < ((int64_t)1 << 22) && B * W < ((int64_t)1 << 22); }
 constexpr int kMaxSms = 256;   // sizes the workspace, so that it does not depend on the device
+static_assert(BM_LISTS >= (int)kBeamMaxW + BS_CTAS_PER_SM * kMaxSms, "a request's lists");
 struct SelectWs { size_t pieces, stat, total; int64_t lists; };
 SelectWs select_ws(int64_t rows, int64_t V) {
   const int64_t nb = (V + BS_BATCH - 1) / BS_BATCH;
@@ -906,7 +882,7 @@ int launch_beam_select(const BeamSelectDesc& d, int num_sms, unsigned* status, c
   p.n_lists = ws.lists;
   p.status = status;
   const bool vec = ((reinterpret_cast<uintptr_t>(d.logits) | (uintptr_t)(d.ld * 4)) & 15) == 0;
-  const int smem = bs_smem(p.K, vec);
+  const int smem = bs_smem(p.K, vec), fit = std::min(BS_CTAS_PER_SM, 233472 / (smem + 2048));   // (2 KB: static and the system's)
   int dev = 0;
   cudaGetDevice(&dev);
   static bool attr_set[64] = {};
@@ -918,7 +894,7 @@ int launch_beam_select(const BeamSelectDesc& d, int num_sms, unsigned* status, c
       return -1;
     attr_set[dev] = true;
   }
-  const unsigned grid = (unsigned)select_grid(d.B * d.W, p.nb, BS_CTAS_PER_SM * std::min(num_sms, kMaxSms));
+  const unsigned grid = (unsigned)select_grid(d.B * d.W, p.nb, fit * std::min(num_sms, kMaxSms));
   const dim3 threads(BS_THREADS + 32);
   if ((vec ? launch_after(beam_part_kernel<true>, dim3(grid), threads, smem, st, p)
            : launch_after(beam_part_kernel<false>, dim3(grid), threads, smem, st, p)) != cudaSuccess)
