@@ -7,6 +7,7 @@ call raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -495,21 +496,19 @@ def llama_beam_select(logits, scores, finished, pad_token, parents, tokens, out_
         _arg(w, "out_scores", out_scores, f32, dev, kept), *_scratch(w, ws, dev), st), w)
 
 
-def _pools(where, name, pools, dev, n_pages, scales):
-    """PagePool records of [n_layers, n_pages, 128, ...] tensors, or of scales [n_layers, n_pages, parts, 128]; the
-    layers' axis may be missing."""
-    out = []
+def _pools(where, name, pools, dev, n_pages, scales, flat):
+    """Appends the PagePool records of [n_layers, n_pages, 128, heads, width] tensors, or of scales [n_layers, n_pages,
+    parts, 128], to flat (four integers each); the layers' axis may be missing."""
     for t in pools:
         at, s, size = _arg(where, name, t, t.dtype, dev), t.shape, t.element_size()
         k = len(s) - (3 if scales else 4)                # axes before the pages' own
         if scales and 0 <= k <= 1 and s[k] == n_pages and s[-1] == 128:
-            out.append(PagePool(at, s[0] if k else 1, s[-2], size))
+            flat += (at, s[0] if k else 1, s[-2], size)
         elif not scales and 0 <= k <= 1 and s[k] == n_pages and s[k + 1] == 128:
-            out.append(PagePool(at, s[0] if k else 1, 1, s[-2] * s[-1] * size))
+            flat += (at, s[0] if k else 1, 1, s[-2] * s[-1] * size)
         else:
             raise ValueError(f"{where}: {name} must be [n_layers, {n_pages}, " +
                              (f"parts, 128], got {tuple(s)}" if scales else f"128, heads, width], got {tuple(s)}"))
-    return out
 
 
 def llama_beam_reorder_paged(parents, n_cached, n_cached_out, block_table, block_table_out, free_pages, n_pages, kv_pools,
@@ -522,13 +521,16 @@ def llama_beam_reorder_paged(parents, n_cached, n_cached_out, block_table, block
     i32 = torch.int32
     B, W = parents.shape
     P = block_table.shape[-1]
-    records = _pools(w, "kv_pools", kv_pools, dev, n_pages, False) + _pools(w, "scale_pools", scale_pools, dev, n_pages, True)
-    arr = (PagePool * max(1, len(records)))(*records)
+    flat = []
+    _pools(w, "kv_pools", kv_pools, dev, n_pages, False, flat)
+    _pools(w, "scale_pools", scale_pools, dev, n_pages, True, flat)
+    n = len(flat) // 4
+    records = (PagePool * n).from_buffer(array.array("q", flat)) if n else None   # one object, not one per record
     _check(L.llama_beam_reorder_paged(
         _arg(w, "parents", parents, i32, dev), B, W, _arg(w, "n_cached", n_cached, i32, dev, (B * W,)),
         _arg(w, "n_cached_out", n_cached_out, i32, dev, (B * W,)), _arg(w, "block_table", block_table, i32, dev, (B * W, P)),
         _arg(w, "block_table_out", block_table_out, i32, dev, (B * W, P)), P, _arg(w, "free_pages", free_pages, i32, dev),
-        free_pages.numel(), n_pages, arr, len(records), _arg(w, "freed_pages", freed_pages, i32, dev), freed_pages.numel(),
+        free_pages.numel(), n_pages, records, n, _arg(w, "freed_pages", freed_pages, i32, dev), freed_pages.numel(),
         _arg(w, "counts", counts, i32, dev, (2,)), *_scratch(w, ws, dev), st), w)
 
 
