@@ -33,8 +33,10 @@
 namespace llama {
 namespace {
 
-constexpr int DP_THREADS = 224;   // warp 0 TMA, 1 MMA, 2-5 softmax, 6 q -> E4M3 hi / lo
-// two CTAs per SM (2 x 108.8 KB of shared memory), so that one's hand-offs overlap the other's
+// Threads: warp 0 TMA, 1 MMA, then SG groups of four softmax warps, the last warp q -> E4M3 hi / lo.  With 8 rows and more the
+// softmax sets the pace, so two groups share the rows of a tile (a thread has one key of four or eight rows).
+constexpr int dp_threads(int SG) { return 96 + 128 * SG; }
+// two CTAs per SM (2 x 110 KB of shared memory), so that one's hand-offs overlap the other's
 constexpr int DP_KSTAGES = 3;
 constexpr int DP_VSTAGES = 2;
 constexpr int DP_SSTAGES = 4;     // scales
@@ -74,8 +76,8 @@ struct DpSmem {
   static constexpr uint32_t OFF_Q = OFF_V8 + DP_VSTAGES * F8;  // 2 buffers
   static constexpr uint32_t OFF_P = OFF_Q + 2 * OPB;           // 2 buffers
   static constexpr uint32_t OFF_SC = OFF_P + 2 * OPB;
-  static constexpr uint32_t OFF_RED = OFF_SC + DP_SSTAGES * SC;  // [3][4][16] floats
-  static constexpr uint32_t OFF_QS = OFF_RED + 3 * 4 * 16 * 4;   // inverse q scales [2][16]
+  static constexpr uint32_t OFF_RED = OFF_SC + DP_SSTAGES * SC;      // [2 groups][3][4][16] floats
+  static constexpr uint32_t OFF_QS = OFF_RED + 2 * 3 * 4 * 16 * 4;   // inverse q scales [2][16]
   static constexpr uint32_t OFF_BAR = OFF_QS + 2 * 16 * 4;
   static constexpr uint32_t TOTAL = OFF_BAR + 512 + 1024;
 };
@@ -93,12 +95,35 @@ __device__ __forceinline__ void tmem_ld16_dp(uint32_t taddr, uint32_t (&v)[16]) 
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr));
 }
+// N columns of 32-bit TMEM cells, 32 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 4) tmem_ld4(taddr, v);
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+  else tmem_ld16_dp(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&v)[N]) {
+  static_assert(N == 4 || N == 8 || N == 16, "columns");
+  if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+  else if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else tmem_st16(taddr, v);
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void softmax_sync_dp() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync_dp(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 __device__ __forceinline__ float warp_max_dp(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -161,10 +186,12 @@ __device__ __forceinline__ bool next_piece(const DecodeAttn8pParams& p, Pieces& 
 }
 
 // R query rows per CTA: R / PACK query heads of each of its PACK KV heads.
+constexpr int dp_groups(int R) { return R >= 8 ? 2 : 1; }
 template <int R, int PACK>
-__global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kernel(const __grid_constant__ DecodeAttn8pParams p) {
+__global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) decode_attn8p_kernel(const __grid_constant__ DecodeAttn8pParams p) {
   using L = DpSmem;
   constexpr int HD = 128 / PACK, RH = R / PACK;
+  constexpr int SG = dp_groups(R), RT = R / SG, DP_THREADS = dp_threads(SG);   // softmax groups, rows of each
   constexpr int NP = R <= 8 ? 16 : 32;   // operand rows: hi 0..R-1, lo R..2R-1, zero padding
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -172,7 +199,7 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + P_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* start = reinterpret_cast<int*>(tmem_slot + 2);                  // first sequence and tile of the range
-  int64_t* wsum = reinterpret_cast<int64_t*>(bars + P_COUNT + 2);      // [7]
+  int64_t* wsum = reinterpret_cast<int64_t*>(bars + P_COUNT + 2);      // [warps]
   float* red = reinterpret_cast<float*>(smem + L::OFF_RED);
   float* qinv = reinterpret_cast<float*>(smem + L::OFF_QS);
 
@@ -190,7 +217,7 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
       if (i == P_QR || i == P_QR + 1) cnt = 32;
       if (i == P_SFREE || i == P_SFREE + 1 || i == P_PF || i == P_PF + 1 || i == P_OFREE || i == P_QC || i == P_QC + 1 ||
           (i >= P_SCE && i < P_SCE + DP_SSTAGES))
-        cnt = 128;
+        cnt = 128 * SG;
       mbar_init(&bars[i], cnt);
     }
     *abort_flag = 0;
@@ -326,60 +353,63 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
     if (lane == 0) {  // ---------------------------------------------------- MMA issuer
       const uint32_t idesc_s = idesc_f8(128, NP);
       const uint32_t idesc_o = idesc_f8(128, NP, /*a_mn_major=*/true);
-      int tile = 0, it = 0;
-      bool ok = true;
       Pieces s = it0;
-      for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
-        const int qb = it & 1;
-        if (!mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
+      // S^T of tile gt, the first of piece it or a later one
+      auto issue_s = [&](int gt, int it, bool first) -> bool {
+        const int st = gt % DP_KSTAGES, sb = gt & 1, qb = it & 1;
+        if (first && !mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) return false;
+        if (!mbar_wait(&bars[P_KF + st], (gt / DP_KSTAGES) & 1, abort_flag, p.status)) return false;
+        if (!mbar_wait(&bars[P_SFREE + sb], ((gt >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
         tc_fence_after();
         const uint64_t qd0 = sdesc_sw128(sbase + L::OFF_Q + qb * L::OPB, 16, 1024);
+        const uint64_t kd0 = sdesc_sw128(sbase + L::OFF_K8 + st * L::F8, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)   // 32 bytes of the row per step
+          tc_mma_e4m3(tS + sb * NP, kd0 + (uint64_t)(2 * k), qd0 + (uint64_t)(2 * k), idesc_s, k > 0 ? 1u : 0u);
+        tc_commit(&bars[P_SF + sb]);
+        tc_commit(&bars[P_KE + st]);
+        return true;
+      };
+      auto issue_pv = [&](int gt, int it, bool first) -> bool {
+        const int st = gt % DP_VSTAGES, pb = gt & 1;
+        if (!mbar_wait(&bars[P_PF + pb], (gt >> 1) & 1, abort_flag, p.status)) return false;
+        if (!mbar_wait(&bars[P_VF + st], (gt / DP_VSTAGES) & 1, abort_flag, p.status)) return false;
+        if (first && !mbar_wait(&bars[P_OFREE], (it & 1) ^ 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        // V^T: M = bytes of the row (MN-major), 8-key groups 1024 bytes apart
+        const uint64_t vd0 = sdesc_sw128(sbase + L::OFF_V8 + st * L::F8, 16384, 1024);
+        const uint64_t pd0 = sdesc_sw128(sbase + L::OFF_P + pb * L::OPB, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)   // 32 keys per step
+          tc_mma_e4m3(tO, vd0 + (uint64_t)(k * 4096 >> 4), pd0 + (uint64_t)(2 * k), idesc_o, (!first || k > 0) ? 1u : 0u);
+        tc_commit(&bars[P_OD + pb]);
+        tc_commit(&bars[P_VE + st]);
+        return true;
+      };
+      // the next tile's S^T goes out before this one's P V, the next piece's first tile included
+      int tile = 0, it = 0;
+      bool ok = next_piece(p, s, b, t0, t1, nt, n_keys) && issue_s(0, 0, true);
+      while (ok) {
         const int n = t1 - t0;
-        auto issue_s = [&](int j) -> bool {
-          const int gt = tile + j;
-          const int st = gt % DP_KSTAGES, sb = gt & 1;
-          if (!mbar_wait(&bars[P_KF + st], (gt / DP_KSTAGES) & 1, abort_flag, p.status)) return false;
-          if (!mbar_wait(&bars[P_SFREE + sb], ((gt >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint64_t kd0 = sdesc_sw128(sbase + L::OFF_K8 + st * L::F8, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)   // 32 bytes of the row per step
-            tc_mma_e4m3(tS + sb * NP, kd0 + (uint64_t)(2 * k), qd0 + (uint64_t)(2 * k), idesc_s, k > 0 ? 1u : 0u);
-          tc_commit(&bars[P_SF + sb]);
-          tc_commit(&bars[P_KE + st]);
-          return true;
-        };
-        auto issue_pv = [&](int j) -> bool {
-          const int gt = tile + j;
-          const int st = gt % DP_VSTAGES, pb = gt & 1;
-          if (!mbar_wait(&bars[P_PF + pb], (gt >> 1) & 1, abort_flag, p.status)) return false;
-          if (!mbar_wait(&bars[P_VF + st], (gt / DP_VSTAGES) & 1, abort_flag, p.status)) return false;
-          if (j == 0 && !mbar_wait(&bars[P_OFREE], (it & 1) ^ 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-          // V^T: M = bytes of the row (MN-major), 8-key groups 1024 bytes apart
-          const uint64_t vd0 = sdesc_sw128(sbase + L::OFF_V8 + st * L::F8, 16384, 1024);
-          const uint64_t pd0 = sdesc_sw128(sbase + L::OFF_P + pb * L::OPB, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)   // 32 keys per step
-            tc_mma_e4m3(tO, vd0 + (uint64_t)(k * 4096 >> 4), pd0 + (uint64_t)(2 * k), idesc_o, (j > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&bars[P_OD + pb]);
-          tc_commit(&bars[P_VE + st]);
-          return true;
-        };
-        for (int j = 0; j < n; ++j) {
-          if (!issue_s(j)) { ok = false; break; }
-          if (j > 0 && !issue_pv(j - 1)) { ok = false; break; }
+        bool more = false;
+        for (int j = 0; ok && j < n; ++j, ++tile) {
+          if (j + 1 < n) {
+            ok = issue_s(tile + 1, it, false);
+          } else {
+            tc_commit(&bars[P_QE + (it & 1)]);
+            more = next_piece(p, s, b, t0, t1, nt, n_keys);
+            if (more) ok = issue_s(tile + 1, it + 1, true);
+          }
+          ok = ok && issue_pv(tile, it, j == 0);
         }
-        if (!ok) break;
-        tc_commit(&bars[P_QE + qb]);
-        if (!issue_pv(n - 1)) break;
-        tile += n;
+        ++it;
+        ok = ok && more;
       }
       int no_abort = 0;
       tc_commit(&bars[P_DRAIN]);
       mbar_wait(&bars[P_DRAIN], 0, &no_abort, p.status);
     }
-  } else if (warp == 6) {  // ------------------------------------------- q -> E4M3 hi / lo operand
+  } else if (warp == 2 + 4 * SG) {  // ------------------------------------ q -> E4M3 hi / lo operand
     constexpr int VH = HD / 8;                  // 8-element chunks of a row
     constexpr int NCH = R * VH;
     constexpr int PER = (NCH + 31) / 32;
@@ -427,34 +457,44 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
       __syncwarp();
       mbar_arrive(&bars[P_QR + qb]);
     }
-  } else {  // ------------------------------------------------------------ softmax warps 2..5
-    const int qw = warp & 3;   // a warp reaches TMEM lanes 32 * (warp % 4) ..
+  } else {  // ------------------------------------------------------------ softmax warps
+    const int sg = (warp - 2) >> 2, qw = warp & 3;   // a warp reaches TMEM lanes 32 * (warp % 4) ..
     const int t = qw * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
+    const int h0 = sg * RT;                          // this group's first row
+    // scales: of packed heads one for each half of the rows, which a group of two has to itself
+    constexpr int NSC = PACK / SG > 1 ? 2 : 1;
+    const int sc0 = PACK == 2 && SG == 2 ? sg : 0;
+    // columns of this group's rows: hi and lo side by side (one group), or two blocks of RT
+    constexpr int LD = SG == 1 ? 16 : RT;
+    auto hi_lo = [&](uint32_t base, uint32_t (&hi)[LD], uint32_t (&lo)[LD]) {   // (one group: all 16 columns in hi)
+      tmem_ld_cols<LD>(base + h0 + lane_off, hi);
+      if constexpr (SG == 2) tmem_ld_cols<LD>(base + R + h0 + lane_off, lo);
+      tc_wait_ld();
+    };
+    float* red_g = red + sg * 192;
     int tile = 0, it = 0;
     bool ok = true;
     Pieces s = it0;
     for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
       const int qb = it & 1;
       if (!mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
-      float sc[R], m_ref[R], lsum[R];
+      float m_ref[RT], lsum[RT];
 #pragma unroll
-      for (int h = 0; h < R; ++h) {
-        sc[h] = p.scale_log2 * qinv[qb * 16 + h];
-        m_ref[h] = -INFINITY;
-        lsum[h] = 0.f;
+      for (int i = 0; i < RT; ++i) {
+        m_ref[i] = -INFINITY;
+        lsum[i] = 0.f;
       }
-      mbar_arrive(&bars[P_QC + qb]);
       for (int tt = t0; tt < t1; ++tt, ++tile) {
         const int sb = tile & 1, ss = tile % DP_SSTAGES;
         const bool valid = tt * 128 + t < n_keys;
         if (!mbar_wait(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
-        float ks[PACK], lvs[PACK], ivs[PACK];
+        float ks[NSC], lvs[NSC], ivs[NSC];
         {
-          const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC);
+          const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC) + sc0 * 128;
 #pragma unroll
-          for (int k = 0; k < PACK; ++k) {
-            ks[k] = scales[k * 128 + t];
+          for (int k = 0; k < NSC; ++k) {
+            ks[k] = scales[k * 128 + t] * p.scale_log2;
             const float v = fmaxf(scales[256 + k * 128 + t], 7.88860905e-31f);   // 2^-100: a zero scale has a logarithm too
             lvs[k] = __log2f(v);
             ivs[k] = valid ? 1.f / v : 0.f;
@@ -463,73 +503,77 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
         mbar_arrive(&bars[P_SCE + ss]);
         if (!mbar_wait(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
-        uint32_t sv[NP];
-#pragma unroll
-        for (int c = 0; c < NP / 16; ++c) tmem_ld16_dp(tS + sb * NP + c * 16 + lane_off, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
-        tc_wait_ld();
+        uint32_t hi[LD], lo[LD];
+        hi_lo(tS + sb * NP, hi, lo);
         tc_fence_before();
         mbar_arrive(&bars[P_SFREE + sb]);
-        float e[R];   // log2 of weight * value scale
+        float e[RT];   // log2 of weight * value scale
 #pragma unroll
-        for (int h = 0; h < R; ++h)
-          e[h] = valid ? fmaf(fmaf(__uint_as_float(sv[R + h]), 1.f / kDpLo, __uint_as_float(sv[h])), sc[h] * ks[h / RH], lvs[h / RH])
-                       : -INFINITY;
-        float* rbuf = red + (tile & 1) * 64;
-#pragma unroll
-        for (int h = 0; h < R; ++h) {
-          const float v = warp_max_dp(e[h]);
-          if (lane == h) rbuf[qw * 16 + h] = v;
+        for (int i = 0; i < RT; ++i) {
+          const int k = NSC == 2 ? i / RH : 0;
+          const float fine = __uint_as_float(SG == 1 ? hi[(R + i) % LD] : lo[i % LD]);
+          e[i] = valid ? fmaf(fmaf(fine, 1.f / kDpLo, __uint_as_float(hi[i])), qinv[qb * 16 + h0 + i] * ks[k], lvs[k]) : -INFINITY;
         }
-        softmax_sync_dp();
-        float alpha[R];
+        float* rbuf = red_g + (tile & 1) * 64;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float v = warp_max_dp(e[i]);
+          if (lane == i) rbuf[qw * 16 + i] = v;
+        }
+        softmax_sync_dp(sg);
+        auto tile_max = [&](int i) { return fmaxf(fmaxf(rbuf[i], rbuf[16 + i]), fmaxf(rbuf[32 + i], rbuf[48 + i])); };
         bool resc = false;
 #pragma unroll
-        for (int h = 0; h < R; ++h) {
-          const float tm = fmaxf(fmaxf(rbuf[h], rbuf[16 + h]), fmaxf(rbuf[32 + h], rbuf[48 + h]));
-          alpha[h] = 1.f;
-          if (m_ref[h] == -INFINITY) {
-            m_ref[h] = tm;
-          } else if (tm > m_ref[h] + kDpRescaleLog2) {
-            alpha[h] = exp2f(m_ref[h] - tm);
-            m_ref[h] = tm;
-            resc = true;
-          }
+        for (int i = 0; i < RT; ++i) {
+          const float tm = tile_max(i);
+          if (m_ref[i] == -INFINITY) m_ref[i] = tm;
+          else resc = resc || tm > m_ref[i] + kDpRescaleLog2;
         }
         const int pb = tile & 1;
         if (tile >= 2) {
           if (!mbar_wait(&bars[P_OD + pb], ((tile - 2) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         }
-        if (resc) {   // the same in all 128 threads, which saw the same maxima
+        if (resc) {   // the same in all 128 threads of the group, which saw the same maxima
           if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after();
+          uint32_t oh[LD], ol[LD];
+          hi_lo(tO, oh, ol);
 #pragma unroll
-          for (int c = 0; c < NP / 16; ++c) {
-            uint32_t ov[16];
-            tmem_ld16_dp(tO + c * 16 + lane_off, ov);
-            tc_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int col = c * 16 + k;
-              if (col < 2 * R) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha[col % R]);
-            }
-            tmem_st16(tO + c * 16 + lane_off, ov);
+          for (int i = 0; i < RT; ++i) {
+            const float tm = tile_max(i);
+            if (!(tm > m_ref[i] + kDpRescaleLog2)) continue;
+            const float alpha = exp2f(m_ref[i] - tm);
+            m_ref[i] = tm;
+            lsum[i] *= alpha;
+            oh[i] = __float_as_uint(__uint_as_float(oh[i]) * alpha);
+            uint32_t& fine = SG == 1 ? oh[(R + i) % LD] : ol[i % LD];
+            fine = __float_as_uint(__uint_as_float(fine) * alpha);
           }
+          tmem_st_cols<LD>(tO + h0 + lane_off, oh);
+          if constexpr (SG == 2) tmem_st_cols<LD>(tO + R + h0 + lane_off, ol);
           tc_wait_st();
-#pragma unroll
-          for (int h = 0; h < R; ++h) lsum[h] *= alpha[h];
         }
-        // P^T rows: h (hi) and R + h (lo), this thread's key in byte t of each row
+        // P^T rows: h (hi) and R + h (lo), this thread's key in byte t of each row; two rows are converted at a time
         uint8_t* pbase = smem + L::OFF_P + pb * L::OPB;
 #pragma unroll
-        for (int h = 0; h < R; ++h) {
-          const float w = exp2f(e[h] - (m_ref[h] - kDpPScaleLog2));
-          uint32_t lo;
-          const uint32_t hi = split_fine(w, 0.f, lo);
-          lsum[h] = fmaf(w, ivs[h / RH], lsum[h]);
-          pbase[sw128_at(h, t)] = (uint8_t)(hi & 0xFFu);
-          pbase[sw128_at(R + h, t)] = (uint8_t)(lo & 0xFFu);
+        for (int i = 0; i < RT; i += 2) {
+          float w[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (i + j < RT) {
+              w[j] = exp2f(e[i + j] - (m_ref[i + j] - kDpPScaleLog2));
+              lsum[i + j] = fmaf(w[j], ivs[NSC == 2 ? (i + j) / RH : 0], lsum[i + j]);
+            }
+          uint32_t lo2;
+          const uint32_t hi2 = split_fine(w[0], w[1], lo2);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (i + j < RT) {
+              pbase[sw128_at(h0 + i + j, t)] = (uint8_t)(hi2 >> (8 * j));
+              pbase[sw128_at(R + h0 + i + j, t)] = (uint8_t)(lo2 >> (8 * j));
+            }
         }
-        if ((tt + 1) * 128 > n_keys) {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
+        if (sg == 0 && (tt + 1) * 128 > n_keys) {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
           const int vs = tile % DP_VSTAGES;
           if (!mbar_wait(&bars[P_VF + vs], (tile / DP_VSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
           if (!valid) {
@@ -543,29 +587,30 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
         mbar_arrive(&bars[P_PF + pb]);
       }
       if (!ok) break;
+      mbar_arrive(&bars[P_QC + qb]);   // the q scales have been read
       if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
-      uint32_t ov[NP];
-#pragma unroll
-      for (int c = 0; c < NP / 16; ++c) tmem_ld16_dp(tO + c * 16 + lane_off, *reinterpret_cast<uint32_t(*)[16]>(ov + 16 * c));
-      tc_wait_ld();
+      uint32_t oh[LD], ol[LD];
+      hi_lo(tO, oh, ol);
       tc_fence_before();
       mbar_arrive(&bars[P_OFREE]);
-      float* lbuf = red + 128;
+      float* lbuf = red_g + 128;
 #pragma unroll
-      for (int h = 0; h < R; ++h) {
-        float v = lsum[h];
+      for (int i = 0; i < RT; ++i) {
+        float v = lsum[i];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == h) lbuf[qw * 16 + h] = v;
+        if (lane == i) lbuf[qw * 16 + i] = v;
       }
-      softmax_sync_dp();
+      softmax_sync_dp(sg);
       const bool whole = t0 == 0 && t1 == nt;
       const int64_t part = ((int64_t)(2 * range + (t0 == 0 ? 1 : 0)) * p.groups + group) * R;
 #pragma unroll
-      for (int h = 0; h < R; ++h) {
-        const float l = (lbuf[h] + lbuf[16 + h]) + (lbuf[32 + h] + lbuf[48 + h]);
-        const float ot = fmaf(__uint_as_float(ov[R + h]), 1.f / kDpLo, __uint_as_float(ov[h]));
+      for (int i = 0; i < RT; ++i) {
+        const int h = h0 + i;
+        const float l = (lbuf[i] + lbuf[16 + i]) + (lbuf[32 + i] + lbuf[48 + i]);
+        const float fine = __uint_as_float(SG == 1 ? oh[(R + i) % LD] : ol[i % LD]);
+        const float ot = fmaf(fine, 1.f / kDpLo, __uint_as_float(oh[i]));
         const bool own = h / RH == t / HD;      // lane t holds byte t of the row: another head's, for half the rows
         if (whole) {
           const int head = head_of(h);
@@ -573,7 +618,7 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
           if (own && head >= 0 && in_extent(at, 1, (int64_t)p.B * p.n_q * HD)) p.o[at] = f2bf(ot / l);
         } else if (in_extent(part + h, 1, (int64_t)2 * p.n_ranges * p.groups * R)) {
           if (own) p.part_o[(part + h) * HD + t % HD] = ot;
-          if (t == 0) p.part_ml[part + h] = make_float2(m_ref[h], l);
+          if (t == 0) p.part_ml[part + h] = make_float2(m_ref[i], l);
         }
       }
     }
@@ -587,59 +632,101 @@ __global__ void __launch_bounds__(DP_THREADS, DP_CTAS_PER_SM) decode_attn8p_kern
   }
 }
 
-// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (range, group,
-// row): the sequence whose first part is the range's tail.  The latency of its dependent loads is what it costs, so every warp
-// forms all weights, one part per lane, and takes every fourth part's row, four elements per lane, all loads in flight.
-constexpr int DJ_WARPS = 4;
-__global__ void __launch_bounds__(32 * DJ_WARPS) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
-  __shared__ float4 sum[DJ_WARPS][32];
-  const int range = blockIdx.x, group = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (x, group, row):
+// sequence x, whose place among the ranges it finds from the lengths while the first kernel still runs; where there are more
+// sequences than ranges, the sequence whose first part is range x's tail.  The latency of its dependent loads is what it costs, so each of NW
+// warps takes every NW-th part, its statistics one per lane, its row four elements per lane, eight rows' loads in flight.
+template <int NW, bool BY_SEQ>
+__global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
+  __shared__ float4 sum[NW][32];
+  __shared__ float mx[NW], ls[NW];
+  __shared__ int64_t all[NW], ahead[NW];
+  const int group = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int RH = R / pack, g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
+  int range = blockIdx.x;
+  SplitInfo s{-1, 0};
+  if (BY_SEQ) {   // (the lengths were complete before the first kernel, which triggered past its own wait)
+    const int b = blockIdx.x;
+    int64_t x = 0, y = 0;
+    for (int k = threadIdx.x; k < p.B; k += 32 * NW) {
+      const int nt = tiles_at(p, k);
+      x += nt;
+      if (k < b) y += nt;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if (lane == 0) { all[warp] = x; ahead[warp] = y; }
+    __syncthreads();
+    int64_t T = 0, off = 0;
+    for (int w = 0; w < NW; ++w) { T += all[w]; off += ahead[w]; }
+    const int nt = tiles_at(p, b), n_ranges = (int)min((int64_t)p.n_ranges, T);
+    if (nt > 0) {
+      range = range_with(T, n_ranges, off);
+      s.last = range_with(T, n_ranges, off + nt - 1);
+      if (s.last > range) s.b = b;
+    }
+  }
   pdl_wait();
   pdl_trigger();
-  const SplitInfo s = p.split[range];
+  if (!BY_SEQ) s = p.split[range];
   if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges || g >= p.n_kv || i >= p.r) return;
   const int n = s.last - range + 1;      // parts: the tail of `range`, then the first of each range up to `last`
   auto slot = [&](int k) { return ((int64_t)(k == 0 ? 2 * range + 1 : 2 * (range + k)) * p.groups + group) * R + h; };
-  float m = -INFINITY;
-  for (int k = lane; k < n; k += 32) m = fmaxf(m, p.part_ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool in = lane * 4 < p.hd;
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    float w = 0.f;
-    if (k0 + lane < n) {
-      const float2 ml = p.part_ml[slot(k0 + lane)];
-      w = exp2f(ml.x - m);
-      l += w * ml.y;
-    }
-    float4 v[32 / DJ_WARPS];
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < n; k0 += 32 * NW) {   // (once: there are at most 2 x 152 ranges)
+    // parts k0 + warp, k0 + warp + NW, ..: a lane has one's statistics
+    const int mine = k0 + warp + lane * NW, cnt = min(32, (n - k0 - warp + NW - 1) / NW);
+    const float2 ml = mine < n ? p.part_ml[slot(mine)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
 #pragma unroll
-    for (int j = 0; j < 32 / DJ_WARPS; ++j) {
-      const int k = k0 + j * DJ_WARPS + warp;
-      v[j] = in && k < n ? reinterpret_cast<const float4*>(p.part_o + slot(k) * p.hd)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m2 = fmaxf(m, top);
+    if (m2 > m && m > -INFINITY) {
+      const float a = exp2f(m - m2);
+      l *= a;
+      acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
     }
+    m = m2;
+    const float w = mine < n ? exp2f(ml.x - m) : 0.f;
+    l += w * ml.y;
+    for (int j0 = 0; j0 < cnt; j0 += 8) {
+      float4 v[8];
 #pragma unroll
-    for (int j = 0; j < 32 / DJ_WARPS; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j * DJ_WARPS + warp);
-      acc.x = fmaf(wj, v[j].x, acc.x);
-      acc.y = fmaf(wj, v[j].y, acc.y);
-      acc.z = fmaf(wj, v[j].z, acc.z);
-      acc.w = fmaf(wj, v[j].w, acc.w);
+      for (int j = 0; j < 8; ++j)
+        v[j] = in && j0 + j < cnt ? reinterpret_cast<const float4*>(p.part_o + slot(k0 + warp + (j0 + j) * NW) * p.hd)[lane]
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+        acc.x = fmaf(wj, v[j].x, acc.x);
+        acc.y = fmaf(wj, v[j].y, acc.y);
+        acc.z = fmaf(wj, v[j].z, acc.z);
+        acc.w = fmaf(wj, v[j].w, acc.w);
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   sum[warp][lane] = acc;
+  if (lane == 0) { mx[warp] = m; ls[warp] = l; }
   __syncthreads();
   const int64_t at = ((int64_t)s.b * p.n_q + (int64_t)g * p.r + i) * p.hd + lane * 4;
   if (warp == 0 && in && in_extent(at, 4, (int64_t)p.B * p.n_q * p.hd)) {
-#pragma unroll
-    for (int w = 1; w < DJ_WARPS; ++w) {
+    float M = mx[0];
+    for (int w = 1; w < NW; ++w) M = fmaxf(M, mx[w]);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+    for (int w = 0; w < NW; ++w) {
+      if (w >= n) break;       // warps without parts
+      const float a = exp2f(mx[w] - M);
       const float4 v = sum[w][lane];
-      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+      l = fmaf(a, ls[w], l);
+      acc.x = fmaf(a, v.x, acc.x); acc.y = fmaf(a, v.y, acc.y); acc.z = fmaf(a, v.z, acc.z); acc.w = fmaf(a, v.w, acc.w);
     }
     *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l, acc.y / l), pack_bf2(acc.z / l, acc.w / l));
   }
@@ -682,7 +769,7 @@ int launch_attn(const DecodeAttn8pParams& p, int dev, cudaStream_t st) {
       return -1;
     attr_set[dev] = true;
   }
-  return launch_after(decode_attn8p_kernel<R, PACK>, dim3((unsigned)(p.n_ranges * p.groups)), dim3(DP_THREADS), DpSmem::TOTAL, st, p) ==
+  return launch_after(decode_attn8p_kernel<R, PACK>, dim3((unsigned)(p.n_ranges * p.groups)), dim3(dp_threads(dp_groups(R))), DpSmem::TOTAL, st, p) ==
                  cudaSuccess
              ? 0
              : -1;
@@ -744,8 +831,12 @@ int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st
     }
   }
   if (rc != 0 || ranges == 1) return rc;   // one range cuts nothing
-  return launch_after(decode_join8p_kernel, dim3((unsigned)(ranges - 1), (unsigned)s.groups, (unsigned)s.R), dim3(32 * DJ_WARPS), 0, st, p,
-                      s.R, s.pack) == cudaSuccess ? 0 : -1;
+  const bool by_seq = d.B < ranges, many = by_seq && ranges / d.B > 16;   // many parts of a sequence
+  const dim3 grid((unsigned)(by_seq ? d.B : ranges - 1), (unsigned)s.groups, (unsigned)s.R);
+  const cudaError_t e = many     ? launch_after(decode_join8p_kernel<16, true>, grid, dim3(512), 0, st, p, s.R, s.pack)
+                        : by_seq ? launch_after(decode_join8p_kernel<4, true>, grid, dim3(128), 0, st, p, s.R, s.pack)
+                                 : launch_after(decode_join8p_kernel<4, false>, grid, dim3(128), 0, st, p, s.R, s.pack);
+  return e == cudaSuccess ? 0 : -1;
 }
 
 LLAMA_DEFINE_BOUNDS_READER(decode_attn8p)
