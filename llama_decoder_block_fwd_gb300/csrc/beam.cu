@@ -30,11 +30,11 @@ constexpr int BS_PER = 20;                              // logits of a thread in
 constexpr int BS_BATCH = BS_THREADS * BS_PER;
 constexpr int BS_STAGES = 3;
 constexpr int BS_MAX_K = (int)kBeamMaxOut;
-constexpr int BS_SLACK = 16;                            // entries beyond n_out that the list may keep
+__host__ __device__ constexpr int bs_slack(int K) { return K > 16 ? K : 16; }   // entries beyond n_out that the list may keep
 constexpr int BS_CTAS_PER_SM = 3;
-constexpr int BS_MAX_PIECES = 32;                       // of a row, on average: what the join has to look through
+constexpr int BS_MAX_PIECES = 12;                       // of a row, on average: what the join has to look through
 constexpr int BS_SCAN = 1 << 14;                        // rows up to which every CTA counts those that have to be read
-__host__ __device__ constexpr int bs_list(int K) { return K + BS_SLACK + 2 * K * BS_PER; }
+__host__ __device__ constexpr int bs_list(int K) { return K + bs_slack(K) + 2 * K * BS_PER; }
 __host__ __device__ constexpr int bs_smem(int K, bool vec) { return (vec ? BS_STAGES * BS_BATCH * 4 : 0) + 2 * bs_list(K) * 8; }
 
 struct RowPieces { int slot, n; };   // a row's lists are slot, slot + 1, ..
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     };
     // back to the K best, in order
     auto cut = [&]() {
-      if (n > K + BS_SLACK || (n > K && !floor)) {
+      if (n > K + bs_slack(K) || (n > K && !floor)) {
         for (int i = tid; i < n; i += BS_THREADS) {
           const uint64_t key = list[i];
           int rank = 0;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
 constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: the bar leaves n_out of n_out lists, or of fewer all
 constexpr int BM_LISTS = (int)kBeamMaxW + BS_CTAS_PER_SM * 256;   // of a request, at most (256: kMaxSms)
 constexpr int BM_LEAD = 64;
-constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS;
+constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS * (int)(sizeof(int64_t) + 1);
 
 // Doubles as integers that order as they do.
 __device__ __forceinline__ int64_t ordered(double s) {
@@ -446,9 +446,10 @@ __device__ __forceinline__ double log_sum(float s) {
 }
 
 __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ int64_t score[];                     // [BM_MOST], then their keys and places, then each list's row
+  extern __shared__ int64_t score[];                     // [BM_MOST], their keys, each list's best, their rows, each list's row
   uint64_t* key_sh = reinterpret_cast<uint64_t*>(score + BM_MOST);
-  int* place = reinterpret_cast<int*>(key_sh + BM_MOST);
+  int64_t* head_of = reinterpret_cast<int64_t*>(key_sh + BM_MOST);   // the score of a list's best
+  int* place = reinterpret_cast<int*>(head_of + BM_LISTS);
   uint8_t* row_of = reinterpret_cast<uint8_t*>(place + BM_MOST);
   // a row's candidates score (logit - top) + offset, offset its beam's score less the log of its sum of exp(z - top)
   __shared__ double offset[kBeamMaxW], top[kBeamMaxW];
@@ -533,12 +534,13 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
     __syncthreads();   // (the bar is read before the lists are written again)
 #pragma unroll 1
     for (int i = tid; i < lists * of_each; i += BS_THREADS) {
-      const int l = i / of_each, w = row_of[l];
-      const uint64_t key = key_of(l, i - l * of_each, w);
-      if (!key) continue;
-      const double s = ((double)key_logit(key) - top[w]) + offset[w];
-      if (!(s > -INFINITY)) continue;
-      const int64_t o = ordered(s);
+      const int l = i / of_each, k = i - l * of_each, w = row_of[l];
+      if (pass && head_of[l] < bar) continue;   // a list whose best does not reach the bar
+      const uint64_t key = key_of(l, k, w);
+      const double s = key ? ((double)key_logit(key) - top[w]) + offset[w] : -INFINITY;
+      const int64_t o = s > -INFINITY ? ordered(s) : BM_NONE;
+      if (!pass && k == 0) head_of[l] = o;
+      if (o == BM_NONE) continue;
       // equal scores: the lower beam; within a beam the logits decide, whatever the score's size leaves of them
       if (o > bar || at_bar == INT_MAX || (o == bar && (w < bar_row || (w == bar_row && key >= bar_key)))) {
         const int at = atomicAdd(&n_sh[pass], 1);

@@ -632,17 +632,18 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
   }
 }
 
-// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (x, group, row):
-// sequence x, whose place among the ranges it finds from the lengths while the first kernel still runs; where there are more
-// sequences than ranges, the sequence whose first part is range x's tail.  The latency of its dependent loads is what it costs, so each of NW
-// warps takes every NW-th part, its statistics one per lane, its row four elements per lane, eight rows' loads in flight.
-template <int NW, bool BY_SEQ>
+// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (x, group, z):
+// RB rows of sequence x, whose place among the ranges it finds from the lengths while the first kernel still runs; where there
+// are more sequences than ranges, of the sequence whose first part is range x's tail.  The latency of its dependent loads is what
+// it costs: a lane has one part's statistics, and the parts' rows come four elements per lane, eight rows' loads in flight.  Up to
+// 16 parts, a warp takes a row; of more, the NW warps share each row's.
+template <int NW, int RB, bool BY_SEQ>
 __global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_constant__ DecodeAttn8pParams p, int R, int pack) {
   __shared__ float4 sum[NW][32];
   __shared__ float mx[NW], ls[NW];
   __shared__ int64_t all[NW], ahead[NW];
-  const int group = blockIdx.y, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int RH = R / pack, g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
+  const int group = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int RH = R / pack;
   int range = blockIdx.x;
   SplitInfo s{-1, 0};
   if (BY_SEQ) {   // (the lengths were complete before the first kernel, which triggered past its own wait)
@@ -672,63 +673,86 @@ __global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   if (!BY_SEQ) s = p.split[range];
-  if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges || g >= p.n_kv || i >= p.r) return;
+  if (s.b < 0 || s.b >= p.B || s.last >= p.n_ranges) return;
   const int n = s.last - range + 1;      // parts: the tail of `range`, then the first of each range up to `last`
-  auto slot = [&](int k) { return ((int64_t)(k == 0 ? 2 * range + 1 : 2 * (range + k)) * p.groups + group) * R + h; };
   const bool in = lane * 4 < p.hd;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < n; k0 += 32 * NW) {   // (once: there are at most 2 x 152 ranges)
-    // parts k0 + warp, k0 + warp + NW, ..: a lane has one's statistics
-    const int mine = k0 + warp + lane * NW, cnt = min(32, (n - k0 - warp + NW - 1) / NW);
-    const float2 ml = mine < n ? p.part_ml[slot(mine)] : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
+  // query head of row h, -1 for a padding row
+  auto head_of = [&](int h) {
+    const int g = group / p.subs * pack + h / RH, i = group % p.subs * RH + h % RH;
+    return h < R && g < p.n_kv && i < p.r ? g * p.r + i : -1;
+  };
+  // parts w0, w0 + step, .. of row h: their maximum, sum and weighted rows
+  auto gather = [&](int h, int w0, int step, float& m, float& l, float4& acc) {
+    auto slot = [&](int k) { return ((int64_t)(k == 0 ? 2 * range + 1 : 2 * (range + k)) * p.groups + group) * R + h; };
+    m = -INFINITY;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = w0; k0 < n; k0 += 32 * step) {
+      const int mine = k0 + lane * step, cnt = min(32, (n - k0 + step - 1) / step);
+      const float2 ml = mine < n ? p.part_ml[slot(mine)] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float m2 = fmaxf(m, top);
-    if (m2 > m && m > -INFINITY) {
-      const float a = exp2f(m - m2);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m2 = fmaxf(m, top), a = m > -INFINITY ? exp2f(m - m2) : 0.f;
       l *= a;
       acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
-    }
-    m = m2;
-    const float w = mine < n ? exp2f(ml.x - m) : 0.f;
-    l += w * ml.y;
-    for (int j0 = 0; j0 < cnt; j0 += 8) {
-      float4 v[8];
+      m = m2;
+      const float w = mine < n ? exp2f(ml.x - m) : 0.f;
+      l += w * ml.y;
+      for (int j0 = 0; j0 < cnt; j0 += 8) {
+        float4 v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = in && j0 + j < cnt ? reinterpret_cast<const float4*>(p.part_o + slot(k0 + warp + (j0 + j) * NW) * p.hd)[lane]
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 8; ++j)
+          v[j] = in && j0 + j < cnt ? reinterpret_cast<const float4*>(p.part_o + slot(k0 + (j0 + j) * step) * p.hd)[lane]
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-        acc.x = fmaf(wj, v[j].x, acc.x);
-        acc.y = fmaf(wj, v[j].y, acc.y);
-        acc.z = fmaf(wj, v[j].z, acc.z);
-        acc.w = fmaf(wj, v[j].w, acc.w);
+        for (int j = 0; j < 8; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+          acc.x = fmaf(wj, v[j].x, acc.x);
+          acc.y = fmaf(wj, v[j].y, acc.y);
+          acc.z = fmaf(wj, v[j].z, acc.z);
+          acc.w = fmaf(wj, v[j].w, acc.w);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  sum[warp][lane] = acc;
-  if (lane == 0) { mx[warp] = m; ls[warp] = l; }
-  __syncthreads();
-  const int64_t at = ((int64_t)s.b * p.n_q + (int64_t)g * p.r + i) * p.hd + lane * 4;
-  if (warp == 0 && in && in_extent(at, 4, (int64_t)p.B * p.n_q * p.hd)) {
-    float M = mx[0];
-    for (int w = 1; w < NW; ++w) M = fmaxf(M, mx[w]);
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    l = 0.f;
-    for (int w = 0; w < NW; ++w) {
-      if (w >= n) break;       // warps without parts
-      const float a = exp2f(mx[w] - M);
-      const float4 v = sum[w][lane];
-      l = fmaf(a, ls[w], l);
-      acc.x = fmaf(a, v.x, acc.x); acc.y = fmaf(a, v.y, acc.y); acc.z = fmaf(a, v.z, acc.z); acc.w = fmaf(a, v.w, acc.w);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  };
+  auto store = [&](int head, float l, const float4& acc) {
+    const int64_t at = ((int64_t)s.b * p.n_q + head) * p.hd + lane * 4;
+    if (in && in_extent(at, 4, (int64_t)p.B * p.n_q * p.hd))
+      *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l, acc.y / l), pack_bf2(acc.z / l, acc.w / l));
+  };
+  float m, l;
+  float4 acc;
+  if (RB > 1 && n <= 16) {
+    const int h = blockIdx.z * RB + warp;
+    if (warp >= RB || head_of(h) < 0) return;
+    gather(h, 0, 1, m, l, acc);
+    store(head_of(h), l, acc);
+    return;
+  }
+  for (int r = 0; r < RB; ++r) {
+    const int h = blockIdx.z * RB + r, head = head_of(h);
+    if (head < 0) continue;
+    gather(h, warp, NW, m, l, acc);
+    sum[warp][lane] = acc;
+    if (lane == 0) { mx[warp] = m; ls[warp] = l; }
+    __syncthreads();
+    if (warp == 0) {
+      float M = mx[0];
+      for (int w = 1; w < NW; ++w) M = fmaxf(M, mx[w]);
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      l = 0.f;
+      for (int w = 0; w < min(NW, n); ++w) {       // (warps past n have no parts)
+        const float a = exp2f(mx[w] - M);
+        const float4 v = sum[w][lane];
+        l = fmaf(a, ls[w], l);
+        acc.x = fmaf(a, v.x, acc.x); acc.y = fmaf(a, v.y, acc.y); acc.z = fmaf(a, v.z, acc.z); acc.w = fmaf(a, v.w, acc.w);
+      }
+      store(head, l, acc);
     }
-    *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l, acc.y / l), pack_bf2(acc.z / l, acc.w / l));
+    __syncthreads();
   }
 }
 
@@ -831,11 +855,15 @@ int launch_decode_attn8p(const DecodeAttn8pDesc& d, int num_sms, cudaStream_t st
     }
   }
   if (rc != 0 || ranges == 1) return rc;   // one range cuts nothing
-  const bool by_seq = d.B < ranges, many = by_seq && ranges / d.B > 16;   // many parts of a sequence
-  const dim3 grid((unsigned)(by_seq ? d.B : ranges - 1), (unsigned)s.groups, (unsigned)s.R);
-  const cudaError_t e = many     ? launch_after(decode_join8p_kernel<16, true>, grid, dim3(512), 0, st, p, s.R, s.pack)
-                        : by_seq ? launch_after(decode_join8p_kernel<4, true>, grid, dim3(128), 0, st, p, s.R, s.pack)
-                                 : launch_after(decode_join8p_kernel<4, false>, grid, dim3(128), 0, st, p, s.R, s.pack);
+  // By the parts that a sequence has if all are alike: a warp per row up to 4, a block per row above, a large one above 16.
+  const bool by_seq = d.B < ranges;
+  const int64_t each = ranges / d.B;
+  const int rows_each = by_seq && each > 4 ? 1 : 4;
+  const dim3 grid((unsigned)(by_seq ? d.B : ranges - 1), (unsigned)s.groups, (unsigned)((s.R + rows_each - 1) / rows_each));
+  const cudaError_t e = !by_seq     ? launch_after(decode_join8p_kernel<4, 4, false>, grid, dim3(128), 0, st, p, s.R, s.pack)
+                        : each <= 4 ? launch_after(decode_join8p_kernel<4, 4, true>, grid, dim3(128), 0, st, p, s.R, s.pack)
+                        : each <= 16 ? launch_after(decode_join8p_kernel<4, 1, true>, grid, dim3(128), 0, st, p, s.R, s.pack)
+                                     : launch_after(decode_join8p_kernel<16, 1, true>, grid, dim3(512), 0, st, p, s.R, s.pack);
   return e == cudaSuccess ? 0 : -1;
 }
 
