@@ -22,20 +22,19 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // equal ranges, one per CTA (rows that need not be read left out).  A producer warp streams a range's batches into a ring in
 // shared memory (bulk copies), 256 threads take them.  Each warp sums the exponentials of its 512 logits of a batch from
 // their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
-// n_out-th best of a row's piece so far goes to a list in shared memory, which is cut back to the n_out best when it has
-// grown.  The second kernel joins a request's lists and sums.
+// n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second kernel joins a request's lists and sums.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
 constexpr int BS_PER = 20;                              // logits of a thread in a batch
 constexpr int BS_BATCH = BS_THREADS * BS_PER;
 constexpr int BS_STAGES = 3;
 constexpr int BS_MAX_K = (int)kBeamMaxOut;
-__host__ __device__ constexpr int bs_slack(int K) { return K > 16 ? K : 16; }   // entries beyond n_out that the list may keep
+__host__ __device__ constexpr int bs_slack(int K) { return K > 16 ? K : 16; }   // candidates that may wait for the next cut
 constexpr int BS_CTAS_PER_SM = 3;
 constexpr int BS_MAX_PIECES = 12;                       // of a row, on average: what the join has to look through
 constexpr int BS_SCAN = 1 << 14;                        // rows up to which every CTA counts those that have to be read
-__host__ __device__ constexpr int bs_list(int K) { return K + bs_slack(K) + 2 * K * BS_PER; }
-__host__ __device__ constexpr int bs_smem(int K, bool vec) { return (vec ? BS_STAGES * BS_BATCH * 4 : 0) + 2 * bs_list(K) * 8; }
+__host__ __device__ constexpr int bs_room(int K) { return bs_slack(K) + (K > 16 ? K : 16) * BS_PER; }
+__host__ __device__ constexpr int bs_smem(int K, bool vec) { return (vec ? BS_STAGES * BS_BATCH * 4 : 0) + (bs_room(K) + 2 * K) * 8; }
 
 struct RowPieces { int slot, n; };   // a row's lists are slot, slot + 1, ..
 
@@ -148,9 +147,9 @@ template <bool VEC>
 __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_kernel(const __grid_constant__ SelectParams p) {
   extern __shared__ __align__(16) uint8_t bs_smem_raw[];
   float* ring = reinterpret_cast<float*>(bs_smem_raw);
-  const int K = p.K, room = bs_list(K);
-  uint64_t* list = reinterpret_cast<uint64_t*>(bs_smem_raw + (VEC ? BS_STAGES * BS_BATCH * 4 : 0));
-  uint64_t* other = list + room;
+  const int K = p.K, room = bs_room(K);
+  uint64_t* list = reinterpret_cast<uint64_t*>(bs_smem_raw + (VEC ? BS_STAGES * BS_BATCH * 4 : 0));   // candidates that wait
+  uint64_t *best = list + room, *other = best + K;                                                     // the best of before
   __shared__ uint64_t full[BS_STAGES], pushed[BS_STAGES];   // a batch has landed; every warp has read it and pushed its candidates
   __shared__ int n_sh, cnt[BS_STAGES], wsum[BS_WARPS + 1], start;
   __shared__ volatile int abort_sh;
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     };
     uint64_t floor = 0;        // the piece's K-th best so far: what does not beat it is no candidate
     float bar = -INFINITY;     // its logit; a later equal one has the higher token, so only larger ones count
-    int n = 0;                 // length of the list
+    int n = 0, have = 0;       // candidates that wait, best ones of before (none or K)
     float x[BS_PER], four[BS_PER / 4];   // a batch's logits, the largest of each four
     // batch b, the CTA's j-th: its logits into x, its sums to memory; *top gets this thread's largest
     auto take = [&](int b, float* top) -> bool {
@@ -280,51 +279,58 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       if (lane == 0 && in_extent(at, 1, (int64_t)rows * p.nb * BS_WARPS)) p.stat[at] = make_float2(m, sum);
       return true;
     };
-    // back to the K best, in order
+    // How many of the best and of those that wait are above a key.
+    auto above = [&](uint64_t key) {
+      int rank = 0;
+      for (int c = 0; c < have; ++c) rank += best[c] > key;
+      for (int c = 0; c < n; ++c) rank += list[c] > key;
+      return rank;
+    };
+    // the K best anew, in order
     auto cut = [&]() {
-      if (n > K + bs_slack(K) || (n > K && !floor)) {
-        for (int i = tid; i < n; i += BS_THREADS) {
-          const uint64_t key = list[i];
-          int rank = 0;
-          for (int c = 0; c < n; ++c) rank += list[c] > key;
+      if (n > bs_slack(K) || (have + n > K && !floor)) {
+        for (int i = tid; i < have + n; i += BS_THREADS) {
+          const uint64_t key = i < have ? best[i] : list[i - have];
+          const int rank = above(key);
           if (rank < K) other[rank] = key;
         }
         takers_sync();
-        uint64_t* t = list;
-        list = other;
+        uint64_t* t = best;   // (there are K: bs_slack is no less)
+        best = other;
         other = t;
-        n = K;
-        floor = list[K - 1];
+        have = K;
+        n = 0;
+        floor = best[K - 1];
         bar = key_logit(floor);
       }
     };
     // A logit of batch b again, for the few that are looked at twice.
     auto again = [&](int b, int k) { return token(b, k) < p.V ? __ldg(z + token(b, k)) : -INFINITY; };
     // No room for what is above the bar in batch b (one warp's logits, equal ones, rising rows): a higher bar that the
-    // bests of K to 2 K threads reach, by bisection on the keys, which differ.  At least K logits reach it, and at most
-    // BS_PER of each of those threads.
+    // bests of K threads reach, by bisection on the keys, which differ.  At least K logits reach it, and at most BS_PER of
+    // each of those threads.
     auto squeeze = [&](int b) {
-      uint64_t best = 0, lo = 1, hi = ~0ull;
+      uint64_t mine = 0, lo = 1, hi = ~0ull;
 #pragma unroll 1
       for (int k = 0; k < BS_PER; ++k) {
         const float v = again(b, k);
         const uint64_t key = v > bar ? cand_key(v, token(b, k)) : 0;
-        best = key > best ? key : best;
+        mine = key > mine ? key : mine;
       }
-      if (takers_count(best >= lo) >= 2 * K)
+      if (takers_count(mine >= lo) > K)
         while (hi - lo > 1) {
           const uint64_t mid = lo + (hi - lo) / 2;
-          const int c = takers_count(best >= mid);
+          const int c = takers_count(mine >= mid);
           if (c >= K) {
             lo = mid;
-            if (c <= 2 * K) break;
+            if (c == K) break;
           } else {
             hi = mid;
           }
         }
       if (tid == 0) n_sh = n;
       takers_sync();
-      if (best >= lo)
+      if (mine >= lo)
 #pragma unroll 1
         for (int k = 0; k < BS_PER; ++k) {
           const float v = again(b, k);
@@ -403,13 +409,12 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     // the piece's list in order
     const int64_t slot = place + blockIdx.x;
     const bool in = in_extent(slot, 1, p.n_lists);
-    for (int i = tid; i < n; i += BS_THREADS) {
-      const uint64_t key = list[i];
-      int rank = 0;
-      for (int c = 0; c < n; ++c) rank += list[c] > key;
+    for (int i = tid; i < have + n; i += BS_THREADS) {
+      const uint64_t key = i < have ? best[i] : list[i - have];
+      const int rank = above(key);
       if (rank < K && in) p.keys[slot * K + rank] = key;
     }
-    for (int i = n + tid; i < K; i += BS_THREADS)
+    for (int i = have + n + tid; i < K; i += BS_THREADS)
       if (in) p.keys[slot * K + i] = 0;
     if (b0 == 0 && tid == 0) {   // the row's first piece says how many there are
       const int64_t last = place * p.nb + p.nb - 1;
@@ -519,9 +524,9 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
     }
   }
   __syncthreads();
-  // First the lists' leading entries, n_out or some BM_LEAD in all: their n_out-th best is a bar.  Then what reaches it, of all
+  // First the lists' leading entries, some four times n_out in all: their n_out-th best is a bar.  Then what reaches it, of all
   // entries.  (One loop for both: a kernel this short pays for the code that it runs through once.)
-  const int lead = lists ? min(K, max((K + lists - 1) / lists, BM_LEAD / lists)) : 0;   // of each list
+  const int lead = lists ? min(K, max((K + lists - 1) / lists, max(BM_LEAD, 4 * K) / lists)) : 0;   // of each list
   const int64_t out = (int64_t)b * K;
   const bool in = in_extent(out, K, (int64_t)p.B * K);
   int n = 0;
