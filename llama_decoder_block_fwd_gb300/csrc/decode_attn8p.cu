@@ -33,9 +33,10 @@
 namespace llama {
 namespace {
 
-// Threads: warp 0 TMA, 1 MMA, then SG groups of four softmax warps, the last warp q -> E4M3 hi / lo.  With 8 rows and more the
-// softmax sets the pace, so two groups share the rows of a tile (a thread has one key of four or eight rows).
-constexpr int dp_threads(int SG) { return 96 + 128 * SG; }
+// Threads: warp 0 TMA and q -> E4M3 hi / lo, warp 1 MMA, then SG groups of four softmax warps.  With 8 rows and more the softmax
+// sets the pace, so two groups share the rows of a tile (a thread has one key of four or eight rows); a warp of its own for q
+// would leave two such CTAs 80 registers a thread, and eight rows' state spills there.
+constexpr int dp_threads(int SG) { return 64 + 128 * SG; }
 // two CTAs per SM (2 x 110 KB of shared memory), so that one's hand-offs overlap the other's
 constexpr int DP_KSTAGES = 3;
 constexpr int DP_VSTAGES = 2;
@@ -153,6 +154,31 @@ __device__ __forceinline__ uint32_t sw128_at(int n, int c) {
   return (uint32_t)(n * 128 + ((((c >> 4) ^ (n & 7))) << 4) + (c & 15));
 }
 
+// mbar_wait in few instructions: the roles' loops wait in many places, and together they have to fit the instruction cache.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned* status) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) [[likely]] return true;
+  const unsigned long long t0 = globaltimer_ns();
+  do {
+    if (mbar_try_wait(a, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) [[unlikely]] {
+      atomicOr(status, STATUS_TIMEOUT);
+      *abort = 1;
+    }
+  } while (!*abort);
+  return false;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // ---- the work split
 __device__ __forceinline__ int good_pos(int pos, int max_pos) { return pos < -1 || pos > max_pos ? -1 : pos; }
 __device__ __forceinline__ int tiles_at(const DecodeAttn8pParams& p, int b) {
@@ -211,17 +237,14 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     const int g = g0 + h / RH, i = sub * RH + h % RH;
     return g < p.n_kv && i < p.r ? g * p.r + i : -1;
   };
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < P_COUNT; ++i) {
-      int cnt = 1;
-      if (i == P_QR || i == P_QR + 1) cnt = 32;
-      if (i == P_SFREE || i == P_SFREE + 1 || i == P_PF || i == P_PF + 1 || i == P_OFREE || i == P_QC || i == P_QC + 1 ||
-          (i >= P_SCE && i < P_SCE + DP_SSTAGES))
-        cnt = 128 * SG;
-      mbar_init(&bars[i], cnt);
-    }
-    *abort_flag = 0;
+  if (threadIdx.x < P_COUNT) {
+    const int i = threadIdx.x;
+    const bool softmax = i == P_SFREE || i == P_SFREE + 1 || i == P_PF || i == P_PF + 1 || i == P_OFREE || i == P_QC || i == P_QC + 1 ||
+                         (i >= P_SCE && i < P_SCE + DP_SSTAGES);
+    mbar_init(&bars[i], softmax ? 128 * SG : i == P_QR || i == P_QR + 1 ? 32 : 1);
+    if (i == 0) *abort_flag = 0;
     fence_mbar_init();
+  } else if (threadIdx.x == 64) {
     tma_prefetch_desc(&p.tmK);
     tma_prefetch_desc(&p.tmV);
   }
@@ -307,14 +330,62 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     bool ok = true;
     auto issue_v = [&](int gt) -> bool {
       const int vs = gt % DP_VSTAGES;
-      if (!mbar_wait(&bars[P_VE + vs], ((gt / DP_VSTAGES) & 1) ^ 1, abort_flag, p.status)) return false;
+      if (!wait_for(&bars[P_VE + vs], ((gt / DP_VSTAGES) & 1) ^ 1, abort_flag, p.status)) return false;
       if (!box_in(g0 * HD, p.n_kv * HD, (int64_t)v_page * 128, (int64_t)p.n_pages * 128)) { *abort_flag = 1; return false; }
       mbar_arrive_expect_tx(&bars[P_VF + vs], L::F8);
       tma_load_2d(sbase + L::OFF_V8 + vs * L::F8, &p.tmV, &bars[P_VF + vs], g0 * HD, v_page * 128);
       return true;
     };
+    // the query rows of piece `it` as hi and lo codes, by the whole warp
+    auto put_q = [&](int it) -> bool {
+      constexpr int VH = HD / 8;                  // 8-element chunks of a row
+      constexpr int NCH = R * VH;
+      constexpr int PER = (NCH + 31) / 32;
+      const int qb = it & 1;
+      uint4 w[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int c = lane + 32 * j, head = c < NCH ? head_of(c / VH) : -1;
+        w[j] = head >= 0 ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.n_q + head) * HD + c % VH * 8)
+                         : make_uint4(0, 0, 0, 0);
+      }
+      // the buffer is free once the MMAs of piece it - 2 have read it and the softmax warps its scales
+      if (!wait_for(&bars[P_QE + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+      if (!wait_for(&bars[P_QC + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+      uint8_t* qop = smem + L::OFF_Q + qb * L::OPB;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int c = lane + 32 * j, h = c / VH;
+        const uint32_t e[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int o = VH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // a power of two per row: amax * qs in [128, 256)
+        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+        const int up = min(max(7 - ex, -126), 126);
+        const float qs = exp2_int(up);
+        if (c < NCH) {
+          const int d = c % VH * 8 + h / RH * HD;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            hi[k] = split_fine(__uint_as_float(e[k] << 16) * qs, __uint_as_float(e[k] & 0xFFFF0000u) * qs, lo[k]);
+          *reinterpret_cast<uint2*>(qop + sw128_at(h, d)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(qop + sw128_at(R + h, d)) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          if (c % VH == 0) qinv[qb * 16 + h] = exp2_int(-up);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      mbar_arrive(&bars[P_QR + qb]);
+      return true;
+    };
+    int it = 0;
     Pieces s = it0;
-    while (ok && next_piece(p, s, b, t0, t1, nt, n_keys)) {
+    for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
       const int* row = p.block_table + (int64_t)b * p.max_pages;
       int ids = 0;
       for (int t = t0; t < t1; ++t, ++tile) {
@@ -325,8 +396,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         const int page = __shfl_sync(0xffffffffu, ids, (t - t0) & 31);
         if (lane == 0) {
           const int ks = tile % DP_KSTAGES, sc = tile % DP_SSTAGES;
-          ok = mbar_wait(&bars[P_KE + ks], ((tile / DP_KSTAGES) & 1) ^ 1, abort_flag, p.status) &&
-               mbar_wait(&bars[P_SCE + sc], ((tile / DP_SSTAGES) & 1) ^ 1, abort_flag, p.status);
+          ok = wait_for(&bars[P_KE + ks], ((tile / DP_KSTAGES) & 1) ^ 1, abort_flag, p.status) &&
+               wait_for(&bars[P_SCE + sc], ((tile / DP_SSTAGES) & 1) ^ 1, abort_flag, p.status);
           if (ok && !(box_in(g0 * HD, p.n_kv * HD, (int64_t)page * 128, (int64_t)p.n_pages * 128) &&
                       in_extent(((int64_t)page * p.n_kv + g0) * 128, n_sc * 128, (int64_t)p.n_pages * p.n_kv * 128))) {
             *abort_flag = 1;
@@ -346,6 +417,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         if (!ok) break;
         v_page = page;
+        if (t == t0 && !(ok = put_q(it))) break;   // behind the piece's first K, which is on its way meanwhile
       }
     }
     if (ok && tile > 0 && lane == 0) issue_v(tile - 1);
@@ -357,9 +429,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       // S^T of tile gt, the first of piece it or a later one
       auto issue_s = [&](int gt, int it, bool first) -> bool {
         const int st = gt % DP_KSTAGES, sb = gt & 1, qb = it & 1;
-        if (first && !mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) return false;
-        if (!mbar_wait(&bars[P_KF + st], (gt / DP_KSTAGES) & 1, abort_flag, p.status)) return false;
-        if (!mbar_wait(&bars[P_SFREE + sb], ((gt >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+        if (first && !wait_for(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) return false;
+        if (!wait_for(&bars[P_KF + st], (gt / DP_KSTAGES) & 1, abort_flag, p.status)) return false;
+        if (!wait_for(&bars[P_SFREE + sb], ((gt >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
         tc_fence_after();
         const uint64_t qd0 = sdesc_sw128(sbase + L::OFF_Q + qb * L::OPB, 16, 1024);
         const uint64_t kd0 = sdesc_sw128(sbase + L::OFF_K8 + st * L::F8, 16, 1024);
@@ -372,9 +444,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       };
       auto issue_pv = [&](int gt, int it, bool first) -> bool {
         const int st = gt % DP_VSTAGES, pb = gt & 1;
-        if (!mbar_wait(&bars[P_PF + pb], (gt >> 1) & 1, abort_flag, p.status)) return false;
-        if (!mbar_wait(&bars[P_VF + st], (gt / DP_VSTAGES) & 1, abort_flag, p.status)) return false;
-        if (first && !mbar_wait(&bars[P_OFREE], (it & 1) ^ 1, abort_flag, p.status)) return false;
+        if (!wait_for(&bars[P_PF + pb], (gt >> 1) & 1, abort_flag, p.status)) return false;
+        if (!wait_for(&bars[P_VF + st], (gt / DP_VSTAGES) & 1, abort_flag, p.status)) return false;
+        if (first && !wait_for(&bars[P_OFREE], (it & 1) ^ 1, abort_flag, p.status)) return false;
         tc_fence_after();
         // V^T: M = bytes of the row (MN-major), 8-key groups 1024 bytes apart
         const uint64_t vd0 = sdesc_sw128(sbase + L::OFF_V8 + st * L::F8, 16384, 1024);
@@ -407,55 +479,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       }
       int no_abort = 0;
       tc_commit(&bars[P_DRAIN]);
-      mbar_wait(&bars[P_DRAIN], 0, &no_abort, p.status);
-    }
-  } else if (warp == 2 + 4 * SG) {  // ------------------------------------ q -> E4M3 hi / lo operand
-    constexpr int VH = HD / 8;                  // 8-element chunks of a row
-    constexpr int NCH = R * VH;
-    constexpr int PER = (NCH + 31) / 32;
-    int it = 0;
-    Pieces s = it0;
-    for (; next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
-      const int qb = it & 1;
-      uint4 w[PER];
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int c = lane + 32 * j, head = c < NCH ? head_of(c / VH) : -1;
-        w[j] = head >= 0 ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.n_q + head) * HD + c % VH * 8)
-                         : make_uint4(0, 0, 0, 0);
-      }
-      // the buffer is free once the MMAs of piece it - 2 have read it and the softmax warps its scales
-      if (!mbar_wait(&bars[P_QE + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) break;
-      if (!mbar_wait(&bars[P_QC + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) break;
-      uint8_t* qop = smem + L::OFF_Q + qb * L::OPB;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int c = lane + 32 * j, h = c / VH;
-        const uint32_t e[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
-#pragma unroll
-        for (int o = VH / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // a power of two per row: amax * qs in [128, 256)
-        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-        const int up = min(max(7 - ex, -126), 126);
-        const float qs = exp2_int(up);
-        if (c < NCH) {
-          const int d = c % VH * 8 + h / RH * HD;
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            hi[k] = split_fine(__uint_as_float(e[k] << 16) * qs, __uint_as_float(e[k] & 0xFFFF0000u) * qs, lo[k]);
-          *reinterpret_cast<uint2*>(qop + sw128_at(h, d)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(qop + sw128_at(R + h, d)) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          if (c % VH == 0) qinv[qb * 16 + h] = exp2_int(-up);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      mbar_arrive(&bars[P_QR + qb]);
+      wait_for(&bars[P_DRAIN], 0, &no_abort, p.status);
     }
   } else {  // ------------------------------------------------------------ softmax warps
     const int sg = (warp - 2) >> 2, qw = warp & 3;   // a warp reaches TMEM lanes 32 * (warp % 4) ..
@@ -478,7 +502,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     Pieces s = it0;
     for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
       const int qb = it & 1;
-      if (!mbar_wait(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
+      if (!wait_for(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
       float m_ref[RT], lsum[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -488,7 +512,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       for (int tt = t0; tt < t1; ++tt, ++tile) {
         const int sb = tile & 1, ss = tile % DP_SSTAGES;
         const bool valid = tt * 128 + t < n_keys;
-        if (!mbar_wait(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+        if (!wait_for(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
         float ks[NSC], lvs[NSC], ivs[NSC];
         {
           const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC) + sc0 * 128;
@@ -496,12 +520,12 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
           for (int k = 0; k < NSC; ++k) {
             ks[k] = scales[k * 128 + t] * p.scale_log2;
             const float v = fmaxf(scales[256 + k * 128 + t], 7.88860905e-31f);   // 2^-100: a zero scale has a logarithm too
-            lvs[k] = __log2f(v);
-            ivs[k] = valid ? 1.f / v : 0.f;
+            lvs[k] = lg2(v);
+            ivs[k] = valid ? __fdividef(1.f, v) : 0.f;
           }
         }
         mbar_arrive(&bars[P_SCE + ss]);
-        if (!mbar_wait(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        if (!wait_for(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
         uint32_t hi[LD], lo[LD];
         hi_lo(tS + sb * NP, hi, lo);
@@ -531,10 +555,10 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         }
         const int pb = tile & 1;
         if (tile >= 2) {
-          if (!mbar_wait(&bars[P_OD + pb], ((tile - 2) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!wait_for(&bars[P_OD + pb], ((tile - 2) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         }
-        if (resc) {   // the same in all 128 threads of the group, which saw the same maxima
-          if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        if (resc) [[unlikely]] {   // the same in all 128 threads of the group, which saw the same maxima
+          if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after();
           uint32_t oh[LD], ol[LD];
           hi_lo(tO, oh, ol);
@@ -542,7 +566,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
           for (int i = 0; i < RT; ++i) {
             const float tm = tile_max(i);
             if (!(tm > m_ref[i] + kDpRescaleLog2)) continue;
-            const float alpha = exp2f(m_ref[i] - tm);
+            const float alpha = ex2(m_ref[i] - tm);
             m_ref[i] = tm;
             lsum[i] *= alpha;
             oh[i] = __float_as_uint(__uint_as_float(oh[i]) * alpha);
@@ -561,7 +585,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             if (i + j < RT) {
-              w[j] = exp2f(e[i + j] - (m_ref[i + j] - kDpPScaleLog2));
+              w[j] = ex2(e[i + j] - (m_ref[i + j] - kDpPScaleLog2));
               lsum[i + j] = fmaf(w[j], ivs[NSC == 2 ? (i + j) / RH : 0], lsum[i + j]);
             }
           uint32_t lo2;
@@ -573,9 +597,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
               pbase[sw128_at(R + h0 + i + j, t)] = (uint8_t)(lo2 >> (8 * j));
             }
         }
-        if (sg == 0 && (tt + 1) * 128 > n_keys) {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
+        if (sg == 0 && (tt + 1) * 128 > n_keys) [[unlikely]] {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
           const int vs = tile % DP_VSTAGES;
-          if (!mbar_wait(&bars[P_VF + vs], (tile / DP_VSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!wait_for(&bars[P_VF + vs], (tile / DP_VSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
           if (!valid) {
             uint4* vrow = reinterpret_cast<uint4*>(smem + L::OFF_V8 + vs * L::F8 + t * 128);
 #pragma unroll
@@ -588,7 +612,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       }
       if (!ok) break;
       mbar_arrive(&bars[P_QC + qb]);   // the q scales have been read
-      if (!mbar_wait(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+      if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
       uint32_t oh[LD], ol[LD];
       hi_lo(tO, oh, ol);
