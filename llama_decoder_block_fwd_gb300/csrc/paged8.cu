@@ -17,7 +17,8 @@ namespace llama {
 namespace {
 
 constexpr int A8_THREADS = 256;
-constexpr int A8_TOK = 2;
+constexpr int A8_FEW = 2, A8_MANY = 4;       // tokens of a CTA
+constexpr int A8_MANY_CTAS_PER_SM = 6;
 
 struct Append8Params {
   const uint16_t *q, *k, *v;             // [T] rows of n_q / n_kv / n_kv heads x hd, row strides below
@@ -62,50 +63,66 @@ __device__ __forceinline__ int checked_slot(const Append8Params& p, int t) {
   return slot;
 }
 
-// One 16-byte vector of a head's row, VPH of them in VPH neighbouring lanes: rotated, and for K and V encoded with
-// the scale that the lanes agree on.  Every lane of the warp calls it; `live` says which have a vector.
+// Where a token's rows go.
+struct TokenOut {
+  uint16_t* q;
+  uint8_t *k, *v;
+  float *ks, *vs;      // its scale in head 0
+  int slot;            // -1: nothing is written
+};
+
+// One 16-byte vector of a head's row, VPH of them in VPH neighbouring lanes: rotated, and for K and V (`scales`: some lane of the
+// warp has one) encoded with the scale that the lanes agree on.  Every lane of the warp calls it; `live` says which have a
+// vector: number o of part 0 (q), 1 (k) or 2 (v).
 template <int VPH>
-__device__ __forceinline__ void store_vector(const Append8Params& p, uint4 w, bool live, int part, int o, int t, int slot,
-                                             const float2* cs) {
-  const int g = o / VPH, j = o % VPH;
+__device__ __forceinline__ void store_vector(const Append8Params& p, uint4 w, bool live, bool scales, int part, int o,
+                                             const TokenOut& out, const float2* cs) {
   float x[8];
   unpack8(w, x);
   float u = 0.f;
-  const float4 c0 = reinterpret_cast<const float4*>(cs)[2 * j], c1 = reinterpret_cast<const float4*>(cs)[2 * j + 1];
-  const float2 c[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+  if (scales) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    u = fmaxf(u, part == 2 ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a) + fabsf(b));
-    if (part != 2) {
+    for (int i = 0; i < 8; i += 2) {
+      const float a = fabsf(x[i]), b = fabsf(x[i + 1]);
+      u = fmaxf(u, part == 2 ? fmaxf(a, b) : a + b);
+    }
+#pragma unroll
+    for (int k = VPH / 2; k > 0; k >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, k));
+  }
+  if (!live || out.slot < 0) return;
+  const int j = o % VPH;
+  if (part != 2) {
+    const float4 c0 = reinterpret_cast<const float4*>(cs)[2 * j], c1 = reinterpret_cast<const float4*>(cs)[2 * j + 1];
+    const float2 c[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1];
       x[2 * i] = a * c[i].x - b * c[i].y;
       x[2 * i + 1] = a * c[i].y + b * c[i].x;
     }
   }
-#pragma unroll
-  for (int k = VPH / 2; k > 0; k >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, k));
-  if (!live || slot < 0) return;
   if (part == 0) {
-    const int64_t at = ((int64_t)t * p.n_q * VPH + o) * 8;
-    if (in_extent(at, 8, (int64_t)p.T * p.n_q * p.hd)) *reinterpret_cast<uint4*>(p.q_out + at) = pack8(x);
+    if (in_extent(out.q + o * 8 - p.q_out, 8, (int64_t)p.T * p.n_q * p.hd)) *reinterpret_cast<uint4*>(out.q + o * 8) = pack8(x);
     return;
   }
   const int e = row_scale_exp(u);
-  const int64_t at = ((int64_t)slot * p.n_kv * VPH + o) * 8;
-  if (in_extent(at, 8, p.n_slots * p.n_kv * p.hd))
-    *reinterpret_cast<uint2*>((part == 2 ? p.v_codes : p.k_codes) + at) = encode8(x, exp2_int(-e));
-  const int64_t sat = ((int64_t)(slot / 128) * p.n_kv + g) * 128 + slot % 128;
-  if (j == 0 && in_extent(sat, 1, p.n_slots * p.n_kv)) (part == 2 ? p.v_scale : p.k_scale)[sat] = exp2_int(e);
+  uint8_t* codes = part == 2 ? out.v : out.k;
+  if (in_extent(codes + o * 8 - (part == 2 ? p.v_codes : p.k_codes), 8, p.n_slots * p.n_kv * p.hd))
+    *reinterpret_cast<uint2*>(codes + o * 8) = encode8(x, exp2_int(-e));
+  float* scale = (part == 2 ? out.vs : out.ks) + o / VPH * 128;
+  if (j == 0 && in_extent(scale - (part == 2 ? p.v_scale : p.k_scale), 1, p.n_slots * p.n_kv)) *scale = exp2_int(e);
 }
 
 // HBM bound: every row is read once in 16-byte pieces and written once.  A CTA takes TOK tokens, forms each token's hd / 2
-// cosines and sines once, then walks the vectors of their q, k and v heads, the next ones on their way; the lanes of a head
-// (VPH = hd / 8, a power of two) agree on its scale by shuffles.  8192 tokens of 32/8 heads x 128 (185 MB): 31.9 us = 5.8 TB/s
-// with two tokens per CTA (four 32.3, eight 40 us; a warp per head and token 59 us); 300 tokens, one per CTA, 3.5 us.
+// cosines and sines once, then walks the vectors of their q, k and v heads: vector i of all its tokens at a time, so that what
+// belongs to a place in the row is found once, the next ones on their way; the lanes of a head (VPH = hd / 8, a power
+// of two) agree on its scale by shuffles.  8192 tokens of 32/8 heads x 128 (185 MB): 31.3 us = 5.9 TB/s with four tokens per
+// CTA, 32.9 with two, 34.1 with one; 2048 of 32/32: 16.7, 16.1, 17.8; 1000 of 32/8: 6.5, 6.2, 6.0; 300: 3.4.  So four where
+// that leaves every SM several CTAs, two where it leaves it one.  (A warp per head and token 59 us.)
 template <int VPH, int TOK>
 __global__ void __launch_bounds__(A8_THREADS) rope_append8_kernel(const __grid_constant__ Append8Params p) {
   __shared__ __align__(16) float2 cs[TOK][VPH * 4];
-  __shared__ int slot_sh[TOK];
+  __shared__ TokenOut out[TOK];
   const int q_vec = p.q ? p.n_q * VPH : 0, kv_vec = p.n_kv * VPH, total = q_vec + 2 * kv_vec;
   const int t0 = blockIdx.x * TOK, n = min(TOK, p.T - t0);
   auto place = [&](int i, int& part, int& o) {
@@ -118,13 +135,24 @@ __global__ void __launch_bounds__(A8_THREADS) rope_append8_kernel(const __grid_c
     place(i, part, o);
     const uint16_t* src = part == 0 ? p.q : part == 2 ? p.v : p.k;
     const int64_t stride = part == 0 ? p.q_stride : part == 2 ? p.v_stride : p.k_stride;
+    src += t0 * stride + o * 8;
 #pragma unroll
     for (int tk = 0; tk < TOK; ++tk)
-      if (tk < n) w[tk] = *reinterpret_cast<const uint4*>(src + (t0 + tk) * stride + o * 8);
+      if (tk < n) w[tk] = *reinterpret_cast<const uint4*>(src + tk * stride);
   };
   uint4 w[TOK];
   load(threadIdx.x, w);   // on their way while the angles are formed
-  if (threadIdx.x < TOK) slot_sh[threadIdx.x] = checked_slot(p, t0 + threadIdx.x);
+  if (threadIdx.x < TOK) {
+    TokenOut r;
+    r.slot = checked_slot(p, t0 + threadIdx.x);
+    const int64_t at = max(r.slot, 0), row = at * p.n_kv * p.hd, head0 = at / 128 * p.n_kv * 128 + at % 128;
+    r.q = p.q_out + (int64_t)(t0 + threadIdx.x) * p.n_q * p.hd;
+    r.k = p.k_codes + row;
+    r.v = p.v_codes + row;
+    r.ks = p.k_scale + head0;
+    r.vs = p.v_scale + head0;
+    out[threadIdx.x] = r;
+  }
   for (int i = threadIdx.x; i < TOK * VPH * 4; i += A8_THREADS) {
     const int tk = i % TOK, j = i / TOK;
     if (tk < n) rope_sincos((float)__ldg(p.positions + t0 + tk), p.freq[j], cs[tk][j].y, cs[tk][j].x);
@@ -136,10 +164,10 @@ __global__ void __launch_bounds__(A8_THREADS) rope_append8_kernel(const __grid_c
     load(i + A8_THREADS, next);
     int part, o;
     place(i, part, o);
-    const bool live = i < total;
+    const bool live = i < total, scales = (i | 31) >= q_vec;   // (the warp's last vector is no query's)
 #pragma unroll
     for (int tk = 0; tk < TOK; ++tk)
-      if (tk < n) store_vector<VPH>(p, w[tk], live, part, live ? o : 0, t0 + tk, slot_sh[tk], cs[tk]);
+      if (tk < n) store_vector<VPH>(p, w[tk], live, scales, part, live ? o : 0, out[tk], cs[tk]);
 #pragma unroll
     for (int tk = 0; tk < TOK; ++tk) w[tk] = next[tk];
   }
@@ -333,13 +361,17 @@ int launch_rope_append8(const Append8Desc& d, const RopeFreq* freq, int num_sms,
   p.n_slots = d.n_pages * 128;
   p.status = status;
   memcpy(p.freq, freq, sizeof(RopeFreq) * (d.hd / 2));
-  const dim3 some((unsigned)((d.T + A8_TOK - 1) / A8_TOK)), one((unsigned)d.T);
-  const bool many = d.T >= (int64_t)A8_TOK * num_sms;   // A8_TOK tokens share a pass over the row where every SM gets them
-  switch (d.hd) {
-    case 64: many ? rope_append8_kernel<8, A8_TOK><<<some, A8_THREADS, 0, st>>>(p) : rope_append8_kernel<8, 1><<<one, A8_THREADS, 0, st>>>(p); break;
-    case 128: many ? rope_append8_kernel<16, A8_TOK><<<some, A8_THREADS, 0, st>>>(p) : rope_append8_kernel<16, 1><<<one, A8_THREADS, 0, st>>>(p); break;
-    default: rope_append8_any_kernel<<<one, A8_THREADS, 0, st>>>(p);
-  }
+  const int tok = d.T >= (int64_t)A8_MANY * A8_MANY_CTAS_PER_SM * num_sms ? A8_MANY : d.T >= (int64_t)A8_FEW * num_sms ? A8_FEW : 1;
+  const unsigned grid = (unsigned)((d.T + tok - 1) / tok);
+  if (d.hd == 64)
+    (tok == A8_MANY  ? rope_append8_kernel<8, A8_MANY>
+     : tok == A8_FEW ? rope_append8_kernel<8, A8_FEW>
+                     : rope_append8_kernel<8, 1>)<<<grid, A8_THREADS, 0, st>>>(p);
+  else if (d.hd == 128)
+    (tok == A8_MANY  ? rope_append8_kernel<16, A8_MANY>
+     : tok == A8_FEW ? rope_append8_kernel<16, A8_FEW>
+                     : rope_append8_kernel<16, 1>)<<<grid, A8_THREADS, 0, st>>>(p);
+  else rope_append8_any_kernel<<<(unsigned)d.T, A8_THREADS, 0, st>>>(p);
   return 0;
 }
 

@@ -160,6 +160,32 @@ def test_append_skips_and_latches():
     assert _status() == 0 and np.all(got[1] == 0x55)
 
 
+@pytest.mark.parametrize("T,n_q,n_kv,hd", [(4003, 6, 3, 64), (3661, 4, 1, 128), (8191, 1, 1, 64)])
+def test_append_of_many_tokens_some_skipped(T, n_q, n_kv, hd):
+    import torch
+    rng = np.random.default_rng(T)
+    x = _dev(rng.normal(size=(T, n_q + 2 * n_kv, hd)) * np.exp(rng.normal(size=(T, n_q + 2 * n_kv, 1)) * 3), torch.bfloat16)
+    q, k, v = x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:]
+    n_pages = -(-T // 128) + 1
+    slots = rng.permutation(n_pages * 128)[:T].astype(np.int32)
+    slots[rng.random(T) < 0.3] = -1
+    slots[:9] = -1
+    pos = rng.integers(0, 1 << 17, size=T).astype(np.int32)
+    got = _append(q, k, v, pos, slots, n_pages)
+    assert _status() == 0
+    live = np.flatnonzero(slots >= 0)
+    _check_written(to_f64(k)[live], to_f64(v)[live], pos[live], got, slots[live])
+    assert np.all(got[0][slots < 0] == -3.0)
+    ref = R.rotate(to_f64(q)[live], pos[live], THETA)
+    pair = np.repeat(np.abs(to_f64(q)[live][..., 0::2]) + np.abs(to_f64(q)[live][..., 1::2]), 2, axis=-1)
+    tol = 2.0 ** -8 * np.abs(ref) + pair * (2.0 ** -19 + pos[live].astype(np.float64)[:, None, None] * 1e-11)
+    assert np.all(np.abs(got[0][live] - ref) <= tol)
+    rest = np.setdiff1d(np.arange(n_pages * 128), slots)
+    for codes, scales in ((got[1], got[2]), (got[3], got[4])):
+        c, s = _at(rest, codes, scales)
+        assert np.all(c == 0x55) and np.all(s == -7.0)
+
+
 # -------------------------------------------------------------------------------------- read back
 class Cache:
     """Random codes and scales of sequences of the given lengths in shuffled pages, NaN in every row that no
