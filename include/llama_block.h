@@ -466,9 +466,10 @@ int llama_gqa_attention_decode_paged_kv8(const llama_dims* dims, const void* q, 
  *   parents, tokens [B, n_out] int32: beam (0 .. W-1) and token of each; out_scores [B, n_out] fp32.  Where there are
  *                fewer candidates: -1, -1 and -inf
  *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_SELECT, dims with B and S = W, ..., vocab) bytes, for any n_out
- * The outputs may not overlap the inputs.  Sums of exponentials in fp32, logarithm and scores in fp64 (out_scores
- * rounds once): candidates of one beam are ranked by their logits, those of different beams by scores good to
- * about 2^-22; equal rows with equal scores give equal scores.
+ * The outputs may not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
+ * Exponentials and their sums in fp32, the sum's logarithm to 2^-25, scores in fp64 (out_scores rounds once): candidates
+ * of one beam are ranked by their logits, those of different beams by scores good to about 2^-22; equal rows with equal
+ * scores give equal scores.
  * LLAMA_ERR_UNSUPPORTED for W > 32, n_out > 64 or B * W >= 2^22; LLAMA_ERR_INVALID_ARG for B < 0, W < 1, n_out < 1,
  * vocab < 1 or > 2^30, ld < vocab, pad_token outside [0, vocab) with finished given, NULL arrays; LLAMA_ERR_ALIGNMENT for arrays
  * not 4-byte aligned or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE for a workspace that is too small.    */
@@ -499,11 +500,13 @@ typedef struct llama_page_pool {
  *   pools: HOST array of n_pools records (base: device memory), read before the call returns
  *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_REORDER_PAGED, dims with B and S = W, ..., kv_capacity = 128 * max_pages)
  * A page may stand in several rows of a request, in the same column; other requests may share pages that some kept beam of
- * each holds (a common prompt).  No pool row is written but the copied rows.
+ * each holds (a common prompt).  No pool row is written but the copied rows.  Calls that overlap on the GPU need
+ * workspaces of their own.
  * LLAMA_ERR_UNSUPPORTED for W > 32, B > 8192, n_pages >= 2^24, max_pages > 2^17, n_free or freed_room >= 2^31, n_pools > 8,
- * parts * row_bytes > 2^24, n_layers * parts * row_bytes > 2^27 (16 GB of one page over all layers of a pool); LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's
- * n_layers, parts or row_bytes < 1, row_bytes no multiple of 4), NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte,
- * pools or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE.  Latched as LLAMA_ERR_INVALID_ARG in the device status
+ * parts * row_bytes > 2^24, n_layers * parts * row_bytes > 2^27 (16 GB of one page over all layers of a pool);
+ * LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's n_layers, parts or
+ * row_bytes < 1, row_bytes no multiple of 4), NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte, pools or ws
+ * not 16-byte aligned; LLAMA_ERR_WORKSPACE.  Latched as LLAMA_ERR_INVALID_ARG in the device status
  * word: a parent outside [-1, W) (taken as -1), n_cached outside [0, 128 * max_pages] (taken as 0), page ids outside
  * [0, n_pages) among the held ones (never freed; not copied: the entry is -1), more copies than pages (their entries are -1;
  * counts[0] says what was needed) and more dead pages than freed_room (the rest is not listed; counts[1] counts them). */

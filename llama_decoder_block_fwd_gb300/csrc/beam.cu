@@ -20,9 +20,14 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // ---------------------------------------------------------------------------------------- select
 // HBM bound for many rows, latency for few.  The rows' batches of BS_BATCH logits, one row after the other, are cut into
 // equal ranges, one per CTA (rows that need not be read left out).  A producer warp streams a range's batches into a ring in
-// shared memory (bulk copies), 256 threads take them.  Each warp sums the exponentials of its 512 logits of a batch from
+// shared memory (bulk copies), 256 threads take them.  Each warp sums the exponentials of its 640 logits of a batch from
 // their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
-// n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second kernel joins a request's lists and sums.
+// n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second
+// kernel joins a request's lists and sums.
+// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 45.0 us, the first kernel 40 cold, 4.2 TB/s: half
+// of its issue slots go to an exponential, a comparison and the sums of each logit, and its pieces start and end
+// with the join of eight warps' candidates.  (Registers loaded ahead instead of the ring 52 us, 4 CTAs per SM 46-60.)  One request
+// of 4 beams x 32000: 10.3 us, two launches and their chains.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
 constexpr int BS_PER = 20;                              // logits of a thread in a batch
@@ -427,7 +432,9 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
 }
 
 // Joins a request's rows: each piece's list is in order, so a candidate below the n_out-th best of the lists' heads is none
-// of the n_out best; the others are ranked against each other.
+// of the n_out best; the others are ranked against each other.  One CTA per request, a chain of loads and block barriers: 10.8 us
+// cold for 48 requests of 8 beams and 16 kept.  The candidates that the bar leaves are ranked each against all: for 32 beams and 64
+// kept a bar from 64 entries instead of four times n_out left 3000 of them (324 us in all against 87).
 constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: the bar leaves n_out of n_out lists, or of fewer all
 constexpr int BM_LISTS = (int)kBeamMaxW + BS_CTAS_PER_SM * 256;   // of a request, at most (256: kMaxSms)
 constexpr int BM_LEAD = 64;
@@ -621,7 +628,7 @@ struct ReorderParams {
 __device__ __forceinline__ int run_vecs(const BeamPool& q, int rows) { return (rows * q.row_bytes + 15) / 16; }
 
 // One request per CTA: its new table rows, the copies its new beams need, and its dead pages in order.  A thread takes one
-// entry of the table, (column, beam) in that order; the latency of three dependent loads is what it costs.
+// entry of the table, (column, beam) in that order; the latency of three dependent loads is what it costs, 6.8 us cold.
 __global__ void __launch_bounds__(BR_THREADS) beam_plan_kernel(const __grid_constant__ ReorderParams p, int beams_pow2) {
   __shared__ int n[BR_MAX_W], par[BR_MAX_W], tile[BR_THREADS], wsum[BR_THREADS / 32];
   __shared__ int n_copy_sh;
@@ -728,7 +735,10 @@ __device__ __forceinline__ void store_vec(const char* src, char* to, int at, int
 
 // Bound by HBM for many copies, by the latency of a few dependent loads for few.  Every CTA sums up the requests' pages
 // taken, pages left over and vectors to copy; entries and freed pages are dealt out by request, and the vectors of
-// all copies, one after the other, are cut into equal ranges, one per CTA.
+// all copies, one after the other, are cut into equal ranges, one per CTA.  16 requests of 8 beams, eight layers of 8-bit pages of
+// 8 heads x 128 (149 MB read and written): 33 us with the plan, 22 at a copy's rate; one request of 4 beams over two
+// bf16 layers of 2 heads x 64: 6.5 us.
+// (Contiguous ranges beat chunks in turn, 32-49 us, and 3 CTAs per SM 4 and more: reads and writes of open pages mix.)
 __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(const __grid_constant__ ReorderParams p) {
   extern __shared__ int64_t v0[];   // [B + 1] first vector of each request; then [2][B + 1]: first page taken, first page freed
   int* t0 = reinterpret_cast<int*>(v0 + p.B + 1);

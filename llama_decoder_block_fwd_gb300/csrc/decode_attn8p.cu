@@ -6,7 +6,10 @@
 // kc_j, c_j the E4M3 codes of key and value j of the query head's KV head, ks_j, vs_j their scales.
 //
 // What bounds it: the codes and scales are read once, 2 (hd + 4) bytes per position and KV head, at a few operations
-// per byte, so HBM does, where there are enough tiles, and the latency of one tile's chain where there are few.
+// per byte, so HBM does, where there are enough tiles, and the latency of one tile's chain where there are few.  64 sequences
+// of 2-8 K positions, 32/8 heads x 128 (671 MB): 107.6 us = 6.2 TB/s, 93% of a copy's rate; one of 131000 (277 MB) 47.6 us,
+// 87%; three of 100 to 900: 8.9 us.  With 8 query heads and more per KV head the softmax comes nearest to it (64 sequences of 64/8
+// heads 124 us), and with 16 over one KV head it sets the pace (16/1 heads 36 us where the bytes take 14).
 //
 // Tiles.  A tile is one page (128 positions) by 128 bytes of a row: one KV head of 128, or two of 64 side by side, which
 //   one product serves (each head's query rows hold zeros in the other's bytes).  tcgen05 kind::f8f6f4 reads the codes as

@@ -512,3 +512,71 @@ def test_beam_search_over_the_8_bit_cache(captured):
                     assert_parity(out[b * W + w], R.attend(q[b * W + w], k, v), BF16, f"step {step}, request {b}, beam {w}")
         held = {p for r, n in zip(s.table.tolist(), s.n.tolist()) for p in r[:-(-n // 128)]}
         assert not held & set(s.free) and len(held) + len(s.free) == s.n_pages and len(set(s.free)) == len(s.free)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_beam_calls_behind_a_wait_on_another_stream(captured):
+    """The calls before them have finished early, what they read comes late from another stream: it is waited for."""
+    import torch
+    rng = np.random.default_rng(31)
+    B, W, V, P, n_pages = 3, 4, 9000, 3, 64
+    late, first = (_dev(rng.normal(size=(B * W, V)).astype(np.float32)) for _ in range(2))
+    scores = torch.zeros(B, W, device="cuda")
+    z, zero = torch.zeros_like(late), torch.zeros(B, W, dtype=torch.int32, device="cuda")
+    ws = torch.empty(L.llama_workspace_bytes(L.OP_BEAM_SELECT, _bdims(B, W), L.F32, vocab=V), dtype=torch.uint8, device="cuda")
+    wr = torch.empty(L.llama_workspace_bytes(L.OP_BEAM_REORDER_PAGED, _bdims(B, W), L.F32, kv_capacity=128 * P),
+                     dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty(B, W, dtype=t, device="cuda") for t in (torch.int32, torch.int32, torch.float32)] for _ in range(2)]
+    n_cached = _i32([200] * (B * W))
+    pages = np.full((B * W, P), -1, np.int32)
+    for b in range(B):
+        for w in range(W):
+            pages[b * W + w, :2] = 8 * b, 8 * b + 1 + w
+    table, free = _dev(pages), _i32(range(30, n_pages))
+    late_parents, parents = _i32([[3, 3, 0, 1], [2, 2, 2, 2], [0, 1, 2, 3]]), zero.clone()
+    pool = torch.zeros(n_pages, 128, 1, 16, dtype=torch.uint8, device="cuda")
+    got = [(torch.empty_like(n_cached), torch.full_like(table, -7), torch.full_like(n_cached, -7), _i32([0, 0])) for _ in range(2)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def calls():
+        side.wait_stream(torch.cuda.current_stream())
+        L.llama_beam_select(first, scores, None, 0, *outs[0], ws)
+        L.llama_beam_select(first, scores, None, 0, *outs[0], ws)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000)
+            z.copy_(late)
+        torch.cuda.current_stream().wait_stream(side)
+        L.llama_beam_select(z, scores, None, 0, *outs[1], ws)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000)
+            parents.copy_(late_parents)
+        torch.cuda.current_stream().wait_stream(side)
+        n, t, freed, counts = got[1]
+        L.llama_beam_reorder_paged(parents, n_cached, n, table, t, free, n_pages, [pool], [], freed, counts, wr)
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        calls()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (*outs[1], *got[1])]
+    _check_select(late.cpu().numpy().reshape(B, W, V), np.zeros((B, W)), None, 0, W,
+                  (want[0].cpu().numpy(), want[1].cpu().numpy(), want[2].cpu().numpy().astype(np.float64)))
+    assert want[6].tolist() == [0, 0]      # one copy and one dead page, three and three, none
+    assert want[4].cpu().numpy()[:, :2].tolist() == [[0, 4], [0, 3], [0, 1], [0, 2], [8, 11], [8, 9], [8, 10], [8, 12],
+                                                     [16, 17], [16, 18], [16, 19], [16, 20]]
+    g = None
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            calls()
+    for _ in range(5):
+        z.zero_(), parents.zero_()
+        for t in (*outs[1], *got[1]):
+            t.fill_(-7)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            g.replay() if captured else calls()
+        torch.cuda.synchronize()
+        assert _status() == 0
+        for x, y in zip((*outs[1], *got[1]), want):
+            assert torch.equal(x, y)

@@ -509,3 +509,48 @@ def test_calls_on_a_given_stream_and_twice_give_the_same_bits():
     L.llama_rope_append_paged_kv8(_dims(1, 3, 8, 2, 128), None, x, x, pos, slots, None, *cache, stream=s)
     s.synchronize()
     assert _status() == 0 and cache[3][0, 1, 2] == float(R.row_scale(np.max(np.abs(to_f64(x)[2, 1]))))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_attention_behind_a_wait_on_another_stream(captured):
+    """The call before it has finished early, what it reads comes late from another stream: it is waited for."""
+    import torch
+    lengths = [900, 4, 300]
+    c = Cache(lengths, 2, 128, seed=21)
+    cache, table, late = c.dev(), _dev(c.table), _queries(3, 8, 128, 5)
+    dims = _dims(3, 1, 8, 2, 128)
+    ws = torch.empty(L.llama_workspace_bytes(L.OP_GQA_ATTENTION_DECODE_PAGED_KV8, dims, L.BF16, kv_capacity=900),
+                     dtype=torch.uint8, device="cuda")
+    late_pos, q, pos = _i32([899, 3, 299]), torch.zeros_like(late), _i32([0, 0, 0])
+    o = [torch.zeros_like(late) for _ in range(2)]
+    first, main, side = _queries(3, 8, 128, 6), torch.cuda.Stream(), torch.cuda.Stream()
+    early = _i32([500, 1, 2])
+
+    def calls():
+        side.wait_stream(torch.cuda.current_stream())
+        L.llama_gqa_attention_decode_paged_kv8(dims, first, *cache, table, early, 899, o[0], ws)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000)
+            q.copy_(late)
+            pos.copy_(late_pos)
+        torch.cuda.current_stream().wait_stream(side)
+        L.llama_gqa_attention_decode_paged_kv8(dims, q, *cache, table, pos, 899, o[1], ws)
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        calls()
+    torch.cuda.synchronize()
+    want = o[1].clone()
+    _check_attention(c, late, want)
+    g = None
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            calls()
+    for _ in range(5):
+        q.zero_(), pos.zero_(), o[1].fill_(3.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            g.replay() if captured else calls()
+        torch.cuda.synchronize()
+        assert _status() == 0 and torch.equal(o[1], want)
