@@ -434,8 +434,9 @@ int llama_kv_dequantize_paged(const llama_dims* dims, const void* k_codes, const
  *   max_pos: an upper bound of seq_pos (host value; sizes the work split and the workspace,
  *   llama_workspace_bytes(LLAMA_OP_GQA_ATTENTION_DECODE_PAGED_KV8, dims, ..., kv_capacity = max_pos + 1))
  * head_dim 64 or 128, any n_q / n_kv.  Pages may be shared; rows past a sequence's position are never used, whatever
- * they hold.  A NaN among the codes or scales that a query attends to makes its row NaN (and, for head_dim 64, may make
- * that of the KV head beside its own NaN).  o may not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
+ * they hold.  A NaN among the key codes or the scales that a query attends to makes its row NaN (and, for head_dim 64, may
+ * make that of the KV head beside its own NaN), one among the value codes its element.  o may not overlap the inputs;
+ * calls that overlap on the GPU need workspaces of their own.
  * Numerics: scores, softmax statistics and sums in fp32; q and the products of softmax weight and V scale enter
  * the 8-bit tensor-core products as two E4M3 values each (8 significant bits, the second 2^-5 finer than the
  * format's own range), relative to the largest of their row.

@@ -209,14 +209,16 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
   if (warp == BS_WARPS) {   // ------------------------------------------------ producer
     if (VEC && lane == 0) {
       int j = 0;
-      while (next_row_piece(p, walk, all, row, b0, b1, place)) {
+      bool ok = true;
+      while (ok && next_row_piece(p, walk, all, row, b0, b1, place)) {
         if (all && !row_live(p, row)) continue;
         const float* z = p.z + (int64_t)row * p.ld;
         for (int b = b0; b < b1; ++b, ++j) {
           const int st = j % BS_STAGES, e = b * BS_BATCH;
-          if (j >= BS_STAGES && !mbar_wait(&pushed[st], (j / BS_STAGES - 1) & 1, &abort_sh, p.status)) return;
-          if (!in_extent((int64_t)row * p.ld + e, min(BS_BATCH, p.V - e), (int64_t)(rows - 1) * p.ld + p.V)) { abort_sh = 1; return; }
-          const uint32_t bytes = (min(e + BS_BATCH, p.V) - e) / 4 * 16;   // whole vectors; up to three logits behind them are read directly
+          ok = j < BS_STAGES || mbar_wait(&pushed[st], (j / BS_STAGES - 1) & 1, &abort_sh, p.status);
+          if (!ok) break;
+          uint32_t bytes = (min(e + BS_BATCH, p.V) - e) / 4 * 16;   // whole vectors; up to three logits behind them are read directly
+          if (!in_extent((int64_t)row * p.ld + e, min(BS_BATCH, p.V - e), (int64_t)(rows - 1) * p.ld + p.V)) bytes = 0;
           mbar_arrive_expect_tx(&full[st], bytes);
           if (bytes)
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -224,6 +226,8 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
                          : "memory");
         }
       }
+      int no_abort = 0;   // a CTA that gives up does not leave while its copies are on their way
+      for (int k = max(0, j - BS_STAGES); k < j; ++k) mbar_wait(&full[k % BS_STAGES], (k / BS_STAGES) & 1, &no_abort, p.status);
     }
     return;
   }

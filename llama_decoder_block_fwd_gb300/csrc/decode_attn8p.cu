@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
   if (warp == 0) {  // -------------------------------------------------------- TMA producer
     // V(j) is requested one tile after K(j): P V needs it only after S^T and the softmax of its tile
     const int n_sc = min(PACK, p.n_kv - g0);        // heads whose scales there are
-    int tile = 0, v_page = 0;
+    int tile = 0, v_page = 0, k_sent = 0, v_sent = 0;
     bool ok = true;
     auto issue_v = [&](int gt) -> bool {
       const int vs = gt % DP_VSTAGES;
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       if (!box_in(g0 * HD, p.n_kv * HD, (int64_t)v_page * 128, (int64_t)p.n_pages * 128)) { *abort_flag = 1; return false; }
       mbar_arrive_expect_tx(&bars[P_VF + vs], L::F8);
       tma_load_2d(sbase + L::OFF_V8 + vs * L::F8, &p.tmV, &bars[P_VF + vs], g0 * HD, v_page * 128);
+      v_sent = gt + 1;
       return true;
     };
     // the query rows of piece `it` as hi and lo codes, by the whole warp
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
             mbar_arrive_expect_tx(&bars[P_SCF + sc], 2 * bytes);
             bulk_load(dst, p.k_scale + at, bytes, &bars[P_SCF + sc]);
             bulk_load(dst + 1024, p.v_scale + at, bytes, &bars[P_SCF + sc]);
+            k_sent = tile + 1;
             if (tile > 0) ok = issue_v(tile - 1);
           }
         }
@@ -423,7 +425,13 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         if (t == t0 && !(ok = put_q(it))) break;   // behind the piece's first K, which is on its way meanwhile
       }
     }
-    if (ok && tile > 0 && lane == 0) issue_v(tile - 1);
+    if (lane == 0) {
+      if (ok && tile > 0) issue_v(tile - 1);
+      int no_abort = 0;   // a CTA that gives up does not leave while its copies are on their way
+      for (int k = max(0, k_sent - DP_KSTAGES); k < k_sent; ++k) wait_for(&bars[P_KF + k % DP_KSTAGES], (k / DP_KSTAGES) & 1, &no_abort, p.status);
+      for (int k = max(0, k_sent - DP_SSTAGES); k < k_sent; ++k) wait_for(&bars[P_SCF + k % DP_SSTAGES], (k / DP_SSTAGES) & 1, &no_abort, p.status);
+      for (int k = max(0, v_sent - DP_VSTAGES); k < v_sent; ++k) wait_for(&bars[P_VF + k % DP_VSTAGES], (k / DP_VSTAGES) & 1, &no_abort, p.status);
+    }
   } else if (warp == 1) {
     if (lane == 0) {  // ---------------------------------------------------- MMA issuer
       const uint32_t idesc_s = idesc_f8(128, NP);
