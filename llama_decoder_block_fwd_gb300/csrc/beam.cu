@@ -604,7 +604,12 @@ constexpr int BR_THREADS = 256;
 constexpr int BR_MAX_W = (int)kBeamMaxW;
 constexpr int BR_MAX_POOLS = kBeamMaxPools;
 constexpr int BR_CTAS_PER_SM = 3;
-constexpr int BR_DEEP = 4;           // loads of a thread in flight
+constexpr int BR_CTA_VECS = 4096;    // 16-byte vectors that a CTA copies, where there are enough CTAs
+constexpr int BR_BULK_MIN = 512;     // of a CTA's range from which its long runs go by bulk copies
+constexpr int BR_LONG = 256;         // vectors of a long run, at least
+constexpr int BR_CHUNK = 1024;       // vectors of a bulk copy
+constexpr int BR_SLOTS = 3;          // chunks in shared memory,
+constexpr int BR_LAG = 1;            // of which so many more are on their way in when one goes out
 
 struct BeamPool {
   char* base;
@@ -737,18 +742,67 @@ __device__ __forceinline__ void store_vec(const char* src, char* to, int at, int
     for (; at < bytes; at += 4) *reinterpret_cast<uint32_t*>(to + at) = *reinterpret_cast<const uint32_t*>(src + at);
 }
 
+// Long runs by bulk copies through a ring in shared memory, all of it one thread's: chunk i comes into slot i % BR_SLOTS and goes
+// out when BR_LAG later ones have been asked for.
+struct BulkCopies {
+  char* ring;
+  uint64_t* full;
+  struct Out { char* to; uint32_t bytes; } *out;
+  volatile int* abort;
+  unsigned* status;
+  int in = 0, gone = 0;
+  __device__ __forceinline__ bool store_next() {
+    const int st = gone % BR_SLOTS;
+    if (!mbar_wait(&full[st], (gone / BR_SLOTS) & 1, abort, status)) return false;
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                     reinterpret_cast<uint64_t>(out[st].to)), "r"(smem_u32(ring + st * BR_CHUNK * 16)), "r"(out[st].bytes)
+                 : "memory");
+    ++gone;
+    return true;
+  }
+  __device__ __forceinline__ bool copy(const char* src, char* to, uint32_t bytes) {
+    const int st = in % BR_SLOTS;
+    // slot st's last chunk went out with group in - BR_SLOTS, and in - 1 - BR_LAG is the latest
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BR_SLOTS - 1 - BR_LAG) : "memory");
+    out[st] = Out{to, bytes};
+    mbar_arrive_expect_tx(&full[st], bytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(ring + st * BR_CHUNK * 16)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(&full[st]))
+                 : "memory");
+    ++in;
+    return in <= BR_LAG || store_next();
+  }
+  __device__ __forceinline__ void finish() {
+    bool ok = true;
+    while (ok && gone < in) ok = store_next();
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    int no_abort = 0;   // (a CTA that gives up does not leave while its copies are on their way)
+    for (int k = max(0, in - BR_SLOTS); k < in; ++k) mbar_wait(&full[k % BR_SLOTS], (k / BR_SLOTS) & 1, &no_abort, status);
+  }
+};
+
 // Bound by HBM for many copies, by the latency of a few dependent loads for few.  Every CTA sums up the requests' pages
 // taken, pages left over and vectors to copy; entries and freed pages are dealt out by request, and the vectors of
-// all copies, one after the other, are cut into equal ranges, one per CTA.  16 requests of 8 beams, eight layers of 8-bit pages of
-// 8 heads x 128 (149 MB read and written): 33 us with the plan, 22 at a copy's rate; one request of 4 beams over two
-// bf16 layers of 2 heads x 64: 6.5 us.
-// (Contiguous ranges beat chunks in turn, 32-49 us, and 3 CTAs per SM 4 and more: reads and writes of open pages mix.)
+// all copies, one after the other, are cut into equal ranges, one per CTA, where one thread drives bulk copies for the long runs
+// (rows) while the other warps move the short ones (scales).  16 requests of 8 beams, eight layers of 8-bit pages of 8 heads x
+// 128 (149 MB read and written): 27.4 us with the plan, 22 at a copy's rate; through registers, four loads in flight per thread,
+// 34 (the next four on their way before these are stored 36, chunks in turn instead of ranges 32-49); chunks of 4 to 12 KB 28-32,
+// four CTAs 29; two CTAs with a slot more 26.6, but 13.6 instead of 12.3 for 16 requests of 4 beams over four bf16 layers
+// (9.8 at a copy's rate).  One request of 4 beams over two bf16 layers of 2 heads x 64: 6.3 us.
 __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(const __grid_constant__ ReorderParams p) {
   extern __shared__ int64_t v0[];   // [B + 1] first vector of each request; then [2][B + 1]: first page taken, first page freed
   int* t0 = reinterpret_cast<int*>(v0 + p.B + 1);
   int* f0 = t0 + p.B + 1;
   __shared__ int64_t wsum[3][BR_THREADS / 32];
+  __shared__ uint64_t full[BR_SLOTS];
+  __shared__ BulkCopies::Out out[BR_SLOTS];
+  __shared__ volatile int abort_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < BR_SLOTS; ++i) mbar_init(&full[i], 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
   pdl_wait();
   const int per = (p.B + BR_THREADS - 1) / BR_THREADS;
   const int s0 = min(p.B, tid * per), s1 = min(p.B, s0 + per);
@@ -805,57 +859,66 @@ __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(c
     const int mid = (lo + hi) >> 1;
     if (v0[mid] <= x) lo = mid; else hi = mid;
   }
-  int b = lo, i = 0, k = 0;
-  int64_t first = v0[b];   // of copy i's part in pool k
-  while (x < x1) {
-    const int copies = p.found[b].copies;
-    if (i == copies) { ++b; i = 0; continue; }
-    const BeamCopy c = p.copies[(int64_t)b * p.W + i];
-    const int dst = copy_target(p, b, i, p.found[b].dead, t0[b], c.src);
-    for (k = 0; k < p.n_pools && x < x1; ++k) {
-      const BeamPool& q = p.pool[k];
-      const int nv = run_vecs(q, c.rows), bytes = c.rows * q.row_bytes;
-      const int64_t total = (int64_t)q.runs * nv;
-      if (x >= first + total) { first += total; continue; }
-      const int v_from = (int)(x - first), v_to = (int)min(total, x1 - first);
-      const char* src = q.base + (int64_t)c.src * q.page_bytes;
-      char* to = q.base + (int64_t)dst * q.page_bytes;
-      // (a layer holds both pages whole; the last row that is written lies in the last run)
-      const bool in = in_extent((int64_t)max(dst, 0) * q.page_bytes, q.page_bytes, q.layer_bytes) &&
-                      in_extent((int64_t)(q.parts - 1) * 128 * q.row_bytes, bytes, q.page_bytes);
-      if (dst < 0 || !in) {
-      } else if (nv >= BR_THREADS) {   // long runs, one after the other
-        int run = v_from / nv, r0 = v_from - run * nv, layer = run / q.parts, part = run - layer * q.parts;
-        for (int v = v_from; v < v_to;) {
-          const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
-          const int r1 = min(nv, r0 + v_to - v);
-          for (int r = r0 + tid; r < r1; r += BR_THREADS * BR_DEEP) {
-            uint4 w[BR_DEEP];
-#pragma unroll
-            for (int j = 0; j < BR_DEEP; ++j)
-              if (r + j * BR_THREADS < r1 && (r + j * BR_THREADS) * 16 + 16 <= bytes)
-                w[j] = *reinterpret_cast<const uint4*>(src + o + (int64_t)(r + j * BR_THREADS) * 16);
-#pragma unroll
-            for (int j = 0; j < BR_DEEP; ++j)
-              if (r + j * BR_THREADS < r1) store_vec(src + o, to + o, (r + j * BR_THREADS) * 16, bytes, w[j]);
-          }
-          v += r1 - r0;
-          r0 = 0;
-          if (++part == q.parts) { part = 0; ++layer; }
+  // part(q, src, to, nv, bytes, from, n): vectors [from, n) of a copy's runs of nv vectors, `bytes` bytes, in pool q
+  auto walk = [&](auto part) {
+    int64_t first = v0[lo];   // of copy i's vectors in pool k
+    for (int b = lo, i = 0; x < x1;) {
+      const BeamFound f = p.found[b];
+      if (i == f.copies) { ++b; i = 0; continue; }
+      const BeamCopy c = p.copies[(int64_t)b * p.W + i];
+      const int dst = copy_target(p, b, i, f.dead, t0[b], c.src);
+      for (int k = 0; k < p.n_pools && x < x1; ++k) {
+        const BeamPool& q = p.pool[k];
+        const int nv = run_vecs(q, c.rows), bytes = c.rows * q.row_bytes;
+        const int64_t total = (int64_t)q.runs * nv;
+        if (x < first + total) {
+          const int v_from = (int)(x - first), v_to = (int)min(total, x1 - first);
+          // (a layer holds both pages whole; the last row that is written lies in the last run)
+          if (dst >= 0 && in_extent((int64_t)dst * q.page_bytes, q.page_bytes, q.layer_bytes) &&
+              in_extent((int64_t)(q.parts - 1) * 128 * q.row_bytes, bytes, q.page_bytes))
+            part(q, q.base + (int64_t)c.src * q.page_bytes, q.base + (int64_t)dst * q.page_bytes, nv, bytes, v_from, v_to);
+          x = first + v_to;
         }
-      } else {
-        for (int v = v_from + tid; v < v_to; v += BR_THREADS) {
-          const int run = v / nv, layer = run / q.parts, part = run - layer * q.parts, r = (v - run * nv) * 16;
-          const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r + 16 <= bytes) w = *reinterpret_cast<const uint4*>(src + o + r);
-          store_vec(src + o, to + o, r, bytes, w);
-        }
+        first += total;
       }
-      x = first + v_to;
-      first += total;
+      ++i;
     }
-    ++i;
+  };
+  const bool bulk = x1 - x >= BR_BULK_MIN;   // then warp 0 has the long runs and the others the rest
+  if (bulk && warp == 0) {
+    if (lane == 0) {
+      BulkCopies copier{reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(f0 + p.B + 1) + 127) & ~uintptr_t(127)), full, out, &abort_sh, p.status};
+      bool ok = true;
+      walk([&](const BeamPool& q, const char* src, char* to, int nv, int bytes, int v, int v_to) {
+        if (nv < BR_LONG) return;
+        int run = v / nv, r0 = v - run * nv, layer = run / q.parts, part = run - layer * q.parts;
+        while (ok && v < v_to) {
+          const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
+          const int r1 = min(min(nv, r0 + BR_CHUNK), r0 + v_to - v), whole = min(r1, bytes / 16);
+          if (whole > r0) ok = copier.copy(src + o + (int64_t)r0 * 16, to + o + (int64_t)r0 * 16, (whole - r0) * 16);
+          if (whole < r1) store_vec(src + o, to + o, whole * 16, bytes, make_uint4(0, 0, 0, 0));   // the words behind the last whole vector
+          v += r1 - r0;
+          r0 = r1;
+          if (r0 == nv) {
+            r0 = 0;
+            if (++part == q.parts) { part = 0; ++layer; }
+          }
+        }
+      });
+      copier.finish();
+    }
+  } else {
+    const int t = bulk ? tid - 32 : tid, n = bulk ? BR_THREADS - 32 : BR_THREADS;
+    walk([&](const BeamPool& q, const char* src, char* to, int nv, int bytes, int v_from, int v_to) {
+      if (bulk && nv >= BR_LONG) return;
+      for (int v = v_from + t; v < v_to; v += n) {
+        const int run = v / nv, layer = run / q.parts, part = run - layer * q.parts, r = (v - run * nv) * 16;
+        const int64_t o = layer * q.layer_bytes + (int64_t)part * 128 * q.row_bytes;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r + 16 <= bytes) w = *reinterpret_cast<const uint4*>(src + o + r);
+        store_vec(src + o, to + o, r, bytes, w);
+      }
+    });
   }
   // entries of the copies, and the dead pages left over
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -958,10 +1021,9 @@ int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status,
   cudaGetDevice(&dev);
   static bool attr_set[64] = {};
   if (dev < 0 || dev >= 64) return -1;
-  const int per_request = (int)(sizeof(int64_t) + 2 * sizeof(int));
+  auto smem = [](int64_t B) { return (int)((B + 1) * (sizeof(int64_t) + 2 * sizeof(int)) + 128 + BR_SLOTS * BR_CHUNK * 16); };
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(beam_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kPlanMaxSeqs + 1) * per_request) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(beam_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem(kPlanMaxSeqs)) != cudaSuccess)
       return -1;
     attr_set[dev] = true;
   }
@@ -971,9 +1033,9 @@ int launch_beam_reorder(const BeamReorderDesc& d, int num_sms, unsigned* status,
     if (launch_after(beam_plan_kernel, dim3((unsigned)d.B), dim3(BR_THREADS), 0, st, p, pow2) != cudaSuccess) return -1;
   }
   // CTAs for a few thousand vectors each, were every beam but one of each request to copy a whole page
-  const int64_t work = std::max<int64_t>(d.B, (d.B * (d.W - 1) * vecs + 4 * BR_THREADS * BR_DEEP - 1) / (4 * BR_THREADS * BR_DEEP));
+  const int64_t work = std::max<int64_t>(d.B, (d.B * (d.W - 1) * vecs + BR_CTA_VECS - 1) / BR_CTA_VECS);
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(BR_CTAS_PER_SM * num_sms, work));
-  return launch_after(beam_copy_kernel, dim3(grid), dim3(BR_THREADS), (size_t)(d.B + 1) * per_request, st, p) == cudaSuccess ? 0 : -1;
+  return launch_after(beam_copy_kernel, dim3(grid), dim3(BR_THREADS), smem(d.B), st, p) == cudaSuccess ? 0 : -1;
 }
 
 LLAMA_DEFINE_BOUNDS_READER(beam)

@@ -313,6 +313,18 @@ def test_reorder_of_many_requests_and_long_rows():
         assert _status() == 0
 
 
+@pytest.mark.parametrize("bits,n_kv,hd", [(8, 3, 100), (16, 1, 150), (8, 8, 128), (16, 5, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_reorder_of_long_runs_in_many_layers(bits, n_kv, hd, in_place):
+    """Ranges that begin and end inside runs of many kilobytes, rows that are not whole vectors (300 bytes), scales beside them."""
+    b = Beams(5, 4, [[229, 101, 355, 383], [127] * 4, [130, 1, 2, 200], [128, 256, 77, 77], [250] * 4], n_kv, hd, layers=7, bits=bits,
+              seed=hd)
+    parents = [[0, 0, 2, 3], [1, 1, 1, 1], [3, 0, 3, 3], [2, 0, 2, 1], [3, 2, 1, 0]]
+    got = b.run(parents, in_place)
+    assert _status() == 0
+    b.check(parents, got, in_place)
+
+
 def test_reorder_of_open_pages_that_beams_already_share():
     """Beams that start from one prompt with its open page in every row: each but the first gets its own."""
     s = Beams(1, 4, [[300] * 4], seed=2)
