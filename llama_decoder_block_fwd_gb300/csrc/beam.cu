@@ -24,9 +24,9 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
 // n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second
 // kernel joins a request's lists and sums.
-// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 45.0 us, the first kernel 40 cold, 4.2 TB/s: half
-// of its issue slots go to an exponential, a comparison and the sums of each logit, and its pieces start and end
-// with the join of eight warps' candidates.  (Registers loaded ahead instead of the ring 52 us, 4 CTAs per SM 46-60.)  One request
+// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 44.6 us, the first kernel 39.5 cold, 4.1 TB/s.
+// Each further request costs 0.63 us (6.5 TB/s); the rest, some 18 us, are the ranges' starts, the pieces' first batches, whose
+// candidates are many, their ends, and the join.  (Registers loaded ahead instead of the ring 52 us, 4 CTAs per SM 46-60.)  One request
 // of 4 beams x 32000: 10.3 us, two launches and their chains.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
@@ -128,8 +128,26 @@ __device__ __forceinline__ int takers_count(bool v) {
 }
 
 __device__ __forceinline__ bool row_live(const SelectParams& p, int row) {
-  return !(p.finished && __ldg(p.finished + row)) && __ldg(p.scores + row) > -INFINITY;
+  const int done = p.finished ? __ldg(p.finished + row) : 0;
+  return __ldg(p.scores + row) > -INFINITY && !done;
 }
+// a / b for 0 <= a, 0 < b: a 64-bit division costs some hundred instructions, and few calls need one.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// T batches in n ranges, as equal as can be and all over alike: where every row gets a whole number, no range ends inside one.
+// (With the longer ones all in front 8 requests of 4 rows take 17.5 us, not 15.5: a piece costs as much as several batches.)
+struct Ranges {
+  int64_t T;
+  int n;
+  __device__ __forceinline__ int64_t first(int i) const { return quotient(i * T, n); }
+  __device__ __forceinline__ int with(int64_t x) const {   // the range that holds batch x
+    int i = (int)min((int64_t)n - 1, quotient(x * n, T));
+    while (i + 1 < n && first(i + 1) <= x) ++i;
+    while (i > 0 && first(i) > x) --i;
+    return i;
+  }
+};
 // The pieces of a CTA's range: batches [b0, b1) of a row, the row's place among those that are read.
 struct RowWalk { int row, b; int64_t place, left; };
 __device__ __forceinline__ bool next_row_piece(const SelectParams& p, RowWalk& s, bool all, int& row, int& b0, int& b1, int64_t& place) {
@@ -194,8 +212,9 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
   // no more ranges than batches, so that each of them has some
   const int ranges = (int)min((int64_t)gridDim.x, T);
   if ((int)blockIdx.x >= ranges) return;
-  const int64_t x0 = (int64_t)blockIdx.x * T / ranges, x1 = (int64_t)(blockIdx.x + 1) * T / ranges;
-  const int place0 = (int)(x0 / p.nb);
+  const Ranges cuts{T, ranges};
+  const int64_t x0 = cuts.first(blockIdx.x), x1 = cuts.first(blockIdx.x + 1);
+  const int place0 = (int)quotient(x0, p.nb);
   if (!all && first <= place0 && place0 < first + mine) {
     int r = r0, k = first;
     for (;; ++r)
@@ -203,7 +222,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     start = r;
   }
   __syncthreads();
-  RowWalk walk{all ? place0 : start, (int)(x0 % p.nb), place0, x1 - x0};
+  RowWalk walk{all ? place0 : start, (int)(x0 - (int64_t)place0 * p.nb), place0, x1 - x0};
   int row, b0, b1;
   int64_t place;
   if (warp == BS_WARPS) {   // ------------------------------------------------ producer
@@ -426,11 +445,8 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     for (int i = have + n + tid; i < K; i += BS_THREADS)
       if (in) p.keys[slot * K + i] = 0;
     if (b0 == 0 && tid == 0) {   // the row's first piece says how many there are
-      const int64_t last = place * p.nb + p.nb - 1;
-      int c = (int)min((int64_t)ranges - 1, last * ranges / T);
-      while (c + 1 < ranges && (int64_t)(c + 1) * T / ranges <= last) ++c;
-      while (c > 0 && (int64_t)c * T / ranges > last) --c;
-      if (in_extent(row, 1, rows)) p.pieces[row] = RowPieces{(int)slot, c - (int)blockIdx.x + 1};
+      const int last = cuts.with((place + 1) * p.nb - 1);
+      if (in_extent(row, 1, rows)) p.pieces[row] = RowPieces{(int)slot, last - (int)blockIdx.x + 1};
     }
   }
 }
@@ -442,6 +458,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
 constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: the bar leaves n_out of n_out lists, or of fewer all
 constexpr int BM_LISTS = (int)kBeamMaxW + BS_CTAS_PER_SM * 256;   // of a request, at most (256: kMaxSms)
 constexpr int BM_LEAD = 64;
+constexpr int BM_LOADS = 8;   // of a lane at a time
 constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS * (int)(sizeof(int64_t) + 1);
 
 // Doubles as integers that order as they do.
@@ -510,22 +527,22 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
     const int n = p.nb * BS_WARPS;
     float m = -INFINITY, s = 0.f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 32 * 4) {   // 4 loads of a lane at a time
-      float2 v[4];
-      float top4 = -INFINITY;
+    for (int i0 = 0; i0 < n; i0 += 32 * BM_LOADS) {
+      float2 v[BM_LOADS];
+      float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < BM_LOADS; ++k) {
         const int i = i0 + k * 32 + lane;
         v[k] = i < n ? st[i] : make_float2(-INFINITY, 0.f);
-        top4 = fmaxf(top4, v[k].x);
+        top = fmaxf(top, v[k].x);
       }
       float mx;
-      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(top4));
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(top));
       if (mx == -INFINITY) continue;
-      float s4 = 0.f;
+      float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s4 += v[k].y * exp_from(v[k].x, mx);
-      join_sums(m, s, mx, s4);
+      for (int k = 0; k < BM_LOADS; ++k) sum += v[k].y * exp_from(v[k].x, mx);
+      join_sums(m, s, mx, sum);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
