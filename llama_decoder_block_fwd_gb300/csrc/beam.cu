@@ -24,10 +24,10 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
 // n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second
 // kernel joins a request's lists and sums.
-// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 44.6 us, the first kernel 39.5 cold, 4.1 TB/s.
+// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 44.4 us, the first kernel 39.5 cold, 4.1 TB/s.
 // Each further request costs 0.63 us (6.5 TB/s); the rest, some 18 us, are the ranges' starts, the pieces' first batches, whose
 // candidates are many, their ends, and the join.  (Registers loaded ahead instead of the ring 52 us, 4 CTAs per SM 46-60.)  One request
-// of 4 beams x 32000: 10.3 us, two launches and their chains.
+// of 4 beams x 32000: 10.1 us, two launches and their chains.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
 constexpr int BS_PER = 20;                              // logits of a thread in a batch
@@ -496,38 +496,21 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
   __shared__ int64_t bar_sh;
   __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh[2], bar_at;   // first: list of each row, of the request's
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, K = p.K;
-  pdl_wait();
-  pdl_trigger();
-  // kind: 0 no candidates, 1 logits, 2 finished
-  if (tid < 32) {
-    int n = 0;
-    if (lane < p.W) {
-      const int row = b * p.W + lane;
-      const float base = p.scores[row];
-      const bool done = p.finished && p.finished[row];
-      const RowPieces r = p.pieces[row];                 // (set for kind 1 alone)
-      kind[lane] = !(base > -INFINITY) ? 0 : done ? 2 : 1;
-      offset[lane] = base;
-      top[lane] = 0.0;
-      n = kind[lane] == 1 ? r.n : kind[lane] == 2;
-      slot0[lane] = r.slot;
-    }
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    first[lane + 1] = x;
-    if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
+  // kind: 0 no candidates, 1 logits, 2 finished  (the caller's arrays were complete before the first kernel, which triggered past
+  // its own wait)
+  if (tid < p.W) {
+    const int row = b * p.W + tid;
+    const float base = p.scores[row];
+    const int done = p.finished ? p.finished[row] : 0;
+    kind[tid] = !(base > -INFINITY) ? 0 : done ? 2 : 1;
+    offset[tid] = base;
+    top[tid] = 0.0;
   }
   __syncthreads();
-  const int lists = first[p.W];
-  for (int w = 0; w < p.W; ++w)
-    for (int l = first[w] + tid; l < first[w + 1]; l += BS_THREADS) row_of[l] = (uint8_t)w;
-  auto key_of = [&](int l, int k, int w) -> uint64_t {   // entry k of list l, of row w
-    return kind[w] == 1 ? p.keys[(int64_t)(slot0[w] + l - first[w]) * K + k] : k == 0 ? cand_key(0.f, p.pad) : 0;
-  };
+  pdl_wait();
+  pdl_trigger();
+  RowPieces pieces{0, 0};
+  if (tid < p.W && kind[tid] == 1) pieces = p.pieces[b * p.W + tid];   // on its way while the sums are formed
   for (int w = tid >> 5; w < p.W; w += BS_WARPS) {   // a warp per row
     if (kind[w] != 1) continue;
     const float2* st = p.stat + (int64_t)(b * p.W + w) * p.nb * BS_WARPS;
@@ -558,6 +541,25 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
       top[w] = m;
     }
   }
+  if (tid < 32) {
+    const int n = lane >= p.W ? 0 : kind[lane] == 1 ? pieces.n : kind[lane] == 2;
+    if (lane < p.W) slot0[lane] = pieces.slot;
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    first[lane + 1] = x;
+    if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
+  }
+  __syncthreads();
+  const int lists = first[p.W];
+  for (int w = 0; w < p.W; ++w)
+    for (int l = first[w] + tid; l < first[w + 1]; l += BS_THREADS) row_of[l] = (uint8_t)w;
+  auto key_of = [&](int l, int k, int w) -> uint64_t {   // entry k of list l, of row w
+    return kind[w] == 1 ? p.keys[(int64_t)(slot0[w] + l - first[w]) * K + k] : k == 0 ? cand_key(0.f, p.pad) : 0;
+  };
   __syncthreads();
   // First the lists' leading entries, some four times n_out in all: their n_out-th best is a bar.  Then what reaches it, of all
   // entries.  (One loop for both: a kernel this short pays for the code that it runs through once.)
