@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
 // Joins a request's rows: each piece's list is in order, so a candidate below the n_out-th best of the lists' heads is none
 // of the n_out best; the others are ranked against each other.  One CTA per request, a chain of loads and block barriers: 10.8 us
 // cold for 48 requests of 8 beams and 16 kept.  The candidates that the bar leaves are ranked each against all: for 32 beams and 64
-// kept a bar from 64 entries instead of four times n_out left 3000 of them (324 us in all against 87).
+// kept a bar from 64 entries instead of four times n_out left 3000 of them (324 us in all against 85).
 constexpr int BM_MOST = BS_MAX_K * BS_MAX_K;   // candidates at most: the bar leaves n_out of n_out lists, or of fewer all
 constexpr int BM_LISTS = (int)kBeamMaxW + BS_CTAS_PER_SM * 256;   // of a request, at most (256: kMaxSms)
 constexpr int BM_LEAD = 64;
 constexpr int BM_LOADS = 8;   // of a lane at a time
-constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS * (int)(sizeof(int64_t) + 1);
+constexpr int BM_SMEM = BM_MOST * (int)(2 * sizeof(int64_t) + sizeof(int)) + BM_LISTS * (int)(sizeof(int64_t) + sizeof(uint16_t) + 1);
 
 // Doubles as integers that order as they do.
 __device__ __forceinline__ int64_t ordered(double s) {
@@ -490,11 +490,12 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
   uint64_t* key_sh = reinterpret_cast<uint64_t*>(score + BM_MOST);
   int64_t* head_of = reinterpret_cast<int64_t*>(key_sh + BM_MOST);   // the score of a list's best
   int* place = reinterpret_cast<int*>(head_of + BM_LISTS);
-  uint8_t* row_of = reinterpret_cast<uint8_t*>(place + BM_MOST);
+  uint16_t* good = reinterpret_cast<uint16_t*>(place + BM_MOST);     // lists whose best reaches the bar
+  uint8_t* row_of = reinterpret_cast<uint8_t*>(good + BM_LISTS);
   // a row's candidates score (logit - top) + offset, offset its beam's score less the log of its sum of exp(z - top)
   __shared__ double offset[kBeamMaxW], top[kBeamMaxW];
   __shared__ int64_t bar_sh;
-  __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh[2], bar_at;   // first: list of each row, of the request's
+  __shared__ int kind[kBeamMaxW], first[kBeamMaxW + 1], slot0[kBeamMaxW], n_sh[2], n_good, bar_at;   // first: list of each row, of the request's
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, K = p.K;
   // kind: 0 no candidates, 1 logits, 2 finished  (the caller's arrays were complete before the first kernel, which triggered past
   // its own wait)
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
       if (lane >= o) x += y;
     }
     first[lane + 1] = x;
-    if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
+    if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = n_good = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
   }
   __syncthreads();
   const int lists = first[p.W];
@@ -573,11 +574,18 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
     const int at_bar = bar_at, of_each = pass ? K : lead;
     const uint64_t bar_key = at_bar == INT_MAX ? 0 : key_sh[at_bar];
     const int bar_row = at_bar == INT_MAX ? 0 : place[at_bar];
-    __syncthreads();   // (the bar is read before the lists are written again)
+    __syncthreads();   // (the bar is read before the candidates are written again)
+    const bool many = pass && lists * K > BS_THREADS;   // then only lists whose best reaches the bar are walked through
+    if (many) {
+      for (int l = tid; l < lists; l += BS_THREADS)
+        if (head_of[l] >= bar) good[atomicAdd(&n_good, 1)] = (uint16_t)l;
+      __syncthreads();
+    }
+    const int total = (many ? n_good : lists) * of_each;
 #pragma unroll 1
-    for (int i = tid; i < lists * of_each; i += BS_THREADS) {
-      const int l = i / of_each, k = i - l * of_each, w = row_of[l];
-      if (pass && head_of[l] < bar) continue;   // a list whose best does not reach the bar
+    for (int i = tid; i < total; i += BS_THREADS) {
+      const int at = i / of_each, k = i - at * of_each, l = many ? good[at] : at, w = row_of[l];
+      if (pass && head_of[l] < bar) continue;
       const uint64_t key = key_of(l, k, w);
       const double s = key ? ((double)key_logit(key) - top[w]) + offset[w] : -INFINITY;
       const int64_t o = s > -INFINITY ? ordered(s) : BM_NONE;
