@@ -437,9 +437,9 @@ int llama_kv_dequantize_paged(const llama_dims* dims, const void* k_codes, const
  * they hold.  A NaN among the key codes or the scales that a query attends to makes its row NaN (and, for head_dim 64, may
  * make that of the KV head beside its own NaN), one among the value codes its element.  o may not overlap the inputs;
  * calls that overlap on the GPU need workspaces of their own.
- * Numerics: scores, softmax statistics and sums in fp32; q and the products of softmax weight and V scale enter
- * the 8-bit tensor-core products as two E4M3 values each (8 significant bits, the second 2^-5 finer than the
- * format's own range), relative to the largest of their row.
+ * Numerics: scores, softmax statistics and sums in fp32.  q enters the 8-bit tensor-core products as two E4M3 values (a bf16's 8
+ * significant bits down to 2^-15 of the row's largest, an error of 2^-22 of that below), the products of softmax weight and V scale
+ * as three E5M2 values: off by 2^-11 of themselves down to 2^-25 of the row's largest, by 2^-38 of that below.
  * LLAMA_ERR_UNSUPPORTED for another head_dim, n_q > 65536, B > 65535, B n_kv >= 2^24, n_pages >= 2^24, max_pages >= 2^31;
  * LLAMA_ERR_INVALID_ARG for S != 1, other bad dims, n_pages < 1, max_pages < 1, max_pos < 0, max_pos >= 128 * max_pages
  * or 2^24, NULL arrays; LLAMA_ERR_ALIGNMENT for integer arrays not 4-byte or others not 16-byte aligned;

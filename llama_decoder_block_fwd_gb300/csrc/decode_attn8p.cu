@@ -16,9 +16,12 @@
 //   TMA lands them: S^T = K Q^T (M = 128 keys) and O^T += V^T P^T (M = 128 bytes of the row, V as the MN-major operand).
 //   One thread per key does the softmax of its tile; the scales come with the tile by bulk copies, a head's 128
 //   scales of a page being contiguous.
-// Operands.  The other side is E4M3 too, so q and P enter as x = hi + 2^-5 lo, hi = e4m3(x), lo = e4m3(32 (x - hi)): 8
-//   significant bits, and 2^-5 below the format's smallest step for what is small beside its row's largest (the
-//   tail beside one heavy key).  The lo rows ride in the padding of the operand's N = 16 (32 for 16 rows).
+// Operands.  The other side has 8 bits an element too.  q enters as x = hi + 2^-5 lo in E4M3, hi = e4m3(x), lo = e4m3(32 (x - hi)): all
+//   of a bf16's bits down to 2^-15 of the row's largest.  P enters as three E5M2 values, x = a + b/16 + c/256, each the
+//   rounding of what the ones before it leave: off by 2^-11 of x (2^-3 after the first, 2^-4 more with each further one) down to 2^-25
+//   of the row's largest, by 2^-38 of that below.  So a tail of 2^24 small weights beside a heavy one keeps its sum, where
+//   E4M3's few binades lose it (two E4M3 parts: a tail that is 30% of the row, off by 14% of itself).  The further rows ride
+//   in the padding of the operand's N = 16 (P: 32 for 8 rows, 48 for 16).
 // Scales.  A key's scale multiplies its row of S^T.  A value's scale cannot leave the sum over keys, so P holds
 //   w_j = exp(s_j) vs_j, as 2^(s_j + log2 vs_j - m) with m the running maximum of that exponent: the largest
 //   product, not the largest weight, has the format's full precision.  The sum of weights is that of w_j / vs_j in fp32.
@@ -45,12 +48,13 @@ constexpr int DP_KSTAGES = 3;
 constexpr int DP_VSTAGES = 2;
 constexpr int DP_SSTAGES = 4;     // scales
 constexpr int DP_CTAS_PER_SM = 2;
-constexpr uint32_t DP_TMEM_COLS = 128;   // S^T 2 x NP (cols 0..63), O^T NP (cols 64..)
-// O and l keep their reference until a tile's maximum exceeds it by 2 (log2), so w <= 4 before the 2^6 below
-// and w * 2^6 <= 256 stays under E4M3's 448 (the factor cancels in O / l); 32 (x - hi) <= 256 there too.
+constexpr uint32_t DP_TMEM_COLS = 128;   // S^T 2 x NQ (cols 0..63), O^T NP (cols 64..111)
+// O and l keep their reference until a tile's maximum exceeds it by 2 (log2), so w <= 4 before the 2^13 below
+// and w * 2^13 <= 2^15 stays under E5M2's 57344 (the factor cancels in O / l); half a step there is 2^11, so 16 (x - a) <= 2^15 too.
 constexpr float kDpRescaleLog2 = 2.0f;
-constexpr float kDpPScaleLog2 = 6.0f;
-constexpr float kDpLo = 32.0f;
+constexpr float kDpPScaleLog2 = 13.0f;
+constexpr float kDpLo = 32.0f;      // q's second part
+constexpr float kDpStep = 16.0f;    // each further part of P
 
 struct SplitInfo { int b, last; };   // the sequence whose first part is this range's tail (-1: none), the range of its last part
 
@@ -73,13 +77,14 @@ struct DecodeAttn8pParams {   // 128-byte aligned by its tensor maps
 
 struct DpSmem {
   static constexpr uint32_t F8 = 128 * 128;     // one code tile
-  static constexpr uint32_t OPB = 32 * 128;     // q or P operand: up to 32 rows of 128 codes
+  static constexpr uint32_t OPB = 32 * 128;     // q operand: up to 32 rows of 128 codes
+  static constexpr uint32_t PB = 48 * 128;      // P operand
   static constexpr uint32_t SC = 4 * 512;       // scales of a tile: K of two heads, V of two heads
   static constexpr uint32_t OFF_K8 = 0;
   static constexpr uint32_t OFF_V8 = OFF_K8 + DP_KSTAGES * F8;
   static constexpr uint32_t OFF_Q = OFF_V8 + DP_VSTAGES * F8;  // 2 buffers
   static constexpr uint32_t OFF_P = OFF_Q + 2 * OPB;           // 2 buffers
-  static constexpr uint32_t OFF_SC = OFF_P + 2 * OPB;
+  static constexpr uint32_t OFF_SC = OFF_P + 2 * PB;
   static constexpr uint32_t OFF_RED = OFF_SC + DP_SSTAGES * SC;      // [2 groups][3][4][16] floats
   static constexpr uint32_t OFF_QS = OFF_RED + 2 * 3 * 4 * 16 * 4;   // inverse q scales [2][16]
   static constexpr uint32_t OFF_BAR = OFF_QS + 2 * 16 * 4;
@@ -133,11 +138,12 @@ __device__ __forceinline__ float warp_max_dp(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-// Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format 0) and an fp32 accumulator.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn_major = false) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor for kind::f8f6f4 with E4M3 A (format 0), E4M3 or E5M2 B (1) and an fp32 accumulator.
+enum : uint32_t { B_E4M3 = 0, B_E5M2 = 1 };
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t b_format, bool a_mn_major = false) {
+  return (1u << 4) | (b_format << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -151,6 +157,27 @@ __device__ __forceinline__ uint32_t split_fine(float a, float b, uint32_t& lo) {
   const float2 h = e4m3x2_to_f2(hi);
   lo = e4m3x2((a - h.x) * kDpLo, (b - h.y) * kDpLo);
   return hi;
+}
+// Two floats to two E5M2 codes (round to nearest even, saturating): a in the low byte; and back, an E5M2 code being the upper byte of
+// a half.
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
+  return c;
+}
+__device__ __forceinline__ float2 e5m2x2_to_f2(uint32_t c) {
+  const uint32_t h = __byte_perm(c, 0, 0x1404);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// x = p0 + p1 / 16 + p2 / 256 in E5M2 (a's codes in the low bytes).
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t (&p)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    p[k] = e5m2x2(a, b);
+    const float2 h = e5m2x2_to_f2(p[k]);
+    a = (a - h.x) * kDpStep;
+    b = (b - h.y) * kDpStep;
+  }
 }
 // Byte offset of (row n, byte c) in a K-major operand of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128_at(int n, int c) {
@@ -221,7 +248,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
   using L = DpSmem;
   constexpr int HD = 128 / PACK, RH = R / PACK;
   constexpr int SG = dp_groups(R), RT = R / SG, DP_THREADS = dp_threads(SG);   // softmax groups, rows of each
-  constexpr int NP = R <= 8 ? 16 : 32;   // operand rows: hi 0..R-1, lo R..2R-1, zero padding
+  constexpr int NQ = R <= 8 ? 16 : 32;              // q's operand rows: hi 0..R-1, lo R..2R-1, zero padding
+  constexpr int NP = (3 * R + 15) / 16 * 16;        // P's: its parts 0..R-1, R..2R-1, 2R..3R-1, zero padding
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     tma_prefetch_desc(&p.tmV);
   }
   // the padding rows and, of packed heads, the other head's bytes stay zero in the q and P operands
-  for (int i = threadIdx.x; i < (int)(4 * L::OPB) / 16; i += DP_THREADS)
+  for (int i = threadIdx.x; i < (int)(L::OFF_SC - L::OFF_Q) / 16; i += DP_THREADS)
     reinterpret_cast<uint4*>(smem + L::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) { tmem_alloc(tmem_slot, DP_TMEM_COLS); tmem_relinquish(); }
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem;          // S^T buffers: columns 0..NP-1 and NP..2NP-1
+  const uint32_t tS = tmem;          // S^T buffers: columns 0..NQ-1 and NQ..2NQ-1
   const uint32_t tO = tmem + 64;     // O^T: columns 64..64+NP-1
   const uint32_t sbase = smem_u32(smem);
   Pieces it0;
@@ -434,8 +462,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ---------------------------------------------------- MMA issuer
-      const uint32_t idesc_s = idesc_f8(128, NP);
-      const uint32_t idesc_o = idesc_f8(128, NP, /*a_mn_major=*/true);
+      const uint32_t idesc_s = idesc_f8(128, NQ, B_E4M3);
+      const uint32_t idesc_o = idesc_f8(128, NP, B_E5M2, /*a_mn_major=*/true);
       Pieces s = it0;
       // S^T of tile gt, the first of piece it or a later one
       auto issue_s = [&](int gt, int it, bool first) -> bool {
@@ -448,7 +476,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         const uint64_t kd0 = sdesc_sw128(sbase + L::OFF_K8 + st * L::F8, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)   // 32 bytes of the row per step
-          tc_mma_e4m3(tS + sb * NP, kd0 + (uint64_t)(2 * k), qd0 + (uint64_t)(2 * k), idesc_s, k > 0 ? 1u : 0u);
+          tc_mma_f8(tS + sb * NQ, kd0 + (uint64_t)(2 * k), qd0 + (uint64_t)(2 * k), idesc_s, k > 0 ? 1u : 0u);
         tc_commit(&bars[P_SF + sb]);
         tc_commit(&bars[P_KE + st]);
         return true;
@@ -461,10 +489,10 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         tc_fence_after();
         // V^T: M = bytes of the row (MN-major), 8-key groups 1024 bytes apart
         const uint64_t vd0 = sdesc_sw128(sbase + L::OFF_V8 + st * L::F8, 16384, 1024);
-        const uint64_t pd0 = sdesc_sw128(sbase + L::OFF_P + pb * L::OPB, 16, 1024);
+        const uint64_t pd0 = sdesc_sw128(sbase + L::OFF_P + pb * L::PB, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)   // 32 keys per step
-          tc_mma_e4m3(tO, vd0 + (uint64_t)(k * 4096 >> 4), pd0 + (uint64_t)(2 * k), idesc_o, (!first || k > 0) ? 1u : 0u);
+          tc_mma_f8(tO, vd0 + (uint64_t)(k * 4096 >> 4), pd0 + (uint64_t)(2 * k), idesc_o, (!first || k > 0) ? 1u : 0u);
         tc_commit(&bars[P_OD + pb]);
         tc_commit(&bars[P_VE + st]);
         return true;
@@ -500,13 +528,15 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     // scales: of packed heads one for each half of the rows, which a group of two has to itself
     constexpr int NSC = PACK / SG > 1 ? 2 : 1;
     const int sc0 = PACK == 2 && SG == 2 ? sg : 0;
-    // columns of this group's rows: hi and lo side by side (one group), or two blocks of RT
-    constexpr int LD = SG == 1 ? 16 : RT;
-    auto hi_lo = [&](uint32_t base, uint32_t (&hi)[LD], uint32_t (&lo)[LD]) {   // (one group: all 16 columns in hi)
-      tmem_ld_cols<LD>(base + h0 + lane_off, hi);
-      if constexpr (SG == 2) tmem_ld_cols<LD>(base + R + h0 + lane_off, lo);
+    // columns of this group's rows: the parts side by side (one group), or blocks of RT columns R apart
+    constexpr int LD = SG == 1 ? 16 : RT, QL = SG == 1 ? 1 : 2, PL = SG == 1 ? 1 : 3;   // columns of a load, loads of S^T, of O^T
+    auto load = [&](uint32_t base, auto& v) {
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(v) / sizeof(v[0])); ++k) tmem_ld_cols<LD>(base + k * R + h0 + lane_off, v[k]);
       tc_wait_ld();
     };
+    // part k of row i of what was loaded
+    auto at = [](auto& v, int k, int i) -> uint32_t& { return SG == 1 ? v[0][(k * R + i) % LD] : v[k * (SG - 1)][i % LD]; };
     float* red_g = red + sg * 192;
     int tile = 0, it = 0;
     bool ok = true;
@@ -538,16 +568,16 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         mbar_arrive(&bars[P_SCE + ss]);
         if (!wait_for(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
         tc_fence_after();
-        uint32_t hi[LD], lo[LD];
-        hi_lo(tS + sb * NP, hi, lo);
+        uint32_t st[QL][LD];
+        load(tS + sb * NQ, st);
         tc_fence_before();
         mbar_arrive(&bars[P_SFREE + sb]);
         float e[RT];   // log2 of weight * value scale
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const int k = NSC == 2 ? i / RH : 0;
-          const float fine = __uint_as_float(SG == 1 ? hi[(R + i) % LD] : lo[i % LD]);
-          e[i] = valid ? fmaf(fmaf(fine, 1.f / kDpLo, __uint_as_float(hi[i])), qinv[qb * 16 + h0 + i] * ks[k], lvs[k]) : -INFINITY;
+          const float score = fmaf(__uint_as_float(at(st, 1, i)), 1.f / kDpLo, __uint_as_float(at(st, 0, i)));
+          e[i] = valid ? fmaf(score, qinv[qb * 16 + h0 + i] * ks[k], lvs[k]) : -INFINITY;
         }
         float* rbuf = red_g + (tile & 1) * 64;
 #pragma unroll
@@ -571,41 +601,44 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         if (resc) [[unlikely]] {   // the same in all 128 threads of the group, which saw the same maxima
           if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
           tc_fence_after();
-          uint32_t oh[LD], ol[LD];
-          hi_lo(tO, oh, ol);
+          float alpha[RT];
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float tm = tile_max(i);
-            if (!(tm > m_ref[i] + kDpRescaleLog2)) continue;
-            const float alpha = ex2(m_ref[i] - tm);
-            m_ref[i] = tm;
-            lsum[i] *= alpha;
-            oh[i] = __float_as_uint(__uint_as_float(oh[i]) * alpha);
-            uint32_t& fine = SG == 1 ? oh[(R + i) % LD] : ol[i % LD];
-            fine = __float_as_uint(__uint_as_float(fine) * alpha);
+            const bool up = tm > m_ref[i] + kDpRescaleLog2;
+            alpha[i] = up ? ex2(m_ref[i] - tm) : 1.f;
+            if (up) m_ref[i] = tm;
+            lsum[i] *= alpha[i];
           }
-          tmem_st_cols<LD>(tO + h0 + lane_off, oh);
-          if constexpr (SG == 2) tmem_st_cols<LD>(tO + R + h0 + lane_off, ol);
+#pragma unroll
+          for (int k = 0; k < PL; ++k) {
+            uint32_t ot[LD];
+            tmem_ld_cols<LD>(tO + k * R + h0 + lane_off, ot);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < (SG == 1 ? 3 * R : RT); ++i) ot[i] = __float_as_uint(__uint_as_float(ot[i]) * alpha[i % RT]);
+            tmem_st_cols<LD>(tO + k * R + h0 + lane_off, ot);
+          }
           tc_wait_st();
         }
-        // P^T rows: h (hi) and R + h (lo), this thread's key in byte t of each row; two rows are converted at a time
-        uint8_t* pbase = smem + L::OFF_P + pb * L::OPB;
+        // P^T rows h, R + h and 2R + h, this thread's key in byte t of each; two rows are converted at a time
+        uint8_t* pbase = smem + L::OFF_P + pb * L::PB;
 #pragma unroll
         for (int i = 0; i < RT; i += 2) {
           float w[2] = {0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             if (i + j < RT) {
-              w[j] = ex2(e[i + j] - (m_ref[i + j] - kDpPScaleLog2));
+              w[j] = ex2((e[i + j] - m_ref[i + j]) + kDpPScaleLog2);   // (the difference first: large scores keep their digits)
               lsum[i + j] = fmaf(w[j], ivs[NSC == 2 ? (i + j) / RH : 0], lsum[i + j]);
             }
-          uint32_t lo2;
-          const uint32_t hi2 = split_fine(w[0], w[1], lo2);
+          uint32_t part[3];
+          split_weights(w[0], w[1], part);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             if (i + j < RT) {
-              pbase[sw128_at(h0 + i + j, t)] = (uint8_t)(hi2 >> (8 * j));
-              pbase[sw128_at(R + h0 + i + j, t)] = (uint8_t)(lo2 >> (8 * j));
+#pragma unroll
+              for (int k = 0; k < 3; ++k) pbase[sw128_at(k * R + h0 + i + j, t)] = (uint8_t)(part[k] >> (8 * j));
             }
         }
         if (sg == 0 && (tt + 1) * 128 > n_keys) [[unlikely]] {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
@@ -625,8 +658,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       mbar_arrive(&bars[P_QC + qb]);   // the q scales have been read
       if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
       tc_fence_after();
-      uint32_t oh[LD], ol[LD];
-      hi_lo(tO, oh, ol);
+      uint32_t ot[PL][LD];
+      load(tO, ot);
       tc_fence_before();
       mbar_arrive(&bars[P_OFREE]);
       float* lbuf = red_g + 128;
@@ -644,15 +677,15 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       for (int i = 0; i < RT; ++i) {
         const int h = h0 + i;
         const float l = (lbuf[i] + lbuf[16 + i]) + (lbuf[32 + i] + lbuf[48 + i]);
-        const float fine = __uint_as_float(SG == 1 ? oh[(R + i) % LD] : ol[i % LD]);
-        const float ot = fmaf(fine, 1.f / kDpLo, __uint_as_float(oh[i]));
+        const float fine = fmaf(__uint_as_float(at(ot, 2, i)), 1.f / kDpStep, __uint_as_float(at(ot, 1, i)));
+        const float sum = fmaf(fine, 1.f / kDpStep, __uint_as_float(at(ot, 0, i)));
         const bool own = h / RH == t / HD;      // lane t holds byte t of the row: another head's, for half the rows
         if (whole) {
           const int head = head_of(h);
-          const int64_t at = ((int64_t)b * p.n_q + head) * HD + t % HD;
-          if (own && head >= 0 && in_extent(at, 1, (int64_t)p.B * p.n_q * HD)) p.o[at] = f2bf(ot / l);
+          const int64_t to = ((int64_t)b * p.n_q + head) * HD + t % HD;
+          if (own && head >= 0 && in_extent(to, 1, (int64_t)p.B * p.n_q * HD)) p.o[to] = f2bf(sum / l);
         } else if (in_extent(part + h, 1, (int64_t)2 * p.n_ranges * p.groups * R)) {
-          if (own) p.part_o[(part + h) * HD + t % HD] = ot;
+          if (own) p.part_o[(part + h) * HD + t % HD] = sum;
           if (t == 0) p.part_ml[part + h] = make_float2(m_ref[i], l);
         }
       }

@@ -1,0 +1,118 @@
+"""The 8-bit paged cache on the GPU where its values are at the edges of what the calls take: NaN and infinities that are
+attended to, scales over their whole range, long tails of small softmax weights, keys whose bound lies on a scale's border."""
+import numpy as np
+import pytest
+
+import llama_decoder_block_fwd_gb300 as L
+from tests import kv8_paged_ref as R
+from tests.helpers import to_f64
+from tests.test_gpu_kv8_paged import Cache, _append, _at, _attend, _dev, _queries, _status
+
+pytestmark = pytest.mark.gpu
+
+
+def _parts(q, k, v):
+    """R.attend's rows, and the same sums over |v|, which errors of the weights are relative to."""
+    with np.errstate(all="ignore"):
+        return R.attend(q, k, v), R.attend(q, k, np.abs(v))
+
+
+def _tol(ref, size):
+    """Half a bf16 step of the result; a weight enters the product with 2^-11 of itself, its exponent is off by 2^-18
+    (fp32 exponents up to 128 in size, the exponential's own 2^-22), q by 2^-9 of what is 2^-15 below its row's largest:
+    2^-10 of the sum of sizes holds them all."""
+    return 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size
+
+
+def _close(got, q, k, v, heads=None):
+    ref, size = _parts(q, k, v)
+    h = range(len(q)) if heads is None else heads
+    err, tol = np.abs(got - ref), _tol(ref, size)
+    assert np.all(err[h] <= tol[h]), float(np.max(err[h] / tol[h]))
+
+
+# rows of one, four, eight and sixteen heads a tile, packed heads, and a last KV head without its neighbour
+SHAPES = [(2, 2, 128), (8, 2, 128), (16, 2, 128), (32, 2, 128), (5, 5, 64), (12, 3, 64), (32, 4, 64)]
+
+
+# ------------------------------------------------------------------------------------------- tails
+def _tail(n, scores, sink, seed=0):
+    """A cache of one head of 128 whose key j scores scores[j] < 0, the sink's 0, by its scale and a code of -1 in element 0 (query
+    element 0 is 1, the others 0).  Values of ordinary size, those of the sink -1."""
+    c = Cache([n], 1, 8, seed=seed)        # the table
+    rng = np.random.default_rng(seed)
+    codes = np.zeros((c.n_pages, 128, 1, 128), np.uint8)
+    vc = rng.integers(0x30, 0x48, size=codes.shape, dtype=np.uint8)          # 0.5 .. 3.75
+    ks, vs = np.ones((c.n_pages, 1, 128), np.float32), np.ones((c.n_pages, 1, 128), np.float32)
+    pos = np.arange(n)
+    page, row = c.table[0, pos // 128], pos % 128
+    codes[page, row, 0, 0] = 0xB8
+    ks[page, 0, row] = -np.asarray(scores) * np.sqrt(128.0)
+    codes[page[sink], row[sink]] = 0
+    vc[page[sink], row[sink]] = 0xB8
+    c.codes, c.scales = [codes, vc], [ks, vs]
+    return c
+
+
+def _tail_sums(c, pages):
+    """sum of w v, of w |v| and of w over the rows of the given pages, each page's by itself."""
+    s = R.E4M3[c.codes[0][pages, :, 0, 0]] * c.scales[0][pages, 0].astype(np.float64) / np.sqrt(128.0)
+    w = np.exp(s)
+    out = [np.zeros((len(pages), 128)), np.zeros((len(pages), 128)), w.sum(-1)]
+    for i, page in enumerate(pages):
+        v = R.E4M3[c.codes[1][page, :, 0]]
+        out[0][i], out[1][i] = w[i] @ v, w[i] @ np.abs(v)
+    return out
+
+
+def _check_tail(c, n, heads=4, B=1, seqs=None):
+    import torch
+    q = np.zeros((B, heads, 128))
+    q[..., 0] = 1.0
+    got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1] * B, table=seqs, max_pos=n - 1))
+    assert _status() == 0
+    table = c.table[0, :-(-n // 128)]
+    pages, count = np.unique(table, return_counts=True)
+    num, size, den = (np.tensordot(count, x, 1) for x in _tail_sums(c, pages))
+    if n % 128:                                     # what lies behind the last key is nothing
+        last, rows = table[-1], np.arange(n % 128, 128)
+        w = np.exp(R.E4M3[c.codes[0][last, rows, 0, 0]] * c.scales[0][last, 0, rows].astype(np.float64) / np.sqrt(128.0))
+        v = R.E4M3[c.codes[1][last, rows, 0]]
+        num, size, den = num - w @ v, size - w @ np.abs(v), den - w.sum()
+    ref, size = num / den, size / den
+    err = np.abs(got.reshape(-1, 128) - ref)
+    assert np.all(err <= _tol(ref, size)), (float(np.max(err / size)), float(np.max(err / _tol(ref, size))))
+
+
+@pytest.mark.parametrize("n,factor", [(60000, 1e5), (131000, 3e5), (131000, 7e4), (1 << 20, 2e6), (1 << 20, 1.1e7)])
+def test_equal_small_weights_beside_a_heavy_key_keep_their_sum(n, factor):
+    """n keys of weight 1 beside one of weight `factor`: a rounding of the small weights would be the same for all."""
+    c = _tail(n, np.where(np.arange(n) == 77, 0.0, -np.log(factor)), 77)
+    for heads in (1, 4, 8, 16):
+        _check_tail(c, n, heads)
+
+
+@pytest.mark.parametrize("n,factor,sigma", [(131000, 4e6, 2.0), (1 << 20, 4e6, 1.0), (1 << 20, 3e7, 2.0)])
+def test_spread_small_weights_beside_a_heavy_key_keep_their_sum(n, factor, sigma):
+    x = np.minimum(np.random.default_rng(n).normal(size=n) * sigma - np.log(factor), -0.01)
+    x[n // 2] = 0.0
+    _check_tail(_tail(n, x, n // 2), n)
+
+
+@pytest.mark.parametrize("n,factor", [(40000, 1e5), (131000, 3e5), (131000, 1e6), (400000, 4e6)])
+def test_small_weights_keep_their_sum_within_one_cta(n, factor):
+    """As many sequences as there are ranges, all over the same pages, so that a sequence is one CTA's or two's."""
+    B = 320
+    c = _tail(n, np.where(np.arange(n) == 5, 0.0, -np.log(factor)), 5)
+    for heads in (4, 16):
+        _check_tail(c, n, heads, B, np.repeat(c.table, B, 0))
+
+
+def test_small_weights_of_a_very_long_sequence():
+    """2^24 positions, the most that the call takes, over a few pages: the heavy key has half of the row."""
+    n, m = 1 << 24, 32
+    c = _tail(m * 128, np.full(m * 128, -np.log(2.0 ** 24)), 9)
+    pages = c.table[0, :m].copy()
+    order = np.concatenate([[0], np.tile(np.arange(1, m), n // 128 // (m - 1) + 1)])[:n // 128]     # the sink's page once
+    c.table = np.concatenate([pages[order], [-1]])[None].astype(np.int32)
+    _check_tail(c, n)
