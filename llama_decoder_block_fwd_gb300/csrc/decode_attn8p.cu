@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         for (int i = 0; i < RT; ++i) {
           const float tm = tile_max(i);
           if (m_ref[i] == -INFINITY) m_ref[i] = tm;
-          else resc = resc || tm > m_ref[i] + kDpRescaleLog2;
+          else resc = resc || tm - m_ref[i] > kDpRescaleLog2;   // (a sum would round to more than 2 above a large m_ref)
         }
         const int pb = tile & 1;
         if (tile >= 2) {
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float tm = tile_max(i);
-            const bool up = tm > m_ref[i] + kDpRescaleLog2;
+            const bool up = tm - m_ref[i] > kDpRescaleLog2;
             alpha[i] = up ? ex2(m_ref[i] - tm) : 1.f;
             if (up) m_ref[i] = tm;
             lsum[i] *= alpha[i];

@@ -35,11 +35,20 @@ def _close(got, q, k, v, heads=None):
 SHAPES = [(2, 2, 128), (8, 2, 128), (16, 2, 128), (32, 2, 128), (5, 5, 64), (12, 3, 64), (32, 4, 64)]
 
 
+def _blank(lengths, n_kv, hd, seed=0):
+    """A cache with a table and NaN in every row, to be filled in."""
+    c = Cache(lengths, 1, 8, seed=seed)
+    c.n_kv, c.hd = n_kv, hd
+    c.codes = [np.full((c.n_pages, 128, n_kv, hd), 0x7F, np.uint8) for _ in range(2)]
+    c.scales = [np.full((c.n_pages, n_kv, 128), np.nan, np.float32) for _ in range(2)]
+    return c
+
+
 # ------------------------------------------------------------------------------------------- tails
 def _tail(n, scores, sink, seed=0):
     """A cache of one head of 128 whose key j scores scores[j] < 0, the sink's 0, by its scale and a code of -1 in element 0 (query
     element 0 is 1, the others 0).  Values of ordinary size, those of the sink -1."""
-    c = Cache([n], 1, 8, seed=seed)        # the table
+    c = _blank([n], 1, 128, seed)
     rng = np.random.default_rng(seed)
     codes = np.zeros((c.n_pages, 128, 1, 128), np.uint8)
     vc = rng.integers(0x30, 0x48, size=codes.shape, dtype=np.uint8)          # 0.5 .. 3.75
@@ -65,12 +74,8 @@ def _tail_sums(c, pages):
     return out
 
 
-def _check_tail(c, n, heads=4, B=1, seqs=None):
-    import torch
-    q = np.zeros((B, heads, 128))
-    q[..., 0] = 1.0
-    got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1] * B, table=seqs, max_pos=n - 1))
-    assert _status() == 0
+def _tail_row(c, n):
+    """The row and the sum of sizes, by the table's pages."""
     table = c.table[0, :-(-n // 128)]
     pages, count = np.unique(table, return_counts=True)
     num, size, den = (np.tensordot(count, x, 1) for x in _tail_sums(c, pages))
@@ -79,17 +84,26 @@ def _check_tail(c, n, heads=4, B=1, seqs=None):
         w = np.exp(R.E4M3[c.codes[0][last, rows, 0, 0]] * c.scales[0][last, 0, rows].astype(np.float64) / np.sqrt(128.0))
         v = R.E4M3[c.codes[1][last, rows, 0]]
         num, size, den = num - w @ v, size - w @ np.abs(v), den - w.sum()
-    ref, size = num / den, size / den
-    err = np.abs(got.reshape(-1, 128) - ref)
-    assert np.all(err <= _tol(ref, size)), (float(np.max(err / size)), float(np.max(err / _tol(ref, size))))
+    return num / den, size / den
+
+
+def _check_tail(c, n, all_heads=(4,), B=1, seqs=None):
+    import torch
+    ref, size = _tail_row(c, n)
+    for heads in all_heads:
+        q = np.zeros((B, heads, 128))
+        q[..., 0] = 1.0
+        got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1] * B, table=seqs, max_pos=n - 1))
+        assert _status() == 0
+        err = np.abs(got.reshape(-1, 128) - ref)
+        assert np.all(err <= _tol(ref, size)), (float(np.max(err / size)), float(np.max(err / _tol(ref, size))))
 
 
 @pytest.mark.parametrize("n,factor", [(60000, 1e5), (131000, 3e5), (131000, 7e4), (1 << 20, 2e6), (1 << 20, 1.1e7)])
 def test_equal_small_weights_beside_a_heavy_key_keep_their_sum(n, factor):
     """n keys of weight 1 beside one of weight `factor`: a rounding of the small weights would be the same for all."""
     c = _tail(n, np.where(np.arange(n) == 77, 0.0, -np.log(factor)), 77)
-    for heads in (1, 4, 8, 16):
-        _check_tail(c, n, heads)
+    _check_tail(c, n, (1, 4, 8, 16))
 
 
 @pytest.mark.parametrize("n,factor,sigma", [(131000, 4e6, 2.0), (1 << 20, 4e6, 1.0), (1 << 20, 3e7, 2.0)])
@@ -104,8 +118,7 @@ def test_small_weights_keep_their_sum_within_one_cta(n, factor):
     """As many sequences as there are ranges, all over the same pages, so that a sequence is one CTA's or two's."""
     B = 320
     c = _tail(n, np.where(np.arange(n) == 5, 0.0, -np.log(factor)), 5)
-    for heads in (4, 16):
-        _check_tail(c, n, heads, B, np.repeat(c.table, B, 0))
+    _check_tail(c, n, (4, 16), B, np.repeat(c.table, B, 0))
 
 
 def test_small_weights_of_a_very_long_sequence():
@@ -116,3 +129,32 @@ def test_small_weights_of_a_very_long_sequence():
     order = np.concatenate([[0], np.tile(np.arange(1, m), n // 128 // (m - 1) + 1)])[:n // 128]     # the sink's page once
     c.table = np.concatenate([pages[order], [-1]])[None].astype(np.int32)
     _check_tail(c, n)
+
+
+# ------------------------------------------------------------------------------------ large scores
+@pytest.mark.parametrize("n_q,n_kv,hd", [(320, 320, 128), (1240, 310, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 25, 6e7, 2.0 ** 28, 1e18])
+def test_equal_values_come_back_whatever_the_scores(n_q, n_kv, hd, size):
+    """Every value is the same, so the row is that value whatever the weights: the product's weights and those that are summed up
+    agree where scores are so large that a step of fp32 is more than the weights' whole range.  Scores rise from tile to tile."""
+    import torch
+    n = 900
+    c = _blank([n], n_kv, hd, 4)
+    rng = np.random.default_rng(int(np.log2(size)))
+    pos = np.arange(n)
+    page, row = c.table[0, pos // 128], pos % 128
+    c.codes[0][page, row] = 0x00
+    c.codes[0][page, row, :, 0] = 0x38                                  # 1.0, times a scale that makes the score
+    step = np.maximum(2.0 ** -24, 3.0 / size)                           # a few units of the score, or of its last place
+    rise = rng.integers(0, 4, size=(8, n_kv)).cumsum(0)[pos // 128] + 0.25 * rng.random((n, n_kv))
+    c.scales[0][page, :, row] = size * np.sqrt(hd) / 1.4426950408889634 * (1 + step * rise)
+    value = rng.integers(0x30, 0x60, size=(n_kv, hd)).astype(np.uint8)
+    c.codes[1][page, row] = value
+    c.scales[1][page, :, row] = 1.0
+    q = np.zeros((1, n_q, hd))
+    q[..., 0] = 1.0
+    got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1]))
+    assert _status() == 0
+    want = np.repeat(R.E4M3[value], n_q // n_kv, 0)
+    # half a bf16 step, 2^-11 of each weight in the product, 2^-14 for some 900 additions in fp32
+    assert np.all(np.abs(got[0] - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)), float(np.max(np.abs(got[0] - want) / want))
