@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
 #pragma unroll
           for (int k = 0; k < NSC; ++k) {
             ks[k] = scales[k * 128 + t] * p.scale_log2;
-            const float v = fmaxf(scales[256 + k * 128 + t], 7.88860905e-31f);   // 2^-100: a zero scale has a logarithm too
+            const float vs = scales[256 + k * 128 + t];
+            const float v = vs < 7.88860905e-31f ? 7.88860905e-31f : vs;   // 2^-100: a zero scale has a logarithm too; a NaN stays
             lvs[k] = lg2(v);
             ivs[k] = valid ? __fdividef(1.f, v) : 0.f;
           }

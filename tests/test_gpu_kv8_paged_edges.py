@@ -158,3 +158,34 @@ def test_equal_values_come_back_whatever_the_scores(n_q, n_kv, hd, size):
     want = np.repeat(R.E4M3[value], n_q // n_kv, 0)
     # half a bf16 step, 2^-11 of each weight in the product, 2^-14 for some 900 additions in fp32
     assert np.all(np.abs(got[0] - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)), float(np.max(np.abs(got[0] - want) / want))
+
+
+# --------------------------------------------------------------------------------------------- NaN
+@pytest.mark.parametrize("n_q,n_kv,hd", SHAPES)
+@pytest.mark.parametrize("what", ["k code", "v code", "k scale", "v scale"])
+@pytest.mark.parametrize("at", [0, 150, 290])
+def test_a_nan_that_is_attended_to_shows(n_q, n_kv, hd, what, at):
+    """Of KV head 0 of sequence 0, in its first, a middle and its last, partly filled page: a NaN key code or scale makes the
+    head's rows NaN, a NaN value code its element; other heads and the other sequence are as without it."""
+    c = Cache([300, 200], n_kv, hd, seed=at + hd)
+    q = _queries(2, n_q, hd, n_q)
+    qf, clean = to_f64(q), [c.rows(b) for b in range(2)]
+    page, row = c.table[0, at // 128], at % 128
+    if what.endswith("code"):
+        c.codes[what[0] == "v"][page, row, 0, 5] = 0x7F
+    else:
+        c.scales[what[0] == "v"][page, 0, row] = np.nan
+    got = to_f64(_attend(c, q, [299, 199]))
+    assert _status() == 0
+    r = n_q // n_kv
+    _close(got[1], qf[1], *clean[1])
+    rest = list(range(2 * r if hd == 64 else r, n_q))        # of two heads of 64 side by side the other may be NaN too
+    if rest:
+        _close(got[0], qf[0], *clean[0], rest)
+    if what == "v code":
+        assert np.all(np.isnan(got[0, :r, 5]))
+        ref, size = _parts(qf[0], *clean[0])
+        keep = np.arange(hd) != 5
+        assert np.all(np.abs(got[0, :r] - ref[:r])[:, keep] <= _tol(ref, size)[:r][:, keep])
+    else:
+        assert np.all(np.isnan(got[0, :r]))
