@@ -24,7 +24,11 @@
 //   in the padding of the operand's N = 16 (P: 32 for 8 rows, 48 for 16).
 // Scales.  A key's scale multiplies its row of S^T.  A value's scale cannot leave the sum over keys, so P holds
 //   w_j = exp(s_j) vs_j, as 2^(s_j + log2 vs_j - m) with m the running maximum of that exponent: the largest
-//   product, not the largest weight, has the format's full precision.  The sum of weights is that of w_j / vs_j in fp32.
+//   product, not the largest weight, has the format's full precision.  The weights themselves, for their sum, are exponentials of
+//   their own against the same m, 2^(s_j - m): where value scales lie far apart a key of small values may have most of the
+//   weight.  For scales of 2^-100 .. 2^100 the largest weight lies in 2^-100 .. 2^102, so that 2^24 of them, and twice that, are
+//   finite in fp32, and what is 2^-49 of the largest is still there (the exponential keeps subnormal results).  Sums are brought
+//   to a new m by its square root twice, since 2^(m - m') may be nothing where the sum is large.
 // Split.  The pages of all sequences, one after the other, are cut into equal ranges; range i of head group g is CTA
 //   i * groups + g, so the CTAs that run side by side read all heads of the same pages (a page's rows are contiguous
 //   over heads).  A sequence inside one range is finished there; of one that a cut goes through, each range leaves a part
@@ -50,9 +54,11 @@ constexpr int DP_SSTAGES = 4;     // scales
 constexpr int DP_CTAS_PER_SM = 2;
 constexpr uint32_t DP_TMEM_COLS = 128;   // S^T 2 x NQ (cols 0..63), O^T NP (cols 64..111)
 // O and l keep their reference until a tile's maximum exceeds it by 2 (log2), so w <= 4 before the 2^13 below
-// and w * 2^13 <= 2^15 stays under E5M2's 57344 (the factor cancels in O / l); half a step there is 2^11, so 16 (x - a) <= 2^15 too.
+// and w * 2^13 <= 2^15 stays under E5M2's 57344 (kDpOut takes the factors out of O / l); half a step there is 2^11, so 16 (x - a) <= 2^15 too.
 constexpr float kDpRescaleLog2 = 2.0f;
 constexpr float kDpPScaleLog2 = 13.0f;
+constexpr float kDpLScaleLog2 = 1.0f;                        // l's weights are 2^1 2^(s - m)
+constexpr float kDpOut = 1.f / 4096.f;                       // O / l to the row: 2^(1 - 13)
 constexpr float kDpLo = 32.0f;      // q's second part
 constexpr float kDpStep = 16.0f;    // each further part of P
 
@@ -201,6 +207,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_full(float x) {   // with subnormal results
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float lg2(float x) {
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         const int sb = tile & 1, ss = tile % DP_SSTAGES;
         const bool valid = tt * 128 + t < n_keys;
         if (!wait_for(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
-        float ks[NSC], lvs[NSC], ivs[NSC];
+        float ks[NSC], lvs[NSC];
         {
           const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC) + sc0 * 128;
 #pragma unroll
@@ -562,8 +573,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
             ks[k] = scales[k * 128 + t] * p.scale_log2;
             const float vs = scales[256 + k * 128 + t];
             const float v = vs < 7.88860905e-31f ? 7.88860905e-31f : vs;   // 2^-100: a zero scale has a logarithm too; a NaN stays
-            lvs[k] = lg2(v);
-            ivs[k] = valid ? __fdividef(1.f, v) : 0.f;
+            lvs[k] = valid ? lg2(v) : 0.f;
           }
         }
         mbar_arrive(&bars[P_SCE + ss]);
@@ -607,9 +617,10 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
           for (int i = 0; i < RT; ++i) {
             const float tm = tile_max(i);
             const bool up = tm - m_ref[i] > kDpRescaleLog2;
-            alpha[i] = up ? ex2(m_ref[i] - tm) : 1.f;
+            const float half = up ? ex2(0.5f * (m_ref[i] - tm)) : 1.f;
+            alpha[i] = half * half;
             if (up) m_ref[i] = tm;
-            lsum[i] *= alpha[i];
+            lsum[i] = lsum[i] * half * half;
           }
 #pragma unroll
           for (int k = 0; k < PL; ++k) {
@@ -630,8 +641,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             if (i + j < RT) {
-              w[j] = ex2((e[i + j] - m_ref[i + j]) + kDpPScaleLog2);   // (the difference first: large scores keep their digits)
-              lsum[i + j] = fmaf(w[j], ivs[NSC == 2 ? (i + j) / RH : 0], lsum[i + j]);
+              const float d = e[i + j] - m_ref[i + j];   // (first: large scores keep their digits)
+              w[j] = ex2(d + kDpPScaleLog2);
+              lsum[i + j] += ex2_full(d - (lvs[NSC == 2 ? (i + j) / RH : 0] - kDpLScaleLog2));
             }
           uint32_t part[3];
           split_weights(w[0], w[1], part);
@@ -684,7 +696,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         if (whole) {
           const int head = head_of(h);
           const int64_t to = ((int64_t)b * p.n_q + head) * HD + t % HD;
-          if (own && head >= 0 && in_extent(to, 1, (int64_t)p.B * p.n_q * HD)) p.o[to] = f2bf(sum / l);
+          if (own && head >= 0 && in_extent(to, 1, (int64_t)p.B * p.n_q * HD)) p.o[to] = f2bf(sum / l * kDpOut);
         } else if (in_extent(part + h, 1, (int64_t)2 * p.n_ranges * p.groups * R)) {
           if (own) p.part_o[(part + h) * HD + t % HD] = sum;
           if (t == 0) p.part_ml[part + h] = make_float2(m_ref[i], l);
@@ -701,7 +713,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
   }
 }
 
-// Joins the parts of the sequences that cuts go through: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  Block (x, group, z):
+// Joins the parts of the sequences that cuts go through: o = kDpOut sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i (the l_i by square
+// roots, see Scales above).  Block (x, group, z):
 // RB rows of sequence x, whose place among the ranges it finds from the lengths while the first kernel still runs; where there
 // are more sequences than ranges, of the sequence whose first part is range x's tail.  The latency of its dependent loads is what
 // it costs: a lane has one part's statistics, and the parts' rows come four elements per lane, eight rows' loads in flight.  Up to
@@ -762,12 +775,12 @@ __global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_con
       float top = ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m2 = fmaxf(m, top), a = m > -INFINITY ? exp2f(m - m2) : 0.f;
-      l *= a;
+      const float m2 = fmaxf(m, top), h0 = m > -INFINITY ? exp2f(0.5f * (m - m2)) : 0.f, a = h0 * h0;
+      l = l * h0 * h0;
       acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
       m = m2;
-      const float w = mine < n ? exp2f(ml.x - m) : 0.f;
-      l += w * ml.y;
+      const float half = mine < n ? exp2f(0.5f * (ml.x - m)) : 0.f, w = half * half;
+      l += ml.y * half * half;
       for (int j0 = 0; j0 < cnt; j0 += 8) {
         float4 v[8];
 #pragma unroll
@@ -790,7 +803,7 @@ __global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_con
   auto store = [&](int head, float l, const float4& acc) {
     const int64_t at = ((int64_t)s.b * p.n_q + head) * p.hd + lane * 4;
     if (in && in_extent(at, 4, (int64_t)p.B * p.n_q * p.hd))
-      *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l, acc.y / l), pack_bf2(acc.z / l, acc.w / l));
+      *reinterpret_cast<uint2*>(p.o + at) = make_uint2(pack_bf2(acc.x / l * kDpOut, acc.y / l * kDpOut), pack_bf2(acc.z / l * kDpOut, acc.w / l * kDpOut));
   };
   float m, l;
   float4 acc;
@@ -814,9 +827,9 @@ __global__ void __launch_bounds__(32 * NW) decode_join8p_kernel(const __grid_con
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
       l = 0.f;
       for (int w = 0; w < min(NW, n); ++w) {       // (warps past n have no parts)
-        const float a = exp2f(mx[w] - M);
+        const float half = exp2f(0.5f * (mx[w] - M)), a = half * half;
         const float4 v = sum[w][lane];
-        l = fmaf(a, ls[w], l);
+        l += ls[w] * half * half;
         acc.x = fmaf(a, v.x, acc.x); acc.y = fmaf(a, v.y, acc.y); acc.z = fmaf(a, v.z, acc.z); acc.w = fmaf(a, v.w, acc.w);
       }
       store(head, l, acc);

@@ -189,3 +189,89 @@ def test_a_nan_that_is_attended_to_shows(n_q, n_kv, hd, what, at):
         assert np.all(np.abs(got[0, :r] - ref[:r])[:, keep] <= _tol(ref, size)[:r][:, keep])
     else:
         assert np.all(np.isnan(got[0, :r]))
+
+
+# ------------------------------------------------------------------------------------------ scales
+def _with_scales(lengths, n_kv, hd, exps, seed=0, zero_rows=False):
+    """Random codes of sizes 1 to 15, value scales 2^exps[b][position]; zero_rows: rows at 2^-100 are zeros."""
+    c = _blank(lengths, n_kv, hd, seed)
+    rng = np.random.default_rng(seed)
+    for b, n in enumerate(lengths):
+        pos = np.arange(n)
+        page, row = c.table[b, pos // 128], pos % 128
+        e = np.broadcast_to(np.asarray(exps[b], np.float64).reshape(n, -1), (n, n_kv))
+        codes = rng.integers(0x38, 0x57, size=(n, n_kv, hd), dtype=np.uint8) + np.uint8(128) * rng.integers(0, 2, size=(n, n_kv, hd), dtype=np.uint8)
+        if zero_rows:
+            codes[e == -100] = 0
+        c.codes[0][page, row] = rng.integers(0, 0x3C, size=codes.shape, dtype=np.uint8) + np.uint8(128) * rng.integers(0, 2, size=codes.shape, dtype=np.uint8)
+        c.scales[0][page, :, row] = 2.0 ** rng.integers(-2, 2, size=(n, n_kv))
+        c.codes[1][page, row] = codes
+        c.scales[1][page, :, row] = 2.0 ** e
+    return c
+
+
+PAIRS = [(40, -100, False), (70, -70, False), (100, -100, False), (66, -66, False), (20, -100, False), (40, -100, True),
+         (100, -100, True), (20, -100, True)]
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd", [(4, 1, 128), (16, 1, 128), (8, 2, 64), (32, 2, 64)])
+@pytest.mark.parametrize("hi,lo,zero_rows", PAIRS)
+def test_value_scales_far_apart_leave_the_weights_alone(n_q, n_kv, hd, hi, lo, zero_rows):
+    """Two kinds of keys of equal scores: what the smaller values add to the sum of weights stays, within a tile, from tile to
+    tile in either order, and between the parts of a sequence."""
+    lengths = [2, 100, 256, 256, 700]
+    even = lambda n: np.where(np.arange(n) % 2, hi, lo)
+    exps = [even(2), np.where(np.arange(100) < 90, lo, hi), np.where(np.arange(256) < 128, hi, lo),
+            np.where(np.arange(256) < 128, lo, hi), even(700)]
+    c = _with_scales(lengths, n_kv, hd, exps, seed=hi, zero_rows=zero_rows)
+    import torch
+    q = torch.zeros(len(lengths), n_q, hd, dtype=torch.bfloat16, device="cuda")       # every key scores 0
+    got = to_f64(_attend(c, q, [n - 1 for n in lengths]))
+    assert _status() == 0
+    for b in range(len(lengths)):
+        _close(got[b], np.zeros((n_q, hd)), *c.rows(b))
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd", [(320, 320, 128), (310, 310, 64)])
+@pytest.mark.parametrize("rising", [False, True])
+def test_value_scales_far_apart_from_tile_to_tile_of_one_cta(n_q, n_kv, hd, rising):
+    """With this many heads a sequence's tiles are one CTA's, which has to bring its sums to a new reference."""
+    n = 400
+    e = np.linspace(-100, 100, 4)[np.arange(n) // 128]
+    c = _with_scales([n], n_kv, hd, [e if rising else -e], seed=3)
+    import torch
+    q = torch.zeros(1, n_q, hd, dtype=torch.bfloat16, device="cuda")
+    got = to_f64(_attend(c, q, [n - 1]))
+    assert _status() == 0
+    _close(got[0], np.zeros((n_q, hd)), *c.rows(0))
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd", SHAPES)
+def test_value_scales_over_their_whole_range(n_q, n_kv, hd):
+    """A scale anywhere in 2^-100 .. 2^100 for each key and head, and scores that differ."""
+    rng = np.random.default_rng(hd + n_q)
+    lengths = [1, 129, 900, 5000]
+    c = _with_scales(lengths, n_kv, hd, [rng.integers(-100, 101, size=(n, n_kv)) for n in lengths], seed=n_q)
+    q = _queries(len(lengths), n_q, hd, n_q, 1.0)
+    got = to_f64(_attend(c, q, [n - 1 for n in lengths]))
+    assert _status() == 0
+    for b in range(len(lengths)):
+        _close(got[b], to_f64(q)[b], *c.rows(b))
+
+
+def test_heavy_keys_of_zero_values():
+    """A key with nearly all the weight and a row of zeros (scale 2^-100) beside large values: the row is small, not large."""
+    n, hd = 300, 128
+    for hi, score in ((0, 20.0), (20, 30.0), (100, 60.0)):
+        c = _with_scales([n], 1, hd, [np.where(np.arange(n) == 140, -100, hi)], seed=hi, zero_rows=True)
+        pos = np.arange(n)
+        page, row = c.table[0, pos // 128], pos % 128
+        c.codes[0][page, row] = 0
+        c.codes[0][c.table[0, 1], 12, 0, 0] = 0x38            # 1.0, times a scale that makes the score
+        c.scales[0][page, :, row] = score * np.sqrt(hd) / 4.0
+        q = np.zeros((1, 4, hd))
+        q[0, :, 0] = 4.0
+        import torch
+        got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1]))
+        assert _status() == 0
+        _close(got[0], q[0], *c.rows(0))
