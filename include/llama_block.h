@@ -437,6 +437,7 @@ int llama_kv_dequantize_paged(const llama_dims* dims, const void* k_codes, const
  * they hold.  A NaN among the key codes or the scales that a query attends to makes its row NaN (and, for head_dim 64, may
  * make that of the KV head beside its own NaN), one among the value codes its element.  o may not overlap the inputs;
  * calls that overlap on the GPU need workspaces of their own.
+ * An infinity or a NaN in a row of q makes that head's row NaN.  Scores have to be finite in fp32.
  * Numerics: scores, softmax statistics and sums in fp32.  q enters the 8-bit tensor-core products as two E4M3 values (a bf16's 8
  * significant bits down to 2^-15 of the row's largest, an error of 2^-22 of that below), the products of softmax weight and V scale
  * as three E5M2 values: off by 2^-11 of themselves down to 2^-25 of the row's largest, by 2^-38 of that below.

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         // a power of two per row: amax * qs in [128, 256)
         const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
         const int up = min(max(7 - ex, -126), 126);
-        const float qs = exp2_int(up);
+        const float qs = ex > 127 ? __uint_as_float(0x7FC00000u) : exp2_int(up);   // an infinity makes the row NaN, as its scores are
         if (c < NCH) {
           const int d = c % VH * 8 + h / RH * HD;
           uint32_t hi[4], lo[4];

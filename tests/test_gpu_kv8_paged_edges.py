@@ -191,6 +191,26 @@ def test_a_nan_that_is_attended_to_shows(n_q, n_kv, hd, what, at):
         assert np.all(np.isnan(got[0, :r]))
 
 
+@pytest.mark.parametrize("n_q,n_kv,hd", SHAPES)
+@pytest.mark.parametrize("x", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("zero_keys", [False, True])
+def test_a_query_that_is_not_finite_makes_its_row_nan(n_q, n_kv, hd, x, zero_keys):
+    """inf times the keys is inf, -inf or, where the keys are zero, NaN, and the softmax of each is NaN: its own row, no other."""
+    import torch
+    c = Cache([300, 7], n_kv, hd, seed=hd)
+    if zero_keys:
+        c.codes[0][..., hd - 1] = 0
+    qf = np.random.default_rng(n_q).normal(size=(2, n_q, hd))
+    clean = to_f64(_dev(qf, torch.bfloat16))
+    qf[0, n_q - 1, hd - 1] = x
+    got = to_f64(_attend(c, _dev(qf, torch.bfloat16), [299, 6]))
+    assert _status() == 0
+    assert np.all(np.isnan(got[0, n_q - 1]))
+    if n_q > 1:
+        _close(got[0], clean[0], *c.rows(0), list(range(n_q - 1)))
+    _close(got[1], clean[1], *c.rows(1))
+
+
 # ------------------------------------------------------------------------------------------ scales
 def _with_scales(lengths, n_kv, hd, exps, seed=0, zero_rows=False):
     """Random codes of sizes 1 to 15, value scales 2^exps[b][position]; zero_rows: rows at 2^-100 are zeros."""
