@@ -392,9 +392,11 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         w[j] = head >= 0 ? *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.n_q + head) * HD + c % VH * 8)
                          : make_uint4(0, 0, 0, 0);
       }
-      // the buffer is free once the MMAs of piece it - 2 have read it and the softmax warps its scales
-      if (!wait_for(&bars[P_QE + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
-      if (!wait_for(&bars[P_QC + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status)) return false;
+      // the buffer is free once the MMAs of piece it - 2 have read it and the softmax warps its scales; the lanes go on together or
+      // not at all (the row maxima are the whole warp's)
+      const bool free = wait_for(&bars[P_QE + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status) &&
+                        wait_for(&bars[P_QC + qb], ((it >> 1) & 1) ^ 1, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, free)) return false;
       uint8_t* qop = smem + L::OFF_Q + qb * L::OPB;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -532,6 +534,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       wait_for(&bars[P_DRAIN], 0, &no_abort, p.status);
     }
   } else {  // ------------------------------------------------------------ softmax warps
+    // A wait that is given up (another one then was, and the rows are undefined) changes nothing of a thread's way: the threads of a
+    // group meet at its barrier and in shuffles, so one that left would hold up the others for good.  After the abort no wait
+    // lasts, and the tiles that are left are gone through in a moment.
     const int sg = (warp - 2) >> 2, qw = warp & 3;   // a warp reaches TMEM lanes 32 * (warp % 4) ..
     const int t = qw * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qw * 32) << 16;
@@ -550,11 +555,11 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
     auto at = [](auto& v, int k, int i) -> uint32_t& { return SG == 1 ? v[0][(k * R + i) % LD] : v[k * (SG - 1)][i % LD]; };
     float* red_g = red + sg * 192;
     int tile = 0, it = 0;
-    bool ok = true;
     Pieces s = it0;
-    for (; ok && next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
+    auto await = [&](int bar, int parity) { wait_for(&bars[bar], (uint32_t)parity, abort_flag, p.status); };
+    for (; next_piece(p, s, b, t0, t1, nt, n_keys); ++it) {
       const int qb = it & 1;
-      if (!wait_for(&bars[P_QR + qb], (it >> 1) & 1, abort_flag, p.status)) break;
+      await(P_QR + qb, (it >> 1) & 1);
       float m_ref[RT], lsum[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
       for (int tt = t0; tt < t1; ++tt, ++tile) {
         const int sb = tile & 1, ss = tile % DP_SSTAGES;
         const bool valid = tt * 128 + t < n_keys;
-        if (!wait_for(&bars[P_SCF + ss], (tile / DP_SSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+        await(P_SCF + ss, (tile / DP_SSTAGES) & 1);
         float ks[NSC], lvs[NSC];
         {
           const float* scales = reinterpret_cast<const float*>(smem + L::OFF_SC + ss * L::SC) + sc0 * 128;
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
           }
         }
         mbar_arrive(&bars[P_SCE + ss]);
-        if (!wait_for(&bars[P_SF + sb], (tile >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+        await(P_SF + sb, (tile >> 1) & 1);
         tc_fence_after();
         uint32_t st[QL][LD];
         load(tS + sb * NQ, st);
@@ -606,11 +611,9 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
           else resc = resc || tm - m_ref[i] > kDpRescaleLog2;   // (a sum would round to more than 2 above a large m_ref)
         }
         const int pb = tile & 1;
-        if (tile >= 2) {
-          if (!wait_for(&bars[P_OD + pb], ((tile - 2) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
-        }
+        if (tile >= 2) await(P_OD + pb, ((tile - 2) >> 1) & 1);
         if (resc) [[unlikely]] {   // the same in all 128 threads of the group, which saw the same maxima
-          if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          await(P_OD + ((tile - 1) & 1), ((tile - 1) >> 1) & 1);
           tc_fence_after();
           float alpha[RT];
 #pragma unroll
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         }
         if (sg == 0 && (tt + 1) * 128 > n_keys) [[unlikely]] {   // rows behind the last key may hold anything, NaN codes too: zeros for the product
           const int vs = tile % DP_VSTAGES;
-          if (!wait_for(&bars[P_VF + vs], (tile / DP_VSTAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+          await(P_VF + vs, (tile / DP_VSTAGES) & 1);
           if (!valid) {
             uint4* vrow = reinterpret_cast<uint4*>(smem + L::OFF_V8 + vs * L::F8 + t * 128);
 #pragma unroll
@@ -667,9 +670,8 @@ __global__ void __launch_bounds__(dp_threads(dp_groups(R)), DP_CTAS_PER_SM) deco
         tc_fence_before();
         mbar_arrive(&bars[P_PF + pb]);
       }
-      if (!ok) break;
       mbar_arrive(&bars[P_QC + qb]);   // the q scales have been read
-      if (!wait_for(&bars[P_OD + ((tile - 1) & 1)], ((tile - 1) >> 1) & 1, abort_flag, p.status)) { ok = false; break; }
+      await(P_OD + ((tile - 1) & 1), ((tile - 1) >> 1) & 1);
       tc_fence_after();
       uint32_t ot[PL][LD];
       load(tO, ot);

@@ -1,0 +1,31 @@
+"""Waits that are given up: what the sources have to keep to, so that threads which meet at barriers and in shuffles give up
+together or not at all (a thread that leaves alone holds the others up for good).  Read from the sources: no GPU is used, and
+none is made to wait."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "llama_decoder_block_fwd_gb300", "csrc")
+
+
+def _code(name):
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", text), text
+
+
+def test_softmax_threads_of_the_8_bit_paged_attention_never_leave_alone():
+    """Their loop runs over the range's tiles, whatever a wait says: no wait's result decides on anything."""
+    _, text = _code("decode_attn8p.cu")
+    role = text[text.index("- softmax warps"):text.index("// Joins the parts")]
+    role = re.sub(r"//[^\n]*", "", role)
+    assert role.count("softmax_sync_dp(") == 2 and "warp_max_dp(" in role       # (what they meet in is there)
+    assert not re.search(r"\bbreak\b|\bgoto\b|\bok\b", role)
+    assert not re.search(r"(if|while|&&|\|\||=|return)\s*\(?\s*!?\s*(wait_for|mbar_wait)", role)
+
+
+def test_loading_warp_of_the_8_bit_paged_attention_gives_up_as_one():
+    """Its lanes convert q together, so each lane's waits there are put to a vote before the shuffles."""
+    code, _ = _code("decode_attn8p.cu")
+    put_q = code[code.index("auto put_q"):code.index("int it = 0;")]
+    waits = put_q.index("wait_for("), put_q.rindex("wait_for(")
+    assert "return false" not in put_q[:waits[1]] and put_q.index("__all_sync(0xffffffffu, free)") > waits[1]
+    assert put_q.index("__shfl_xor_sync") > put_q.index("__all_sync")
