@@ -119,14 +119,6 @@ __device__ __forceinline__ float warp_nth(float v, int n) {
   }
 }
 
-// The 256 threads that take the logits.
-__device__ __forceinline__ void takers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ int takers_count(bool v) {
-  int n;
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.popc.u32 %0, 1, 256, p;\n\t}" : "=r"(n) : "r"((int)v) : "memory");
-  return n;
-}
-
 __device__ __forceinline__ bool row_live(const SelectParams& p, int row) {
   const int done = p.finished ? __ldg(p.finished + row) : 0;
   return __ldg(p.scores + row) > -INFINITY && !done;
@@ -174,7 +166,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
   uint64_t* list = reinterpret_cast<uint64_t*>(bs_smem_raw + (VEC ? BS_STAGES * BS_BATCH * 4 : 0));   // candidates that wait
   uint64_t *best = list + room, *other = best + K;                                                     // the best of before
   __shared__ uint64_t full[BS_STAGES], pushed[BS_STAGES];   // a batch has landed; every warp has read it and pushed its candidates
-  __shared__ int n_sh, cnt[BS_STAGES], wsum[BS_WARPS + 1], start;
+  __shared__ int n_sh, cnt[BS_STAGES], votes[3], wsum[BS_WARPS + 1], start;
   __shared__ volatile int abort_sh;
   __shared__ float red[BS_WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = p.B * p.W;
@@ -184,6 +176,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       mbar_init(&pushed[i], BS_WARPS);
       cnt[i] = 0;
     }
+    votes[0] = votes[1] = votes[2] = 0;
     abort_sh = 0;
     fence_mbar_init();
   }
@@ -257,6 +250,21 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
     }
     return;
   }
+  // The takers' warps meet at one_gave_up alone: false from meet, and from what calls it, ends all of them.  A warp of which a
+  // lane's wait ran out goes there with give_up.
+  auto meet = []() -> bool { return !one_gave_up<1, BS_THREADS>(false); };
+  auto give_up = []() -> bool { one_gave_up<1, BS_THREADS>(true); return false; };
+  int n_votes = 0;
+  // The takers for which v holds.  Count i is votes[i % 3]; the next one's is cleared by the time that everyone is here.
+  auto count = [&](bool v, int& c) -> bool {
+    const int i = n_votes++ % 3;
+    const unsigned mask = __ballot_sync(0xffffffffu, v);
+    if (tid == 0) votes[(i + 1) % 3] = 0;
+    if (lane == 0 && mask) atomicAdd(&votes[i], __popc(mask));
+    if (!meet()) return false;
+    c = votes[i];
+    return true;
+  };
   int j = 0;   // batches of this CTA so far
   while (next_row_piece(p, walk, all, row, b0, b1, place)) {
     if (all && !row_live(p, row)) continue;
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       if (!VEC) {
         load(b, x);
       } else {
-        if (!mbar_wait(&full[st], (j / BS_STAGES) & 1, &abort_sh, p.status)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (j / BS_STAGES) & 1, &abort_sh, p.status))) return give_up();
         const float4* v = reinterpret_cast<const float4*>(ring + st * BS_BATCH) + tid;
 #pragma unroll
         for (int k = 0; k < BS_PER; k += 4) {
@@ -322,14 +330,14 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       return rank;
     };
     // the K best anew, in order; K candidates without a bar are enough for one
-    auto cut = [&]() {
+    auto cut = [&]() -> bool {
       if (n > bs_slack(K) || (have + n >= K && !floor)) {
         for (int i = tid; i < have + n; i += BS_THREADS) {
           const uint64_t key = i < have ? best[i] : list[i - have];
           const int rank = above(key);
           if (rank < K) other[rank] = key;
         }
-        takers_sync();
+        if (!meet()) return false;
         uint64_t* t = best;   // (there are K: bs_slack is no less)
         best = other;
         other = t;
@@ -338,24 +346,27 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
         floor = best[K - 1];
         bar = key_logit(floor);
       }
+      return true;
     };
     // A logit of batch b again, for the few that are looked at twice.
     auto again = [&](int b, int k) { return token(b, k) < p.V ? __ldg(z + token(b, k)) : -INFINITY; };
     // No room for what is above the bar in batch b (one warp's logits, equal ones, rising rows): a higher bar that the
     // bests of K threads reach, by bisection on the keys, which differ.  At least K logits reach it, and at most BS_PER of
     // each of those threads.
-    auto squeeze = [&](int b) {
+    auto squeeze = [&](int b) -> bool {
       uint64_t mine = 0, lo = 1, hi = ~0ull;
+      int c;
 #pragma unroll 1
       for (int k = 0; k < BS_PER; ++k) {
         const float v = again(b, k);
         const uint64_t key = v > bar ? cand_key(v, token(b, k)) : 0;
         mine = key > mine ? key : mine;
       }
-      if (takers_count(mine >= lo) > K)
+      if (!count(mine >= lo, c)) return false;
+      if (c > K)
         while (hi - lo > 1) {
           const uint64_t mid = lo + (hi - lo) / 2;
-          const int c = takers_count(mine >= mid);
+          if (!count(mine >= mid, c)) return false;
           if (c >= K) {
             lo = mid;
             if (c == K) break;
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
           }
         }
       if (tid == 0) n_sh = n;
-      takers_sync();
+      if (!meet()) return false;
       if (mine >= lo)
 #pragma unroll 1
         for (int k = 0; k < BS_PER; ++k) {
@@ -375,8 +386,9 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
             if (at < room) list[at] = key;
           }
         }
-      takers_sync();
+      if (!meet()) return false;
       n = min(n_sh, room);
+      return true;
     };
     // What counts(logit) says of batch b, the CTA's j-th, to the list: the fours that have some are looked at again where
     // they lie (a loop, since a kernel this short pays for the code that it runs through once).
@@ -407,30 +419,29 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       if (!take(b0, &top)) return;
       const float w = warp_nth(top, (K + BS_WARPS - 1) / BS_WARPS);
       if (lane == 0) red[warp] = w;
-      takers_sync();
+      if (!meet()) return;
       if (tid == 0) cnt[(j + BS_STAGES - 1) % BS_STAGES] = 0;
       float least = red[0];
 #pragma unroll
       for (int i = 1; i < BS_WARPS; ++i) least = fminf(least, red[i]);
       if (top >= least) push(b0, [&](float v) { return v >= least && v > -INFINITY; });
-      takers_sync();
+      if (!meet()) return;
       if (lane == 0) mbar_arrive(&pushed[j % BS_STAGES]);
       const int c = cnt[j % BS_STAGES];
-      if (c > room) squeeze(b0);
-      else n = c;
-      cut();
+      if (c <= room) n = c;
+      else if (!squeeze(b0)) return;
+      if (!cut()) return;
       ++j;
     }
     // The others push what beats the bar and go on; the list is looked at when the next batch has been summed up, so that the
     // warps need not wait for one another.  The CTA's batch i counts in cnt[i % BS_STAGES].
     auto settle = [&](int i, int b) -> bool {
-      if (!mbar_wait(&pushed[i % BS_STAGES], (i / BS_STAGES) & 1, &abort_sh, p.status)) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(&pushed[i % BS_STAGES], (i / BS_STAGES) & 1, &abort_sh, p.status))) return give_up();
       const int c = cnt[i % BS_STAGES];
       if (tid == 0) cnt[(i + BS_STAGES - 1) % BS_STAGES] = 0;      // batch i - 1's, which everyone has read
-      if (n + c > room) squeeze(b);
-      else n += c;
-      cut();
-      return true;
+      if (n + c <= room) n += c;
+      else if (!squeeze(b)) return false;
+      return cut();
     };
     for (int b = b0 + 1; b < b1; ++b, ++j) {
       float top;
@@ -456,6 +467,7 @@ __global__ void __launch_bounds__(BS_THREADS + 32, BS_CTAS_PER_SM) beam_part_ker
       if (in_extent(row, 1, rows)) p.pieces[row] = RowPieces{(int)slot, last - (int)blockIdx.x + 1};
     }
   }
+  meet();
 }
 
 // Joins a request's rows: each piece's list is in order, so a candidate below the n_out-th best of the lists' heads is none

@@ -171,6 +171,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// THREADS threads, whole warps, meet at hardware barrier ID and tell each other whether one has given up a wait: all get the same
+// answer.  A warp that gives up comes here next, wherever the others are to meet it, instead of leaving them waiting; then all
+// leave.  (Every warp has to come once more before it ends, so that nobody who gives up waits here alone.)
+template <int ID, int THREADS>
+__device__ __forceinline__ bool one_gave_up(bool mine) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((int)mine), "n"(ID), "n"(THREADS)
+      : "memory");
+  return any != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");

@@ -29,3 +29,19 @@ def test_loading_warp_of_the_8_bit_paged_attention_gives_up_as_one():
     waits = put_q.index("wait_for("), put_q.rindex("wait_for(")
     assert "return false" not in put_q[:waits[1]] and put_q.index("__all_sync(0xffffffffu, free)") > waits[1]
     assert put_q.index("__shfl_xor_sync") > put_q.index("__all_sync")
+
+
+def test_takers_of_beam_selection_give_up_together():
+    """They meet at one_gave_up alone, which gives all of them the same answer; a wait is a whole warp's, and one that runs out goes
+    there too; whatever meets ends its caller where it fails; and every warp meets the others once more at its end."""
+    code, _ = _code("beam.cu")
+    part = code[code.index("auto meet ="):code.index("constexpr int BM_MOST")]
+    assert not re.search(r"bar\.sync|barrier\.cta|__syncthreads", part)
+    waits = list(re.finditer(r"if \(!__all_sync\(0xffffffffu, mbar_wait\([^;]*\) return give_up\(\);", part))
+    assert len(waits) == part.count("mbar_wait(") == 2
+    for call in re.finditer(r"\b(meet|count|squeeze|cut|settle|take)\(", part[:part.rindex("meet();")]):
+        before = part[max(0, call.start() - 40):call.start()].rstrip()
+        assert re.search(r"(!|return)$", before), part[call.start() - 40:call.end() + 20]
+    assert re.search(r"meet\(\);\s*\}\s*$", part)
+    common, _ = _code("common.cuh")
+    assert "barrier.cta.red.or.pred" in common
