@@ -555,7 +555,9 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
     }
   }
   if (tid < 32) {
-    const int n = lane >= p.W ? 0 : kind[lane] == 1 ? pieces.n : kind[lane] == 2;
+    // (a first kernel that gave up may have left some unwritten: whatever lies there, no list is looked for where none is)
+    const bool there = pieces.slot >= 0 && pieces.n >= 0 && (int64_t)pieces.slot + pieces.n <= p.n_lists;
+    const int n = lane >= p.W ? 0 : kind[lane] == 1 ? (there ? pieces.n : 0) : kind[lane] == 2;
     if (lane < p.W) slot0[lane] = pieces.slot;
     int x = n;
 #pragma unroll
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(BS_THREADS) beam_merge_kernel(const __grid_con
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    first[lane + 1] = x;
+    first[lane + 1] = __shfl_sync(0xffffffffu, x, 31) <= BM_LISTS ? x : 0;
     if (lane == 0) { first[0] = 0; n_sh[0] = n_sh[1] = n_good = 0; bar_sh = BM_NONE; bar_at = INT_MAX; }
   }
   __syncthreads();

@@ -45,3 +45,12 @@ def test_takers_of_beam_selection_give_up_together():
     assert re.search(r"meet\(\);\s*\}\s*$", part)
     common, _ = _code("common.cuh")
     assert "barrier.cta.red.or.pred" in common
+
+
+def test_join_of_beam_selection_looks_for_no_list_where_none_is():
+    """After a first kernel that gave up, a row's record of its lists may be whatever the workspace held: it is held against the
+    lists that there are, and a request's against the room for them, before anything is indexed by it."""
+    code, _ = _code("beam.cu")
+    join = code[code.index("beam_merge_kernel("):code.index("int64_t select_grid(")]
+    checks = join.index("(int64_t)pieces.slot + pieces.n <= p.n_lists"), join.index("<= BM_LISTS")
+    assert "pieces.slot >= 0 && pieces.n >= 0" in join and max(checks) < join.index("row_of[l]") and max(checks) < join.index("p.keys[")
