@@ -3,7 +3,7 @@
 //
 // write: x the rotated K row or the V row of one head, u = max |v_i| for V and max (|a| + |b|) over the
 //   pairs for K (a rotation keeps a pair inside that circle, so the scale is the same at every
-//   position and no code saturates); scale 2^e, e the smallest with u <= 448 * 2^e; code = E4M3(x * 2^-e).
+//   position and no code saturates; summed upwards, so that what is above 448 * 2^e does not round onto it); scale 2^e, e the smallest with u <= 448 * 2^e; code = E4M3(x * 2^-e).
 //   A power of two costs a floating-point code nothing, and code * scale has a bf16 value.
 // read: x = code * scale.
 #include <algorithm>
@@ -84,7 +84,7 @@ __device__ __forceinline__ void store_vector(const Append8Params& p, uint4 w, bo
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const float a = fabsf(x[i]), b = fabsf(x[i + 1]);
-      u = fmaxf(u, part == 2 ? fmaxf(a, b) : a + b);
+      u = fmaxf(u, part == 2 ? fmaxf(a, b) : __fadd_ru(a, b));
     }
 #pragma unroll
     for (int k = VPH / 2; k > 0; k >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, k));
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(A8_THREADS) rope_append8_any_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a = x[2 * i], b = x[2 * i + 1];
-        u = fmaxf(u, is_v ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a) + fabsf(b));
+        u = fmaxf(u, is_v ? fmaxf(fabsf(a), fabsf(b)) : __fadd_ru(fabsf(a), fabsf(b)));
         if (!is_v) {
           const float2 c = cs[lane * 4 + i];
           x[2 * i] = a * c.x - b * c.y;

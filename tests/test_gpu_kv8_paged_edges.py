@@ -295,3 +295,29 @@ def test_heavy_keys_of_zero_values():
         got = to_f64(_attend(c, _dev(q, torch.bfloat16), [n - 1]))
         assert _status() == 0
         _close(got[0], q[0], *c.rows(0))
+
+
+# ------------------------------------------------------------------------------------------ append
+@pytest.mark.parametrize("hd,n_kv,T", [(64, 1, 7), (128, 2, 7), (72, 1, 7), (128, 2, 700)])
+def test_append_scale_of_keys_on_a_border(hd, n_kv, T):
+    """|a| + |b| on 448 * 2^e and above it by less than a rounding of fp32: the scale is the definition's."""
+    import torch
+    k = np.zeros((T, n_kv, hd))
+    pairs = [(448.0, 2.0 ** -20), (2.0 ** -30, -448.0), (446.0, 2.0), (224.0, -224.0), (448.0 * 2 ** 40, 2.0 ** -90),
+             (448.0 * 2.0 ** -60, 2.0 ** -120), (256.0, 192.0)]
+    for t in range(T):
+        k[t, :, 2 * (t % (hd // 2)):2 * (t % (hd // 2)) + 2] = pairs[t % 7]
+    kd = _dev(k, torch.bfloat16)
+    np.testing.assert_array_equal(to_f64(kd), k)
+    slots, pos = np.arange(T), np.zeros(T)
+    got = _append(None, kd, kd, pos, slots, -(-T // 128))
+    assert _status() == 0
+    a, b = np.abs(k[..., 0::2]), np.abs(k[..., 1::2])
+    e = np.full((T, n_kv), -100)
+    for i in range(-100, 101):                          # a + b <= 448 * 2^i, without rounding the sum
+        over = np.any(a > 448 * 2.0 ** i - b, -1) | np.any((a >= 448 * 2.0 ** i) & (b > 0), -1) | np.any((b >= 448 * 2.0 ** i) & (a > 0), -1)
+        e = np.where(over, min(i + 1, 100), e)
+    want = 2.0 ** e.astype(np.float64)
+    codes, scales = _at(slots, got[1], got[2])
+    np.testing.assert_array_equal(scales, want)
+    np.testing.assert_array_equal(R.E4M3[codes], R.E4M3[R.encode(k / want[..., None])])
