@@ -470,8 +470,9 @@ int llama_gqa_attention_decode_paged_kv8(const llama_dims* dims, const void* q, 
  *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_SELECT, dims with B and S = W, ..., vocab) bytes, for any n_out
  * The outputs may not overlap the inputs; calls that overlap on the GPU need workspaces of their own.
  * Exponentials and their sums in fp32, the sum's logarithm to 2^-25, scores in fp64 (out_scores rounds once): candidates
- * of one beam are ranked by their logits, those of different beams by scores good to about 2^-22; equal rows with equal
- * scores give equal scores.
+ * of one beam are ranked by their logits, those of different beams by scores good to 2^-18 (vocab up to 163840; 2^-21 more for each
+ * 163840 beyond), which is the most that fp32 and the exponential's instruction can add up to; equal rows with equal scores give
+ * equal scores.
  * LLAMA_ERR_UNSUPPORTED for W > 32, n_out > 64 or B * W >= 2^22; LLAMA_ERR_INVALID_ARG for B < 0, W < 1, n_out < 1,
  * vocab < 1 or > 2^30, ld < vocab, pad_token outside [0, vocab) with finished given, NULL arrays; LLAMA_ERR_ALIGNMENT for arrays
  * not 4-byte aligned or ws not 16-byte aligned; LLAMA_ERR_WORKSPACE for a workspace that is too small.    */

@@ -76,7 +76,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// exp(x - m) with the difference formed first, so that large logits keep their digits.
+// exp(x - m) with the difference formed first, so that large logits keep their digits.  Off by 2.23 * 2^-24 of the distance (a
+// difference, a product and log2(e), each rounded) and 2^-22 (the instruction): with distances whose mean under the softmax is at most
+// ln V, two of these and some 25 additions in a row, a sum is off by 2^-18 of itself at most, for 163840 logits.
 __device__ __forceinline__ float exp_from(float x, float m) { return exp2_fast((x - m) * 1.4426950408889634f); }
 __device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2) {
   const float mx = fmaxf(m, m2);
