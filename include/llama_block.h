@@ -504,7 +504,8 @@ typedef struct llama_page_pool {
  *   ws: llama_workspace_bytes(LLAMA_OP_BEAM_REORDER_PAGED, dims with B and S = W, ..., kv_capacity = 128 * max_pages)
  * A page may stand in several rows of a request, in the same column; other requests may share pages that some kept beam of
  * each holds (a common prompt).  No pool row is written but the copied rows.  Calls that overlap on the GPU need
- * workspaces of their own.
+ * workspaces of their own.  More than 8 pools, or layers in pools of their own: several calls on the same inputs, none of them in
+ * place but the last; each writes the same tables and lists and copies its own pools.
  * LLAMA_ERR_UNSUPPORTED for W > 32, B > 8192, n_pages >= 2^24, max_pages > 2^17, n_free or freed_room >= 2^31, n_pools > 8,
  * parts * row_bytes > 2^24, n_layers * parts * row_bytes > 2^27 (16 GB of one page over all layers of a pool);
  * LLAMA_ERR_INVALID_ARG for other bad counts (negative; W, n_pages or max_pages < 1; a pool's n_layers, parts or
