@@ -439,7 +439,7 @@ int llama_kv_dequantize_paged(const llama_dims* dims, const void* k_codes, const
  * calls that overlap on the GPU need workspaces of their own.
  * An infinity or a NaN in a row of q makes that head's row NaN.  Scores have to be finite in fp32.
  * Numerics: scores, softmax statistics and sums in fp32.  q enters the 8-bit tensor-core products as two E4M3 values (a bf16's 8
- * significant bits down to 2^-15 of the row's largest, an error of 2^-22 of that below), the products of softmax weight and V scale
+ * significant bits down to 2^-14 of the row's largest, an error of 2^-22 of that below), the products of softmax weight and V scale
  * as three E5M2 values: off by 2^-11 of themselves down to 2^-25 of the row's largest, by 2^-38 of that below.
  * LLAMA_ERR_UNSUPPORTED for another head_dim, n_q > 65536, B > 65535, B n_kv >= 2^24, n_pages >= 2^24, max_pages >= 2^31;
  * LLAMA_ERR_INVALID_ARG for S != 1, other bad dims, n_pages < 1, max_pages < 1, max_pos < 0, max_pos >= 128 * max_pages

@@ -24,10 +24,10 @@ constexpr size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 // their own maximum; these sums do not depend on where the rows are cut, so equal rows give equal scores.  What beats the
 // n_out-th best of a row's piece so far waits in shared memory, and now and then the n_out best are taken anew.  The second
 // kernel joins a request's lists and sums.
-// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 44.4 us, the first kernel 39.5 cold, 4.1 TB/s.
+// 48 requests of 8 beams x 128256, a seventh of them finished (167 MB), 16 kept: 44.4 us, the first kernel 40.2 cold, 4.0 TB/s.
 // Each further request costs 0.63 us (6.5 TB/s); the rest, some 18 us, are the ranges' starts, the pieces' first batches, whose
 // candidates are many, their ends, and the join.  (Registers loaded ahead instead of the ring 52 us, 4 CTAs per SM 46-60.)  One request
-// of 4 beams x 32000: 10.1 us, two launches and their chains.
+// of 4 beams x 32000: 10.5 us, two launches and their chains.
 constexpr int BS_THREADS = 256;
 constexpr int BS_WARPS = BS_THREADS / 32;
 constexpr int BS_PER = 20;                              // logits of a thread in a batch
@@ -835,10 +835,10 @@ struct BulkCopies {
 // taken, pages left over and vectors to copy; entries and freed pages are dealt out by request, and the vectors of
 // all copies, one after the other, are cut into equal ranges, one per CTA, where one thread drives bulk copies for the long runs
 // (rows) while the other warps move the short ones (scales).  16 requests of 8 beams, eight layers of 8-bit pages of 8 heads x
-// 128 (149 MB read and written): 27.4 us with the plan, 22 at a copy's rate; through registers, four loads in flight per thread,
+// 128 (149 MB read and written): 27.6 us with the plan, 22 at a copy's rate; through registers, four loads in flight per thread,
 // 34 (the next four on their way before these are stored 36, chunks in turn instead of ranges 32-49); chunks of 4 to 12 KB 28-32,
 // four CTAs 29; two CTAs with a slot more 26.6, but 13.6 instead of 12.3 for 16 requests of 4 beams over four bf16 layers
-// (9.8 at a copy's rate).  One request of 4 beams over two bf16 layers of 2 heads x 64: 6.3 us.
+// (9.8 at a copy's rate).  One request of 4 beams over two bf16 layers of 2 heads x 64: 6.5 us.
 __global__ void __launch_bounds__(BR_THREADS, BR_CTAS_PER_SM) beam_copy_kernel(const __grid_constant__ ReorderParams p) {
   extern __shared__ int64_t v0[];   // [B + 1] first vector of each request; then [2][B + 1]: first page taken, first page freed
   int* t0 = reinterpret_cast<int*>(v0 + p.B + 1);

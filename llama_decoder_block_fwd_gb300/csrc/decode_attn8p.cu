@@ -7,9 +7,9 @@
 //
 // What bounds it: the codes and scales are read once, 2 (hd + 4) bytes per position and KV head, at a few operations
 // per byte, so HBM does, where there are enough tiles, and the latency of one tile's chain where there are few.  64 sequences
-// of 2-8 K positions, 32/8 heads x 128 (671 MB): 107.6 us = 6.2 TB/s, 93% of a copy's rate; one of 131000 (277 MB) 47.6 us,
-// 87%; three of 100 to 900: 8.9 us.  With 8 query heads and more per KV head the softmax comes nearest to it (64 sequences of 64/8
-// heads 124 us), and with 16 over one KV head it sets the pace (16/1 heads 36 us where the bytes take 14).
+// of 2-8 K positions, 32/8 heads x 128 (671 MB): 109.0 us = 6.2 TB/s, 92% of a copy's rate; one of 131000 (277 MB) 48.0 us,
+// 86%; three of 100 to 900: 9.2 us.  With 8 query heads and more per KV head the softmax comes nearest to it (64 sequences of 64/8
+// heads 124 us), and with 16 over one KV head it sets the pace (16/1 heads 35 us where the bytes take 14).
 //
 // Tiles.  A tile is one page (128 positions) by 128 bytes of a row: one KV head of 128, or two of 64 side by side, which
 //   one product serves (each head's query rows hold zeros in the other's bytes).  tcgen05 kind::f8f6f4 reads the codes as
@@ -17,7 +17,7 @@
 //   One thread per key does the softmax of its tile; the scales come with the tile by bulk copies, a head's 128
 //   scales of a page being contiguous.
 // Operands.  The other side has 8 bits an element too.  q enters as x = hi + 2^-5 lo in E4M3, hi = e4m3(x), lo = e4m3(32 (x - hi)): all
-//   of a bf16's bits down to 2^-15 of the row's largest.  P enters as three E5M2 values, x = a + b/16 + c/256, each the
+//   of a bf16's bits down to 2^-14 of the row's largest, off by 2^-22 of that below.  P enters as three E5M2 values, x = a + b/16 + c/256, each the
 //   rounding of what the ones before it leave: off by 2^-11 of x (2^-3 after the first, 2^-4 more with each further one) down to 2^-25
 //   of the row's largest, by 2^-38 of that below.  So a tail of 2^24 small weights beside a heavy one keeps its sum, where
 //   E4M3's few binades lose it (two E4M3 parts: a tail that is 30% of the row, off by 14% of itself).  The further rows ride
@@ -47,7 +47,7 @@ namespace {
 // sets the pace, so two groups share the rows of a tile (a thread has one key of four or eight rows); a warp of its own for q
 // would leave two such CTAs 80 registers a thread, and eight rows' state spills there.
 constexpr int dp_threads(int SG) { return 64 + 128 * SG; }
-// two CTAs per SM (2 x 110 KB of shared memory), so that one's hand-offs overlap the other's
+// two CTAs per SM (2 x 114 KB of shared memory), so that one's hand-offs overlap the other's
 constexpr int DP_KSTAGES = 3;
 constexpr int DP_VSTAGES = 2;
 constexpr int DP_SSTAGES = 4;     // scales

@@ -235,7 +235,7 @@ struct Dequant8Params {
 
 // HBM bound.  A unit is DQ_ROWS rows of a page of K or of V; the CTAs take the units of all sequences, one after the
 // other, in turn, so that at any time they work on neighbouring ones.  16 ragged sequences of 1000-6000 positions, 8 heads
-// x 128 (337 MB): 55.6 us = 6.07 TB/s, 91% of a copy's rate; a contiguous range per CTA 57.6 us, 16-byte stores
+// x 128 (337 MB): 56.3 us = 6.0 TB/s, 90% of a copy's rate; a contiguous range per CTA 57.6 us, 16-byte stores
 // 67 us, 4 and 6 CTAs per SM 57-62 us, streaming loads 3-4 us more.
 constexpr int DQ_THREADS = 256;
 constexpr int DQ_ROWS = 32;

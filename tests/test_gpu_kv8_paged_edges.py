@@ -19,7 +19,8 @@ def _parts(q, k, v):
 
 def _tol(ref, size):
     """Half a bf16 step of the result; a weight enters the product with 2^-11 of itself, its exponent is off by 2^-18
-    (fp32 exponents up to 128 in size, the exponential's own 2^-22), q by 2^-9 of what is 2^-15 below its row's largest:
+    (fp32 exponents up to 128 in size, the exponential's own 2^-22), q by 2^-22 of its row's largest
+    where an element is below 2^-14 of that:
     2^-10 of the sum of sizes holds them all."""
     return 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size
 
